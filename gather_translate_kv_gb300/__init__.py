@@ -2,7 +2,7 @@
 
 Argument marshalling only: every function below checks tensor dtypes, shapes,
 devices and contiguity, then calls the C entry point of the same name in
-``include/kv_pool.h``; every step of the data path runs in that library's
+``include/kv_pool.h`` or ``include/kv_attention.h``; every step of the data path runs in that library's
 CUDA kernels. PyTorch provides device memory and streams. There is no other
 implementation to fall back to: if ``libgtkv.so`` is missing, every call
 raises ``RuntimeError``.
@@ -22,6 +22,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgtkv.so")
 HEADER = os.path.join(os.path.dirname(_PKG), "include", "kv_pool.h")
+ATTENTION_HEADER = os.path.join(os.path.dirname(_PKG), "include", "kv_attention.h")
 
 KV_OK = 0
 STATUS = {
@@ -30,6 +31,8 @@ STATUS = {
     -8: "KV_ERR_CAPACITY",
 }
 KV_DEV_ERR_ROW, KV_DEV_ERR_V2P, KV_DEV_ERR_TABLE, KV_DEV_ERR_FORM, KV_DEV_ERR_TIMEOUT = 1, 2, 4, 8, 16
+KV_DEV_ERR_POSITION = 32  # kv_attention.h
+KV_TYPE = {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}
 
 
 class KVError(RuntimeError):
@@ -71,6 +74,33 @@ class kv_pool_info_t(ctypes.Structure):
     ]
 
 
+class kv_batch_t(ctypes.Structure):
+    _fields_ = [
+        ("table_dev", ctypes.c_void_p),
+        ("seq_start_dev", ctypes.c_void_p),
+        ("seq_len_dev", ctypes.c_void_p),
+        ("cu_dev", ctypes.c_void_p),
+        ("n_rows", ctypes.c_int64),
+        ("n_seqs", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("kernel_facing", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class kv_rotary_t(ctypes.Structure):
+    _fields_ = [
+        ("cos_sin_dev", ctypes.c_void_p),
+        ("positions_dev", ctypes.c_void_p),
+        ("n_positions", ctypes.c_int64),
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("n_axes", ctypes.c_int32),
+        ("axis_pairs", ctypes.c_int32 * 4),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 def make_desc(layer_num, head_num, head_dim, itemsize, page_size, num_pages, anchor_bytes=0,
               v_head_dim=None, latent_only=False) -> kv_pool_desc:
     """Pool geometry; latent_only=True makes an MLA pool (one latent row of
@@ -83,8 +113,8 @@ _lib = None
 
 
 def header_functions() -> list[str]:
-    """Names of the functions include/kv_pool.h declares."""
-    src = open(HEADER).read()
+    """Names of the functions include/kv_pool.h and include/kv_attention.h declare."""
+    src = open(HEADER).read() + open(ATTENTION_HEADER).read()
     src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
     return re.findall(r"^\s*(?:const\s+)?[A-Za-z_][\w\s\*]*?\b(kv_\w+)\s*\(", src, flags=re.M)
 
@@ -130,6 +160,11 @@ def load(path: str) -> ctypes.CDLL:
         "kv_gather_plan_kf": [vp, vp, i32, i32, vp, vp, vp, i64, vp],
         "kv_gather_layer_planned_kf": [vp, i32, vp, i64, vp, i32, i32, vp, vp, vp, vp, vp, i64, vp],
         "kv_pool_last_error": [vp, vp, P(i32)],
+        "kv_scale_bytes": [vp, P(i64)],
+        "kv_append_layer": [vp, i32, vp, i32, vp, i64, vp, i64, vp, vp, i64, i32, vp, vp, vp],
+        "kv_attend_workspace_bytes": [vp, i32, i32, i64, P(i64)],
+        "kv_attend_layer": [vp, i32, vp, i32, vp, i64, i32, vp, vp, ctypes.c_float, i32, i32, vp, vp, i64, vp],
+        "kv_gather_layer_scaled": [vp, i32, vp, vp, i32, vp, vp, vp],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -423,6 +458,177 @@ def kv_translate_block_table(pool: KVPool, virt_bt: torch.Tensor, seq_len: torch
         pool.handle, _dev(virt_bt, "virt_bt", torch.int32), n_seqs, max_pages, _dev(seq_len, "seq_len", torch.int32),
         _dev(v2p, "v2p", torch.int32), v2p.numel(), _dev(out_bt, "out_bt", torch.int32), _stream(stream)))
     return out_bt
+
+
+# ------------------------------------------------------- include/kv_attention.h
+
+@dataclass
+class KVBatch:
+    """A kv_batch and the tensors it points to; build it once per step and use
+    it for every layer's append, attention and gather."""
+
+    struct: kv_batch_t
+    ptr: int
+    n_rows: int
+    n_seqs: int
+    tensors: tuple
+
+
+def kv_batch(block_table: torch.Tensor, seq_len: torch.Tensor, cu: torch.Tensor, n_rows: int,
+             seq_start: torch.Tensor | None = None, kernel_facing: bool = False) -> KVBatch:
+    """The step's tokens: [seq_start, seq_len) of each sequence, at rows cu[s] on of n_rows."""
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [n_seqs, max_pages]")
+    n_seqs, max_pages = block_table.shape
+    if seq_len.numel() != n_seqs or cu.numel() != n_seqs + 1:
+        raise ValueError("seq_len must be [n_seqs] and cu [n_seqs + 1]")
+    if seq_start is not None and seq_start.numel() != n_seqs:
+        raise ValueError("seq_start must be [n_seqs]")
+    if n_rows < 0:
+        raise ValueError("n_rows must not be negative")
+    st = kv_batch_t(_dev(block_table, "block_table", torch.int32), _dev(seq_start, "seq_start", torch.int32),
+                    _dev(seq_len, "seq_len", torch.int32), _dev(cu, "cu", torch.int64), n_rows, n_seqs, max_pages,
+                    1 if kernel_facing else 0, 0)
+    return KVBatch(st, ctypes.addressof(st), n_rows, n_seqs, (block_table, seq_len, cu, seq_start))
+
+
+@dataclass
+class KVRotary:
+    """A kv_rotary and the tensors it points to."""
+
+    struct: kv_rotary_t
+    ptr: int
+    tensors: tuple
+
+
+def kv_rotary(cos_sin: torch.Tensor, positions: torch.Tensor | None = None, axis_pairs=None,
+              interleaved: bool = False) -> KVRotary:
+    """cos_sin: float32 [n_positions, rotary_dim], cosines of the pairs then
+    sines; positions: int32 [n_axes, n_rows] (or [n_rows] for one axis), None
+    for a token's index in its sequence; axis_pairs: pairs of each axis."""
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [n_positions, rotary_dim]")
+    n_pos, rd = cos_sin.shape
+    if axis_pairs is None:
+        if positions is not None and positions.dim() == 2 and positions.shape[0] != 1:
+            raise ValueError("axis_pairs must say how many pairs each axis turns")
+        axis_pairs = (rd // 2,)
+    axes = len(axis_pairs)
+    if not 1 <= axes <= 4:
+        raise ValueError("1 to 4 axes")
+    if positions is not None and positions.shape[:-1] not in ((axes,), () if axes == 1 else (axes,)):
+        raise ValueError("positions must be [n_axes, n_rows]")
+    st = kv_rotary_t(_dev(cos_sin, "cos_sin", torch.float32), _dev(positions, "positions", torch.int32), n_pos, rd,
+                     1 if interleaved else 0, axes, (ctypes.c_int32 * 4)(*axis_pairs), 0)
+    return KVRotary(st, ctypes.addressof(st), (cos_sin, positions))
+
+
+def _rows(t: torch.Tensor, name: str, n_rows: int, dtype=None) -> tuple[int, int]:
+    """Address and row stride of a [n_rows, heads, dim] tensor whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.dim() != 3 or t.shape[0] != n_rows:
+        raise ValueError(f"{name} must be [n_rows = {n_rows}, heads, dim], got {list(t.shape)}")
+    if t.stride(2) != 1 and t.shape[2] > 1 or t.stride(1) != t.shape[2] and t.shape[1] > 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    return t.data_ptr(), t.stride(0) if n_rows > 1 else t.shape[1] * t.shape[2]
+
+
+def _type(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in KV_TYPE:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    return KV_TYPE[t.dtype]
+
+
+def _heads(t: torch.Tensor, name: str, heads: int | None, pool: KVPool) -> None:
+    if t.shape[2] != pool.desc.head_dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must have rows of [{'heads' if heads is None else heads}, {pool.desc.head_dim}], "
+                         f"got {list(t.shape[1:])}")
+
+
+def _scales(pool: KVPool, scales: torch.Tensor | None):
+    if pool.desc.itemsize != 1:
+        if scales is not None:
+            raise ValueError("only pools of itemsize 1 have scales")
+        return None
+    if scales is None:
+        raise ValueError("a pool of itemsize 1 needs its scales")
+    return _dev(scales, "scales", torch.float32,
+                4 * pool.desc.num_pages * pool.desc.layer_num * 2 * pool.desc.head_num)
+
+
+def kv_scale_bytes(pool: KVPool) -> int:
+    """Bytes of an 8-bit pool's scales, float32 [num_pages, L, 2, H]."""
+    out = ctypes.c_int64()
+    _check("kv_scale_bytes", lib().kv_scale_bytes(pool.handle, ctypes.byref(out)))
+    return out.value
+
+
+def kv_append_layer(pool: KVPool, layer: int, batch: KVBatch, k: torch.Tensor, v: torch.Tensor,
+                    rotary: KVRotary | None = None, q: torch.Tensor | None = None,
+                    q_out: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None) -> None:
+    """Append the batch's rows of k (rotated) and v to the cache and write the
+    rotated q to q_out. k, v and q may be slices of a wider tensor's rows."""
+    n, H = batch.n_rows, pool.desc.head_num
+    kp, ks = _rows(k, "k", n)
+    vp, vs = _rows(v, "v", n, k.dtype)
+    _heads(k, "k", H, pool)
+    _heads(v, "v", H, pool)
+    if rotary is not None and rotary.tensors[1] is not None and rotary.tensors[1].shape[-1] != n:
+        raise ValueError(f"the rotation's positions are for {rotary.tensors[1].shape[-1]} rows, the batch has {n}")
+    qp, qs, qh, op = None, 0, 0, None
+    if q is not None:
+        qp, qs = _rows(q, "q", n, k.dtype)
+        _heads(q, "q", None, pool)
+        qh = q.shape[1]
+        if q_out is None or q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        op = _dev(q_out, "q_out", k.dtype)
+    _check("kv_append_layer", lib().kv_append_layer(
+        pool.handle, layer, batch.ptr, _type(k, "k"), kp, ks, vp, vs, None if rotary is None else rotary.ptr, qp, qs,
+        qh, op, _scales(pool, scales), _stream(stream)))
+
+
+def kv_attend_workspace_bytes(pool: KVPool, q_heads: int, n_seqs: int, n_rows: int) -> int:
+    out = ctypes.c_int64()
+    _check("kv_attend_workspace_bytes", lib().kv_attend_workspace_bytes(pool.handle, q_heads, n_seqs, n_rows,
+                                                                        ctypes.byref(out)))
+    return out.value
+
+
+def kv_attend_layer(pool: KVPool, layer: int, batch: KVBatch, q: torch.Tensor, out: torch.Tensor, scale: float,
+                    workspace: torch.Tensor, window: int = 0, sinks: int = 0, scales: torch.Tensor | None = None,
+                    lse: torch.Tensor | None = None, stream=None) -> None:
+    """Attention of the batch's rows q [n_rows, q_heads, dim] over the layer's
+    cache into out (and the log-sum-exp into lse [n_rows, q_heads]).
+    workspace: uint8, kv_attend_workspace_bytes() long, one per call in flight."""
+    n = batch.n_rows
+    qp, qs = _rows(q, "q", n)
+    _heads(q, "q", None, pool)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is not None and tuple(lse.shape) != (n, q.shape[1]):
+        raise ValueError("lse must be [n_rows, q_heads]")
+    _check("kv_attend_layer", lib().kv_attend_layer(
+        pool.handle, layer, batch.ptr, _type(q, "q"), qp, qs, q.shape[1], _dev(out, "out", q.dtype),
+        _dev(lse, "lse", torch.float32), scale, window, sinks, _scales(pool, scales),
+        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream)))
+
+
+def kv_gather_layer_scaled(pool: KVPool, layer: int, batch: KVBatch, scales: torch.Tensor, out_k: torch.Tensor,
+                           out_v: torch.Tensor, stream=None) -> None:
+    """The values (code times scale) of the batch's tokens, one layer's K and V
+    as [n_rows, H, D] of out_k's type."""
+    shape = (batch.n_rows, pool.desc.head_num, pool.desc.head_dim)
+    if tuple(out_k.shape) != shape or tuple(out_v.shape) != shape:
+        raise ValueError(f"out_k and out_v must be {list(shape)}")
+    _check("kv_gather_layer_scaled", lib().kv_gather_layer_scaled(
+        pool.handle, layer, batch.ptr, _scales(pool, scales), _type(out_k, "out_k"), _dev(out_k, "out_k"),
+        _dev(out_v, "out_v", out_k.dtype), _stream(stream)))
 
 
 def kv_pool_last_error(pool: KVPool, stream=None) -> int:
