@@ -1,0 +1,840 @@
+// Attention of few rows a sequence (decode steps, drafted tokens): at most 16
+// rows, a row being a (token, query head) pair of one KV head. Every key and
+// value is read once and meets a handful of rows, so the bound is memory; the
+// work is laid out so that nothing stands between the loads.
+//
+// One warp owns one KV head over its own run of keys, 16 keys a step, and never
+// talks to another warp. Both products run as mma m16n8k16 with the CACHE as
+// the 16-row operand, S^T = K Q^T and O^T = V^T P^T, rows as the 8 (or 16)
+// columns, so 4 query heads fill half of an instruction instead of a quarter.
+// A lane's operand registers are filled from 16-byte pieces that it copied to
+// shared memory itself (cp.async, a ring of its own): the order of the summed
+// index is free, so lane (g, c) = (lane / 4, lane % 4) takes whole 16-byte
+// pieces of keys g and g + 8 for K, and its eighth of the elements of keys 2c,
+// 2c + 1, 2c + 8, 2c + 9 for V, where byte permutes pair up two keys. No
+// transpose, no bank conflict, no barrier. Codes become fp16 (exact) on the
+// way into the registers; P^T comes out of the score registers by movmatrix.
+//
+// Softmax: the running reference m moves only when a score exceeds it by
+// 2^8 (a vote per step), so the common step has no shuffle. Weights are
+// 2^(t - m), t = score * log2(e) + log2(value scale): the scale of an 8-bit
+// value is part of its weight, so that weights stay in one range, and the
+// denominator adds weight / scale. Weights meet the values as fp16 (11 bits),
+// lifted by 2^6 so that 2^-30 of the largest still counts; for bf16 caches as
+// a sum of two bf16 (16 bits), the second product being free under the memory
+// bound. Queries for 8-bit caches are fp16 after a power-of-two scaling per row, exact for all
+// bits that matter (2^-29 of the row's largest).
+//
+// Workers (as many warps as share a step's heads) take equal shares of all
+// steps of the batch (kv_attend_split.cuh); units cut at a border are joined by
+// k_attend_join from 32-bit partial sums in the workspace.
+#include <type_traits>
+
+#include "kv_attend_few.h"
+#include "kv_attend_split.cuh"
+
+namespace gtkv {
+
+namespace {
+
+constexpr int kFewWarps = 4;
+constexpr int kFewBlock = 32 * kFewWarps;
+constexpr int kFewBlocksPerSM = 3;
+constexpr float kNoRef = -1e30f;  // reference before the first key; finite, so that -inf - m stays -inf
+
+template <class C>
+struct FewType {
+  static constexpr int kSize = 2;       // bytes per cached element
+  static constexpr bool kSplitP = false;
+  static constexpr float kLift = 6.0f;  // log2 of the weights' lift
+};
+template <>
+struct FewType<CodeE4M3> {
+  static constexpr int kSize = 1;
+  static constexpr bool kSplitP = false;
+  static constexpr float kLift = 6.0f;
+};
+template <>
+struct FewType<__nv_bfloat16> {
+  static constexpr int kSize = 2;
+  static constexpr bool kSplitP = true;
+  static constexpr float kLift = 0.0f;
+};
+
+__device__ __forceinline__ uint32_t shared_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool ok) {
+  const int n = ok ? N : 0;  // 0: the bytes become zero
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+template <class C>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  if constexpr (std::is_same_v<C, __nv_bfloat16>)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8x8 transpose of 16-bit elements over the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Two e4m3 codes (bytes 0 and 1 of a half word) as two fp16.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
+  uint32_t y;
+  asm("{.reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(y) : "r"(w));
+  return y;
+}
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
+  uint32_t y;
+  asm("{.reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(y) : "r"(w));
+  return y;
+}
+
+// All ones in the elements of a word of cached values that are not finite.
+template <class C>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  if constexpr (std::is_same_v<C, CodeE4M3>)
+    return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+  else if constexpr (std::is_same_v<C, __half>)
+    return __vcmpeq2(w & 0x7c007c00u, 0x7c007c00u);
+  else
+    return __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_h(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_b(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <class C, int D>
+struct FewShape {
+  static constexpr int kSize = FewType<C>::kSize;
+  static constexpr int kRow = D * kSize;      // bytes of a head's row
+  static constexpr int kKC = kRow / 64;       // 16-byte pieces of a key that a lane holds
+  static constexpr int kVB = kRow / 8;        // bytes of a value that a lane holds
+  static constexpr int kK = 16 * kRow;        // bytes of a step's K, and of its V
+  static constexpr int kMeta = 144;           // 32 scales, the mask of live keys
+  static constexpr int kStage = 2 * kK + kMeta;
+  static constexpr int kStages = kRow >= 256 ? 2 : kRow >= 128 ? 4 : 6;
+  static constexpr int kSmem = kFewWarps * kStages * kStage;
+  static constexpr int kKS = D / 16;          // k16 steps of the score product
+  static constexpr int kMT = D / 16;          // 16-element tiles of the output
+};
+
+// P16: the page size is a multiple of 16, so a step's keys share a page and a
+// lane looks up the pages of 32 steps ahead at once; otherwise every key's entry is
+// read on its own, one step ahead.
+template <class C, int D, int NT, bool P16>
+__global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
+    k_attend_few(DevPool p, Batch b, AttendArgs a, FewSplit w) {
+  using Sh = FewShape<C, D>;
+  constexpr bool kE4M3 = std::is_same_v<C, CodeE4M3>;
+  constexpr float kLift = FewType<C>::kLift;
+  constexpr int NQ = 8 * NT;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ ShareStart loc[kFewWarps];
+  __shared__ int64_t tmp[kFewWarps];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, c = lane & 3;
+  const int kw = kFewWarps / w.hw;             // workers of the block
+  const int wk = warp / w.hw;                  // this warp's worker in the block
+  const int hw = warp - wk * w.hw;             // its head of the worker's group
+  const int32_t n_groups = a.H / w.hw;
+  int bits = 0;
+
+  auto tiles_of = [&](const Seq& q) { return q.n == 0 || q.n > w.max_new ? 0 : (q.n * a.G + NQ - 1) / NQ; };
+  auto span_of = [&](const Seq& q, int32_t t) {
+    const int32_t f0 = t * NQ, f1 = min(f0 + NQ, q.n * a.G);
+    return key_span<16>(a, q, f0, f1);
+  };
+  const int64_t worker0 = static_cast<int64_t>(blockIdx.x) * kw;
+  const int64_t share = find_shares<kFewBlock, kFewWarps>(
+      b.n_seqs, worker0, w.n_workers, w.min_share, loc, tmp, [&](int32_t s) -> int64_t {
+        int err = 0;
+        const Seq q = seq_of(p, b, s, err);
+        if (blockIdx.x == 0) bits |= err;
+        int64_t n = 0;
+        for (int32_t t = 0; t < tiles_of(q); ++t) n += span_of(q, t).steps();
+        return n * n_groups;
+      });
+  const int64_t worker = worker0 + wk;
+  SplitRecord rec{-1, 0, 0, 0};
+  ShareStart at = loc[wk];
+  if (worker >= w.n_workers) at.s = -1;
+
+  // the warp's ring
+  const uint32_t ring0 = shared_u32(ring) + warp * Sh::kStages * Sh::kStage;
+  const uint8_t* pool = reinterpret_cast<const uint8_t*>(p.base);
+  const int64_t row_bytes = p.vpr * 16;
+
+  int64_t left = at.s < 0 ? 0 : share;
+  int32_t s = at.s, tile = 0, group = 0;
+  int32_t step0 = 0;
+  Seq q{0, 0, 0};
+  KeySpan span{0, 0, 0};
+  if (left > 0) {  // the unit and step where the share begins
+    int err = 0;
+    q = seq_of(p, b, s, err);
+    int64_t off = at.off;
+    for (;;) {
+      span = span_of(q, tile);
+      const int64_t n = static_cast<int64_t>(span.steps()) * n_groups;
+      if (off < n) break;
+      off -= n;
+      ++tile;
+    }
+    group = static_cast<int32_t>(off / span.steps());
+    step0 = static_cast<int32_t>(off - static_cast<int64_t>(group) * span.steps());
+  }
+
+  while (left > 0) {
+    const int32_t n_steps = span.steps();
+    const int32_t end = left < n_steps - step0 ? step0 + static_cast<int32_t>(left) : n_steps;
+    const int32_t h = group * w.hw + hw;
+    const int32_t f0 = tile * NQ;
+    const int32_t nf = min(NQ, q.n * a.G - f0);  // rows of the tile
+    const int32_t i0 = q.a + f0 / a.G, i1 = q.a + (f0 + nf - 1) / a.G;
+
+    // ---- issue of a step's loads
+    int32_t ent = 0;  // P16: page of step seg_base + lane (0: tombstone); else: raw entry of key lane % 16 of the next step
+    auto page_of_step = [&](int32_t i) -> int32_t {
+      if (i >= end) return 0;
+      const int64_t k = div_ps(p, static_cast<int64_t>(span.block(i)) * 16);
+      return static_cast<int32_t>(
+          page_of_entry(p, b, __ldg(b.table + static_cast<int64_t>(s) * b.max_pages + k), bits));
+    };
+    auto entry_of_key = [&](int32_t i) -> int32_t {  // general: table entry of key `lane % 16` of step i
+      const int64_t j = static_cast<int64_t>(span.block(i < end ? i : step0)) * 16 + (lane & 15);
+      return i < end && j <= i1 ? __ldg(b.table + static_cast<int64_t>(s) * b.max_pages + div_ps(p, j)) : 0;
+    };
+    int32_t seg_base = step0;  // P16: `ent` covers steps [seg_base, seg_base + 32)
+    int32_t ent_next = 0;
+    if constexpr (P16) {
+      ent = page_of_step(step0 + lane);
+      ent_next = page_of_step(step0 + 32 + lane);
+    } else {
+      ent = entry_of_key(step0);
+    }
+    auto issue = [&](int32_t i, int stage) {
+      if (i < end) {
+        const uint32_t st = ring0 + stage * Sh::kStage;
+        const int64_t j0 = static_cast<int64_t>(span.block(i)) * 16;
+        int32_t page;     // of the step (P16) or of key lane % 16
+        int32_t rk;       // row of key 0, or of key lane % 16
+        uint32_t live;    // bit k: key k is a token of the cache
+        if constexpr (P16) {
+          if (i >= seg_base + 32) {
+            seg_base += 32;
+            ent = ent_next;
+            ent_next = page_of_step(seg_base + 32 + lane);
+          }
+          page = __shfl_sync(kFull, ent, i - seg_base);
+          live = page == 0 ? 0 : j0 + 15 <= i1 ? 0xffffu : (1u << (i1 - j0 + 1)) - 1;
+          const int32_t off = p.ps_shift >= 0 ? static_cast<int32_t>(j0) & (static_cast<int32_t>(p.ps) - 1)
+                                              : static_cast<int32_t>(j0) % static_cast<int32_t>(p.ps);
+          rk = static_cast<int32_t>(page * p.stride + 2 * static_cast<int64_t>(a.layer) * p.ps) + off;
+        } else {
+          const int32_t e = ent;
+          ent = entry_of_key(i + 1);
+          const int64_t j = j0 + (lane & 15);
+          page = j <= i1 ? static_cast<int32_t>(page_of_entry(p, b, e, bits)) : 0;
+          rk = static_cast<int32_t>(page * p.stride + 2 * static_cast<int64_t>(a.layer) * p.ps + (j - div_ps(p, j) * p.ps));
+          live = __ballot_sync(kFull, page != 0) & 0xffffu;
+        }
+        auto row = [&](int key) -> int64_t {
+          if constexpr (P16)
+            return static_cast<int64_t>(rk) + key;
+          else
+            return __shfl_sync(kFull, rk, key);
+        };
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int key = g + 8 * half;
+          const int64_t r = row(key);
+          const bool ok = live >> key & 1;
+          const uint8_t* src = pool + (ok ? r * row_bytes + h * Sh::kRow + c * 16 : 0);
+#pragma unroll
+          for (int ch = 0; ch < Sh::kKC; ++ch)
+            copy_async<16>(st + (half * Sh::kKC + ch) * 512 + lane * 16, src + (ok ? ch * 64 : 0), ok);
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const int key = 2 * c + (kk & 1) + 8 * (kk >> 1);
+          const int64_t r = row(key) + p.ps;
+          const bool ok = live >> key & 1;
+          const uint8_t* src = pool + (ok ? r * row_bytes + h * Sh::kRow + g * Sh::kVB : 0);
+          if constexpr (Sh::kVB == 8) {
+            copy_async<8>(st + Sh::kK + kk * 256 + lane * 8, src, ok);
+          } else {
+#pragma unroll
+            for (int ch = 0; ch < Sh::kVB / 16; ++ch)
+              copy_async<16>(st + Sh::kK + (kk * (Sh::kVB / 16) + ch) * 512 + lane * 16, src + (ok ? ch * 16 : 0), ok);
+          }
+        }
+        if constexpr (kE4M3) {  // lanes 0-15: scales of K, 16-31: of V
+          const bool ok = live >> (lane & 15) & 1;
+          const float* sc =
+              a.scales + (ok ? (static_cast<int64_t>(page) * p.blocks + 2 * a.layer + (lane >> 4)) * a.H + h : 0);
+          copy_async<4>(st + 2 * Sh::kK + lane * 4, sc, ok);
+        }
+        if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + 2 * Sh::kK + 128), "r"(live) : "memory");
+      }
+      copy_commit();
+    };
+    for (int i = 0; i < Sh::kStages - 1; ++i) issue(step0 + i, i);
+
+    // ---- the queries, while the first loads are in flight
+    uint32_t qf[NT][Sh::kKS][2];
+    float cq[NT][2];
+    int32_t pos[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int32_t f = f0 + nt * 8 + g;
+      const bool ok = nt * 8 + g < nf;
+      const int64_t q0 = ok ? (q.row0 + f / a.G) * a.q_stride + static_cast<int64_t>(h * a.G + f % a.G) * D : 0;
+      float row_c = a.scale_log2;
+      constexpr int EC = 16 / Sh::kSize;  // elements of a lane's piece
+      if constexpr (!kE4M3) {
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) + q0;
+#pragma unroll
+        for (int ch = 0; ch < Sh::kKC; ++ch) {
+          const uint16_t* e = src + ch * 32 + c * 8;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (ok) {
+            if (w.q_wide) {
+              v = __ldg(reinterpret_cast<const uint4*>(e));
+            } else {
+              uint16_t* d = reinterpret_cast<uint16_t*>(&v);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) d[k] = __ldg(e + k);
+            }
+          }
+          qf[nt][2 * ch][0] = v.x, qf[nt][2 * ch][1] = v.y;
+          qf[nt][2 * ch + 1][0] = v.z, qf[nt][2 * ch + 1][1] = v.w;
+        }
+      } else {
+        float x[Sh::kKC][EC];
+        float amax = 0.0f;
+#pragma unroll
+        for (int ch = 0; ch < Sh::kKC; ++ch)
+#pragma unroll
+          for (int k = 0; k < EC; ++k) {
+            x[ch][k] = ok ? load_q(a, a.q, q0 + ch * 64 + c * 16 + k) : 0.0f;
+            amax = fmaxf(amax, fabsf(x[ch][k]));
+          }
+        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+        // amax * 2^k in [2^14, 2^15)
+        int k = 14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23);
+        k = amax > 0.0f ? max(-100, min(100, k)) : 0;
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+        row_c *= __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+#pragma unroll
+        for (int ch = 0; ch < Sh::kKC; ++ch)
+#pragma unroll
+          for (int wd = 0; wd < 4; ++wd) {
+            qf[nt][ch * 4 + wd][0] = pack_h(x[ch][4 * wd] * up, x[ch][4 * wd + 1] * up);
+            qf[nt][ch * 4 + wd][1] = pack_h(x[ch][4 * wd + 2] * up, x[ch][4 * wd + 3] * up);
+          }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // columns 2c and 2c + 1 of the scores
+        cq[nt][e] = __shfl_sync(kFull, row_c, (2 * c + e) * 4);
+        pos[nt][e] = q.a + min(f0 + nt * 8 + 2 * c + e, f0 + nf - 1) / a.G;
+      }
+    }
+
+    float o[Sh::kMT][NT][4];
+    float ref[NT][2], sum[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int mt = 0; mt < Sh::kMT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.0f;
+      ref[nt][0] = ref[nt][1] = kNoRef;
+      sum[nt][0] = sum[nt][1] = 0.0f;
+    }
+
+    int stage = 0;
+    for (int32_t i = step0; i < end; ++i) {
+      {
+        int ahead = stage + Sh::kStages - 1;
+        if (ahead >= Sh::kStages) ahead -= Sh::kStages;
+        issue(i + Sh::kStages - 1, ahead);
+      }
+      copy_wait<Sh::kStages - 1>();
+      __syncwarp();
+      const uint32_t st = ring0 + stage * Sh::kStage;
+      const uint32_t live = lds32(st + 2 * Sh::kK + 128);
+      const int32_t j0 = span.block(i) * 16;
+
+      // ---- scores
+      float x[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[nt][e] = 0.0f;
+#pragma unroll
+      for (int ch = 0; ch < Sh::kKC; ++ch) {
+        const uint4 u = lds128(st + ch * 512 + lane * 16), v = lds128(st + (Sh::kKC + ch) * 512 + lane * 16);
+        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+        if constexpr (kE4M3) {
+#pragma unroll
+          for (int wd = 0; wd < 4; ++wd) {
+            const uint32_t a0 = codes_lo(uu[wd]), a1 = codes_lo(vv[wd]), a2 = codes_hi(uu[wd]), a3 = codes_hi(vv[wd]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma<C>(x[nt], a0, a1, a2, a3, qf[nt][ch * 4 + wd][0], qf[nt][ch * 4 + wd][1]);
+          }
+        } else {
+#pragma unroll
+          for (int wd = 0; wd < 2; ++wd)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma<C>(x[nt], uu[2 * wd], vv[2 * wd], uu[2 * wd + 1], vv[2 * wd + 1], qf[nt][ch * 2 + wd][0],
+                     qf[nt][ch * 2 + wd][1]);
+        }
+      }
+
+      // ---- weights; x[.][0], [1]: key g, columns 2c, 2c + 1; [2], [3]: key g + 8
+      float lv[2] = {0.0f, 0.0f}, iv[2] = {1.0f, 1.0f}, sk[2] = {1.0f, 1.0f};
+      if constexpr (kE4M3) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sk[e] = __uint_as_float(lds32(st + 2 * Sh::kK + (g + 8 * e) * 4));
+          const float sv = __uint_as_float(lds32(st + 2 * Sh::kK + 64 + (g + 8 * e) * 4));
+          lv[e] = lg2(sv);
+          iv[e] = __fdividef(1.0f, sv);
+        }
+      }
+      const bool mask = live != 0xffffu || j0 + 15 > i0 || (a.window && j0 <= i1 - a.window);
+      bool over = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float t = kE4M3 ? fmaf(x[nt][e] * sk[e >> 1], cq[nt][e & 1], lv[e >> 1]) : x[nt][e] * cq[nt][e & 1];
+          if (mask) {
+            const int key = g + 8 * (e >> 1);
+            if (!(live >> key & 1) || !in_sight(a, pos[nt][e & 1], j0 + key)) t = -INFINITY;
+          }
+          x[nt][e] = t;
+          over = over || t > ref[nt][e & 1] + 8.0f;
+        }
+      if (__any_sync(kFull, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float m = fmaxf(x[nt][e], x[nt][e + 2]);
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
+            m = fmaxf(ref[nt][e], m);
+            const float keep = ex2(ref[nt][e] - m);
+            ref[nt][e] = m;
+            sum[nt][e] *= keep;
+#pragma unroll
+            for (int mt = 0; mt < Sh::kMT; ++mt) {
+              o[mt][nt][e] *= keep;
+              o[mt][nt][e + 2] *= keep;
+            }
+          }
+      }
+      // A value that is not finite must reach the rows that see its key and no
+      // other, but 0 * NaN would spread it. Where some row may not see some
+      // key, such elements are zeroed here and the rows that do see the key
+      // get a NaN denominator: they are done again, key by key, at the end.
+      if (mask) {
+        uint32_t keys = 0;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+          for (int wd = 0; wd < Sh::kVB / 4; ++wd) {
+            const uint32_t at = st + Sh::kK + (Sh::kVB == 8 ? kk * 256 + lane * 8 + wd * 4
+                                                            : (kk * (Sh::kVB / 16) + wd / 4) * 512 + lane * 16 + wd % 4 * 4);
+            const uint32_t v = lds32(at), bad = not_finite<C>(v);
+            if (bad) {
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v & ~bad) : "memory");
+              keys |= 1u << (2 * c + (kk & 1) + 8 * (kk >> 1));
+            }
+          }
+        keys = __reduce_or_sync(kFull, keys);
+        if (keys) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (keys >> (g + 8 * (e >> 1)) & 1 && x[nt][e] != -INFINITY) sum[nt][e & 1] = NAN;
+        }
+      }
+      uint32_t pb[NT][2], pl[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[e] = ex2(x[nt][e] - ref[nt][e & 1] + kLift);
+          // a dead key adds nothing, whatever its zero-filled scale's inverse is
+          if constexpr (kE4M3)
+            sum[nt][e & 1] += live >> (g + 8 * (e >> 1)) & 1 ? y[e] * iv[e >> 1] : 0.0f;
+          else
+            sum[nt][e & 1] += y[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if constexpr (FewType<C>::kSplitP) {
+            const float h0 = __bfloat162float(__float2bfloat16_rn(y[2 * e]));
+            const float h1 = __bfloat162float(__float2bfloat16_rn(y[2 * e + 1]));
+            pb[nt][e] = transpose8(pack_b(h0, h1));
+            pl[nt][e] = transpose8(pack_b(y[2 * e] - h0, y[2 * e + 1] - h1));
+          } else {
+            pb[nt][e] = transpose8(pack_h(y[2 * e], y[2 * e + 1]));
+          }
+        }
+      }
+
+      // ---- values: registers of keys 2c, 2c + 1 (a0, a1) and 2c + 8, 2c + 9 (a2, a3)
+      auto tile_mma = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma<C>(o[mt][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+          if constexpr (FewType<C>::kSplitP) mma<C>(o[mt][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+        }
+      };
+      constexpr int VC = Sh::kVB >= 16 ? Sh::kVB / 16 : 1;  // pieces of a value
+      constexpr int VW = Sh::kVB >= 16 ? 4 : 2;             // words of a piece
+#pragma unroll
+      for (int ch = 0; ch < VC; ++ch) {
+        uint32_t v[4][VW];
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          if constexpr (VW == 4) {
+            const uint4 u = lds128(st + Sh::kK + (kk * VC + ch) * 512 + lane * 16);
+            v[kk][0] = u.x, v[kk][1] = u.y, v[kk][2] = u.z, v[kk][3] = u.w;
+          } else {
+            const uint2 u = lds64(st + Sh::kK + kk * 256 + lane * 8);
+            v[kk][0] = u.x, v[kk][1] = u.y;
+          }
+        }
+#pragma unroll
+        for (int wd = 0; wd < VW; ++wd) {
+          if constexpr (kE4M3) {
+            const uint32_t x0 = __byte_perm(v[0][wd], v[1][wd], 0x5140), y0 = __byte_perm(v[0][wd], v[1][wd], 0x7362);
+            const uint32_t x1 = __byte_perm(v[2][wd], v[3][wd], 0x5140), y1 = __byte_perm(v[2][wd], v[3][wd], 0x7362);
+            tile_mma(ch * 8 + 2 * wd, codes_lo(x0), codes_hi(x0), codes_lo(x1), codes_hi(x1));
+            tile_mma(ch * 8 + 2 * wd + 1, codes_lo(y0), codes_hi(y0), codes_lo(y1), codes_hi(y1));
+          } else {
+            tile_mma(ch * 4 + wd, __byte_perm(v[0][wd], v[1][wd], 0x5410), __byte_perm(v[0][wd], v[1][wd], 0x7632),
+                     __byte_perm(v[2][wd], v[3][wd], 0x5410), __byte_perm(v[2][wd], v[3][wd], 0x7632));
+          }
+        }
+      }
+      if (++stage == Sh::kStages) stage = 0;
+      __syncwarp();  // the stage's scales and mask are free for the next issue
+    }
+    copy_wait<0>();
+
+    // ---- the segment's end. o[mt][nt]: elements g D/8 + 2 mt (+ 1: [2], [3]) of columns 2c, 2c + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sum[nt][e] += __shfl_xor_sync(kFull, sum[nt][e], 4);
+        sum[nt][e] += __shfl_xor_sync(kFull, sum[nt][e], 8);
+        sum[nt][e] += __shfl_xor_sync(kFull, sum[nt][e], 16);
+      }
+    const bool whole = step0 == 0 && end == n_steps;
+    if (whole) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int col = nt * 8 + 2 * c + e;
+          const int32_t f = f0 + col;
+          const float inv = sum[nt][e] == 0.0f ? 0.0f : __fdividef(1.0f, sum[nt][e]);
+          bool bad = !(sum[nt][e] <= 3.402823466e38f);
+          const int64_t r = q.row0 + f / a.G;
+          const int32_t qh = h * a.G + f % a.G;
+#pragma unroll
+          for (int mt = 0; mt < Sh::kMT; ++mt) {
+            const float y0 = o[mt][nt][e] * inv, y1 = o[mt][nt][e + 2] * inv;
+            bad = bad || !(fabsf(y0) <= 3.402823466e38f) || !(fabsf(y1) <= 3.402823466e38f);
+            if (col < nf) {
+              const uint32_t y = a.type == KV_TYPE_BF16 ? pack_b(y0, y1) : pack_h(y0, y1);
+              uint16_t* out = static_cast<uint16_t*>(a.out) + (r * a.Q + qh) * D + g * (D / 8) + 2 * mt;
+              if (w.out_wide) {
+                *reinterpret_cast<uint32_t*>(out) = y;
+              } else {
+                out[0] = static_cast<uint16_t>(y);
+                out[1] = static_cast<uint16_t>(y >> 16);
+              }
+            }
+          }
+          if (a.lse && g == 0 && col < nf)
+            a.lse[r * a.Q + qh] = sum[nt][e] == 0.0f ? -INFINITY : (ref[nt][e] - kLift + log2f(sum[nt][e])) * kLn2;
+          // columns with anything not finite are done again, key by key
+          const uint32_t again = __ballot_sync(kFull, bad && col < nf);
+          if (again) {
+            __syncwarp();
+            for (int k = 0; k < 4; ++k)
+              if (again & (0x11111111u << k)) {
+                const int32_t ff = f0 + nt * 8 + 2 * k + e;
+                attend_row<C>(p, b, a, s, q.a + ff / a.G, q.row0 + ff / a.G, h * a.G + ff % a.G, &bits);
+              }
+          }
+        }
+    } else {
+      const int slot = step0 == 0 ? 1 : 0;
+      float* part = w.part + ((worker * w.hw + hw) * 2 + slot) * static_cast<int64_t>(NQ * (D + 2));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int col = nt * 8 + 2 * c + e;
+#pragma unroll
+          for (int mt = 0; mt < Sh::kMT; mt += 2)
+            *reinterpret_cast<float4*>(part + col * D + g * (D / 8) + 2 * mt) =
+                make_float4(o[mt][nt][e], o[mt][nt][e + 2], o[mt + 1][nt][e], o[mt + 1][nt][e + 2]);
+          if (g == 0) {
+            part[NQ * D + col] = ref[nt][e];
+            part[NQ * (D + 1) + col] = sum[nt][e];
+          }
+        }
+      if (slot == 1) {
+        rec.s = s;
+        rec.tile = tile;
+        rec.head = group;
+      } else {
+        rec.cont = end == n_steps ? 3 : 1;
+      }
+    }
+    left -= end - step0;
+
+    // ---- the next unit
+    step0 = 0;
+    if (left > 0 && ++group == n_groups) {
+      group = 0;
+      ++tile;
+      while (tile >= tiles_of(q)) {
+        tile = 0;
+        if (++s >= b.n_seqs) break;
+        int err = 0;
+        q = seq_of(p, b, s, err);
+      }
+      if (s >= b.n_seqs) break;
+      span = span_of(q, tile);
+    }
+  }
+  if (w.join && worker < w.n_workers && hw == 0 && lane == 0) w.rec[worker] = rec;
+  store_bits(p, bits);
+}
+
+// Joins the partial sums of units that were cut: block x looks at worker x's
+// unfinished unit and adds the continuing segments of the workers after it, one
+// warp a row, in the workers' order.
+template <class C, int D, int NT>
+__global__ void __launch_bounds__(kFewBlock) k_attend_join(DevPool p, Batch b, AttendArgs a, FewSplit w) {
+  constexpr int NQ = 8 * NT;
+  constexpr int E = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t worker = blockIdx.x;
+  const SplitRecord rec = w.rec[worker];
+  if (rec.s < 0) return;
+  int64_t last = worker + 1;
+  while (last + 1 < w.n_workers && !(w.rec[last].cont & 2)) ++last;
+  const int lane = threadIdx.x & 31;
+  const int item = blockIdx.y * kFewWarps + (threadIdx.x >> 5);  // (head of the group, column)
+  const int hw = item / NQ, col = item - hw * NQ;
+  int bits = 0;
+  const Seq q = seq_of(p, b, rec.s, bits);
+  const int32_t f = rec.tile * NQ + col;
+  if (hw >= w.hw || f >= q.n * a.G) return;
+  auto part = [&](int64_t k) {
+    return w.part + ((k * w.hw + hw) * 2 + (k == worker ? 1 : 0)) * static_cast<int64_t>(NQ * (D + 2));
+  };
+  float m = kNoRef;
+  for (int64_t k = worker + lane; k <= last; k += 32) m = fmaxf(m, part(k)[NQ * D + col]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  float acc[E], sum = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll 4
+  for (int64_t k = worker; k <= last; ++k) {
+    const float* x = part(k);
+    const float f_ = ex2(x[NQ * D + col] - m);
+    sum += x[NQ * (D + 1) + col] * f_;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] += x[col * D + lane * E + e] * f_;
+  }
+  const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+  bool bad = !(sum <= 3.402823466e38f);
+  const int64_t r = q.row0 + f / a.G;
+  const int32_t qh = (rec.head * w.hw + hw) * a.G + f % a.G;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float y = acc[e] * inv;
+    bad = bad || !(fabsf(y) <= 3.402823466e38f);
+    store_out(a, (r * a.Q + qh) * D + lane * E + e, y);
+  }
+  if (a.lse && lane == 0)
+    a.lse[r * a.Q + qh] = sum == 0.0f ? -INFINITY : (m - FewType<C>::kLift + log2f(sum)) * kLn2;
+  if (__any_sync(kFull, bad)) {
+    __syncwarp();
+    attend_row<C>(p, b, a, rec.s, q.a + f / a.G, r, qh, &bits);
+  }
+  store_bits(p, bits);
+}
+
+template <class C, int D, int NT>
+cudaError_t launch(const DevPool& p, const Batch& b, const AttendArgs& a, FewSplit w, cudaStream_t s) {
+  using Sh = FewShape<C, D>;
+  auto kernel = p.ps % 16 == 0 ? k_attend_few<C, D, NT, true> : k_attend_few<C, D, NT, false>;
+  kernel<<<w.blocks, kFewBlock, Sh::kSmem, s>>>(p, b, a, w);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !w.join) return e;
+  // the join may start while the kernel before it drains; it waits for that kernel's end itself
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(w.n_workers), static_cast<unsigned>((w.hw * 8 * NT + kFewWarps - 1) / kFewWarps));
+  cfg.blockDim = dim3(kFewBlock);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_attend_join<C, D, NT>, p, b, a, w);
+}
+
+template <class C>
+cudaError_t launch_c(const DevPool& p, const Batch& b, const AttendArgs& a, const FewSplit& w, int nt, cudaStream_t s) {
+  if (a.D == 64) return nt == 1 ? launch<C, 64, 1>(p, b, a, w, s) : launch<C, 64, 2>(p, b, a, w, s);
+  return nt == 1 ? launch<C, 128, 1>(p, b, a, w, s) : launch<C, 128, 2>(p, b, a, w, s);
+}
+
+template <class C, int D, int NT>
+cudaError_t prepare_one() {
+  cudaError_t e = cudaFuncSetAttribute(k_attend_few<C, D, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       FewShape<C, D>::kSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_attend_few<C, D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             FewShape<C, D>::kSmem);
+  return e;
+}
+
+template <class C>
+cudaError_t prepare_c() {
+  cudaError_t e = prepare_one<C, 64, 1>();
+  if (e == cudaSuccess) e = prepare_one<C, 64, 2>();
+  if (e == cudaSuccess) e = prepare_one<C, 128, 1>();
+  if (e == cudaSuccess) e = prepare_one<C, 128, 2>();
+  return e;
+}
+
+constexpr int kMinShare = 8;  // steps of 16 keys below which a worker's share is not cut
+
+int heads_of_worker(int32_t H) { return H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1; }
+
+}  // namespace
+
+cudaError_t prepare_attend_few() {
+  cudaError_t e = prepare_c<CodeE4M3>();
+  if (e == cudaSuccess) e = prepare_c<__half>();
+  if (e == cudaSuccess) e = prepare_c<__nv_bfloat16>();
+  return e;
+}
+
+int64_t attend_few_workspace(int32_t H, int32_t D, int sm_count) {
+  const int64_t warps = static_cast<int64_t>(sm_count) * kFewBlocksPerSM * kFewWarps;
+  const int64_t rec = (warps * static_cast<int64_t>(sizeof(SplitRecord)) + 255) / 256 * 256;
+  return rec + warps * 2 * 16 * (D + 2) * 4;
+}
+
+cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs& a, bool e4m3, int32_t max_new,
+                              void* workspace, int sm_count, cudaStream_t s) {
+  FewSplit w{};
+  w.hw = heads_of_worker(a.H);
+  w.max_new = max_new;
+  const int kw = kFewWarps / w.hw;
+  const int nt = a.G * static_cast<int64_t>(b.n_rows < max_new ? b.n_rows : max_new) <= 8 ? 1 : 2;
+  // steps of one unit at most, and of all units
+  int64_t most = static_cast<int64_t>(b.max_pages) * p.ps / 16 + 1;
+  if (a.window) {
+    const int64_t seen = (static_cast<int64_t>(a.window) + max_new) / 16 + 2 + (a.sinks + 15) / 16;
+    most = seen < most ? seen : most;
+  }
+  const int64_t tiles = (b.n_rows * a.G) / (8 * nt) + b.n_seqs;  // row tiles of all sequences
+  const int64_t all = most * tiles * (a.H / w.hw);
+  const int64_t cap = static_cast<int64_t>(sm_count) * kFewBlocksPerSM * kw;
+  w.min_share = kMinShare;
+  int64_t workers = (all + w.min_share - 1) / w.min_share;
+  workers = workers > cap ? cap : workers;
+  w.blocks = static_cast<int>((workers + kw - 1) / kw);
+  w.n_workers = static_cast<int64_t>(w.blocks) * kw;
+  w.join = 1;
+  w.rec = static_cast<SplitRecord*>(workspace);
+  const int64_t warps = static_cast<int64_t>(sm_count) * kFewBlocksPerSM * kFewWarps;
+  w.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                    (warps * static_cast<int64_t>(sizeof(SplitRecord)) + 255) / 256 * 256);
+  w.q_wide = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.q_stride % 8 == 0;
+  w.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 3u) == 0;
+  if (e4m3) return launch_c<CodeE4M3>(p, b, a, w, nt, s);
+  if (a.type == KV_TYPE_BF16) return launch_c<__nv_bfloat16>(p, b, a, w, nt, s);
+  return launch_c<__half>(p, b, a, w, nt, s);
+}
+
+}  // namespace gtkv

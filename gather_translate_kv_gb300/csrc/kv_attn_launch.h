@@ -30,6 +30,8 @@ struct AttendArgs {
   int32_t type;         // KV_TYPE_BF16 or KV_TYPE_F16, of q and out
 };
 
+// Per-device set-up of the attention kernels (their shared-memory limits); called by kv_pool_create.
+cudaError_t prepare_attend();
 int64_t attend_workspace_bytes(int32_t H, int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int sm_count);
 cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, bool e4m3, void* workspace,
                           int sm_count, cudaStream_t s);
