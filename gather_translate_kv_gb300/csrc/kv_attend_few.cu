@@ -28,9 +28,7 @@
 // Workers (as many warps as share a step's heads) take equal shares of all
 // steps of the batch (kv_attend_split.cuh); units cut at a border are joined by
 // k_attend_join from 32-bit partial sums in the workspace.
-#include <type_traits>
-
-#include "kv_attend_few.h"
+#include "kv_attend_launch.h"
 #include "kv_attend_split.cuh"
 
 namespace gtkv {
@@ -40,8 +38,6 @@ namespace {
 constexpr int kFewWarps = 4;
 constexpr int kFewBlock = 32 * kFewWarps;
 constexpr int kFewBlocksPerSM = 3;
-constexpr float kNoRef = -1e30f;  // reference before the first key; finite, so that -inf - m stays -inf
-
 template <class C>
 struct FewType {
   static constexpr int kSize = 2;       // bytes per cached element
@@ -60,24 +56,6 @@ struct FewType<__nv_bfloat16> {
   static constexpr bool kSplitP = true;
   static constexpr float kLift = 0.0f;
 };
-
-__device__ __forceinline__ uint32_t shared_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-template <int N>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool ok) {
-  const int n = ok ? N : 0;  // 0: the bytes become zero
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 v;
@@ -115,49 +93,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// Two e4m3 codes (bytes 0 and 1 of a half word) as two fp16.
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
-  uint32_t y;
-  asm("{.reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(y) : "r"(w));
-  return y;
-}
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
-  uint32_t y;
-  asm("{.reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(y) : "r"(w));
-  return y;
-}
-
-// All ones in the elements of a word of cached values that are not finite.
-template <class C>
-__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-  if constexpr (std::is_same_v<C, CodeE4M3>)
-    return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
-  else if constexpr (std::is_same_v<C, __half>)
-    return __vcmpeq2(w & 0x7c007c00u, 0x7c007c00u);
-  else
-    return __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u);
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_h(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t pack_b(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 template <class C, int D>
 struct FewShape {
   static constexpr int kSize = FewType<C>::kSize;
@@ -178,7 +113,7 @@ struct FewShape {
 // read on its own, one step ahead.
 template <class C, int D, int NT, bool P16>
 __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
-    k_attend_few(DevPool p, Batch b, AttendArgs a, FewSplit w) {
+    k_attend_few(DevPool p, Batch b, AttendArgs a, Split w) {
   using Sh = FewShape<C, D>;
   constexpr bool kE4M3 = std::is_same_v<C, CodeE4M3>;
   constexpr float kLift = FewType<C>::kLift;
@@ -679,89 +614,21 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
       span = span_of(q, tile);
     }
   }
-  if (w.join && worker < w.n_workers && hw == 0 && lane == 0) w.rec[worker] = rec;
-  store_bits(p, bits);
-}
-
-// Joins the partial sums of units that were cut: block x looks at worker x's
-// unfinished unit and adds the continuing segments of the workers after it, one
-// warp a row, in the workers' order.
-template <class C, int D, int NT>
-__global__ void __launch_bounds__(kFewBlock) k_attend_join(DevPool p, Batch b, AttendArgs a, FewSplit w) {
-  constexpr int NQ = 8 * NT;
-  constexpr int E = D / 32;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t worker = blockIdx.x;
-  const SplitRecord rec = w.rec[worker];
-  if (rec.s < 0) return;
-  int64_t last = worker + 1;
-  while (last + 1 < w.n_workers && !(w.rec[last].cont & 2)) ++last;
-  const int lane = threadIdx.x & 31;
-  const int item = blockIdx.y * kFewWarps + (threadIdx.x >> 5);  // (head of the group, column)
-  const int hw = item / NQ, col = item - hw * NQ;
-  int bits = 0;
-  const Seq q = seq_of(p, b, rec.s, bits);
-  const int32_t f = rec.tile * NQ + col;
-  if (hw >= w.hw || f >= q.n * a.G) return;
-  auto part = [&](int64_t k) {
-    return w.part + ((k * w.hw + hw) * 2 + (k == worker ? 1 : 0)) * static_cast<int64_t>(NQ * (D + 2));
-  };
-  float m = kNoRef;
-  for (int64_t k = worker + lane; k <= last; k += 32) m = fmaxf(m, part(k)[NQ * D + col]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-  float acc[E], sum = 0.0f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-  for (int64_t k = worker; k <= last; ++k) {
-    const float* x = part(k);
-    const float f_ = ex2(x[NQ * D + col] - m);
-    sum += x[NQ * (D + 1) + col] * f_;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += x[col * D + lane * E + e] * f_;
-  }
-  const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
-  bool bad = !(sum <= 3.402823466e38f);
-  const int64_t r = q.row0 + f / a.G;
-  const int32_t qh = (rec.head * w.hw + hw) * a.G + f % a.G;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float y = acc[e] * inv;
-    bad = bad || !(fabsf(y) <= 3.402823466e38f);
-    store_out(a, (r * a.Q + qh) * D + lane * E + e, y);
-  }
-  if (a.lse && lane == 0)
-    a.lse[r * a.Q + qh] = sum == 0.0f ? -INFINITY : (m - FewType<C>::kLift + log2f(sum)) * kLn2;
-  if (__any_sync(kFull, bad)) {
-    __syncwarp();
-    attend_row<C>(p, b, a, rec.s, q.a + f / a.G, r, qh, &bits);
-  }
+  if (worker < w.n_workers && hw == 0 && lane == 0) w.rec[worker] = rec;
   store_bits(p, bits);
 }
 
 template <class C, int D, int NT>
-cudaError_t launch(const DevPool& p, const Batch& b, const AttendArgs& a, FewSplit w, cudaStream_t s) {
+cudaError_t launch(const DevPool& p, const Batch& b, const AttendArgs& a, Split w, cudaStream_t s) {
   using Sh = FewShape<C, D>;
   auto kernel = p.ps % 16 == 0 ? k_attend_few<C, D, NT, true> : k_attend_few<C, D, NT, false>;
   kernel<<<w.blocks, kFewBlock, Sh::kSmem, s>>>(p, b, a, w);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !w.join) return e;
-  // the join may start while the kernel before it drains; it waits for that kernel's end itself
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(w.n_workers), static_cast<unsigned>((w.hw * 8 * NT + kFewWarps - 1) / kFewWarps));
-  cfg.blockDim = dim3(kFewBlock);
-  cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_attend_join<C, D, NT>, p, b, a, w);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? launch_join<C, D>(p, b, a, w, s) : e;
 }
 
 template <class C>
-cudaError_t launch_c(const DevPool& p, const Batch& b, const AttendArgs& a, const FewSplit& w, int nt, cudaStream_t s) {
+cudaError_t launch_c(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, int nt, cudaStream_t s) {
   if (a.D == 64) return nt == 1 ? launch<C, 64, 1>(p, b, a, w, s) : launch<C, 64, 2>(p, b, a, w, s);
   return nt == 1 ? launch<C, 128, 1>(p, b, a, w, s) : launch<C, 128, 2>(p, b, a, w, s);
 }
@@ -800,13 +667,12 @@ cudaError_t prepare_attend_few() {
 
 int64_t attend_few_workspace(int32_t H, int32_t D, int sm_count) {
   const int64_t warps = static_cast<int64_t>(sm_count) * kFewBlocksPerSM * kFewWarps;
-  const int64_t rec = (warps * static_cast<int64_t>(sizeof(SplitRecord)) + 255) / 256 * 256;
-  return rec + warps * 2 * 16 * (D + 2) * 4;
+  return split_record_bytes(warps) + warps * 2 * 16 * (D + 2) * 4;
 }
 
 cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs& a, bool e4m3, int32_t max_new,
                               void* workspace, int sm_count, cudaStream_t s) {
-  FewSplit w{};
+  Split w{};
   w.hw = heads_of_worker(a.H);
   w.max_new = max_new;
   const int kw = kFewWarps / w.hw;
@@ -825,13 +691,13 @@ cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs
   workers = workers > cap ? cap : workers;
   w.blocks = static_cast<int>((workers + kw - 1) / kw);
   w.n_workers = static_cast<int64_t>(w.blocks) * kw;
-  w.join = 1;
   w.rec = static_cast<SplitRecord*>(workspace);
   const int64_t warps = static_cast<int64_t>(sm_count) * kFewBlocksPerSM * kFewWarps;
-  w.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                    (warps * static_cast<int64_t>(sizeof(SplitRecord)) + 255) / 256 * 256);
+  w.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + split_record_bytes(warps));
+  w.nq = 8 * nt;
+  w.lift = !e4m3 && a.type == KV_TYPE_BF16 ? FewType<__nv_bfloat16>::kLift : FewType<__half>::kLift;
   w.q_wide = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.q_stride % 8 == 0;
-  w.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 3u) == 0;
+  w.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
   if (e4m3) return launch_c<CodeE4M3>(p, b, a, w, nt, s);
   if (a.type == KV_TYPE_BF16) return launch_c<__nv_bfloat16>(p, b, a, w, nt, s);
   return launch_c<__half>(p, b, a, w, nt, s);

@@ -1,0 +1,786 @@
+// Attention of many rows a sequence (prompts, chunks, long drafts) on the
+// 5th-generation tensor cores.
+//
+// A block owns a unit: up to 256 rows of one KV head of a sequence, a row being
+// a (token, query head of the group) pair, as two tiles of 128 rows. For each 128 keys
+//   S_w = Q_w K^T   (tile w of rows; both operands in shared memory)
+//   P_w = 2^(t - m) (softmax warps; written over S_w in tensor memory)
+//   O_w += P_w V    (P_w from tensor memory, V as the M/N-major operand)
+// with S_0, S_1, O_0, O_1 filling the 512 columns of tensor memory. The two
+// tiles alternate: while four warps turn S_0 into P_0 the tensor cores work on tile 1
+// and the other way round, which is what bounds the kernel: per 128 keys and
+// tile 4 * 128 * 128 * D operations on the tensor cores against 128 * 128
+// exponentials.
+//
+// Warps 0-3 and 4-7: softmax of tile 0 and 1, one row a thread (no shuffles).
+// Warps 8-11: loaders; they look up the pages, copy keys and values into the
+// 128-byte-swizzled operand layout with cp.async (16-bit caches) or through
+// registers, turning codes into fp16 (8-bit caches), and zero what is no live
+// token. Pages of any size end anywhere in a tile, so keys are placed row by
+// row rather than by a tensor map. Warp 12 issues the products.
+//
+// The running reference m of a row moves only when a tile's maximum exceeds it
+// by 2^8; only then is O read back and scaled. Weights meet the values as the cache's 16-bit type (bf16, or
+// fp16 lifted by 2^6 for fp16 and 8-bit caches); denominators add the 32-bit weights. The scale of
+// an 8-bit value is part of its weight, t = score * log2(e) + log2(scale), and
+// the denominator adds weight / scale. Queries for 8-bit caches become fp16
+// after a power-of-two scaling per row.
+//
+// Work is cut as in kv_attend_split.cuh, 128 keys a step.
+#include "kv_attend_launch.h"
+#include "kv_attend_split.cuh"
+#include "kv_umma.cuh"
+
+namespace gtkv {
+
+namespace {
+
+constexpr int kTileThreads = 512;  // 13 working warps; the launch's registers are split among four groups
+constexpr int kRows = 256;         // rows of a unit
+constexpr int kKeys = 128;         // keys of a step
+constexpr int kSlots = 4;          // steps whose scales and masks are kept
+
+struct Slot {
+  float ks[kKeys];   // scale of the key
+  float lv[kKeys];   // log2 of the value's scale
+  float iv[kKeys];   // its inverse
+  uint32_t live[4];  // keys that are tokens
+  uint32_t nan[4];   // keys whose value had elements that are not finite (zeroed)
+};
+
+enum Bar { kQFull, kQFree, kKFull, kKFree = kKFull + 2, kVFull = kKFree + 2, kVFree = kVFull + 2, kSFull = kVFree + 2,
+           kPReady = kSFull + 2, kODone = kPReady + 2, kDrain = kODone + 2, kBars };
+
+template <int D>
+struct TileSmem {
+  static constexpr int kOperand = 128 * D * 2;        // a tile of Q, K or V
+  static constexpr int kQ = 0;                        // two tiles
+  static constexpr int kK = 2 * kOperand;             // two stages
+  static constexpr int kV = 4 * kOperand;             // two stages
+  static constexpr int kSlot = 6 * kOperand;
+  static constexpr int kQScale = kSlot + kSlots * static_cast<int>(sizeof(Slot));
+  static constexpr int kBar = kQScale + kRows * 4;
+  static constexpr int kMisc = kBar + kBars * 8;      // tensor memory address, stop word
+  static constexpr int kBytes = kMisc + 16 + 1024;    // + room to align to the swizzle's 1024 bytes
+};
+
+// One segment of a block's share: steps [step0, end) of a unit.
+struct Segment {
+  Seq q;
+  KeySpan span;
+  int32_t s, tile, h;
+  int32_t step0, end;
+  int32_t f0, nf;  // rows
+};
+
+template <bool kE4M3>
+struct TileWalk {
+  const DevPool& p;
+  const Batch& b;
+  const AttendArgs& a;
+  const Split& w;
+  int64_t left;
+  Segment g;
+
+  __device__ __forceinline__ int32_t tiles() const {
+    return g.q.n < w.min_new || g.q.n == 0 ? 0 : static_cast<int32_t>((static_cast<int64_t>(g.q.n) * a.G + kRows - 1) / kRows);
+  }
+  __device__ __forceinline__ void shape() {
+    g.f0 = g.tile * kRows;
+    g.nf = min(kRows, g.q.n * a.G - g.f0);
+    g.span = key_span<kKeys>(a, g.q, g.f0, g.f0 + g.nf);
+  }
+  __device__ __forceinline__ void cut() {
+    const int32_t n = g.span.steps() - g.step0;
+    g.end = g.step0 + static_cast<int32_t>(left < n ? left : n);
+  }
+  // The first segment of a share; false when there is none.
+  __device__ bool start(const ShareStart& at, int64_t share) {
+    left = at.s < 0 ? 0 : share;
+    if (left == 0) return false;
+    int err = 0;
+    g.s = at.s;
+    g.tile = 0;
+    g.q = seq_of(p, b, g.s, err);
+    int64_t off = at.off;
+    for (;;) {
+      shape();
+      const int64_t n = static_cast<int64_t>(g.span.steps()) * a.H;
+      if (off < n) break;
+      off -= n;
+      ++g.tile;
+    }
+    g.h = static_cast<int32_t>(off / g.span.steps());
+    g.step0 = static_cast<int32_t>(off - static_cast<int64_t>(g.h) * g.span.steps());
+    cut();
+    return true;
+  }
+  __device__ bool next() {
+    left -= g.end - g.step0;
+    if (left <= 0) return false;
+    g.step0 = 0;
+    if (++g.h == a.H) {
+      g.h = 0;
+      ++g.tile;
+      while (g.tile >= tiles()) {
+        g.tile = 0;
+        if (++g.s >= b.n_seqs) return false;
+        int err = 0;
+        g.q = seq_of(p, b, g.s, err);
+      }
+      shape();
+    }
+    cut();
+    return true;
+  }
+};
+
+__device__ __forceinline__ void sts128(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+// Byte offset of 16-byte piece `ch` (of D / 8) of row `row` in a swizzled operand tile.
+__device__ __forceinline__ uint32_t piece_at(int row, int ch) {
+  return static_cast<uint32_t>((ch >> 3) * (128 * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+}
+
+// 16 codes as two pieces of 8 fp16.
+__device__ __forceinline__ void decode16(const uint4& v, uint4& lo, uint4& hi) {
+  lo = make_uint4(codes_lo(v.x), codes_hi(v.x), codes_lo(v.y), codes_hi(v.y));
+  hi = make_uint4(codes_lo(v.z), codes_hi(v.z), codes_lo(v.w), codes_hi(v.w));
+}
+
+__device__ __forceinline__ float2 ffma2(float2 x, float2 y, float2 z) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+  return r;
+}
+
+template <class C, int D>
+__global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batch b, AttendArgs a, Split w) {
+  using Sm = TileSmem<D>;
+  constexpr bool kE4M3 = std::is_same_v<C, CodeE4M3>;
+  constexpr bool kBf16 = std::is_same_v<C, __nv_bfloat16>;
+  constexpr float kLift = kBf16 ? 0.0f : 6.0f;
+  constexpr int kPieces = D / 8;  // 16-byte pieces of a 16-bit row
+  extern __shared__ uint8_t dyn[];
+  __shared__ ShareStart loc[1];
+  __shared__ int64_t tmp[kTileThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t base = (shared_u32(dyn) + 1023u) & ~1023u;
+  uint8_t* gen = dyn + (base - shared_u32(dyn));
+  volatile int* stop = reinterpret_cast<volatile int*>(gen + Sm::kMisc + 8);
+  Slot* slots = reinterpret_cast<Slot*>(gen + Sm::kSlot);
+  float* qscale = reinterpret_cast<float*>(gen + Sm::kQScale);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto bar = [&](int i) -> uint32_t { return base + Sm::kBar + i * 8; };
+  int bits = 0;
+
+  if (warp == 12) tmem_alloc(base + Sm::kMisc, 512);
+  if (tid == 0) {
+    stop[0] = stop[1] = 0;  // [1]: some row is not finite
+    for (int i = 0; i < kBars; ++i) {
+      const bool loads = i == kQFull || (i >= kKFull && i < kKFree) || (i >= kVFull && i < kVFree);
+      const bool soft = i >= kPReady && i < kODone;
+      mbar_init_n(bar(i), loads || soft ? 128 : 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  TileWalk<kE4M3> walk{p, b, a, w, 0, {}};
+  const int64_t share = find_shares<kTileThreads, 1>(b.n_seqs, blockIdx.x, w.n_workers, w.min_share, loc, tmp,
+                                                     [&](int32_t s) -> int64_t {
+                                                       int err = 0;
+                                                       walk.g.q = seq_of(p, b, s, err);
+                                                       if (blockIdx.x == 0) bits |= err;
+                                                       int64_t n = 0;
+                                                       for (walk.g.tile = 0; walk.g.tile < walk.tiles(); ++walk.g.tile) {
+                                                         walk.shape();
+                                                         n += walk.g.span.steps();
+                                                       }
+                                                       return n * a.H;
+                                                     });
+  tmem_before_sync();
+  __syncthreads();
+  tmem_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gen + Sm::kMisc);
+  bool more = walk.start(loc[0], share);
+  const Segment& g = walk.g;
+
+  if (warp < 8) {
+    // ------------------------------------------------------------- softmax
+    const int wt = warp >> 2;                       // tile of rows
+    const int r = tid & 127;                        // row of the tile
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t tS = lanes + wt * 128, tO = lanes + 256 + wt * D;
+    uint32_t n = 0;       // steps of the block so far
+    uint32_t mine = 0;    // of them, steps of this tile
+    uint32_t done = 0;    // units of this tile
+    SplitRecord rec{-1, 0, 0, 0};
+    // the queries carry the scale's sign; a scale of 0 must keep -inf * c = -inf
+    const float c0 = fmaxf(fabsf(a.scale_log2), 1e-37f);
+    bool ok = true;
+    for (; more && ok; more = walk.next()) {
+      const bool here = wt * 128 < g.nf;  // the unit has rows in this tile
+      if (g.step0 > 0 || g.end < g.span.steps()) {
+        if (g.step0 == 0)
+          rec.s = g.s, rec.tile = g.tile, rec.head = g.h;
+        else
+          rec.cont = g.end == g.span.steps() ? 3 : 1;
+      }
+      if (!here) {
+        n += g.end - g.step0;
+        continue;
+      }
+      const int32_t f = g.f0 + wt * 128 + r;
+      const int32_t fc = min(f, g.f0 + g.nf - 1);
+      const bool row_ok = f < g.f0 + g.nf;
+      const int32_t pos = g.q.a + fc / a.G;
+      const int32_t i0 = g.q.a + (g.f0 + wt * 128) / a.G;
+      const int32_t i1 = g.q.a + min(g.f0 + wt * 128 + 127, g.f0 + g.nf - 1) / a.G;
+      float c = c0;
+      float ref = kNoRef;
+      float2 sum = make_float2(0.0f, 0.0f);
+      for (int32_t i = g.step0; i < g.end && ok; ++i, ++n, ++mine) {
+        ok = wait_or_stop(bar(kSFull + wt), mine & 1, stop);
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        tmem_after_sync();
+        const Slot& sl = slots[n % kSlots];
+        const int32_t j0 = g.span.block(i) * kKeys;
+        if (kE4M3 && i == g.step0) c = c0 * qscale[wt * 128 + r];
+        const uint4 live = *reinterpret_cast<const uint4*>(sl.live);
+        const bool cut = j0 + kKeys - 1 > i0 || (a.window && j0 <= i1 - a.window);
+        const bool dead = (live.x & live.y & live.z & live.w) != 0xffffffffu;
+        // columns [lo, hi] and those below `first` are in sight
+        const int hi = pos - j0;
+        const int lo = a.window ? pos - a.window + 1 - j0 : -1;
+        const int first = a.window ? a.sinks - j0 : 0;
+        // scores of 32 columns: raw (16-bit caches) or as exponents of two (8-bit), -inf where not in sight
+        auto scores = [&](int k, uint32_t (&raw)[32]) {
+          if constexpr (kE4M3) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 ks = *reinterpret_cast<const float4*>(sl.ks + 32 * k + e);
+              const float4 lv = *reinterpret_cast<const float4*>(sl.lv + 32 * k + e);
+              raw[e] = __float_as_uint(fmaf(__uint_as_float(raw[e]) * ks.x, c, lv.x));
+              raw[e + 1] = __float_as_uint(fmaf(__uint_as_float(raw[e + 1]) * ks.y, c, lv.y));
+              raw[e + 2] = __float_as_uint(fmaf(__uint_as_float(raw[e + 2]) * ks.z, c, lv.z));
+              raw[e + 3] = __float_as_uint(fmaf(__uint_as_float(raw[e + 3]) * ks.w, c, lv.w));
+            }
+          }
+          constexpr uint32_t kNone = 0xff800000u;  // -inf
+          if (cut) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * k + e > hi || (32 * k + e < lo && 32 * k + e >= first)) raw[e] = kNone;
+          }
+          if (dead) {
+            const uint32_t lw = k == 0 ? live.x : k == 1 ? live.y : k == 2 ? live.z : live.w;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(lw >> e & 1)) raw[e] = kNone;
+          }
+        };
+        uint32_t ra[32], rb[32];
+        auto buf = [&](int k) -> uint32_t(&)[32] { return k & 1 ? rb : ra; };
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        tmem_load32(tS, ra);
+        tmem_wait_ld(ra);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t(&x)[32] = buf(k);
+          if (k < 3) tmem_load32(tS + 32 * (k + 1), buf(k + 1));
+          scores(k, x);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(x[e]));
+          if (k < 3) tmem_wait_ld(buf(k + 1));
+        }
+        float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (!kE4M3) m *= c;
+        const bool move = m > ref + 8.0f;
+        if (__any_sync(kFull, move)) {
+          const float next = move ? m : ref;
+          const float keep = ex2(ref - next);
+          ref = next;
+          sum.x *= keep;
+          sum.y *= keep;
+          if (i > g.step0) {  // the products so far are done: the score product was issued after them
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+              tmem_load32(tO + 32 * k, ra);
+              tmem_wait_ld(ra);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ra[e] = __float_as_uint(__uint_as_float(ra[e]) * keep);
+              tmem_store32(tO + 32 * k, ra);
+            }
+          }
+        }
+        if (cut || dead) {
+          // values that are not finite were zeroed; rows that see such a key are done again at the end
+          ok = wait_or_stop(bar(kVFull + (n & 1)), (n >> 1) & 1, stop);
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+          const uint4 nan4 = *reinterpret_cast<const uint4*>(sl.nan);
+          if (nan4.x | nan4.y | nan4.z | nan4.w) {
+            const uint32_t nw[4] = {nan4.x, nan4.y, nan4.z, nan4.w};
+            for (int e = 0; e < kKeys; ++e)
+              if (nw[e >> 5] >> (e & 31) & 1 && in_sight(a, pos, j0 + e)) sum.x = NAN;
+          }
+        }
+        // weights; those of 32 keys fill 16 columns, all of them below the scores still to be read
+        const float off = kLift - ref;
+        const float2 off2 = make_float2(off, off), c2 = kE4M3 ? make_float2(1.0f, 1.0f) : make_float2(c, c);
+        tmem_load32(tS, ra);
+        tmem_wait_ld(ra);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t(&x)[32] = buf(k);
+          if (k < 3) tmem_load32(tS + 32 * (k + 1), buf(k + 1));
+          scores(k, x);
+          uint32_t out[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 t = ffma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, off2);
+            const float2 y = make_float2(ex2(t.x), ex2(t.y));
+            const float2 iv = kE4M3 ? *reinterpret_cast<const float2*>(sl.iv + 32 * k + 2 * e) : make_float2(1.0f, 1.0f);
+            sum = ffma2(y, iv, sum);
+            out[e] = kBf16 ? pack_b(y.x, y.y) : pack_h(y.x, y.y);
+          }
+          if (k < 3) tmem_wait_ld(buf(k + 1));
+          tmem_store16(tS + 16 * k, out);
+        }
+        tmem_wait_st();
+        tmem_before_sync();
+        mbar_arrive(bar(kPReady + wt));
+      }
+      if (!ok) break;
+      // ---- the unit's rows
+      ok = __all_sync(kFull, wait_or_stop(bar(kODone + wt), done & 1, stop));
+      if (!ok) break;
+      ++done;
+      tmem_after_sync();
+      const float total = sum.x + sum.y;
+      const bool whole = g.step0 == 0 && g.end == g.span.steps();
+      const int64_t orow = g.q.row0 + fc / a.G;
+      const int32_t qh = g.h * a.G + fc % a.G;
+      if (whole) {
+        bool bad = !(total <= 3.402823466e38f);
+        const float inv = bad ? NAN : total == 0.0f ? 0.0f : __fdividef(1.0f, total);
+        uint16_t* out = static_cast<uint16_t*>(a.out) + (orow * a.Q + qh) * D;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t raw[32];
+          tmem_load32(tO + 32 * k, raw);
+          tmem_wait_ld(raw);
+          uint32_t y[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float y0 = __uint_as_float(raw[2 * e]) * inv, y1 = __uint_as_float(raw[2 * e + 1]) * inv;
+            bad = bad || !(fabsf(y0) <= 3.402823466e38f) || !(fabsf(y1) <= 3.402823466e38f);
+            y[e] = a.type == KV_TYPE_BF16 ? pack_b(y0, y1) : pack_h(y0, y1);
+          }
+          if (row_ok) {
+            if (w.out_wide) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                reinterpret_cast<uint4*>(out + 32 * k)[e] = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                out[32 * k + 2 * e] = static_cast<uint16_t>(y[e]);
+                out[32 * k + 2 * e + 1] = static_cast<uint16_t>(y[e] >> 16);
+              }
+            }
+          }
+        }
+        if (a.lse && row_ok) a.lse[orow * a.Q + qh] = total == 0.0f ? -INFINITY : (ref - kLift + log2f(total)) * kLn2;
+        if (bad && row_ok) stop[1] = 1;
+      } else {
+        const int slot = g.step0 == 0 ? 1 : 0;
+        const int row = wt * 128 + r;
+        float* part = w.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * (static_cast<int64_t>(kRows) * (D + 2));
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t raw[32];
+          tmem_load32(tO + 32 * k, raw);
+          tmem_wait_ld(raw);
+          if (row_ok) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<uint4*>(part + row * D + 32 * k)[e] =
+                  make_uint4(raw[4 * e], raw[4 * e + 1], raw[4 * e + 2], raw[4 * e + 3]);
+          }
+        }
+        part[kRows * D + row] = ref;
+        part[kRows * (D + 1) + row] = total;
+      }
+    }
+    if (tid == 0) w.rec[blockIdx.x] = ok ? rec : SplitRecord{-1, 0, 0, 0};
+    // rows that came out with anything not finite are done again, key by key
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (stop[1] && !*stop && walk.start(loc[0], share)) do {
+      if (g.step0 > 0 || g.end < g.span.steps()) continue;  // the join's
+      for (int32_t k = warp; k < g.nf; k += 8) {
+        const int32_t f = g.f0 + k;
+        const int64_t orow = g.q.row0 + f / a.G;
+        const int32_t qh = g.h * a.G + f % a.G;
+        const uint16_t* out = static_cast<const uint16_t*>(a.out) + (orow * a.Q + qh) * D;
+        bool bad = false;
+        for (int e = lane; e < D; e += 32) bad = bad || (out[e] & (a.type == KV_TYPE_BF16 ? 0x7f80 : 0x7c00)) == (a.type == KV_TYPE_BF16 ? 0x7f80 : 0x7c00);
+        if (__any_sync(kFull, bad)) attend_row<C>(p, b, a, g.s, g.q.a + f / a.G, orow, qh, &bits);
+      }
+    } while (walk.next());
+  } else if (warp < 12) {
+    // ------------------------------------------------------------- loaders
+    const int lw = warp - 8;
+    const uint8_t* pool = reinterpret_cast<const uint8_t*>(p.base);
+    const int64_t row_bytes = p.vpr * 16;
+    uint32_t n = 0;   // steps of the block so far
+    uint32_t u = 0;   // units
+    bool ok = true;
+    // the loader's 32 keys of a step: key lw * 32 + lane is this lane's
+    auto entry = [&](int32_t i) -> int32_t {
+      if (i >= g.end) return 0;
+      const int64_t j = static_cast<int64_t>(g.span.block(i)) * kKeys + lw * 32 + lane;
+      const int32_t last = g.q.a + (g.f0 + g.nf - 1) / a.G;
+      if (j > last) return 0;
+      return __ldg(b.table + static_cast<int64_t>(g.s) * b.max_pages + div_ps(p, j));
+    };
+    for (; more && ok; more = walk.next(), ++u) {
+      const int32_t i0 = g.q.a + g.f0 / a.G, i1 = g.q.a + (g.f0 + g.nf - 1) / a.G;
+      const int64_t head = static_cast<int64_t>(g.h) * D * (kE4M3 ? 1 : 2);
+      int32_t ent = entry(g.step0);
+      for (int32_t i = g.step0; i < g.end && ok; ++i, ++n) {
+        const uint32_t stage = n & 1, parity = ((n >> 1) & 1) ^ 1;
+        const uint32_t kt = base + Sm::kK + stage * Sm::kOperand, vt = base + Sm::kV + stage * Sm::kOperand;
+        Slot& sl = slots[n % kSlots];
+        const int32_t j0 = g.span.block(i) * kKeys;
+        const int64_t j = static_cast<int64_t>(j0) + lw * 32 + lane;
+        const int32_t page = static_cast<int32_t>(page_of_entry(p, b, ent, bits));
+        ent = entry(i + 1);
+        const int32_t row = page == 0 ? -1
+                                      : static_cast<int32_t>(page * p.stride + 2 * static_cast<int64_t>(a.layer) * p.ps +
+                                                             (j - div_ps(p, j) * p.ps));
+        const uint32_t live = __ballot_sync(kFull, page != 0);
+        const bool partial = j0 + kKeys - 1 > i0 || (a.window && j0 <= i1 - a.window) || live != kFull;
+
+        constexpr int RB = kE4M3 ? D : 2 * D;   // bytes of a head's row
+        constexpr int LPR = RB / 16 < 8 ? RB / 16 : 8;  // lanes a row
+        constexpr int RPI = 32 / LPR;           // rows a round
+        constexpr int PPR = RB / 16 / LPR;      // pieces of a row a lane
+        constexpr int IT = 32 / RPI;
+        const int lr = lane / LPR, lc = lane % LPR;
+
+        if constexpr (kE4M3) {
+          float ks = 0.0f, vs = 0.0f;
+          if (page != 0) {
+            const int64_t at = (static_cast<int64_t>(page) * p.blocks + 2 * a.layer) * a.H + g.h;
+            ks = __ldg(a.scales + at);
+            vs = __ldg(a.scales + at + a.H);
+          }
+          uint4 kv[IT], vv[IT];
+#pragma unroll
+          for (int it = 0; it < IT; ++it) {
+            const int rr = it * RPI + lr;
+            const int64_t ro = __shfl_sync(kFull, row, rr);
+            kv[it] = make_uint4(0, 0, 0, 0);
+            if (ro >= 0) kv[it] = __ldg(reinterpret_cast<const uint4*>(pool + ro * row_bytes + head + lc * 16));
+          }
+#pragma unroll
+          for (int it = 0; it < IT; ++it) {
+            const int rr = it * RPI + lr;
+            const int64_t ro = __shfl_sync(kFull, row, rr);
+            vv[it] = make_uint4(0, 0, 0, 0);
+            if (ro >= 0) vv[it] = __ldg(reinterpret_cast<const uint4*>(pool + (ro + p.ps) * row_bytes + head + lc * 16));
+          }
+          ok = __all_sync(kFull, wait_or_stop(bar(kKFree + stage), parity, stop));
+          if (!ok) break;
+          sl.ks[lw * 32 + lane] = ks;
+          sl.lv[lw * 32 + lane] = lg2(vs);
+          sl.iv[lw * 32 + lane] = page != 0 ? __fdividef(1.0f, vs) : 0.0f;
+          if (lane == 0) sl.live[lw] = live;
+#pragma unroll
+          for (int it = 0; it < IT; ++it) {
+            const int rr = lw * 32 + it * RPI + lr;
+            uint4 lo, hi;
+            decode16(kv[it], lo, hi);
+            sts128(kt + piece_at(rr, 2 * lc), lo);
+            sts128(kt + piece_at(rr, 2 * lc + 1), hi);
+          }
+          fence_async_shared();
+          mbar_arrive(bar(kKFull + stage));
+          ok = __all_sync(kFull, wait_or_stop(bar(kVFree + stage), parity, stop));
+          if (!ok) break;
+          uint32_t bad_rows = 0;
+#pragma unroll
+          for (int it = 0; it < IT; ++it) {
+            const int rr = lw * 32 + it * RPI + lr;
+            if (partial) {
+              const uint4 z = make_uint4(not_finite<C>(vv[it].x), not_finite<C>(vv[it].y), not_finite<C>(vv[it].z),
+                                         not_finite<C>(vv[it].w));
+              if (z.x | z.y | z.z | z.w) {
+                bad_rows |= 1u << (it * RPI + lr);
+                vv[it] = make_uint4(vv[it].x & ~z.x, vv[it].y & ~z.y, vv[it].z & ~z.z, vv[it].w & ~z.w);
+              }
+            }
+            uint4 lo, hi;
+            decode16(vv[it], lo, hi);
+            sts128(vt + piece_at(rr, 2 * lc), lo);
+            sts128(vt + piece_at(rr, 2 * lc + 1), hi);
+          }
+          bad_rows = __reduce_or_sync(kFull, bad_rows);
+          if (lane == 0) sl.nan[lw] = bad_rows;
+          fence_async_shared();
+          mbar_arrive(bar(kVFull + stage));
+        } else {
+          ok = __all_sync(kFull, wait_or_stop(bar(kKFree + stage), parity, stop));
+          if (!ok) break;
+          if (lane == 0) sl.live[lw] = live;
+#pragma unroll
+          for (int it = 0; it < IT; ++it) {
+            const int rr = it * RPI + lr;
+            const int64_t ro = __shfl_sync(kFull, row, rr);
+            const uint8_t* src = pool + (ro >= 0 ? ro * row_bytes + head : 0) + lc * 16;
+#pragma unroll
+            for (int k = 0; k < PPR; ++k)
+              copy_async<16>(kt + piece_at(lw * 32 + rr, lc + k * LPR), src + k * LPR * 16, ro >= 0);
+          }
+          copy_commit();
+          ok = __all_sync(kFull, wait_or_stop(bar(kVFree + stage), parity, stop));
+          if (!ok) break;
+#pragma unroll
+          for (int it = 0; it < IT; ++it) {
+            const int rr = it * RPI + lr;
+            const int64_t ro = __shfl_sync(kFull, row, rr);
+            const uint8_t* src = pool + (ro >= 0 ? (ro + p.ps) * row_bytes + head : 0) + lc * 16;
+#pragma unroll
+            for (int k = 0; k < PPR; ++k)
+              copy_async<16>(vt + piece_at(lw * 32 + rr, lc + k * LPR), src + k * LPR * 16, ro >= 0);
+          }
+          copy_commit();
+          copy_wait<1>();
+          fence_async_shared();
+          mbar_arrive(bar(kKFull + stage));
+          copy_wait<0>();
+          uint32_t bad_rows = 0;
+          if (partial) {
+#pragma unroll
+            for (int it = 0; it < IT; ++it)
+#pragma unroll
+              for (int k = 0; k < PPR; ++k) {
+                const uint32_t at = vt + piece_at(lw * 32 + it * RPI + lr, lc + k * LPR);
+                const uint4 v = lds128(at);
+                const uint4 z = make_uint4(not_finite<C>(v.x), not_finite<C>(v.y), not_finite<C>(v.z), not_finite<C>(v.w));
+                if (z.x | z.y | z.z | z.w) {
+                  bad_rows |= 1u << (it * RPI + lr);
+                  sts128(at, make_uint4(v.x & ~z.x, v.y & ~z.y, v.z & ~z.z, v.w & ~z.w));
+                }
+              }
+          }
+          bad_rows = __reduce_or_sync(kFull, bad_rows);
+          if (lane == 0) sl.nan[lw] = bad_rows;
+          fence_async_shared();
+          mbar_arrive(bar(kVFull + stage));
+        }
+        if (i == g.step0) {
+          // the unit's queries: 64 rows a warp, the row's address looked up by a lane each
+          ok = __all_sync(kFull, wait_or_stop(bar(kQFree), (u & 1) ^ 1, stop));
+          if (!ok) break;
+          const int32_t fa = lw * 64 + lane, fb = fa + 32;
+          auto q_at = [&](int32_t f) -> int64_t {
+            const int32_t ff = g.f0 + f;
+            return f < g.nf ? (g.q.row0 + ff / a.G) * a.q_stride + static_cast<int64_t>(g.h * a.G + ff % a.G) * D : -1;
+          };
+          const int64_t qa = q_at(fa), qb = q_at(fb);
+          constexpr int QL = kPieces < 8 ? kPieces : 8, QR = 32 / QL, QP = kPieces / QL;
+          const int ql = lane / QL, qc = lane % QL;
+          for (int it = 0; it < 64 / QR; ++it) {
+            const int rr = it * QR + ql;
+            const int64_t va = __shfl_sync(kFull, qa, rr & 31), vb = __shfl_sync(kFull, qb, rr & 31);
+            const int64_t at = rr < 32 ? va : vb;
+            uint4 v[QP];
+#pragma unroll
+            for (int k = 0; k < QP; ++k) {
+              v[k] = make_uint4(0, 0, 0, 0);
+              if (at >= 0) {
+                const uint16_t* src = static_cast<const uint16_t*>(a.q) + at + (qc + k * QL) * 8;
+                if (w.q_wide) {
+                  v[k] = __ldg(reinterpret_cast<const uint4*>(src));
+                } else {
+                  uint16_t* e = reinterpret_cast<uint16_t*>(&v[k]);
+#pragma unroll
+                  for (int z = 0; z < 8; ++z) e[z] = __ldg(src + z);
+                }
+              }
+            }
+            if constexpr (kE4M3) {  // fp16 after a power of two that brings the row's largest to [2^14, 2^15)
+              float x[QP][8];
+              float amax = 0.0f;
+#pragma unroll
+              for (int k = 0; k < QP; ++k)
+#pragma unroll
+                for (int z = 0; z < 8; ++z) {
+                  const uint16_t e = reinterpret_cast<const uint16_t*>(&v[k])[z];
+                  x[k][z] = a.type == KV_TYPE_BF16 ? __uint_as_float(static_cast<uint32_t>(e) << 16)
+                                                   : __half2float(__ushort_as_half(e));
+                  amax = fmaxf(amax, fabsf(x[k][z]));
+                }
+#pragma unroll
+              for (int o = QL / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+              int ex = 14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23);
+              ex = amax > 0.0f ? max(-100, min(100, ex)) : 0;
+              const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+              if (qc == 0) qscale[lw * 64 + rr] = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+#pragma unroll
+              for (int k = 0; k < QP; ++k)
+                v[k] = make_uint4(pack_h(x[k][0] * up, x[k][1] * up), pack_h(x[k][2] * up, x[k][3] * up),
+                                  pack_h(x[k][4] * up, x[k][5] * up), pack_h(x[k][6] * up, x[k][7] * up));
+            }
+            const int row_q = lw * 64 + rr;
+            if (a.scale_log2 < 0.0f) {
+#pragma unroll
+              for (int k = 0; k < QP; ++k)
+                v[k] = make_uint4(v[k].x ^ 0x80008000u, v[k].y ^ 0x80008000u, v[k].z ^ 0x80008000u, v[k].w ^ 0x80008000u);
+            }
+#pragma unroll
+            for (int k = 0; k < QP; ++k)
+              sts128(base + Sm::kQ + (row_q >> 7) * Sm::kOperand + piece_at(row_q & 127, qc + k * QL), v[k]);
+          }
+          fence_async_shared();
+          mbar_arrive(bar(kQFull));
+        }
+      }
+    }
+    copy_wait<0>();
+  } else {
+    if (warp == 12 && lane == 0) {
+      // ------------------------------------------------------------- products
+      constexpr uint32_t kQK = umma_f16(kBf16, kKeys, false), kPV = umma_f16(kBf16, D, true);
+      uint32_t n = 0, u = 0;
+      uint32_t cnt[2] = {0, 0};  // steps of each tile
+      bool ok = true;
+      auto qk = [&](int wt, uint32_t stage) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t at = (k >> 2) * (128 * 128) + (k & 3) * 32;
+          umma_ss(tmem + wt * 128, smem_operand(base + Sm::kQ + wt * Sm::kOperand + at, 16),
+                  smem_operand(base + Sm::kK + stage * Sm::kOperand + at, 16), kQK, k > 0);
+        }
+        umma_commit(bar(kSFull + wt));
+      };
+      auto pv = [&](int wt, uint32_t stage, bool add) {
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          umma_ts(tmem + 256 + wt * D, tmem + wt * 128 + k * 8,
+                  smem_operand(base + Sm::kV + stage * Sm::kOperand + k * 2048, 128 * 128), kPV, add || k > 0);
+      };
+      for (; more && ok; more = walk.next(), ++u) {
+        const int nt = g.nf > 128 ? 2 : 1;
+        ok = wait_or_stop(bar(kKFull + (n & 1)), (n >> 1) & 1, stop) && wait_or_stop(bar(kQFull), u & 1, stop);
+        if (!ok) break;
+        tmem_after_sync();
+        for (int wt = 0; wt < nt; ++wt) qk(wt, n & 1);
+        umma_commit(bar(kKFree + (n & 1)));
+        if (g.end - g.step0 == 1) umma_commit(bar(kQFree));
+        for (int32_t i = g.step0; i < g.end; ++i, ++n) {
+          const uint32_t stage = n & 1, phase = (n >> 1) & 1;
+          const bool last = i + 1 == g.end;
+          for (int wt = 0; wt < nt && ok; ++wt) {
+            ok = wait_or_stop(bar(kPReady + wt), cnt[wt] & 1, stop) && wait_or_stop(bar(kVFull + stage), phase, stop);
+            if (ok && !last) ok = wait_or_stop(bar(kKFull + (stage ^ 1)), ((n + 1) >> 1) & 1, stop);
+            if (!ok) break;
+            ++cnt[wt];
+            tmem_after_sync();
+            pv(wt, stage, i > g.step0);
+            if (last)
+              umma_commit(bar(kODone + wt));
+            else
+              qk(wt, stage ^ 1);
+          }
+          if (!ok) break;
+          umma_commit(bar(kVFree + stage));
+          if (!last) {
+            umma_commit(bar(kKFree + (stage ^ 1)));
+            if (i + 2 == g.end) umma_commit(bar(kQFree));
+          }
+        }
+      }
+      umma_commit(bar(kDrain));  // tensor memory is freed when nothing is in flight
+      const long long t0 = clock64();
+      while (!mbar_try(bar(kDrain), 0) && clock64() - t0 < kWaitClocks) {
+      }
+    }
+    __syncwarp();
+  }
+  tmem_before_sync();
+  __syncthreads();
+  tmem_after_sync();
+  if (warp == 12) tmem_free(tmem, 512);
+  if (tid == 0 && *stop) bits |= KV_DEV_ERR_TIMEOUT;
+  store_bits(p, bits);
+}
+
+template <class C, int D>
+cudaError_t launch(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, cudaStream_t s) {
+  k_attend_tile<C, D><<<w.blocks, kTileThreads, TileSmem<D>::kBytes, s>>>(p, b, a, w);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? launch_join<C, D>(p, b, a, w, s) : e;
+}
+
+template <class C>
+cudaError_t prepare_c() {
+  cudaError_t e = cudaFuncSetAttribute(k_attend_tile<C, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       TileSmem<64>::kBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_attend_tile<C, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileSmem<128>::kBytes);
+  return e;
+}
+
+constexpr int kMinShare = 2;  // steps of 128 keys below which a block's share is not cut
+
+}  // namespace
+
+cudaError_t prepare_attend_tile() {
+  cudaError_t e = prepare_c<CodeE4M3>();
+  if (e == cudaSuccess) e = prepare_c<__half>();
+  if (e == cudaSuccess) e = prepare_c<__nv_bfloat16>();
+  return e;
+}
+
+int64_t attend_tile_workspace(int32_t D, int sm_count) {
+  return split_record_bytes(sm_count) + static_cast<int64_t>(sm_count) * 2 * kRows * (D + 2) * 4;
+}
+
+cudaError_t launch_attend_tile(const DevPool& p, const Batch& b, const AttendArgs& a, bool e4m3, int32_t min_new,
+                               void* workspace, int sm_count, cudaStream_t s) {
+  Split w{};
+  w.hw = 1;
+  w.nq = kRows;
+  w.min_new = min_new;
+  w.min_share = kMinShare;
+  const int64_t steps = static_cast<int64_t>(b.max_pages) * p.ps / kKeys + 1;
+  const int64_t tiles = b.n_rows * a.G / kRows + (b.n_rows < b.n_seqs ? b.n_rows : b.n_seqs);
+  const int64_t blocks = (steps * tiles * a.H + kMinShare - 1) / kMinShare;
+  w.blocks = static_cast<int>(blocks < sm_count ? blocks : sm_count);
+  w.n_workers = w.blocks;
+  w.rec = static_cast<SplitRecord*>(workspace);
+  w.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + split_record_bytes(sm_count));
+  w.q_wide = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.q_stride % 8 == 0;
+  w.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
+  w.lift = !e4m3 && a.type == KV_TYPE_BF16 ? 0.0f : 6.0f;
+  auto go = [&]<class C>() {
+    return a.D == 64 ? launch<C, 64>(p, b, a, w, s) : launch<C, 128>(p, b, a, w, s);
+  };
+  if (e4m3) return go.template operator()<CodeE4M3>();
+  return a.type == KV_TYPE_BF16 ? go.template operator()<__nv_bfloat16>() : go.template operator()<__half>();
+}
+
+}  // namespace gtkv
