@@ -1,6 +1,6 @@
-// Attention over the pages: which kernel takes a call, and the row-by-row form.
-#include "kv_attend.cuh"
-#include "kv_attend_launch.h"
+// Attention over the pages: which kernels take a call, the join of cut units,
+// and the row-by-row form.
+#include "kv_attend_split.cuh"
 
 namespace gtkv {
 
@@ -45,21 +45,47 @@ cudaError_t prepare_attend() {
   return e == cudaSuccess ? prepare_attend_tile() : e;
 }
 
-int64_t attend_workspace_bytes(int32_t H, int32_t, int32_t D, int32_t, int64_t, int sm_count) {
-  if (!has_tiles(D)) return 16;
-  const int64_t few = attend_few_workspace(H, D, sm_count), tile = attend_tile_workspace(D, sm_count);
-  return few > tile ? few : tile;  // the two run one after the other
+namespace {
+
+int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+
+template <class C>
+cudaError_t launch_join(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& few, const Split& tile,
+                        int sm_count, cudaStream_t s) {
+  const int workers = few.n_workers > tile.n_workers ? few.n_workers : tile.n_workers;
+  const int rows = workers * (few.n_workers ? few.hw * few.nq : tile.nq);
+  const dim3 grid(rows < sm_count ? rows : sm_count);
+  return launch_overlapped(a.D == 64 ? k_attend_join<C, 64> : k_attend_join<C, 128>, grid, kJoinBlock, 0, s, p, b, a,
+                           few, tile);
 }
 
+}  // namespace
+
+int64_t attend_workspace_bytes(int32_t, int32_t, int32_t D, int32_t, int64_t, int sm_count) {
+  if (!has_tiles(D)) return 16;
+  return align256(attend_few_workspace(D, sm_count)) + attend_tile_workspace(D, sm_count);
+}
+
+// Which kernels: the few-rows kernel alone when the sequences' rows of a KV
+// head number at most 16 on average (decode steps and drafts; a longer sequence among
+// them takes several row tiles there), else both, each taking the sequences on its side of 16
+// rows. Lengths are known on the device alone, so the rule goes by averages.
 cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, bool e4m3, void* workspace,
                           int sm_count, cudaStream_t s) {
   if (!has_tiles(a.D)) return launch_rows(p, b, a, e4m3, s);
-  const int32_t few = 16 / a.G;  // new tokens up to which a sequence's rows of a KV head are few
-  if (few > 0) {
-    const cudaError_t e = launch_attend_few(p, b, a, e4m3, few, workspace, sm_count, s);
-    if (e != cudaSuccess || b.n_rows <= few) return e;
-  }
-  return launch_attend_tile(p, b, a, e4m3, few + 1, workspace, sm_count, s);
+  const bool only_few = b.n_rows * a.G <= 16 * static_cast<int64_t>(b.n_seqs);
+  const int32_t limit = only_few ? 0x7fffffff : 16 / a.G;
+  Split few{}, tile{};
+  cudaError_t e = cudaSuccess;
+  if (limit > 0) e = launch_attend_few(p, b, a, e4m3, limit, workspace, sm_count, &few, s);
+  if (e == cudaSuccess && !only_few)
+    e = launch_attend_tile(p, b, a, e4m3, limit + 1,
+                           static_cast<uint8_t*>(workspace) + align256(attend_few_workspace(a.D, sm_count)), sm_count,
+                           limit > 0, &tile, s);
+  if (e != cudaSuccess) return e;
+  if (e4m3) return launch_join<CodeE4M3>(p, b, a, few, tile, sm_count, s);
+  return a.type == KV_TYPE_BF16 ? launch_join<__nv_bfloat16>(p, b, a, few, tile, sm_count, s)
+                                : launch_join<__half>(p, b, a, few, tile, sm_count, s);
 }
 
 }  // namespace gtkv

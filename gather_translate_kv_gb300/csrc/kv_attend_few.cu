@@ -38,6 +38,7 @@ namespace {
 constexpr int kFewWarps = 4;
 constexpr int kFewBlock = 32 * kFewWarps;
 constexpr int kFewBlocksPerSM = 3;
+constexpr int kUnitCost = 2;  // steps' worth of a unit's queries and output
 template <class C>
 struct FewType {
   static constexpr int kSize = 2;       // bytes per cached element
@@ -135,17 +136,17 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
     const int32_t f0 = t * NQ, f1 = min(f0 + NQ, q.n * a.G);
     return key_span<16>(a, q, f0, f1);
   };
-  const int64_t worker0 = static_cast<int64_t>(blockIdx.x) * kw;
+  const int32_t worker0 = static_cast<int32_t>(blockIdx.x) * kw;
   const int64_t share = find_shares<kFewBlock, kFewWarps>(
       b.n_seqs, worker0, w.n_workers, w.min_share, loc, tmp, [&](int32_t s) -> int64_t {
         int err = 0;
         const Seq q = seq_of(p, b, s, err);
         if (blockIdx.x == 0) bits |= err;
         int64_t n = 0;
-        for (int32_t t = 0; t < tiles_of(q); ++t) n += span_of(q, t).steps();
+        for (int32_t t = 0; t < tiles_of(q); ++t) n += span_of(q, t).steps() + kUnitCost;
         return n * n_groups;
       });
-  const int64_t worker = worker0 + wk;
+  const int32_t worker = worker0 + wk;
   SplitRecord rec{-1, 0, 0, 0};
   ShareStart at = loc[wk];
   if (worker >= w.n_workers) at.s = -1;
@@ -166,13 +167,16 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
     int64_t off = at.off;
     for (;;) {
       span = span_of(q, tile);
-      const int64_t n = static_cast<int64_t>(span.steps()) * n_groups;
+      const int64_t n = static_cast<int64_t>(span.steps() + kUnitCost) * n_groups;
       if (off < n) break;
       off -= n;
       ++tile;
     }
-    group = static_cast<int32_t>(off / span.steps());
-    step0 = static_cast<int32_t>(off - static_cast<int64_t>(group) * span.steps());
+    const int32_t unit = span.steps() + kUnitCost;
+    group = static_cast<int32_t>(off / unit);
+    const int32_t in = static_cast<int32_t>(off - static_cast<int64_t>(group) * unit);
+    step0 = in < kUnitCost ? 0 : in - kUnitCost;
+    left -= in < kUnitCost ? kUnitCost - in : 0;
   }
 
   while (left > 0) {
@@ -574,7 +578,7 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
         }
     } else {
       const int slot = step0 == 0 ? 1 : 0;
-      float* part = w.part + ((worker * w.hw + hw) * 2 + slot) * static_cast<int64_t>(NQ * (D + 2));
+      float* part = w.part + ((static_cast<int64_t>(worker) * w.hw + hw) * 2 + slot) * static_cast<int64_t>(NQ * (D + 2));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -589,15 +593,10 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
             part[NQ * (D + 1) + col] = sum[nt][e];
           }
         }
-      if (slot == 1) {
-        rec.s = s;
-        rec.tile = tile;
-        rec.head = group;
-      } else {
-        rec.cont = end == n_steps ? 3 : 1;
-      }
+      if (slot == 1)
+        rec = SplitRecord{s, tile, group, worker + static_cast<int32_t>((n_steps - end + share - 1) / share)};
     }
-    left -= end - step0;
+    left -= end - step0 + kUnitCost;  // and the head of the next unit
 
     // ---- the next unit
     step0 = 0;
@@ -623,8 +622,7 @@ cudaError_t launch(const DevPool& p, const Batch& b, const AttendArgs& a, Split 
   using Sh = FewShape<C, D>;
   auto kernel = p.ps % 16 == 0 ? k_attend_few<C, D, NT, true> : k_attend_few<C, D, NT, false>;
   kernel<<<w.blocks, kFewBlock, Sh::kSmem, s>>>(p, b, a, w);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? launch_join<C, D>(p, b, a, w, s) : e;
+  return cudaGetLastError();
 }
 
 template <class C>
@@ -665,32 +663,35 @@ cudaError_t prepare_attend_few() {
   return e;
 }
 
-int64_t attend_few_workspace(int32_t H, int32_t D, int sm_count) {
+int64_t attend_few_workspace(int32_t D, int sm_count) {
   const int64_t warps = static_cast<int64_t>(sm_count) * kFewBlocksPerSM * kFewWarps;
   return split_record_bytes(warps) + warps * 2 * 16 * (D + 2) * 4;
 }
 
 cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs& a, bool e4m3, int32_t max_new,
-                              void* workspace, int sm_count, cudaStream_t s) {
+                              void* workspace, int sm_count, Split* out, cudaStream_t s) {
   Split w{};
   w.hw = heads_of_worker(a.H);
   w.max_new = max_new;
   const int kw = kFewWarps / w.hw;
-  const int nt = a.G * static_cast<int64_t>(b.n_rows < max_new ? b.n_rows : max_new) <= 8 ? 1 : 2;
+  // one tile of 8 columns when the sequences' rows of a KV head fit on average, else 16
+  const int nt = b.n_rows * a.G <= 8 * static_cast<int64_t>(b.n_seqs) ? 1 : 2;
   // steps of one unit at most, and of all units
   int64_t most = static_cast<int64_t>(b.max_pages) * p.ps / 16 + 1;
   if (a.window) {
-    const int64_t seen = (static_cast<int64_t>(a.window) + max_new) / 16 + 2 + (a.sinks + 15) / 16;
+    const int64_t seen = (static_cast<int64_t>(a.window) + 16) / 16 + 2 + (a.sinks + 15) / 16;
     most = seen < most ? seen : most;
   }
   const int64_t tiles = (b.n_rows * a.G) / (8 * nt) + b.n_seqs;  // row tiles of all sequences
-  const int64_t all = most * tiles * (a.H / w.hw);
-  const int64_t cap = static_cast<int64_t>(sm_count) * kFewBlocksPerSM * kw;
+  const int64_t all = (most + kUnitCost) * tiles * (a.H / w.hw);
+  int64_t cap = static_cast<int64_t>(sm_count) * kFewBlocksPerSM * kw;
+  cap = cap < kMaxWorkers ? cap : kMaxWorkers;
   w.min_share = kMinShare;
   int64_t workers = (all + w.min_share - 1) / w.min_share;
   workers = workers > cap ? cap : workers;
   w.blocks = static_cast<int>((workers + kw - 1) / kw);
-  w.n_workers = static_cast<int64_t>(w.blocks) * kw;
+  if (w.blocks * kw > kMaxWorkers) w.blocks = kMaxWorkers / kw;
+  w.n_workers = w.blocks * kw;
   w.rec = static_cast<SplitRecord*>(workspace);
   const int64_t warps = static_cast<int64_t>(sm_count) * kFewBlocksPerSM * kFewWarps;
   w.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + split_record_bytes(warps));
@@ -698,6 +699,7 @@ cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs
   w.lift = !e4m3 && a.type == KV_TYPE_BF16 ? FewType<__nv_bfloat16>::kLift : FewType<__half>::kLift;
   w.q_wide = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.q_stride % 8 == 0;
   w.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
+  *out = w;
   if (e4m3) return launch_c<CodeE4M3>(p, b, a, w, nt, s);
   if (a.type == KV_TYPE_BF16) return launch_c<__nv_bfloat16>(p, b, a, w, nt, s);
   return launch_c<__half>(p, b, a, w, nt, s);

@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "kv_attend.cuh"
+#include "kv_attend_launch.h"
 
 namespace gtkv {
 
@@ -37,12 +38,6 @@ __device__ __forceinline__ KeySpan key_span(const AttendArgs& a, const Seq& q, i
   k.n_first = nf < k.b0 ? nf : k.b0;
   return k;
 }
-
-// What a worker leaves behind for the join.
-struct SplitRecord {
-  int32_t s, tile, head;  // unit of the unfinished last segment (slot 1), s < 0: none
-  int32_t cont;           // bit 0: slot 0 holds a continuing segment; bit 1: the unit ends with it
-};
 
 // Where the workers' shares begin. Called by all THREADS threads of a block
 // for its KW workers; loc[k] = {sequence, offset in its steps} or s = -1.
@@ -107,30 +102,11 @@ __device__ __forceinline__ int64_t find_shares(int32_t n_seqs, int64_t first_wor
   return share;
 }
 
-// Where a call's partial results are, and how its units are shaped.
-struct Split {
-  SplitRecord* rec;   // one per worker
-  float* part;        // [worker][head of the worker][slot][nq * (D + 2)]: sums, references, denominators
-  int64_t n_workers;
-  int32_t hw;         // KV heads of a worker
-  int32_t nq;         // rows of a unit
-  int32_t min_share;  // steps
-  int32_t min_new, max_new;  // new tokens of the sequences that the kernel takes
-  int32_t blocks;
-  int32_t q_wide;     // query rows start on 16 bytes
-  int32_t out_wide;   // out starts on 16 bytes
-  float lift;         // log2 of the weights' lift
-};
-
-inline int64_t split_record_bytes(int64_t workers) {
-  return (workers * static_cast<int64_t>(sizeof(SplitRecord)) + 255) / 256 * 256;
-}
-
 namespace {
 
 constexpr float kNoRef = -1e30f;  // reference before the first key; finite, so that -inf - m stays -inf
 
-constexpr int kJoinBlock = 128;
+constexpr int kJoinBlock = 256;
 
 __device__ __forceinline__ uint32_t shared_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -194,78 +170,114 @@ __device__ __forceinline__ uint32_t pack_b(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Joins the partial sums of units that were cut: block x looks at worker x's
-// unfinished unit and adds the continuing segments of the workers after it, one
-// warp a row, in the workers' order.
+// Joins the partial sums of units that were cut, adding a unit's segments in
+// the workers' order. An item is a row of a cut unit; a warp takes one, or, when there are few items
+// (a long context of few rows, cut many times), the eight warps of a block
+// share its segments.
 template <class C, int D>
-__global__ void __launch_bounds__(kJoinBlock) k_attend_join(DevPool p, Batch b, AttendArgs a, Split w) {
-  constexpr int E = D / 32;
-  const int NQ = w.nq;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t worker = blockIdx.x;
-  const SplitRecord rec = w.rec[worker];
-  if (rec.s < 0) return;
-  int64_t last = worker + 1;
-  while (last + 1 < w.n_workers && !(w.rec[last].cont & 2)) ++last;
-  const int lane = threadIdx.x & 31;
-  const int item = blockIdx.y * (kJoinBlock / 32) + (threadIdx.x >> 5);  // (head of the group, column)
-  const int hw = item / NQ, col = item - hw * NQ;
-  int bits = 0;
-  const Seq q = seq_of(p, b, rec.s, bits);
-  const int32_t f = rec.tile * NQ + col;
-  if (hw >= w.hw || f >= q.n * a.G) return;
-  auto part = [&](int64_t k) {
-    return w.part + ((k * w.hw + hw) * 2 + (k == worker ? 1 : 0)) * (static_cast<int64_t>(NQ) * (D + 2));
-  };
-  float m = kNoRef;
-  for (int64_t k = worker + lane; k <= last; k += 32) m = fmaxf(m, part(k)[NQ * D + col]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-  float acc[E], sum = 0.0f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-  for (int64_t k = worker; k <= last; ++k) {
-    const float* x = part(k);
-    const float f_ = ex2(x[NQ * D + col] - m);
-    sum += x[NQ * (D + 1) + col] * f_;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += x[col * D + lane * E + e] * f_;
+__device__ __forceinline__ void join_split(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w,
+                                           int32_t* owners, float* tmp, int& bits) {
+  constexpr int E = D / 32, NW = kJoinBlock / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // the workers that left a unit unfinished
+  int32_t count = 0;
+  int32_t* warp_count = reinterpret_cast<int32_t*>(tmp);
+  for (int32_t w0 = 0; w0 < w.n_workers; w0 += kJoinBlock) {
+    const bool own = w0 + tid < w.n_workers && w.rec[w0 + tid].s >= 0;
+    const uint32_t vote = __ballot_sync(kFull, own);
+    if (lane == 0) warp_count[warp] = __popc(vote);
+    __syncthreads();
+    int32_t at = count;
+    for (int k = 0; k < NW; ++k) {
+      if (k < warp) at += warp_count[k];
+      count += warp_count[k];
+    }
+    if (own) owners[at + __popc(vote & ((1u << lane) - 1))] = w0 + tid;
+    __syncthreads();
   }
-  const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
-  bool bad = !(sum <= 3.402823466e38f);
-  const int64_t r = q.row0 + f / a.G;
-  const int32_t qh = (rec.head * w.hw + hw) * a.G + f % a.G;
+  const int32_t rows = w.hw * w.nq;
+  const int32_t items = count * rows;
+  const bool shared = items <= 2 * static_cast<int32_t>(gridDim.x);  // a block an item
+  const int32_t stride = shared ? gridDim.x : gridDim.x * NW;
+  const int64_t part_floats = static_cast<int64_t>(w.nq) * (D + 2);
+  for (int32_t i = shared ? blockIdx.x : blockIdx.x * NW + warp; i < items; i += stride) {
+    const int32_t worker = owners[i / rows];
+    const int32_t hw = i % rows / w.nq, col = i % w.nq;
+    const SplitRecord rec = w.rec[worker];
+    const Seq q = seq_of(p, b, rec.s, bits);
+    const int32_t f = rec.tile * w.nq + col;
+    if (f >= q.n * a.G) continue;
+    auto part = [&](int32_t k) {
+      return w.part + ((static_cast<int64_t>(k) * w.hw + hw) * 2 + (k == worker ? 1 : 0)) * part_floats;
+    };
+    const int32_t k0 = worker + (shared ? warp : 0), kd = shared ? NW : 1;
+    float m = kNoRef;
+    for (int32_t k = k0 + lane * kd; k <= rec.last; k += 32 * kd) m = fmaxf(m, part(k)[w.nq * D + col]);
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float y = acc[e] * inv;
-    bad = bad || !(fabsf(y) <= 3.402823466e38f);
-    store_out(a, (r * a.Q + qh) * D + lane * E + e, y);
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    float acc[E], sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll 8
+    for (int32_t k = k0; k <= rec.last; k += kd) {
+      const float* x = part(k);
+      const float scale = ex2(x[w.nq * D + col] - m);
+      sum += x[w.nq * (D + 1) + col] * scale;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += x[col * D + lane * E + e] * scale;
+    }
+    if (shared) {
+      float* at = tmp + warp * (D + 2);
+#pragma unroll
+      for (int e = 0; e < E; ++e) at[lane * E + e] = acc[e];
+      if (lane == 0) at[D] = m, at[D + 1] = sum;
+      __syncthreads();
+      if (warp == 0) {
+        float top = kNoRef;
+        for (int k = 0; k < NW; ++k) top = fmaxf(top, tmp[k * (D + 2) + D]);
+        m = top;
+        sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+        for (int k = 0; k < NW; ++k) {
+          const float scale = ex2(tmp[k * (D + 2) + D] - top);
+          sum += tmp[k * (D + 2) + D + 1] * scale;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += tmp[k * (D + 2) + lane * E + e] * scale;
+        }
+      }
+    }
+    if (!shared || warp == 0) {
+      const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+      bool bad = !(sum <= 3.402823466e38f);
+      const int64_t r = q.row0 + f / a.G;
+      const int32_t qh = (rec.head * w.hw + hw) * a.G + f % a.G;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float y = acc[e] * inv;
+        bad = bad || !(fabsf(y) <= 3.402823466e38f);
+        store_out(a, (r * a.Q + qh) * D + lane * E + e, y);
+      }
+      if (a.lse && lane == 0) a.lse[r * a.Q + qh] = sum == 0.0f ? -INFINITY : (m - w.lift + log2f(sum)) * kLn2;
+      if (__any_sync(kFull, bad)) {
+        __syncwarp();
+        attend_row<C>(p, b, a, rec.s, q.a + f / a.G, r, qh, &bits);
+      }
+    }
+    if (shared) __syncthreads();
   }
-  if (a.lse && lane == 0)
-    a.lse[r * a.Q + qh] = sum == 0.0f ? -INFINITY : (m - w.lift + log2f(sum)) * kLn2;
-  if (__any_sync(kFull, bad)) {
-    __syncwarp();
-    attend_row<C>(p, b, a, rec.s, q.a + f / a.G, r, qh, &bits);
-  }
-  store_bits(p, bits);
 }
 
-
-// The join may start while the kernel before it drains; it waits for that kernel's end itself.
 template <class C, int D>
-cudaError_t launch_join(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(w.n_workers),
-                     static_cast<unsigned>((w.hw * w.nq + kJoinBlock / 32 - 1) / (kJoinBlock / 32)));
-  cfg.blockDim = dim3(kJoinBlock);
-  cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_attend_join<C, D>, p, b, a, w);
+__global__ void __launch_bounds__(kJoinBlock) k_attend_join(DevPool p, Batch b, AttendArgs a, Split few, Split tile) {
+  __shared__ int32_t owners[kMaxWorkers];
+  __shared__ float tmp[kJoinBlock / 32 * (D + 2)];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int bits = 0;
+  if (few.n_workers) join_split<C, D>(p, b, a, few, owners, tmp, bits);
+  __syncthreads();
+  if (tile.n_workers) join_split<C, D>(p, b, a, tile, owners, tmp, bits);
+  store_bits(p, bits);
 }
 
 }  // namespace

@@ -27,7 +27,6 @@
 // after a power-of-two scaling per row.
 //
 // Work is cut as in kv_attend_split.cuh, 128 keys a step.
-#include "kv_attend_launch.h"
 #include "kv_attend_split.cuh"
 #include "kv_umma.cuh"
 
@@ -35,10 +34,11 @@ namespace gtkv {
 
 namespace {
 
-constexpr int kTileThreads = 512;  // 13 working warps; the launch's registers are split among four groups
+constexpr int kTileThreads = 416;  // 13 warps
 constexpr int kRows = 256;         // rows of a unit
 constexpr int kKeys = 128;         // keys of a step
 constexpr int kSlots = 4;          // steps whose scales and masks are kept
+constexpr int kUnitCost = 1;       // steps' worth of a unit's queries and output
 
 struct Slot {
   float ks[kKeys];   // scale of the key
@@ -90,9 +90,11 @@ struct TileWalk {
     g.nf = min(kRows, g.q.n * a.G - g.f0);
     g.span = key_span<kKeys>(a, g.q, g.f0, g.f0 + g.nf);
   }
-  __device__ __forceinline__ void cut() {
+  __device__ __forceinline__ bool cut() {
+    if (left <= 0) return false;
     const int32_t n = g.span.steps() - g.step0;
     g.end = g.step0 + static_cast<int32_t>(left < n ? left : n);
+    return true;
   }
   // The first segment of a share; false when there is none.
   __device__ bool start(const ShareStart& at, int64_t share) {
@@ -105,18 +107,20 @@ struct TileWalk {
     int64_t off = at.off;
     for (;;) {
       shape();
-      const int64_t n = static_cast<int64_t>(g.span.steps()) * a.H;
+      const int64_t n = static_cast<int64_t>(g.span.steps() + kUnitCost) * a.H;
       if (off < n) break;
       off -= n;
       ++g.tile;
     }
-    g.h = static_cast<int32_t>(off / g.span.steps());
-    g.step0 = static_cast<int32_t>(off - static_cast<int64_t>(g.h) * g.span.steps());
-    cut();
-    return true;
+    const int32_t unit = g.span.steps() + kUnitCost;
+    g.h = static_cast<int32_t>(off / unit);
+    const int32_t in = static_cast<int32_t>(off - static_cast<int64_t>(g.h) * unit);
+    g.step0 = in < kUnitCost ? 0 : in - kUnitCost;
+    left -= in < kUnitCost ? kUnitCost - in : 0;
+    return cut();
   }
   __device__ bool next() {
-    left -= g.end - g.step0;
+    left -= g.end - g.step0 + kUnitCost;  // and the head of the next unit
     if (left <= 0) return false;
     g.step0 = 0;
     if (++g.h == a.H) {
@@ -130,8 +134,7 @@ struct TileWalk {
       }
       shape();
     }
-    cut();
-    return true;
+    return cut();
   }
 };
 
@@ -164,7 +167,17 @@ __device__ __forceinline__ float2 ffma2(float2 x, float2 y, float2 z) {
   return r;
 }
 
-template <class C, int D>
+__device__ __forceinline__ float2 fadd2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n"
+      " mov.b64 {%0, %1}, d;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+
+// P16: the page size is a multiple of 16, so 16 keys share the scales of an 8-bit cache.
+template <class C, int D, bool P16>
 __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batch b, AttendArgs a, Split w) {
   using Sm = TileSmem<D>;
   constexpr bool kE4M3 = std::is_same_v<C, CodeE4M3>;
@@ -186,7 +199,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
 
   if (warp == 12) tmem_alloc(base + Sm::kMisc, 512);
   if (tid == 0) {
-    stop[0] = stop[1] = 0;  // [1]: some row is not finite
+    stop[0] = 0;
+    stop[1] = 0;  // some row is not finite
     for (int i = 0; i < kBars; ++i) {
       const bool loads = i == kQFull || (i >= kKFull && i < kKFree) || (i >= kVFull && i < kVFree);
       const bool soft = i >= kPReady && i < kODone;
@@ -203,7 +217,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
                                                        int64_t n = 0;
                                                        for (walk.g.tile = 0; walk.g.tile < walk.tiles(); ++walk.g.tile) {
                                                          walk.shape();
-                                                         n += walk.g.span.steps();
+                                                         n += walk.g.span.steps() + kUnitCost;
                                                        }
                                                        return n * a.H;
                                                      });
@@ -229,12 +243,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
     bool ok = true;
     for (; more && ok; more = walk.next()) {
       const bool here = wt * 128 < g.nf;  // the unit has rows in this tile
-      if (g.step0 > 0 || g.end < g.span.steps()) {
-        if (g.step0 == 0)
-          rec.s = g.s, rec.tile = g.tile, rec.head = g.h;
-        else
-          rec.cont = g.end == g.span.steps() ? 3 : 1;
-      }
+      if (g.step0 == 0 && g.end < g.span.steps())
+        rec = SplitRecord{g.s, g.tile, g.h,
+                          static_cast<int32_t>(blockIdx.x + (g.span.steps() - g.end + share - 1) / share)};
       if (!here) {
         n += g.end - g.step0;
         continue;
@@ -259,61 +270,110 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
         const uint4 live = *reinterpret_cast<const uint4*>(sl.live);
         const bool cut = j0 + kKeys - 1 > i0 || (a.window && j0 <= i1 - a.window);
         const bool dead = (live.x & live.y & live.z & live.w) != 0xffffffffu;
-        // columns [lo, hi] and those below `first` are in sight
-        const int hi = pos - j0;
-        const int lo = a.window ? pos - a.window + 1 - j0 : -1;
-        const int first = a.window ? a.sinks - j0 : 0;
-        // scores of 32 columns: raw (16-bit caches) or as exponents of two (8-bit), -inf where not in sight
-        auto scores = [&](int k, uint32_t (&raw)[32]) {
-          if constexpr (kE4M3) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 ks = *reinterpret_cast<const float4*>(sl.ks + 32 * k + e);
-              const float4 lv = *reinterpret_cast<const float4*>(sl.lv + 32 * k + e);
-              raw[e] = __float_as_uint(fmaf(__uint_as_float(raw[e]) * ks.x, c, lv.x));
-              raw[e + 1] = __float_as_uint(fmaf(__uint_as_float(raw[e + 1]) * ks.y, c, lv.y));
-              raw[e + 2] = __float_as_uint(fmaf(__uint_as_float(raw[e + 2]) * ks.z, c, lv.z));
-              raw[e + 3] = __float_as_uint(fmaf(__uint_as_float(raw[e + 3]) * ks.w, c, lv.w));
-            }
-          }
-          constexpr uint32_t kNone = 0xff800000u;  // -inf
-          if (cut) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * k + e > hi || (32 * k + e < lo && 32 * k + e >= first)) raw[e] = kNone;
-          }
-          if (dead) {
+        if (cut || dead) {
+          // scores out of sight become -inf in place, so that the steps below need no masks
+          const int hi = pos - j0;  // columns [lo, hi] and those below `first` are in sight
+          const int lo = a.window ? pos - a.window + 1 - j0 : -1;
+          const int first = a.window ? a.sinks - j0 : 0;
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            uint32_t x[32];
+            tmem_load32(tS + 32 * k, x);
             const uint32_t lw = k == 0 ? live.x : k == 1 ? live.y : k == 2 ? live.z : live.w;
+            uint32_t sight = lw;
+            const int h = hi - 32 * k, l = lo - 32 * k, z = first - 32 * k;
+            sight &= h >= 31 ? kFull : h < 0 ? 0 : (2u << h) - 1;
+            sight &= (l <= 0 ? kFull : l > 31 ? 0 : ~((1u << l) - 1)) | (z <= 0 ? 0 : z > 31 ? kFull : (1u << z) - 1);
+            tmem_wait_ld(x);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (!(lw >> e & 1)) raw[e] = kNone;
+              if (!(sight >> e & 1)) x[e] = 0xff800000u;
+            tmem_store32(tS + 32 * k, x);
           }
-        };
-        uint32_t ra[32], rb[32];
-        auto buf = [&](int k) -> uint32_t(&)[32] { return k & 1 ? rb : ra; };
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        tmem_load32(tS, ra);
-        tmem_wait_ld(ra);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t(&x)[32] = buf(k);
-          if (k < 3) tmem_load32(tS + 32 * (k + 1), buf(k + 1));
-          scores(k, x);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(x[e]));
-          if (k < 3) tmem_wait_ld(buf(k + 1));
+          tmem_wait_st();
+          // values that are not finite were zeroed; rows that see such a key are done again at the end
+          ok = wait_or_stop(bar(kVFull + (n & 1)), (n >> 1) & 1, stop);
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+          const uint4 nan4 = *reinterpret_cast<const uint4*>(sl.nan);
+          if (nan4.x | nan4.y | nan4.z | nan4.w) {
+            const uint32_t nw[4] = {nan4.x, nan4.y, nan4.z, nan4.w};
+#pragma unroll 1
+            for (int e = 0; e < kKeys; ++e)
+              if (nw[e >> 5] >> (e & 31) & 1 && in_sight(a, pos, j0 + e)) sum.x = NAN;
+          }
         }
-        float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (!kE4M3) m *= c;
-        const bool move = m > ref + 8.0f;
-        if (__any_sync(kFull, move)) {
+        // Weights under the present reference, and the largest exponent on the
+        // way; only when that is more than 8 above the reference (the first step of a
+        // unit, and seldom after) the reference moves and the step is done again.
+        uint32_t P[64];
+        for (;;) {
+          const float off = kLift - (ref == kNoRef ? 0.0f : ref);  // (kNoRef itself would swallow the scores)
+          float2 add = make_float2(0.0f, 0.0f);
+          float mx0 = -INFINITY, mx1 = -INFINITY;
+          uint32_t ra[32], rb[32];
+          auto buf = [&](int k) -> uint32_t(&)[32] { return k & 1 ? rb : ra; };
+          tmem_load32(tS, ra);
+          tmem_wait_ld(ra);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t(&x)[32] = buf(k);
+            if (k < 3) tmem_load32(tS + 32 * (k + 1), buf(k + 1));
+            if constexpr (kE4M3 && P16) {
+              // 16 keys share a page, so their scales
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const int key = 32 * k + 16 * z;
+                const float cs = c * sl.ks[key], os = off + sl.lv[key];
+                float2 part = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int e = 8 * z; e < 8 * z + 8; ++e) {
+                  const float2 t = ffma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
+                                         make_float2(cs, cs), make_float2(os, os));
+                  mx0 = fmaxf(mx0, t.x);
+                  mx1 = fmaxf(mx1, t.y);
+                  const float2 y = make_float2(ex2(t.x), ex2(t.y));
+                  part = fadd2(part, y);
+                  P[16 * k + e] = pack_h(y.x, y.y);
+                }
+                add = ffma2(part, make_float2(sl.iv[key], sl.iv[key]), add);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float2 t = make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                if constexpr (kE4M3) {
+                  const float2 ks = *reinterpret_cast<const float2*>(sl.ks + 32 * k + 2 * e);
+                  const float2 lv = *reinterpret_cast<const float2*>(sl.lv + 32 * k + 2 * e);
+                  t = ffma2(t, make_float2(ks.x * c, ks.y * c), make_float2(lv.x + off, lv.y + off));
+                } else {
+                  t = ffma2(t, make_float2(c, c), make_float2(off, off));
+                }
+                mx0 = fmaxf(mx0, t.x);
+                mx1 = fmaxf(mx1, t.y);
+                const float2 y = make_float2(ex2(t.x), ex2(t.y));
+                if constexpr (kE4M3)
+                  add = ffma2(y, *reinterpret_cast<const float2*>(sl.iv + 32 * k + 2 * e), add);
+                else
+                  add = fadd2(add, y);
+                P[16 * k + e] = kBf16 ? pack_b(y.x, y.y) : pack_h(y.x, y.y);
+              }
+            }
+            if (k < 3) tmem_wait_ld(buf(k + 1));
+          }
+          const float m = fmaxf(mx0, mx1) - off;
+          const bool move = m > ref + 8.0f;
+          if (!__any_sync(kFull, move)) {
+            sum = fadd2(sum, add);
+            break;
+          }
           const float next = move ? m : ref;
           const float keep = ex2(ref - next);
           ref = next;
           sum.x *= keep;
           sum.y *= keep;
           if (i > g.step0) {  // the products so far are done: the score product was issued after them
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < D / 32; ++k) {
               tmem_load32(tO + 32 * k, ra);
               tmem_wait_ld(ra);
@@ -323,40 +383,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
             }
           }
         }
-        if (cut || dead) {
-          // values that are not finite were zeroed; rows that see such a key are done again at the end
-          ok = wait_or_stop(bar(kVFull + (n & 1)), (n >> 1) & 1, stop);
-          ok = __all_sync(kFull, ok);
-          if (!ok) break;
-          const uint4 nan4 = *reinterpret_cast<const uint4*>(sl.nan);
-          if (nan4.x | nan4.y | nan4.z | nan4.w) {
-            const uint32_t nw[4] = {nan4.x, nan4.y, nan4.z, nan4.w};
-            for (int e = 0; e < kKeys; ++e)
-              if (nw[e >> 5] >> (e & 31) & 1 && in_sight(a, pos, j0 + e)) sum.x = NAN;
-          }
-        }
-        // weights; those of 32 keys fill 16 columns, all of them below the scores still to be read
-        const float off = kLift - ref;
-        const float2 off2 = make_float2(off, off), c2 = kE4M3 ? make_float2(1.0f, 1.0f) : make_float2(c, c);
-        tmem_load32(tS, ra);
-        tmem_wait_ld(ra);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t(&x)[32] = buf(k);
-          if (k < 3) tmem_load32(tS + 32 * (k + 1), buf(k + 1));
-          scores(k, x);
-          uint32_t out[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 t = ffma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, off2);
-            const float2 y = make_float2(ex2(t.x), ex2(t.y));
-            const float2 iv = kE4M3 ? *reinterpret_cast<const float2*>(sl.iv + 32 * k + 2 * e) : make_float2(1.0f, 1.0f);
-            sum = ffma2(y, iv, sum);
-            out[e] = kBf16 ? pack_b(y.x, y.y) : pack_h(y.x, y.y);
-          }
-          if (k < 3) tmem_wait_ld(buf(k + 1));
-          tmem_store16(tS + 16 * k, out);
-        }
+        tmem_store32(tS, reinterpret_cast<uint32_t(&)[32]>(P[0]));
+        tmem_store32(tS + 32, reinterpret_cast<uint32_t(&)[32]>(P[32]));
         tmem_wait_st();
         tmem_before_sync();
         mbar_arrive(bar(kPReady + wt));
@@ -390,8 +418,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           if (row_ok) {
             if (w.out_wide) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                reinterpret_cast<uint4*>(out + 32 * k)[e] = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+              for (int e = 0; e < 16; e += 8)  // whole 32-byte sectors: a lane's row is its own
+                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out + 32 * k + 2 * e), "r"(y[e]),
+                             "r"(y[e + 1]), "r"(y[e + 2]), "r"(y[e + 3]), "r"(y[e + 4]), "r"(y[e + 5]), "r"(y[e + 6]),
+                             "r"(y[e + 7])
+                             : "memory");
             } else {
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
@@ -443,6 +474,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
     const int lw = warp - 8;
     const uint8_t* pool = reinterpret_cast<const uint8_t*>(p.base);
     const int64_t row_bytes = p.vpr * 16;
+    constexpr int RB = kE4M3 ? D : 2 * D;           // bytes of a head's row
+    constexpr int LPR = RB / 16 < 8 ? RB / 16 : 8;  // lanes a row
+    constexpr int RPI = 32 / LPR;                   // rows a round
+    constexpr int PPR = RB / 16 / LPR;              // pieces of a row a lane
+    constexpr int IT = 32 / RPI;
+    const int lr = lane / LPR, lc = lane % LPR;
     uint32_t n = 0;   // steps of the block so far
     uint32_t u = 0;   // units
     bool ok = true;
@@ -454,59 +491,150 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
       if (j > last) return 0;
       return __ldg(b.table + static_cast<int64_t>(g.s) * b.max_pages + div_ps(p, j));
     };
-    for (; more && ok; more = walk.next(), ++u) {
+    struct Keys {
+      int32_t row, page;  // this lane's key; row -1: no token
+      uint32_t live;
+      bool partial;       // some row may not see some key
+    };
+    auto keys_of = [&](int32_t i, int32_t ent) -> Keys {
+      Keys k;
+      const int32_t j0 = g.span.block(i) * kKeys;
+      const int64_t j = static_cast<int64_t>(j0) + lw * 32 + lane;
+      k.page = static_cast<int32_t>(page_of_entry(p, b, ent, bits));
+      k.row = k.page == 0 ? -1
+                          : static_cast<int32_t>(k.page * p.stride + 2 * static_cast<int64_t>(a.layer) * p.ps +
+                                                 (j - div_ps(p, j) * p.ps));
+      k.live = __ballot_sync(kFull, k.page != 0);
       const int32_t i0 = g.q.a + g.f0 / a.G, i1 = g.q.a + (g.f0 + g.nf - 1) / a.G;
-      const int64_t head = static_cast<int64_t>(g.h) * D * (kE4M3 ? 1 : 2);
-      int32_t ent = entry(g.step0);
-      for (int32_t i = g.step0; i < g.end && ok; ++i, ++n) {
-        const uint32_t stage = n & 1, parity = ((n >> 1) & 1) ^ 1;
-        const uint32_t kt = base + Sm::kK + stage * Sm::kOperand, vt = base + Sm::kV + stage * Sm::kOperand;
-        Slot& sl = slots[n % kSlots];
-        const int32_t j0 = g.span.block(i) * kKeys;
-        const int64_t j = static_cast<int64_t>(j0) + lw * 32 + lane;
-        const int32_t page = static_cast<int32_t>(page_of_entry(p, b, ent, bits));
-        ent = entry(i + 1);
-        const int32_t row = page == 0 ? -1
-                                      : static_cast<int32_t>(page * p.stride + 2 * static_cast<int64_t>(a.layer) * p.ps +
-                                                             (j - div_ps(p, j) * p.ps));
-        const uint32_t live = __ballot_sync(kFull, page != 0);
-        const bool partial = j0 + kKeys - 1 > i0 || (a.window && j0 <= i1 - a.window) || live != kFull;
+      k.partial = j0 + kKeys - 1 > i0 || (a.window && j0 <= i1 - a.window) || k.live != kFull;
+      return k;
+    };
+    auto wait = [&](uint32_t at, uint32_t parity) {
+      ok = __all_sync(kFull, wait_or_stop(at, parity, stop));
+      return ok;
+    };
 
-        constexpr int RB = kE4M3 ? D : 2 * D;   // bytes of a head's row
-        constexpr int LPR = RB / 16 < 8 ? RB / 16 : 8;  // lanes a row
-        constexpr int RPI = 32 / LPR;           // rows a round
-        constexpr int PPR = RB / 16 / LPR;      // pieces of a row a lane
-        constexpr int IT = 32 / RPI;
-        const int lr = lane / LPR, lc = lane % LPR;
+    // the unit's queries: 64 rows a warp, the row's address looked up by a lane each
+    auto load_queries = [&]() {
+      auto q_at = [&](int32_t f) -> int64_t {
+        const int32_t ff = g.f0 + f;
+        return f < g.nf ? (g.q.row0 + ff / a.G) * a.q_stride + static_cast<int64_t>(g.h * a.G + ff % a.G) * D : -1;
+      };
+      const int64_t qa = q_at(lw * 64 + lane), qb = q_at(lw * 64 + 32 + lane);
+      constexpr int QP = kPieces / 8;  // pieces of a row a lane; 8 lanes a row, 4 rows a round
+      const int ql = lane >> 3, qc = lane & 7;
+      auto q_tile = [&](int rr) { return base + Sm::kQ + ((lw * 64 + rr) >> 7) * Sm::kOperand; };
+      if (!kE4M3 && w.q_wide && a.scale_log2 >= 0.0f) {
+#pragma unroll
+        for (int it = 0; it < 16; ++it) {
+          const int rr = it * 4 + ql;
+          const int64_t at = __shfl_sync(kFull, it < 8 ? qa : qb, rr & 31);
+          const uint16_t* src = static_cast<const uint16_t*>(a.q) + (at >= 0 ? at : 0) + qc * 8;
+#pragma unroll
+          for (int k = 0; k < QP; ++k)
+            copy_async<16>(q_tile(rr) + piece_at((lw * 64 + rr) & 127, qc + k * 8), src + k * 64, at >= 0);
+        }
+        return;
+      }
+      constexpr int B = 4;  // rounds whose loads are in flight together
+#pragma unroll 1
+      for (int it0 = 0; it0 < 16; it0 += B) {
+        uint4 v[B][QP];
+#pragma unroll
+        for (int z = 0; z < B; ++z) {
+          const int rr = (it0 + z) * 4 + ql;
+          const int64_t va = __shfl_sync(kFull, qa, rr & 31), vb = __shfl_sync(kFull, qb, rr & 31);
+          const int64_t at = rr < 32 ? va : vb;
+#pragma unroll
+          for (int k = 0; k < QP; ++k) {
+            v[z][k] = make_uint4(0, 0, 0, 0);
+            if (at >= 0) {
+              const uint16_t* src = static_cast<const uint16_t*>(a.q) + at + (qc + k * 8) * 8;
+              if (w.q_wide) {
+                v[z][k] = __ldg(reinterpret_cast<const uint4*>(src));
+              } else {
+                uint32_t e[8];
+#pragma unroll
+                for (int y = 0; y < 8; ++y) e[y] = __ldg(src + y);
+                v[z][k] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int z = 0; z < B; ++z) {
+          const int rr = (it0 + z) * 4 + ql;
+          if constexpr (kE4M3) {  // fp16 after a power of two that brings the row's largest to [2^14, 2^15)
+            float x[QP][8];
+            float amax = 0.0f;
+#pragma unroll
+            for (int k = 0; k < QP; ++k) {
+              const uint32_t e[4] = {v[z][k].x, v[z][k].y, v[z][k].z, v[z][k].w};
+#pragma unroll
+              for (int y = 0; y < 8; ++y) {
+                const uint32_t h = y & 1 ? e[y >> 1] >> 16 : e[y >> 1] & 0xffffu;
+                x[k][y] = a.type == KV_TYPE_BF16 ? __uint_as_float(h << 16)
+                                                 : __half2float(__ushort_as_half(static_cast<uint16_t>(h)));
+                amax = fmaxf(amax, fabsf(x[k][y]));
+              }
+            }
+#pragma unroll
+            for (int o = 4; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+            int ex = 14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23);
+            ex = amax > 0.0f ? max(-100, min(100, ex)) : 0;
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+            if (qc == 0) qscale[lw * 64 + rr] = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+#pragma unroll
+            for (int k = 0; k < QP; ++k)
+              v[z][k] = make_uint4(pack_h(x[k][0] * up, x[k][1] * up), pack_h(x[k][2] * up, x[k][3] * up),
+                                   pack_h(x[k][4] * up, x[k][5] * up), pack_h(x[k][6] * up, x[k][7] * up));
+          }
+          const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0;
+#pragma unroll
+          for (int k = 0; k < QP; ++k)
+            sts128(q_tile(rr) + piece_at((lw * 64 + rr) & 127, qc + k * 8),
+                   make_uint4(v[z][k].x ^ flip, v[z][k].y ^ flip, v[z][k].z ^ flip, v[z][k].w ^ flip));
+        }
+      }
+    };
 
-        if constexpr (kE4M3) {
-          float ks = 0.0f, vs = 0.0f;
-          if (page != 0) {
-            const int64_t at = (static_cast<int64_t>(page) * p.blocks + 2 * a.layer) * a.H + g.h;
+    if constexpr (kE4M3) {
+      // Codes of the next step are on their way in registers while this
+      // step's are turned into fp16: K's are asked for once K is stored, V's once V is.
+      uint4 kv[IT], vv[IT];
+      auto fetch = [&](uint4 (&x)[IT], const Keys& k, int64_t off) {
+        const int64_t head = static_cast<int64_t>(g.h) * D + lc * 16;
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+          const int64_t ro = __shfl_sync(kFull, k.row, it * RPI + lr);
+          x[it] = make_uint4(0, 0, 0, 0);
+          if (ro >= 0) x[it] = __ldg(reinterpret_cast<const uint4*>(pool + (ro + off) * row_bytes + head));
+        }
+      };
+      for (; more && ok; more = walk.next(), ++u) {
+        int32_t ent = entry(g.step0 + 1);
+        Keys cur = keys_of(g.step0, entry(g.step0));
+        float ks = 0.0f, vs = 0.0f;
+        auto fetch_scales = [&](const Keys& k) {
+          ks = vs = 0.0f;
+          if (k.page != 0) {
+            const int64_t at = (static_cast<int64_t>(k.page) * p.blocks + 2 * a.layer) * a.H + g.h;
             ks = __ldg(a.scales + at);
             vs = __ldg(a.scales + at + a.H);
           }
-          uint4 kv[IT], vv[IT];
-#pragma unroll
-          for (int it = 0; it < IT; ++it) {
-            const int rr = it * RPI + lr;
-            const int64_t ro = __shfl_sync(kFull, row, rr);
-            kv[it] = make_uint4(0, 0, 0, 0);
-            if (ro >= 0) kv[it] = __ldg(reinterpret_cast<const uint4*>(pool + ro * row_bytes + head + lc * 16));
-          }
-#pragma unroll
-          for (int it = 0; it < IT; ++it) {
-            const int rr = it * RPI + lr;
-            const int64_t ro = __shfl_sync(kFull, row, rr);
-            vv[it] = make_uint4(0, 0, 0, 0);
-            if (ro >= 0) vv[it] = __ldg(reinterpret_cast<const uint4*>(pool + (ro + p.ps) * row_bytes + head + lc * 16));
-          }
-          ok = __all_sync(kFull, wait_or_stop(bar(kKFree + stage), parity, stop));
-          if (!ok) break;
-          sl.ks[lw * 32 + lane] = ks;
+        };
+        fetch_scales(cur);
+        fetch(kv, cur, 0);
+        fetch(vv, cur, p.ps);
+        for (int32_t i = g.step0; i < g.end; ++i, ++n) {
+          const uint32_t stage = n & 1, parity = ((n >> 1) & 1) ^ 1;
+          const uint32_t kt = base + Sm::kK + stage * Sm::kOperand, vt = base + Sm::kV + stage * Sm::kOperand;
+          Slot& sl = slots[n % kSlots];
+          if (!wait(bar(kKFree + stage), parity)) break;
+          sl.ks[lw * 32 + lane] = cur.page != 0 ? ks : 1.0f;  // no token: 2^-inf through lv, whatever the score
           sl.lv[lw * 32 + lane] = lg2(vs);
-          sl.iv[lw * 32 + lane] = page != 0 ? __fdividef(1.0f, vs) : 0.0f;
-          if (lane == 0) sl.live[lw] = live;
+          sl.iv[lw * 32 + lane] = cur.page != 0 ? __fdividef(1.0f, vs) : 0.0f;
+          if (lane == 0) sl.live[lw] = cur.live;
 #pragma unroll
           for (int it = 0; it < IT; ++it) {
             const int rr = lw * 32 + it * RPI + lr;
@@ -517,13 +645,25 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           }
           fence_async_shared();
           mbar_arrive(bar(kKFull + stage));
-          ok = __all_sync(kFull, wait_or_stop(bar(kVFree + stage), parity, stop));
-          if (!ok) break;
+          if (i == g.step0) {
+            if (!wait(bar(kQFree), (u & 1) ^ 1)) break;
+            load_queries();
+            fence_async_shared();
+            mbar_arrive(bar(kQFull));
+          }
+          Keys next{-1, 0, 0, false};
+          if (i + 1 < g.end) {
+            next = keys_of(i + 1, ent);
+            ent = entry(i + 2);
+            fetch_scales(next);
+            fetch(kv, next, 0);
+          }
+          if (!wait(bar(kVFree + stage), parity)) break;
           uint32_t bad_rows = 0;
 #pragma unroll
           for (int it = 0; it < IT; ++it) {
             const int rr = lw * 32 + it * RPI + lr;
-            if (partial) {
+            if (cur.partial) {
               const uint4 z = make_uint4(not_finite<C>(vv[it].x), not_finite<C>(vv[it].y), not_finite<C>(vv[it].z),
                                          not_finite<C>(vv[it].w));
               if (z.x | z.y | z.z | z.w) {
@@ -540,124 +680,80 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           if (lane == 0) sl.nan[lw] = bad_rows;
           fence_async_shared();
           mbar_arrive(bar(kVFull + stage));
-        } else {
-          ok = __all_sync(kFull, wait_or_stop(bar(kKFree + stage), parity, stop));
-          if (!ok) break;
-          if (lane == 0) sl.live[lw] = live;
+          cur = next;
+          if (i + 1 < g.end) fetch(vv, cur, p.ps);
+        }
+      }
+    } else {
+      // One more copy is always in flight: V of a step is announced after K of
+      // the next has been asked for, K after V of its own step.
+      bool pending = false, pending_partial = false;
+      auto copy = [&](uint32_t to, const Keys& k, int64_t off) {
+        const int64_t head = static_cast<int64_t>(g.h) * RB;
 #pragma unroll
-          for (int it = 0; it < IT; ++it) {
-            const int rr = it * RPI + lr;
-            const int64_t ro = __shfl_sync(kFull, row, rr);
-            const uint8_t* src = pool + (ro >= 0 ? ro * row_bytes + head : 0) + lc * 16;
+        for (int it = 0; it < IT; ++it) {
+          const int rr = it * RPI + lr;
+          const int64_t ro = __shfl_sync(kFull, k.row, rr);
+          const uint8_t* src = pool + (ro >= 0 ? (ro + off) * row_bytes + head : 0) + lc * 16;
 #pragma unroll
-            for (int k = 0; k < PPR; ++k)
-              copy_async<16>(kt + piece_at(lw * 32 + rr, lc + k * LPR), src + k * LPR * 16, ro >= 0);
+          for (int z = 0; z < PPR; ++z)
+            copy_async<16>(to + piece_at(lw * 32 + rr, lc + z * LPR), src + z * LPR * 16, ro >= 0);
+        }
+        copy_commit();
+      };
+      auto announce_v = [&](uint32_t m) {  // V of step m has arrived
+        uint32_t bad_rows = 0;
+        if (pending_partial) {
+          const uint32_t vt = base + Sm::kV + (m & 1) * Sm::kOperand;
+#pragma unroll
+          for (int it = 0; it < IT; ++it)
+#pragma unroll
+            for (int z = 0; z < PPR; ++z) {
+              const uint32_t at = vt + piece_at(lw * 32 + it * RPI + lr, lc + z * LPR);
+              const uint4 v = lds128(at);
+              const uint4 x = make_uint4(not_finite<C>(v.x), not_finite<C>(v.y), not_finite<C>(v.z), not_finite<C>(v.w));
+              if (x.x | x.y | x.z | x.w) {
+                bad_rows |= 1u << (it * RPI + lr);
+                sts128(at, make_uint4(v.x & ~x.x, v.y & ~x.y, v.z & ~x.z, v.w & ~x.w));
+              }
+            }
+        }
+        bad_rows = __reduce_or_sync(kFull, bad_rows);
+        if (lane == 0) slots[m % kSlots].nan[lw] = bad_rows;
+        fence_async_shared();
+        mbar_arrive(bar(kVFull + (m & 1)));
+        pending = false;
+      };
+      for (; more && ok; more = walk.next(), ++u) {
+        int32_t ent = entry(g.step0);
+        for (int32_t i = g.step0; i < g.end; ++i, ++n) {
+          const uint32_t stage = n & 1, parity = ((n >> 1) & 1) ^ 1;
+          const Keys cur = keys_of(i, ent);
+          ent = entry(i + 1);
+          if (!wait(bar(kKFree + stage), parity)) break;
+          if (lane == 0) slots[n % kSlots].live[lw] = cur.live;
+          copy(base + Sm::kK + stage * Sm::kOperand, cur, 0);
+          if (pending) {
+            copy_wait<1>();
+            announce_v(n - 1);
           }
-          copy_commit();
-          ok = __all_sync(kFull, wait_or_stop(bar(kVFree + stage), parity, stop));
-          if (!ok) break;
-#pragma unroll
-          for (int it = 0; it < IT; ++it) {
-            const int rr = it * RPI + lr;
-            const int64_t ro = __shfl_sync(kFull, row, rr);
-            const uint8_t* src = pool + (ro >= 0 ? (ro + p.ps) * row_bytes + head : 0) + lc * 16;
-#pragma unroll
-            for (int k = 0; k < PPR; ++k)
-              copy_async<16>(vt + piece_at(lw * 32 + rr, lc + k * LPR), src + k * LPR * 16, ro >= 0);
+          if (i == g.step0) {
+            if (!wait(bar(kQFree), (u & 1) ^ 1)) break;
+            load_queries();
+            copy_commit();
           }
-          copy_commit();
+          if (!wait(bar(kVFree + stage), parity)) break;
+          copy(base + Sm::kV + stage * Sm::kOperand, cur, p.ps);
+          pending = true;
+          pending_partial = cur.partial;
           copy_wait<1>();
           fence_async_shared();
           mbar_arrive(bar(kKFull + stage));
-          copy_wait<0>();
-          uint32_t bad_rows = 0;
-          if (partial) {
-#pragma unroll
-            for (int it = 0; it < IT; ++it)
-#pragma unroll
-              for (int k = 0; k < PPR; ++k) {
-                const uint32_t at = vt + piece_at(lw * 32 + it * RPI + lr, lc + k * LPR);
-                const uint4 v = lds128(at);
-                const uint4 z = make_uint4(not_finite<C>(v.x), not_finite<C>(v.y), not_finite<C>(v.z), not_finite<C>(v.w));
-                if (z.x | z.y | z.z | z.w) {
-                  bad_rows |= 1u << (it * RPI + lr);
-                  sts128(at, make_uint4(v.x & ~z.x, v.y & ~z.y, v.z & ~z.z, v.w & ~z.w));
-                }
-              }
-          }
-          bad_rows = __reduce_or_sync(kFull, bad_rows);
-          if (lane == 0) sl.nan[lw] = bad_rows;
-          fence_async_shared();
-          mbar_arrive(bar(kVFull + stage));
-        }
-        if (i == g.step0) {
-          // the unit's queries: 64 rows a warp, the row's address looked up by a lane each
-          ok = __all_sync(kFull, wait_or_stop(bar(kQFree), (u & 1) ^ 1, stop));
-          if (!ok) break;
-          const int32_t fa = lw * 64 + lane, fb = fa + 32;
-          auto q_at = [&](int32_t f) -> int64_t {
-            const int32_t ff = g.f0 + f;
-            return f < g.nf ? (g.q.row0 + ff / a.G) * a.q_stride + static_cast<int64_t>(g.h * a.G + ff % a.G) * D : -1;
-          };
-          const int64_t qa = q_at(fa), qb = q_at(fb);
-          constexpr int QL = kPieces < 8 ? kPieces : 8, QR = 32 / QL, QP = kPieces / QL;
-          const int ql = lane / QL, qc = lane % QL;
-          for (int it = 0; it < 64 / QR; ++it) {
-            const int rr = it * QR + ql;
-            const int64_t va = __shfl_sync(kFull, qa, rr & 31), vb = __shfl_sync(kFull, qb, rr & 31);
-            const int64_t at = rr < 32 ? va : vb;
-            uint4 v[QP];
-#pragma unroll
-            for (int k = 0; k < QP; ++k) {
-              v[k] = make_uint4(0, 0, 0, 0);
-              if (at >= 0) {
-                const uint16_t* src = static_cast<const uint16_t*>(a.q) + at + (qc + k * QL) * 8;
-                if (w.q_wide) {
-                  v[k] = __ldg(reinterpret_cast<const uint4*>(src));
-                } else {
-                  uint16_t* e = reinterpret_cast<uint16_t*>(&v[k]);
-#pragma unroll
-                  for (int z = 0; z < 8; ++z) e[z] = __ldg(src + z);
-                }
-              }
-            }
-            if constexpr (kE4M3) {  // fp16 after a power of two that brings the row's largest to [2^14, 2^15)
-              float x[QP][8];
-              float amax = 0.0f;
-#pragma unroll
-              for (int k = 0; k < QP; ++k)
-#pragma unroll
-                for (int z = 0; z < 8; ++z) {
-                  const uint16_t e = reinterpret_cast<const uint16_t*>(&v[k])[z];
-                  x[k][z] = a.type == KV_TYPE_BF16 ? __uint_as_float(static_cast<uint32_t>(e) << 16)
-                                                   : __half2float(__ushort_as_half(e));
-                  amax = fmaxf(amax, fabsf(x[k][z]));
-                }
-#pragma unroll
-              for (int o = QL / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-              int ex = 14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23);
-              ex = amax > 0.0f ? max(-100, min(100, ex)) : 0;
-              const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-              if (qc == 0) qscale[lw * 64 + rr] = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-#pragma unroll
-              for (int k = 0; k < QP; ++k)
-                v[k] = make_uint4(pack_h(x[k][0] * up, x[k][1] * up), pack_h(x[k][2] * up, x[k][3] * up),
-                                  pack_h(x[k][4] * up, x[k][5] * up), pack_h(x[k][6] * up, x[k][7] * up));
-            }
-            const int row_q = lw * 64 + rr;
-            if (a.scale_log2 < 0.0f) {
-#pragma unroll
-              for (int k = 0; k < QP; ++k)
-                v[k] = make_uint4(v[k].x ^ 0x80008000u, v[k].y ^ 0x80008000u, v[k].z ^ 0x80008000u, v[k].w ^ 0x80008000u);
-            }
-#pragma unroll
-            for (int k = 0; k < QP; ++k)
-              sts128(base + Sm::kQ + (row_q >> 7) * Sm::kOperand + piece_at(row_q & 127, qc + k * QL), v[k]);
-          }
-          fence_async_shared();
-          mbar_arrive(bar(kQFull));
+          if (i == g.step0) mbar_arrive(bar(kQFull));
         }
       }
+      copy_wait<0>();
+      if (pending && ok) announce_v(n - 1);
     }
     copy_wait<0>();
   } else {
@@ -723,25 +819,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
   tmem_before_sync();
   __syncthreads();
   tmem_after_sync();
+  // launched over the tail of the few-rows kernel: the join waits for this
+  // kernel alone, so this kernel ends after that one
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 12) tmem_free(tmem, 512);
   if (tid == 0 && *stop) bits |= KV_DEV_ERR_TIMEOUT;
   store_bits(p, bits);
 }
 
-template <class C, int D>
-cudaError_t launch(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, cudaStream_t s) {
-  k_attend_tile<C, D><<<w.blocks, kTileThreads, TileSmem<D>::kBytes, s>>>(p, b, a, w);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? launch_join<C, D>(p, b, a, w, s) : e;
-}
-
-template <class C>
-cudaError_t prepare_c() {
-  cudaError_t e = cudaFuncSetAttribute(k_attend_tile<C, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       TileSmem<64>::kBytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_attend_tile<C, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileSmem<128>::kBytes);
-  return e;
+template <class C, int D, bool P16>
+cudaError_t prepare_one() {
+  return cudaFuncSetAttribute(k_attend_tile<C, D, P16>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileSmem<D>::kBytes);
 }
 
 constexpr int kMinShare = 2;  // steps of 128 keys below which a block's share is not cut
@@ -749,9 +837,12 @@ constexpr int kMinShare = 2;  // steps of 128 keys below which a block's share i
 }  // namespace
 
 cudaError_t prepare_attend_tile() {
-  cudaError_t e = prepare_c<CodeE4M3>();
-  if (e == cudaSuccess) e = prepare_c<__half>();
-  if (e == cudaSuccess) e = prepare_c<__nv_bfloat16>();
+  cudaError_t e = cudaSuccess;
+  for (cudaError_t (*one)() :
+       {prepare_one<CodeE4M3, 64, false>, prepare_one<CodeE4M3, 64, true>, prepare_one<CodeE4M3, 128, false>,
+        prepare_one<CodeE4M3, 128, true>, prepare_one<__half, 64, false>, prepare_one<__half, 128, false>,
+        prepare_one<__nv_bfloat16, 64, false>, prepare_one<__nv_bfloat16, 128, false>})
+    if (e == cudaSuccess) e = one();
   return e;
 }
 
@@ -760,13 +851,13 @@ int64_t attend_tile_workspace(int32_t D, int sm_count) {
 }
 
 cudaError_t launch_attend_tile(const DevPool& p, const Batch& b, const AttendArgs& a, bool e4m3, int32_t min_new,
-                               void* workspace, int sm_count, cudaStream_t s) {
+                               void* workspace, int sm_count, bool after, Split* out, cudaStream_t s) {
   Split w{};
   w.hw = 1;
   w.nq = kRows;
   w.min_new = min_new;
   w.min_share = kMinShare;
-  const int64_t steps = static_cast<int64_t>(b.max_pages) * p.ps / kKeys + 1;
+  const int64_t steps = static_cast<int64_t>(b.max_pages) * p.ps / kKeys + 1 + kUnitCost;
   const int64_t tiles = b.n_rows * a.G / kRows + (b.n_rows < b.n_seqs ? b.n_rows : b.n_seqs);
   const int64_t blocks = (steps * tiles * a.H + kMinShare - 1) / kMinShare;
   w.blocks = static_cast<int>(blocks < sm_count ? blocks : sm_count);
@@ -774,13 +865,18 @@ cudaError_t launch_attend_tile(const DevPool& p, const Batch& b, const AttendArg
   w.rec = static_cast<SplitRecord*>(workspace);
   w.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + split_record_bytes(sm_count));
   w.q_wide = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.q_stride % 8 == 0;
-  w.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
+  w.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
   w.lift = !e4m3 && a.type == KV_TYPE_BF16 ? 0.0f : 6.0f;
-  auto go = [&]<class C>() {
-    return a.D == 64 ? launch<C, 64>(p, b, a, w, s) : launch<C, 128>(p, b, a, w, s);
+  *out = w;
+  auto go = [&]<class C, bool P16>() {
+    auto kernel = a.D == 64 ? k_attend_tile<C, 64, P16> : k_attend_tile<C, 128, P16>;
+    const int smem = a.D == 64 ? TileSmem<64>::kBytes : TileSmem<128>::kBytes;
+    if (after) return launch_overlapped(kernel, dim3(w.blocks), kTileThreads, smem, s, p, b, a, w);
+    kernel<<<w.blocks, kTileThreads, smem, s>>>(p, b, a, w);
+    return cudaGetLastError();
   };
-  if (e4m3) return go.template operator()<CodeE4M3>();
-  return a.type == KV_TYPE_BF16 ? go.template operator()<__nv_bfloat16>() : go.template operator()<__half>();
+  if (e4m3) return p.ps % 16 == 0 ? go.template operator()<CodeE4M3, true>() : go.template operator()<CodeE4M3, false>();
+  return a.type == KV_TYPE_BF16 ? go.template operator()<__nv_bfloat16, false>() : go.template operator()<__half, false>();
 }
 
 }  // namespace gtkv
