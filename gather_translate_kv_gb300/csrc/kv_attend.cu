@@ -54,7 +54,7 @@ cudaError_t launch_join(const DevPool& p, const Batch& b, const AttendArgs& a, c
                         int sm_count, cudaStream_t s) {
   const int workers = few.n_workers > tile.n_workers ? few.n_workers : tile.n_workers;
   const int rows = workers * (few.n_workers ? few.hw * few.nq : tile.nq);
-  const dim3 grid(rows < sm_count ? rows : sm_count);
+  const dim3 grid(rows / (kJoinBlock / 32) < 4 * sm_count ? (rows + kJoinBlock / 32 - 1) / (kJoinBlock / 32) : 4 * sm_count);
   return launch_overlapped(a.D == 64 ? k_attend_join<C, 64> : k_attend_join<C, 128>, grid, kJoinBlock, 0, s, p, b, a,
                            few, tile);
 }

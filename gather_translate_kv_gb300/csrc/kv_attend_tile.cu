@@ -37,32 +37,41 @@ namespace {
 constexpr int kTileThreads = 416;  // 13 warps
 constexpr int kRows = 256;         // rows of a unit
 constexpr int kKeys = 128;         // keys of a step
-constexpr int kSlots = 4;          // steps whose scales and masks are kept
-constexpr int kUnitCost = 1;       // steps' worth of a unit's queries and output
+constexpr int kSlots = 8;          // steps whose scales and masks are kept
+constexpr int kUnitCost = 3;       // steps' worth of a unit's queries and output
 
-struct Slot {
-  float ks[kKeys];   // scale of the key
-  float lv[kKeys];   // log2 of the value's scale
-  float iv[kKeys];   // its inverse
+// What the softmax warps need to know of a step's keys.
+struct Masks {
   uint32_t live[4];  // keys that are tokens
   uint32_t nan[4];   // keys whose value had elements that are not finite (zeroed)
 };
-
-enum Bar { kQFull, kQFree, kKFull, kKFree = kKFull + 2, kVFull = kKFree + 2, kVFree = kVFull + 2, kSFull = kVFree + 2,
-           kPReady = kSFull + 2, kODone = kPReady + 2, kDrain = kODone + 2, kBars };
-
-template <int D>
-struct TileSmem {
-  static constexpr int kOperand = 128 * D * 2;        // a tile of Q, K or V
-  static constexpr int kQ = 0;                        // two tiles
-  static constexpr int kK = 2 * kOperand;             // two stages
-  static constexpr int kV = 4 * kOperand;             // two stages
-  static constexpr int kSlot = 6 * kOperand;
-  static constexpr int kQScale = kSlot + kSlots * static_cast<int>(sizeof(Slot));
-  static constexpr int kBar = kQScale + kRows * 4;
-  static constexpr int kMisc = kBar + kBars * 8;      // tensor memory address, stop word
-  static constexpr int kBytes = kMisc + 16 + 1024;    // + room to align to the swizzle's 1024 bytes
+struct Scales {
+  float ks[kKeys];  // scale of the key
+  float lv[kKeys];  // log2 of the value's scale
+  float iv[kKeys];  // its inverse
 };
+
+// Tiles of keys and values pass through one ring of operand tiles, K of step n
+// as tile 2n and V as tile 2n + 1; codes of 8-bit caches through a ring of raw tiles before it.
+template <class C, int D>
+struct TileSmem {
+  static constexpr bool kE4M3 = std::is_same_v<C, CodeE4M3>;
+  static constexpr int kOperand = 128 * D * 2;  // a tile of Q, K or V
+  static constexpr int kRing = D == 64 ? 8 : kE4M3 ? 3 : 5;
+  static constexpr int kRawRing = kE4M3 ? 3 : 0;
+  static constexpr int kQ = 0;  // two tiles
+  static constexpr int kTiles = 2 * kOperand;
+  static constexpr int kRaw = kTiles + kRing * kOperand;
+  static constexpr int kMasks = kRaw + kRawRing * (kOperand / 2);
+  static constexpr int kScales = kMasks + kSlots * static_cast<int>(sizeof(Masks));
+  static constexpr int kQScale = kScales + (kE4M3 ? kSlots * static_cast<int>(sizeof(Scales)) : 0);
+  static constexpr int kBar = kQScale + (kE4M3 ? 2 * kRows * 4 : 0);  // of this unit's and the next one's rows
+  enum Bar { kFull, kFree = kFull + kRing, kQFull = kFree + kRing, kQFree = kQFull + 2, kSFull = kQFree + 2,
+             kPReady = kSFull + 2, kODone = kPReady + 2, kDrain = kODone + 2, kBars };
+  static constexpr int kMisc = kBar + kBars * 8;   // tensor memory address, stop word
+  static constexpr int kBytes = kMisc + 16 + 1024;  // + room to align to the swizzle's 1024 bytes
+};
+static_assert(TileSmem<__half, 128>::kBytes <= 227 * 1024 && TileSmem<CodeE4M3, 128>::kBytes <= 227 * 1024);
 
 // One segment of a block's share: steps [step0, end) of a unit.
 struct Segment {
@@ -138,6 +147,12 @@ struct TileWalk {
   }
 };
 
+// The warp's earlier writes are seen by whoever waits on the barrier.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 __device__ __forceinline__ void sts128(uint32_t at, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -179,7 +194,7 @@ __device__ __forceinline__ float2 fadd2(float2 x, float2 y) {
 // P16: the page size is a multiple of 16, so 16 keys share the scales of an 8-bit cache.
 template <class C, int D, bool P16>
 __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batch b, AttendArgs a, Split w) {
-  using Sm = TileSmem<D>;
+  using Sm = TileSmem<C, D>;
   constexpr bool kE4M3 = std::is_same_v<C, CodeE4M3>;
   constexpr bool kBf16 = std::is_same_v<C, __nv_bfloat16>;
   constexpr float kLift = kBf16 ? 0.0f : 6.0f;
@@ -191,7 +206,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
   const uint32_t base = (shared_u32(dyn) + 1023u) & ~1023u;
   uint8_t* gen = dyn + (base - shared_u32(dyn));
   volatile int* stop = reinterpret_cast<volatile int*>(gen + Sm::kMisc + 8);
-  Slot* slots = reinterpret_cast<Slot*>(gen + Sm::kSlot);
+  Masks* masks = reinterpret_cast<Masks*>(gen + Sm::kMasks);
+  Scales* scales = reinterpret_cast<Scales*>(gen + Sm::kScales);  // 8-bit caches
   float* qscale = reinterpret_cast<float*>(gen + Sm::kQScale);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto bar = [&](int i) -> uint32_t { return base + Sm::kBar + i * 8; };
@@ -201,10 +217,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
   if (tid == 0) {
     stop[0] = 0;
     stop[1] = 0;  // some row is not finite
-    for (int i = 0; i < kBars; ++i) {
-      const bool loads = i == kQFull || (i >= kKFull && i < kKFree) || (i >= kVFull && i < kVFree);
-      const bool soft = i >= kPReady && i < kODone;
-      mbar_init_n(bar(i), loads || soft ? 128 : 1);
+    for (int i = 0; i < Sm::kBars; ++i) {
+      const bool warps4 = i < Sm::kFree || (i >= Sm::kPReady && i < Sm::kODone);  // one arrival a warp
+      const bool warps2 = i >= Sm::kQFull && i < Sm::kQFree;
+      mbar_init_n(bar(i), warps4 ? 4 : warps2 ? 2 : 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -260,14 +276,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
       float ref = kNoRef;
       float2 sum = make_float2(0.0f, 0.0f);
       for (int32_t i = g.step0; i < g.end && ok; ++i, ++n, ++mine) {
-        ok = wait_or_stop(bar(kSFull + wt), mine & 1, stop);
+        ok = wait_or_stop(bar(Sm::kSFull + wt), mine & 1, stop);
         ok = __all_sync(kFull, ok);
         if (!ok) break;
         tmem_after_sync();
-        const Slot& sl = slots[n % kSlots];
+        const Masks& mk = masks[n % kSlots];
+        const Scales& sl = scales[n % kSlots];
         const int32_t j0 = g.span.block(i) * kKeys;
-        if (kE4M3 && i == g.step0) c = c0 * qscale[wt * 128 + r];
-        const uint4 live = *reinterpret_cast<const uint4*>(sl.live);
+        if (kE4M3 && i == g.step0) c = c0 * qscale[(done & 1) * kRows + wt * 128 + r];
+        const uint4 live = *reinterpret_cast<const uint4*>(mk.live);
         const bool cut = j0 + kKeys - 1 > i0 || (a.window && j0 <= i1 - a.window);
         const bool dead = (live.x & live.y & live.z & live.w) != 0xffffffffu;
         if (cut || dead) {
@@ -292,10 +309,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           }
           tmem_wait_st();
           // values that are not finite were zeroed; rows that see such a key are done again at the end
-          ok = wait_or_stop(bar(kVFull + (n & 1)), (n >> 1) & 1, stop);
+          ok = wait_or_stop(bar(Sm::kFull + (2 * n + 1) % Sm::kRing), (2 * n + 1) / Sm::kRing & 1, stop);
           ok = __all_sync(kFull, ok);
           if (!ok) break;
-          const uint4 nan4 = *reinterpret_cast<const uint4*>(sl.nan);
+          const uint4 nan4 = *reinterpret_cast<const uint4*>(mk.nan);
           if (nan4.x | nan4.y | nan4.z | nan4.w) {
             const uint32_t nw[4] = {nan4.x, nan4.y, nan4.z, nan4.w};
 #pragma unroll 1
@@ -303,9 +320,36 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
               if (nw[e >> 5] >> (e & 31) & 1 && in_sight(a, pos, j0 + e)) sum.x = NAN;
           }
         }
+        auto log_scale = [&](int e, float off, float2& m, float2& o) {  // exponents of columns e, e + 1: x m + o
+          const float2 ks = *reinterpret_cast<const float2*>(sl.ks + e), lv = *reinterpret_cast<const float2*>(sl.lv + e);
+          m = make_float2(ks.x * c, ks.y * c);
+          o = make_float2(lv.x + off, lv.y + off);
+        };
+        if (i == g.step0) {  // the reference starts as the first step's maximum
+          float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            uint32_t x[32];
+            tmem_load32(tS + 32 * k, x);
+            tmem_wait_ld(x);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float2 t = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+              if constexpr (kE4M3) {
+                float2 mm, oo;
+                log_scale(32 * k + e, 0.0f, mm, oo);
+                t = ffma2(t, mm, oo);
+              }
+              m0 = fmaxf(m0, t.x);
+              m1 = fmaxf(m1, t.y);
+            }
+          }
+          const float m = fmaxf(m0, m1) * (kE4M3 ? 1.0f : c);
+          if (m > -INFINITY) ref = m;
+        }
         // Weights under the present reference, and the largest exponent on the
-        // way; only when that is more than 8 above the reference (the first step of a
-        // unit, and seldom after) the reference moves and the step is done again.
+        // way; only when that is more than 8 above the reference (seldom) the
+        // reference moves and the step is done again.
         uint32_t P[64];
         for (;;) {
           const float off = kLift - (ref == kNoRef ? 0.0f : ref);  // (kNoRef itself would swallow the scores)
@@ -343,9 +387,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
               for (int e = 0; e < 16; ++e) {
                 float2 t = make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
                 if constexpr (kE4M3) {
-                  const float2 ks = *reinterpret_cast<const float2*>(sl.ks + 32 * k + 2 * e);
-                  const float2 lv = *reinterpret_cast<const float2*>(sl.lv + 32 * k + 2 * e);
-                  t = ffma2(t, make_float2(ks.x * c, ks.y * c), make_float2(lv.x + off, lv.y + off));
+                  float2 mm, oo;
+                  log_scale(32 * k + 2 * e, off, mm, oo);
+                  t = ffma2(t, mm, oo);
                 } else {
                   t = ffma2(t, make_float2(c, c), make_float2(off, off));
                 }
@@ -387,11 +431,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
         tmem_store32(tS + 32, reinterpret_cast<uint32_t(&)[32]>(P[32]));
         tmem_wait_st();
         tmem_before_sync();
-        mbar_arrive(bar(kPReady + wt));
+        warp_arrive(bar(Sm::kPReady + wt));
       }
       if (!ok) break;
       // ---- the unit's rows
-      ok = __all_sync(kFull, wait_or_stop(bar(kODone + wt), done & 1, stop));
+      ok = __all_sync(kFull, wait_or_stop(bar(Sm::kODone + wt), done & 1, stop));
       if (!ok) break;
       ++done;
       tmem_after_sync();
@@ -481,7 +525,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
     constexpr int IT = 32 / RPI;
     const int lr = lane / LPR, lc = lane % LPR;
     uint32_t n = 0;   // steps of the block so far
-    uint32_t u = 0;   // units
+    uint32_t u = 0;   // units with rows in the warp's tile of queries
+    const int qt = lw >> 1;
     bool ok = true;
     // the loader's 32 keys of a step: key lw * 32 + lane is this lane's
     auto entry = [&](int32_t i) -> int32_t {
@@ -515,12 +560,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
     };
 
     // the unit's queries: 64 rows a warp, the row's address looked up by a lane each
-    auto load_queries = [&]() {
+    auto query_rows = [&](int64_t& qa, int64_t& qb) {
       auto q_at = [&](int32_t f) -> int64_t {
         const int32_t ff = g.f0 + f;
         return f < g.nf ? (g.q.row0 + ff / a.G) * a.q_stride + static_cast<int64_t>(g.h * a.G + ff % a.G) * D : -1;
       };
-      const int64_t qa = q_at(lw * 64 + lane), qb = q_at(lw * 64 + 32 + lane);
+      qa = q_at(lw * 64 + lane);
+      qb = q_at(lw * 64 + 32 + lane);
+    };
+    auto load_queries = [&](int64_t qa, int64_t qb) {
       constexpr int QP = kPieces / 8;  // pieces of a row a lane; 8 lanes a row, 4 rows a round
       const int ql = lane >> 3, qc = lane & 7;
       auto q_tile = [&](int rr) { return base + Sm::kQ + ((lw * 64 + rr) >> 7) * Sm::kOperand; };
@@ -583,7 +631,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
             int ex = 14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23);
             ex = amax > 0.0f ? max(-100, min(100, ex)) : 0;
             const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-            if (qc == 0) qscale[lw * 64 + rr] = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+            if (qc == 0) qscale[(u & 1) * kRows + lw * 64 + rr] = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
 #pragma unroll
             for (int k = 0; k < QP; ++k)
               v[z][k] = make_uint4(pack_h(x[k][0] * up, x[k][1] * up), pack_h(x[k][2] * up, x[k][3] * up),
@@ -598,113 +646,146 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
       }
     };
 
-    if constexpr (kE4M3) {
-      // Codes of the next step are on their way in registers while this
-      // step's are turned into fp16: K's are asked for once K is stored, V's once V is.
-      uint4 kv[IT], vv[IT];
-      auto fetch = [&](uint4 (&x)[IT], const Keys& k, int64_t off) {
-        const int64_t head = static_cast<int64_t>(g.h) * D + lc * 16;
+    auto full = [&](uint32_t t) { return bar(Sm::kFull + t % Sm::kRing); };
+    auto operand = [&](uint32_t t) { return base + Sm::kTiles + t % Sm::kRing * Sm::kOperand; };
+    // waits until tile t - kRing has been used
+    auto claim = [&](uint32_t t) { return wait(bar(Sm::kFree + t % Sm::kRing), (t / Sm::kRing & 1) ^ 1); };
+    auto copy = [&](auto at, int32_t row_of_lane, int64_t off) {  // at(round, piece): where a lane's piece goes
+      const int64_t head = static_cast<int64_t>(g.h) * RB + lc * 16;
 #pragma unroll
-        for (int it = 0; it < IT; ++it) {
-          const int64_t ro = __shfl_sync(kFull, k.row, it * RPI + lr);
-          x[it] = make_uint4(0, 0, 0, 0);
-          if (ro >= 0) x[it] = __ldg(reinterpret_cast<const uint4*>(pool + (ro + off) * row_bytes + head));
+      for (int it = 0; it < IT; ++it) {
+        const int64_t ro = __shfl_sync(kFull, row_of_lane, it * RPI + lr);
+        const uint8_t* src = pool + (ro >= 0 ? (ro + off) * row_bytes + head : 0);
+#pragma unroll
+        for (int z = 0; z < PPR; ++z) copy_async<16>(at(it, z), src + (ro >= 0 ? z * LPR * 16 : 0), ro >= 0);
+      }
+      copy_commit();
+    };
+    if constexpr (kE4M3) {
+      // A step's codes are copied one step ahead; a lane turns the very pieces
+      // that it copied into fp16, so the raw ring needs no barrier. Order of
+      // a step: copy K(n + 1), turn K(n), copy V(n + 1), turn V(n); the raw
+      // tile that a copy overwrites is the one turned just before it.
+      struct Step {
+        Keys k;
+        float ks, vs;
+        bool first, queries;  // first of its unit; the unit has rows in the warp's tile
+      };
+      const uint32_t raw0 = base + Sm::kRaw + lw * 32 * RB + lane * 16;
+      auto raw = [&](uint32_t t, int it) { return raw0 + t % 3 * (Sm::kOperand / 2) + it * 512; };
+      int64_t qa = -1, qb = -1;
+      // the step after the one in `walk`, as far as its lookups go
+      int32_t i = more ? g.step0 : 0, ent = more ? entry(g.step0) : 0;
+      bool have = more;
+      auto look = [&]() -> Step {
+        Step s;
+        s.k = keys_of(i, ent);
+        s.first = i == g.step0;
+        s.queries = qt * 128 < g.nf;
+        ent = entry(i + 1);
+        s.ks = s.vs = 0.0f;
+        if (s.k.page != 0) {
+          const int64_t at = (static_cast<int64_t>(s.k.page) * p.blocks + 2 * a.layer) * a.H + g.h;
+          s.ks = __ldg(a.scales + at);
+          s.vs = __ldg(a.scales + at + a.H);
+        }
+        return s;
+      };
+      auto advance = [&]() {
+        if (++i == g.end) {
+          have = walk.next();
+          if (have) {
+            i = g.step0;
+            ent = entry(i);
+          }
         }
       };
-      for (; more && ok; more = walk.next(), ++u) {
-        int32_t ent = entry(g.step0 + 1);
-        Keys cur = keys_of(g.step0, entry(g.step0));
-        float ks = 0.0f, vs = 0.0f;
-        auto fetch_scales = [&](const Keys& k) {
-          ks = vs = 0.0f;
-          if (k.page != 0) {
-            const int64_t at = (static_cast<int64_t>(k.page) * p.blocks + 2 * a.layer) * a.H + g.h;
-            ks = __ldg(a.scales + at);
-            vs = __ldg(a.scales + at + a.H);
-          }
-        };
-        fetch_scales(cur);
-        fetch(kv, cur, 0);
-        fetch(vv, cur, p.ps);
-        for (int32_t i = g.step0; i < g.end; ++i, ++n) {
-          const uint32_t stage = n & 1, parity = ((n >> 1) & 1) ^ 1;
-          const uint32_t kt = base + Sm::kK + stage * Sm::kOperand, vt = base + Sm::kV + stage * Sm::kOperand;
-          Slot& sl = slots[n % kSlots];
-          if (!wait(bar(kKFree + stage), parity)) break;
-          sl.ks[lw * 32 + lane] = cur.page != 0 ? ks : 1.0f;  // no token: 2^-inf through lv, whatever the score
-          sl.lv[lw * 32 + lane] = lg2(vs);
-          sl.iv[lw * 32 + lane] = cur.page != 0 ? __fdividef(1.0f, vs) : 0.0f;
-          if (lane == 0) sl.live[lw] = cur.live;
-#pragma unroll
-          for (int it = 0; it < IT; ++it) {
-            const int rr = lw * 32 + it * RPI + lr;
-            uint4 lo, hi;
-            decode16(kv[it], lo, hi);
-            sts128(kt + piece_at(rr, 2 * lc), lo);
-            sts128(kt + piece_at(rr, 2 * lc + 1), hi);
-          }
-          fence_async_shared();
-          mbar_arrive(bar(kKFull + stage));
-          if (i == g.step0) {
-            if (!wait(bar(kQFree), (u & 1) ^ 1)) break;
-            load_queries();
-            fence_async_shared();
-            mbar_arrive(bar(kQFull));
-          }
-          Keys next{-1, 0, 0, false};
-          if (i + 1 < g.end) {
-            next = keys_of(i + 1, ent);
-            ent = entry(i + 2);
-            fetch_scales(next);
-            fetch(kv, next, 0);
-          }
-          if (!wait(bar(kVFree + stage), parity)) break;
-          uint32_t bad_rows = 0;
-#pragma unroll
-          for (int it = 0; it < IT; ++it) {
-            const int rr = lw * 32 + it * RPI + lr;
-            if (cur.partial) {
-              const uint4 z = make_uint4(not_finite<C>(vv[it].x), not_finite<C>(vv[it].y), not_finite<C>(vv[it].z),
-                                         not_finite<C>(vv[it].w));
-              if (z.x | z.y | z.z | z.w) {
-                bad_rows |= 1u << (it * RPI + lr);
-                vv[it] = make_uint4(vv[it].x & ~z.x, vv[it].y & ~z.y, vv[it].z & ~z.z, vv[it].w & ~z.w);
-              }
-            }
-            uint4 lo, hi;
-            decode16(vv[it], lo, hi);
-            sts128(vt + piece_at(rr, 2 * lc), lo);
-            sts128(vt + piece_at(rr, 2 * lc + 1), hi);
-          }
-          bad_rows = __reduce_or_sync(kFull, bad_rows);
-          if (lane == 0) sl.nan[lw] = bad_rows;
-          fence_async_shared();
-          mbar_arrive(bar(kVFull + stage));
-          cur = next;
-          if (i + 1 < g.end) fetch(vv, cur, p.ps);
-        }
-      }
-    } else {
-      // One more copy is always in flight: V of a step is announced after K of
-      // the next has been asked for, K after V of its own step.
-      bool pending = false, pending_partial = false;
-      auto copy = [&](uint32_t to, const Keys& k, int64_t off) {
-        const int64_t head = static_cast<int64_t>(g.h) * RB;
+      auto turn_tile = [&](uint32_t t, bool check) -> uint32_t {
+        uint32_t bad_rows = 0;
+        const uint32_t to = operand(t);
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
-          const int rr = it * RPI + lr;
-          const int64_t ro = __shfl_sync(kFull, k.row, rr);
-          const uint8_t* src = pool + (ro >= 0 ? (ro + off) * row_bytes + head : 0) + lc * 16;
-#pragma unroll
-          for (int z = 0; z < PPR; ++z)
-            copy_async<16>(to + piece_at(lw * 32 + rr, lc + z * LPR), src + z * LPR * 16, ro >= 0);
+          uint4 v = lds128(raw(t, it));
+          if (check) {
+            const uint4 z = make_uint4(not_finite<C>(v.x), not_finite<C>(v.y), not_finite<C>(v.z), not_finite<C>(v.w));
+            if (z.x | z.y | z.z | z.w) {
+              bad_rows |= 1u << (it * RPI + lr);
+              v = make_uint4(v.x & ~z.x, v.y & ~z.y, v.z & ~z.z, v.w & ~z.w);
+            }
+          }
+          uint4 lo, hi;
+          decode16(v, lo, hi);
+          const int rr = lw * 32 + it * RPI + lr;
+          sts128(to + piece_at(rr, 2 * lc), lo);
+          sts128(to + piece_at(rr, 2 * lc + 1), hi);
         }
-        copy_commit();
+        fence_async_shared();
+        return bad_rows;
+      };
+      if (have) {
+        Step cur = look();
+        copy([&](int it, int) { return raw(0, it); }, cur.k.row, 0);
+        copy([&](int it, int) { return raw(1, it); }, cur.k.row, p.ps);
+        query_rows(qa, qb);
+        for (bool go = true; go;) {
+          const uint32_t t = 2 * n;
+          int64_t na = -1, nb = -1;
+          advance();
+          go = have;
+          Step next{};
+          if (have) {
+            next = look();
+            copy([&](int it, int) { return raw(t + 2, it); }, next.k.row, 0);
+            if (next.first) query_rows(na, nb);
+          } else {
+            copy_commit();
+          }
+          copy_wait<2>();
+          if (!claim(t)) break;
+          Scales& sl = scales[n % kSlots];
+          sl.ks[lw * 32 + lane] = cur.k.page != 0 ? cur.ks : 1.0f;  // no token: 2^-inf through lv, whatever the score
+          sl.lv[lw * 32 + lane] = lg2(cur.vs);
+          sl.iv[lw * 32 + lane] = cur.k.page != 0 ? __fdividef(1.0f, cur.vs) : 0.0f;
+          if (lane == 0) masks[n % kSlots].live[lw] = cur.k.live;
+          turn_tile(t, false);
+          warp_arrive(full(t));
+          if (cur.first && cur.queries) {
+            if (!wait(bar(Sm::kQFree + qt), (u & 1) ^ 1)) break;
+            load_queries(qa, qb);
+            fence_async_shared();
+            warp_arrive(bar(Sm::kQFull + qt));
+            ++u;
+          }
+          if (have)
+            copy([&](int it, int) { return raw(t + 3, it); }, next.k.row, p.ps);
+          else
+            copy_commit();
+          copy_wait<2>();
+          if (!claim(t + 1)) break;
+          const uint32_t bad_rows = __reduce_or_sync(kFull, turn_tile(t + 1, cur.k.partial));
+          if (lane == 0) masks[n % kSlots].nan[lw] = bad_rows;
+          warp_arrive(full(t + 1));
+          if (next.first) {
+            qa = na;
+            qb = nb;
+          }
+          cur = next;
+          ++n;
+        }
+      }
+      copy_wait<0>();
+    } else {
+      // One more copy is always in flight: a tile is announced after the next
+      // one has been asked for.
+      bool pending = false, pending_partial = false;
+      auto put = [&](uint32_t t, const Keys& k, int64_t off) {
+        const uint32_t to = operand(t);
+        copy([&](int it, int z) { return to + piece_at(lw * 32 + it * RPI + lr, lc + z * LPR); }, k.row, off);
       };
       auto announce_v = [&](uint32_t m) {  // V of step m has arrived
         uint32_t bad_rows = 0;
         if (pending_partial) {
-          const uint32_t vt = base + Sm::kV + (m & 1) * Sm::kOperand;
+          const uint32_t vt = operand(2 * m + 1);
 #pragma unroll
           for (int it = 0; it < IT; ++it)
 #pragma unroll
@@ -719,99 +800,134 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
             }
         }
         bad_rows = __reduce_or_sync(kFull, bad_rows);
-        if (lane == 0) slots[m % kSlots].nan[lw] = bad_rows;
+        if (lane == 0) masks[m % kSlots].nan[lw] = bad_rows;
         fence_async_shared();
-        mbar_arrive(bar(kVFull + (m & 1)));
+        warp_arrive(full(2 * m + 1));
         pending = false;
       };
-      for (; more && ok; more = walk.next(), ++u) {
+      for (; more && ok; more = walk.next()) {
+        const bool queries = qt * 128 < g.nf;
         int32_t ent = entry(g.step0);
         for (int32_t i = g.step0; i < g.end; ++i, ++n) {
-          const uint32_t stage = n & 1, parity = ((n >> 1) & 1) ^ 1;
           const Keys cur = keys_of(i, ent);
           ent = entry(i + 1);
-          if (!wait(bar(kKFree + stage), parity)) break;
-          if (lane == 0) slots[n % kSlots].live[lw] = cur.live;
-          copy(base + Sm::kK + stage * Sm::kOperand, cur, 0);
+          if (!claim(2 * n)) break;
+          if (lane == 0) masks[n % kSlots].live[lw] = cur.live;
+          put(2 * n, cur, 0);
           if (pending) {
             copy_wait<1>();
             announce_v(n - 1);
           }
-          if (i == g.step0) {
-            if (!wait(bar(kQFree), (u & 1) ^ 1)) break;
-            load_queries();
+          if (i == g.step0 && queries) {
+            if (!wait(bar(Sm::kQFree + qt), (u & 1) ^ 1)) break;
+            int64_t qa, qb;
+            query_rows(qa, qb);
+            load_queries(qa, qb);
             copy_commit();
           }
-          if (!wait(bar(kVFree + stage), parity)) break;
-          copy(base + Sm::kV + stage * Sm::kOperand, cur, p.ps);
+          if (!claim(2 * n + 1)) break;
+          put(2 * n + 1, cur, p.ps);
           pending = true;
           pending_partial = cur.partial;
           copy_wait<1>();
           fence_async_shared();
-          mbar_arrive(bar(kKFull + stage));
-          if (i == g.step0) mbar_arrive(bar(kQFull));
+          warp_arrive(full(2 * n));
+          if (i == g.step0 && queries) {
+            warp_arrive(bar(Sm::kQFull + qt));
+            ++u;
+          }
         }
       }
       copy_wait<0>();
       if (pending && ok) announce_v(n - 1);
     }
-    copy_wait<0>();
   } else {
-    if (warp == 12 && lane == 0) {
+    if (warp == 12) {
+      // All lanes run along, so that operands and waits stay warp-uniform (a lone
+      // lane's operands would be moved to uniform registers one by one, which
+      // took 85 cycles a product against its 64); one elected lane issues.
       // ------------------------------------------------------------- products
       constexpr uint32_t kQK = umma_f16(kBf16, kKeys, false), kPV = umma_f16(kBf16, D, true);
-      uint32_t n = 0, u = 0;
-      uint32_t cnt[2] = {0, 0};  // steps of each tile
+      const bool elected = elect_one();
+      const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+      uint32_t n = 0;
+      uint32_t weights[2] = {0, 0}, queries[2] = {0, 0};  // phases of each tile's barriers
       bool ok = true;
-      auto qk = [&](int wt, uint32_t stage) {
+      auto slot_of = [&](uint32_t t) { return t % Sm::kRing; };
+      auto wait = [&](uint32_t at, uint32_t parity) { return __all_sync(kFull, wait_or_stop(at, parity, stop)) != 0; };
+      auto full = [&](uint32_t t) { return wait(bar(Sm::kFull + slot_of(t)), t / Sm::kRing & 1); };
+      const uint32_t ub = __shfl_sync(kFull, base, 0);
+      const uint32_t q0 = smem_operand_lo(ub + Sm::kQ, 16), k0 = smem_operand_lo(ub + Sm::kTiles, 16);
+      const uint32_t v0 = smem_operand_lo(ub + Sm::kTiles, 128 * 128);
+      auto qk = [&](int wt, uint32_t t) {
+        const uint32_t qd = q0 + wt * (Sm::kOperand >> 4), kd = k0 + slot_of(t) * (Sm::kOperand >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t at = (k >> 2) * (128 * 128) + (k & 3) * 32;
-          umma_ss(tmem + wt * 128, smem_operand(base + Sm::kQ + wt * Sm::kOperand + at, 16),
-                  smem_operand(base + Sm::kK + stage * Sm::kOperand + at, 16), kQK, k > 0);
+          const uint32_t at = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+          umma_ss(elected, tm + wt * 128, qd + at, kd + at, kQK, k > 0);
         }
-        umma_commit(bar(kSFull + wt));
+        umma_commit(elected, bar(Sm::kSFull + wt));
       };
-      auto pv = [&](int wt, uint32_t stage, bool add) {
+      auto pv = [&](int wt, uint32_t t, bool add) {
+        const uint32_t vd = v0 + slot_of(t) * (Sm::kOperand >> 4);
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k)
-          umma_ts(tmem + 256 + wt * D, tmem + wt * 128 + k * 8,
-                  smem_operand(base + Sm::kV + stage * Sm::kOperand + k * 2048, 128 * 128), kPV, add || k > 0);
+          umma_ts(elected, tm + 256 + wt * D, tm + wt * 128 + k * 8, vd + (k * 2048 >> 4), kPV, add || k > 0);
       };
-      for (; more && ok; more = walk.next(), ++u) {
-        const int nt = g.nf > 128 ? 2 : 1;
-        ok = wait_or_stop(bar(kKFull + (n & 1)), (n >> 1) & 1, stop) && wait_or_stop(bar(kQFull), u & 1, stop);
-        if (!ok) break;
+      auto scores = [&](int wt, uint32_t t, bool first, bool last) {
+        if (first) ok = wait(bar(Sm::kQFull + wt), queries[wt]++ & 1);
+        if (!ok) return;
         tmem_after_sync();
-        for (int wt = 0; wt < nt; ++wt) qk(wt, n & 1);
-        umma_commit(bar(kKFree + (n & 1)));
-        if (g.end - g.step0 == 1) umma_commit(bar(kQFree));
-        for (int32_t i = g.step0; i < g.end; ++i, ++n) {
-          const uint32_t stage = n & 1, phase = (n >> 1) & 1;
-          const bool last = i + 1 == g.end;
-          for (int wt = 0; wt < nt && ok; ++wt) {
-            ok = wait_or_stop(bar(kPReady + wt), cnt[wt] & 1, stop) && wait_or_stop(bar(kVFull + stage), phase, stop);
-            if (ok && !last) ok = wait_or_stop(bar(kKFull + (stage ^ 1)), ((n + 1) >> 1) & 1, stop);
-            if (!ok) break;
-            ++cnt[wt];
-            tmem_after_sync();
-            pv(wt, stage, i > g.step0);
-            if (last)
-              umma_commit(bar(kODone + wt));
-            else
-              qk(wt, stage ^ 1);
-          }
-          if (!ok) break;
-          umma_commit(bar(kVFree + stage));
-          if (!last) {
-            umma_commit(bar(kKFree + (stage ^ 1)));
-            if (i + 2 == g.end) umma_commit(bar(kQFree));
-          }
-        }
+        qk(wt, t);
+        if (last) umma_commit(elected, bar(Sm::kQFree + wt));
+      };
+      // Runs on from unit to unit: behind a tile's O += P V comes its next S,
+      // be it the next unit's first.
+      more = __any_sync(kFull, more);
+      int nt = __shfl_sync(kFull, g.nf > 128 ? 2 : 1, 0);
+      int32_t i = 0, steps = __shfl_sync(kFull, g.end - g.step0, 0);
+      if (more) {
+        ok = full(0);
+        scores(0, 0, true, steps == 1);
+        if (ok && nt > 1) scores(1, 0, true, steps == 1);
+        umma_commit(elected, bar(Sm::kFree));
       }
-      umma_commit(bar(kDrain));  // tensor memory is freed when nothing is in flight
+#pragma unroll 1
+      while (more && ok) {
+        const bool last = i + 1 == steps;
+        int next_nt = nt;
+        int32_t next_i = i + 1, next_steps = steps;
+        if (last) {
+          more = __any_sync(kFull, walk.next());
+          next_nt = __shfl_sync(kFull, !more ? 0 : g.nf > 128 ? 2 : 1, 0);
+          next_i = 0;
+          next_steps = __shfl_sync(kFull, g.end - g.step0, 0);
+        }
+        // V of this step and K of the next are there long before the weights as a rule
+        ok = full(2 * n + 1) && (!more || full(2 * n + 2));
+#pragma unroll
+        for (int wt = 0; wt < 2; ++wt) {
+          if (ok && wt < nt) {
+            ok = wait(bar(Sm::kPReady + wt), weights[wt]++ & 1);
+            if (ok) {
+              tmem_after_sync();
+              pv(wt, 2 * n + 1, i > 0);
+              if (last) umma_commit(elected, bar(Sm::kODone + wt));
+            }
+          }
+          if (ok && wt < next_nt) scores(wt, 2 * n + 2, next_i == 0, next_i + 1 == next_steps);
+        }
+        if (!ok) break;
+        umma_commit(elected, bar(Sm::kFree + slot_of(2 * n + 1)));
+        if (more) umma_commit(elected, bar(Sm::kFree + slot_of(2 * n + 2)));
+        i = next_i;
+        steps = next_steps;
+        nt = next_nt;
+        ++n;
+      }
+      umma_commit(elected, bar(Sm::kDrain));  // tensor memory is freed when nothing is in flight
       const long long t0 = clock64();
-      while (!mbar_try(bar(kDrain), 0) && clock64() - t0 < kWaitClocks) {
+      while (!mbar_try(bar(Sm::kDrain), 0) && clock64() - t0 < kWaitClocks) {
       }
     }
     __syncwarp();
@@ -829,7 +945,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
 
 template <class C, int D, bool P16>
 cudaError_t prepare_one() {
-  return cudaFuncSetAttribute(k_attend_tile<C, D, P16>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileSmem<D>::kBytes);
+  return cudaFuncSetAttribute(k_attend_tile<C, D, P16>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileSmem<C, D>::kBytes);
 }
 
 constexpr int kMinShare = 2;  // steps of 128 keys below which a block's share is not cut
@@ -870,7 +986,7 @@ cudaError_t launch_attend_tile(const DevPool& p, const Batch& b, const AttendArg
   *out = w;
   auto go = [&]<class C, bool P16>() {
     auto kernel = a.D == 64 ? k_attend_tile<C, 64, P16> : k_attend_tile<C, 128, P16>;
-    const int smem = a.D == 64 ? TileSmem<64>::kBytes : TileSmem<128>::kBytes;
+    const int smem = a.D == 64 ? TileSmem<C, 64>::kBytes : TileSmem<C, 128>::kBytes;
     if (after) return launch_overlapped(kernel, dim3(w.blocks), kTileThreads, smem, s, p, b, a, w);
     kernel<<<w.blocks, kTileThreads, smem, s>>>(p, b, a, w);
     return cudaGetLastError();

@@ -104,10 +104,9 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16
 // K-major (rows are M or N, 64 16-bit elements of K each): groups of 8 rows
 // follow each other at 1024 bytes. M/N-major (rows are K): groups of 8 K at
 // 1024 bytes, the next 64 of M/N `lead` bytes on.
-__device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lead) {
-  return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | static_cast<uint64_t>(lead >> 4) << 16 |
-         static_cast<uint64_t>(1024 >> 4) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
-}
+// The descriptor's low word (addresses add to it in units of 16 bytes) and its constant high word.
+__device__ __forceinline__ uint32_t smem_operand_lo(uint32_t addr, uint32_t lead) { return addr >> 4 | lead >> 4 << 16; }
+constexpr uint32_t kOperandHi = 1024 >> 4 | 1u << 14 | 2u << 29;
 
 // kind::f16 with 32-bit sums, M = 128; bf16: operands are bf16, else fp16.
 __host__ __device__ constexpr uint32_t umma_f16(bool bf16, int n, bool b_mn_major) {
@@ -115,23 +114,34 @@ __host__ __device__ constexpr uint32_t umma_f16(bool bf16, int n, bool b_mn_majo
          static_cast<uint32_t>(n / 8) << 17 | (128u / 16) << 24;
 }
 
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void umma_ss(bool elected, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "{\n .reg .pred p, e;\n .reg .b64 a, b;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 e, %6, 0;\n mov.b64 a, {%1, %5};\n"
+      " mov.b64 b, {%2, %5};\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(kOperandHi), "r"(static_cast<uint32_t>(elected))
       : "memory");
 }
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void umma_ts(bool elected, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "{\n .reg .pred p, e;\n .reg .b64 b;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 e, %6, 0;\n mov.b64 b, {%2, %5};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(kOperandHi), "r"(static_cast<uint32_t>(elected))
       : "memory");
 }
-// Arrives on `bar` when all products issued by this thread so far are done.
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// Products and commits are issued by the elected lane; the others pass them over.
+// A commit arrives on `bar` when all products that lane issued so far are done.
+__device__ __forceinline__ void umma_commit(bool elected, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.u32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
+      "r"(static_cast<uint32_t>(elected))
+      : "memory");
+}
+// One lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+  return e != 0;
 }
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
