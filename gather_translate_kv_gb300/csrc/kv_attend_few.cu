@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
   auto tiles_of = [&](const Seq& q) { return q.n == 0 || q.n > w.max_new ? 0 : (q.n * a.G + NQ - 1) / NQ; };
   auto span_of = [&](const Seq& q, int32_t t) {
     const int32_t f0 = t * NQ, f1 = min(f0 + NQ, q.n * a.G);
-    return key_span<16>(a, q, f0, f1);
+    return key_span<16>(a, q.a + f0 / a.G, q.a + (f1 - 1) / a.G);
   };
   const int32_t worker0 = static_cast<int32_t>(blockIdx.x) * kw;
   const int64_t share = find_shares<kFewBlock, kFewWarps>(

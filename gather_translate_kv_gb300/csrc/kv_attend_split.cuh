@@ -18,7 +18,7 @@
 
 namespace gtkv {
 
-// Rows [f0, f1) of sequence q: blocks [0, n_first) and [b0, b1) of `step` keys.
+// Rows at positions i0 to i1: blocks [0, n_first) and [b0, b1) of STEP keys.
 struct KeySpan {
   int32_t n_first;  // blocks that hold the first tokens, before the window's
   int32_t b0, b1;
@@ -27,8 +27,7 @@ struct KeySpan {
 };
 
 template <int STEP>
-__device__ __forceinline__ KeySpan key_span(const AttendArgs& a, const Seq& q, int32_t f0, int32_t f1) {
-  const int32_t i0 = q.a + f0 / a.G, i1 = q.a + (f1 - 1) / a.G;  // first and last position
+__device__ __forceinline__ KeySpan key_span(const AttendArgs& a, int32_t i0, int32_t i1) {
   KeySpan k;
   k.b1 = i1 / STEP + 1;
   const int32_t lo = a.window && i0 + 1 > a.window ? i0 + 1 - a.window : 0;

@@ -80,6 +80,7 @@ struct Segment {
   int32_t s, tile, h;
   int32_t step0, end;
   int32_t f0, nf;  // rows
+  int32_t i0, i1;  // positions of the first and the last
 };
 
 template <bool kE4M3>
@@ -97,7 +98,9 @@ struct TileWalk {
   __device__ __forceinline__ void shape() {
     g.f0 = g.tile * kRows;
     g.nf = min(kRows, g.q.n * a.G - g.f0);
-    g.span = key_span<kKeys>(a, g.q, g.f0, g.f0 + g.nf);
+    g.i0 = g.q.a + g.f0 / a.G;
+    g.i1 = g.q.a + (g.f0 + g.nf - 1) / a.G;
+    g.span = key_span<kKeys>(a, g.i0, g.i1);
   }
   __device__ __forceinline__ bool cut() {
     if (left <= 0) return false;
@@ -517,7 +520,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
     // ------------------------------------------------------------- loaders
     const int lw = warp - 8;
     const uint8_t* pool = reinterpret_cast<const uint8_t*>(p.base);
-    const int64_t row_bytes = p.vpr * 16;
     constexpr int RB = kE4M3 ? D : 2 * D;           // bytes of a head's row
     constexpr int LPR = RB / 16 < 8 ? RB / 16 : 8;  // lanes a row
     constexpr int RPI = 32 / LPR;                   // rows a round
@@ -532,8 +534,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
     auto entry = [&](int32_t i) -> int32_t {
       if (i >= g.end) return 0;
       const int64_t j = static_cast<int64_t>(g.span.block(i)) * kKeys + lw * 32 + lane;
-      const int32_t last = g.q.a + (g.f0 + g.nf - 1) / a.G;
-      if (j > last) return 0;
+      if (j > g.i1) return 0;
       return __ldg(b.table + static_cast<int64_t>(g.s) * b.max_pages + div_ps(p, j));
     };
     struct Keys {
@@ -550,8 +551,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
                           : static_cast<int32_t>(k.page * p.stride + 2 * static_cast<int64_t>(a.layer) * p.ps +
                                                  (j - div_ps(p, j) * p.ps));
       k.live = __ballot_sync(kFull, k.page != 0);
-      const int32_t i0 = g.q.a + g.f0 / a.G, i1 = g.q.a + (g.f0 + g.nf - 1) / a.G;
-      k.partial = j0 + kKeys - 1 > i0 || (a.window && j0 <= i1 - a.window) || k.live != kFull;
+      k.partial = j0 + kKeys - 1 > g.i0 || (a.window && j0 <= g.i1 - a.window) || k.live != kFull;
       return k;
     };
     auto wait = [&](uint32_t at, uint32_t parity) {
@@ -650,14 +650,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
     auto operand = [&](uint32_t t) { return base + Sm::kTiles + t % Sm::kRing * Sm::kOperand; };
     // waits until tile t - kRing has been used
     auto claim = [&](uint32_t t) { return wait(bar(Sm::kFree + t % Sm::kRing), (t / Sm::kRing & 1) ^ 1); };
-    auto copy = [&](auto at, int32_t row_of_lane, int64_t off) {  // at(round, piece): where a lane's piece goes
-      const int64_t head = static_cast<int64_t>(g.h) * RB + lc * 16;
+    const int32_t row_bytes = static_cast<int32_t>(p.vpr * 16);
+    // Copies 32 rows (of lane k the k-th) of K, or of V when `v`; at(round, piece): where a lane's piece goes.
+    auto copy = [&](auto at, int32_t row_of_lane, bool v) {
+      const uint8_t* from = pool + static_cast<int64_t>(g.h) * RB + lc * 16 + (v ? p.ps * row_bytes : 0);
+      int32_t ro[IT];  // all shuffles first: their latencies overlap
+#pragma unroll
+      for (int it = 0; it < IT; ++it) ro[it] = __shfl_sync(kFull, row_of_lane, it * RPI + lr);
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
-        const int64_t ro = __shfl_sync(kFull, row_of_lane, it * RPI + lr);
-        const uint8_t* src = pool + (ro >= 0 ? (ro + off) * row_bytes + head : 0);
+        const bool ok = ro[it] >= 0;
+        const uint8_t* src = from + static_cast<int64_t>(ok ? ro[it] : 0) * row_bytes;
 #pragma unroll
-        for (int z = 0; z < PPR; ++z) copy_async<16>(at(it, z), src + (ro >= 0 ? z * LPR * 16 : 0), ro >= 0);
+        for (int z = 0; z < PPR; ++z) copy_async<16>(at(it, z), src + z * LPR * 16, ok);
       }
       copy_commit();
     };
@@ -724,8 +729,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
       };
       if (have) {
         Step cur = look();
-        copy([&](int it, int) { return raw(0, it); }, cur.k.row, 0);
-        copy([&](int it, int) { return raw(1, it); }, cur.k.row, p.ps);
+        copy([&](int it, int) { return raw(0, it); }, cur.k.row, false);
+        copy([&](int it, int) { return raw(1, it); }, cur.k.row, true);
         query_rows(qa, qb);
         for (bool go = true; go;) {
           const uint32_t t = 2 * n;
@@ -735,7 +740,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           Step next{};
           if (have) {
             next = look();
-            copy([&](int it, int) { return raw(t + 2, it); }, next.k.row, 0);
+            copy([&](int it, int) { return raw(t + 2, it); }, next.k.row, false);
             if (next.first) query_rows(na, nb);
           } else {
             copy_commit();
@@ -757,7 +762,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
             ++u;
           }
           if (have)
-            copy([&](int it, int) { return raw(t + 3, it); }, next.k.row, p.ps);
+            copy([&](int it, int) { return raw(t + 3, it); }, next.k.row, true);
           else
             copy_commit();
           copy_wait<2>();
@@ -778,9 +783,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
       // One more copy is always in flight: a tile is announced after the next
       // one has been asked for.
       bool pending = false, pending_partial = false;
-      auto put = [&](uint32_t t, const Keys& k, int64_t off) {
+      auto put = [&](uint32_t t, const Keys& k) {
         const uint32_t to = operand(t);
-        copy([&](int it, int z) { return to + piece_at(lw * 32 + it * RPI + lr, lc + z * LPR); }, k.row, off);
+        copy([&](int it, int z) { return to + piece_at(lw * 32 + it * RPI + lr, lc + z * LPR); }, k.row, t & 1);
       };
       auto announce_v = [&](uint32_t m) {  // V of step m has arrived
         uint32_t bad_rows = 0;
@@ -813,7 +818,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           ent = entry(i + 1);
           if (!claim(2 * n)) break;
           if (lane == 0) masks[n % kSlots].live[lw] = cur.live;
-          put(2 * n, cur, 0);
+          put(2 * n, cur);
           if (pending) {
             copy_wait<1>();
             announce_v(n - 1);
@@ -826,7 +831,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
             copy_commit();
           }
           if (!claim(2 * n + 1)) break;
-          put(2 * n + 1, cur, p.ps);
+          put(2 * n + 1, cur);
           pending = true;
           pending_partial = cur.partial;
           copy_wait<1>();
