@@ -197,41 +197,50 @@ __device__ __forceinline__ int64_t scale_at(const DevPool& p, int32_t H, int64_t
   return (page * p.blocks + 2 * layer + kv) * H + h;  // blocks = 2L: [page][layer][K or V][head]
 }
 
-// One row: heads [h_lo, h_hi) of the list (queries, keys, values). A lane keeps its task
-// and so its cosines and sines for all heads; four heads' loads are in flight
-// before any store.
+// Heads [0, heads) of the list (queries, keys, values) of rows r0 on, tpr
+// threads a row (32, 64, ... 256). A lane keeps its task and so its cosines
+// and sines for all heads. The loads of U heads are issued before the row's place is
+// looked up: the lookups are a chain of dependent loads, four or five round trips long.
 template <class T>
-__device__ __forceinline__ void append_row(const DevPool& p, const Batch& b, const AppendArgs& g, const Rot& t,
-                                           int64_t r, int h_lo, int h_hi, int& bits) {
+__device__ __forceinline__ void append_rows(const DevPool& p, const Batch& b, const AppendArgs& g, const Rot& t,
+                                            int64_t r0, int tpr, int heads, int& bits) {
+  const int64_t r = r0 + threadIdx.x / tpr;
+  if (r >= b.n_rows) return;  // whole warps
+  const int lt = threadIdx.x % tpr;
   const int nt = g.D / 16;
-  const int groups = kAppendBlock / nt;
-  const int grp = threadIdx.x / nt;
+  const int groups = tpr / nt;
+  const int grp = lt / nt;
+  const Task task = task_of(t, lt - grp * nt);
+  const T* q = static_cast<const T*>(g.q) + r * g.q_stride;
+  const T* kk = static_cast<const T*>(g.k) + r * g.k_stride;
+  const T* vv = static_cast<const T*>(g.v) + r * g.v_stride;
+  constexpr int U = sizeof(T) == 2 ? 6 : 3;
+  Raw<T> raw[U];
+  const int h_lo = grp < groups ? grp : heads;  // lanes left over by the tasks have no head
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * groups;
+      if (h < heads)
+        raw[u] = load_raw<T>(h < g.Q ? q + h * g.D : h < g.Q + g.H ? kk + (h - g.Q) * g.D : vv + (h - g.Q - g.H) * g.D,
+                             task);
+    }
+  };
+  load(h_lo);
   const Token k = token_of_row(p, b, r, bits);
-  if (!k.ok || grp >= groups) return;
+  if (!k.ok) return;
   if (!positions_ok(t, b, r, k.j)) {
     bits |= KV_DEV_ERR_POSITION;
     return;
   }
-  const Task task = task_of(t, threadIdx.x - grp * nt);
   float c[8], s[8];
   if (task.c8 >= 0) load_cs(t, b, r, k.j, task, c, s);
-  const T* q = static_cast<const T*>(g.q) + r * g.q_stride;
-  const T* kk = static_cast<const T*>(g.k) + r * g.k_stride;
-  const T* vv = static_cast<const T*>(g.v) + r * g.v_stride;
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;
-  for (int h0 = h_lo + grp; h0 < h_hi; h0 += groups * U) {
-    Raw<T> raw[U];
+  for (int h0 = h_lo; h0 < heads; h0 += groups * U) {
+    if (h0 != h_lo) load(h0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = h0 + u * groups;
-      if (h < h_hi)
-        raw[u] = load_raw<T>(h < g.Q ? q + h * g.D : h < g.Q + g.H ? kk + (h - g.Q) * g.D : vv + (h - g.Q - g.H) * g.D,
-                             task);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * groups;
-      if (h >= h_hi) break;
+      if (h >= heads) break;
       T* y;
       if (h < g.Q) {
         y = static_cast<T*>(g.q_out) + (r * g.Q + h) * g.D;
@@ -252,12 +261,16 @@ __device__ __forceinline__ void append_row(const DevPool& p, const Batch& b, con
   }
 }
 
-// Pools that hold the inputs' own type: one block per row.
+// Threads a row: a quarter of a block where rows are many, so that a lane has
+// several heads' loads in flight; a whole block where there are few (a decode
+// step), whose time is the chain of lookups and not the traffic.
+inline int threads_per_row(int64_t n_rows) { return n_rows >= 1024 ? 64 : kAppendBlock; }
+
+// Pools that hold the inputs' own type.
 template <class T>
-__global__ void __launch_bounds__(kAppendBlock) k_append(DevPool p, Batch b, AppendArgs g, Rot t) {
+__global__ void __launch_bounds__(kAppendBlock) k_append(DevPool p, Batch b, AppendArgs g, Rot t, int tpr) {
   int bits = 0;
-  for (int64_t r = blockIdx.x; r < b.n_rows; r += gridDim.x)
-    append_row<T>(p, b, g, t, r, 0, g.Q + 2 * g.H, bits);
+  append_rows<T>(p, b, g, t, static_cast<int64_t>(blockIdx.x) * (kAppendBlock / tpr), tpr, g.Q + 2 * g.H, bits);
   store_bits(p, bits);
 }
 
@@ -274,125 +287,149 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a <= 3.402823466e38f ? a : 0.0f;  // infinities and NaN do not count
 }
 
-// The scale after the append, from the page's earlier scale and the largest new magnitude of the warp.
-__device__ __forceinline__ float new_scale(float amax, float* at, bool held, float* base) {
+// The scale after the append, from the page's earlier scale (0: none) and the largest new magnitude of the warp.
+__device__ __forceinline__ float new_scale(float amax, float old, float* base) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-  float old = held ? *at : 0.0f;
   if (!(old > 0.0f && old <= 3.402823466e38f)) old = 0.0f;
   *base = old;
   return fmaxf(old, power_of_two(amax));
 }
 
-// 8-bit pools. One warp takes one head of K or V of one page run: 32 / (D / 16)
-// tokens at a time, four such waves held in registers, so a run of up to 16
-// tokens of 128 elements (32 of 64) is read once; longer runs (pages past 16 or 32 tokens) are
-// read again, from L1 or L2, once the scale is known. Blocks after the runs'
-// rotate the queries, one row each.
+// 8-bit pools. A block takes one page run, a warp two heads of it at a time
+// (of K and of V where there are eight KV heads): 32 / (D / 16) tokens a
+// wave, four waves of both held in registers as they were loaded, so a run of up to
+// 16 tokens of 128 elements (32 of 64) is read once; longer runs are read
+// again, from L1 or L2, once the scale is known. The rotation is done twice, for the
+// maximum and for the codes: it is cheaper than the registers that would keep
+// its result. Blocks after the runs' rotate the queries.
 template <class T>
-__global__ void __launch_bounds__(kAppendBlock) k_append_e4m3(DevPool p, Batch b, AppendArgs g, Rot t, bool by_row,
-                                                              int64_t n_runs, int32_t blocks_per_run) {
+__global__ void __launch_bounds__(kAppendBlock, 2) k_append_e4m3(DevPool p, Batch b, AppendArgs g, Rot t, bool by_row,
+                                                              int64_t n_runs, int tpr) {
   int bits = 0;
-  const int64_t run_blocks = n_runs * blocks_per_run;
-  for (int64_t blk = blockIdx.x; blk < run_blocks + (g.Q ? b.n_rows : 0); blk += gridDim.x) {
-    if (blk >= run_blocks) {
-      append_row<T>(p, b, g, t, blk - run_blocks, 0, g.Q, bits);
-      continue;
-    }
-    const int64_t c = blk / blocks_per_run;
-    const int kvh = static_cast<int>(blk - c * blocks_per_run) * (kAppendBlock / 32) + (threadIdx.x >> 5);
-    if (kvh >= 2 * g.H) continue;
-    const PageRun run = page_run(p, b, c, by_row, bits);
-    if (run.m == 0 || run.page == 0) continue;
-    const int kv = kvh >= g.H, h = kvh - kv * g.H;
-    const int lane = threadIdx.x & 31;
-    const int nt = g.D / 16;
-    const int tpw = 32 / nt;  // tokens a wave
-    const int tok = lane / nt;
-    const bool in = tok < tpw;
-    Task task = task_of(t, lane - tok * nt);
-    const bool turned = kv == 0 && task.c8 >= 0;
-    const T* src = kv ? static_cast<const T*>(g.v) + h * g.D : static_cast<const T*>(g.k) + h * g.D;
-    const int64_t stride = kv ? g.v_stride : g.k_stride;
-    const int64_t j0 = static_cast<int64_t>(run.off);  // token j of the sequence is j0 + i plus whole pages
-    const Seq q = seq_of(p, b, run.s, bits);
-    const int64_t jseq = q.a + (run.row - q.row0);
-    constexpr int W = 4;
-    float x[W][16];
-    uint32_t have = 0;
-    auto load = [&](int i0) {
-      Raw<T> raw[W];
-      have = 0;
+  if (blockIdx.x >= n_runs) {
+    append_rows<T>(p, b, g, t, (blockIdx.x - n_runs) * static_cast<int64_t>(kAppendBlock / tpr), tpr, g.Q, bits);
+    store_bits(p, bits);
+    return;
+  }
+  const PageRun run = page_run(p, b, blockIdx.x, by_row, bits);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int NW = kAppendBlock / 32;
+  const int nt = g.D / 16;
+  const int tpw = 32 / nt;  // tokens a wave
+  const int tok = lane / nt;
+  const bool in = tok < tpw;
+  const Task task = task_of(t, lane - tok * nt);
+  constexpr int W = 4, HB = 1;
+  const bool one = run.m <= W * tpw;  // the run fits the registers
+  const bool held = run.off > 0;
+  for (int kvh0 = warp; run.m != 0 && run.page != 0 && kvh0 < 2 * g.H; kvh0 += NW * HB) {
+    Raw<T> raw[HB][W];
+    auto head = [&](int n) { return kvh0 + n * NW; };
+    auto load = [&](int n, int i0) {
+      const int kvh = head(n), kv = kvh >= g.H;
+      const T* src = (kv ? static_cast<const T*>(g.v) : static_cast<const T*>(g.k)) + (kvh - kv * g.H) * g.D;
+      const int64_t stride = kv ? g.v_stride : g.k_stride;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const int i = i0 + w * tpw + tok;
-        if (in && i < run.m) {
-          raw[w] = load_raw<T>(src + (run.row + i) * stride, task);
-          have |= 1u << w;
-        }
-      }
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const int i = i0 + w * tpw + tok;
-        if (!(have >> w & 1)) continue;
-        unpack(raw[w], x[w]);
-        if (!positions_ok(t, b, run.row + i, jseq + i)) {
-          bits |= KV_DEV_ERR_POSITION;
-          have &= ~(1u << w);
-        } else if (turned) {
-          float cs[8], sn[8];
-          load_cs(t, b, run.row + i, jseq + i, task, cs, sn);
-          turn16(t, x[w], cs, sn);
-        }
+        if (in && i < run.m && kvh < 2 * g.H) raw[n][w] = load_raw<T>(src + (run.row + i) * stride, task);
       }
     };
-    float amax = 0.0f;
-    for (int i0 = 0; i0 < run.m; i0 += W * tpw) {
-      load(i0);
+    // wave w of the tokens from i0 on: its 16 values, false where there is no such token
+    auto values = [&](int n, int i0, int w, float (&x)[16]) -> bool {
+      const int i = i0 + w * tpw + tok;
+      if (!in || i >= run.m) return false;
+      if (!positions_ok(t, b, run.row + i, run.j + i)) {
+        bits |= KV_DEV_ERR_POSITION;
+        return false;
+      }
+      unpack(raw[n][w], x);
+      if (head(n) < g.H && task.c8 >= 0) {
+        float c[8], s[8];
+        load_cs(t, b, run.row + i, run.j + i, task, c, s);
+        turn16(t, x, c, s);
+      }
+      return true;
+    };
+    // earlier tokens' codes, asked for before it is known whether the scale moves
+    uint2 old[HB][W][2];
 #pragma unroll
-      for (int w = 0; w < W; ++w)
-        if (have >> w & 1) {
+    for (int n = 0; n < HB; ++n) {
+      const int kvh = head(n), kv = kvh >= g.H;
+      load(n, 0);
+      if (one) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) amax = fmaxf(amax, finite_abs(x[w][e]));
-        }
-    }
-    float* at = g.scales + scale_at(p, g.H, run.page, g.layer, kv, h);
-    const bool held = run.off > 0 && jseq > 0;
-    float base;
-    const float S = new_scale(amax, at, held, &base);
-    if (held && base != S) {  // the earlier tokens' codes under the new scale
-      const float f = base / S;
-      for (int i = tok; in && i < j0; i += tpw) {
-        uint8_t* y = pool_row<uint8_t>(p, g.layer, kv, run.page, i) + h * g.D;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint2* at8 = reinterpret_cast<uint2*>(y + (half ? task.b : task.a));
-          uint2 v = *at8;
-          uint8_t* e = reinterpret_cast<uint8_t*>(&v);
-#pragma unroll
-          for (int n = 0; n < 8; ++n) e[n] = to_e4m3(from_e4m3(e[n]) * f);
-          *at8 = v;
+        for (int w = 0; w < W; ++w) {
+          const int i = w * tpw + tok;
+          if (in && i < run.off && kvh < 2 * g.H) {
+            const uint8_t* y = pool_row<uint8_t>(p, g.layer, kv, run.page, i) + (kvh - kv * g.H) * g.D;
+            old[n][w][0] = *reinterpret_cast<const uint2*>(y + task.a);
+            old[n][w][1] = *reinterpret_cast<const uint2*>(y + task.b);
+          }
         }
       }
     }
-    const float inv = 1.0f / S;
-    const bool again = run.m > W * tpw;
-    for (int i0 = 0; i0 < run.m; i0 += W * tpw) {
-      if (again) load(i0);
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        if (!(have >> w & 1)) continue;
-        uint8_t* y = pool_row<uint8_t>(p, g.layer, kv, run.page, run.off + i0 + w * tpw + tok) + h * g.D;
-        uint2 v[2];
-        uint8_t* e = reinterpret_cast<uint8_t*>(v);
+    for (int n = 0; n < HB; ++n) {
+      const int kvh = head(n), kv = kvh >= g.H, h = kvh - kv * g.H;
+      if (kvh >= 2 * g.H) break;  // (warp-uniform)
+      float* at = g.scales + scale_at(p, g.H, run.page, g.layer, kv, h);
+      const float before = held ? *at : 0.0f;
+      float amax = 0.0f;
+      for (int i0 = 0; i0 < run.m; i0 += W * tpw) {
+        if (i0 > 0) load(n, i0);
 #pragma unroll
-        for (int n = 0; n < 16; ++n) e[n] = to_e4m3(x[w][n] * inv);
-        *reinterpret_cast<uint2*>(y + task.a) = v[0];
-        *reinterpret_cast<uint2*>(y + task.b) = v[1];
+        for (int w = 0; w < W; ++w) {
+          float x[16];
+          if (values(n, i0, w, x)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) amax = fmaxf(amax, finite_abs(x[e]));
+          }
+        }
       }
+      float base;
+      const float S = new_scale(amax, before, &base);
+      uint8_t* page = pool_row<uint8_t>(p, g.layer, kv, run.page, 0) + h * g.D;
+      const int64_t row_bytes = p.vpr * 16;
+      if (held && base != S) {  // the earlier tokens' codes under the new scale
+        const float f = base / S;
+        auto put = [&](int i, uint2 v0, uint2 v1) {
+          uint8_t* y = page + i * row_bytes;
+          *reinterpret_cast<uint2*>(y + task.a) = make_uint2(rescale4(v0.x, f), rescale4(v0.y, f));
+          *reinterpret_cast<uint2*>(y + task.b) = make_uint2(rescale4(v1.x, f), rescale4(v1.y, f));
+        };
+        if (one) {
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            const int i = w * tpw + tok;
+            if (in && i < run.off) put(i, old[n][w][0], old[n][w][1]);
+          }
+        }
+        for (int i = (one ? W * tpw : 0) + tok; in && i < run.off; i += tpw) {
+          const uint8_t* y = page + i * row_bytes;
+          put(i, *reinterpret_cast<const uint2*>(y + task.a), *reinterpret_cast<const uint2*>(y + task.b));
+        }
+      }
+      const float inv = 1.0f / S;
+      for (int i0 = 0; i0 < run.m; i0 += W * tpw) {
+        if (!one) load(n, i0);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          float x[16];
+          if (!values(n, i0, w, x)) continue;
+          uint8_t* y = page + (run.off + i0 + w * tpw + tok) * row_bytes;
+          uint32_t v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = encode4(x[4 * e] * inv, x[4 * e + 1] * inv, x[4 * e + 2] * inv, x[4 * e + 3] * inv);
+          *reinterpret_cast<uint2*>(y + task.a) = make_uint2(v[0], v[1]);
+          *reinterpret_cast<uint2*>(y + task.b) = make_uint2(v[2], v[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) *at = S;
     }
-    __syncwarp();
-    if (lane == 0) *at = S;
   }
   store_bits(p, bits);
 }
@@ -417,8 +454,7 @@ __global__ void __launch_bounds__(kAppendBlock) k_append_any(DevPool p, Batch b,
     const bool is_q = head < g.Q;
     if (run.m == 0 || (run.page == 0 && !is_q)) continue;
     const int kv = head >= g.Q + g.H, h = is_q ? head : head - g.Q - kv * g.H;
-    const Seq q = seq_of(p, b, run.s, bits);
-    const int64_t jseq = q.a + (run.row - q.row0);
+    const int64_t jseq = run.j;
     const T* src = static_cast<const T*>(is_q ? g.q : kv ? g.v : g.k) + static_cast<int64_t>(h) * g.D;
     const int64_t stride = is_q ? g.q_stride : kv ? g.v_stride : g.k_stride;
     // element offsets and values of unit u of token i
@@ -456,9 +492,9 @@ __global__ void __launch_bounds__(kAppendBlock) k_append_any(DevPool p, Batch b,
         }
       }
       at = g.scales + scale_at(p, g.H, run.page, g.layer, kv, h);
-      const bool held = run.off > 0 && jseq > 0;
+      const bool held = run.off > 0;
       float base;
-      S = new_scale(amax, at, held, &base);
+      S = new_scale(amax, held ? *at : 0.0f, &base);
       if (held && base != S) {
         const float f = base / S;
         for (int i = 0; i < run.off; ++i) {
@@ -513,45 +549,88 @@ cudaError_t launch(const DevPool& p, const Batch& b, const AppendArgs& g, const 
       k_append_any<T, true><<<n, kAppendBlock, 0, s>>>(p, b, g, t, by_row, n_runs);
     else
       k_append_any<T, false><<<n, kAppendBlock, 0, s>>>(p, b, g, t, by_row, n_runs);
-  } else if (e4m3) {
-    const int per_run = (2 * g.H + kAppendBlock / 32 - 1) / (kAppendBlock / 32);
-    k_append_e4m3<T><<<grid(n_runs * per_run + (g.Q ? b.n_rows : 0)), kAppendBlock, 0, s>>>(p, b, g, t, by_row, n_runs,
-                                                                                          per_run);
   } else {
-    k_append<T><<<grid(b.n_rows), kAppendBlock, 0, s>>>(p, b, g, t);
+    const int tpr = threads_per_row(b.n_rows);
+    const int64_t row_blocks = (b.n_rows + kAppendBlock / tpr - 1) / (kAppendBlock / tpr);
+    if (row_blocks + n_runs > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    if (e4m3)
+      k_append_e4m3<T><<<grid(n_runs + (g.Q ? row_blocks : 0)), kAppendBlock, 0, s>>>(p, b, g, t, by_row, n_runs, tpr);
+    else
+      k_append<T><<<grid(row_blocks), kAppendBlock, 0, s>>>(p, b, g, t, tpr);
   }
   return cudaGetLastError();
 }
 
-// Scaled gather: a block per (page run, K or V), 16 codes a thread.
+// Scaled gather: a block per page run, K and then V, 16 codes a thread and
+// step. A run's rows are consecutive in the pool and in the output, so both sides are whole
+// streams; four loads are in flight before any store.
 template <class T>
 __global__ void __launch_bounds__(kAppendBlock) k_gather_scaled(DevPool p, Batch b, const float* __restrict__ scales,
                                                                 int32_t layer, int32_t H, int32_t D, T* out_k,
-                                                                T* out_v, bool by_row, int64_t n_runs) {
+                                                                T* out_v, bool by_row) {
   int bits = 0;
-  for (int64_t blk = blockIdx.x; blk < 2 * n_runs; blk += gridDim.x) {
-    const int kv = static_cast<int>(blk & 1);
-    const PageRun run = page_run(p, b, blk >> 1, by_row, bits);
-    if (run.m == 0) continue;
-    const int64_t n = run.m * p.vpr;  // rows of a run are consecutive in the pool and in the output
+  const PageRun run = page_run(p, b, blockIdx.x, by_row, bits);
+  store_bits(p, bits);
+  if (run.m == 0) return;
+  const int32_t vpr = static_cast<int32_t>(p.vpr);
+  const int64_t n = static_cast<int64_t>(run.m) * vpr;
+  const bool whole = D % 16 == 0;  // a piece of 16 codes lies in one head
+  constexpr int U = 4;
+  const int32_t step = kAppendBlock % vpr;
+  for (int kv = 0; kv < 2; ++kv) {
     const uint4* src = reinterpret_cast<const uint4*>(pool_row<uint8_t>(p, layer, kv, run.page, run.off));
     T* dst = (kv ? out_v : out_k) + run.row * H * D;
     const float* sc = scales + scale_at(p, H, run.page, layer, kv, 0);
-    for (int64_t i = threadIdx.x; i < n; i += kAppendBlock) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (run.page != 0) v = __ldg(src + i);
-      const uint8_t* e = reinterpret_cast<const uint8_t*>(&v);
-      const int e0 = static_cast<int>(i % p.vpr) * 16;
-      uint4 o[sizeof(T)];
-      T* y = reinterpret_cast<T*>(o);
+    int32_t col = threadIdx.x % vpr;  // piece of the row
+    for (int64_t i0 = threadIdx.x; i0 < n; i0 += kAppendBlock * U) {
+      uint4 v[U];
+      float f[U];
+      int32_t cols[U];
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        y[k] = Elem<T>::put(run.page != 0 ? from_e4m3(e[k]) * __ldg(sc + (e0 + k) / D) : 0.0f);
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = i0 + u * kAppendBlock;
+        cols[u] = col;
+        v[u] = make_uint4(0, 0, 0, 0);
+        f[u] = 0.0f;
+        if (i < n && run.page != 0) {
+          v[u] = __ldg(src + i);
+          if (whole) f[u] = __ldg(sc + col * 16 / D);
+        }
+        col += step;
+        if (col >= vpr) col -= vpr;
+      }
 #pragma unroll
-      for (int k = 0; k < static_cast<int>(sizeof(T)); ++k) reinterpret_cast<uint4*>(dst + i * 16)[k] = o[k];
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = i0 + u * kAppendBlock;
+        if (i >= n) break;
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        float x[16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 lo = halves(codes_lo(w[k])), hi = halves(codes_hi(w[k]));
+          x[4 * k] = lo.x, x[4 * k + 1] = lo.y, x[4 * k + 2] = hi.x, x[4 * k + 3] = hi.y;
+        }
+        if (whole) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) x[k] = run.page != 0 ? x[k] * f[u] : 0.0f;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) x[k] = run.page != 0 ? x[k] * __ldg(sc + (cols[u] * 16 + k) / D) : 0.0f;
+        }
+        uint4 o[sizeof(T)];
+        T* y = reinterpret_cast<T*>(o);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) y[k] = Elem<T>::put(x[k]);
+#pragma unroll
+        for (int k = 0; k < static_cast<int>(sizeof(T)); ++k) {
+          uint4* to = reinterpret_cast<uint4*>(dst + i * 16) + k;
+          asm volatile("st.global.cs.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(to), "r"(o[k].x), "r"(o[k].y), "r"(o[k].z),
+                       "r"(o[k].w)
+                       : "memory");
+        }
+      }
     }
   }
-  store_bits(p, bits);
 }
 
 }  // namespace
@@ -584,10 +663,9 @@ cudaError_t launch_gather_scaled(const DevPool& p, const Batch& b, int32_t layer
                                  const float* scales, int32_t type, void* out_k, void* out_v, cudaStream_t s) {
   const bool by_row = runs_by_row(b, p.ps);
   const int64_t n_runs = run_numbers(b, p.ps, by_row);
-  const int64_t n = 2 * n_runs;
-  const unsigned grid = static_cast<unsigned>(n < 1 ? 1 : n > 0x7fffffff ? 0x7fffffff : n);
+  if (n_runs > 0x7fffffff) return cudaErrorInvalidConfiguration;
   auto go = [&]<class T>(T* k, T* v) {
-    k_gather_scaled<T><<<grid, kAppendBlock, 0, s>>>(p, b, scales, layer, H, D, k, v, by_row, n_runs);
+    k_gather_scaled<T><<<static_cast<unsigned>(n_runs), kAppendBlock, 0, s>>>(p, b, scales, layer, H, D, k, v, by_row);
   };
   if (type == KV_TYPE_BF16)
     go(static_cast<__nv_bfloat16*>(out_k), static_cast<__nv_bfloat16*>(out_v));

@@ -125,19 +125,6 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Two e4m3 codes (bytes 0 and 1 of a half word) as two fp16.
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
-  uint32_t y;
-  asm("{.reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(y) : "r"(w));
-  return y;
-}
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
-  uint32_t y;
-  asm("{.reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(y) : "r"(w));
-  return y;
-}
-
-
 // All ones in the elements of a word of cached values that are not finite.
 template <class C>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {

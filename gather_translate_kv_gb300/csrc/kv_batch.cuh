@@ -89,6 +89,7 @@ __device__ __forceinline__ int32_t warp_search(int32_t n, int64_t x, F&& key) {
 // smaller range) a run's number is the row of its first token instead.
 struct PageRun {
   int64_t row;   // row of the first token
+  int64_t j;     // its index in the sequence
   int64_t page;  // physical page, 0: tombstone
   int32_t s;
   int32_t off;   // offset of the first token in the page
@@ -102,7 +103,7 @@ inline bool runs_by_row(const Batch& b, int64_t ps) { return run_numbers(b, ps, 
 
 // Called by whole warps.
 __device__ __forceinline__ PageRun page_run(const DevPool& p, const Batch& b, int64_t c, bool by_row, int& bits) {
-  PageRun r{0, 0, 0, 0, 0};
+  PageRun r{0, 0, 0, 0, 0, 0};
   const int64_t ps = p.ps;
   r.s = by_row ? warp_search(b.n_seqs, c, [&](int32_t s) { return __ldg(b.cu + s); })
                : warp_search(b.n_seqs, c, [&](int32_t s) { return div_ps(p, __ldg(b.cu + s)) + 2 * static_cast<int64_t>(s); });
@@ -125,6 +126,7 @@ __device__ __forceinline__ PageRun page_run(const DevPool& p, const Batch& b, in
   const int64_t left = static_cast<int64_t>(q.a) + q.n - j;
   r.m = static_cast<int32_t>(left < ps - r.off ? left : ps - r.off);
   r.row = q.row0 + (j - q.a);
+  r.j = j;
   r.page = page_of_entry(p, b, __ldg(b.table + static_cast<int64_t>(r.s) * b.max_pages + k), bits);
   return r;
 }
@@ -157,6 +159,35 @@ __device__ __forceinline__ float from_e4m3(uint8_t c) {
 }
 __device__ __forceinline__ uint8_t to_e4m3(float x) {
   return isfinite(x) ? __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3) : 0x7f;
+}
+
+// Two e4m3 codes (bytes 0 and 1 of a half word) as two fp16.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
+  uint32_t y;
+  asm("{.reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(y) : "r"(w));
+  return y;
+}
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
+  uint32_t y;
+  asm("{.reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(y) : "r"(w));
+  return y;
+}
+
+__device__ __forceinline__ float2 halves(uint32_t h2) { return __half22float2(*reinterpret_cast<const __half2*>(&h2)); }
+
+// Four floats as four codes; what is not finite becomes the NaN code.
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  auto fin = [](float x) { return fabsf(x) <= 3.402823466e38f ? x : NAN; };
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(fin(b)), "f"(fin(a)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(fin(d)), "f"(fin(c)));
+  return lo | static_cast<uint32_t>(hi) << 16;
+}
+
+// Four codes times f, as codes again.
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
+  const float2 a = halves(codes_lo(w)), b = halves(codes_hi(w));
+  return encode4(a.x * f, a.y * f, b.x * f, b.y * f);
 }
 
 __device__ __forceinline__ void store_bits(const DevPool& p, int bits) {
