@@ -523,42 +523,81 @@ def kv_rotary(cos_sin: torch.Tensor, positions: torch.Tensor | None = None, axis
     return KVRotary(st, ctypes.addressof(st), (cos_sin, positions))
 
 
-def _rows(t: torch.Tensor, name: str, n_rows: int, dtype=None) -> tuple[int, int]:
-    """Address and row stride of a [n_rows, heads, dim] tensor whose rows are contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    if t.dim() != 3 or t.shape[0] != n_rows:
-        raise ValueError(f"{name} must be [n_rows = {n_rows}, heads, dim], got {list(t.shape)}")
-    if t.stride(2) != 1 and t.shape[2] > 1 or t.stride(1) != t.shape[2] and t.shape[1] > 1:
+# The calls below run once per layer and step: they look at each tensor as few
+# times as their checks allow.
+
+def _here() -> int:
+    return torch.cuda.current_device()
+
+
+def _raw_stream(stream, device: int) -> int:
+    """The stream's handle; the current stream's when None."""
+    if stream is None:
+        return _current_raw_stream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        return stream.cuda_stream
+    return int(stream)
+
+
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _on(t: torch.Tensor, name: str, device: int) -> None:
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor" if not t.is_cuda else
+                         f"{name} is on {t.device}, the current device is cuda:{device}")
+
+
+def _rows(t: torch.Tensor, name: str, n_rows: int, heads: int | None, dim: int, device: int,
+          dtype=None) -> tuple[int, int, int]:
+    """Address, row stride and heads of a [n_rows, heads, dim] tensor whose rows are contiguous."""
+    _on(t, name, device)
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != n_rows or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [n_rows = {n_rows}, {'heads' if heads is None else heads}, {dim}], "
+                         f"got {list(shape)}")
+    st = t.stride()
+    if st[2] != 1 and dim > 1 or st[1] != dim and shape[1] > 1:
         raise ValueError(f"{name}'s rows must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    return t.data_ptr(), t.stride(0) if n_rows > 1 else t.shape[1] * t.shape[2]
+    return t.data_ptr(), st[0] if n_rows > 1 else shape[1] * dim, shape[1]
+
+
+def _whole(t: torch.Tensor, name: str, shape: tuple, dtype, device: int) -> int:
+    """Address of a contiguous tensor of the given shape and type."""
+    _on(t, name, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _type(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in KV_TYPE:
+    code = KV_TYPE.get(t.dtype)
+    if code is None:
         raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
-    return KV_TYPE[t.dtype]
+    return code
 
 
-def _heads(t: torch.Tensor, name: str, heads: int | None, pool: KVPool) -> None:
-    if t.shape[2] != pool.desc.head_dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must have rows of [{'heads' if heads is None else heads}, {pool.desc.head_dim}], "
-                         f"got {list(t.shape[1:])}")
-
-
-def _scales(pool: KVPool, scales: torch.Tensor | None):
-    if pool.desc.itemsize != 1:
+def _scales(pool: KVPool, scales: torch.Tensor | None, device: int) -> int | None:
+    d = pool.desc
+    if d.itemsize != 1:
         if scales is not None:
             raise ValueError("only pools of itemsize 1 have scales")
         return None
     if scales is None:
         raise ValueError("a pool of itemsize 1 needs its scales")
-    return _dev(scales, "scales", torch.float32,
-                4 * pool.desc.num_pages * pool.desc.layer_num * 2 * pool.desc.head_num)
+    _on(scales, "scales", device)
+    if scales.dtype != torch.float32 or not scales.is_contiguous():
+        raise ValueError("scales must be contiguous float32")
+    if scales.numel() != d.num_pages * d.layer_num * 2 * d.head_num:
+        raise ValueError(f"scales hold {scales.numel()} values, expected [num_pages, L, 2, H]")
+    return scales.data_ptr()
 
 
 def kv_scale_bytes(pool: KVPool) -> int:
@@ -573,24 +612,23 @@ def kv_append_layer(pool: KVPool, layer: int, batch: KVBatch, k: torch.Tensor, v
                     q_out: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None) -> None:
     """Append the batch's rows of k (rotated) and v to the cache and write the
     rotated q to q_out. k, v and q may be slices of a wider tensor's rows."""
-    n, H = batch.n_rows, pool.desc.head_num
-    kp, ks = _rows(k, "k", n)
-    vp, vs = _rows(v, "v", n, k.dtype)
-    _heads(k, "k", H, pool)
-    _heads(v, "v", H, pool)
+    d, n, dev = pool.desc, batch.n_rows, _here()
+    H, D, dtype = d.head_num, d.head_dim, k.dtype
+    kp, ks, _ = _rows(k, "k", n, H, D, dev)
+    vp, vs, _ = _rows(v, "v", n, H, D, dev, dtype)
     if rotary is not None and rotary.tensors[1] is not None and rotary.tensors[1].shape[-1] != n:
         raise ValueError(f"the rotation's positions are for {rotary.tensors[1].shape[-1]} rows, the batch has {n}")
     qp, qs, qh, op = None, 0, 0, None
     if q is not None:
-        qp, qs = _rows(q, "q", n, k.dtype)
-        _heads(q, "q", None, pool)
-        qh = q.shape[1]
-        if q_out is None or q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-        op = _dev(q_out, "q_out", k.dtype)
-    _check("kv_append_layer", lib().kv_append_layer(
+        qp, qs, qh = _rows(q, "q", n, None, D, dev, dtype)
+        if q_out is None:
+            raise ValueError("q_out must be given with q")
+        op = _whole(q_out, "q_out", q.shape, dtype, dev)
+    rc = (_lib or lib()).kv_append_layer(
         pool.handle, layer, batch.ptr, _type(k, "k"), kp, ks, vp, vs, None if rotary is None else rotary.ptr, qp, qs,
-        qh, op, _scales(pool, scales), _stream(stream)))
+        qh, op, _scales(pool, scales, dev), _raw_stream(stream, dev))
+    if rc:
+        raise KVError("kv_append_layer", rc)
 
 
 def kv_attend_workspace_bytes(pool: KVPool, q_heads: int, n_seqs: int, n_rows: int) -> int:
@@ -606,29 +644,32 @@ def kv_attend_layer(pool: KVPool, layer: int, batch: KVBatch, q: torch.Tensor, o
     """Attention of the batch's rows q [n_rows, q_heads, dim] over the layer's
     cache into out (and the log-sum-exp into lse [n_rows, q_heads]).
     workspace: uint8, kv_attend_workspace_bytes() long, one per call in flight."""
-    n = batch.n_rows
-    qp, qs = _rows(q, "q", n)
-    _heads(q, "q", None, pool)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if lse is not None and tuple(lse.shape) != (n, q.shape[1]):
-        raise ValueError("lse must be [n_rows, q_heads]")
-    _check("kv_attend_layer", lib().kv_attend_layer(
-        pool.handle, layer, batch.ptr, _type(q, "q"), qp, qs, q.shape[1], _dev(out, "out", q.dtype),
-        _dev(lse, "lse", torch.float32), scale, window, sinks, _scales(pool, scales),
-        _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream)))
+    n, dev = batch.n_rows, _here()
+    qp, qs, qh = _rows(q, "q", n, None, pool.desc.head_dim, dev)
+    op = _whole(out, "out", q.shape, q.dtype, dev)
+    lp = None if lse is None else _whole(lse, "lse", (n, qh), torch.float32, dev)
+    _on(workspace, "workspace", dev)
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous uint8")
+    rc = (_lib or lib()).kv_attend_layer(
+        pool.handle, layer, batch.ptr, _type(q, "q"), qp, qs, qh, op, lp, scale, window, sinks,
+        _scales(pool, scales, dev), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        raise KVError("kv_attend_layer", rc)
 
 
 def kv_gather_layer_scaled(pool: KVPool, layer: int, batch: KVBatch, scales: torch.Tensor, out_k: torch.Tensor,
                            out_v: torch.Tensor, stream=None) -> None:
     """The values (code times scale) of the batch's tokens, one layer's K and V
     as [n_rows, H, D] of out_k's type."""
-    shape = (batch.n_rows, pool.desc.head_num, pool.desc.head_dim)
-    if tuple(out_k.shape) != shape or tuple(out_v.shape) != shape:
-        raise ValueError(f"out_k and out_v must be {list(shape)}")
-    _check("kv_gather_layer_scaled", lib().kv_gather_layer_scaled(
-        pool.handle, layer, batch.ptr, _scales(pool, scales), _type(out_k, "out_k"), _dev(out_k, "out_k"),
-        _dev(out_v, "out_v", out_k.dtype), _stream(stream)))
+    shape, dev = (batch.n_rows, pool.desc.head_num, pool.desc.head_dim), _here()
+    if pool.desc.itemsize != 1:
+        raise ValueError("only pools of itemsize 1 have scales")
+    kp, vp = (_whole(t, name, shape, out_k.dtype, dev) for t, name in ((out_k, "out_k"), (out_v, "out_v")))
+    rc = (_lib or lib()).kv_gather_layer_scaled(pool.handle, layer, batch.ptr, _scales(pool, scales, dev),
+                                                _type(out_k, "out_k"), kp, vp, _raw_stream(stream, dev))
+    if rc:
+        raise KVError("kv_gather_layer_scaled", rc)
 
 
 def kv_pool_last_error(pool: KVPool, stream=None) -> int:
