@@ -83,6 +83,8 @@ cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a,
                            static_cast<uint8_t*>(workspace) + align256(attend_few_workspace(a.D, sm_count)), sm_count,
                            limit > 0, &tile, s);
   if (e != cudaSuccess) return e;
+  if (few.whole) few.n_workers = 0;
+  if (few.n_workers == 0 && tile.n_workers == 0) return e;
   if (e4m3) return launch_join<CodeE4M3>(p, b, a, few, tile, sm_count, s);
   return a.type == KV_TYPE_BF16 ? launch_join<__nv_bfloat16>(p, b, a, few, tile, sm_count, s)
                                 : launch_join<__half>(p, b, a, few, tile, sm_count, s);

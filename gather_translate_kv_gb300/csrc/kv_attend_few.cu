@@ -7,12 +7,12 @@
 // talks to another warp. Both products run as mma m16n8k16 with the CACHE as
 // the 16-row operand, S^T = K Q^T and O^T = V^T P^T, rows as the 8 (or 16)
 // columns, so 4 query heads fill half of an instruction instead of a quarter.
-// A lane's operand registers are filled from 16-byte pieces that it copied to
-// shared memory itself (cp.async, a ring of its own): the order of the summed
-// index is free, so lane (g, c) = (lane / 4, lane % 4) takes whole 16-byte
-// pieces of keys g and g + 8 for K, and its eighth of the elements of keys 2c,
-// 2c + 1, 2c + 8, 2c + 9 for V, where byte permutes pair up two keys. No
-// transpose, no bank conflict, no barrier. Codes become fp16 (exact) on the
+// The order of the summed index is free, so operand registers are filled from
+// whole 16-byte pieces of the rows as they lie in the cache: lane (g, c) =
+// (lane / 4, lane % 4) takes pieces of keys g and g + 8 for K, and its eighth
+// of the elements of keys 2c, 2c + 1, 2c + 8, 2c + 9 for V, where byte
+// permutes pair up two keys. Rows come by cp.async into a ring of the warp's
+// own, whole rows an instruction. No transpose, no bank conflict, no barrier. Codes become fp16 (exact) on the
 // way into the registers; P^T comes out of the score registers by movmatrix.
 //
 // Softmax: the running reference m moves only when a score exceeds it by
@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kFewWarps = 4;
 constexpr int kFewBlock = 32 * kFewWarps;
-constexpr int kFewBlocksPerSM = 3;
+constexpr int kFewBlocksPerSM = 4;  // at most
 constexpr int kUnitCost = 2;  // steps' worth of a unit's queries and output
 template <class C>
 struct FewType {
@@ -100,10 +100,18 @@ struct FewShape {
   static constexpr int kRow = D * kSize;      // bytes of a head's row
   static constexpr int kKC = kRow / 64;       // 16-byte pieces of a key that a lane holds
   static constexpr int kVB = kRow / 8;        // bytes of a value that a lane holds
+  static constexpr int kVC = kVB < 16 ? 1 : kVB / 16;  // pieces of it, 128 bytes apart
   static constexpr int kK = 16 * kRow;        // bytes of a step's K, and of its V
+  static constexpr int kLPR = kRow / 16;       // lanes that copy a row
+  static constexpr int kRPR = 32 / kLPR;       // rows a round
+  static constexpr int kRounds = 16 / kRPR;
+  // what round `it` adds to the swap of V's pieces, in bytes of the address
+  static __device__ __forceinline__ constexpr uint32_t flip_v(int it) {
+    return kRow >= 256 ? (it & 3) * 32 : kRow >= 128 ? (it & 1) * 64 : 0;
+  }
   static constexpr int kMeta = 144;           // 32 scales, the mask of live keys
   static constexpr int kStage = 2 * kK + kMeta;
-  static constexpr int kStages = kRow >= 256 ? 2 : kRow >= 128 ? 4 : 6;
+  static constexpr int kStages = kRow >= 256 ? 2 : kRow >= 128 ? 3 : 6;
   static constexpr int kSmem = kFewWarps * kStages * kStage;
   static constexpr int kKS = D / 16;          // k16 steps of the score product
   static constexpr int kMT = D / 16;          // 16-element tiles of the output
@@ -112,8 +120,11 @@ struct FewShape {
 // P16: the page size is a multiple of 16, so a step's keys share a page and a
 // lane looks up the pages of 32 steps ahead at once; otherwise every key's entry is
 // read on its own, one step ahead.
+// Resident blocks: shared memory for 256-byte rows, registers for 16 columns allow three.
+constexpr int few_blocks(int row, int nt) { return row >= 256 || nt > 1 ? 3 : kFewBlocksPerSM; }
+
 template <class C, int D, int NT, bool P16>
-__global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
+__global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT))
     k_attend_few(DevPool p, Batch b, AttendArgs a, Split w) {
   using Sh = FewShape<C, D>;
   constexpr bool kE4M3 = std::is_same_v<C, CodeE4M3>;
@@ -143,6 +154,7 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
         const Seq q = seq_of(p, b, s, err);
         if (blockIdx.x == 0) bits |= err;
         int64_t n = 0;
+        if (w.whole) return static_cast<int64_t>(tiles_of(q)) * n_groups;
         for (int32_t t = 0; t < tiles_of(q); ++t) n += span_of(q, t).steps() + kUnitCost;
         return n * n_groups;
       });
@@ -151,10 +163,18 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
   ShareStart at = loc[wk];
   if (worker >= w.n_workers) at.s = -1;
 
-  // the warp's ring
+  // The warp's ring. A row's 16-byte pieces are permuted within it so that the
+  // reads below meet no bank twice: K's piece p of row r sits at p ^ 4 (r % 2),
+  // V's at p ^ 2 (r / 2 % 4) (64-byte rows: p and p ^ (r / 2 % 4)).
+  const int cr = lane / Sh::kLPR, cp = lane % Sh::kLPR;  // row of a round and piece that the lane copies
+  const uint32_t put_k = cr * Sh::kRow + (Sh::kRow > 64 ? cp ^ (cr & 1) * 4 : cp) * 16;
+  const uint32_t put_v = cr * Sh::kRow + (Sh::kRow >= 256 ? cp : Sh::kRow > 64 ? cp ^ (cr >> 1) * 2 : cp ^ (cr >> 1 & 3)) * 16;
+  const uint32_t get_k = g * Sh::kRow + (Sh::kRow > 64 ? c ^ (g & 1) * 4 : c) * 16;  // ^ 64 ch, + 8 rows
+  const uint32_t get_v = 2 * c * Sh::kRow + (Sh::kRow > 64 ? (g ^ 2 * c) * 16 : ((g >> 1) ^ c) * 16 + (g & 1) * 8);
+  auto key_at = [](int kk) { return ((kk & 1) + 8 * (kk >> 1)) * Sh::kRow; };  // of keys 2c, 2c + 1, 2c + 8, 2c + 9
   const uint32_t ring0 = shared_u32(ring) + warp * Sh::kStages * Sh::kStage;
   const uint8_t* pool = reinterpret_cast<const uint8_t*>(p.base);
-  const int64_t row_bytes = p.vpr * 16;
+  const int32_t row_bytes = static_cast<int32_t>(p.vpr * 16);
 
   int64_t left = at.s < 0 ? 0 : share;
   int32_t s = at.s, tile = 0, group = 0;
@@ -167,27 +187,34 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
     int64_t off = at.off;
     for (;;) {
       span = span_of(q, tile);
-      const int64_t n = static_cast<int64_t>(span.steps() + kUnitCost) * n_groups;
+      const int64_t n = static_cast<int64_t>(w.whole ? 1 : span.steps() + kUnitCost) * n_groups;
       if (off < n) break;
       off -= n;
       ++tile;
     }
-    const int32_t unit = span.steps() + kUnitCost;
-    group = static_cast<int32_t>(off / unit);
-    const int32_t in = static_cast<int32_t>(off - static_cast<int64_t>(group) * unit);
-    step0 = in < kUnitCost ? 0 : in - kUnitCost;
-    left -= in < kUnitCost ? kUnitCost - in : 0;
+    if (w.whole) {
+      group = static_cast<int32_t>(off);
+    } else {
+      const int32_t unit = span.steps() + kUnitCost;
+      group = static_cast<int32_t>(off / unit);
+      const int32_t in = static_cast<int32_t>(off - static_cast<int64_t>(group) * unit);
+      step0 = in < kUnitCost ? 0 : in - kUnitCost;
+      left -= in < kUnitCost ? kUnitCost - in : 0;
+    }
   }
 
   while (left > 0) {
     const int32_t n_steps = span.steps();
-    const int32_t end = left < n_steps - step0 ? step0 + static_cast<int32_t>(left) : n_steps;
+    const int32_t end = !w.whole && left < n_steps - step0 ? step0 + static_cast<int32_t>(left) : n_steps;
     const int32_t h = group * w.hw + hw;
     const int32_t f0 = tile * NQ;
     const int32_t nf = min(NQ, q.n * a.G - f0);  // rows of the tile
     const int32_t i0 = q.a + f0 / a.G, i1 = q.a + (f0 + nf - 1) / a.G;
 
     // ---- issue of a step's loads
+    const int64_t off = static_cast<int64_t>(cr) * row_bytes + h * Sh::kRow + cp * 16;
+    const int64_t round_bytes = Sh::kRPR * static_cast<int64_t>(row_bytes), v_bytes = p.ps * row_bytes;
+    uint32_t whole_stages = 0;  // bit s: all 16 keys of stage s are tokens
     int32_t ent = 0;  // P16: page of step seg_base + lane (0: tombstone); else: raw entry of key lane % 16 of the next step
     auto page_of_step = [&](int32_t i) -> int32_t {
       if (i >= end) return 0;
@@ -233,43 +260,39 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
           rk = static_cast<int32_t>(page * p.stride + 2 * static_cast<int64_t>(a.layer) * p.ps + (j - div_ps(p, j) * p.ps));
           live = __ballot_sync(kFull, page != 0) & 0xffffu;
         }
-        auto row = [&](int key) -> int64_t {
-          if constexpr (P16)
-            return static_cast<int64_t>(rk) + key;
-          else
-            return __shfl_sync(kFull, rk, key);
-        };
+        const bool all = P16 && live == 0xffffu;
+        whole_stages = (whole_stages & ~(1u << stage)) | static_cast<uint32_t>(all) << stage;
+        const uint8_t* base = pool + off;
+        if (all) {  // every key is a token: one base address and constant offsets
+          base += static_cast<int64_t>(rk) * row_bytes;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int key = g + 8 * half;
-          const int64_t r = row(key);
-          const bool ok = live >> key & 1;
-          const uint8_t* src = pool + (ok ? r * row_bytes + h * Sh::kRow + c * 16 : 0);
+          for (int it = 0; it < Sh::kRounds; ++it) copy_async<16>(st + put_k + it * 512, base + it * round_bytes);
+          base += v_bytes;
 #pragma unroll
-          for (int ch = 0; ch < Sh::kKC; ++ch)
-            copy_async<16>(st + (half * Sh::kKC + ch) * 512 + lane * 16, src + (ok ? ch * 64 : 0), ok);
-        }
+          for (int it = 0; it < Sh::kRounds; ++it)
+            copy_async<16>(st + Sh::kK + (put_v ^ Sh::flip_v(it)) + it * 512, base + it * round_bytes);
+        } else {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const int key = 2 * c + (kk & 1) + 8 * (kk >> 1);
-          const int64_t r = row(key) + p.ps;
-          const bool ok = live >> key & 1;
-          const uint8_t* src = pool + (ok ? r * row_bytes + h * Sh::kRow + g * Sh::kVB : 0);
-          if constexpr (Sh::kVB == 8) {
-            copy_async<8>(st + Sh::kK + kk * 256 + lane * 8, src, ok);
-          } else {
-#pragma unroll
-            for (int ch = 0; ch < Sh::kVB / 16; ++ch)
-              copy_async<16>(st + Sh::kK + (kk * (Sh::kVB / 16) + ch) * 512 + lane * 16, src + (ok ? ch * 16 : 0), ok);
+          for (int it = 0; it < Sh::kRounds; ++it) {
+            const int key = it * Sh::kRPR + cr;
+            const int32_t r = P16 ? rk + it * Sh::kRPR : __shfl_sync(kFull, rk, key) - cr;
+            const bool ok = live >> key & 1;
+            const uint8_t* src = ok ? base + static_cast<int64_t>(r) * row_bytes : pool;
+            copy_async<16>(st + put_k + it * 512, src, ok);
+            copy_async<16>(st + Sh::kK + (put_v ^ Sh::flip_v(it)) + it * 512, src + (ok ? v_bytes : 0), ok);
           }
+          if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + 2 * Sh::kK + 128), "r"(live) : "memory");
         }
-        if constexpr (kE4M3) {  // lanes 0-15: scales of K, 16-31: of V
+        if constexpr (kE4M3 && P16) {  // one scale of K (lane 0) and one of V (lane 1)
+          if (lane < 2)
+            copy_async<4>(st + 2 * Sh::kK + lane * 4,
+                          a.scales + (static_cast<int64_t>(page) * p.blocks + 2 * a.layer + lane) * a.H + h);
+        } else if constexpr (kE4M3) {  // lanes 0-15: scales of K, 16-31: of V
           const bool ok = live >> (lane & 15) & 1;
           const float* sc =
               a.scales + (ok ? (static_cast<int64_t>(page) * p.blocks + 2 * a.layer + (lane >> 4)) * a.H + h : 0);
           copy_async<4>(st + 2 * Sh::kK + lane * 4, sc, ok);
         }
-        if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + 2 * Sh::kK + 128), "r"(live) : "memory");
       }
       copy_commit();
     };
@@ -358,41 +381,52 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
       copy_wait<Sh::kStages - 1>();
       __syncwarp();
       const uint32_t st = ring0 + stage * Sh::kStage;
-      const uint32_t live = lds32(st + 2 * Sh::kK + 128);
+      const uint32_t live = whole_stages >> stage & 1 ? 0xffffu : lds32(st + 2 * Sh::kK + 128);
       const int32_t j0 = span.block(i) * 16;
 
       // ---- scores
-      float x[NT][4];
+      float x[NT][4], x2[NT][4];  // two sums, so that products wait half as long for one another
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[nt][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) x[nt][e] = x2[nt][e] = 0.0f;
 #pragma unroll
       for (int ch = 0; ch < Sh::kKC; ++ch) {
-        const uint4 u = lds128(st + ch * 512 + lane * 16), v = lds128(st + (Sh::kKC + ch) * 512 + lane * 16);
+        const uint4 u = lds128(st + (get_k ^ ch * 64)), v = lds128(st + (get_k ^ ch * 64) + 8 * Sh::kRow);
         const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
         if constexpr (kE4M3) {
 #pragma unroll
           for (int wd = 0; wd < 4; ++wd) {
             const uint32_t a0 = codes_lo(uu[wd]), a1 = codes_lo(vv[wd]), a2 = codes_hi(uu[wd]), a3 = codes_hi(vv[wd]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma<C>(x[nt], a0, a1, a2, a3, qf[nt][ch * 4 + wd][0], qf[nt][ch * 4 + wd][1]);
+            for (int nt = 0; nt < NT; ++nt)
+              mma<C>(wd & 1 ? x2[nt] : x[nt], a0, a1, a2, a3, qf[nt][ch * 4 + wd][0], qf[nt][ch * 4 + wd][1]);
           }
         } else {
 #pragma unroll
           for (int wd = 0; wd < 2; ++wd)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma<C>(x[nt], uu[2 * wd], vv[2 * wd], uu[2 * wd + 1], vv[2 * wd + 1], qf[nt][ch * 2 + wd][0],
-                     qf[nt][ch * 2 + wd][1]);
+              mma<C>(wd & 1 ? x2[nt] : x[nt], uu[2 * wd], vv[2 * wd], uu[2 * wd + 1], vv[2 * wd + 1],
+                     qf[nt][ch * 2 + wd][0], qf[nt][ch * 2 + wd][1]);
         }
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[nt][e] += x2[nt][e];
 
       // ---- weights; x[.][0], [1]: key g, columns 2c, 2c + 1; [2], [3]: key g + 8
       float lv[2] = {0.0f, 0.0f}, iv[2] = {1.0f, 1.0f}, sk[2] = {1.0f, 1.0f};
       if constexpr (kE4M3) {
+        if constexpr (P16) {
+          const uint2 kv = lds64(st + 2 * Sh::kK);
+          sk[0] = sk[1] = __uint_as_float(kv.x);
+          lv[0] = lv[1] = lg2(__uint_as_float(kv.y));
+          iv[0] = iv[1] = __fdividef(1.0f, __uint_as_float(kv.y));
+        }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < (P16 ? 0 : 2); ++e) {
           sk[e] = __uint_as_float(lds32(st + 2 * Sh::kK + (g + 8 * e) * 4));
           const float sv = __uint_as_float(lds32(st + 2 * Sh::kK + 64 + (g + 8 * e) * 4));
           lv[e] = lg2(sv);
@@ -443,8 +477,7 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
           for (int wd = 0; wd < Sh::kVB / 4; ++wd) {
-            const uint32_t at = st + Sh::kK + (Sh::kVB == 8 ? kk * 256 + lane * 8 + wd * 4
-                                                            : (kk * (Sh::kVB / 16) + wd / 4) * 512 + lane * 16 + wd % 4 * 4);
+            const uint32_t at = st + Sh::kK + get_v + key_at(kk) + wd / 4 * 128 + wd % 4 * 4;
             const uint32_t v = lds32(at), bad = not_finite<C>(v);
             if (bad) {
               asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v & ~bad) : "memory");
@@ -469,7 +502,7 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
           y[e] = ex2(x[nt][e] - ref[nt][e & 1] + kLift);
           // a dead key adds nothing, whatever its zero-filled scale's inverse is
           if constexpr (kE4M3)
-            sum[nt][e & 1] += live >> (g + 8 * (e >> 1)) & 1 ? y[e] * iv[e >> 1] : 0.0f;
+            sum[nt][e & 1] += live == 0xffffu || live >> (g + 8 * (e >> 1)) & 1 ? y[e] * iv[e >> 1] : 0.0f;
           else
             sum[nt][e & 1] += y[e];
         }
@@ -494,7 +527,7 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
           if constexpr (FewType<C>::kSplitP) mma<C>(o[mt][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
         }
       };
-      constexpr int VC = Sh::kVB >= 16 ? Sh::kVB / 16 : 1;  // pieces of a value
+      constexpr int VC = Sh::kVC;
       constexpr int VW = Sh::kVB >= 16 ? 4 : 2;             // words of a piece
 #pragma unroll
       for (int ch = 0; ch < VC; ++ch) {
@@ -502,10 +535,10 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           if constexpr (VW == 4) {
-            const uint4 u = lds128(st + Sh::kK + (kk * VC + ch) * 512 + lane * 16);
+            const uint4 u = lds128(st + Sh::kK + get_v + key_at(kk) + ch * 128);
             v[kk][0] = u.x, v[kk][1] = u.y, v[kk][2] = u.z, v[kk][3] = u.w;
           } else {
-            const uint2 u = lds64(st + Sh::kK + kk * 256 + lane * 8);
+            const uint2 u = lds64(st + Sh::kK + get_v + key_at(kk));
             v[kk][0] = u.x, v[kk][1] = u.y;
           }
         }
@@ -527,7 +560,8 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
     }
     copy_wait<0>();
 
-    // ---- the segment's end. o[mt][nt]: elements g D/8 + 2 mt (+ 1: [2], [3]) of columns 2c, 2c + 1
+    // ---- the segment's end. o[mt][nt]: elements element(mt) (+ 1: [2], [3]) of columns 2c, 2c + 1
+    auto element = [&](int mt) { return Sh::kVC == 1 ? g * (D / 8) + 2 * mt : mt / 4 * 64 + g * 8 + mt % 4 * 2; };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -554,7 +588,7 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
             bad = bad || !(fabsf(y0) <= 3.402823466e38f) || !(fabsf(y1) <= 3.402823466e38f);
             if (col < nf) {
               const uint32_t y = a.type == KV_TYPE_BF16 ? pack_b(y0, y1) : pack_h(y0, y1);
-              uint16_t* out = static_cast<uint16_t*>(a.out) + (r * a.Q + qh) * D + g * (D / 8) + 2 * mt;
+              uint16_t* out = static_cast<uint16_t*>(a.out) + (r * a.Q + qh) * D + element(mt);
               if (w.out_wide) {
                 *reinterpret_cast<uint32_t*>(out) = y;
               } else {
@@ -586,7 +620,7 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
           const int col = nt * 8 + 2 * c + e;
 #pragma unroll
           for (int mt = 0; mt < Sh::kMT; mt += 2)
-            *reinterpret_cast<float4*>(part + col * D + g * (D / 8) + 2 * mt) =
+            *reinterpret_cast<float4*>(part + col * D + element(mt)) =
                 make_float4(o[mt][nt][e], o[mt][nt][e + 2], o[mt + 1][nt][e], o[mt + 1][nt][e + 2]);
           if (g == 0) {
             part[NQ * D + col] = ref[nt][e];
@@ -596,7 +630,7 @@ __global__ void __launch_bounds__(kFewBlock, kFewBlocksPerSM)
       if (slot == 1)
         rec = SplitRecord{s, tile, group, worker + static_cast<int32_t>((n_steps - end + share - 1) / share)};
     }
-    left -= end - step0 + kUnitCost;  // and the head of the next unit
+    left -= w.whole ? 1 : end - step0 + kUnitCost;  // and the head of the next unit
 
     // ---- the next unit
     step0 = 0;
@@ -650,6 +684,7 @@ cudaError_t prepare_c() {
   return e;
 }
 
+constexpr int kWhole = 24;    // steps up to which units are not cut
 constexpr int kMinShare = 8;  // steps of 16 keys below which a worker's share is not cut
 
 int heads_of_worker(int32_t H) { return H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1; }
@@ -683,10 +718,12 @@ cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs
     most = seen < most ? seen : most;
   }
   const int64_t tiles = (b.n_rows * a.G) / (8 * nt) + b.n_seqs;  // row tiles of all sequences
-  const int64_t all = (most + kUnitCost) * tiles * (a.H / w.hw);
-  int64_t cap = static_cast<int64_t>(sm_count) * kFewBlocksPerSM * kw;
+  // units that are short anyway are never cut, and then there is nothing to join
+  w.whole = most <= kWhole;
+  const int64_t all = (w.whole ? 1 : most + kUnitCost) * tiles * (a.H / w.hw);
+  int64_t cap = static_cast<int64_t>(sm_count) * few_blocks(a.D * (e4m3 ? 1 : 2), nt) * kw;
   cap = cap < kMaxWorkers ? cap : kMaxWorkers;
-  w.min_share = kMinShare;
+  w.min_share = w.whole ? 1 : kMinShare;
   int64_t workers = (all + w.min_share - 1) / w.min_share;
   workers = workers > cap ? cap : workers;
   w.blocks = static_cast<int>((workers + kw - 1) / kw);

@@ -28,6 +28,7 @@ struct Split {
   int32_t blocks;
   int32_t q_wide;     // query rows start on 16 bytes
   int32_t out_wide;   // out is aligned for the kernel's widest stores
+  int32_t whole;      // units are not cut: nothing to join
   float lift;         // log2 of the weights' lift
 };
 
