@@ -111,8 +111,10 @@ struct FewShape {
   }
   static constexpr int kMeta = 144;           // 32 scales, the mask of live keys
   static constexpr int kStage = 2 * kK + kMeta;
+  // Stages of a warp's ring: as many as shared memory holds with all the
+  // blocks that fit an SM, or, for calls of one block an SM, whose time is latency, six.
   static constexpr int kStages = kRow >= 256 ? 2 : kRow >= 128 ? 3 : 6;
-  static constexpr int kSmem = kFewWarps * kStages * kStage;
+  static constexpr int kDeep = 6;
   static constexpr int kKS = D / 16;          // k16 steps of the score product
   static constexpr int kMT = D / 16;          // 16-element tiles of the output
 };
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
         return n * n_groups;
       });
   const int32_t worker = worker0 + wk;
-  SplitRecord rec{-1, 0, 0, 0};
+  SplitRecord rec{-1, 0, 0, 0, 0, 0, 0};
   ShareStart at = loc[wk];
   if (worker >= w.n_workers) at.s = -1;
 
@@ -172,7 +174,8 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
   const uint32_t get_k = g * Sh::kRow + (Sh::kRow > 64 ? c ^ (g & 1) * 4 : c) * 16;  // ^ 64 ch, + 8 rows
   const uint32_t get_v = 2 * c * Sh::kRow + (Sh::kRow > 64 ? (g ^ 2 * c) * 16 : ((g >> 1) ^ c) * 16 + (g & 1) * 8);
   auto key_at = [](int kk) { return ((kk & 1) + 8 * (kk >> 1)) * Sh::kRow; };  // of keys 2c, 2c + 1, 2c + 8, 2c + 9
-  const uint32_t ring0 = shared_u32(ring) + warp * Sh::kStages * Sh::kStage;
+  const int stages = w.deep ? Sh::kDeep : Sh::kStages;
+  const uint32_t ring0 = shared_u32(ring) + warp * stages * Sh::kStage;
   const uint8_t* pool = reinterpret_cast<const uint8_t*>(p.base);
   const int32_t row_bytes = static_cast<int32_t>(p.vpr * 16);
 
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
       }
       copy_commit();
     };
-    for (int i = 0; i < Sh::kStages - 1; ++i) issue(step0 + i, i);
+    for (int i = 0; i < stages - 1; ++i) issue(step0 + i, i);
 
     // ---- the queries, while the first loads are in flight
     uint32_t qf[NT][Sh::kKS][2];
@@ -374,11 +377,14 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
     int stage = 0;
     for (int32_t i = step0; i < end; ++i) {
       {
-        int ahead = stage + Sh::kStages - 1;
-        if (ahead >= Sh::kStages) ahead -= Sh::kStages;
-        issue(i + Sh::kStages - 1, ahead);
+        int ahead = stage + stages - 1;
+        if (ahead >= stages) ahead -= stages;
+        issue(i + stages - 1, ahead);
       }
-      copy_wait<Sh::kStages - 1>();
+      if (w.deep)
+        copy_wait<Sh::kDeep - 1>();
+      else
+        copy_wait<Sh::kStages - 1>();
       __syncwarp();
       const uint32_t st = ring0 + stage * Sh::kStage;
       const uint32_t live = whole_stages >> stage & 1 ? 0xffffu : lds32(st + 2 * Sh::kK + 128);
@@ -555,7 +561,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
           }
         }
       }
-      if (++stage == Sh::kStages) stage = 0;
+      if (++stage == stages) stage = 0;
       __syncwarp();  // the stage's scales and mask are free for the next issue
     }
     copy_wait<0>();
@@ -628,7 +634,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
           }
         }
       if (slot == 1)
-        rec = SplitRecord{s, tile, group, worker + static_cast<int32_t>((n_steps - end + share - 1) / share)};
+        rec = SplitRecord{s, q.a, f0, nf, group, worker + static_cast<int32_t>((n_steps - end + share - 1) / share), q.row0};
     }
     left -= w.whole ? 1 : end - step0 + kUnitCost;  // and the head of the next unit
 
@@ -655,7 +661,7 @@ template <class C, int D, int NT>
 cudaError_t launch(const DevPool& p, const Batch& b, const AttendArgs& a, Split w, cudaStream_t s) {
   using Sh = FewShape<C, D>;
   auto kernel = p.ps % 16 == 0 ? k_attend_few<C, D, NT, true> : k_attend_few<C, D, NT, false>;
-  kernel<<<w.blocks, kFewBlock, Sh::kSmem, s>>>(p, b, a, w);
+  kernel<<<w.blocks, kFewBlock, kFewWarps * (w.deep ? Sh::kDeep : Sh::kStages) * Sh::kStage, s>>>(p, b, a, w);
   return cudaGetLastError();
 }
 
@@ -668,10 +674,10 @@ cudaError_t launch_c(const DevPool& p, const Batch& b, const AttendArgs& a, cons
 template <class C, int D, int NT>
 cudaError_t prepare_one() {
   cudaError_t e = cudaFuncSetAttribute(k_attend_few<C, D, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       FewShape<C, D>::kSmem);
+                                       kFewWarps * FewShape<C, D>::kDeep * FewShape<C, D>::kStage);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(k_attend_few<C, D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             FewShape<C, D>::kSmem);
+                             kFewWarps * FewShape<C, D>::kDeep * FewShape<C, D>::kStage);
   return e;
 }
 
@@ -684,8 +690,8 @@ cudaError_t prepare_c() {
   return e;
 }
 
-constexpr int kWhole = 24;    // steps up to which units are not cut
-constexpr int kMinShare = 8;  // steps of 16 keys below which a worker's share is not cut
+constexpr int kWhole = 24;    // steps up to which units are not cut where they fill the GPU; a third of it where they do not
+constexpr int kMinShare = 4;  // steps of 16 keys below which a worker's share is not cut
 
 int heads_of_worker(int32_t H) { return H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1; }
 
@@ -718,10 +724,10 @@ cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs
     most = seen < most ? seen : most;
   }
   const int64_t tiles = (b.n_rows * a.G) / (8 * nt) + b.n_seqs;  // row tiles of all sequences
-  // units that are short anyway are never cut, and then there is nothing to join
-  w.whole = most <= kWhole;
-  const int64_t all = (w.whole ? 1 : most + kUnitCost) * tiles * (a.H / w.hw);
   int64_t cap = static_cast<int64_t>(sm_count) * few_blocks(a.D * (e4m3 ? 1 : 2), nt) * kw;
+  // units that are short anyway are never cut, and then there is nothing to join
+  w.whole = most <= (tiles * (a.H / w.hw) >= cap ? kWhole : kWhole / 3);
+  const int64_t all = (w.whole ? 1 : most + kUnitCost) * tiles * (a.H / w.hw);
   cap = cap < kMaxWorkers ? cap : kMaxWorkers;
   w.min_share = w.whole ? 1 : kMinShare;
   int64_t workers = (all + w.min_share - 1) / w.min_share;
@@ -729,6 +735,7 @@ cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs
   w.blocks = static_cast<int>((workers + kw - 1) / kw);
   if (w.blocks * kw > kMaxWorkers) w.blocks = kMaxWorkers / kw;
   w.n_workers = w.blocks * kw;
+  w.deep = w.blocks <= sm_count;
   w.rec = static_cast<SplitRecord*>(workspace);
   const int64_t warps = static_cast<int64_t>(sm_count) * kFewBlocksPerSM * kFewWarps;
   w.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + split_record_bytes(warps));

@@ -12,8 +12,12 @@ constexpr int kMaxWorkers = 2048;
 // What a worker leaves behind for the join: the unit that its last segment
 // left unfinished, s < 0 for none, and the last worker that continues it.
 struct SplitRecord {
-  int32_t s, tile, head;
-  int32_t last;
+  int32_t s;       // sequence
+  int32_t a;       // position of its first new token
+  int32_t f0, nf;  // rows [f0, f0 + nf) of the sequence
+  int32_t head;    // KV head, or group of heads
+  int32_t last;    // worker
+  int64_t row0;    // row of the tensors that f = 0 belongs to
 };
 
 // Where a call's partial results are, and how its units are shaped.
@@ -28,6 +32,7 @@ struct Split {
   int32_t blocks;
   int32_t q_wide;     // query rows start on 16 bytes
   int32_t out_wide;   // out is aligned for the kernel's widest stores
+  int32_t deep;       // the longer ring
   int32_t whole;      // units are not cut: nothing to join
   float lift;         // log2 of the weights' lift
 };

@@ -164,20 +164,21 @@ __device__ __forceinline__ uint32_t pack_b(float lo, float hi) {
 }
 
 // Joins the partial sums of units that were cut, adding a unit's segments in
-// the workers' order. An item is a row of a cut unit; a warp takes one, or, when there are few items
-// (a long context of few rows, cut many times), the eight warps of a block
-// share its segments.
+// the workers' order under a running reference. An item is a row of a cut unit; a warp takes one, or,
+// when there are few items (a long context of few rows, cut many times), the
+// eight warps of a block share its segments.
 template <class C, int D>
 __device__ __forceinline__ void join_split(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w,
                                            int32_t* owners, float* tmp, int& bits) {
-  constexpr int E = D / 32, NW = kJoinBlock / 32;
+  constexpr int E = D / 32, NW = kJoinBlock / 32, U = 4;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // the workers that left a unit unfinished
+  // the workers that left a unit unfinished, and their rows (at most 256)
   int32_t count = 0;
   int32_t* warp_count = reinterpret_cast<int32_t*>(tmp);
   for (int32_t w0 = 0; w0 < w.n_workers; w0 += kJoinBlock) {
-    const bool own = w0 + tid < w.n_workers && w.rec[w0 + tid].s >= 0;
-    const uint32_t vote = __ballot_sync(kFull, own);
+    int32_t nf = 0;
+    if (w0 + tid < w.n_workers && w.rec[w0 + tid].s >= 0) nf = w.rec[w0 + tid].nf;
+    const uint32_t vote = __ballot_sync(kFull, nf > 0);
     if (lane == 0) warp_count[warp] = __popc(vote);
     __syncthreads();
     int32_t at = count;
@@ -185,7 +186,7 @@ __device__ __forceinline__ void join_split(const DevPool& p, const Batch& b, con
       if (k < warp) at += warp_count[k];
       count += warp_count[k];
     }
-    if (own) owners[at + __popc(vote & ((1u << lane) - 1))] = w0 + tid;
+    if (nf > 0) owners[at + __popc(vote & ((1u << lane) - 1))] = (w0 + tid) << 9 | nf;
     __syncthreads();
   }
   const int32_t rows = w.hw * w.nq;
@@ -193,31 +194,42 @@ __device__ __forceinline__ void join_split(const DevPool& p, const Batch& b, con
   const bool shared = items <= 2 * static_cast<int32_t>(gridDim.x);  // a block an item
   const int32_t stride = shared ? gridDim.x : gridDim.x * NW;
   const int64_t part_floats = static_cast<int64_t>(w.nq) * (D + 2);
-  for (int32_t i = shared ? blockIdx.x : blockIdx.x * NW + warp; i < items; i += stride) {
-    const int32_t worker = owners[i / rows];
-    const int32_t hw = i % rows / w.nq, col = i % w.nq;
-    const SplitRecord rec = w.rec[worker];
-    const Seq q = seq_of(p, b, rec.s, bits);
-    const int32_t f = rec.tile * w.nq + col;
-    if (f >= q.n * a.G) continue;
-    auto part = [&](int32_t k) {
-      return w.part + ((static_cast<int64_t>(k) * w.hw + hw) * 2 + (k == worker ? 1 : 0)) * part_floats;
-    };
-    const int32_t k0 = worker + (shared ? warp : 0), kd = shared ? NW : 1;
-    float m = kNoRef;
-    for (int32_t k = k0 + lane * kd; k <= rec.last; k += 32 * kd) m = fmaxf(m, part(k)[w.nq * D + col]);
+  auto add = [&](float& m, float& sum, float (&acc)[E], float m2, float s2, const float (&x)[E]) {
+    const float top = fmaxf(m, m2);
+    const float k1 = ex2(m - top), k2 = ex2(m2 - top);
+    m = top;
+    sum = sum * k1 + s2 * k2;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    float acc[E], sum = 0.0f;
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * k1 + x[e] * k2;
+  };
+  for (int32_t i = shared ? blockIdx.x : blockIdx.x * NW + warp; i < items; i += stride) {
+    const int32_t owner = owners[i / rows], worker = owner >> 9;
+    const int32_t hw = i % rows / w.nq, col = i % w.nq;
+    if (col >= (owner & 511)) continue;
+    const SplitRecord rec = w.rec[worker];
+    float m = kNoRef, sum = 0.0f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-#pragma unroll 8
-    for (int32_t k = k0; k <= rec.last; k += kd) {
-      const float* x = part(k);
-      const float scale = ex2(x[w.nq * D + col] - m);
-      sum += x[w.nq * (D + 1) + col] * scale;
+    const int32_t kd = shared ? NW : 1;
+    for (int32_t k0 = worker + (shared ? warp : 0); k0 <= rec.last; k0 += U * kd) {
+      float mk[U], sk[U], x[U][E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += x[col * D + lane * E + e] * scale;
+      for (int u = 0; u < U; ++u) {
+        const int32_t k = k0 + u * kd;
+        mk[u] = kNoRef;
+        sk[u] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[u][e] = 0.0f;
+        if (k <= rec.last) {
+          const float* at = w.part + ((static_cast<int64_t>(k) * w.hw + hw) * 2 + (k == worker ? 1 : 0)) * part_floats;
+          mk[u] = at[w.nq * D + col];
+          sk[u] = at[w.nq * (D + 1) + col];
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[u][e] = at[col * D + lane * E + e];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) add(m, sum, acc, mk[u], sk[u], x[u]);
     }
     if (shared) {
       float* at = tmp + warp * (D + 2);
@@ -226,24 +238,19 @@ __device__ __forceinline__ void join_split(const DevPool& p, const Batch& b, con
       if (lane == 0) at[D] = m, at[D + 1] = sum;
       __syncthreads();
       if (warp == 0) {
-        float top = kNoRef;
-        for (int k = 0; k < NW; ++k) top = fmaxf(top, tmp[k * (D + 2) + D]);
-        m = top;
-        sum = 0.0f;
+        for (int k = 1; k < NW; ++k) {
+          float x[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-        for (int k = 0; k < NW; ++k) {
-          const float scale = ex2(tmp[k * (D + 2) + D] - top);
-          sum += tmp[k * (D + 2) + D + 1] * scale;
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += tmp[k * (D + 2) + lane * E + e] * scale;
+          for (int e = 0; e < E; ++e) x[e] = tmp[k * (D + 2) + lane * E + e];
+          add(m, sum, acc, tmp[k * (D + 2) + D], tmp[k * (D + 2) + D + 1], x);
         }
       }
     }
     if (!shared || warp == 0) {
       const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
       bool bad = !(sum <= 3.402823466e38f);
-      const int64_t r = q.row0 + f / a.G;
+      const int32_t f = rec.f0 + col;
+      const int64_t r = rec.row0 + f / a.G;
       const int32_t qh = (rec.head * w.hw + hw) * a.G + f % a.G;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -254,7 +261,7 @@ __device__ __forceinline__ void join_split(const DevPool& p, const Batch& b, con
       if (a.lse && lane == 0) a.lse[r * a.Q + qh] = sum == 0.0f ? -INFINITY : (m - w.lift + log2f(sum)) * kLn2;
       if (__any_sync(kFull, bad)) {
         __syncwarp();
-        attend_row<C>(p, b, a, rec.s, q.a + f / a.G, r, qh, &bits);
+        attend_row<C>(p, b, a, rec.s, rec.a + f / a.G, r, qh, &bits);
       }
     }
     if (shared) __syncthreads();

@@ -256,15 +256,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
     uint32_t n = 0;       // steps of the block so far
     uint32_t mine = 0;    // of them, steps of this tile
     uint32_t done = 0;    // units of this tile
-    SplitRecord rec{-1, 0, 0, 0};
+    SplitRecord rec{-1, 0, 0, 0, 0, 0, 0};
     // the queries carry the scale's sign; a scale of 0 must keep -inf * c = -inf
     const float c0 = fmaxf(fabsf(a.scale_log2), 1e-37f);
     bool ok = true;
     for (; more && ok; more = walk.next()) {
       const bool here = wt * 128 < g.nf;  // the unit has rows in this tile
       if (g.step0 == 0 && g.end < g.span.steps())
-        rec = SplitRecord{g.s, g.tile, g.h,
-                          static_cast<int32_t>(blockIdx.x + (g.span.steps() - g.end + share - 1) / share)};
+        rec = SplitRecord{g.s, g.q.a, g.f0, g.nf, g.h,
+                          static_cast<int32_t>(blockIdx.x + (g.span.steps() - g.end + share - 1) / share), g.q.row0};
       if (!here) {
         n += g.end - g.step0;
         continue;
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
         part[kRows * (D + 1) + row] = total;
       }
     }
-    if (tid == 0) w.rec[blockIdx.x] = ok ? rec : SplitRecord{-1, 0, 0, 0};
+    if (tid == 0) w.rec[blockIdx.x] = ok ? rec : SplitRecord{-1, 0, 0, 0, 0, 0, 0};
     // rows that came out with anything not finite are done again, key by key
     asm volatile("bar.sync 1, 256;" ::: "memory");
     if (stop[1] && !*stop && walk.start(loc[0], share)) do {
