@@ -74,17 +74,19 @@ __device__ __forceinline__ uint32_t lds32(uint32_t at) {
   return v;
 }
 
+// d (+)= A B; `first`: d starts from zero.
 template <class C>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
+                                    uint32_t b1, bool first = false) {
+  const float z0 = first ? 0.0f : d[0], z1 = first ? 0.0f : d[1], z2 = first ? 0.0f : d[2], z3 = first ? 0.0f : d[3];
   if constexpr (std::is_same_v<C, __nv_bfloat16>)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z0), "f"(z1), "f"(z2), "f"(z3));
   else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z0), "f"(z1), "f"(z2), "f"(z3));
 }
 
 // 8x8 transpose of 16-bit elements over the warp.
@@ -215,7 +217,11 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
     const int32_t i0 = q.a + f0 / a.G, i1 = q.a + (f0 + nf - 1) / a.G;
 
     // ---- issue of a step's loads
-    const int64_t off = static_cast<int64_t>(cr) * row_bytes + h * Sh::kRow + cp * 16;
+    // the lane's piece of row 0 of a page, in the layer's block of keys; rows are below 2^31
+    const uint8_t* from = pool + (2 * static_cast<int64_t>(a.layer) * p.ps + cr) * row_bytes + h * Sh::kRow + cp * 16;
+    const int32_t page_rows = static_cast<int32_t>(p.stride), ps = static_cast<int32_t>(p.ps);
+    const float* scale_at = kE4M3 ? a.scales + 2 * static_cast<int64_t>(a.layer) * a.H + h : nullptr;  // of page 0
+    const int32_t page_scales = p.blocks * a.H;
     const int64_t round_bytes = Sh::kRPR * static_cast<int64_t>(row_bytes), v_bytes = p.ps * row_bytes;
     uint32_t whole_stages = 0;  // bit s: all 16 keys of stage s are tokens
     int32_t ent = 0;  // P16: page of step seg_base + lane (0: tombstone); else: raw entry of key lane % 16 of the next step
@@ -240,7 +246,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
     auto issue = [&](int32_t i, int stage) {
       if (i < end) {
         const uint32_t st = ring0 + stage * Sh::kStage;
-        const int64_t j0 = static_cast<int64_t>(span.block(i)) * 16;
+        const int32_t j0 = span.block(i) * 16;
         int32_t page;     // of the step (P16) or of key lane % 16
         int32_t rk;       // row of key 0, or of key lane % 16
         uint32_t live;    // bit k: key k is a token of the cache
@@ -251,21 +257,19 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
             ent_next = page_of_step(seg_base + 32 + lane);
           }
           page = __shfl_sync(kFull, ent, i - seg_base);
-          live = page == 0 ? 0 : j0 + 15 <= i1 ? 0xffffu : (1u << (i1 - j0 + 1)) - 1;
-          const int32_t off = p.ps_shift >= 0 ? static_cast<int32_t>(j0) & (static_cast<int32_t>(p.ps) - 1)
-                                              : static_cast<int32_t>(j0) % static_cast<int32_t>(p.ps);
-          rk = static_cast<int32_t>(page * p.stride + 2 * static_cast<int64_t>(a.layer) * p.ps) + off;
+          live = page == 0 ? 0 : i1 - j0 >= 15 ? 0xffffu : (2u << (i1 - j0)) - 1;
+          rk = page * page_rows + (p.ps_shift >= 0 ? j0 & (ps - 1) : j0 % ps);
         } else {
           const int32_t e = ent;
           ent = entry_of_key(i + 1);
-          const int64_t j = j0 + (lane & 15);
-          page = j <= i1 ? static_cast<int32_t>(page_of_entry(p, b, e, bits)) : 0;
-          rk = static_cast<int32_t>(page * p.stride + 2 * static_cast<int64_t>(a.layer) * p.ps + (j - div_ps(p, j) * p.ps));
+          const int32_t j = j0 + (lane & 15);
+          page = (lane & 15) <= i1 - j0 ? static_cast<int32_t>(page_of_entry(p, b, e, bits)) : 0;
+          rk = page * page_rows + (page != 0 ? j % ps : 0);
           live = __ballot_sync(kFull, page != 0) & 0xffffu;
         }
         const bool all = P16 && live == 0xffffu;
         whole_stages = (whole_stages & ~(1u << stage)) | static_cast<uint32_t>(all) << stage;
-        const uint8_t* base = pool + off;
+        const uint8_t* base = from;
         if (all) {  // every key is a token: one base address and constant offsets
           base += static_cast<int64_t>(rk) * row_bytes;
 #pragma unroll
@@ -289,12 +293,11 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
         if constexpr (kE4M3 && P16) {  // one scale of K (lane 0) and one of V (lane 1)
           if (lane < 2)
             copy_async<4>(st + 2 * Sh::kK + lane * 4,
-                          a.scales + (static_cast<int64_t>(page) * p.blocks + 2 * a.layer + lane) * a.H + h);
+                          scale_at + static_cast<int64_t>(page) * page_scales + lane * a.H);
         } else if constexpr (kE4M3) {  // lanes 0-15: scales of K, 16-31: of V
           const bool ok = live >> (lane & 15) & 1;
-          const float* sc =
-              a.scales + (ok ? (static_cast<int64_t>(page) * p.blocks + 2 * a.layer + (lane >> 4)) * a.H + h : 0);
-          copy_async<4>(st + 2 * Sh::kK + lane * 4, sc, ok);
+          copy_async<4>(st + 2 * Sh::kK + lane * 4,
+                        scale_at + (ok ? static_cast<int64_t>(page) * page_scales + (lane >> 4) * a.H : 0), ok);
         }
       }
       copy_commit();
@@ -336,9 +339,26 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
 #pragma unroll
         for (int ch = 0; ch < Sh::kKC; ++ch)
 #pragma unroll
-          for (int k = 0; k < EC; ++k) {
-            x[ch][k] = ok ? load_q(a, a.q, q0 + ch * 64 + c * 16 + k) : 0.0f;
-            amax = fmaxf(amax, fabsf(x[ch][k]));
+          for (int half = 0; half < 2; ++half) {
+            const uint16_t* src = static_cast<const uint16_t*>(a.q) + q0 + ch * 64 + c * 16 + half * 8;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (ok && w.q_wide) {
+              v = __ldg(reinterpret_cast<const uint4*>(src));
+            } else if (ok) {
+              uint32_t e[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) e[k] = __ldg(src + k);
+              v = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+            }
+            const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = a.type == KV_TYPE_BF16 ? make_float2(__uint_as_float(vw[k] << 16), __uint_as_float(vw[k] & 0xffff0000u))
+                                                      : halves(vw[k]);
+              x[ch][half * 8 + 2 * k] = f.x;
+              x[ch][half * 8 + 2 * k + 1] = f.y;
+              amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
           }
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
@@ -363,14 +383,17 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
     }
 
     float o[Sh::kMT][NT][4];
-    float ref[NT][2], sum[NT][2];
+    // exponents are taken below `low` = reference - lift; they may reach `high`
+    // before the reference moves (-inf: no key seen yet, so any key moves it)
+    float low[NT][2], high[NT][2], sum[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int mt = 0; mt < Sh::kMT; ++mt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.0f;
-      ref[nt][0] = ref[nt][1] = kNoRef;
+      low[nt][0] = low[nt][1] = 0.0f;
+      high[nt][0] = high[nt][1] = -INFINITY;
       sum[nt][0] = sum[nt][1] = 0.0f;
     }
 
@@ -391,11 +414,9 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
       const int32_t j0 = span.block(i) * 16;
 
       // ---- scores
-      float x[NT][4], x2[NT][4];  // two sums, so that products wait half as long for one another
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[nt][e] = x2[nt][e] = 0.0f;
+      // two sums for one tile of columns, so that products wait half as long for one another
+      constexpr bool kTwo = NT == 1;
+      float x[NT][4], x2[NT][4];
 #pragma unroll
       for (int ch = 0; ch < Sh::kKC; ++ch) {
         const uint4 u = lds128(st + (get_k ^ ch * 64)), v = lds128(st + (get_k ^ ch * 64) + 8 * Sh::kRow);
@@ -406,21 +427,23 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
             const uint32_t a0 = codes_lo(uu[wd]), a1 = codes_lo(vv[wd]), a2 = codes_hi(uu[wd]), a3 = codes_hi(vv[wd]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma<C>(wd & 1 ? x2[nt] : x[nt], a0, a1, a2, a3, qf[nt][ch * 4 + wd][0], qf[nt][ch * 4 + wd][1]);
+              mma<C>(kTwo && wd & 1 ? x2[nt] : x[nt], a0, a1, a2, a3, qf[nt][ch * 4 + wd][0], qf[nt][ch * 4 + wd][1],
+                     ch * 4 + wd < 1 + kTwo);
           }
         } else {
 #pragma unroll
           for (int wd = 0; wd < 2; ++wd)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma<C>(wd & 1 ? x2[nt] : x[nt], uu[2 * wd], vv[2 * wd], uu[2 * wd + 1], vv[2 * wd + 1],
-                     qf[nt][ch * 2 + wd][0], qf[nt][ch * 2 + wd][1]);
+              mma<C>(kTwo && wd & 1 ? x2[nt] : x[nt], uu[2 * wd], vv[2 * wd], uu[2 * wd + 1], vv[2 * wd + 1],
+                     qf[nt][ch * 2 + wd][0], qf[nt][ch * 2 + wd][1], ch * 2 + wd < 1 + kTwo);
         }
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[nt][e] += x2[nt][e];
+        for (int e = 0; e < 4; ++e)
+          if (kTwo) x[nt][e] += x2[nt][e];
 
       // ---- weights; x[.][0], [1]: key g, columns 2c, 2c + 1; [2], [3]: key g + 8
       float lv[2] = {0.0f, 0.0f}, iv[2] = {1.0f, 1.0f}, sk[2] = {1.0f, 1.0f};
@@ -445,13 +468,14 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float t = kE4M3 ? fmaf(x[nt][e] * sk[e >> 1], cq[nt][e & 1], lv[e >> 1]) : x[nt][e] * cq[nt][e & 1];
+          float t = kE4M3 ? fmaf(x[nt][e], cq[nt][e & 1] * sk[e >> 1], lv[e >> 1] - low[nt][e & 1])
+                          : fmaf(x[nt][e], cq[nt][e & 1], -low[nt][e & 1]);
           if (mask) {
             const int key = g + 8 * (e >> 1);
             if (!(live >> key & 1) || !in_sight(a, pos[nt][e & 1], j0 + key)) t = -INFINITY;
           }
           x[nt][e] = t;
-          over = over || t > ref[nt][e & 1] + 8.0f;
+          over = over || t > high[nt][e & 1];
         }
       if (__any_sync(kFull, over)) {
 #pragma unroll
@@ -462,42 +486,21 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
-            m = fmaxf(ref[nt][e], m);
-            const float keep = ex2(ref[nt][e] - m);
-            ref[nt][e] = m;
-            sum[nt][e] *= keep;
+            if (m > kLift || (m > -INFINITY && high[nt][e] == -INFINITY)) {  // the maximum becomes the reference
+              const float up = m - kLift;
+              const float keep = high[nt][e] == -INFINITY ? 0.0f : ex2(-up);
+              low[nt][e] += up;
+              high[nt][e] = kLift + 8.0f;
+              x[nt][e] -= up;
+              x[nt][e + 2] -= up;
+              sum[nt][e] *= keep;
 #pragma unroll
-            for (int mt = 0; mt < Sh::kMT; ++mt) {
-              o[mt][nt][e] *= keep;
-              o[mt][nt][e + 2] *= keep;
+              for (int mt = 0; mt < Sh::kMT; ++mt) {
+                o[mt][nt][e] *= keep;
+                o[mt][nt][e + 2] *= keep;
+              }
             }
           }
-      }
-      // A value that is not finite must reach the rows that see its key and no
-      // other, but 0 * NaN would spread it. Where some row may not see some
-      // key, such elements are zeroed here and the rows that do see the key
-      // get a NaN denominator: they are done again, key by key, at the end.
-      if (mask) {
-        uint32_t keys = 0;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-          for (int wd = 0; wd < Sh::kVB / 4; ++wd) {
-            const uint32_t at = st + Sh::kK + get_v + key_at(kk) + wd / 4 * 128 + wd % 4 * 4;
-            const uint32_t v = lds32(at), bad = not_finite<C>(v);
-            if (bad) {
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v & ~bad) : "memory");
-              keys |= 1u << (2 * c + (kk & 1) + 8 * (kk >> 1));
-            }
-          }
-        keys = __reduce_or_sync(kFull, keys);
-        if (keys) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (keys >> (g + 8 * (e >> 1)) & 1 && x[nt][e] != -INFINITY) sum[nt][e & 1] = NAN;
-        }
       }
       uint32_t pb[NT][2], pl[NT][2];
 #pragma unroll
@@ -505,12 +508,18 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
         float y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          y[e] = ex2(x[nt][e] - ref[nt][e & 1] + kLift);
+          y[e] = ex2(x[nt][e]);
           // a dead key adds nothing, whatever its zero-filled scale's inverse is
-          if constexpr (kE4M3)
-            sum[nt][e & 1] += live == 0xffffu || live >> (g + 8 * (e >> 1)) & 1 ? y[e] * iv[e >> 1] : 0.0f;
-          else
+          if constexpr (kE4M3 && !P16)
+            sum[nt][e & 1] += live >> (g + 8 * (e >> 1)) & 1 ? y[e] * iv[e >> 1] : 0.0f;
+          else if constexpr (!kE4M3)
             sum[nt][e & 1] += y[e];
+        }
+        if constexpr (kE4M3 && P16) {
+          if (live) {
+            sum[nt][0] = fmaf(y[0] + y[2], iv[0], sum[nt][0]);
+            sum[nt][1] = fmaf(y[1] + y[3], iv[0], sum[nt][1]);
+          }
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -546,6 +555,29 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
           } else {
             const uint2 u = lds64(st + Sh::kK + get_v + key_at(kk));
             v[kk][0] = u.x, v[kk][1] = u.y;
+          }
+        }
+        // A value that is not finite must reach the rows that see its key and no
+        // other, but 0 * NaN would spread it. Where some row may not see some
+        // key, such elements are zeroed here and the rows that do see the key
+        // get a NaN denominator: they are done again, key by key, at the end.
+        if (mask) {
+          uint32_t keys = 0;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int wd = 0; wd < VW; ++wd) {
+              const uint32_t bad = not_finite<C>(v[kk][wd]);
+              v[kk][wd] &= ~bad;
+              if (bad) keys |= 1u << (2 * c + (kk & 1) + 8 * (kk >> 1));
+            }
+          keys = __reduce_or_sync(kFull, keys);
+          if (keys) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (keys >> (g + 8 * (e >> 1)) & 1 && x[nt][e] != -INFINITY) sum[nt][e & 1] = NAN;
           }
         }
 #pragma unroll
@@ -604,7 +636,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
             }
           }
           if (a.lse && g == 0 && col < nf)
-            a.lse[r * a.Q + qh] = sum[nt][e] == 0.0f ? -INFINITY : (ref[nt][e] - kLift + log2f(sum[nt][e])) * kLn2;
+            a.lse[r * a.Q + qh] = sum[nt][e] == 0.0f ? -INFINITY : (low[nt][e] + log2f(sum[nt][e])) * kLn2;
           // columns with anything not finite are done again, key by key
           const uint32_t again = __ballot_sync(kFull, bad && col < nf);
           if (again) {
@@ -629,7 +661,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
             *reinterpret_cast<float4*>(part + col * D + element(mt)) =
                 make_float4(o[mt][nt][e], o[mt][nt][e + 2], o[mt + 1][nt][e], o[mt + 1][nt][e + 2]);
           if (g == 0) {
-            part[NQ * D + col] = ref[nt][e];
+            part[NQ * D + col] = high[nt][e] == -INFINITY ? kNoRef : low[nt][e];
             part[NQ * (D + 1) + col] = sum[nt][e];
           }
         }
@@ -740,7 +772,7 @@ cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs
   const int64_t warps = static_cast<int64_t>(sm_count) * kFewBlocksPerSM * kFewWarps;
   w.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + split_record_bytes(warps));
   w.nq = 8 * nt;
-  w.lift = !e4m3 && a.type == KV_TYPE_BF16 ? FewType<__nv_bfloat16>::kLift : FewType<__half>::kLift;
+  w.lift = 0.0f;  // the partial results' references are below it already
   w.q_wide = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.q_stride % 8 == 0;
   w.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
   *out = w;
