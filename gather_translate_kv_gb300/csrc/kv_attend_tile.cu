@@ -329,25 +329,33 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           o = make_float2(lv.x + off, lv.y + off);
         };
         if (i == g.step0) {  // the reference starts as the first step's maximum
-          float m0 = -INFINITY, m1 = -INFINITY;
+          float m = -INFINITY;
+          if constexpr (!kE4M3) {  // the loads' own maximum
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            uint32_t x[32];
-            tmem_load32(tS + 32 * k, x);
-            tmem_wait_ld(x);
+            for (int k = 0; k < 4; ++k) {
+              uint32_t x[32];
+              float top;
+              tmem_load32_max(tS + 32 * k, x, top);
+              tmem_wait_ld(x);
+              tmem_tie(x, top);
+              m = fmaxf(m, top);
+            }
+            m *= c;
+          } else {
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              uint32_t x[32];
+              tmem_load32(tS + 32 * k, x);
+              tmem_wait_ld(x);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float2 t = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-              if constexpr (kE4M3) {
+              for (int e = 0; e < 32; e += 2) {
                 float2 mm, oo;
                 log_scale(32 * k + e, 0.0f, mm, oo);
-                t = ffma2(t, mm, oo);
+                const float2 t = ffma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mm, oo);
+                m = fmaxf(m, fmaxf(t.x, t.y));
               }
-              m0 = fmaxf(m0, t.x);
-              m1 = fmaxf(m1, t.y);
             }
           }
-          const float m = fmaxf(m0, m1) * (kE4M3 ? 1.0f : c);
           if (m > -INFINITY) ref = m;
         }
         // Weights under the present reference, and the largest exponent on the
@@ -450,6 +458,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
         bool bad = !(total <= 3.402823466e38f);
         const float inv = bad ? NAN : total == 0.0f ? 0.0f : __fdividef(1.0f, total);
         uint16_t* out = static_cast<uint16_t*>(a.out) + (orow * a.Q + qh) * D;
+        const float2 inv2 = make_float2(inv, inv), none = make_float2(0.0f, 0.0f);
+        float2 zero = none;  // stays 0 while all values are finite
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
           uint32_t raw[32];
@@ -458,9 +468,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           uint32_t y[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float y0 = __uint_as_float(raw[2 * e]) * inv, y1 = __uint_as_float(raw[2 * e + 1]) * inv;
-            bad = bad || !(fabsf(y0) <= 3.402823466e38f) || !(fabsf(y1) <= 3.402823466e38f);
-            y[e] = a.type == KV_TYPE_BF16 ? pack_b(y0, y1) : pack_h(y0, y1);
+            const float2 v = ffma2(make_float2(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), inv2, none);
+            zero = ffma2(v, none, zero);
+            y[e] = a.type == KV_TYPE_BF16 ? pack_b(v.x, v.y) : pack_h(v.x, v.y);
           }
           if (row_ok) {
             if (w.out_wide) {
@@ -480,6 +490,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           }
         }
         if (a.lse && row_ok) a.lse[orow * a.Q + qh] = total == 0.0f ? -INFINITY : (ref - kLift + log2f(total)) * kLn2;
+        bad = bad || !(zero.x + zero.y == 0.0f);
         if (bad && row_ok) stop[1] = 1;
       } else {
         const int slot = g.step0 == 0 ? 1 : 0;
