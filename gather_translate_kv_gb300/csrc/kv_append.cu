@@ -197,27 +197,31 @@ __device__ __forceinline__ int64_t scale_at(const DevPool& p, int32_t H, int64_t
   return (page * p.blocks + 2 * layer + kv) * H + h;  // blocks = 2L: [page][layer][K or V][head]
 }
 
-// Heads [0, heads) of the list (queries, keys, values) of rows r0 on, tpr
-// threads a row (32, 64, ... 256). A lane keeps its task and so its cosines
-// and sines for all heads. The loads of U heads are issued before the row's place is
-// looked up: the lookups are a chain of dependent loads, four or five round trips long.
+constexpr int kRowThreads = 64;                       // threads a row
+constexpr int kRowsAtOnce = kAppendBlock / kRowThreads;
+constexpr int kMaxRows = 16;                          // rows a block
+
+// Heads [0, heads) of the list (queries, keys, values) of rows [r0, r0 + rows),
+// 64 threads a row, four rows at a time. Where the rows belong is a chain of four or
+// five dependent loads; the block's warps follow it for all its rows at once,
+// while the first rows' data is already on its way. A lane keeps its task and
+// so its cosines and sines for all heads of a row, U of them in flight.
 template <class T>
 __device__ __forceinline__ void append_rows(const DevPool& p, const Batch& b, const AppendArgs& g, const Rot& t,
-                                            int64_t r0, int tpr, int heads, int& bits) {
-  const int64_t r = r0 + threadIdx.x / tpr;
-  if (r >= b.n_rows) return;  // whole warps
-  const int lt = threadIdx.x % tpr;
+                                            int64_t r0, int rows, int heads, Token* tokens, int& bits) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = threadIdx.x / kRowThreads, lt = threadIdx.x % kRowThreads;
   const int nt = g.D / 16;
-  const int groups = tpr / nt;
+  const int groups = kRowThreads / nt;
   const int grp = lt / nt;
   const Task task = task_of(t, lt - grp * nt);
-  const T* q = static_cast<const T*>(g.q) + r * g.q_stride;
-  const T* kk = static_cast<const T*>(g.k) + r * g.k_stride;
-  const T* vv = static_cast<const T*>(g.v) + r * g.v_stride;
   constexpr int U = sizeof(T) == 2 ? 6 : 3;
   Raw<T> raw[U];
   const int h_lo = grp < groups ? grp : heads;  // lanes left over by the tasks have no head
-  auto load = [&](int h0) {
+  auto load = [&](int64_t r, int h0) {
+    const T* q = static_cast<const T*>(g.q) + r * g.q_stride;
+    const T* kk = static_cast<const T*>(g.k) + r * g.k_stride;
+    const T* vv = static_cast<const T*>(g.v) + r * g.v_stride;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = h0 + u * groups;
@@ -226,51 +230,62 @@ __device__ __forceinline__ void append_rows(const DevPool& p, const Batch& b, co
                              task);
     }
   };
-  load(h_lo);
-  const Token k = token_of_row(p, b, r, bits);
-  if (!k.ok) return;
-  if (!positions_ok(t, b, r, k.j)) {
-    bits |= KV_DEV_ERR_POSITION;
-    return;
-  }
-  float c[8], s[8];
-  if (task.c8 >= 0) load_cs(t, b, r, k.j, task, c, s);
-  for (int h0 = h_lo; h0 < heads; h0 += groups * U) {
-    if (h0 != h_lo) load(h0);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * groups;
-      if (h >= heads) break;
-      T* y;
-      if (h < g.Q) {
-        y = static_cast<T*>(g.q_out) + (r * g.Q + h) * g.D;
-      } else {
-        if (k.page == 0) break;  // tombstone: not stored (keys and values come after all queries)
-        const int kv = h >= g.Q + g.H;
-        y = pool_row<T>(p, g.layer, kv, k.page, k.off) + (h - g.Q - kv * g.H) * g.D;
+  if (sub < rows && r0 + sub < b.n_rows) load(r0 + sub, h_lo);
+  for (int i = warp; i < rows; i += kAppendBlock / 32) {
+    Token k{0, 0, 0, false};
+    if (r0 + i < b.n_rows) {
+      k = token_of_row(p, b, r0 + i, bits);
+      if (k.ok && !positions_ok(t, b, r0 + i, k.j)) {
+        bits |= KV_DEV_ERR_POSITION;
+        k.ok = false;
       }
-      if (task.c8 >= 0 && h < g.Q + g.H) {
-        float x[16];
-        unpack(raw[u], x);
-        turn16(t, x, c, s);
-        store16(y, task, x);
-      } else {
-        store_raw(y, task, raw[u]);
+    }
+    if (lane == 0) tokens[i] = k;
+  }
+  __syncthreads();
+  for (int i = sub; i < rows; i += kRowsAtOnce) {
+    const int64_t r = r0 + i;
+    const Token k = tokens[i];
+    if (!k.ok) continue;
+    float c[8], s[8];
+    if (i != sub) load(r, h_lo);
+    if (task.c8 >= 0) load_cs(t, b, r, k.j, task, c, s);
+    for (int h0 = h_lo; h0 < heads; h0 += groups * U) {
+      if (h0 != h_lo) load(r, h0);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * groups;
+        if (h >= heads) break;
+        T* y;
+        if (h < g.Q) {
+          y = static_cast<T*>(g.q_out) + (r * g.Q + h) * g.D;
+        } else {
+          if (k.page == 0) break;  // tombstone: not stored (keys and values come after all queries)
+          const int kv = h >= g.Q + g.H;
+          y = pool_row<T>(p, g.layer, kv, k.page, k.off) + (h - g.Q - kv * g.H) * g.D;
+        }
+        if (task.c8 >= 0 && h < g.Q + g.H) {
+          float x[16];
+          unpack(raw[u], x);
+          turn16(t, x, c, s);
+          store16(y, task, x);
+        } else {
+          store_raw(y, task, raw[u]);
+        }
       }
     }
   }
 }
 
-// Threads a row: a quarter of a block where rows are many, so that a lane has
-// several heads' loads in flight; a whole block where there are few (a decode
-// step), whose time is the chain of lookups and not the traffic.
-inline int threads_per_row(int64_t n_rows) { return n_rows >= 1024 ? 64 : kAppendBlock; }
+// Rows a block: sixteen share one chain of lookups where there are blocks enough.
+inline int rows_per_block(int64_t n_rows) { return n_rows >= 4096 ? kMaxRows : kRowsAtOnce; }
 
 // Pools that hold the inputs' own type.
 template <class T>
-__global__ void __launch_bounds__(kAppendBlock) k_append(DevPool p, Batch b, AppendArgs g, Rot t, int tpr) {
+__global__ void __launch_bounds__(kAppendBlock, 2) k_append(DevPool p, Batch b, AppendArgs g, Rot t, int rows) {
+  __shared__ Token tokens[kMaxRows];
   int bits = 0;
-  append_rows<T>(p, b, g, t, static_cast<int64_t>(blockIdx.x) * (kAppendBlock / tpr), tpr, g.Q + 2 * g.H, bits);
+  append_rows<T>(p, b, g, t, static_cast<int64_t>(blockIdx.x) * rows, rows, g.Q + 2 * g.H, tokens, bits);
   store_bits(p, bits);
 }
 
@@ -287,148 +302,249 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a <= 3.402823466e38f ? a : 0.0f;  // infinities and NaN do not count
 }
 
-// The scale after the append, from the page's earlier scale (0: none) and the largest new magnitude of the warp.
+// The scale after the append, from the page's earlier scale (0: none) and the largest new magnitude.
 __device__ __forceinline__ float new_scale(float amax, float old, float* base) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
   if (!(old > 0.0f && old <= 3.402823466e38f)) old = 0.0f;
   *base = old;
   return fmaxf(old, power_of_two(amax));
 }
 
-// 8-bit pools. A block takes one page run, a warp two heads of it at a time
-// (of K and of V where there are eight KV heads): 32 / (D / 16) tokens a
-// wave, four waves of both held in registers as they were loaded, so a run of up to
-// 16 tokens of 128 elements (32 of 64) is read once; longer runs are read
-// again, from L1 or L2, once the scale is known. The rotation is done twice, for the
-// maximum and for the codes: it is cheaper than the registers that would keep
-// its result. Blocks after the runs' rotate the queries.
+// 8-bit pools, few tokens a run (decode steps): a warp takes K or V of a run,
+// D / 16 lanes a head, so one token of eight 64-element heads fills it. Four
+// tokens and the codes of eight earlier ones are in flight per lane.
 template <class T>
-__global__ void __launch_bounds__(kAppendBlock, 2) k_append_e4m3(DevPool p, Batch b, AppendArgs g, Rot t, bool by_row,
-                                                              int64_t n_runs, int tpr) {
-  int bits = 0;
-  if (blockIdx.x >= n_runs) {
-    append_rows<T>(p, b, g, t, (blockIdx.x - n_runs) * static_cast<int64_t>(kAppendBlock / tpr), tpr, g.Q, bits);
-    store_bits(p, bits);
-    return;
+__device__ __forceinline__ void append_run_few(const DevPool& p, const Batch& b, const AppendArgs& g, const Rot& t,
+                                               const PageRun& run, int kv, int& bits) {
+  const int lane = threadIdx.x & 31;
+  const int nt = g.D / 16, heads_at_once = 32 / nt;
+  const int grp = lane / nt, part = lane - grp * nt;
+  const Task task = task_of(t, part);
+  const int64_t row_bytes = p.vpr * 16;
+  const int64_t stride = kv ? g.v_stride : g.k_stride;
+  constexpr int M = sizeof(T) == 2 ? 4 : 2, O = 8;
+  for (int h0 = 0; h0 < g.H; h0 += heads_at_once) {
+    const int h = h0 + grp;
+    const bool in = grp < heads_at_once && h < g.H;
+    const T* src = (kv ? static_cast<const T*>(g.v) : static_cast<const T*>(g.k)) + h * g.D;
+    uint8_t* page = pool_row<uint8_t>(p, g.layer, kv, run.page, 0) + h * g.D;
+    float* at = g.scales + scale_at(p, g.H, run.page, g.layer, kv, in ? h : 0);
+    Raw<T> raw[M];
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int i = 0; i < M; ++i)
+        if (in && i0 + i < run.m) raw[i] = load_raw<T>(src + (run.row + i0 + i) * stride, task);
+    };
+    auto values = [&](int i0, int i, float (&x)[16]) -> bool {
+      if (!in || i0 + i >= run.m) return false;
+      const int64_t r = run.row + i0 + i, j = run.j + i0 + i;
+      if (!positions_ok(t, b, r, j)) {
+        bits |= KV_DEV_ERR_POSITION;
+        return false;
+      }
+      unpack(raw[i], x);
+      if (kv == 0 && task.c8 >= 0) {
+        float c[8], s[8];
+        load_cs(t, b, r, j, task, c, s);
+        turn16(t, x, c, s);
+      }
+      return true;
+    };
+    uint2 old[O][2];
+    auto load_old = [&](int i0) {
+#pragma unroll
+      for (int i = 0; i < O; ++i)
+        if (in && i0 + i < run.off) {
+          const uint8_t* y = page + (i0 + i) * row_bytes;
+          old[i][0] = *reinterpret_cast<const uint2*>(y + task.a);
+          old[i][1] = *reinterpret_cast<const uint2*>(y + task.b);
+        }
+    };
+    load(0);
+    const float before = in && run.off > 0 ? *at : 0.0f;
+    load_old(0);
+    float amax = 0.0f;
+    for (int i0 = 0; i0 < run.m; i0 += M) {
+      if (i0 > 0) load(i0);
+#pragma unroll
+      for (int i = 0; i < M; ++i) {
+        float x[16];
+        if (values(i0, i, x)) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) amax = fmaxf(amax, finite_abs(x[e]));
+        }
+      }
+    }
+    float top = amax;  // over the head's lanes
+    for (int o = 1; o < nt; ++o) {
+      const int other = grp * nt + (part + o) % nt;
+      top = fmaxf(top, __shfl_sync(kFull, amax, other & 31));
+    }
+    float base;
+    const float S = new_scale(top, before, &base);
+    if (run.off > 0 && base != S) {  // the earlier tokens' codes under the new scale
+      const float f = base / S;
+      for (int i0 = 0; i0 < run.off; i0 += O) {
+        if (i0 > 0) load_old(i0);
+#pragma unroll
+        for (int i = 0; i < O; ++i)
+          if (in && i0 + i < run.off) {
+            uint8_t* y = page + (i0 + i) * row_bytes;
+            *reinterpret_cast<uint2*>(y + task.a) = make_uint2(rescale4(old[i][0].x, f), rescale4(old[i][0].y, f));
+            *reinterpret_cast<uint2*>(y + task.b) = make_uint2(rescale4(old[i][1].x, f), rescale4(old[i][1].y, f));
+          }
+      }
+    }
+    const float inv = 1.0f / S;
+    for (int i0 = 0; i0 < run.m; i0 += M) {
+      if (run.m > M) load(i0);
+#pragma unroll
+      for (int i = 0; i < M; ++i) {
+        float x[16];
+        if (!values(i0, i, x)) continue;
+        uint8_t* y = page + (run.off + i0 + i) * row_bytes;
+        uint32_t v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = encode4(x[4 * e] * inv, x[4 * e + 1] * inv, x[4 * e + 2] * inv, x[4 * e + 3] * inv);
+        *reinterpret_cast<uint2*>(y + task.a) = make_uint2(v[0], v[1]);
+        *reinterpret_cast<uint2*>(y + task.b) = make_uint2(v[2], v[3]);
+      }
+    }
+    __syncwarp();
+    if (in && part == 0) *at = S;
   }
-  const PageRun run = page_run(p, b, blockIdx.x, by_row, bits);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int NW = kAppendBlock / 32;
+}
+
+// 8-bit pools, page by page: a warp takes one head of K or V of a run, 32 /
+// (D / 16) tokens a wave, four waves held in registers as they were loaded, so
+// a run of up to 16 tokens of 128 elements (32 of 64) is read once; longer
+// runs are read again, from L1 or L2, once the scale is known. The rotation is
+// done twice, for the maximum and for the codes: it is cheaper than the
+// registers that would keep its result.
+template <class T>
+__device__ __forceinline__ void append_run(const DevPool& p, const Batch& b, const AppendArgs& g, const Rot& t,
+                                           const PageRun& run, int kvh, int& bits) {
+  const int lane = threadIdx.x & 31;
   const int nt = g.D / 16;
   const int tpw = 32 / nt;  // tokens a wave
   const int tok = lane / nt;
   const bool in = tok < tpw;
   const Task task = task_of(t, lane - tok * nt);
-  constexpr int W = 4, HB = 1;
+  constexpr int W = 4;
   const bool one = run.m <= W * tpw;  // the run fits the registers
   const bool held = run.off > 0;
-  for (int kvh0 = warp; run.m != 0 && run.page != 0 && kvh0 < 2 * g.H; kvh0 += NW * HB) {
-    Raw<T> raw[HB][W];
-    auto head = [&](int n) { return kvh0 + n * NW; };
-    auto load = [&](int n, int i0) {
-      const int kvh = head(n), kv = kvh >= g.H;
-      const T* src = (kv ? static_cast<const T*>(g.v) : static_cast<const T*>(g.k)) + (kvh - kv * g.H) * g.D;
-      const int64_t stride = kv ? g.v_stride : g.k_stride;
+  const int kv = kvh >= g.H, h = kvh - kv * g.H;
+  const T* src = (kv ? static_cast<const T*>(g.v) : static_cast<const T*>(g.k)) + h * g.D;
+  const int64_t stride = kv ? g.v_stride : g.k_stride;
+  Raw<T> raw[W];
+  auto load = [&](int i0) {
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const int i = i0 + w * tpw + tok;
-        if (in && i < run.m && kvh < 2 * g.H) raw[n][w] = load_raw<T>(src + (run.row + i) * stride, task);
-      }
-    };
-    // wave w of the tokens from i0 on: its 16 values, false where there is no such token
-    auto values = [&](int n, int i0, int w, float (&x)[16]) -> bool {
+    for (int w = 0; w < W; ++w) {
       const int i = i0 + w * tpw + tok;
-      if (!in || i >= run.m) return false;
-      if (!positions_ok(t, b, run.row + i, run.j + i)) {
-        bits |= KV_DEV_ERR_POSITION;
-        return false;
-      }
-      unpack(raw[n][w], x);
-      if (head(n) < g.H && task.c8 >= 0) {
-        float c[8], s[8];
-        load_cs(t, b, run.row + i, run.j + i, task, c, s);
-        turn16(t, x, c, s);
-      }
-      return true;
-    };
-    // earlier tokens' codes, asked for before it is known whether the scale moves
-    uint2 old[HB][W][2];
+      if (in && i < run.m) raw[w] = load_raw<T>(src + (run.row + i) * stride, task);
+    }
+  };
+  // wave w of the tokens from i0 on: its 16 values, false where there is no such token
+  auto values = [&](int i0, int w, float (&x)[16]) -> bool {
+    const int i = i0 + w * tpw + tok;
+    if (!in || i >= run.m) return false;
+    if (!positions_ok(t, b, run.row + i, run.j + i)) {
+      bits |= KV_DEV_ERR_POSITION;
+      return false;
+    }
+    unpack(raw[w], x);
+    if (kv == 0 && task.c8 >= 0) {
+      float c[8], s[8];
+      load_cs(t, b, run.row + i, run.j + i, task, c, s);
+      turn16(t, x, c, s);
+    }
+    return true;
+  };
+  load(0);
+  float* at = g.scales + scale_at(p, g.H, run.page, g.layer, kv, h);
+  const float before = held ? *at : 0.0f;
+  float amax = 0.0f;
+  for (int i0 = 0; i0 < run.m; i0 += W * tpw) {
+    if (i0 > 0) load(i0);
 #pragma unroll
-    for (int n = 0; n < HB; ++n) {
-      const int kvh = head(n), kv = kvh >= g.H;
-      load(n, 0);
-      if (one) {
+    for (int w = 0; w < W; ++w) {
+      float x[16];
+      if (values(i0, w, x)) {
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-          const int i = w * tpw + tok;
-          if (in && i < run.off && kvh < 2 * g.H) {
-            const uint8_t* y = pool_row<uint8_t>(p, g.layer, kv, run.page, i) + (kvh - kv * g.H) * g.D;
-            old[n][w][0] = *reinterpret_cast<const uint2*>(y + task.a);
-            old[n][w][1] = *reinterpret_cast<const uint2*>(y + task.b);
-          }
-        }
+        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, finite_abs(x[e]));
       }
     }
+  }
 #pragma unroll
-    for (int n = 0; n < HB; ++n) {
-      const int kvh = head(n), kv = kvh >= g.H, h = kvh - kv * g.H;
-      if (kvh >= 2 * g.H) break;  // (warp-uniform)
-      float* at = g.scales + scale_at(p, g.H, run.page, g.layer, kv, h);
-      const float before = held ? *at : 0.0f;
-      float amax = 0.0f;
-      for (int i0 = 0; i0 < run.m; i0 += W * tpw) {
-        if (i0 > 0) load(n, i0);
+  for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+  float base;
+  const float S = new_scale(amax, before, &base);
+  uint8_t* page = pool_row<uint8_t>(p, g.layer, kv, run.page, 0) + h * g.D;
+  const int64_t row_bytes = p.vpr * 16;
+  if (held && base != S) {  // the earlier tokens' codes under the new scale
+    const float f = base / S;
+#pragma unroll 4
+    for (int i = tok; i < run.off; i += tpw) {
+      if (!in) break;
+      uint8_t* y = page + i * row_bytes;
+      const uint2 v0 = *reinterpret_cast<const uint2*>(y + task.a), v1 = *reinterpret_cast<const uint2*>(y + task.b);
+      *reinterpret_cast<uint2*>(y + task.a) = make_uint2(rescale4(v0.x, f), rescale4(v0.y, f));
+      *reinterpret_cast<uint2*>(y + task.b) = make_uint2(rescale4(v1.x, f), rescale4(v1.y, f));
+    }
+  }
+  const float inv = 1.0f / S;
+  for (int i0 = 0; i0 < run.m; i0 += W * tpw) {
+    if (!one) load(i0);
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-          float x[16];
-          if (values(n, i0, w, x)) {
+    for (int w = 0; w < W; ++w) {
+      float x[16];
+      if (!values(i0, w, x)) continue;
+      uint8_t* y = page + (run.off + i0 + w * tpw + tok) * row_bytes;
+      uint32_t v[4];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) amax = fmaxf(amax, finite_abs(x[e]));
-          }
-        }
-      }
-      float base;
-      const float S = new_scale(amax, before, &base);
-      uint8_t* page = pool_row<uint8_t>(p, g.layer, kv, run.page, 0) + h * g.D;
-      const int64_t row_bytes = p.vpr * 16;
-      if (held && base != S) {  // the earlier tokens' codes under the new scale
-        const float f = base / S;
-        auto put = [&](int i, uint2 v0, uint2 v1) {
-          uint8_t* y = page + i * row_bytes;
-          *reinterpret_cast<uint2*>(y + task.a) = make_uint2(rescale4(v0.x, f), rescale4(v0.y, f));
-          *reinterpret_cast<uint2*>(y + task.b) = make_uint2(rescale4(v1.x, f), rescale4(v1.y, f));
-        };
-        if (one) {
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-            const int i = w * tpw + tok;
-            if (in && i < run.off) put(i, old[n][w][0], old[n][w][1]);
-          }
-        }
-        for (int i = (one ? W * tpw : 0) + tok; in && i < run.off; i += tpw) {
-          const uint8_t* y = page + i * row_bytes;
-          put(i, *reinterpret_cast<const uint2*>(y + task.a), *reinterpret_cast<const uint2*>(y + task.b));
-        }
-      }
-      const float inv = 1.0f / S;
-      for (int i0 = 0; i0 < run.m; i0 += W * tpw) {
-        if (!one) load(n, i0);
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-          float x[16];
-          if (!values(n, i0, w, x)) continue;
-          uint8_t* y = page + (run.off + i0 + w * tpw + tok) * row_bytes;
-          uint32_t v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[e] = encode4(x[4 * e] * inv, x[4 * e + 1] * inv, x[4 * e + 2] * inv, x[4 * e + 3] * inv);
-          *reinterpret_cast<uint2*>(y + task.a) = make_uint2(v[0], v[1]);
-          *reinterpret_cast<uint2*>(y + task.b) = make_uint2(v[2], v[3]);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) *at = S;
+      for (int e = 0; e < 4; ++e)
+        v[e] = encode4(x[4 * e] * inv, x[4 * e + 1] * inv, x[4 * e + 2] * inv, x[4 * e + 3] * inv);
+      *reinterpret_cast<uint2*>(y + task.a) = make_uint2(v[0], v[1]);
+      *reinterpret_cast<uint2*>(y + task.b) = make_uint2(v[2], v[3]);
+    }
+  }
+  __syncwarp();
+  if (lane == 0) *at = S;
+}
+
+constexpr int kRunsPerBlock = 4;
+
+// Four runs a block, looked up by a warp each, then shared out by head (or,
+// where runs are a few tokens, by K and V); blocks after the runs' rotate the queries.
+template <class T, bool FEW>
+__global__ void __launch_bounds__(kAppendBlock, 2) k_append_e4m3(DevPool p, Batch b, AppendArgs g, Rot t, int64_t n_runs,
+                                                                 int rows) {
+  __shared__ Token tokens[kMaxRows];
+  __shared__ PageRun runs[kRunsPerBlock];
+  int bits = 0;
+  const int64_t run_blocks = (n_runs + kRunsPerBlock - 1) / kRunsPerBlock;
+  if (blockIdx.x >= run_blocks) {
+    append_rows<T>(p, b, g, t, (blockIdx.x - run_blocks) * rows, rows, g.Q, tokens, bits);
+    store_bits(p, bits);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int NW = kAppendBlock / 32;
+  if (warp < kRunsPerBlock) {
+    const int64_t c = blockIdx.x * static_cast<int64_t>(kRunsPerBlock) + warp;
+    PageRun run{0, 0, 0, 0, 0, 0};
+    if (c < n_runs) run = page_run(p, b, c, FEW, bits);
+    if (lane == 0) runs[warp] = run;
+  }
+  __syncthreads();
+  if constexpr (FEW) {
+    const PageRun run = runs[warp >> 1];
+    static_assert(NW == 2 * kRunsPerBlock);
+    if (run.m != 0 && run.page != 0) append_run_few<T>(p, b, g, t, run, warp & 1, bits);
+  } else {
+    for (int i = warp; i < kRunsPerBlock * 2 * g.H; i += NW) {
+      const PageRun run = runs[i / (2 * g.H)];
+      if (run.m != 0 && run.page != 0) append_run<T>(p, b, g, t, run, i % (2 * g.H), bits);
     }
   }
   store_bits(p, bits);
@@ -491,6 +607,8 @@ __global__ void __launch_bounds__(kAppendBlock) k_append_any(DevPool p, Batch b,
           amax = fmaxf(amax, fmaxf(finite_abs(x1), finite_abs(x2)));
         }
       }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
       at = g.scales + scale_at(p, g.H, run.page, g.layer, kv, h);
       const bool held = run.off > 0;
       float base;
@@ -550,13 +668,17 @@ cudaError_t launch(const DevPool& p, const Batch& b, const AppendArgs& g, const 
     else
       k_append_any<T, false><<<n, kAppendBlock, 0, s>>>(p, b, g, t, by_row, n_runs);
   } else {
-    const int tpr = threads_per_row(b.n_rows);
-    const int64_t row_blocks = (b.n_rows + kAppendBlock / tpr - 1) / (kAppendBlock / tpr);
-    if (row_blocks + n_runs > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    if (e4m3)
-      k_append_e4m3<T><<<grid(n_runs + (g.Q ? row_blocks : 0)), kAppendBlock, 0, s>>>(p, b, g, t, by_row, n_runs, tpr);
+    const int rows = rows_per_block(b.n_rows);
+    const int64_t row_blocks = (b.n_rows + rows - 1) / rows;
+    const int64_t run_blocks = (n_runs + kRunsPerBlock - 1) / kRunsPerBlock;
+    if (row_blocks + run_blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const unsigned blocks = grid(run_blocks + (g.Q ? row_blocks : 0));
+    if (!e4m3)
+      k_append<T><<<grid(row_blocks), kAppendBlock, 0, s>>>(p, b, g, t, rows);
+    else if (by_row)
+      k_append_e4m3<T, true><<<blocks, kAppendBlock, 0, s>>>(p, b, g, t, n_runs, rows);
     else
-      k_append<T><<<grid(row_blocks), kAppendBlock, 0, s>>>(p, b, g, t, tpr);
+      k_append_e4m3<T, false><<<blocks, kAppendBlock, 0, s>>>(p, b, g, t, n_runs, rows);
   }
   return cudaGetLastError();
 }
