@@ -7,10 +7,11 @@
 //
 // All of it is memory traffic: rows in, rows out, a few operations per
 // element, so the kernels are built around 16-byte loads. A lane takes the 16
-// elements of a "task": two 8-element chunks that hold the 8 pairs
-// 8c .. 8c + 7 under either pairing (chunks c and c + rotary_dim / 16 for
-// half pairing, 2c and 2c + 1 for adjacent pairs), so it needs 8 cosines and
-// 8 sines and no other lane's data. D / 16 lanes cover a head's row.
+// elements of a "task": chunks c and c + rotary_dim / 16 of 8 elements, which
+// hold 8 whole pairs under either pairing (pairs 8c .. 8c + 7 for half
+// pairing, 4c .. and rotary_dim / 4 + 4c .. for adjacent pairs), so it needs 8
+// cosines and 8 sines and no other lane's data, and the lanes' chunks follow
+// one another. D / 16 lanes cover a head's row.
 #include "kv_attn_launch.h"
 #include "kv_batch.cuh"
 
@@ -30,14 +31,14 @@ struct Rot {
   int32_t end[4];  // first pair past each axis
 };
 
+// Axis of pair f.
+__device__ __forceinline__ int axis_of(const Rot& t, int f) {
+  return (t.n_axes > 1 && f >= t.end[0]) + (t.n_axes > 2 && f >= t.end[1]) + (t.n_axes > 3 && f >= t.end[2]);
+}
+
 // Position of token j (row r) on the axis of pair f; -1 when outside the table.
 __device__ __forceinline__ int64_t position(const Rot& t, const Batch& b, int64_t r, int64_t j, int f) {
-  int64_t q = j;
-  if (t.pos) {
-    int a = 0;
-    while (a + 1 < t.n_axes && f >= t.end[a]) ++a;
-    q = __ldg(t.pos + a * b.n_rows + r);
-  }
+  const int64_t q = t.pos ? __ldg(t.pos + axis_of(t, f) * b.n_rows + r) : j;
   return q >= 0 && q < t.n_pos ? q : -1;
 }
 
@@ -62,14 +63,15 @@ __device__ __forceinline__ void turn(float& x1, float& x2, float c, float s) {
 // ---- a lane's task -----------------------------------------------------------
 
 struct Task {
-  int a, b;  // element offsets of its two chunks in a head
-  int c8;    // first of its 8 pairs, -1: not rotated
+  int a, b;    // element offsets of its two chunks in a head
+  int f0, f1;  // first of the first and of the last four of its 8 pairs, -1: not rotated
 };
 
-__device__ __forceinline__ Task task_of(const Rot& t, int c) {
+__device__ __forceinline__ Task task_of(const Rot& t, int D, int c) {
   const int n = t.rd / 16;
-  if (c < n && !t.interleaved) return {c * 8, t.rd / 2 + c * 8, c * 8};
-  return {c * 16, c * 16 + 8, c < n ? c * 8 : -1};
+  if (c >= n) return {t.rd + (c - n) * 8, t.rd + (D - t.rd) / 2 + (c - n) * 8, -1, -1};
+  if (t.interleaved) return {c * 8, t.rd / 2 + c * 8, c * 4, t.rd / 4 + c * 4};
+  return {c * 8, t.rd / 2 + c * 8, c * 8, c * 8 + 4};
 }
 
 template <class T>
@@ -120,27 +122,26 @@ __device__ __forceinline__ void store_raw(T* y, const Task& k, const Raw<T>& r) 
   }
 }
 
-// Cosines and sines of the task's 8 pairs for one row (positions checked before).
-__device__ __forceinline__ void load_cs(const Rot& t, const Batch& b, int64_t r, int64_t j, const Task& k,
-                                        float (&c)[8], float (&s)[8]) {
-  const int64_t p0 = position(t, b, r, j, k.c8), p1 = position(t, b, r, j, k.c8 + 7);
-  if (p0 == p1) {  // 8 pairs of one axis (or of axes at the same position)
-    bool one = true;
-    for (int a = 0; a + 1 < t.n_axes; ++a) one = one && (t.end[a] <= k.c8 || t.end[a] > k.c8 + 7);
-    if (one) {
-      const float4* row = reinterpret_cast<const float4*>(t.cs + p0 * t.rd + k.c8);
-      const float4* rsn = reinterpret_cast<const float4*>(t.cs + p0 * t.rd + t.rd / 2 + k.c8);
-      const float4 c0 = __ldg(row), c1 = __ldg(row + 1), s0 = __ldg(rsn), s1 = __ldg(rsn + 1);
-      c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
-      s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w, s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
-      return;
-    }
-  }
+// Cosines and sines of the task's 8 pairs; pos(f): position on the axis of
+// pair f (positions checked before).
+template <class F>
+__device__ __forceinline__ void load_cs(const Rot& t, const Task& k, F&& pos, float (&c)[8], float (&s)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t q = position(t, b, r, j, k.c8 + i);
-    c[i] = __ldg(t.cs + q * t.rd + k.c8 + i);
-    s[i] = __ldg(t.cs + q * t.rd + t.rd / 2 + k.c8 + i);
+  for (int h = 0; h < 2; ++h) {
+    const int f = h ? k.f1 : k.f0;
+    if (axis_of(t, f) == axis_of(t, f + 3)) {
+      const float* row = t.cs + pos(f) * t.rd + f;
+      const float4 x = __ldg(reinterpret_cast<const float4*>(row)), y = __ldg(reinterpret_cast<const float4*>(row + t.rd / 2));
+      c[4 * h] = x.x, c[4 * h + 1] = x.y, c[4 * h + 2] = x.z, c[4 * h + 3] = x.w;
+      s[4 * h] = y.x, s[4 * h + 1] = y.y, s[4 * h + 2] = y.z, s[4 * h + 3] = y.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* row = t.cs + pos(f + i) * t.rd + f + i;
+        c[4 * h + i] = __ldg(row);
+        s[4 * h + i] = __ldg(row + t.rd / 2);
+      }
+    }
   }
 }
 
@@ -154,17 +155,17 @@ __device__ __forceinline__ void turn16(const Rot& t, float (&x)[16], const float
   }
 }
 
-// The step's token of a row: its index j in the sequence and page row, or ok = false.
+// The token of row r, if it is one of sequence s (ok): its index j in the sequence and its page row.
 struct Token {
   int64_t j;
   int64_t page;
   int32_t off;
   bool ok;
+  int32_t pos[4];  // on each axis
 };
 
-__device__ __forceinline__ Token token_of_row(const DevPool& p, const Batch& b, int64_t r, int& bits) {
-  Token t{0, 0, 0, false};
-  const int32_t s = warp_search(b.n_seqs, r, [&](int32_t i) { return __ldg(b.cu + i); });
+__device__ __forceinline__ Token token_of_row(const DevPool& p, const Batch& b, int32_t s, int64_t r, int& bits) {
+  Token t{};
   const Seq q = seq_of(p, b, s, bits);
   if (r < q.row0 || r - q.row0 >= q.n) return t;
   t.j = q.a + (r - q.row0);
@@ -201,77 +202,126 @@ constexpr int kRowThreads = 64;                       // threads a row
 constexpr int kRowsAtOnce = kAppendBlock / kRowThreads;
 constexpr int kMaxRows = 16;                          // rows a block
 
+constexpr int kStagePieces = 8;                        // pieces of 16 bytes a thread
+constexpr int kStageBytes = kStagePieces * 16 * kAppendBlock;
+constexpr int kAppendStages = 3;
+constexpr int kAppendSmem = kAppendStages * kStageBytes;
+
 // Heads [0, heads) of the list (queries, keys, values) of rows [r0, r0 + rows),
-// 64 threads a row, four rows at a time. Where the rows belong is a chain of four or
-// five dependent loads; the block's warps follow it for all its rows at once,
-// while the first rows' data is already on its way. A lane keeps its task and
-// so its cosines and sines for all heads of a row, U of them in flight.
+// 64 threads a row, four rows at a time. A thread copies the pieces that it
+// will turn into shared memory of its own (cp.async), two batches of heads or groups of
+// rows ahead, so that loads never stop; no barrier is needed for them. Where the rows belong is a
+// chain of four or five dependent loads; one warp follows it, a row a lane,
+// under the first copies.
 template <class T>
 __device__ __forceinline__ void append_rows(const DevPool& p, const Batch& b, const AppendArgs& g, const Rot& t,
-                                            int64_t r0, int rows, int heads, Token* tokens, int& bits) {
+                                            int64_t r0, int rows, int heads, Token* tokens, uint8_t* stage, int& bits) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = threadIdx.x / kRowThreads, lt = threadIdx.x % kRowThreads;
   const int nt = g.D / 16;
   const int groups = kRowThreads / nt;
   const int grp = lt / nt;
-  const Task task = task_of(t, lt - grp * nt);
-  constexpr int U = sizeof(T) == 2 ? 6 : 3;
-  Raw<T> raw[U];
+  const Task task = task_of(t, g.D, lt - grp * nt);
+  constexpr int V = sizeof(T);  // pieces of a task
+  constexpr int U = kStagePieces / V;  // heads a batch
   const int h_lo = grp < groups ? grp : heads;  // lanes left over by the tasks have no head
-  auto load = [&](int64_t r, int h0) {
-    const T* q = static_cast<const T*>(g.q) + r * g.q_stride;
-    const T* kk = static_cast<const T*>(g.k) + r * g.k_stride;
-    const T* vv = static_cast<const T*>(g.v) + r * g.v_stride;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * groups;
-      if (h < heads)
-        raw[u] = load_raw<T>(h < g.Q ? q + h * g.D : h < g.Q + g.H ? kk + (h - g.Q) * g.D : vv + (h - g.Q - g.H) * g.D,
-                             task);
-    }
-  };
-  if (sub < rows && r0 + sub < b.n_rows) load(r0 + sub, h_lo);
-  for (int i = warp; i < rows; i += kAppendBlock / 32) {
-    Token k{0, 0, 0, false};
-    if (r0 + i < b.n_rows) {
-      k = token_of_row(p, b, r0 + i, bits);
-      if (k.ok && !positions_ok(t, b, r0 + i, k.j)) {
-        bits |= KV_DEV_ERR_POSITION;
-        k.ok = false;
-      }
-    }
-    if (lane == 0) tokens[i] = k;
-  }
-  __syncthreads();
-  for (int i = sub; i < rows; i += kRowsAtOnce) {
-    const int64_t r = r0 + i;
-    const Token k = tokens[i];
-    if (!k.ok) continue;
-    float c[8], s[8];
-    if (i != sub) load(r, h_lo);
-    if (task.c8 >= 0) load_cs(t, b, r, k.j, task, c, s);
-    for (int h0 = h_lo; h0 < heads; h0 += groups * U) {
-      if (h0 != h_lo) load(r, h0);
+  const int batches = (heads + groups * U - 1) / (groups * U);
+  const int items = (rows + kRowsAtOnce - 1) / kRowsAtOnce * batches;
+  const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(stage)) + threadIdx.x * 16;
+  auto slot = [&](int item, int u, int v) { return mine + item % kAppendStages * kStageBytes + (u * V + v) * (kAppendBlock * 16); };
+  auto copy = [&](int item) {
+    const int64_t r = r0 + sub + item / batches * kRowsAtOnce;
+    if (item < items && r < b.n_rows && r - r0 < rows) {
+      const T* q = static_cast<const T*>(g.q) + r * g.q_stride;
+      const T* kk = static_cast<const T*>(g.k) + r * g.k_stride;
+      const T* vv = static_cast<const T*>(g.v) + r * g.v_stride;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * groups;
-        if (h >= heads) break;
-        T* y;
-        if (h < g.Q) {
-          y = static_cast<T*>(g.q_out) + (r * g.Q + h) * g.D;
-        } else {
-          if (k.page == 0) break;  // tombstone: not stored (keys and values come after all queries)
-          const int kv = h >= g.Q + g.H;
-          y = pool_row<T>(p, g.layer, kv, k.page, k.off) + (h - g.Q - kv * g.H) * g.D;
+        const int h = h_lo + (item % batches * U + u) * groups;
+        if (h < heads) {
+          const T* x = h < g.Q ? q + h * g.D : h < g.Q + g.H ? kk + (h - g.Q) * g.D : vv + (h - g.Q - g.H) * g.D;
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const T* from = x + (v < V / 2 ? task.a : task.b) + v % (V / 2) * (16 / V);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot(item, u, v)), "l"(from) : "memory");
+          }
         }
-        if (task.c8 >= 0 && h < g.Q + g.H) {
-          float x[16];
-          unpack(raw[u], x);
-          turn16(t, x, c, s);
-          store16(y, task, x);
-        } else {
-          store_raw(y, task, raw[u]);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  copy(0);
+  copy(1);
+  if (warp == 0) {  // a row a lane; the first one's sequence is searched for, the others go on from there
+    int32_t q = warp_search(b.n_seqs, r0, [&](int32_t i) { return __ldg(b.cu + i); });
+    const int64_t r = r0 + lane;
+    if (lane < rows) {
+      Token k{};
+      if (r < b.n_rows) {
+        while (q + 1 < b.n_seqs && r >= __ldg(b.cu + q + 1)) ++q;
+        k = token_of_row(p, b, q, r, bits);
+        if (k.ok && t.rd > 0) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int64_t at = x < t.n_axes && t.pos ? __ldg(t.pos + x * b.n_rows + r) : k.j;
+            if (x < t.n_axes && (at < 0 || at >= t.n_pos)) k.ok = false;
+            k.pos[x] = static_cast<int32_t>(at);
+          }
+          if (!k.ok) bits |= KV_DEV_ERR_POSITION;
         }
+      }
+      tokens[lane] = k;
+    }
+  }
+  __syncthreads();
+  // cosines and sines of this group of rows and of the next
+  float c[8], s[8], c_next[8], s_next[8];
+  auto ask_cs = [&](int i) {
+    if (task.f0 >= 0 && i < rows && tokens[i].ok)
+      load_cs(t, task, [&](int f) -> int64_t { return tokens[i].pos[axis_of(t, f)]; }, c_next, s_next);
+  };
+  ask_cs(sub);
+  for (int item = 0; item < items; ++item) {
+    copy(item + 2);
+    const int i = sub + item / batches * kRowsAtOnce;
+    const bool live = i < rows && tokens[i].ok;
+    if (item % batches == 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        c[e] = c_next[e];
+        s[e] = s_next[e];
+      }
+      ask_cs(i + kRowsAtOnce);
+    }
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+    if (!live) continue;
+    const int64_t r = r0 + i, page = tokens[i].page;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h_lo + (item % batches * U + u) * groups;
+      if (h >= heads) break;
+      T* y;
+      if (h < g.Q) {
+        y = static_cast<T*>(g.q_out) + (r * g.Q + h) * g.D;
+      } else {
+        if (page == 0) break;  // tombstone: not stored (keys and values come after all queries)
+        const int kv = h >= g.Q + g.H;
+        y = pool_row<T>(p, g.layer, kv, page, tokens[i].off) + (h - g.Q - kv * g.H) * g.D;
+      }
+      Raw<T> raw;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(raw.v[v].x), "=r"(raw.v[v].y), "=r"(raw.v[v].z), "=r"(raw.v[v].w)
+                     : "r"(slot(item, u, v))
+                     : "memory");
+      if (task.f0 >= 0 && h < g.Q + g.H) {
+        float x[16];
+        unpack(raw, x);
+        turn16(t, x, c, s);
+        store16(y, task, x);
+      } else {
+        store_raw(y, task, raw);
       }
     }
   }
@@ -280,13 +330,16 @@ __device__ __forceinline__ void append_rows(const DevPool& p, const Batch& b, co
 // Rows a block: sixteen share one chain of lookups where there are blocks enough.
 inline int rows_per_block(int64_t n_rows) { return n_rows >= 4096 ? kMaxRows : kRowsAtOnce; }
 
-// Pools that hold the inputs' own type.
+// Pools that hold the inputs' own type; for 8-bit pools the queries alone
+// (heads = Q), launched over the tail of k_append_e4m3, which it therefore outlasts.
 template <class T>
-__global__ void __launch_bounds__(kAppendBlock, 2) k_append(DevPool p, Batch b, AppendArgs g, Rot t, int rows) {
+__global__ void __launch_bounds__(kAppendBlock, 2) k_append(DevPool p, Batch b, AppendArgs g, Rot t, int rows, int heads) {
+  extern __shared__ __align__(16) uint8_t stage[];
   __shared__ Token tokens[kMaxRows];
   int bits = 0;
-  append_rows<T>(p, b, g, t, static_cast<int64_t>(blockIdx.x) * rows, rows, g.Q + 2 * g.H, tokens, bits);
+  append_rows<T>(p, b, g, t, static_cast<int64_t>(blockIdx.x) * rows, rows, heads, tokens, stage, bits);
   store_bits(p, bits);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // The least 2^e, e >= -60, with amax <= 448 * 2^e (448 = 1.75 * 2^8), amax finite and >= 0.
@@ -318,7 +371,7 @@ __device__ __forceinline__ void append_run_few(const DevPool& p, const Batch& b,
   const int lane = threadIdx.x & 31;
   const int nt = g.D / 16, heads_at_once = 32 / nt;
   const int grp = lane / nt, part = lane - grp * nt;
-  const Task task = task_of(t, part);
+  const Task task = task_of(t, g.D, part);
   const int64_t row_bytes = p.vpr * 16;
   const int64_t stride = kv ? g.v_stride : g.k_stride;
   constexpr int M = sizeof(T) == 2 ? 4 : 2, O = 8;
@@ -342,9 +395,9 @@ __device__ __forceinline__ void append_run_few(const DevPool& p, const Batch& b,
         return false;
       }
       unpack(raw[i], x);
-      if (kv == 0 && task.c8 >= 0) {
+      if (kv == 0 && task.f0 >= 0) {
         float c[8], s[8];
-        load_cs(t, b, r, j, task, c, s);
+        load_cs(t, task, [&](int f) { return position(t, b, r, j, f); }, c, s);
         turn16(t, x, c, s);
       }
       return true;
@@ -421,15 +474,41 @@ __device__ __forceinline__ void append_run_few(const DevPool& p, const Batch& b,
 // runs are read again, from L1 or L2, once the scale is known. The rotation is
 // done twice, for the maximum and for the codes: it is cheaper than the
 // registers that would keep its result.
+// The first tokens' cosines and sines and whether their positions are good lie
+// in shared memory, for all heads of the run.
+constexpr int kRunTokens = 32;
+struct alignas(16) RunTable {
+  float cs[kRunTokens * 256];  // [token][rotary_dim], rotary_dim <= 256
+  uint8_t ok[kRunTokens];
+};
+
+__device__ __forceinline__ void fill_run_table(const Batch& b, const Rot& t, const PageRun& run, RunTable* table) {
+  const int m = run.m < kRunTokens ? run.m : kRunTokens;
+  for (int i = threadIdx.x; i < m; i += kAppendBlock) table->ok[i] = positions_ok(t, b, run.row + i, run.j + i);
+  if (t.rd == 0 || t.rd > 256) return;
+  const int quads = t.rd / 4;
+  for (int x = threadIdx.x; x < m * quads; x += kAppendBlock) {
+    const int i = x / quads, e = x % quads * 4;
+    const int f = e % (t.rd / 2);  // rotary_dim is a multiple of 16 here, so the four are one half's
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t q = position(t, b, run.row + i, run.j + i, f + k);
+      v[k] = q < 0 ? 0.0f : __ldg(t.cs + q * t.rd + e + k);
+    }
+    *reinterpret_cast<float4*>(table->cs + i * t.rd + e) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+
 template <class T>
 __device__ __forceinline__ void append_run(const DevPool& p, const Batch& b, const AppendArgs& g, const Rot& t,
-                                           const PageRun& run, int kvh, int& bits) {
+                                           const PageRun& run, int kvh, const RunTable* table, int& bits) {
   const int lane = threadIdx.x & 31;
   const int nt = g.D / 16;
   const int tpw = 32 / nt;  // tokens a wave
   const int tok = lane / nt;
   const bool in = tok < tpw;
-  const Task task = task_of(t, lane - tok * nt);
+  const Task task = task_of(t, g.D, lane - tok * nt);
   constexpr int W = 4;
   const bool one = run.m <= W * tpw;  // the run fits the registers
   const bool held = run.off > 0;
@@ -448,14 +527,25 @@ __device__ __forceinline__ void append_run(const DevPool& p, const Batch& b, con
   auto values = [&](int i0, int w, float (&x)[16]) -> bool {
     const int i = i0 + w * tpw + tok;
     if (!in || i >= run.m) return false;
-    if (!positions_ok(t, b, run.row + i, run.j + i)) {
+    const bool kept = i < kRunTokens;
+    if (!(kept ? table->ok[i] != 0 : positions_ok(t, b, run.row + i, run.j + i))) {
       bits |= KV_DEV_ERR_POSITION;
       return false;
     }
     unpack(raw[w], x);
-    if (kv == 0 && task.c8 >= 0) {
+    if (kv == 0 && task.f0 >= 0) {
       float c[8], s[8];
-      load_cs(t, b, run.row + i, run.j + i, task, c, s);
+      if (kept && t.rd <= 256) {
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const float* at = table->cs + i * t.rd + (z ? task.f1 : task.f0);
+          const float4 u = *reinterpret_cast<const float4*>(at), v = *reinterpret_cast<const float4*>(at + t.rd / 2);
+          c[4 * z] = u.x, c[4 * z + 1] = u.y, c[4 * z + 2] = u.z, c[4 * z + 3] = u.w;
+          s[4 * z] = v.x, s[4 * z + 1] = v.y, s[4 * z + 2] = v.z, s[4 * z + 3] = v.w;
+        }
+      } else {
+        load_cs(t, task, [&](int f) { return position(t, b, run.row + i, run.j + i, f); }, c, s);
+      }
       turn16(t, x, c, s);
     }
     return true;
@@ -512,22 +602,17 @@ __device__ __forceinline__ void append_run(const DevPool& p, const Batch& b, con
   if (lane == 0) *at = S;
 }
 
-constexpr int kRunsPerBlock = 4;
+// Runs of a few tokens: four a block; longer ones: one, so that there are blocks enough.
+constexpr __host__ __device__ int runs_per_block(bool few) { return few ? 4 : 1; }
 
-// Four runs a block, looked up by a warp each, then shared out by head (or,
-// where runs are a few tokens, by K and V); blocks after the runs' rotate the queries.
+// A block's runs, looked up by a warp each, then shared out by head (or, where
+// runs are a few tokens, by K and V).
 template <class T, bool FEW>
-__global__ void __launch_bounds__(kAppendBlock, 2) k_append_e4m3(DevPool p, Batch b, AppendArgs g, Rot t, int64_t n_runs,
-                                                                 int rows) {
-  __shared__ Token tokens[kMaxRows];
+__global__ void __launch_bounds__(kAppendBlock, 2) k_append_e4m3(DevPool p, Batch b, AppendArgs g, Rot t, int64_t n_runs) {
+  constexpr int kRunsPerBlock = runs_per_block(FEW);
   __shared__ PageRun runs[kRunsPerBlock];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int bits = 0;
-  const int64_t run_blocks = (n_runs + kRunsPerBlock - 1) / kRunsPerBlock;
-  if (blockIdx.x >= run_blocks) {
-    append_rows<T>(p, b, g, t, (blockIdx.x - run_blocks) * rows, rows, g.Q, tokens, bits);
-    store_bits(p, bits);
-    return;
-  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int NW = kAppendBlock / 32;
   if (warp < kRunsPerBlock) {
@@ -542,9 +627,12 @@ __global__ void __launch_bounds__(kAppendBlock, 2) k_append_e4m3(DevPool p, Batc
     static_assert(NW == 2 * kRunsPerBlock);
     if (run.m != 0 && run.page != 0) append_run_few<T>(p, b, g, t, run, warp & 1, bits);
   } else {
-    for (int i = warp; i < kRunsPerBlock * 2 * g.H; i += NW) {
-      const PageRun run = runs[i / (2 * g.H)];
-      if (run.m != 0 && run.page != 0) append_run<T>(p, b, g, t, run, i % (2 * g.H), bits);
+    __shared__ RunTable table;
+    const PageRun run = runs[0];
+    if (run.m != 0 && run.page != 0) {  // (the whole block)
+      fill_run_table(b, t, run, &table);
+      __syncthreads();
+      for (int i = warp; i < 2 * g.H; i += NW) append_run<T>(p, b, g, t, run, i, &table, bits);
     }
   }
   store_bits(p, bits);
@@ -670,15 +758,17 @@ cudaError_t launch(const DevPool& p, const Batch& b, const AppendArgs& g, const 
   } else {
     const int rows = rows_per_block(b.n_rows);
     const int64_t row_blocks = (b.n_rows + rows - 1) / rows;
-    const int64_t run_blocks = (n_runs + kRunsPerBlock - 1) / kRunsPerBlock;
-    if (row_blocks + run_blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const unsigned blocks = grid(run_blocks + (g.Q ? row_blocks : 0));
-    if (!e4m3)
-      k_append<T><<<grid(row_blocks), kAppendBlock, 0, s>>>(p, b, g, t, rows);
-    else if (by_row)
-      k_append_e4m3<T, true><<<blocks, kAppendBlock, 0, s>>>(p, b, g, t, n_runs, rows);
-    else
-      k_append_e4m3<T, false><<<blocks, kAppendBlock, 0, s>>>(p, b, g, t, n_runs, rows);
+    const int64_t run_blocks = (n_runs + runs_per_block(by_row) - 1) / runs_per_block(by_row);
+    if (row_blocks > 0x7fffffff || run_blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    if (!e4m3) {
+      k_append<T><<<grid(row_blocks), kAppendBlock, kAppendSmem, s>>>(p, b, g, t, rows, g.Q + 2 * g.H);
+    } else {
+      auto runs = by_row ? k_append_e4m3<T, true> : k_append_e4m3<T, false>;
+      runs<<<grid(run_blocks), kAppendBlock, 0, s>>>(p, b, g, t, n_runs);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess || g.Q == 0) return e;
+      return launch_overlapped(k_append<T>, dim3(grid(row_blocks)), kAppendBlock, kAppendSmem, s, p, b, g, t, rows, g.Q);
+    }
   }
   return cudaGetLastError();
 }
@@ -755,7 +845,18 @@ __global__ void __launch_bounds__(kAppendBlock) k_gather_scaled(DevPool p, Batch
   }
 }
 
+template <class T>
+cudaError_t prepare_type() {
+  return cudaFuncSetAttribute(k_append<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendSmem);
+}
+
 }  // namespace
+
+cudaError_t prepare_append() {
+  cudaError_t e = prepare_type<__nv_bfloat16>();
+  if (e == cudaSuccess) e = prepare_type<__half>();
+  return e == cudaSuccess ? prepare_type<float>() : e;
+}
 
 cudaError_t launch_append(const DevPool& p, const Batch& b, int32_t layer, int32_t type, bool e4m3, int32_t H,
                           int32_t D, const void* k, int64_t k_stride, const void* v, int64_t v_stride,

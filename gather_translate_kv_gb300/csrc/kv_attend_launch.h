@@ -53,21 +53,4 @@ cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs
 cudaError_t launch_attend_tile(const DevPool& p, const Batch& b, const AttendArgs& a, bool e4m3, int32_t min_new,
                                void* workspace, int sm_count, bool after, Split* w, cudaStream_t s);
 
-// A launch that starts while the kernel before it drains (programmatic dependent launch).
-template <class... A, class... B>
-inline cudaError_t launch_overlapped(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t s,
-                                     const B&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 }  // namespace gtkv

@@ -30,10 +30,28 @@ struct AttendArgs {
   int32_t type;         // KV_TYPE_BF16 or KV_TYPE_F16, of q and out
 };
 
-// Per-device set-up of the attention kernels (their shared-memory limits); called by kv_pool_create.
+// Per-device set-up of the kernels (their shared-memory limits); called by kv_pool_create.
+cudaError_t prepare_append();
 cudaError_t prepare_attend();
 int64_t attend_workspace_bytes(int32_t H, int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int sm_count);
 cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, bool e4m3, void* workspace,
                           int sm_count, cudaStream_t s);
+
+// A launch that starts while the kernel before it drains (programmatic dependent launch).
+template <class... A, class... B>
+inline cudaError_t launch_overlapped(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                                     const B&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 }  // namespace gtkv

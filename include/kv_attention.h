@@ -81,7 +81,8 @@ typedef struct {
 int kv_scale_bytes(const kv_pool_t* pool, int64_t* bytes);
 
 /* Append one layer's new keys and values through the block table, keys
- * rotated on the way, and write the rotated queries, in one launch.
+ * rotated on the way, and write the rotated queries (in one launch; two that
+ * overlap for an 8-bit pool with queries).
  *  type      KV_TYPE_* of k, v, q and q_out. A pool of itemsize 2 or 4 stores
  *            that type (itemsize 2: BF16 or F16; 4: F32); an 8-bit pool
  *            takes any of the three.
