@@ -273,8 +273,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
       const int32_t fc = min(f, g.f0 + g.nf - 1);
       const bool row_ok = f < g.f0 + g.nf;
       const int32_t pos = g.q.a + fc / a.G;
-      const int32_t i0 = g.q.a + (g.f0 + wt * 128) / a.G;
-      const int32_t i1 = g.q.a + min(g.f0 + wt * 128 + 127, g.f0 + g.nf - 1) / a.G;
       float c = c0;
       float ref = kNoRef;
       float2 sum = make_float2(0.0f, 0.0f);
@@ -288,7 +286,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
         const int32_t j0 = g.span.block(i) * kKeys;
         if (kE4M3 && i == g.step0) c = c0 * qscale[(done & 1) * kRows + wt * 128 + r];
         const uint4 live = *reinterpret_cast<const uint4*>(mk.live);
-        const bool cut = j0 + kKeys - 1 > i0 || (a.window && j0 <= i1 - a.window);
+        // by the unit's rows, as the loaders decide it, so that no zeroed value is missed
+        const bool cut = j0 + kKeys - 1 > g.i0 || (a.window && j0 <= g.i1 - a.window);
         const bool dead = (live.x & live.y & live.z & live.w) != 0xffffffffu;
         if (cut || dead) {
           // scores out of sight become -inf in place, so that the steps below need no masks

@@ -213,6 +213,31 @@ def test_what_is_not_seen_changes_nothing(cache, dtype, lengths, fill):
 
 
 @pytest.mark.parametrize("cache,dtype", CACHES[:3])
+@pytest.mark.parametrize("news", [5, 60, 300, 700])
+@pytest.mark.parametrize("window", [0, 90])
+def test_a_value_that_is_not_finite_reaches_every_row_that_sees_it(cache, dtype, news, window):
+    """One element of one value: NaN in that element of the rows that see it, and nowhere else."""
+    n, group = news + 20, 1
+    w = ref.world(13, [n], [news], cache=cache)
+    q = torch.randn(w.n_rows, group * w.H, w.D, generator=torch.Generator().manual_seed(3)).to(T[dtype])
+    clean = Dev(w).attend(1, q.cuda(), 0.125, window=window)
+    for at in (n - 1, n - news, n - news // 2, 7):
+        bad = ref.World(**{**w.__dict__, "raw": w.raw.clone()})
+        pg, off = ref.page_of(w, 0, at), at % w.ps
+        if cache == "e4m3":
+            bad.view().view(torch.uint8)[pg, 1, 1, off, 0, 9] = 0x7F
+        else:
+            bad.view()[pg, 1, 1, off, 0, 9] = float("nan")
+        out = Dev(bad).attend(1, q.cuda(), 0.125, window=window)
+        pos = torch.arange(news) + n - news
+        sees = (pos >= at) & ((window == 0) | (pos - at < window))
+        want = torch.zeros(out.shape, dtype=torch.bool)
+        want[:news, 0, 9] = sees
+        assert torch.equal(out.isnan().cpu(), want)
+        assert torch.equal(out[:news][~sees], clean[:news][~sees])
+
+
+@pytest.mark.parametrize("cache,dtype", CACHES[:3])
 @pytest.mark.parametrize("news", [3, 40, 150])
 def test_a_later_token_does_not_change_an_earlier_row(cache, dtype, news):
     """A NaN or infinite key or value of one of the new tokens reaches only the rows that see it."""
