@@ -83,7 +83,6 @@ struct Segment {
   int32_t i0, i1;  // positions of the first and the last
 };
 
-template <bool kE4M3>
 struct TileWalk {
   const DevPool& p;
   const Batch& b;
@@ -227,7 +226,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  TileWalk<kE4M3> walk{p, b, a, w, 0, {}};
+  TileWalk walk{p, b, a, w, 0, {}};
   const int64_t share = find_shares<kTileThreads, 1>(b.n_seqs, blockIdx.x, w.n_workers, w.min_share, loc, tmp,
                                                      [&](int32_t s) -> int64_t {
                                                        int err = 0;
