@@ -327,9 +327,17 @@ __device__ __forceinline__ void append_rows(const DevPool& p, const Batch& b, co
   }
 }
 
-// Rows a block: sixteen share one chain of lookups where there are blocks enough.
-inline int rows_per_block(int64_t n_rows) { return n_rows >= 4096 ? kMaxRows : kRowsAtOnce; }
+// Rows a block: as few as let all blocks be resident at once, two on each of
+// 152 SMs, and at most sixteen, which then share one chain of lookups. 8 KV
+// and 32 query heads of 128 in bf16, 4 / 8 / 16 rows: 9.7 / 10.9 / 15.5 us at
+// 400 rows, 13.7 / 13.0 / 15.4 at 1600, 42.0 / 36.2 / 40.0 at 6400, 171 / - / 134 at 32768.
+inline int rows_per_block(int64_t n_rows) {
+  constexpr int64_t kResident = 2 * 152;
+  return n_rows <= kResident * kRowsAtOnce ? kRowsAtOnce : n_rows <= kResident * 2 * kRowsAtOnce ? 2 * kRowsAtOnce : kMaxRows;
+}
 
+// Measured (16 sequences of 2048 tokens, three axes, 806 MB): 131 us, 90 % of the copy rate; 256
+// decode tokens 7.4 us, launch and lookups.
 // Pools that hold the inputs' own type; for 8-bit pools the queries alone
 // (heads = Q), launched over the tail of k_append_e4m3, which it therefore outlasts.
 template <class T>
@@ -602,7 +610,8 @@ __device__ __forceinline__ void append_run(const DevPool& p, const Batch& b, con
   if (lane == 0) *at = S;
 }
 
-// Runs of a few tokens: four a block; longer ones: one, so that there are blocks enough.
+// Runs of a few tokens: four a block; longer ones: one, so that there are blocks enough. 512 decode
+// tokens of eight 64-element heads: 22 us with four and the few-token form, 31 us page by page.
 constexpr __host__ __device__ int runs_per_block(bool few) { return few ? 4 : 1; }
 
 // A block's runs, looked up by a warp each, then shared out by head (or, where
@@ -775,7 +784,8 @@ cudaError_t launch(const DevPool& p, const Batch& b, const AppendArgs& g, const 
 
 // Scaled gather: a block per page run, K and then V, 16 codes a thread and
 // step. A run's rows are consecutive in the pool and in the output, so both sides are whole
-// streams; four loads are in flight before any store.
+// streams; four loads are in flight before any store. Measured: 284 us for 1.81 GB of whole sequences (94 % of the copy
+// rate), 44 us for 201 MB of 128-token windows, whose blocks wait longer on their lookups than on their rows.
 template <class T>
 __global__ void __launch_bounds__(kAppendBlock) k_gather_scaled(DevPool p, Batch b, const float* __restrict__ scales,
                                                                 int32_t layer, int32_t H, int32_t D, T* out_k,

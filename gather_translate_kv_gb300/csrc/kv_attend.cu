@@ -67,14 +67,19 @@ int64_t attend_workspace_bytes(int32_t, int32_t, int32_t D, int32_t, int64_t, in
 }
 
 // Which kernels: the few-rows kernel alone when the sequences' rows of a KV
-// head number at most 16 on average (decode steps and drafts; a longer sequence among
-// them takes several row tiles there), else both, each taking the sequences on its side of 16
-// rows. Lengths are known on the device alone, so the rule goes by averages.
+// head number at most 16 (8-bit caches: 32) on average (decode steps and
+// drafts; a longer sequence among them takes several row tiles there), else both, each taking the
+// sequences on its side of that. Lengths are known on the device alone, so the
+// rule goes by averages. 32 sequences of 4000 tokens, 4 query heads a KV head,
+// D = 128, few-rows against tile kernel: 16-bit 109 / 127 us at 8 rows, 137 /
+// 129 at 16, 205 / 135 at 32; 8-bit, whose codes the tile kernel is slow to
+// turn into fp16, 83 / 184 at 16, 137 / 191 at 32, 247 / 196 at 64.
 cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, bool e4m3, void* workspace,
                           int sm_count, cudaStream_t s) {
   if (!has_tiles(a.D)) return launch_rows(p, b, a, e4m3, s);
-  const bool only_few = b.n_rows * a.G <= 16 * static_cast<int64_t>(b.n_seqs);
-  const int32_t limit = only_few ? 0x7fffffff : 16 / a.G;
+  const int32_t few_rows = e4m3 ? 32 : 16;
+  const bool only_few = b.n_rows * a.G <= few_rows * static_cast<int64_t>(b.n_seqs);
+  const int32_t limit = only_few ? 0x7fffffff : few_rows / a.G;
   Split few{}, tile{};
   cudaError_t e = cudaSuccess;
   if (limit > 0) e = launch_attend_few(p, b, a, e4m3, limit, workspace, sm_count, &few, s);
