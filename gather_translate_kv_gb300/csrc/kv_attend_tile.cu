@@ -33,9 +33,10 @@
 // 57 % of them the tensor pipe's, the rest the chain from scores through
 // weights to the second product, and a unit ~8 us more for its queries and
 // output. The softmax warps are at the limit of 128 registers a thread. 4
-// chunks of ~1000 tokens on 6001 to 8190 (8-bit) 555 us: there the four loader
-// warps bound it, ~5800 cycles a step; seven of them took a third longer, for
-// they take issue slots from the softmax warps.
+// chunks of ~1000 tokens on 6001 to 8190 (8-bit) 555 us: there a step
+// takes ~5800 cycles, as long as the four loader warps need for their lookups, copies and
+// turned codes. Three more warps, sharing rounds of rows or taking the values
+// alone, made it slower (630 against 945 us, 4 x 1000 tokens on 8000), idle ones did not (647).
 #include "kv_attend_split.cuh"
 #include "kv_umma.cuh"
 
