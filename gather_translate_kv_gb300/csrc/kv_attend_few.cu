@@ -25,8 +25,8 @@
 // bound. Queries for 8-bit caches are fp16 after a power-of-two scaling per row, exact for all
 // bits that matter (2^-29 of the row's largest).
 //
-// Measured: 256 sequences of 4096 tokens (bf16, 8 KV heads of 128, 4.3 GB) 688
-// us, 92 % of the copy rate; 40 sequences of 9 to 40 961 tokens with drafts
+// Measured: 256 sequences of 4096 tokens (bf16, 8 KV heads of 128, 4.3 GB) 696
+// us, 91 % of the copy rate; 40 sequences of 9 to 40 961 tokens with drafts
 // (8-bit, 1.68 GB) 362 us, 68 %, bound by the instructions that turn codes into
 // fp16; one sequence of 203 tokens 14 us, latency.
 //

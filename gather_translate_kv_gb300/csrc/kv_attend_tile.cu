@@ -29,11 +29,11 @@
 // Work is cut as in kv_attend_split.cuh, 128 keys a step.
 //
 // Measured: 16 prompts of 2048 tokens (bf16, 8 KV and 32 query heads of 128,
-// 550 GFLOP) 697 us, 42 % of the measured cuBLAS burst: a step of both tiles takes ~3600 cycles,
+// 550 GFLOP) 698 us, 42 % of the measured cuBLAS burst: a step of both tiles takes ~3600 cycles,
 // 57 % of them the tensor pipe's, the rest the chain from scores through
 // weights to the second product, and a unit ~8 us more for its queries and
 // output. The softmax warps are at the limit of 128 registers a thread. 4
-// chunks of ~1000 tokens on 6001 to 8190 (8-bit) 555 us: there a step
+// chunks of ~1000 tokens on 6001 to 8190 (8-bit) 556 us: there a step
 // takes ~5800 cycles, as long as the four loader warps need for their lookups, copies and
 // turned codes. Three more warps, sharing rounds of rows or taking the values
 // alone, made it slower (630 against 945 us, 4 x 1000 tokens on 8000), idle ones did not (647).
