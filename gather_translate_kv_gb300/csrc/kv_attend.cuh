@@ -29,6 +29,12 @@ __device__ __forceinline__ bool in_sight(const AttendArgs& a, int64_t i, int64_t
   return j <= i && (a.window == 0 || i - j < a.window || j < a.sinks);
 }
 
+// Does some row at positions from i0 on, past token `j`, see one of tokens [j, last]? (tombstones apart)
+// Entries of other tokens are not looked up: a window that has moved on leaves them stale.
+__device__ __forceinline__ bool some_row_sees(const AttendArgs& a, int64_t i0, int64_t j, int64_t last) {
+  return a.window == 0 || i0 - last < a.window || j < a.sinks;
+}
+
 __device__ __forceinline__ float load_q(const AttendArgs& a, const void* q, int64_t i) {
   return a.type == KV_TYPE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(q)[i])
                                 : __half2float(static_cast<const __half*>(q)[i]);

@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
     };
     auto entry_of_key = [&](int32_t i) -> int32_t {  // general: table entry of key `lane % 16` of step i
       const int64_t j = static_cast<int64_t>(span.block(i < end ? i : step0)) * 16 + (lane & 15);
-      return i < end && j <= i1 ? __ldg(b.table + static_cast<int64_t>(s) * b.max_pages + div_ps(p, j)) : 0;
+      return i < end && j <= i1 && some_row_sees(a, i0, j, j) ? __ldg(b.table + static_cast<int64_t>(s) * b.max_pages + div_ps(p, j)) : 0;
     };
     int32_t seg_base = step0;  // P16: `ent` covers steps [seg_base, seg_base + 32)
     int32_t ent_next = 0;

@@ -553,7 +553,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
     auto entry = [&](int32_t i) -> int32_t {
       if (i >= g.end) return 0;
       const int64_t j = static_cast<int64_t>(g.span.block(i)) * kKeys + lw * 32 + lane;
-      if (j > g.i1) return 0;
+      // (keys that share the scales of 16 share their page too, so all of them are looked up or none)
+      constexpr int64_t kShared = kE4M3 && P16 ? 15 : 0;
+      if (j > g.i1 || !some_row_sees(a, g.i0, j & ~kShared, j | kShared)) return 0;
       return __ldg(b.table + static_cast<int64_t>(g.s) * b.max_pages + div_ps(p, j));
     };
     struct Keys {
