@@ -272,6 +272,10 @@ __device__ __forceinline__ void append_rows(const DevPool& p, const Batch& b, co
       }
       tokens[lane] = k;
     }
+  } else {
+    constexpr int kSpare = kAppendBlock - 32;
+    check_seqs(p, b, static_cast<int64_t>(blockIdx.x) * kSpare + threadIdx.x - 32,
+               static_cast<int64_t>(gridDim.x) * kSpare, bits);
   }
   __syncthreads();
   // cosines and sines of this group of rows and of the next
@@ -632,6 +636,10 @@ __global__ void __launch_bounds__(kAppendBlock, 2) k_append_e4m3(DevPool p, Batc
     PageRun run{0, 0, 0, 0, 0, 0};
     if (c < n_runs) run = page_run(p, b, c, FEW, bits);
     if (lane == 0) runs[warp] = run;
+  } else {
+    constexpr int kSpare = kAppendBlock - 32 * kRunsPerBlock;
+    check_seqs(p, b, static_cast<int64_t>(blockIdx.x) * kSpare + threadIdx.x - 32 * kRunsPerBlock,
+               static_cast<int64_t>(gridDim.x) * kSpare, bits);
   }
   __syncthreads();
   if constexpr (FEW) {
@@ -657,6 +665,8 @@ template <class T, bool E4M3>
 __global__ void __launch_bounds__(kAppendBlock) k_append_any(DevPool p, Batch b, AppendArgs g, Rot t, bool by_row,
                                                              int64_t n_runs) {
   int bits = 0;
+  check_seqs(p, b, static_cast<int64_t>(blockIdx.x) * kAppendBlock + threadIdx.x,
+             static_cast<int64_t>(gridDim.x) * kAppendBlock, bits);
   const int lane = threadIdx.x & 31;
   const int heads = g.Q + 2 * g.H;
   const int half = t.rd / 2;
@@ -794,6 +804,8 @@ __global__ void __launch_bounds__(kAppendBlock) k_gather_scaled(DevPool p, Batch
                                                                 int32_t layer, int32_t H, int32_t D, T* out_k,
                                                                 T* out_v, bool by_row) {
   int bits = 0;
+  check_seqs(p, b, static_cast<int64_t>(blockIdx.x) * kAppendBlock + threadIdx.x,
+             static_cast<int64_t>(gridDim.x) * kAppendBlock, bits);
   const PageRun run = page_run(p, b, blockIdx.x, by_row, bits);
   store_bits(p, bits);
   if (run.m == 0) return;

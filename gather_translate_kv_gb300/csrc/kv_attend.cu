@@ -12,6 +12,8 @@ constexpr int kRowBlock = 128;
 template <class C>
 __global__ void __launch_bounds__(kRowBlock) k_attend_rows(DevPool p, Batch b, AttendArgs a) {
   int bits = 0;
+  check_seqs(p, b, static_cast<int64_t>(blockIdx.x) * kRowBlock + threadIdx.x,
+             static_cast<int64_t>(gridDim.x) * kRowBlock, bits);
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kRowBlock / 32);
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kRowBlock / 32) + (threadIdx.x >> 5); w < b.n_rows * a.Q;
        w += warps) {

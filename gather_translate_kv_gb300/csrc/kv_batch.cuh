@@ -47,6 +47,13 @@ __device__ __forceinline__ Seq seq_of(const DevPool& p, const Batch& b, int32_t 
   return q;
 }
 
+// Raises KV_DEV_ERR_TABLE for every inconsistent sequence. Kernels that find
+// sequences through rows or runs never meet one that owns none of them, so
+// they have spare threads (number `first` of `step` in the grid) look at all.
+__device__ __forceinline__ void check_seqs(const DevPool& p, const Batch& b, int64_t first, int64_t step, int& bits) {
+  for (int64_t s = first; s < b.n_seqs; s += step) seq_of(p, b, static_cast<int32_t>(s), bits);
+}
+
 // Table entry -> physical page, 0 (the sink) for tombstones and bad entries.
 __device__ __forceinline__ int64_t page_of_entry(const DevPool& p, const Batch& b, int32_t e, int& bits) {
   if (e <= 0) return 0;

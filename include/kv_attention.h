@@ -12,7 +12,7 @@
  * written. A sequence whose metadata is inconsistent (seq_start < 0,
  * seq_len > max_pages * page_size, a cu span that is negative, shorter than
  * its tokens, or outside [0, n_rows]) takes no part and sets
- * KV_DEV_ERR_TABLE. Page 0 is the pool's sink and holds no tokens: a
+ * KV_DEV_ERR_TABLE (a batch of no rows is not looked at). Page 0 is the pool's sink and holds no tokens: a
  * table entry that is negative or names page 0 is a tombstone, whose tokens
  * are not stored, not visible to attention, and gathered as zeros. An entry
  * past the pool sets KV_DEV_ERR_ROW, one off the kernel-facing grid

@@ -42,3 +42,128 @@ def test_pages_that_no_row_sees_are_not_read(cache, dtype, lengths, ps, window, 
     w.table[held & ~seen] = 0x7FFFFFF1  # past the pool, and off the kernel-facing grid
     again = check_attend(w, 4, dtype, **kw)
     assert torch.equal(again[rows], clean[rows])
+
+
+# ------------------------------------------------- metadata that is inconsistent
+
+# lens, news of three sequences whose runs are numbered by row, and by page
+BY = {"row": ([40, 70, 33], [1, 1, 1]), "page": ([40, 70, 33], [25, 30, 20])}
+
+
+def broken(kind, by, *, D=64, cache="bf16", seed=1):
+    """A batch with one inconsistent sequence, the World of what is left of it
+    (that sequence without new tokens), and the error bit that it has to set."""
+    lens, news = BY[by]
+    lost = {"no span": 1, "outside": 2, "short span": 0, "start": 1, "len": 1, "backwards": 2}[kind]
+    kept = [0 if s == lost else n for s, n in enumerate(news)]
+    w = ref.world(seed, lens, kept, D=D, cache=cache)
+    d = Dev(w)
+    start = [n - m for n, m in zip(lens, news)]
+    lens = list(lens)
+    if kind in ("short span", "start", "len"):  # its rows are there
+        w.gap[lost] = news[lost]
+    cu = w.cu.tolist()
+    if kind == "short span":
+        start[0] -= 1
+    elif kind == "start":
+        start[1] = -2
+    elif kind == "len":
+        lens[1] = w.table.shape[1] * w.ps + 1
+    elif kind == "outside":  # all rows past the tensors
+        cu[3] = w.n_rows + news[2]
+    elif kind == "backwards":  # the span ends before it begins
+        cu[3] = w.n_rows - 1
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    d.batch = gt.kv_batch(torch.from_numpy(w.table).cuda(), i32(lens), torch.tensor(cu, device="cuda"), w.n_rows,
+                          seq_start=i32(start))
+    return w, d
+
+
+KINDS = ["no span", "outside", "short span", "start", "len", "backwards"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("by", list(BY))
+@pytest.mark.parametrize("D", [64, 24])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_append_reports_an_inconsistent_sequence(kind, by, D, cache):
+    """KV_DEV_ERR_TABLE is set, nothing of that sequence is written, and the others are stored."""
+    w, d = broken(kind, by, D=D, cache=cache)
+    g = torch.Generator().manual_seed(2)
+    k, v, q = (torch.randn(w.n_rows, w.H, D, generator=g).to(torch.bfloat16) for _ in range(3))
+    q_out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    gt.kv_append_layer(d.pool, 1, d.batch, k.cuda(), v.cuda(), q=q.cuda(), q_out=q_out, scales=d.scales)
+    assert d.error() == gt.KV_DEV_ERR_TABLE
+    raw, scales = ref.append(w, 1, k, v, None)
+    assert torch.equal(d.raw.cpu(), raw)
+    if scales is not None:
+        assert torch.equal(d.scales.cpu(), scales)
+    want = torch.full(q.shape, 7.0, dtype=torch.bfloat16)
+    for r, _, _ in w.rows():
+        want[r] = q[r]
+    assert torch.equal(q_out.cpu(), want)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("by", list(BY))
+def test_scaled_gather_reports_an_inconsistent_sequence(kind, by):
+    w, d = broken(kind, by, cache="e4m3")
+    outs = [torch.full((w.n_rows, w.H, w.D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    gt.kv_gather_layer_scaled(d.pool, 1, d.batch, d.scales, *outs)
+    assert d.error() == gt.KV_DEV_ERR_TABLE
+    val = w.values()
+    for which in (0, 1):
+        want = torch.full(outs[0].shape, 7.0, dtype=torch.bfloat16)
+        for r, s, j in w.rows():
+            want[r] = val[ref.page_of(w, s, j), 1, which, j % w.ps].to(torch.bfloat16)
+        assert torch.equal(outs[which].cpu(), want)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("by", list(BY))
+@pytest.mark.parametrize("D", [64, 80])
+def test_attention_reports_an_inconsistent_sequence(kind, by, D):
+    w, d = broken(kind, by, D=D)
+    q = torch.randn(w.n_rows, 4, D, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    out = d.attend(1, q.cuda(), 0.125).cpu().double()
+    assert d.error() == gt.KV_DEV_ERR_TABLE
+    want, _, size = ref.attend(w, 1, q, 0.125)
+    rows = [r for r, _, _ in w.rows()]
+    rest = sorted(set(range(w.n_rows)) - set(rows))
+    assert (out[rest] == 7.0).all()
+    u = 2.0 ** -8
+    assert ((out - want).abs() <= u * want.abs() + (u + 2.0 ** -12) * size)[rows].all()
+
+
+@pytest.mark.parametrize("by", list(BY))
+@pytest.mark.parametrize("D", [64, 24])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("entry", ["past the pool", "off the grid"])
+def test_append_and_gather_report_bad_entries(by, D, cache, entry):
+    """A bad entry counts as a tombstone: its tokens alone are not stored, and are read as zeros."""
+    lens, news = BY[by]
+    w = ref.world(3, lens, news, D=D, cache=cache)
+    kf = entry == "off the grid"
+    d = Dev(w, kernel_facing=kf)
+    page = (lens[1] - 1) // w.ps
+    d.batch.tensors[0][1, page] = int(w.table[1, page]) * 2 * w.L + 1 if kf else w.P
+    bit = gt.KV_DEV_ERR_FORM if kf else gt.KV_DEV_ERR_ROW
+    w.table[1, page] = 0
+    g = torch.Generator().manual_seed(2)
+    k, v = (torch.randn(w.n_rows, w.H, D, generator=g).to(torch.bfloat16) for _ in range(2))
+    gt.kv_append_layer(d.pool, 1, d.batch, k.cuda(), v.cuda(), scales=d.scales)
+    assert d.error() == bit
+    raw, scales = ref.append(w, 1, k, v, None)
+    assert torch.equal(d.raw.cpu(), raw)
+    if cache != "e4m3":
+        return
+    assert torch.equal(d.scales.cpu(), scales)
+    outs = [torch.full(k.shape, 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    gt.kv_gather_layer_scaled(d.pool, 1, d.batch, d.scales, *outs)
+    assert d.error() == bit
+    val = w.values(raw, scales)
+    for which in (0, 1):
+        for r, s, j in w.rows():
+            pg = ref.page_of(w, s, j)
+            want = val[pg, 1, which, j % w.ps] if pg else torch.zeros(w.H, D, dtype=torch.float64)
+            assert torch.equal(outs[which][r].cpu(), want.to(torch.bfloat16))
