@@ -458,14 +458,14 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
           const uint2 kv = lds64(st + 2 * Sh::kK);
           sk[0] = sk[1] = __uint_as_float(kv.x);
           lv[0] = lv[1] = lg2(__uint_as_float(kv.y));
-          iv[0] = iv[1] = __fdividef(1.0f, __uint_as_float(kv.y));
+          iv[0] = iv[1] = rcp(__uint_as_float(kv.y));
         }
 #pragma unroll
         for (int e = 0; e < (P16 ? 0 : 2); ++e) {
           sk[e] = __uint_as_float(lds32(st + 2 * Sh::kK + (g + 8 * e) * 4));
           const float sv = __uint_as_float(lds32(st + 2 * Sh::kK + 64 + (g + 8 * e) * 4));
           lv[e] = lg2(sv);
-          iv[e] = __fdividef(1.0f, sv);
+          iv[e] = rcp(sv);
         }
       }
       const bool mask = live != 0xffffu || j0 + 15 > i0 || (a.window && j0 <= i1 - a.window);
@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
         for (int e = 0; e < 2; ++e) {
           const int col = nt * 8 + 2 * c + e;
           const int32_t f = f0 + col;
-          const float inv = sum[nt][e] == 0.0f ? 0.0f : __fdividef(1.0f, sum[nt][e]);
+          const float inv = sum[nt][e] == 0.0f ? 0.0f : rcp(sum[nt][e]);
           bool bad = !(sum[nt][e] <= 3.402823466e38f);
           const int64_t r = q.row0 + f / a.G;
           const int32_t qh = h * a.G + f % a.G;

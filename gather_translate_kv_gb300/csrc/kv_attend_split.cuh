@@ -153,6 +153,13 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Over the whole range, subnormal results included (a quick division is 0 for
+// divisors past 2^126, which denominators under the smallest scales of 8-bit values reach).
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 __device__ __forceinline__ uint32_t pack_h(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -249,7 +256,7 @@ __device__ __forceinline__ void join_split(const DevPool& p, const Batch& b, con
       }
     }
     if (!shared || warp == 0) {
-      const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+      const float inv = sum == 0.0f ? 0.0f : rcp(sum);
       bool bad = !(sum <= 3.402823466e38f);
       const int32_t f = rec.f0 + col;
       const int64_t r = rec.row0 + f / a.G;

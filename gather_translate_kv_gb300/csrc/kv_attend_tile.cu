@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
       const int32_t qh = g.h * a.G + fc % a.G;
       if (whole) {
         bool bad = !(total <= 3.402823466e38f);
-        const float inv = bad ? NAN : total == 0.0f ? 0.0f : __fdividef(1.0f, total);
+        const float inv = bad ? NAN : total == 0.0f ? 0.0f : rcp(total);
         uint16_t* out = static_cast<uint16_t*>(a.out) + (orow * a.Q + qh) * D;
         const float2 inv2 = make_float2(inv, inv), none = make_float2(0.0f, 0.0f);
         float2 zero = none;  // stays 0 while all values are finite
@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           Scales& sl = scales[n % kSlots];
           sl.ks[lw * 32 + lane] = cur.k.page != 0 ? cur.ks : 1.0f;  // no token: 2^-inf through lv, whatever the score
           sl.lv[lw * 32 + lane] = lg2(cur.vs);
-          sl.iv[lw * 32 + lane] = cur.k.page != 0 ? __fdividef(1.0f, cur.vs) : 0.0f;
+          sl.iv[lw * 32 + lane] = cur.k.page != 0 ? rcp(cur.vs) : 0.0f;
           if (lane == 0) masks[n % kSlots].live[lw] = cur.k.live;
           turn_tile(t, false);
           warp_arrive(full(t));

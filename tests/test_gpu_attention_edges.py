@@ -167,3 +167,17 @@ def test_append_and_gather_report_bad_entries(by, D, cache, entry):
             pg = ref.page_of(w, s, j)
             want = val[pg, 1, which, j % w.ps] if pg else torch.zeros(w.H, D, dtype=torch.float64)
             assert torch.equal(outs[which][r].cpu(), want.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("lengths", ["decode", "chunks", "long"])
+@pytest.mark.parametrize("ps", [16, 24])
+@pytest.mark.parametrize("scale", [2.0 ** -126, 2.0 ** -122, 2.0 ** -118, 2.0 ** -115, 2.0 ** -112, 1.5 * 2.0 ** 126])
+def test_value_scales_at_the_ends_of_their_range(lengths, ps, scale):
+    """Denominators (weights over scales) and 1 / scale near both ends of the 32-bit range."""
+    w = ref.world(19, *LENGTHS[lengths], ps=ps, cache="e4m3")
+    w.scales[:, :, 1] = scale
+    if scale > 1:  # codes of 1, 1/2 and their negatives, so that the values are finite
+        codes = torch.tensor([0x38, 0x30, 0xB8, 0xB0], dtype=torch.uint8)
+        v = w.view().view(torch.uint8)[:, :, 1]
+        v.copy_(codes[(v & 3).long()])
+    check_attend(w, 4, "bf16")
