@@ -19,10 +19,13 @@
 // 2^8 (a vote per step), so the common step has no shuffle. Weights are
 // 2^(t - m), t = score * log2(e) + log2(value scale): the scale of an 8-bit
 // value is part of its weight, so that weights stay in one range, and the
-// denominator adds weight / scale. Weights meet the values as fp16 (11 bits),
-// lifted by 2^6 so that 2^-30 of the largest still counts; for bf16 caches as
-// a sum of two bf16 (16 bits), the second product being free under the memory
-// bound. Queries for 8-bit caches are fp16 after a power-of-two scaling per row, exact for all
+// denominator adds weight / scale. Weights meet the values as the sum of two 16-bit
+// parts and keep 16 bits (bf16) or 22 (fp16, lifted by 2^6 so that 2^-30 of the largest
+// still counts): the result's error is then the output's own rounding and no more, where one part
+// alone adds 40 % to it (fp16 output, 4096 keys, root mean square: 5.39e-6 and 7.54e-6). Under
+// 16-bit caches the second product is free, memory being the bound. Of 8-bit caches read
+// into bf16, whose 8 bits hide the 11 of one fp16 part (8.73e-5 and 8.79e-5), the weights are
+// one part: drafts take 364 us so and 405 with two. Queries for 8-bit caches are fp16 after a power-of-two scaling per row, exact for all
 // bits that matter (2^-29 of the row's largest).
 //
 // Measured: 256 sequences of 4096 tokens (bf16, 8 KV heads of 128, 4.3 GB) 696
@@ -47,19 +50,16 @@ constexpr int kUnitCost = 2;  // steps' worth of a unit's queries and output
 template <class C>
 struct FewType {
   static constexpr int kSize = 2;       // bytes per cached element
-  static constexpr bool kSplitP = false;
   static constexpr float kLift = 6.0f;  // log2 of the weights' lift
 };
 template <>
 struct FewType<CodeE4M3> {
   static constexpr int kSize = 1;
-  static constexpr bool kSplitP = false;
   static constexpr float kLift = 6.0f;
 };
 template <>
 struct FewType<__nv_bfloat16> {
   static constexpr int kSize = 2;
-  static constexpr bool kSplitP = true;
   static constexpr float kLift = 0.0f;
 };
 
@@ -133,7 +133,8 @@ struct FewShape {
 // Resident blocks: shared memory for 256-byte rows, registers for 16 columns allow three.
 constexpr int few_blocks(int row, int nt) { return row >= 256 || nt > 1 ? 3 : kFewBlocksPerSM; }
 
-template <class C, int D, int NT, bool P16>
+// TWO: weights in two parts.
+template <class C, int D, int NT, bool P16, bool TWO>
 __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT))
     k_attend_few(DevPool p, Batch b, AttendArgs a, Split w) {
   using Sh = FewShape<C, D>;
@@ -529,13 +530,12 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          if constexpr (FewType<C>::kSplitP) {
-            const float h0 = __bfloat162float(__float2bfloat16_rn(y[2 * e]));
-            const float h1 = __bfloat162float(__float2bfloat16_rn(y[2 * e + 1]));
-            pb[nt][e] = transpose8(pack_b(h0, h1));
-            pl[nt][e] = transpose8(pack_b(y[2 * e] - h0, y[2 * e + 1] - h1));
-          } else {
-            pb[nt][e] = transpose8(pack_h(y[2 * e], y[2 * e + 1]));
+          constexpr bool kBf16 = std::is_same_v<C, __nv_bfloat16>;
+          const uint32_t hi = pack16<kBf16>(y[2 * e], y[2 * e + 1]);
+          pb[nt][e] = transpose8(hi);
+          if constexpr (TWO) {
+            const float2 h = unpack16<kBf16>(hi);
+            pl[nt][e] = transpose8(pack16<kBf16>(y[2 * e] - h.x, y[2 * e + 1] - h.y));
           }
         }
       }
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mma<C>(o[mt][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-          if constexpr (FewType<C>::kSplitP) mma<C>(o[mt][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+          if constexpr (TWO) mma<C>(o[mt][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
         }
       };
       constexpr int VC = Sh::kVC;
@@ -698,7 +698,10 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
 template <class C, int D, int NT>
 cudaError_t launch(const DevPool& p, const Batch& b, const AttendArgs& a, Split w, cudaStream_t s) {
   using Sh = FewShape<C, D>;
-  auto kernel = p.ps % 16 == 0 ? k_attend_few<C, D, NT, true> : k_attend_few<C, D, NT, false>;
+  constexpr bool kOne = std::is_same_v<C, CodeE4M3>;  // one part will do for a bf16 output
+  const bool one = kOne && a.type == KV_TYPE_BF16;
+  auto kernel = p.ps % 16 == 0 ? (one ? k_attend_few<C, D, NT, true, !kOne> : k_attend_few<C, D, NT, true, true>)
+                               : (one ? k_attend_few<C, D, NT, false, !kOne> : k_attend_few<C, D, NT, false, true>);
   kernel<<<w.blocks, kFewBlock, kFewWarps * (w.deep ? Sh::kDeep : Sh::kStages) * Sh::kStage, s>>>(p, b, a, w);
   return cudaGetLastError();
 }
@@ -711,11 +714,13 @@ cudaError_t launch_c(const DevPool& p, const Batch& b, const AttendArgs& a, cons
 
 template <class C, int D, int NT>
 cudaError_t prepare_one() {
-  cudaError_t e = cudaFuncSetAttribute(k_attend_few<C, D, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kFewWarps * FewShape<C, D>::kDeep * FewShape<C, D>::kStage);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_attend_few<C, D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kFewWarps * FewShape<C, D>::kDeep * FewShape<C, D>::kStage);
+  constexpr bool kOne = std::is_same_v<C, CodeE4M3>;
+  cudaError_t e = cudaSuccess;
+  for (auto kernel : {k_attend_few<C, D, NT, true, true>, k_attend_few<C, D, NT, false, true>,
+                      k_attend_few<C, D, NT, true, !kOne>, k_attend_few<C, D, NT, false, !kOne>})
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kFewWarps * FewShape<C, D>::kDeep * FewShape<C, D>::kStage);
   return e;
 }
 

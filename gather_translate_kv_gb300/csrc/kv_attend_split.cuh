@@ -170,6 +170,15 @@ __device__ __forceinline__ uint32_t pack_b(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  return BF16 ? pack_b(lo, hi) : pack_h(lo, hi);
+}
+template <bool BF16>
+__device__ __forceinline__ float2 unpack16(uint32_t w) {
+  return BF16 ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)) : halves(w);
+}
+
 // Joins the partial sums of units that were cut, adding a unit's segments in
 // the workers' order under a running reference. An item is a row of a cut unit; a warp takes one, or,
 // when there are few items (a long context of few rows, cut many times), the

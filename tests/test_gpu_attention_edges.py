@@ -181,3 +181,42 @@ def test_value_scales_at_the_ends_of_their_range(lengths, ps, scale):
         v = w.view().view(torch.uint8)[:, :, 1]
         v.copy_(codes[(v & 3).long()])
     check_attend(w, 4, "bf16")
+
+
+@pytest.mark.parametrize("cache,dtype", [("bf16", "bf16"), ("fp16", "fp16"), ("e4m3", "fp16")])
+@pytest.mark.parametrize("lengths", ["decode", "drafts", "long"])
+@pytest.mark.parametrize("D,ps", [(64, 16), (128, 64), (64, 24)])
+def test_weights_keep_more_than_sixteen_bits(cache, dtype, lengths, D, ps):
+    """Two kinds of keys, a and b, with values 1 and -c: where c balances the
+    two, what is left is small beside the values, and an error that the
+    rounding of the weights leaves is not hidden by the output's own rounding.
+
+    Bounds. Half a unit of the output (2^-8 bf16, 2^-11 fp16) of |out|; the
+    weights meet the values as two 16-bit parts, 2^-16 relative at most; the
+    exponents are sums of 32-bit products of total magnitude below 16, in
+    steps of 16, and leave 2^-16 at most: 2^-15 of the mean of |v|.
+    """
+    w = ref.world(23, *LENGTHS[lengths], D=D, ps=ps, cache=cache)
+    g = torch.Generator().manual_seed(4)
+    kinds = torch.randn(2, w.H, D, generator=g)
+    c = 2.0 ** (torch.arange(D) / (D / 8) - 4.0)  # a factor of 256 in steps of 2^(8 / D)
+    v = w.view()
+    first = torch.arange(w.ps) % 2 == 0
+    pair = torch.stack([torch.ones(D), -c])  # values of the two kinds
+    scale = 1.0
+    if cache == "e4m3":
+        w.scales[:] = 2.0 ** -4
+        scale = 2.0 ** 4
+    for which, x in ((0, kinds), (1, pair[:, None].expand(2, w.H, D))):
+        v[:, :, which] = torch.where(first[:, None, None], x[0] * scale, x[1] * scale).to(v.dtype)
+    d = Dev(w)
+    q = torch.randn(w.n_rows, 4 * w.H, D, generator=g).to(T[dtype])
+    out = d.attend(1, q.cuda(), D ** -0.5).cpu().double()
+    assert d.error() == 0
+    want, _, size = ref.attend(w, 1, q, D ** -0.5)
+    rows = [r for r, _, _ in w.rows()]
+    u = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}[dtype]
+    tol = u * want.abs() + 2.0 ** -15 * size + 2.0 ** -25
+    assert (want.abs() < size / 8)[rows].any()  # some are balanced
+    over = ((out - want).abs() / tol)[rows].max()
+    assert over <= 1, float(over)
