@@ -9,8 +9,8 @@
 // with S_0, S_1, O_0, O_1 filling the 512 columns of tensor memory. The two
 // tiles alternate: while four warps turn S_0 into P_0 the tensor cores work on tile 1
 // and the other way round, which is what bounds the kernel: per 128 keys and
-// tile 4 * 128 * 128 * D operations on the tensor cores against 128 * 128
-// exponentials.
+// tile 4 * 128 * 128 * D operations (6 with weights in two parts) on the tensor cores against
+// 128 * 128 exponentials.
 //
 // Warps 0-3 and 4-7: softmax of tile 0 and 1, one row a thread (no shuffles).
 // Warps 8-11: loaders; they look up the pages, copy keys and values into the
@@ -20,8 +20,14 @@
 // row rather than by a tensor map. Warp 12 issues the products.
 //
 // The running reference m of a row moves only when a tile's maximum exceeds it
-// by 2^8; only then is O read back and scaled. Weights meet the values as the cache's 16-bit type (bf16, or
-// fp16 lifted by 2^6 for fp16 and 8-bit caches); denominators add the 32-bit weights. The scale of
+// by 2^8; only then is O read back and scaled. A first pass over the scores finds that
+// maximum, a second turns them into weights in place. Weights meet the values as two parts of
+// the cache's 16-bit type (bf16, or fp16 lifted by 2^6 for fp16 and 8-bit caches), rounded
+// and what the rounding left, so that the result's error is the output's own rounding: 1.479e-4
+// (root mean square, prompts of 2048 tokens in bf16), as the formula in 32 bits has it, where one part
+// gave 1.903e-4 for 698 us instead of 831. Of 8-bit caches read into bf16, whose 8 bits
+// hide fp16's 11, one part is enough (7.45e-5 and 7.39e-5; 1180 and 1420 us for the same prompts in 8 bits). Denominators
+// add the 32-bit weights. The scale of
 // an 8-bit value is part of its weight, t = score * log2(e) + log2(scale), and
 // the denominator adds weight / scale. Queries for 8-bit caches become fp16
 // after a power-of-two scaling per row.
@@ -29,14 +35,14 @@
 // Work is cut as in kv_attend_split.cuh, 128 keys a step.
 //
 // Measured: 16 prompts of 2048 tokens (bf16, 8 KV and 32 query heads of 128,
-// 550 GFLOP) 698 us, 42 % of the measured cuBLAS burst: a step of both tiles takes ~3600 cycles,
-// 57 % of them the tensor pipe's, the rest the chain from scores through
-// weights to the second product, and a unit ~8 us more for its queries and
-// output. The softmax warps are at the limit of 128 registers a thread. 4
-// chunks of ~1000 tokens on 6001 to 8190 (8-bit) 556 us: there a step
-// takes ~5800 cycles, as long as the four loader warps need for their lookups, copies and
-// turned codes. Three more warps, sharing rounds of rows or taking the values
-// alone, made it slower (630 against 945 us, 4 x 1000 tokens on 8000), idle ones did not (647).
+// 550 GFLOP) 831 us, 35 % of the measured cuBLAS burst; 4 of 8192 tokens 2220 us. From the two, a step of
+// both tiles takes 2.1 us (4390 cycles at 2070 MHz; 48 products of 64 cycles each are
+// 70 % of them), the rest the chain from scores through
+// weights to the second product, and a unit ~13 us more for its queries,
+// masked last step and output. The kernel is at the limit of 128 registers a thread. 4
+// chunks of ~1000 tokens on 6001 to 8190 (8-bit) 530 us; three more loader warps there, sharing rounds of rows or
+// taking the values alone, made an earlier form slower (630 against 945 us, 4 x 1000 tokens on 8000), idle ones
+// did not (647).
 #include "kv_attend_split.cuh"
 #include "kv_umma.cuh"
 
@@ -204,7 +210,8 @@ __device__ __forceinline__ float2 fadd2(float2 x, float2 y) {
 }
 
 // P16: the page size is a multiple of 16, so 16 keys share the scales of an 8-bit cache.
-template <class C, int D, bool P16>
+// TWO: weights in two parts.
+template <class C, int D, bool P16, bool TWO>
 __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batch b, AttendArgs a, Split w) {
   using Sm = TileSmem<C, D>;
   constexpr bool kE4M3 = std::is_same_v<C, CodeE4M3>;
@@ -336,100 +343,40 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           m = make_float2(ks.x * c, ks.y * c);
           o = make_float2(lv.x + off, lv.y + off);
         };
-        if (i == g.step0) {  // the reference starts as the first step's maximum
-          float m = -INFINITY;
-          if constexpr (!kE4M3) {  // the loads' own maximum
+        // the step's largest exponent
+        float m = -INFINITY;
+        if constexpr (!kE4M3) {  // the loads' own maximum
 #pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-              uint32_t x[32];
-              float top;
-              tmem_load32_max(tS + 32 * k, x, top);
-              tmem_wait_ld(x);
-              tmem_tie(x, top);
-              m = fmaxf(m, top);
-            }
-            m *= c;
-          } else {
-#pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-              uint32_t x[32];
-              tmem_load32(tS + 32 * k, x);
-              tmem_wait_ld(x);
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float2 mm, oo;
-                log_scale(32 * k + e, 0.0f, mm, oo);
-                const float2 t = ffma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mm, oo);
-                m = fmaxf(m, fmaxf(t.x, t.y));
-              }
-            }
-          }
-          if (m > -INFINITY) ref = m;
-        }
-        // Weights under the present reference, and the largest exponent on the
-        // way; only when that is more than 8 above the reference (seldom) the
-        // reference moves and the step is done again.
-        uint32_t P[64];
-        for (;;) {
-          const float off = kLift - (ref == kNoRef ? 0.0f : ref);  // (kNoRef itself would swallow the scores)
-          float2 add = make_float2(0.0f, 0.0f);
-          float mx0 = -INFINITY, mx1 = -INFINITY;
-          uint32_t ra[32], rb[32];
-          auto buf = [&](int k) -> uint32_t(&)[32] { return k & 1 ? rb : ra; };
-          tmem_load32(tS, ra);
-          tmem_wait_ld(ra);
-#pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint32_t(&x)[32] = buf(k);
-            if (k < 3) tmem_load32(tS + 32 * (k + 1), buf(k + 1));
-            if constexpr (kE4M3 && P16) {
-              // 16 keys share a page, so their scales
+            uint32_t x[32];
+            float top;
+            tmem_load32_max(tS + 32 * k, x, top);
+            tmem_wait_ld(x);
+            tmem_tie(x, top);
+            m = fmaxf(m, top);
+          }
+          m *= c;
+        } else if constexpr (P16) {
+#pragma unroll 2
+          for (int key = 0; key < kKeys; key += 16)
+            m = fmaxf(m, fmaf(tmem_max16(tS + key), c * sl.ks[key], sl.lv[key]));
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            uint32_t x[32];
+            tmem_load32(tS + 32 * k, x);
+            tmem_wait_ld(x);
 #pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const int key = 32 * k + 16 * z;
-                const float cs = c * sl.ks[key], os = off + sl.lv[key];
-                float2 part = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int e = 8 * z; e < 8 * z + 8; ++e) {
-                  const float2 t = ffma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
-                                         make_float2(cs, cs), make_float2(os, os));
-                  mx0 = fmaxf(mx0, t.x);
-                  mx1 = fmaxf(mx1, t.y);
-                  const float2 y = make_float2(ex2(t.x), ex2(t.y));
-                  part = fadd2(part, y);
-                  P[16 * k + e] = pack_h(y.x, y.y);
-                }
-                add = ffma2(part, make_float2(sl.iv[key], sl.iv[key]), add);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float2 t = make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-                if constexpr (kE4M3) {
-                  float2 mm, oo;
-                  log_scale(32 * k + 2 * e, off, mm, oo);
-                  t = ffma2(t, mm, oo);
-                } else {
-                  t = ffma2(t, make_float2(c, c), make_float2(off, off));
-                }
-                mx0 = fmaxf(mx0, t.x);
-                mx1 = fmaxf(mx1, t.y);
-                const float2 y = make_float2(ex2(t.x), ex2(t.y));
-                if constexpr (kE4M3)
-                  add = ffma2(y, *reinterpret_cast<const float2*>(sl.iv + 32 * k + 2 * e), add);
-                else
-                  add = fadd2(add, y);
-                P[16 * k + e] = kBf16 ? pack_b(y.x, y.y) : pack_h(y.x, y.y);
-              }
+            for (int e = 0; e < 32; e += 2) {
+              float2 mm, oo;
+              log_scale(32 * k + e, 0.0f, mm, oo);
+              const float2 t = ffma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mm, oo);
+              m = fmaxf(m, fmaxf(t.x, t.y));
             }
-            if (k < 3) tmem_wait_ld(buf(k + 1));
           }
-          const float m = fmaxf(mx0, mx1) - off;
-          const bool move = m > ref + 8.0f;
-          if (!__any_sync(kFull, move)) {
-            sum = fadd2(sum, add);
-            break;
-          }
+        }
+        const bool move = m > ref + 8.0f;  // (always so for a row's first keys)
+        if (__any_sync(kFull, move)) {
           const float next = move ? m : ref;
           const float keep = ex2(ref - next);
           ref = next;
@@ -438,16 +385,64 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           if (i > g.step0) {  // the products so far are done: the score product was issued after them
 #pragma unroll 1
             for (int k = 0; k < D / 32; ++k) {
-              tmem_load32(tO + 32 * k, ra);
-              tmem_wait_ld(ra);
+              uint32_t x[32];
+              tmem_load32(tO + 32 * k, x);
+              tmem_wait_ld(x);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) ra[e] = __float_as_uint(__uint_as_float(ra[e]) * keep);
-              tmem_store32(tO + 32 * k, ra);
+              for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * keep);
+              tmem_store32(tO + 32 * k, x);
             }
           }
         }
-        tmem_store32(tS, reinterpret_cast<uint32_t(&)[32]>(P[0]));
-        tmem_store32(tS + 32, reinterpret_cast<uint32_t(&)[32]>(P[32]));
+        // Weights over the scores of their keys: the 16 columns of 16 keys take their 8 words of
+        // rounded weights and, with TWO, 8 words of what the rounding left.
+        const float off = kLift - (ref == kNoRef ? 0.0f : ref);  // (kNoRef itself would swallow the scores)
+        {
+          float2 add = make_float2(0.0f, 0.0f);
+          uint32_t ra[32], rb[32];
+          auto buf = [&](int k) -> uint32_t(&)[32] { return k & 1 ? rb : ra; };
+          tmem_load32(tS, ra);
+          tmem_wait_ld(ra);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t(&x)[32] = buf(k);
+            if (k < 3) tmem_load32(tS + 32 * (k + 1), buf(k + 1));
+            uint32_t P[32];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const int key = 32 * k + 16 * z;
+              float2 ms = make_float2(c, c), os = make_float2(off, off), part = make_float2(0.0f, 0.0f);
+              if constexpr (kE4M3 && P16) {  // 16 keys share a page, so their scales
+                ms.x = ms.y = c * sl.ks[key];
+                os.x = os.y = off + sl.lv[key];
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                if constexpr (kE4M3 && !P16) log_scale(key + 2 * e, off, ms, os);
+                const float2 t = ffma2(make_float2(__uint_as_float(x[16 * z + 2 * e]),
+                                                   __uint_as_float(x[16 * z + 2 * e + 1])), ms, os);
+                const float2 y = make_float2(ex2(t.x), ex2(t.y));
+                if constexpr (kE4M3 && P16)
+                  part = fadd2(part, y);
+                else if constexpr (kE4M3)
+                  add = ffma2(y, *reinterpret_cast<const float2*>(sl.iv + key + 2 * e), add);
+                else
+                  add = fadd2(add, y);
+                const uint32_t hi = pack16<kBf16>(y.x, y.y);
+                P[16 * z + e] = hi;
+                if constexpr (TWO) {
+                  const float2 lo = ffma2(unpack16<kBf16>(hi), make_float2(-1.0f, -1.0f), y);
+                  P[16 * z + 8 + e] = pack16<kBf16>(lo.x, lo.y);
+                }
+              }
+              if constexpr (kE4M3 && P16) add = ffma2(part, make_float2(sl.iv[key], sl.iv[key]), add);
+              if constexpr (!TWO) tmem_store8(tS + key, &P[16 * z]);
+            }
+            if constexpr (TWO) tmem_store32(tS + 32 * k, P);
+            if (k < 3) tmem_wait_ld(buf(k + 1));
+          }
+          sum = fadd2(sum, add);
+        }
         tmem_wait_st();
         tmem_before_sync();
         warp_arrive(bar(Sm::kPReady + wt));
@@ -897,8 +892,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
       auto pv = [&](int wt, uint32_t t, bool add) {
         const uint32_t vd = v0 + slot_of(t) * (Sm::kOperand >> 4);
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          umma_ts(elected, tm + 256 + wt * D, tm + wt * 128 + k * 8, vd + (k * 2048 >> 4), kPV, add || k > 0);
+        for (int k = 0; k < kKeys / 16; ++k) {
+          umma_ts(elected, tm + 256 + wt * D, tm + wt * 128 + k * 16, vd + (k * 2048 >> 4), kPV, add || k > 0);
+          if constexpr (TWO)
+            umma_ts(elected, tm + 256 + wt * D, tm + wt * 128 + k * 16 + 8, vd + (k * 2048 >> 4), kPV, true);
+        }
       };
       auto scores = [&](int wt, uint32_t t, bool first, bool last) {
         if (first) ok = wait(bar(Sm::kQFull + wt), queries[wt]++ & 1);
@@ -969,9 +967,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
   store_bits(p, bits);
 }
 
-template <class C, int D, bool P16>
+template <class C, int D, bool P16, bool TWO>
 cudaError_t prepare_one() {
-  return cudaFuncSetAttribute(k_attend_tile<C, D, P16>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileSmem<C, D>::kBytes);
+  return cudaFuncSetAttribute(k_attend_tile<C, D, P16, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileSmem<C, D>::kBytes);
 }
 
 constexpr int kMinShare = 2;  // steps of 128 keys below which a block's share is not cut
@@ -981,9 +979,12 @@ constexpr int kMinShare = 2;  // steps of 128 keys below which a block's share i
 cudaError_t prepare_attend_tile() {
   cudaError_t e = cudaSuccess;
   for (cudaError_t (*one)() :
-       {prepare_one<CodeE4M3, 64, false>, prepare_one<CodeE4M3, 64, true>, prepare_one<CodeE4M3, 128, false>,
-        prepare_one<CodeE4M3, 128, true>, prepare_one<__half, 64, false>, prepare_one<__half, 128, false>,
-        prepare_one<__nv_bfloat16, 64, false>, prepare_one<__nv_bfloat16, 128, false>})
+       {prepare_one<CodeE4M3, 64, false, false>, prepare_one<CodeE4M3, 64, true, false>,
+        prepare_one<CodeE4M3, 128, false, false>, prepare_one<CodeE4M3, 128, true, false>,
+        prepare_one<CodeE4M3, 64, false, true>, prepare_one<CodeE4M3, 64, true, true>,
+        prepare_one<CodeE4M3, 128, false, true>, prepare_one<CodeE4M3, 128, true, true>,
+        prepare_one<__half, 64, false, true>, prepare_one<__half, 128, false, true>,
+        prepare_one<__nv_bfloat16, 64, false, true>, prepare_one<__nv_bfloat16, 128, false, true>})
     if (e == cudaSuccess) e = one();
   return e;
 }
@@ -1010,15 +1011,19 @@ cudaError_t launch_attend_tile(const DevPool& p, const Batch& b, const AttendArg
   w.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
   w.lift = !e4m3 && a.type == KV_TYPE_BF16 ? 0.0f : 6.0f;
   *out = w;
-  auto go = [&]<class C, bool P16>() {
-    auto kernel = a.D == 64 ? k_attend_tile<C, 64, P16> : k_attend_tile<C, 128, P16>;
+  auto go = [&]<class C, bool P16, bool TWO>() {
+    auto kernel = a.D == 64 ? k_attend_tile<C, 64, P16, TWO> : k_attend_tile<C, 128, P16, TWO>;
     const int smem = a.D == 64 ? TileSmem<C, 64>::kBytes : TileSmem<C, 128>::kBytes;
     if (after) return launch_overlapped(kernel, dim3(w.blocks), kTileThreads, smem, s, p, b, a, w);
     kernel<<<w.blocks, kTileThreads, smem, s>>>(p, b, a, w);
     return cudaGetLastError();
   };
-  if (e4m3) return p.ps % 16 == 0 ? go.template operator()<CodeE4M3, true>() : go.template operator()<CodeE4M3, false>();
-  return a.type == KV_TYPE_BF16 ? go.template operator()<__nv_bfloat16, false>() : go.template operator()<__half, false>();
+  const bool bf16 = a.type == KV_TYPE_BF16;
+  if (!e4m3)
+    return bf16 ? go.template operator()<__nv_bfloat16, false, true>() : go.template operator()<__half, false, true>();
+  if (p.ps % 16 == 0)
+    return bf16 ? go.template operator()<CodeE4M3, true, false>() : go.template operator()<CodeE4M3, true, true>();
+  return bf16 ? go.template operator()<CodeE4M3, false, false>() : go.template operator()<CodeE4M3, false, true>();
 }
 
 }  // namespace gtkv

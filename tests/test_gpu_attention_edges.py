@@ -184,7 +184,7 @@ def test_value_scales_at_the_ends_of_their_range(lengths, ps, scale):
 
 
 @pytest.mark.parametrize("cache,dtype", [("bf16", "bf16"), ("fp16", "fp16"), ("e4m3", "fp16")])
-@pytest.mark.parametrize("lengths", ["decode", "drafts", "long"])
+@pytest.mark.parametrize("lengths", ["decode", "drafts", "long", "chunks", "prompt"])
 @pytest.mark.parametrize("D,ps", [(64, 16), (128, 64), (64, 24)])
 def test_weights_keep_more_than_sixteen_bits(cache, dtype, lengths, D, ps):
     """Two kinds of keys, a and b, with values 1 and -c: where c balances the
