@@ -239,7 +239,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
     for (int i = 0; i < Sm::kBars; ++i) {
       const bool warps4 = i < Sm::kFree || (i >= Sm::kPReady && i < Sm::kODone);  // one arrival a warp
       const bool warps2 = i >= Sm::kQFull && i < Sm::kQFree;
-      mbar_init_n(bar(i), warps4 ? 4 : warps2 ? 2 : 1);
+      const int test = i >= Sm::kPReady && i < Sm::kODone ? GTKV_TEST_EXTRA_ARRIVALS : 0;
+      mbar_init_n(bar(i), (warps4 ? 4 : warps2 ? 2 : 1) + test);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }

@@ -1,8 +1,18 @@
 // 5th-generation tensor core (tcgen05) pieces: descriptors, tensor memory,
 // mbarriers with bounded waits.
+//
+// A wait that runs out ends its block's work: every other wait of the block
+// gives up too, the copies and products in flight are waited for, tensor memory is
+// freed, and KV_DEV_ERR_TIMEOUT goes into the pool's error word.
+// GTKV_TEST_EXTRA_ARRIVALS makes the barriers of finished weights expect that
+// many arrivals more than they get; only the test build that checks this path sets it.
 #pragma once
 
 #include "kv_bulk.cuh"
+
+#ifndef GTKV_TEST_EXTRA_ARRIVALS
+#define GTKV_TEST_EXTRA_ARRIVALS 0
+#endif
 
 namespace gtkv {
 

@@ -127,6 +127,9 @@ int kv_append_layer(const kv_pool_t* pool, int32_t layer, const kv_batch* batch,
  *  scales_dev  the 8-bit pool's scales (positive; any value, not only powers of two), else NULL
  *  workspace_dev  kv_attend_workspace_bytes() bytes, 16-byte aligned, contents
  *            arbitrary; calls that overlap on the GPU need one each
+ * Should a wait inside the kernel for many rows a sequence run out (about a second; not
+ * expected on a healthy GPU), the call sets KV_DEV_ERR_TIMEOUT, ends, and leaves the rows
+ * of sequences with many new tokens unspecified.
  * Sums, maxima and the softmax statistics are held in 32 bits. head_dim is
  * at most 256; 64 and 128 run on the tensor cores. */
 int kv_attend_workspace_bytes(const kv_pool_t* pool, int32_t q_heads, int32_t n_seqs, int64_t n_rows,

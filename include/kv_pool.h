@@ -86,7 +86,8 @@ enum {
                               (its tokens skipped) */
 #define KV_DEV_ERR_TIMEOUT 16 /* gather / move: a load into shared memory did not complete
                                  within its bounded wait (~1 s); that block's remaining rows
-                                 are left untouched. Not expected on a healthy GPU. */
+                                 are left untouched. Not expected on a healthy GPU.
+                                 (attention: see kv_attend_layer) */
 
 typedef struct kv_pool kv_pool_t; /* opaque, host-side, owned by the library */
 
