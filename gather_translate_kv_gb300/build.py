@@ -20,7 +20,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgtkv.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-NVCC_FLAGS = ["-O3", "-std=c++20", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC] + ARCH
+# uncompressed: nvcc would compress the larger units' device code, which costs a process 9 ms at their first use
+NVCC_FLAGS = ["-O3", "-std=c++20", "-lineinfo", "--no-compress", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC] + ARCH
 
 
 def nvcc() -> str:

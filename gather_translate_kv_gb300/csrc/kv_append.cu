@@ -877,10 +877,13 @@ cudaError_t prepare_type() {
 
 }  // namespace
 
-cudaError_t prepare_append() {
-  cudaError_t e = prepare_type<__nv_bfloat16>();
-  if (e == cudaSuccess) e = prepare_type<__half>();
-  return e == cudaSuccess ? prepare_type<float>() : e;
+cudaError_t prepare_append(const kv_pool_desc& d) {
+  cudaError_t e = cudaSuccess;
+  if (d.latent_only || d.head_dim % 16 != 0) return e;  // refused, or k_append_any's
+  if (d.itemsize != 4) e = prepare_type<__nv_bfloat16>();
+  if (d.itemsize != 4 && e == cudaSuccess) e = prepare_type<__half>();
+  if (d.itemsize != 2 && e == cudaSuccess) e = prepare_type<float>();
+  return e;
 }
 
 cudaError_t launch_append(const DevPool& p, const Batch& b, int32_t layer, int32_t type, bool e4m3, int32_t H,

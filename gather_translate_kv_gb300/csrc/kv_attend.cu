@@ -42,9 +42,11 @@ bool has_tiles(int32_t D) { return D == 64 || D == 128; }
 
 }  // namespace
 
-cudaError_t prepare_attend() {
-  const cudaError_t e = prepare_attend_few();
-  return e == cudaSuccess ? prepare_attend_tile() : e;
+cudaError_t prepare_attend(const kv_pool_desc& d) {
+  if (d.latent_only || d.itemsize > 2 || !has_tiles(d.head_dim)) return cudaSuccess;
+  const bool e4m3 = d.itemsize == 1, p16 = d.page_size % 16 == 0;
+  const cudaError_t e = prepare_attend_few(d.head_dim, e4m3, p16);
+  return e == cudaSuccess ? prepare_attend_tile(d.head_dim, e4m3, p16) : e;
 }
 
 namespace {

@@ -713,24 +713,19 @@ cudaError_t launch_c(const DevPool& p, const Batch& b, const AttendArgs& a, cons
 }
 
 template <class C, int D, int NT>
-cudaError_t prepare_one() {
-  constexpr bool kOne = std::is_same_v<C, CodeE4M3>;
-  cudaError_t e = cudaSuccess;
-  for (auto kernel : {k_attend_few<C, D, NT, true, true>, k_attend_few<C, D, NT, false, true>,
-                      k_attend_few<C, D, NT, true, !kOne>, k_attend_few<C, D, NT, false, !kOne>})
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kFewWarps * FewShape<C, D>::kDeep * FewShape<C, D>::kStage);
+cudaError_t prepare_one(bool p16) {
+  constexpr int kBytes = kFewWarps * FewShape<C, D>::kDeep * FewShape<C, D>::kStage;
+  auto set = [](auto kernel) { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes); };
+  cudaError_t e = set(p16 ? k_attend_few<C, D, NT, true, true> : k_attend_few<C, D, NT, false, true>);
+  if constexpr (std::is_same_v<C, CodeE4M3>)
+    if (e == cudaSuccess) e = set(p16 ? k_attend_few<C, D, NT, true, false> : k_attend_few<C, D, NT, false, false>);
   return e;
 }
 
 template <class C>
-cudaError_t prepare_c() {
-  cudaError_t e = prepare_one<C, 64, 1>();
-  if (e == cudaSuccess) e = prepare_one<C, 64, 2>();
-  if (e == cudaSuccess) e = prepare_one<C, 128, 1>();
-  if (e == cudaSuccess) e = prepare_one<C, 128, 2>();
-  return e;
+cudaError_t prepare_c(int32_t D, bool p16) {
+  const cudaError_t e = D == 64 ? prepare_one<C, 64, 1>(p16) : prepare_one<C, 128, 1>(p16);
+  return e != cudaSuccess ? e : D == 64 ? prepare_one<C, 64, 2>(p16) : prepare_one<C, 128, 2>(p16);
 }
 
 constexpr int kWhole = 24;    // steps up to which units are not cut where they fill the GPU; a third of it where they do not
@@ -740,11 +735,10 @@ int heads_of_worker(int32_t H) { return H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1; }
 
 }  // namespace
 
-cudaError_t prepare_attend_few() {
-  cudaError_t e = prepare_c<CodeE4M3>();
-  if (e == cudaSuccess) e = prepare_c<__half>();
-  if (e == cudaSuccess) e = prepare_c<__nv_bfloat16>();
-  return e;
+cudaError_t prepare_attend_few(int32_t D, bool e4m3, bool p16) {
+  if (e4m3) return prepare_c<CodeE4M3>(D, p16);
+  const cudaError_t e = prepare_c<__half>(D, p16);
+  return e == cudaSuccess ? prepare_c<__nv_bfloat16>(D, p16) : e;
 }
 
 int64_t attend_few_workspace(int32_t D, int sm_count) {

@@ -41,9 +41,10 @@ inline int64_t split_record_bytes(int64_t workers) {
   return (workers * static_cast<int64_t>(sizeof(SplitRecord)) + 255) / 256 * 256;
 }
 
-// Shared-memory limits of the kernels on the current device (pool creation).
-cudaError_t prepare_attend_few();
-cudaError_t prepare_attend_tile();
+// Shared-memory limits, on the current device, of the kernels for one kind of pool (p16: its page size is a multiple
+// of 16).
+cudaError_t prepare_attend_few(int32_t D, bool e4m3, bool p16);
+cudaError_t prepare_attend_tile(int32_t D, bool e4m3, bool p16);
 int64_t attend_few_workspace(int32_t D, int sm_count);
 int64_t attend_tile_workspace(int32_t D, int sm_count);
 // Sequences of at most max_new, and of at least min_new, new tokens; *w says

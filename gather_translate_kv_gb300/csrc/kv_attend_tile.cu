@@ -968,26 +968,27 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
   store_bits(p, bits);
 }
 
-template <class C, int D, bool P16, bool TWO>
-cudaError_t prepare_one() {
-  return cudaFuncSetAttribute(k_attend_tile<C, D, P16, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileSmem<C, D>::kBytes);
+template <class C, bool P16, bool TWO>
+cudaError_t prepare_one(int32_t D) {
+  return D == 64 ? cudaFuncSetAttribute(k_attend_tile<C, 64, P16, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        TileSmem<C, 64>::kBytes)
+                 : cudaFuncSetAttribute(k_attend_tile<C, 128, P16, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        TileSmem<C, 128>::kBytes);
 }
 
 constexpr int kMinShare = 2;  // steps of 128 keys below which a block's share is not cut
 
 }  // namespace
 
-cudaError_t prepare_attend_tile() {
-  cudaError_t e = cudaSuccess;
-  for (cudaError_t (*one)() :
-       {prepare_one<CodeE4M3, 64, false, false>, prepare_one<CodeE4M3, 64, true, false>,
-        prepare_one<CodeE4M3, 128, false, false>, prepare_one<CodeE4M3, 128, true, false>,
-        prepare_one<CodeE4M3, 64, false, true>, prepare_one<CodeE4M3, 64, true, true>,
-        prepare_one<CodeE4M3, 128, false, true>, prepare_one<CodeE4M3, 128, true, true>,
-        prepare_one<__half, 64, false, true>, prepare_one<__half, 128, false, true>,
-        prepare_one<__nv_bfloat16, 64, false, true>, prepare_one<__nv_bfloat16, 128, false, true>})
-    if (e == cudaSuccess) e = one();
-  return e;
+cudaError_t prepare_attend_tile(int32_t D, bool e4m3, bool p16) {
+  cudaError_t e;
+  if (!e4m3) {
+    e = prepare_one<__half, false, true>(D);
+    return e == cudaSuccess ? prepare_one<__nv_bfloat16, false, true>(D) : e;
+  }
+  e = p16 ? prepare_one<CodeE4M3, true, false>(D) : prepare_one<CodeE4M3, false, false>(D);
+  if (e != cudaSuccess) return e;
+  return p16 ? prepare_one<CodeE4M3, true, true>(D) : prepare_one<CodeE4M3, false, true>(D);
 }
 
 int64_t attend_tile_workspace(int32_t D, int sm_count) {

@@ -30,9 +30,11 @@ struct AttendArgs {
   int32_t type;         // KV_TYPE_BF16 or KV_TYPE_F16, of q and out
 };
 
-// Per-device set-up of the kernels (their shared-memory limits); called by kv_pool_create.
-cudaError_t prepare_append();
-cudaError_t prepare_attend();
+// Set-up of the kernels on the current device (their shared-memory limits), of those
+// that calls on a pool of this geometry can take (a pool more takes 84 us so, and 106 when
+// all kernels are set up each time). Called by kv_pool_create.
+cudaError_t prepare_append(const kv_pool_desc& d);
+cudaError_t prepare_attend(const kv_pool_desc& d);
 int64_t attend_workspace_bytes(int32_t H, int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int sm_count);
 cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, bool e4m3, void* workspace,
                           int sm_count, cudaStream_t s);

@@ -153,7 +153,8 @@ int kv_pool_required_bytes(const kv_pool_desc* desc, int64_t* total_bytes, int64
  * Additionally requires R % 16 == 0 and anchor_bytes % 16 == 0
  * (KV_ERR_ALIGN): every kernel moves rows as 16-byte vectors.
  * Also allocates the pool's device error word (8 bytes) and raises the
- * shared-memory limits of the gather, append and attention kernels on the current device (a property of
+ * shared-memory limits of the gather kernels and of the append and attention
+ * kernels for this geometry on the current device (a property of
  * the functions, set here so that no later call has to; create pools outside
  * stream capture). Launches no kernel.
  * On success *out receives the handle; on failure *out is set to NULL and

@@ -1,8 +1,12 @@
 """Edges of the operators of kv_attention.h on the GPU: metadata that is
 inconsistent, pages that nobody sees, the ends of the scales' range, the bits
-that weights keep, calls on two streams at once. Plain forms: attention_ref.py.
+that weights keep, pools of one geometry alone, calls on two streams at once. Plain forms: attention_ref.py.
 """
 from __future__ import annotations
+
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -220,3 +224,32 @@ def test_weights_keep_more_than_sixteen_bits(cache, dtype, lengths, D, ps):
     assert (want.abs() < size / 8)[rows].any()  # some are balanced
     over = ((out - want).abs() / tol)[rows].max()
     assert over <= 1, float(over)
+
+
+STEP = """
+import sys, torch
+sys.path[:0] = sys.argv[1:3]
+import attention_ref as ref
+from test_gpu_attention import check_attend, run_append
+D, ps, cache, dtype = int(sys.argv[3]), int(sys.argv[4]), sys.argv[5], sys.argv[6]
+w = ref.world(1, [40, 150], [1, 100], D=D, ps=ps, cache=cache)
+if dtype != "fp32":  # attention takes 16-bit rows
+    check_attend(w, 8, dtype)
+    check_attend(ref.world(2, [40, 150], [1, 2], D=D, ps=ps, cache=cache), 32, dtype)
+run_append(w, 4, dtype, None)
+print("done")
+"""
+
+
+def test_a_pool_prepares_the_kernels_of_its_own_geometry():
+    """A process whose only pool is of one geometry can call everything on it."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    cases = [(D, ps, c, t) for D in (64, 128) for ps in (16, 24) for c, t in (("e4m3", "bf16"), ("e4m3", "fp16"))]
+    cases += [(D, 16, c, c) for D in (64, 128) for c in ("bf16", "fp16", "fp32")] + [(16, 16, "e4m3", "fp32")]
+    for at in range(0, len(cases), 5):
+        run = [(c, subprocess.Popen([sys.executable, "-c", STEP, here, os.path.dirname(here), *map(str, c)],
+                                    stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
+               for c in cases[at:at + 5]]
+        for c, p in run:
+            out, _ = p.communicate(timeout=300)
+            assert p.returncode == 0 and out.endswith("done\n"), (c, out)
