@@ -253,3 +253,55 @@ def test_a_pool_prepares_the_kernels_of_its_own_geometry():
         for c, p in run:
             out, _ = p.communicate(timeout=300)
             assert p.returncode == 0 and out.endswith("done\n"), (c, out)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_two_streams_at_once(cache):
+    """Steps on two streams with pages, tensors and workspaces of their own,
+    nothing awaited in between: the same bits as one after the other."""
+    lens, news = [900, 64, 300, 1300], [1, 40, 300, 3]
+    w = ref.world(29, lens, news, D=128, cache=cache)
+    rot = ref.rotation(1, 128, 2048, w.n_rows)
+    g = torch.Generator().manual_seed(3)
+    rows = [(int(w.cu[s]), int(w.cu[s + 1])) for s in range(4)]
+    x = torch.randn(w.n_rows, 12, 128, generator=g).to(torch.bfloat16).cuda()
+    both = ((0, 1), (2, 3))
+
+    def run(streams):
+        d = Dev(w)
+        r = gt.kv_rotary(rot.table.cuda())
+        parts = []
+        for seqs in both:
+            a, b = rows[seqs[0]][0], rows[seqs[1]][1]
+            n = b - a
+            i32 = lambda y: torch.tensor(y, dtype=torch.int32, device="cuda")  # noqa: E731
+            ls = [w.lens[s] for s in seqs]
+            ns = [w.news[s] for s in seqs]
+            batch = gt.kv_batch(torch.from_numpy(w.table[list(seqs)]).cuda(), i32(ls),
+                                torch.tensor([0, ns[0], n], device="cuda"), n,
+                                seq_start=i32([p - m for p, m in zip(ls, ns)]))
+            ws = torch.empty(gt.kv_attend_workspace_bytes(d.pool, 8, 2, n), dtype=torch.uint8, device="cuda")
+            q, k, v = (y.contiguous() for y in x[a:b].split([8, 2, 2], 1))
+            q_out, out = torch.empty_like(q), torch.empty_like(q)
+            back = [torch.empty(n, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+            parts.append((batch, ws, q, k, v, q_out, out, back))
+        torch.cuda.synchronize()
+        for layer in (0, 1) * 8:
+            for (batch, ws, q, k, v, q_out, out, back), st in zip(parts, streams):
+                gt.kv_append_layer(d.pool, layer, batch, k, v, rotary=r, q=q, q_out=q_out, scales=d.scales, stream=st)
+                gt.kv_attend_layer(d.pool, layer, batch, q_out, out, 0.09, ws, scales=d.scales, stream=st)
+                if cache == "e4m3":
+                    gt.kv_gather_layer_scaled(d.pool, layer, batch, d.scales, *back, stream=st)
+                if streams[0] is streams[1]:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert d.error() == 0
+        done = [t.clone() for p in parts for t in (p[5], p[6], *(p[7] if cache == "e4m3" else ()))]
+        return done + [d.raw] + ([d.scales] if cache == "e4m3" else [])
+
+    one = torch.cuda.Stream()
+    want = run((one, one))
+    for _ in range(3):
+        got = run((torch.cuda.Stream(), torch.cuda.Stream()))
+        for a, b in zip(got, want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
