@@ -8,8 +8,9 @@
  * [seq_start[s], seq_len[s]) are the step's, row cu[s] + j - seq_start[s] of
  * every [n_rows, heads, dim] tensor. It is the gather's metadata
  * (kv_gather_layer), so one batch serves append, attention and gather.
- * Rows of no token (cu spans longer than the tokens) are neither read nor
- * written. A sequence whose metadata is inconsistent (seq_start < 0,
+ * Rows of no token (cu spans longer than the tokens) are not written; they
+ * may be read (append copies rows while it looks up whose they are), and
+ * their contents do not matter. A sequence whose metadata is inconsistent (seq_start < 0,
  * seq_len > max_pages * page_size, a cu span that is negative, shorter than
  * its tokens, or outside [0, n_rows]) takes no part and sets
  * KV_DEV_ERR_TABLE (a batch of no rows is not looked at). Page 0 is the pool's sink and holds no tokens: a
