@@ -331,13 +331,13 @@ __device__ __forceinline__ void append_rows(const DevPool& p, const Batch& b, co
   }
 }
 
-// Rows a block: as few as let all blocks be resident at once, two on each of
-// 152 SMs, and at most sixteen, which then share one chain of lookups. 8 KV
-// and 32 query heads of 128 in bf16, 4 / 8 / 16 rows: 9.7 / 10.9 / 15.5 us at
-// 400 rows, 13.7 / 13.0 / 15.4 at 1600, 42.0 / 36.2 / 40.0 at 6400, 171 / - / 134 at 32768.
-inline int rows_per_block(int64_t n_rows) {
-  constexpr int64_t kResident = 2 * 152;
-  return n_rows <= kResident * kRowsAtOnce ? kRowsAtOnce : n_rows <= kResident * 2 * kRowsAtOnce ? 2 * kRowsAtOnce : kMaxRows;
+// Rows a block: as few as let all blocks be resident at once, two on each
+// SM, and at most sixteen, which then share one chain of lookups. 8 KV
+// and 32 query heads of 128 in bf16, 4 / 8 / 16 rows: 9.5 / 11.5 / 17.1 us at
+// 400 rows, 15.1 / 13.5 / 17.3 at 1600, 42.0 / 35.7 / 39.9 at 6400, 171 / 144 / 135 at 32768.
+inline int rows_per_block(int64_t n_rows, int sm_count) {
+  const int64_t resident = 2 * static_cast<int64_t>(sm_count);
+  return n_rows <= resident * kRowsAtOnce ? kRowsAtOnce : n_rows <= resident * 2 * kRowsAtOnce ? 2 * kRowsAtOnce : kMaxRows;
 }
 
 // Measured (16 sequences of 2048 tokens, three axes, 806 MB): 131 us, 90 % of the copy rate; 256
@@ -764,7 +764,8 @@ bool vec16(const void* x, int64_t stride, size_t size) {
 }
 
 template <class T>
-cudaError_t launch(const DevPool& p, const Batch& b, const AppendArgs& g, const Rot& t, bool e4m3, cudaStream_t s) {
+cudaError_t launch(const DevPool& p, const Batch& b, const AppendArgs& g, const Rot& t, bool e4m3, int sm_count,
+                   cudaStream_t s) {
   const bool by_row = runs_by_row(b, p.ps);
   const int64_t n_runs = run_numbers(b, p.ps, by_row);
   const bool wide = g.D % 16 == 0 && g.D <= 512 && t.rd % 16 == 0 && vec16(g.k, g.k_stride, sizeof(T)) &&
@@ -778,7 +779,7 @@ cudaError_t launch(const DevPool& p, const Batch& b, const AppendArgs& g, const 
     else
       k_append_any<T, false><<<n, kAppendBlock, 0, s>>>(p, b, g, t, by_row, n_runs);
   } else {
-    const int rows = rows_per_block(b.n_rows);
+    const int rows = rows_per_block(b.n_rows, sm_count);
     const int64_t row_blocks = (b.n_rows + rows - 1) / rows;
     const int64_t run_blocks = (n_runs + runs_per_block(by_row) - 1) / runs_per_block(by_row);
     if (row_blocks > 0x7fffffff || run_blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
@@ -889,7 +890,7 @@ cudaError_t prepare_append(const kv_pool_desc& d) {
 cudaError_t launch_append(const DevPool& p, const Batch& b, int32_t layer, int32_t type, bool e4m3, int32_t H,
                           int32_t D, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                           const kv_rotary* rot, const void* q, int64_t q_stride, int32_t Q, void* q_out, float* scales,
-                          cudaStream_t s) {
+                          int sm_count, cudaStream_t s) {
   Rot t{};
   t.n_axes = 1;
   if (rot != nullptr && rot->rotary_dim > 0) {
@@ -904,9 +905,9 @@ cudaError_t launch_append(const DevPool& p, const Batch& b, int32_t layer, int32
   }
   const AppendArgs g{k, v, q, q_out, scales, k_stride, v_stride, q_stride, H, Q, D, layer};
   switch (type) {
-    case KV_TYPE_BF16: return launch<__nv_bfloat16>(p, b, g, t, e4m3, s);
-    case KV_TYPE_F16: return launch<__half>(p, b, g, t, e4m3, s);
-    default: return launch<float>(p, b, g, t, e4m3, s);
+    case KV_TYPE_BF16: return launch<__nv_bfloat16>(p, b, g, t, e4m3, sm_count, s);
+    case KV_TYPE_F16: return launch<__half>(p, b, g, t, e4m3, sm_count, s);
+    default: return launch<float>(p, b, g, t, e4m3, sm_count, s);
   }
 }
 

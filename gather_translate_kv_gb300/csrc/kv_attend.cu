@@ -75,9 +75,10 @@ int64_t attend_workspace_bytes(int32_t, int32_t, int32_t D, int32_t, int64_t, in
 // drafts; a longer sequence among them takes several row tiles there), else both, each taking the
 // sequences on its side of that. Lengths are known on the device alone, so the
 // rule goes by averages. 32 sequences of 4000 tokens, 4 query heads a KV head,
-// D = 128, few-rows against tile kernel: 16-bit 109 / 127 us at 8 rows, 137 /
-// 129 at 16, 205 / 135 at 32; 8-bit, whose codes the tile kernel is slow to
-// turn into fp16, 83 / 184 at 16, 137 / 191 at 32, 247 / 196 at 64.
+// D = 128, few-rows against tile kernel: 16-bit 108 / 150 us at 8 rows, 138 /
+// 152 at 16, 205 / 154 at 24; 8-bit, whose codes the tile kernel is slow to
+// turn into fp16, 83 / 174 at 16, 138 / 183 at 32, 194 / 183 at 48 (fp16 output: 93 / 214 at 16, 151 / 218 at 24,
+// 272 / 226 at 64).
 cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, bool e4m3, void* workspace,
                           int sm_count, cudaStream_t s) {
   if (!has_tiles(a.D)) return launch_rows(p, b, a, e4m3, s);

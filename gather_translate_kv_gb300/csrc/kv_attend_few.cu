@@ -1,5 +1,6 @@
 // Attention of few rows a sequence (decode steps, drafted tokens): at most 16
-// rows, a row being a (token, query head) pair of one KV head. Every key and
+// rows (8-bit caches: 32) on average, a row being a (token, query head) pair of one KV head, in
+// tiles of 8 or 16; a sequence with more takes several tiles. Every key and
 // value is read once and meets a handful of rows, so the bound is memory; the
 // work is laid out so that nothing stands between the loads.
 //
@@ -28,10 +29,10 @@
 // one part: drafts take 364 us so and 405 with two. Queries for 8-bit caches are fp16 after a power-of-two scaling per row, exact for all
 // bits that matter (2^-29 of the row's largest).
 //
-// Measured: 256 sequences of 4096 tokens (bf16, 8 KV heads of 128, 4.3 GB) 696
-// us, 91 % of the copy rate; 40 sequences of 9 to 40 961 tokens with drafts
-// (8-bit, 1.68 GB) 362 us, 68 %, bound by the instructions that turn codes into
-// fp16; one sequence of 203 tokens 14 us, latency.
+// Measured: 256 sequences of 4096 tokens (bf16, 8 KV heads of 128, 4.3 GB) 680 to 698
+// us from one GPU to another, 91 to 93 % of the copy rate; 40 sequences of 9 to 40 961 tokens with drafts
+// (8-bit, 1.68 GB) 364 us, 68 %, bound by latency inside a warp (codes into fp16, products,
+// weights, one after the other) with three warps a scheduler; one sequence of 203 tokens 14 us, latency.
 //
 // Workers (as many warps as share a step's heads) take equal shares of all
 // steps of the batch (kv_attend_split.cuh); units cut at a border are joined by
@@ -128,7 +129,7 @@ struct FewShape {
 
 // P16: the page size is a multiple of 16, so a step's keys share a page and a
 // lane looks up the pages of 32 steps ahead at once; otherwise every key's entry is
-// read on its own, one step ahead. 256 x 4096 tokens in pages of 16, bf16: 686 us against
+// read on its own, one step ahead. 256 x 4096 tokens in pages of 16, bf16, on one GPU: 686 us against
 // 698 by keys; 8-bit, pages of 32: the same within 1 %.
 // Resident blocks: shared memory for 256-byte rows, registers for 16 columns allow three.
 constexpr int few_blocks(int row, int nt) { return row >= 256 || nt > 1 ? 3 : kFewBlocksPerSM; }
@@ -752,8 +753,8 @@ cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs
   w.hw = heads_of_worker(a.H);
   w.max_new = max_new;
   const int kw = kFewWarps / w.hw;
-  // one tile of 8 columns when the sequences' rows of a KV head fit on average, else 16 (4 rows, 256 x 4096 tokens: 686 us
-  // with 8 columns, 803 with 16)
+  // one tile of 8 columns when the sequences' rows of a KV head fit on average, else 16 (4 rows, 256 x 4096 tokens, on one
+  // GPU: 686 us with 8 columns, 803 with 16)
   const int nt = b.n_rows * a.G <= 8 * static_cast<int64_t>(b.n_seqs) ? 1 : 2;
   // steps of one unit at most, and of all units
   int64_t most = static_cast<int64_t>(b.max_pages) * p.ps / 16 + 1;

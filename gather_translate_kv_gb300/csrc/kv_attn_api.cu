@@ -113,7 +113,8 @@ int kv_append_layer(const kv_pool_t* pool, int32_t layer, const kv_batch* batch,
   if (!aligned(k_dev, size) || !aligned(v_dev, size) || !aligned(q_dev, size) || !aligned(q_out_dev, size))
     return KV_ERR_ALIGN;
   return launched(gtkv::launch_append(pool->dev, b, layer, type, it == 1, H, D, k_dev, k_stride, v_dev, v_stride,
-                                      rotary, q_dev, q_stride, q_heads, q_out_dev, scales_dev, as_stream(stream)));
+                                      rotary, q_dev, q_stride, q_heads, q_out_dev, scales_dev, pool->sm_count,
+                                      as_stream(stream)));
 }
 
 int kv_attend_workspace_bytes(const kv_pool_t* pool, int32_t q_heads, int32_t n_seqs, int64_t n_rows,

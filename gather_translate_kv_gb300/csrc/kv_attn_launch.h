@@ -10,7 +10,7 @@ namespace gtkv {
 cudaError_t launch_append(const DevPool& p, const Batch& b, int32_t layer, int32_t type, bool e4m3, int32_t H,
                           int32_t D, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                           const kv_rotary* rot, const void* q, int64_t q_stride, int32_t Q, void* q_out, float* scales,
-                          cudaStream_t s);
+                          int sm_count, cudaStream_t s);
 
 cudaError_t launch_gather_scaled(const DevPool& p, const Batch& b, int32_t layer, int32_t H, int32_t D,
                                  const float* scales, int32_t type, void* out_k, void* out_v, cudaStream_t s);

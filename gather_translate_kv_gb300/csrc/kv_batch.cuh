@@ -103,6 +103,10 @@ struct PageRun {
   int32_t m;     // tokens, 0: empty
 };
 
+// That is at about two tokens a sequence, and so is the crossing of the two forms of the 8-bit append that go with it
+// (k_append_e4m3), by row and by page: 512 sequences, 8 heads of 64, pages of 32, 1 / 2 / 3 / 4 / 7 tokens 24 / 27 / 32 /
+// 44 / 64 and 33 / 33 / 36 / 35 / 61 us; 64 sequences, 8 heads of 128, pages of 16, 20 / 23 / 26 / 28 / 36 and
+// 19 / 21 / 20 / 19 / 25 us.
 inline __host__ __device__ int64_t run_numbers(const Batch& b, int64_t ps, bool by_row) {
   return by_row ? b.n_rows : b.n_rows / ps + 2 * static_cast<int64_t>(b.n_seqs);
 }
