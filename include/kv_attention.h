@@ -123,11 +123,12 @@ int kv_append_layer(const kv_pool_t* pool, int32_t layer, const kv_batch* batch,
  *  type      KV_TYPE_BF16 or KV_TYPE_F16 of q and out; a 16-bit pool holds
  *            the same type, an 8-bit pool takes either.
  *  q_dev     rows of [q_heads, D], q_stride elements from row to row
- *  out_dev   [n_rows, q_heads, D] contiguous
+ *  out_dev   [n_rows, q_heads, D] contiguous, apart from q_dev (rows may be done again from q)
  *  lse_dev   [n_rows, q_heads] float, or NULL
  *  scales_dev  the 8-bit pool's scales (positive; any value, not only powers of two), else NULL
  *  workspace_dev  kv_attend_workspace_bytes() bytes, 16-byte aligned, contents
- *            arbitrary; calls that overlap on the GPU need one each
+ *            arbitrary; calls that overlap on the GPU need one each (its size goes by the
+ *            device and head_dim alone: 81 MB for 128 on 152 SMs)
  * Should a wait inside the kernel for many rows a sequence run out (about a second; not
  * expected on a healthy GPU), the call sets KV_DEV_ERR_TIMEOUT, ends, and leaves the rows
  * of sequences with many new tokens unspecified.
