@@ -32,6 +32,7 @@ STATUS = {
 }
 KV_DEV_ERR_ROW, KV_DEV_ERR_V2P, KV_DEV_ERR_TABLE, KV_DEV_ERR_FORM, KV_DEV_ERR_TIMEOUT = 1, 2, 4, 8, 16
 KV_DEV_ERR_POSITION = 32  # kv_attention.h
+KV_FORMAT_ELEMENTS, KV_FORMAT_E2M1 = 0, 1
 KV_TYPE = {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}
 
 
@@ -53,7 +54,7 @@ class kv_pool_desc(ctypes.Structure):
         ("num_pages", ctypes.c_int64),
         ("anchor_bytes", ctypes.c_int64),
         ("latent_only", ctypes.c_int32),
-        ("reserved", ctypes.c_int32),
+        ("format", ctypes.c_int32),
     ]
 
 
@@ -102,11 +103,12 @@ class kv_rotary_t(ctypes.Structure):
 
 
 def make_desc(layer_num, head_num, head_dim, itemsize, page_size, num_pages, anchor_bytes=0,
-              v_head_dim=None, latent_only=False) -> kv_pool_desc:
+              v_head_dim=None, latent_only=False, format=KV_FORMAT_ELEMENTS) -> kv_pool_desc:
     """Pool geometry; latent_only=True makes an MLA pool (one latent row of
-    head_num * head_dim elements per layer per token, no V)."""
+    head_num * head_dim elements per layer per token, no V); format=KV_FORMAT_E2M1
+    (itemsize 1) one of 4-bit values with a scale for every 16."""
     return kv_pool_desc(layer_num, head_num, head_dim, head_dim if v_head_dim is None else v_head_dim,
-                        itemsize, page_size, num_pages, anchor_bytes, 1 if latent_only else 0, 0)
+                        itemsize, page_size, num_pages, anchor_bytes, 1 if latent_only else 0, format)
 
 
 _lib = None
@@ -586,9 +588,9 @@ def _type(t: torch.Tensor, name: str) -> int:
 
 def _scales(pool: KVPool, scales: torch.Tensor | None, device: int) -> int | None:
     d = pool.desc
-    if d.itemsize != 1:
+    if d.itemsize != 1 or d.format != KV_FORMAT_ELEMENTS:
         if scales is not None:
-            raise ValueError("only pools of itemsize 1 have scales")
+            raise ValueError("only 8-bit pools (itemsize 1) have scales in a tensor of their own")
         return None
     if scales is None:
         raise ValueError("a pool of itemsize 1 needs its scales")
@@ -658,13 +660,13 @@ def kv_attend_layer(pool: KVPool, layer: int, batch: KVBatch, q: torch.Tensor, o
         raise KVError("kv_attend_layer", rc)
 
 
-def kv_gather_layer_scaled(pool: KVPool, layer: int, batch: KVBatch, scales: torch.Tensor, out_k: torch.Tensor,
+def kv_gather_layer_scaled(pool: KVPool, layer: int, batch: KVBatch, scales: torch.Tensor | None, out_k: torch.Tensor,
                            out_v: torch.Tensor, stream=None) -> None:
     """The values (code times scale) of the batch's tokens, one layer's K and V
-    as [n_rows, H, D] of out_k's type."""
+    as [n_rows, H, D] of out_k's type; scales is None for a 4-bit pool."""
     shape, dev = (batch.n_rows, pool.desc.head_num, pool.desc.head_dim), _here()
     if pool.desc.itemsize != 1:
-        raise ValueError("only pools of itemsize 1 have scales")
+        raise ValueError("only pools of itemsize 1 have codes with scales")
     kp, vp = (_whole(t, name, shape, out_k.dtype, dev) for t, name in ((out_k, "out_k"), (out_v, "out_v")))
     rc = (_lib or lib()).kv_gather_layer_scaled(pool.handle, layer, batch.ptr, _scales(pool, scales, dev),
                                                 _type(out_k, "out_k"), kp, vp, _raw_stream(stream, dev))

@@ -12,191 +12,12 @@
 // pairing, 4c .. and rotary_dim / 4 + 4c .. for adjacent pairs), so it needs 8
 // cosines and 8 sines and no other lane's data, and the lanes' chunks follow
 // one another. D / 16 lanes cover a head's row.
-#include "kv_attn_launch.h"
-#include "kv_batch.cuh"
+#include "kv_append.cuh"
+#include "kv_e2m1.cuh"
 
 namespace gtkv {
 
 namespace {
-
-constexpr int kAppendBlock = 256;
-
-struct Rot {
-  const float* cs;
-  const int32_t* pos;
-  int64_t n_pos;
-  int32_t rd;  // rotary_dim, 0: no rotation
-  int32_t interleaved;
-  int32_t n_axes;
-  int32_t end[4];  // first pair past each axis
-};
-
-// Axis of pair f.
-__device__ __forceinline__ int axis_of(const Rot& t, int f) {
-  return (t.n_axes > 1 && f >= t.end[0]) + (t.n_axes > 2 && f >= t.end[1]) + (t.n_axes > 3 && f >= t.end[2]);
-}
-
-// Position of token j (row r) on the axis of pair f; -1 when outside the table.
-__device__ __forceinline__ int64_t position(const Rot& t, const Batch& b, int64_t r, int64_t j, int f) {
-  const int64_t q = t.pos ? __ldg(t.pos + axis_of(t, f) * b.n_rows + r) : j;
-  return q >= 0 && q < t.n_pos ? q : -1;
-}
-
-// Whether every axis' position of the row lies in the table.
-__device__ __forceinline__ bool positions_ok(const Rot& t, const Batch& b, int64_t r, int64_t j) {
-  if (t.rd == 0) return true;
-  if (!t.pos) return j < t.n_pos;
-  for (int a = 0; a < t.n_axes; ++a) {
-    const int64_t q = __ldg(t.pos + a * b.n_rows + r);
-    if (q < 0 || q >= t.n_pos) return false;
-  }
-  return true;
-}
-
-__device__ __forceinline__ void turn(float& x1, float& x2, float c, float s) {
-  const float a = __fsub_rn(__fmul_rn(x1, c), __fmul_rn(x2, s));
-  const float b = __fadd_rn(__fmul_rn(x2, c), __fmul_rn(x1, s));
-  x1 = a;
-  x2 = b;
-}
-
-// ---- a lane's task -----------------------------------------------------------
-
-struct Task {
-  int a, b;    // element offsets of its two chunks in a head
-  int f0, f1;  // first of the first and of the last four of its 8 pairs, -1: not rotated
-};
-
-__device__ __forceinline__ Task task_of(const Rot& t, int D, int c) {
-  const int n = t.rd / 16;
-  if (c >= n) return {t.rd + (c - n) * 8, t.rd + (D - t.rd) / 2 + (c - n) * 8, -1, -1};
-  if (t.interleaved) return {c * 8, t.rd / 2 + c * 8, c * 4, t.rd / 4 + c * 4};
-  return {c * 8, t.rd / 2 + c * 8, c * 8, c * 8 + 4};
-}
-
-template <class T>
-struct Raw {
-  uint4 v[sizeof(T)];  // 16 elements: sizeof(T) vectors of 16 bytes
-};
-
-template <class T>
-__device__ __forceinline__ Raw<T> load_raw(const T* x, const Task& k) {
-  Raw<T> r;
-  constexpr int N = sizeof(T) / 2;  // vectors a chunk
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    r.v[i] = *reinterpret_cast<const uint4*>(x + k.a + i * (16 / sizeof(T)));
-    r.v[N + i] = *reinterpret_cast<const uint4*>(x + k.b + i * (16 / sizeof(T)));
-  }
-  return r;
-}
-
-template <class T>
-__device__ __forceinline__ void unpack(const Raw<T>& r, float (&x)[16]) {
-  const T* e = reinterpret_cast<const T*>(r.v);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = Elem<T>::get(e[i]);
-}
-
-template <class T>
-__device__ __forceinline__ void store16(T* y, const Task& k, const float (&x)[16]) {
-  Raw<T> r;
-  T* e = reinterpret_cast<T*>(r.v);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) e[i] = Elem<T>::put(x[i]);
-  constexpr int N = sizeof(T) / 2;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    *reinterpret_cast<uint4*>(y + k.a + i * (16 / sizeof(T))) = r.v[i];
-    *reinterpret_cast<uint4*>(y + k.b + i * (16 / sizeof(T))) = r.v[N + i];
-  }
-}
-
-template <class T>
-__device__ __forceinline__ void store_raw(T* y, const Task& k, const Raw<T>& r) {
-  constexpr int N = sizeof(T) / 2;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    *reinterpret_cast<uint4*>(y + k.a + i * (16 / sizeof(T))) = r.v[i];
-    *reinterpret_cast<uint4*>(y + k.b + i * (16 / sizeof(T))) = r.v[N + i];
-  }
-}
-
-// Cosines and sines of the task's 8 pairs; pos(f): position on the axis of
-// pair f (positions checked before).
-template <class F>
-__device__ __forceinline__ void load_cs(const Rot& t, const Task& k, F&& pos, float (&c)[8], float (&s)[8]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int f = h ? k.f1 : k.f0;
-    if (axis_of(t, f) == axis_of(t, f + 3)) {
-      const float* row = t.cs + pos(f) * t.rd + f;
-      const float4 x = __ldg(reinterpret_cast<const float4*>(row)), y = __ldg(reinterpret_cast<const float4*>(row + t.rd / 2));
-      c[4 * h] = x.x, c[4 * h + 1] = x.y, c[4 * h + 2] = x.z, c[4 * h + 3] = x.w;
-      s[4 * h] = y.x, s[4 * h + 1] = y.y, s[4 * h + 2] = y.z, s[4 * h + 3] = y.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float* row = t.cs + pos(f + i) * t.rd + f + i;
-        c[4 * h + i] = __ldg(row);
-        s[4 * h + i] = __ldg(row + t.rd / 2);
-      }
-    }
-  }
-}
-
-__device__ __forceinline__ void turn16(const Rot& t, float (&x)[16], const float (&c)[8], const float (&s)[8]) {
-  if (t.interleaved) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) turn(x[2 * i], x[2 * i + 1], c[i], s[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) turn(x[i], x[8 + i], c[i], s[i]);
-  }
-}
-
-// The token of row r, if it is one of sequence s (ok): its index j in the sequence and its page row.
-struct Token {
-  int64_t j;
-  int64_t page;
-  int32_t off;
-  bool ok;
-  int32_t pos[4];  // on each axis
-};
-
-__device__ __forceinline__ Token token_of_row(const DevPool& p, const Batch& b, int32_t s, int64_t r, int& bits) {
-  Token t{};
-  const Seq q = seq_of(p, b, s, bits);
-  if (r < q.row0 || r - q.row0 >= q.n) return t;
-  t.j = q.a + (r - q.row0);
-  const int64_t k = div_ps(p, t.j);
-  t.off = static_cast<int32_t>(t.j - k * p.ps);
-  t.page = page_of_entry(p, b, __ldg(b.table + static_cast<int64_t>(s) * b.max_pages + k), bits);
-  t.ok = true;
-  return t;
-}
-
-struct AppendArgs {
-  const void* k;
-  const void* v;
-  const void* q;
-  void* q_out;
-  float* scales;
-  int64_t k_stride, v_stride, q_stride;  // elements
-  int32_t H, Q, D;
-  int32_t layer;
-};
-
-// First element of (page, offset, K or V, head 0) of the layer in the pool.
-template <class T>
-__device__ __forceinline__ T* pool_row(const DevPool& p, int32_t layer, int kv, int64_t page, int64_t off) {
-  const int64_t row = page * p.stride + (2 * static_cast<int64_t>(layer) + kv) * p.ps + off;
-  return reinterpret_cast<T*>(p.base + row * p.vpr);
-}
-
-__device__ __forceinline__ int64_t scale_at(const DevPool& p, int32_t H, int64_t page, int32_t layer, int kv, int h) {
-  return (page * p.blocks + 2 * layer + kv) * H + h;  // blocks = 2L: [page][layer][K or V][head]
-}
 
 constexpr int kRowThreads = 64;                       // threads a row
 constexpr int kRowsAtOnce = kAppendBlock / kRowThreads;
@@ -207,13 +28,22 @@ constexpr int kStageBytes = kStagePieces * 16 * kAppendBlock;
 constexpr int kAppendStages = 3;
 constexpr int kAppendSmem = kAppendStages * kStageBytes;
 
+__device__ __forceinline__ uint4 lds_vec(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
 // Heads [0, heads) of the list (queries, keys, values) of rows [r0, r0 + rows),
 // 64 threads a row, four rows at a time. A thread copies the pieces that it
 // will turn into shared memory of its own (cp.async), two batches of heads or groups of
 // rows ahead, so that loads never stop; no barrier is needed for them. Where the rows belong is a
 // chain of four or five dependent loads; one warp follows it, a row a lane,
 // under the first copies.
-template <class T>
+// FOUR: the pool holds 4-bit values. A block's 16 elements are the same chunk
+// of two neighbouring lanes, which exchange their largest magnitudes (so
+// rotary_dim and D are multiples of 32).
+template <class T, bool FOUR>
 __device__ __forceinline__ void append_rows(const DevPool& p, const Batch& b, const AppendArgs& g, const Rot& t,
                                             int64_t r0, int rows, int heads, Token* tokens, uint8_t* stage, int& bits) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -303,6 +133,42 @@ __device__ __forceinline__ void append_rows(const DevPool& p, const Batch& b, co
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = h_lo + (item % batches * U + u) * groups;
+      if constexpr (FOUR) {
+        // the lanes of a warp stay together, those without a head among them: neighbours exchange below
+        const bool in = h < heads;
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+        if (in) {
+          Raw<T> raw;
+#pragma unroll
+          for (int v = 0; v < V; ++v) raw.v[v] = lds_vec(slot(item, u, v));
+          unpack(raw, x);
+          if (task.f0 >= 0 && h < g.Q + g.H) turn16(t, x, c, s);
+        }
+        uint32_t top[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top[e >> 3] = max(top[e >> 3], abs_bits(x[e]));
+#pragma unroll
+        for (int z = 0; z < 2; ++z) top[z] = max(top[z], __shfl_xor_sync(kFull, top[z], 1));
+        if (in && h < g.Q) {
+          store16(static_cast<T*>(g.q_out) + (r * g.Q + h) * g.D, task, x);
+        } else if (in && page != 0) {
+          const int kv = h >= g.Q + g.H;
+          const int hh = h - g.Q - kv * g.H;
+          uint8_t* row = pool_row<uint8_t>(p, g.layer, kv, page, tokens[i].off);
+          uint8_t* codes = row + hh * (g.D / 2);
+          uint8_t* bytes = row + code_bytes(g.H, g.D) + hh * (g.D / 16);
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const int at = z ? task.b : task.a;
+            const uint32_t byte = scale_byte(top[z]);
+            *reinterpret_cast<uint32_t*>(codes + at / 2) = encode8(x + 8 * z, scale_inverse(byte));
+            if (at % 16 == 0) bytes[at / 16] = static_cast<uint8_t>(byte);
+          }
+        }
+        continue;
+      }
       if (h >= heads) break;
       T* y;
       if (h < g.Q) {
@@ -314,11 +180,7 @@ __device__ __forceinline__ void append_rows(const DevPool& p, const Batch& b, co
       }
       Raw<T> raw;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(raw.v[v].x), "=r"(raw.v[v].y), "=r"(raw.v[v].z), "=r"(raw.v[v].w)
-                     : "r"(slot(item, u, v))
-                     : "memory");
+      for (int v = 0; v < V; ++v) raw.v[v] = lds_vec(slot(item, u, v));
       if (task.f0 >= 0 && h < g.Q + g.H) {
         float x[16];
         unpack(raw, x);
@@ -344,12 +206,12 @@ inline int rows_per_block(int64_t n_rows, int sm_count) {
 // decode tokens 5.7 us in a CUDA graph, launch and lookups (7.5 us called one by one, at the host's rate).
 // Pools that hold the inputs' own type; for 8-bit pools the queries alone
 // (heads = Q), launched over the tail of k_append_e4m3, which it therefore outlasts.
-template <class T>
+template <class T, bool FOUR>
 __global__ void __launch_bounds__(kAppendBlock, 2) k_append(DevPool p, Batch b, AppendArgs g, Rot t, int rows, int heads) {
   extern __shared__ __align__(16) uint8_t stage[];
   __shared__ Token tokens[kMaxRows];
   int bits = 0;
-  append_rows<T>(p, b, g, t, static_cast<int64_t>(blockIdx.x) * rows, rows, heads, tokens, stage, bits);
+  append_rows<T, FOUR>(p, b, g, t, static_cast<int64_t>(blockIdx.x) * rows, rows, heads, tokens, stage, bits);
   store_bits(p, bits);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -765,15 +627,22 @@ bool vec16(const void* x, int64_t stride, size_t size) {
 }
 
 template <class T>
-cudaError_t launch(const DevPool& p, const Batch& b, const AppendArgs& g, const Rot& t, bool e4m3, int sm_count,
+cudaError_t launch(const DevPool& p, const Batch& b, const AppendArgs& g, const Rot& t, Kind kind, int sm_count,
                    cudaStream_t s) {
+  const bool e4m3 = kind == Kind::kE4M3;
   const bool by_row = runs_by_row(b, p.ps);
   const int64_t n_runs = run_numbers(b, p.ps, by_row);
   const bool wide = g.D % 16 == 0 && g.D <= 512 && t.rd % 16 == 0 && vec16(g.k, g.k_stride, sizeof(T)) &&
                     vec16(g.v, g.v_stride, sizeof(T)) && vec16(t.cs, 0, 4) &&
                     (g.Q == 0 || (vec16(g.q, g.q_stride, sizeof(T)) && vec16(g.q_out, 0, 2)));
   auto grid = [](int64_t n) { return static_cast<unsigned>(n < 1 ? 1 : n > 0x7fffffff ? 0x7fffffff : n); };
-  if (!wide) {
+  if (kind == Kind::kE2M1) {
+    if (!wide || g.D % 32 != 0 || t.rd % 32 != 0) return launch_append4_any<T>(p, b, g, t, by_row, n_runs, s);
+    const int rows = rows_per_block(b.n_rows, sm_count);
+    const int64_t row_blocks = (b.n_rows + rows - 1) / rows;
+    if (row_blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    k_append<T, true><<<grid(row_blocks), kAppendBlock, kAppendSmem, s>>>(p, b, g, t, rows, g.Q + 2 * g.H);
+  } else if (!wide) {
     const unsigned n = grid((n_runs * (g.Q + 2 * g.H) + kAppendBlock / 32 - 1) / (kAppendBlock / 32));
     if (e4m3)
       k_append_any<T, true><<<n, kAppendBlock, 0, s>>>(p, b, g, t, by_row, n_runs);
@@ -785,13 +654,13 @@ cudaError_t launch(const DevPool& p, const Batch& b, const AppendArgs& g, const 
     const int64_t run_blocks = (n_runs + runs_per_block(by_row) - 1) / runs_per_block(by_row);
     if (row_blocks > 0x7fffffff || run_blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     if (!e4m3) {
-      k_append<T><<<grid(row_blocks), kAppendBlock, kAppendSmem, s>>>(p, b, g, t, rows, g.Q + 2 * g.H);
+      k_append<T, false><<<grid(row_blocks), kAppendBlock, kAppendSmem, s>>>(p, b, g, t, rows, g.Q + 2 * g.H);
     } else {
       auto runs = by_row ? k_append_e4m3<T, true> : k_append_e4m3<T, false>;
       runs<<<grid(run_blocks), kAppendBlock, 0, s>>>(p, b, g, t, n_runs);
       const cudaError_t e = cudaGetLastError();
       if (e != cudaSuccess || g.Q == 0) return e;
-      return launch_overlapped(k_append<T>, dim3(grid(row_blocks)), kAppendBlock, kAppendSmem, s, p, b, g, t, rows, g.Q);
+      return launch_overlapped(k_append<T, false>, dim3(grid(row_blocks)), kAppendBlock, kAppendSmem, s, p, b, g, t, rows, g.Q);
     }
   }
   return cudaGetLastError();
@@ -873,8 +742,9 @@ __global__ void __launch_bounds__(kAppendBlock) k_gather_scaled(DevPool p, Batch
 }
 
 template <class T>
-cudaError_t prepare_type() {
-  return cudaFuncSetAttribute(k_append<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendSmem);
+cudaError_t prepare_type(bool four) {
+  return cudaFuncSetAttribute(four ? k_append<T, true> : k_append<T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kAppendSmem);
 }
 
 }  // namespace
@@ -882,13 +752,14 @@ cudaError_t prepare_type() {
 cudaError_t prepare_append(const kv_pool_desc& d) {
   cudaError_t e = cudaSuccess;
   if (d.latent_only || d.head_dim % 16 != 0) return e;  // refused, or k_append_any's
-  if (d.itemsize != 4) e = prepare_type<__nv_bfloat16>();
-  if (d.itemsize != 4 && e == cudaSuccess) e = prepare_type<__half>();
-  if (d.itemsize != 2 && e == cudaSuccess) e = prepare_type<float>();
+  const bool four = kind_of(d) == Kind::kE2M1;
+  if (d.itemsize != 4) e = prepare_type<__nv_bfloat16>(four);
+  if (d.itemsize != 4 && e == cudaSuccess) e = prepare_type<__half>(four);
+  if (d.itemsize != 2 && e == cudaSuccess) e = prepare_type<float>(four);
   return e;
 }
 
-cudaError_t launch_append(const DevPool& p, const Batch& b, int32_t layer, int32_t type, bool e4m3, int32_t H,
+cudaError_t launch_append(const DevPool& p, const Batch& b, int32_t layer, int32_t type, Kind kind, int32_t H,
                           int32_t D, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                           const kv_rotary* rot, const void* q, int64_t q_stride, int32_t Q, void* q_out, float* scales,
                           int sm_count, cudaStream_t s) {
@@ -906,9 +777,9 @@ cudaError_t launch_append(const DevPool& p, const Batch& b, int32_t layer, int32
   }
   const AppendArgs g{k, v, q, q_out, scales, k_stride, v_stride, q_stride, H, Q, D, layer};
   switch (type) {
-    case KV_TYPE_BF16: return launch<__nv_bfloat16>(p, b, g, t, e4m3, sm_count, s);
-    case KV_TYPE_F16: return launch<__half>(p, b, g, t, e4m3, sm_count, s);
-    default: return launch<float>(p, b, g, t, e4m3, sm_count, s);
+    case KV_TYPE_BF16: return launch<__nv_bfloat16>(p, b, g, t, kind, sm_count, s);
+    case KV_TYPE_F16: return launch<__half>(p, b, g, t, kind, sm_count, s);
+    default: return launch<float>(p, b, g, t, kind, sm_count, s);
   }
 }
 

@@ -26,11 +26,13 @@ __global__ void __launch_bounds__(kRowBlock) k_attend_rows(DevPool p, Batch b, A
   store_bits(p, bits);
 }
 
-cudaError_t launch_rows(const DevPool& p, const Batch& b, const AttendArgs& a, bool e4m3, cudaStream_t s) {
+cudaError_t launch_rows(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, cudaStream_t s) {
   const int64_t n = (b.n_rows * a.Q + kRowBlock / 32 - 1) / (kRowBlock / 32);
   const unsigned grid = static_cast<unsigned>(n > 0x7fffffff ? 0x7fffffff : n);
-  if (e4m3)
+  if (kind == Kind::kE4M3)
     k_attend_rows<CodeE4M3><<<grid, kRowBlock, 0, s>>>(p, b, a);
+  else if (kind == Kind::kE2M1)
+    k_attend_rows<CodeE2M1><<<grid, kRowBlock, 0, s>>>(p, b, a);
   else if (a.type == KV_TYPE_BF16)
     k_attend_rows<__nv_bfloat16><<<grid, kRowBlock, 0, s>>>(p, b, a);
   else
@@ -43,7 +45,7 @@ bool has_tiles(int32_t D) { return D == 64 || D == 128; }
 }  // namespace
 
 cudaError_t prepare_attend(const kv_pool_desc& d) {
-  if (d.latent_only || d.itemsize > 2 || !has_tiles(d.head_dim)) return cudaSuccess;
+  if (d.latent_only || d.itemsize > 2 || d.format == KV_FORMAT_E2M1 || !has_tiles(d.head_dim)) return cudaSuccess;
   const bool e4m3 = d.itemsize == 1, p16 = d.page_size % 16 == 0;
   const cudaError_t e = prepare_attend_few(d.head_dim, e4m3, p16);
   return e == cudaSuccess ? prepare_attend_tile(d.head_dim, e4m3, p16) : e;
@@ -79,9 +81,10 @@ int64_t attend_workspace_bytes(int32_t, int32_t, int32_t D, int32_t, int64_t, in
 // 152 at 16, 205 / 154 at 24; 8-bit, whose codes the tile kernel is slow to
 // turn into fp16, 83 / 174 at 16, 138 / 183 at 32, 194 / 183 at 48 (fp16 output: 93 / 214 at 16, 151 / 218 at 24,
 // 272 / 226 at 64).
-cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, bool e4m3, void* workspace,
+cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, void* workspace,
                           int sm_count, cudaStream_t s) {
-  if (!has_tiles(a.D)) return launch_rows(p, b, a, e4m3, s);
+  if (!has_tiles(a.D) || kind == Kind::kE2M1) return launch_rows(p, b, a, kind, s);
+  const bool e4m3 = kind == Kind::kE4M3;
   const int32_t few_rows = e4m3 ? 32 : 16;
   const bool only_few = b.n_rows * a.G <= few_rows * static_cast<int64_t>(b.n_seqs);
   const int32_t limit = only_few ? 0x7fffffff : few_rows / a.G;

@@ -4,24 +4,41 @@
 #pragma once
 
 #include "kv_attn_launch.h"
+#include "kv_e2m1.cuh"
 
 namespace gtkv {
 
 constexpr int kAttendMaxDim = 256;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Cache element types.
+// Cache element types. Head: the elements of one KV head in a row of the cache.
 struct CodeE4M3 {};
+struct CodeE2M1 {};
 
 template <class C>
-struct Cache {
-  using Raw = C;
-  static __device__ __forceinline__ float get(C x) { return Elem<C>::get(x); }
+struct Head {
+  const C* x;
+  __device__ __forceinline__ Head(const void* row, const AttendArgs& a, int32_t h)
+      : x(static_cast<const C*>(row) + static_cast<int64_t>(h) * a.D) {}
+  __device__ __forceinline__ float operator[](int e) const { return Elem<C>::get(x[e]); }
 };
 template <>
-struct Cache<CodeE4M3> {
-  using Raw = uint8_t;
-  static __device__ __forceinline__ float get(uint8_t x) { return from_e4m3(x); }
+struct Head<CodeE4M3> {
+  const uint8_t* x;
+  __device__ __forceinline__ Head(const void* row, const AttendArgs& a, int32_t h)
+      : x(static_cast<const uint8_t*>(row) + static_cast<int64_t>(h) * a.D) {}
+  __device__ __forceinline__ float operator[](int e) const { return from_e4m3(x[e]); }
+};
+template <>
+struct Head<CodeE2M1> {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  __device__ __forceinline__ Head(const void* row, const AttendArgs& a, int32_t h)
+      : codes(static_cast<const uint8_t*>(row) + h * (a.D / 2)),
+        scales(static_cast<const uint8_t*>(row) + code_bytes(a.H, a.D) + h * (a.D / 16)) {}
+  __device__ __forceinline__ float operator[](int e) const {
+    return code_value(codes[e >> 1] >> 4 * (e & 1) & 15, scales[e >> 4]);
+  }
 };
 
 // Does the token at position i see token j <= i? (tombstones apart)
@@ -52,7 +69,6 @@ __device__ __forceinline__ void store_out(const AttendArgs& a, int64_t i, float 
 template <class C>
 __device__ __noinline__ void attend_row(const DevPool& p, const Batch& b, const AttendArgs& a, int32_t s, int64_t i,
                                         int64_t r, int32_t h, int* bits) {
-  using Raw = typename Cache<C>::Raw;
   const int lane = threadIdx.x & 31;
   const int32_t kvh = h / a.G;
   const int64_t q0 = r * a.q_stride + static_cast<int64_t>(h) * a.D;
@@ -83,9 +99,9 @@ __device__ __noinline__ void attend_row(const DevPool& p, const Batch& b, const 
         sk = __ldg(a.scales + at);
         sv = __ldg(a.scales + at + a.H);
       }
-      const Raw* k = reinterpret_cast<const Raw*>(p.base + row * p.vpr) + static_cast<int64_t>(kvh) * a.D;
+      const Head<C> k(p.base + row * p.vpr, a, kvh);
       float d = 0.0f;
-      for (int e = 0; e < a.D; ++e) d = fmaf(load_q(a, a.q, q0 + e), Cache<C>::get(k[e]), d);
+      for (int e = 0; e < a.D; ++e) d = fmaf(load_q(a, a.q, q0 + e), k[e], d);
       x = d * sk * a.scale_log2;
     }
     const uint32_t seen = __ballot_sync(kFull, page != 0);
@@ -105,10 +121,10 @@ __device__ __noinline__ void attend_row(const DevPool& p, const Batch& b, const 
       const int k = __ffs(left) - 1;
       const int64_t rk = __shfl_sync(kFull, row, k);
       const float wk = __shfl_sync(kFull, w, k) * __shfl_sync(kFull, sv, k);
-      const Raw* v = reinterpret_cast<const Raw*>(p.base + (rk + p.ps) * p.vpr) + static_cast<int64_t>(kvh) * a.D;
+      const Head<C> v(p.base + (rk + p.ps) * p.vpr, a, kvh);
 #pragma unroll
       for (int e = 0; e < kAttendMaxDim / 32; ++e)
-        if (lane + 32 * e < a.D) acc[e] = fmaf(wk, Cache<C>::get(v[lane + 32 * e]), acc[e]);
+        if (lane + 32 * e < a.D) acc[e] = fmaf(wk, v[lane + 32 * e], acc[e]);
     }
   }
 #pragma unroll

@@ -60,9 +60,11 @@ int enter(const kv_pool_t* pool, int32_t layer, const kv_batch* in, gtkv::Batch*
   return KV_OK;
 }
 
+gtkv::Kind kind_of(const kv_pool_t* pool) { return gtkv::kind_of(pool->desc); }
+
 // The scale buffer goes with 8-bit pools and with them only.
 int check_scales(const kv_pool_t* pool, const float* scales) {
-  if ((pool->desc.itemsize == 1) != (scales != nullptr)) return KV_ERR_INVALID;
+  if ((kind_of(pool) == gtkv::Kind::kE4M3) != (scales != nullptr)) return KV_ERR_INVALID;
   return aligned(scales, 4) ? KV_OK : KV_ERR_ALIGN;
 }
 
@@ -86,7 +88,8 @@ int check_rotary(const kv_pool_t* pool, const kv_rotary* r) {
 extern "C" {
 
 int kv_scale_bytes(const kv_pool_t* pool, int64_t* bytes) {
-  if (pool == nullptr || bytes == nullptr || pool->desc.itemsize != 1 || pool->desc.latent_only) return KV_ERR_INVALID;
+  if (pool == nullptr || bytes == nullptr || pool->desc.latent_only || kind_of(pool) != gtkv::Kind::kE4M3)
+    return KV_ERR_INVALID;
   *bytes = 4 * pool->desc.num_pages * pool->lay.blocks * pool->desc.head_num;
   return KV_OK;
 }
@@ -112,7 +115,7 @@ int kv_append_layer(const kv_pool_t* pool, int32_t layer, const kv_batch* batch,
   if (q_dev != nullptr && q_dev == q_out_dev && b.n_rows > 1 && q_stride != q_row) return KV_ERR_INVALID;
   if (!aligned(k_dev, size) || !aligned(v_dev, size) || !aligned(q_dev, size) || !aligned(q_out_dev, size))
     return KV_ERR_ALIGN;
-  return launched(gtkv::launch_append(pool->dev, b, layer, type, it == 1, H, D, k_dev, k_stride, v_dev, v_stride,
+  return launched(gtkv::launch_append(pool->dev, b, layer, type, kind_of(pool), H, D, k_dev, k_stride, v_dev, v_stride,
                                       rotary, q_dev, q_stride, q_heads, q_out_dev, scales_dev, pool->sm_count,
                                       as_stream(stream)));
 }
@@ -150,7 +153,7 @@ int kv_attend_layer(const kv_pool_t* pool, int32_t layer, const kv_batch* batch,
     return KV_ERR_ALIGN;
   const gtkv::AttendArgs a{q_dev, out_dev, lse_dev, scales_dev, q_stride, scale * 1.4426950408889634f, window, sinks,
                            H,     q_heads, D,       q_heads / H, layer,   type};
-  return launched(gtkv::launch_attend(pool->dev, b, a, it == 1, workspace_dev, pool->sm_count, as_stream(stream)));
+  return launched(gtkv::launch_attend(pool->dev, b, a, kind_of(pool), workspace_dev, pool->sm_count, as_stream(stream)));
 }
 
 int kv_gather_layer_scaled(const kv_pool_t* pool, int32_t layer, const kv_batch* batch, const float* scales_dev,
@@ -159,11 +162,15 @@ int kv_gather_layer_scaled(const kv_pool_t* pool, int32_t layer, const kv_batch*
   gtkv::Batch b;
   int rc = enter(pool, layer, batch, &b);
   if (rc != KV_OK) return rc;
-  if (type_size(type) == 0 || pool->desc.itemsize != 1 || scales_dev == nullptr) return KV_ERR_INVALID;
+  const gtkv::Kind kind = kind_of(pool);
+  if (type_size(type) == 0 || kind == gtkv::Kind::kElements) return KV_ERR_INVALID;
   if ((rc = check_scales(pool, scales_dev)) != KV_OK) return rc;
   if (b.n_rows == 0) return KV_OK;
   if (out_k_dev == nullptr || out_v_dev == nullptr) return KV_ERR_INVALID;
   if (!aligned(out_k_dev, 16) || !aligned(out_v_dev, 16)) return KV_ERR_ALIGN;
+  if (kind == gtkv::Kind::kE2M1)
+    return launched(gtkv::launch_gather4(pool->dev, b, layer, pool->desc.head_num, pool->desc.head_dim, type, out_k_dev,
+                                         out_v_dev, as_stream(stream)));
   return launched(gtkv::launch_gather_scaled(pool->dev, b, layer, pool->desc.head_num, pool->desc.head_dim, scales_dev,
                                              type, out_k_dev, out_v_dev, as_stream(stream)));
 }

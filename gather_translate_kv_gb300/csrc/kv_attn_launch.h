@@ -7,11 +7,19 @@
 
 namespace gtkv {
 
-cudaError_t launch_append(const DevPool& p, const Batch& b, int32_t layer, int32_t type, bool e4m3, int32_t H,
+// What the cache holds.
+enum class Kind { kElements, kE4M3, kE2M1 };
+inline Kind kind_of(const kv_pool_desc& d) {
+  return d.format == KV_FORMAT_E2M1 ? Kind::kE2M1 : d.itemsize == 1 ? Kind::kE4M3 : Kind::kElements;
+}
+
+cudaError_t launch_append(const DevPool& p, const Batch& b, int32_t layer, int32_t type, Kind kind, int32_t H,
                           int32_t D, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                           const kv_rotary* rot, const void* q, int64_t q_stride, int32_t Q, void* q_out, float* scales,
                           int sm_count, cudaStream_t s);
 
+cudaError_t launch_gather4(const DevPool& p, const Batch& b, int32_t layer, int32_t H, int32_t D, int32_t type,
+                           void* out_k, void* out_v, cudaStream_t s);
 cudaError_t launch_gather_scaled(const DevPool& p, const Batch& b, int32_t layer, int32_t H, int32_t D,
                                  const float* scales, int32_t type, void* out_k, void* out_v, cudaStream_t s);
 
@@ -36,7 +44,7 @@ struct AttendArgs {
 cudaError_t prepare_append(const kv_pool_desc& d);
 cudaError_t prepare_attend(const kv_pool_desc& d);
 int64_t attend_workspace_bytes(int32_t H, int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int sm_count);
-cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, bool e4m3, void* workspace,
+cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, void* workspace,
                           int sm_count, cudaStream_t s);
 
 // A launch that starts while the kernel before it drains (programmatic dependent launch).

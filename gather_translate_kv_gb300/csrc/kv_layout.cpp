@@ -16,7 +16,10 @@ int compute_layout(const kv_pool_desc* d, Layout* out) {
       d->num_pages < 1 || d->anchor_bytes < 0)
     return KV_ERR_INVALID;
   if (d->itemsize != 1 && d->itemsize != 2 && d->itemsize != 4) return KV_ERR_INVALID;
-  if ((d->latent_only != 0 && d->latent_only != 1) || d->reserved != 0) return KV_ERR_INVALID;
+  if (d->latent_only != 0 && d->latent_only != 1) return KV_ERR_INVALID;
+  if (d->format != KV_FORMAT_ELEMENTS && d->format != KV_FORMAT_E2M1) return KV_ERR_INVALID;
+  const bool e2m1 = d->format == KV_FORMAT_E2M1;
+  if (e2m1 && (d->latent_only || d->itemsize != 1 || d->head_dim % 16 != 0)) return KV_ERR_INVALID;
   // build_mha_views: the row-block array exists only for uniform K/V rows;
   // unified_memory_supported_for_model admits MLA (one latent row) regardless.
   if (!d->latent_only && d->head_dim != d->v_head_dim) return KV_ERR_ASYMMETRIC;
@@ -25,6 +28,7 @@ int compute_layout(const kv_pool_desc* d, Layout* out) {
   L.kv_rows = d->latent_only ? 1 : 2;
   L.blocks = L.kv_rows * static_cast<int64_t>(d->layer_num);
   if (!mul(static_cast<int64_t>(d->head_num) * d->head_dim, d->itemsize, &L.R)) return KV_ERR_INVALID;
+  if (e2m1) L.R = (L.R / 2 + L.R / 16 + 15) / 16 * 16;  // codes, scales, whole 16-byte vectors
   // _assert_kernel_id_bound: kernel-facing rows num_pages * 2L * ps < 2^31.
   if (!mul(L.blocks, d->page_size, &L.stride)) return KV_ERR_ID_BOUND;
   if (!mul(d->num_pages, L.stride, &L.n_rows) || L.n_rows >= (int64_t(1) << 31))

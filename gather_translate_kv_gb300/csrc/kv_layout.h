@@ -11,7 +11,7 @@
 namespace gtkv {
 
 struct Layout {
-  int64_t R;              // row bytes, H * D * itemsize
+  int64_t R;              // row bytes: H * D * itemsize, or codes and scales of 4-bit rows
   int64_t blocks;         // row-blocks per page: 2L (MHA/SWA) or L (MLA)
   int64_t kv_rows;        // rows per layer per token: 2 (K, V) or 1 (MLA latent)
   int64_t page_bytes;     // ps * blocks * R

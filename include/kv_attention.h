@@ -25,6 +25,15 @@
  * that move bytes (kv_move, kv_store_layer) do not know of scales: move
  * whole pages together with their scales, or append anew.
  *
+ * 4-bit pools (KV_FORMAT_E2M1). A head's elements are codes of 4 bits (a sign,
+ * two bits of exponent, one of mantissa: 0, .5, 1, 1.5, 2, 3, 4, 6) with a
+ * scale byte s for every 16: value = code * scale, scale the fp16 whose bits
+ * are s << 7, s <= 0xE0 (8192); a greater byte stands for NaN, and so do its
+ * 16 elements. Every value is exact in fp16 and in bf16. Codes and scales of
+ * a token lie in its rows (kv_pool.h), so moves, stores and gathers of rows
+ * carry them, the scales arguments below are NULL, and nothing that is in the cache
+ * changes when tokens are appended behind it.
+ *
  * Like the calls of kv_pool.h these are asynchronous on the stream, allocate
  * nothing, capture into CUDA graphs, need the pool's device current and
  * report data errors in the pool's error word. MLA pools are refused
@@ -86,7 +95,7 @@ int kv_scale_bytes(const kv_pool_t* pool, int64_t* bytes);
  * overlap for an 8-bit pool with queries).
  *  type      KV_TYPE_* of k, v, q and q_out. A pool of itemsize 2 or 4 stores
  *            that type (itemsize 2: BF16 or F16; 4: F32); an 8-bit pool
- *            takes any of the three.
+ *            or a 4-bit pool takes any of the three.
  *  k_dev, v_dev, q_dev  rows of [H, D] ([q_heads, D]) contiguous elements,
  *            *_stride elements from row to row (a fused projection's slices
  *            can be passed as they are), aligned to their elements; loads are
@@ -104,6 +113,12 @@ int kv_scale_bytes(const kv_pool_t* pool, int64_t* bytes);
  *            become rne(code * (base / S)), new ones rne(x * (1 / S)); a
  *            value that is not finite becomes the NaN code. With power-of-two
  *            scales the earlier codes lose nothing but subnormal bits.
+ *  4-bit pools: for each block of 16 elements of a head, x the rotated values
+ *            in 32 bits: h is the largest |x| times the 32-bit 1/6, at most
+ *            8192, in fp16; s is h's bits to the upper eight (>> 7); each
+ *            rounding to nearest even. Codes are rne(x * (1 / scale)), at most
+ *            6 in magnitude, 0 where s is 0. A block that holds a value which
+ *            is not finite gets s = 0xFF and codes that are not specified.
  * Pages are a sequence's own: two sequences of one batch that append to the
  * same page race (bytes and scale unspecified, nothing out of bounds). */
 int kv_append_layer(const kv_pool_t* pool, int32_t layer, const kv_batch* batch, int32_t type, const void* k_dev,
@@ -121,7 +136,7 @@ int kv_append_layer(const kv_pool_t* pool, int32_t layer, const kv_batch* batch,
  * does not change it, infinities and NaN included. Pages that no row of the
  * batch sees are not read.
  *  type      KV_TYPE_BF16 or KV_TYPE_F16 of q and out; a 16-bit pool holds
- *            the same type, an 8-bit pool takes either.
+ *            the same type, an 8-bit or a 4-bit pool takes either.
  *  q_dev     rows of [q_heads, D], q_stride elements from row to row
  *  out_dev   [n_rows, q_heads, D] contiguous, apart from q_dev (rows may be done again from q)
  *  lse_dev   [n_rows, q_heads] float, or NULL
@@ -141,10 +156,10 @@ int kv_attend_layer(const kv_pool_t* pool, int32_t layer, const kv_batch* batch,
                     int32_t sinks, const float* scales_dev, void* workspace_dev, int64_t workspace_bytes,
                     kv_stream_t stream);
 
-/* Gather of an 8-bit pool's values: out[row] = code * scale of the batch's
+/* Gather of an 8-bit or a 4-bit pool's values: out[row] = code * scale of the batch's
  * tokens, one layer's K and V as [n_rows, H, D] of `type` (rounded to nearest
  * even; BF16 holds every product with a power-of-two scale exactly, up to its
- * range), 16-byte aligned. */
+ * range, and 4-bit pools' values in any of the types), 16-byte aligned. */
 int kv_gather_layer_scaled(const kv_pool_t* pool, int32_t layer, const kv_batch* batch, const float* scales_dev,
                            int32_t type, void* out_k_dev, void* out_v_dev, kv_stream_t stream);
 

@@ -94,6 +94,16 @@ typedef struct kv_pool kv_pool_t; /* opaque, host-side, owned by the library */
 /* A cudaStream_t without requiring the CUDA headers. */
 typedef struct CUstream_st* kv_stream_t;
 
+/* What a row holds. To the calls of this header a row is R bytes either way.
+ * KV_FORMAT_E2M1: H * D elements of 4 bits with a scale for every 16. D is a
+ * multiple of 16, itemsize is 1, and R = H * D / 2 + H * D / 16 rounded up to a
+ * multiple of 16: the codes of the heads in order (element 2i of a head in
+ * the low half of its byte i), then the scale bytes of their blocks of 16
+ * elements, then bytes that no call reads or writes. Written and read by the
+ * calls of kv_attention.h, which has the meaning of codes and scales; moves and
+ * stores carry a token's scales along with its codes. MHA / SWA pools only. */
+enum { KV_FORMAT_ELEMENTS = 0, KV_FORMAT_E2M1 = 1 };
+
 /* Pool geometry in the report's notation (build_mha_views' arguments). */
 typedef struct {
   int32_t layer_num;    /* L >= 1                                                  */
@@ -107,7 +117,7 @@ typedef struct {
   int32_t latent_only;  /* 0: MHA/SWA pool, a K and a V row per layer (2L blocks)  */
                         /* 1: MLA pool, one latent row per layer (L blocks, no V;  */
                         /*    v_head_dim is ignored). Zero-initialised = MHA.      */
-  int32_t reserved;     /* must be 0                                               */
+  int32_t format;       /* KV_FORMAT_*: what a row's bytes are                     */
 } kv_pool_desc;
 
 /* Derived layout of a pool (kv_pool_info). */
