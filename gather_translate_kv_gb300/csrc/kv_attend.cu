@@ -45,10 +45,11 @@ bool has_tiles(int32_t D) { return D == 64 || D == 128; }
 }  // namespace
 
 cudaError_t prepare_attend(const kv_pool_desc& d) {
-  if (d.latent_only || d.itemsize > 2 || d.format == KV_FORMAT_E2M1 || !has_tiles(d.head_dim)) return cudaSuccess;
-  const bool e4m3 = d.itemsize == 1, p16 = d.page_size % 16 == 0;
-  const cudaError_t e = prepare_attend_few(d.head_dim, e4m3, p16);
-  return e == cudaSuccess ? prepare_attend_tile(d.head_dim, e4m3, p16) : e;
+  if (d.latent_only || d.itemsize > 2 || !has_tiles(d.head_dim)) return cudaSuccess;
+  const Kind kind = kind_of(d);
+  const bool p16 = d.page_size % 16 == 0;
+  const cudaError_t e = prepare_attend_few(d.head_dim, kind, p16);
+  return e == cudaSuccess && kind != Kind::kE2M1 ? prepare_attend_tile(d.head_dim, kind == Kind::kE4M3, p16) : e;
 }
 
 namespace {
@@ -83,22 +84,22 @@ int64_t attend_workspace_bytes(int32_t, int32_t, int32_t D, int32_t, int64_t, in
 // 272 / 226 at 64).
 cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, void* workspace,
                           int sm_count, cudaStream_t s) {
-  if (!has_tiles(a.D) || kind == Kind::kE2M1) return launch_rows(p, b, a, kind, s);
-  const bool e4m3 = kind == Kind::kE4M3;
-  const int32_t few_rows = e4m3 ? 32 : 16;
-  const bool only_few = b.n_rows * a.G <= few_rows * static_cast<int64_t>(b.n_seqs);
+  if (!has_tiles(a.D)) return launch_rows(p, b, a, kind, s);
+  const int32_t few_rows = kind == Kind::kElements ? 16 : 32;
+  const bool only_few = kind == Kind::kE2M1 || b.n_rows * a.G <= few_rows * static_cast<int64_t>(b.n_seqs);
   const int32_t limit = only_few ? 0x7fffffff : few_rows / a.G;
   Split few{}, tile{};
   cudaError_t e = cudaSuccess;
-  if (limit > 0) e = launch_attend_few(p, b, a, e4m3, limit, workspace, sm_count, &few, s);
+  if (limit > 0) e = launch_attend_few(p, b, a, kind, limit, workspace, sm_count, &few, s);
   if (e == cudaSuccess && !only_few)
-    e = launch_attend_tile(p, b, a, e4m3, limit + 1,
+    e = launch_attend_tile(p, b, a, kind == Kind::kE4M3, limit + 1,
                            static_cast<uint8_t*>(workspace) + align256(attend_few_workspace(a.D, sm_count)), sm_count,
                            limit > 0, &tile, s);
   if (e != cudaSuccess) return e;
   if (few.whole) few.n_workers = 0;
   if (few.n_workers == 0 && tile.n_workers == 0) return e;
-  if (e4m3) return launch_join<CodeE4M3>(p, b, a, few, tile, sm_count, s);
+  if (kind == Kind::kE2M1) return launch_join<CodeE2M1>(p, b, a, few, tile, sm_count, s);
+  if (kind == Kind::kE4M3) return launch_join<CodeE4M3>(p, b, a, few, tile, sm_count, s);
   return a.type == KV_TYPE_BF16 ? launch_join<__nv_bfloat16>(p, b, a, few, tile, sm_count, s)
                                 : launch_join<__half>(p, b, a, few, tile, sm_count, s);
 }
