@@ -49,7 +49,7 @@ cudaError_t prepare_attend(const kv_pool_desc& d) {
   const Kind kind = kind_of(d);
   const bool p16 = d.page_size % 16 == 0;
   const cudaError_t e = prepare_attend_few(d.head_dim, kind, p16);
-  return e == cudaSuccess && kind != Kind::kE2M1 ? prepare_attend_tile(d.head_dim, kind == Kind::kE4M3, p16) : e;
+  return e == cudaSuccess ? prepare_attend_tile(d.head_dim, kind, p16) : e;
 }
 
 namespace {
@@ -86,13 +86,13 @@ cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a,
                           int sm_count, cudaStream_t s) {
   if (!has_tiles(a.D)) return launch_rows(p, b, a, kind, s);
   const int32_t few_rows = kind == Kind::kElements ? 16 : 32;
-  const bool only_few = kind == Kind::kE2M1 || b.n_rows * a.G <= few_rows * static_cast<int64_t>(b.n_seqs);
+  const bool only_few = b.n_rows * a.G <= few_rows * static_cast<int64_t>(b.n_seqs);
   const int32_t limit = only_few ? 0x7fffffff : few_rows / a.G;
   Split few{}, tile{};
   cudaError_t e = cudaSuccess;
   if (limit > 0) e = launch_attend_few(p, b, a, kind, limit, workspace, sm_count, &few, s);
   if (e == cudaSuccess && !only_few)
-    e = launch_attend_tile(p, b, a, kind == Kind::kE4M3, limit + 1,
+    e = launch_attend_tile(p, b, a, kind, limit + 1,
                            static_cast<uint8_t*>(workspace) + align256(attend_few_workspace(a.D, sm_count)), sm_count,
                            limit > 0, &tile, s);
   if (e != cudaSuccess) return e;

@@ -46,14 +46,16 @@ inline int64_t split_record_bytes(int64_t workers) {
 cudaError_t prepare_attend_few(int32_t D, Kind kind, bool p16);
 cudaError_t prepare_few4(int32_t D, bool p16);  // kv_attend_few4.cu
 cudaError_t launch_few4(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, int nt, cudaStream_t s);
-cudaError_t prepare_attend_tile(int32_t D, bool e4m3, bool p16);
+cudaError_t prepare_attend_tile(int32_t D, Kind kind, bool p16);
+cudaError_t prepare_tile4(int32_t D);  // kv_attend_tile4.cu
+cudaError_t launch_tile4(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, bool after, cudaStream_t s);
 int64_t attend_few_workspace(int32_t D, int sm_count);
 int64_t attend_tile_workspace(int32_t D, int sm_count);
 // Sequences of at most max_new, and of at least min_new, new tokens; *w says
 // what is left to join. `after` marks a launch that may overlap the one before it.
 cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, int32_t max_new,
                               void* workspace, int sm_count, Split* w, cudaStream_t s);
-cudaError_t launch_attend_tile(const DevPool& p, const Batch& b, const AttendArgs& a, bool e4m3, int32_t min_new,
+cudaError_t launch_attend_tile(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, int32_t min_new,
                                void* workspace, int sm_count, bool after, Split* w, cudaStream_t s);
 
 }  // namespace gtkv
