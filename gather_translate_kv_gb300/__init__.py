@@ -89,6 +89,15 @@ class kv_batch_t(ctypes.Structure):
     ]
 
 
+class kv_prefix_groups_t(ctypes.Structure):
+    _fields_ = [
+        ("group_dev", ctypes.c_void_p),
+        ("prefix_len_dev", ctypes.c_void_p),
+        ("n_groups", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 class kv_rotary_t(ctypes.Structure):
     _fields_ = [
         ("cos_sin_dev", ctypes.c_void_p),
@@ -166,6 +175,8 @@ def load(path: str) -> ctypes.CDLL:
         "kv_append_layer": [vp, i32, vp, i32, vp, i64, vp, i64, vp, vp, i64, i32, vp, vp, vp],
         "kv_attend_workspace_bytes": [vp, i32, i32, i64, P(i64)],
         "kv_attend_layer": [vp, i32, vp, i32, vp, i64, i32, vp, vp, ctypes.c_float, i32, i32, vp, vp, i64, vp],
+        "kv_attend_shared_workspace_bytes": [vp, i32, i32, i64, P(i64)],
+        "kv_attend_shared_layer": [vp, i32, vp, vp, i32, vp, i64, i32, vp, vp, ctypes.c_float, vp, vp, i64, vp],
         "kv_gather_layer_scaled": [vp, i32, vp, vp, i32, vp, vp, vp],
     }
     for name, args in sig.items():
@@ -640,24 +651,71 @@ def kv_attend_workspace_bytes(pool: KVPool, q_heads: int, n_seqs: int, n_rows: i
     return out.value
 
 
-def kv_attend_layer(pool: KVPool, layer: int, batch: KVBatch, q: torch.Tensor, out: torch.Tensor, scale: float,
-                    workspace: torch.Tensor, window: int = 0, sinks: int = 0, scales: torch.Tensor | None = None,
-                    lse: torch.Tensor | None = None, stream=None) -> None:
-    """Attention of the batch's rows q [n_rows, q_heads, dim] over the layer's
-    cache into out (and the log-sum-exp into lse [n_rows, q_heads]).
-    workspace: uint8, kv_attend_workspace_bytes() long, one per call in flight."""
-    n, dev = batch.n_rows, _here()
+def _attend_args(pool: KVPool, batch: KVBatch, q: torch.Tensor, out: torch.Tensor, lse: torch.Tensor | None,
+                 workspace: torch.Tensor, dev: int) -> tuple:
+    """The library's arguments type, q, q_stride, q_heads, out and lse."""
+    n = batch.n_rows
     qp, qs, qh = _rows(q, "q", n, None, pool.desc.head_dim, dev)
     op = _whole(out, "out", q.shape, q.dtype, dev)
     lp = None if lse is None else _whole(lse, "lse", (n, qh), torch.float32, dev)
     _on(workspace, "workspace", dev)
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous uint8")
+    return _type(q, "q"), qp, qs, qh, op, lp
+
+
+def kv_attend_layer(pool: KVPool, layer: int, batch: KVBatch, q: torch.Tensor, out: torch.Tensor, scale: float,
+                    workspace: torch.Tensor, window: int = 0, sinks: int = 0, scales: torch.Tensor | None = None,
+                    lse: torch.Tensor | None = None, stream=None) -> None:
+    """Attention of the batch's rows q [n_rows, q_heads, dim] over the layer's
+    cache into out (and the log-sum-exp into lse [n_rows, q_heads]).
+    workspace: uint8, kv_attend_workspace_bytes() long, one per call in flight."""
+    dev = _here()
     rc = (_lib or lib()).kv_attend_layer(
-        pool.handle, layer, batch.ptr, _type(q, "q"), qp, qs, qh, op, lp, scale, window, sinks,
+        pool.handle, layer, batch.ptr, *_attend_args(pool, batch, q, out, lse, workspace, dev), scale, window, sinks,
         _scales(pool, scales, dev), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
     if rc:
         raise KVError("kv_attend_layer", rc)
+
+
+@dataclass
+class KVPrefixGroups:
+    """A kv_prefix_groups and the tensors it points to."""
+
+    struct: kv_prefix_groups_t
+    ptr: int
+    tensors: tuple
+
+
+def kv_prefix_groups(group: torch.Tensor, prefix_len: torch.Tensor) -> KVPrefixGroups:
+    """group: int32 [n_groups + 1], the groups' first sequences and the number of sequences; prefix_len: int32
+    [n_groups], the tokens that the sequences of a group share."""
+    if group.dim() != 1 or prefix_len.dim() != 1 or group.numel() != prefix_len.numel() + 1:
+        raise ValueError("group must be [n_groups + 1] and prefix_len [n_groups]")
+    st = kv_prefix_groups_t(_dev(group, "group", torch.int32), _dev(prefix_len, "prefix_len", torch.int32),
+                            prefix_len.numel(), 0)
+    return KVPrefixGroups(st, ctypes.addressof(st), (group, prefix_len))
+
+
+def kv_attend_shared_workspace_bytes(pool: KVPool, q_heads: int, n_seqs: int, n_rows: int) -> int:
+    out = ctypes.c_int64()
+    _check("kv_attend_shared_workspace_bytes", lib().kv_attend_shared_workspace_bytes(
+        pool.handle, q_heads, n_seqs, n_rows, ctypes.byref(out)))
+    return out.value
+
+
+def kv_attend_shared_layer(pool: KVPool, layer: int, batch: KVBatch, groups: KVPrefixGroups, q: torch.Tensor,
+                           out: torch.Tensor, scale: float, workspace: torch.Tensor,
+                           scales: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None) -> None:
+    """kv_attend_layer of a batch whose groups of sequences share their first
+    tokens, which are attended to once for all rows of a group.
+    workspace: uint8, kv_attend_shared_workspace_bytes() long, one per call in flight."""
+    dev = _here()
+    rc = (_lib or lib()).kv_attend_shared_layer(
+        pool.handle, layer, batch.ptr, groups.ptr, *_attend_args(pool, batch, q, out, lse, workspace, dev), scale,
+        _scales(pool, scales, dev), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+    if rc:
+        raise KVError("kv_attend_shared_layer", rc)
 
 
 def kv_gather_layer_scaled(pool: KVPool, layer: int, batch: KVBatch, scales: torch.Tensor | None, out_k: torch.Tensor,

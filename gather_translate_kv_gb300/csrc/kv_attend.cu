@@ -40,8 +40,6 @@ cudaError_t launch_rows(const DevPool& p, const Batch& b, const AttendArgs& a, K
   return cudaGetLastError();
 }
 
-bool has_tiles(int32_t D) { return D == 64 || D == 128; }
-
 }  // namespace
 
 cudaError_t prepare_attend(const kv_pool_desc& d) {
@@ -68,6 +66,14 @@ cudaError_t launch_join(const DevPool& p, const Batch& b, const AttendArgs& a, c
 
 }  // namespace
 
+cudaError_t launch_attend_join(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, const Split& few,
+                               const Split& tile, int sm_count, cudaStream_t s) {
+  if (kind == Kind::kE2M1) return launch_join<CodeE2M1>(p, b, a, few, tile, sm_count, s);
+  if (kind == Kind::kE4M3) return launch_join<CodeE4M3>(p, b, a, few, tile, sm_count, s);
+  return a.type == KV_TYPE_BF16 ? launch_join<__nv_bfloat16>(p, b, a, few, tile, sm_count, s)
+                                : launch_join<__half>(p, b, a, few, tile, sm_count, s);
+}
+
 int64_t attend_workspace_bytes(int32_t, int32_t, int32_t D, int32_t, int64_t, int sm_count) {
   if (!has_tiles(D)) return 16;
   return align256(attend_few_workspace(D, sm_count)) + attend_tile_workspace(D, sm_count);
@@ -82,26 +88,28 @@ int64_t attend_workspace_bytes(int32_t, int32_t, int32_t D, int32_t, int64_t, in
 // 152 at 16, 205 / 154 at 24; 8-bit, whose codes the tile kernel is slow to
 // turn into fp16, 83 / 174 at 16, 138 / 183 at 32, 194 / 183 at 48 (fp16 output: 93 / 214 at 16, 151 / 218 at 24,
 // 272 / 226 at 64).
-cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, void* workspace,
-                          int sm_count, cudaStream_t s) {
-  if (!has_tiles(a.D)) return launch_rows(p, b, a, kind, s);
-  const int32_t few_rows = kind == Kind::kElements ? 16 : 32;
-  const bool only_few = b.n_rows * a.G <= few_rows * static_cast<int64_t>(b.n_seqs);
+cudaError_t launch_tiles(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, void* workspace, int sm_count,
+                         Launch how, cudaStream_t s) {
+  const int32_t few_rows = few_rows_of(kind);
+  const bool only_few = b.n_rows * a.G <= few_rows * spans_of(b);
   const int32_t limit = only_few ? 0x7fffffff : few_rows / a.G;
   Split few{}, tile{};
   cudaError_t e = cudaSuccess;
-  if (limit > 0) e = launch_attend_few(p, b, a, kind, limit, workspace, sm_count, &few, s);
+  if (limit > 0) e = launch_attend_few(p, b, a, kind, limit, workspace, sm_count, how, &few, s);
   if (e == cudaSuccess && !only_few)
     e = launch_attend_tile(p, b, a, kind, limit + 1,
                            static_cast<uint8_t*>(workspace) + align256(attend_few_workspace(a.D, sm_count)), sm_count,
-                           limit > 0, &tile, s);
+                           limit > 0 ? Launch::kAfter : how, &tile, s);
   if (e != cudaSuccess) return e;
   if (few.whole) few.n_workers = 0;
   if (few.n_workers == 0 && tile.n_workers == 0) return e;
-  if (kind == Kind::kE2M1) return launch_join<CodeE2M1>(p, b, a, few, tile, sm_count, s);
-  if (kind == Kind::kE4M3) return launch_join<CodeE4M3>(p, b, a, few, tile, sm_count, s);
-  return a.type == KV_TYPE_BF16 ? launch_join<__nv_bfloat16>(p, b, a, few, tile, sm_count, s)
-                                : launch_join<__half>(p, b, a, few, tile, sm_count, s);
+  return launch_attend_join(p, b, a, kind, few, tile, sm_count, s);
+}
+
+cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, void* workspace,
+                          int sm_count, cudaStream_t s) {
+  if (!has_tiles(a.D)) return launch_rows(p, b, a, kind, s);
+  return launch_tiles(p, b, a, kind, workspace, sm_count, Launch::kPlain, s);
 }
 
 }  // namespace gtkv

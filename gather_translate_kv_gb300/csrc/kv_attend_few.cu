@@ -25,14 +25,14 @@ int64_t attend_few_workspace(int32_t D, int sm_count) {
 }
 
 cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, int32_t max_new,
-                              void* workspace, int sm_count, Split* out, cudaStream_t s) {
+                              void* workspace, int sm_count, Launch how, Split* out, cudaStream_t s) {
   Split w{};
   w.hw = heads_of_worker(a.H);
   w.max_new = max_new;
   const int kw = kFewWarps / w.hw;
   // one tile of 8 columns when the sequences' rows of a KV head fit on average, else 16 (4 rows, 256 x 4096 tokens, on one
   // GPU: 686 us with 8 columns, 803 with 16)
-  const int nt = b.n_rows * a.G <= 8 * static_cast<int64_t>(b.n_seqs) ? 1 : 2;
+  const int nt = b.n_rows * a.G <= 8 * spans_of(b) ? 1 : 2;
   // steps of one unit at most, and of all units
   int64_t most = static_cast<int64_t>(b.max_pages) * p.ps / 16 + 1;
   if (a.window) {
@@ -62,11 +62,13 @@ cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs
   w.lift = 0.0f;  // the partial results' references are below it already
   w.q_wide = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.q_stride % 8 == 0;
   w.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
+  w.first = how == Launch::kFirst;
   *out = w;
-  if (kind == Kind::kE2M1) return launch_few4(p, b, a, w, nt, s);
-  if (kind == Kind::kE4M3) return launch_c<CodeE4M3>(p, b, a, w, nt, s);
-  if (a.type == KV_TYPE_BF16) return launch_c<__nv_bfloat16>(p, b, a, w, nt, s);
-  return launch_c<__half>(p, b, a, w, nt, s);
+  const bool after = how != Launch::kPlain;
+  if (kind == Kind::kE2M1) return launch_few4(p, b, a, w, nt, after, s);
+  if (kind == Kind::kE4M3) return launch_c<CodeE4M3>(p, b, a, w, nt, after, s);
+  if (a.type == KV_TYPE_BF16) return launch_c<__nv_bfloat16>(p, b, a, w, nt, after, s);
+  return launch_c<__half>(p, b, a, w, nt, after, s);
 }
 
 }  // namespace gtkv

@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ ShareStart loc[kFewWarps];
   __shared__ int64_t tmp[kFewWarps];
+  if (w.first) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
@@ -181,9 +182,11 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
   int bits = 0;
 
   auto tiles_of = [&](const Seq& q) { return q.n == 0 || q.n > w.max_new ? 0 : (q.n * a.G + NQ - 1) / NQ; };
-  auto span_of = [&](const Seq& q, int32_t t) {
+  auto span_of = [&](const Seq& q, int32_t s, int32_t t) {
     const int32_t f0 = t * NQ, f1 = min(f0 + NQ, q.n * a.G);
-    return key_span<16>(a, q.a + f0 / a.G, q.a + (f1 - 1) / a.G);
+    KeySpan k = key_span<16>(a, q.a + f0 / a.Gp, q.a + (f1 - 1) / a.Gp);
+    if (b.from) k.b0 = __ldcg(b.from + s) >> 4;
+    return k;
   };
   const int32_t worker0 = static_cast<int32_t>(blockIdx.x) * kw;
   const int64_t share = find_shares<kFewBlock, kFewWarps>(
@@ -193,7 +196,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
         if (blockIdx.x == 0) bits |= err;
         int64_t n = 0;
         if (w.whole) return static_cast<int64_t>(tiles_of(q)) * n_groups;
-        for (int32_t t = 0; t < tiles_of(q); ++t) n += span_of(q, t).steps() + kUnitCost;
+        for (int32_t t = 0; t < tiles_of(q); ++t) n += span_of(q, s, t).steps() + kUnitCost;
         return n * n_groups;
       });
   const int32_t worker = worker0 + wk;
@@ -229,7 +232,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
     q = seq_of(p, b, s, err);
     int64_t off = at.off;
     for (;;) {
-      span = span_of(q, tile);
+      span = span_of(q, s, tile);
       const int64_t n = static_cast<int64_t>(w.whole ? 1 : span.steps() + kUnitCost) * n_groups;
       if (off < n) break;
       off -= n;
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
     const int32_t h = group * w.hw + hw;
     const int32_t f0 = tile * NQ;
     const int32_t nf = min(NQ, q.n * a.G - f0);  // rows of the tile
-    const int32_t i0 = q.a + f0 / a.G, i1 = q.a + (f0 + nf - 1) / a.G;
+    const int32_t i0 = q.a + f0 / a.Gp, i1 = q.a + (f0 + nf - 1) / a.Gp;
 
     // ---- issue of a step's loads
     // the lane's piece of row 0 of a page, in the layer's block of keys; rows are below 2^31
@@ -421,7 +424,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
 #pragma unroll
       for (int e = 0; e < 2; ++e) {  // columns 2c and 2c + 1 of the scores
         cq[nt][e] = __shfl_sync(kFull, row_c, (2 * c + e) * 4);
-        pos[nt][e] = q.a + min(f0 + nt * 8 + 2 * c + e, f0 + nf - 1) / a.G;
+        pos[nt][e] = q.a + min(f0 + nt * 8 + 2 * c + e, f0 + nf - 1) / a.Gp;
       }
     }
 
@@ -733,7 +736,46 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
         sum[nt][e] += __shfl_xor_sync(kFull, sum[nt][e], 16);
       }
     const bool whole = step0 == 0 && end == n_steps;
-    if (whole) {
+    if (whole && a.state) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int col = nt * 8 + 2 * c + e;
+          if (col >= nf) continue;
+          const int64_t at = (q.row0 + (f0 + col) / a.G) * a.Q + h * a.G + (f0 + col) % a.G;
+#pragma unroll
+          for (int mt = 0; mt < Sh::kMT; mt += 2)
+            *reinterpret_cast<float4*>(a.state + at * D + element(mt)) =
+                make_float4(o[mt][nt][e], o[mt][nt][e + 2], o[mt + 1][nt][e], o[mt + 1][nt][e + 2]);
+          if (g == 0) {
+            a.state[a.state_rows * D + at] = high[nt][e] == -INFINITY ? kNoRef : low[nt][e];
+            a.state[a.state_rows * (D + 1) + at] = sum[nt][e];
+          }
+        }
+    } else if (whole) {
+      if (a.prior && __ldcg(b.from + s) != 0) {  // what the rows have summed up before, under one reference
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int32_t f = f0 + min(nt * 8 + 2 * c + e, nf - 1);
+            const int64_t at = (q.row0 + f / a.G) * a.Q + h * a.G + f % a.G;
+            const float ref = __ldcg(a.prior + a.state_rows * D + at), own = high[nt][e] == -INFINITY ? kNoRef : low[nt][e];
+            const float top = fmaxf(ref, own), k1 = ex2(own - top), k2 = ex2(ref - top);
+            sum[nt][e] = sum[nt][e] * k1 + __ldcg(a.prior + a.state_rows * (D + 1) + at) * k2;
+            low[nt][e] = top;
+#pragma unroll
+            for (int mt = 0; mt < Sh::kMT; mt += 2) {
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(a.prior + at * D + element(mt)));
+              o[mt][nt][e] = o[mt][nt][e] * k1 + x.x * k2;
+              o[mt][nt][e + 2] = o[mt][nt][e + 2] * k1 + x.y * k2;
+              o[mt + 1][nt][e] = o[mt + 1][nt][e] * k1 + x.z * k2;
+              o[mt + 1][nt][e + 2] = o[mt + 1][nt][e + 2] * k1 + x.w * k2;
+            }
+          }
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -806,28 +848,31 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
         q = seq_of(p, b, s, err);
       }
       if (s >= b.n_seqs) break;
-      span = span_of(q, tile);
+      span = span_of(q, s, tile);
     }
   }
   if (worker < w.n_workers && hw == 0 && lane == 0) w.rec[worker] = rec;
   store_bits(p, bits);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // whoever waits for this kernel waits for those before it
 }
 
 template <class C, int D, int NT>
-cudaError_t launch(const DevPool& p, const Batch& b, const AttendArgs& a, Split w, cudaStream_t s) {
+cudaError_t launch(const DevPool& p, const Batch& b, const AttendArgs& a, Split w, bool after, cudaStream_t s) {
   using Sh = FewShape<C, D>;
   constexpr bool kOne = std::is_same_v<C, CodeE4M3> || std::is_same_v<C, CodeE2M1>;  // one part will do for a bf16 output
   const bool one = kOne && a.type == KV_TYPE_BF16;
   auto kernel = p.ps % 16 == 0 ? (one ? k_attend_few<C, D, NT, true, !kOne> : k_attend_few<C, D, NT, true, true>)
                                : (one ? k_attend_few<C, D, NT, false, !kOne> : k_attend_few<C, D, NT, false, true>);
-  kernel<<<w.blocks, kFewBlock, kFewWarps * (w.deep ? Sh::kDeep : Sh::kStages) * Sh::kStage, s>>>(p, b, a, w);
+  const int smem = kFewWarps * (w.deep ? Sh::kDeep : Sh::kStages) * Sh::kStage;
+  if (after) return launch_overlapped(kernel, dim3(w.blocks), kFewBlock, smem, s, p, b, a, w);
+  kernel<<<w.blocks, kFewBlock, smem, s>>>(p, b, a, w);
   return cudaGetLastError();
 }
 
 template <class C>
-cudaError_t launch_c(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, int nt, cudaStream_t s) {
-  if (a.D == 64) return nt == 1 ? launch<C, 64, 1>(p, b, a, w, s) : launch<C, 64, 2>(p, b, a, w, s);
-  return nt == 1 ? launch<C, 128, 1>(p, b, a, w, s) : launch<C, 128, 2>(p, b, a, w, s);
+cudaError_t launch_c(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, int nt, bool after, cudaStream_t s) {
+  if (a.D == 64) return nt == 1 ? launch<C, 64, 1>(p, b, a, w, after, s) : launch<C, 64, 2>(p, b, a, w, after, s);
+  return nt == 1 ? launch<C, 128, 1>(p, b, a, w, after, s) : launch<C, 128, 2>(p, b, a, w, after, s);
 }
 
 template <class C, int D, int NT>

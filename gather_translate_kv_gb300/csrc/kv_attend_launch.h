@@ -34,6 +34,7 @@ struct Split {
   int32_t out_wide;   // out is aligned for the kernel's widest stores
   int32_t deep;       // the longer ring
   int32_t whole;      // units are not cut: nothing to join
+  int32_t first;      // the sequences come from the kernel before this one
   float lift;         // log2 of the weights' lift
 };
 
@@ -45,17 +46,27 @@ inline int64_t split_record_bytes(int64_t workers) {
 // of 16).
 cudaError_t prepare_attend_few(int32_t D, Kind kind, bool p16);
 cudaError_t prepare_few4(int32_t D, bool p16);  // kv_attend_few4.cu
-cudaError_t launch_few4(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, int nt, cudaStream_t s);
+cudaError_t launch_few4(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, int nt, bool after, cudaStream_t s);
 cudaError_t prepare_attend_tile(int32_t D, Kind kind, bool p16);
 cudaError_t prepare_tile4(int32_t D);  // kv_attend_tile4.cu
 cudaError_t launch_tile4(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, bool after, cudaStream_t s);
 int64_t attend_few_workspace(int32_t D, int sm_count);
 int64_t attend_tile_workspace(int32_t D, int sm_count);
+// How a kernel follows the one before it: at its end, over its tail, or over its tail but reading its result first.
+enum class Launch { kPlain, kAfter, kFirst };
 // Sequences of at most max_new, and of at least min_new, new tokens; *w says
-// what is left to join. `after` marks a launch that may overlap the one before it.
+// what is left to join.
 cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, int32_t max_new,
-                              void* workspace, int sm_count, Split* w, cudaStream_t s);
+                              void* workspace, int sm_count, Launch how, Split* w, cudaStream_t s);
 cudaError_t launch_attend_tile(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, int32_t min_new,
-                               void* workspace, int sm_count, bool after, Split* w, cudaStream_t s);
+                               void* workspace, int sm_count, Launch how, Split* w, cudaStream_t s);
+// Both, each for the sequences on its side of few_rows_of, and the join (kv_attend.cu).
+cudaError_t launch_tiles(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, void* workspace, int sm_count,
+                         Launch how, cudaStream_t s);
+// Rows a KV head up to which a sequence is the few-rows kernel's.
+inline int32_t few_rows_of(Kind kind) { return kind == Kind::kElements ? 16 : 32; }
+inline bool has_tiles(int32_t D) { return D == 64 || D == 128; }
+cudaError_t launch_attend_join(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, const Split& few,
+                               const Split& tile, int sm_count, cudaStream_t s);
 
 }  // namespace gtkv

@@ -1,0 +1,163 @@
+// Attention of groups of sequences that share their first tokens.
+//
+// The rows of a group see its prefix alike, so the prefix is attended to once,
+// by all of them as if they were rows of one sequence: its keys and values are
+// read once for the group, and where it has many rows they fill the tiles of the
+// tensor cores (k_attend_tile) instead of 4 of their 128 rows. What a row has
+// summed up - sum of weighted values, reference, denominator - goes to the workspace
+// in 32 bits. Then every sequence attends to its own tokens (k_attend_few), takes what its rows have
+// from the prefix under a common reference,
+//   out = (o 2^(m - M) + o' 2^(m' - M)) / (l 2^(m - M) + l' 2^(m' - M)),   M = max(m, m'),
+// and writes the result. Each launch starts over the tail of the one before it.
+#include "kv_attend_launch.h"
+
+namespace gtkv {
+
+namespace {
+
+constexpr int kGroupBlock = 128;
+
+// Looks at all metadata once. own: the sequences, checked; shared: at the index of a group's first sequence with
+// rows the group as one sequence, whose rows all stand at its prefix' last token, else no rows; from: where the
+// sequences' own tokens begin. A prefix is cut to whole steps of 16 keys and ends before any
+// member's new tokens; it is shared by two sequences at least.
+__global__ void __launch_bounds__(kGroupBlock) k_share_groups(DevPool p, Batch b, const int32_t* __restrict__ group,
+                                                              const int32_t* __restrict__ prefix_len, int32_t n_groups,
+                                                              int32_t G, Seq* own, Seq* shared, int32_t* from) {
+  __shared__ int64_t row0[kGroupBlock / 32], row1[kGroupBlock / 32];
+  __shared__ int32_t start[kGroupBlock / 32], first[kGroupBlock / 32], count[kGroupBlock / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int bits = 0;
+  int bad = 0;
+  for (int32_t i = tid; i <= n_groups; i += kGroupBlock) {
+    const int32_t s = __ldg(group + i);
+    bad |= i == 0 ? s != 0 : s < __ldg(group + i - 1);
+    bad |= i == n_groups && s != b.n_seqs;
+  }
+  if (__syncthreads_or(bad)) {  // nothing is shared
+    for (int64_t s = blockIdx.x * static_cast<int64_t>(kGroupBlock) + tid; s < b.n_seqs;
+         s += static_cast<int64_t>(gridDim.x) * kGroupBlock) {
+      own[s] = seq_of(p, b, static_cast<int32_t>(s), bits);
+      shared[s] = Seq{0, 0, 0};
+      from[s] = 0;
+    }
+    store_bits(p, bits | KV_DEV_ERR_TABLE);
+    return;
+  }
+  for (int32_t g = blockIdx.x; g < n_groups; g += gridDim.x) {
+    const int32_t s0 = __ldg(group + g), s1 = __ldg(group + g + 1);
+    int64_t r0 = INT64_MAX, r1 = 0;
+    int32_t a = INT32_MAX, s_first = INT32_MAX, n = 0;
+    for (int32_t s = s0 + tid; s < s1; s += kGroupBlock) {
+      const Seq q = seq_of(p, b, s, bits);
+      own[s] = q;
+      if (q.n == 0) continue;
+      r0 = q.row0 < r0 ? q.row0 : r0;
+      r1 = q.row0 + q.n > r1 ? q.row0 + q.n : r1;
+      a = min(a, q.a);
+      s_first = min(s_first, s);
+      ++n;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const int64_t x0 = __shfl_xor_sync(kFull, r0, o), x1 = __shfl_xor_sync(kFull, r1, o);
+      r0 = x0 < r0 ? x0 : r0;
+      r1 = x1 > r1 ? x1 : r1;
+    }
+    a = __reduce_min_sync(kFull, a);
+    s_first = __reduce_min_sync(kFull, s_first);
+    n = __reduce_add_sync(kFull, n);
+    if (lane == 0) row0[warp] = r0, row1[warp] = r1, start[warp] = a, first[warp] = s_first, count[warp] = n;
+    __syncthreads();
+    r0 = INT64_MAX, r1 = 0, a = INT32_MAX, s_first = INT32_MAX, n = 0;
+#pragma unroll
+    for (int w = 0; w < kGroupBlock / 32; ++w) {
+      r0 = row0[w] < r0 ? row0[w] : r0;
+      r1 = row1[w] > r1 ? row1[w] : r1;
+      a = min(a, start[w]);
+      s_first = min(s_first, first[w]);
+      n += count[w];
+    }
+    __syncthreads();
+    int32_t prefix = min(__ldg(prefix_len + g), a) & ~15;
+    if (n < 2 || prefix < 16 || (r1 - r0) * G > INT32_MAX) prefix = 0;
+    for (int32_t s = s0 + tid; s < s1; s += kGroupBlock) {
+      from[s] = prefix;
+      shared[s] = prefix != 0 && s == s_first ? Seq{r0, prefix - 1, static_cast<int32_t>(r1 - r0)} : Seq{0, 0, 0};
+    }
+  }
+  store_bits(p, bits);
+}
+
+int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+
+struct Workspace {
+  int64_t own, shared, from, tiles, few, state, bytes;
+};
+
+Workspace workspace_of(int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int sm_count) {
+  Workspace w{};
+  auto take = [&](int64_t n) {
+    const int64_t at = w.bytes;
+    w.bytes += align256(n);
+    return at;
+  };
+  w.tiles = take(attend_workspace_bytes(0, Q, D, n_seqs, n_rows, sm_count));
+  if (!has_tiles(D)) return w;
+  w.own = take(n_seqs * static_cast<int64_t>(sizeof(Seq)));
+  w.shared = take(n_seqs * static_cast<int64_t>(sizeof(Seq)));
+  w.from = take(n_seqs * static_cast<int64_t>(sizeof(int32_t)));
+  w.few = take(attend_few_workspace(D, sm_count));
+  w.state = take(n_rows * Q * (D + 2) * 4);
+  return w;
+}
+
+// Rows a KV head and sequence, on average, past which a sequence fills tiles by itself.
+constexpr int kOwnTiles = 128;
+
+}  // namespace
+
+int64_t attend_shared_workspace_bytes(int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int sm_count) {
+  return workspace_of(Q, D, n_seqs, n_rows, sm_count).bytes;
+}
+
+cudaError_t launch_attend_shared(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, const int32_t* group,
+                                 const int32_t* prefix_len, int32_t n_groups, void* workspace, int sm_count,
+                                 cudaStream_t s) {
+  if (!has_tiles(a.D) || n_groups >= b.n_seqs || b.n_rows * a.G > kOwnTiles * static_cast<int64_t>(b.n_seqs))
+    return launch_attend(p, b, a, kind, workspace, sm_count, s);
+  const Workspace w = workspace_of(a.Q, a.D, b.n_seqs, b.n_rows, sm_count);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  Seq* own = reinterpret_cast<Seq*>(ws + w.own);
+  Seq* shared = reinterpret_cast<Seq*>(ws + w.shared);
+  int32_t* from = reinterpret_cast<int32_t*>(ws + w.from);
+  k_share_groups<<<n_groups < 2 * sm_count ? n_groups : 2 * sm_count, kGroupBlock, 0, s>>>(p, b, group, prefix_len, n_groups,
+                                                                                        a.G, own, shared, from);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  Batch bb = b;
+  AttendArgs aa = a;
+  aa.state_rows = b.n_rows * a.Q;
+  bb.seqs = shared;
+  bb.n_spans = n_groups;
+  aa.state = reinterpret_cast<float*>(ws + w.state);
+  aa.lse = nullptr;
+  aa.Gp = INT32_MAX;
+  e = launch_tiles(p, bb, aa, kind, ws + w.tiles, sm_count, Launch::kFirst, s);
+  if (e != cudaSuccess) return e;
+  bb = b;
+  bb.seqs = own;
+  bb.from = from;
+  aa.prior = aa.state;
+  aa.state = nullptr;
+  aa.lse = a.lse;
+  aa.Gp = a.G;
+  Split few{};
+  const Split none{};
+  e = launch_attend_few(p, bb, aa, kind, INT32_MAX, ws + w.few, sm_count, Launch::kAfter, &few, s);
+  if (e != cudaSuccess || few.whole) return e;
+  return launch_attend_join(p, bb, aa, kind, few, none, sm_count, s);
+}
+
+}  // namespace gtkv

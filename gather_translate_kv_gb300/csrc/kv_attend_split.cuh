@@ -265,6 +265,23 @@ __device__ __forceinline__ void join_split(const DevPool& p, const Batch& b, con
       }
     }
     if (!shared || warp == 0) {
+      const int64_t at = (rec.row0 + (rec.f0 + col) / a.G) * a.Q + (rec.head * w.hw + hw) * a.G + (rec.f0 + col) % a.G;
+      if (a.state) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) a.state[at * D + lane * E + e] = acc[e];
+        if (lane == 0) {
+          a.state[a.state_rows * D + at] = m - w.lift;
+          a.state[a.state_rows * (D + 1) + at] = sum;
+        }
+        if (shared) __syncthreads();
+        continue;
+      }
+      if (a.prior && __ldcg(b.from + rec.s) != 0) {
+        float x[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = __ldcg(a.prior + at * D + lane * E + e);
+        add(m, sum, acc, __ldcg(a.prior + a.state_rows * D + at) + w.lift, __ldcg(a.prior + a.state_rows * (D + 1) + at), x);
+      }
       const float inv = sum == 0.0f ? 0.0f : rcp(sum);
       bool bad = !(sum <= 3.402823466e38f);
       const int32_t f = rec.f0 + col;

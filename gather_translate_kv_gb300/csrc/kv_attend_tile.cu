@@ -26,7 +26,7 @@ int64_t attend_tile_workspace(int32_t D, int sm_count) {
 }
 
 cudaError_t launch_attend_tile(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, int32_t min_new,
-                               void* workspace, int sm_count, bool after, Split* out, cudaStream_t s) {
+                               void* workspace, int sm_count, Launch how, Split* out, cudaStream_t s) {
   Split w{};
   w.hw = 1;
   w.nq = kRows;
@@ -42,7 +42,9 @@ cudaError_t launch_attend_tile(const DevPool& p, const Batch& b, const AttendArg
   w.q_wide = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.q_stride % 8 == 0;
   w.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
   w.lift = kind == Kind::kElements && a.type == KV_TYPE_BF16 ? 0.0f : 6.0f;
+  w.first = how == Launch::kFirst;
   *out = w;
+  const bool after = how != Launch::kPlain;
   auto go = [&]<class C, bool P16, bool TWO>() { return launch_one<C, P16, TWO>(p, b, a, w, after, s); };
   const bool bf16 = a.type == KV_TYPE_BF16;
   if (kind == Kind::kE2M1) return launch_tile4(p, b, a, w, after, s);

@@ -118,8 +118,8 @@ struct TileWalk {
   __device__ __forceinline__ void shape() {
     g.f0 = g.tile * kRows;
     g.nf = min(kRows, g.q.n * a.G - g.f0);
-    g.i0 = g.q.a + g.f0 / a.G;
-    g.i1 = g.q.a + (g.f0 + g.nf - 1) / a.G;
+    g.i0 = g.q.a + g.f0 / a.Gp;
+    g.i1 = g.q.a + (g.f0 + g.nf - 1) / a.Gp;
     g.span = key_span<kKeys>(a, g.i0, g.i1);
   }
   __device__ __forceinline__ bool cut() {
@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
   extern __shared__ uint8_t dyn[];
   __shared__ ShareStart loc[1];
   __shared__ int64_t tmp[kTileThreads / 32];
+  if (w.first) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t base = (shared_u32(dyn) + 1023u) & ~1023u;
   uint8_t* gen = dyn + (base - shared_u32(dyn));
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
       const int32_t f = g.f0 + wt * 128 + r;
       const int32_t fc = min(f, g.f0 + g.nf - 1);
       const bool row_ok = f < g.f0 + g.nf;
-      const int32_t pos = g.q.a + fc / a.G;
+      const int32_t pos = g.q.a + fc / a.Gp;
       float c = c0;
       float ref = kNoRef;
       float2 sum = make_float2(0.0f, 0.0f);
@@ -463,7 +464,24 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
       const bool whole = g.step0 == 0 && g.end == g.span.steps();
       const int64_t orow = g.q.row0 + fc / a.G;
       const int32_t qh = g.h * a.G + fc % a.G;
-      if (whole) {
+      if (whole && a.state) {
+        float* to = a.state + (orow * a.Q + qh) * D;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t raw[32];
+          tmem_load32(tO + 32 * k, raw);
+          tmem_wait_ld(raw);
+          if (row_ok) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<uint4*>(to + 32 * k)[e] = make_uint4(raw[4 * e], raw[4 * e + 1], raw[4 * e + 2], raw[4 * e + 3]);
+          }
+        }
+        if (row_ok) {
+          a.state[a.state_rows * D + orow * a.Q + qh] = ref - kLift;
+          a.state[a.state_rows * (D + 1) + orow * a.Q + qh] = total;
+        }
+      } else if (whole) {
         bool bad = !(total <= 3.402823466e38f);
         const float inv = bad ? NAN : total == 0.0f ? 0.0f : rcp(total);
         uint16_t* out = static_cast<uint16_t*>(a.out) + (orow * a.Q + qh) * D;

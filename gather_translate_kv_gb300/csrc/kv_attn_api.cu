@@ -83,6 +83,32 @@ int check_rotary(const kv_pool_t* pool, const kv_rotary* r) {
   return aligned(r->cos_sin_dev, 4) && aligned(r->positions_dev, 4) ? KV_OK : KV_ERR_ALIGN;
 }
 
+// What the two attention calls check alike; fills *b and *a. Nothing to do: KV_OK with b->n_rows = 0.
+int enter_attend(const kv_pool_t* pool, int32_t layer, const kv_batch* batch, int32_t type, const void* q_dev,
+                 int64_t q_stride, int32_t q_heads, void* out_dev, float* lse_dev, float scale, int32_t window,
+                 int32_t sinks, const float* scales_dev, const void* workspace_dev, int64_t workspace_bytes,
+                 int (*need_of)(const kv_pool_t*, int32_t, int32_t, int64_t, int64_t*), gtkv::Batch* b,
+                 gtkv::AttendArgs* a) {
+  int rc = enter(pool, layer, batch, b);
+  if (rc != KV_OK) return rc;
+  const int32_t H = pool->desc.head_num, D = pool->desc.head_dim, it = pool->desc.itemsize;
+  if ((type != KV_TYPE_BF16 && type != KV_TYPE_F16) || (it != 1 && it != 2)) return KV_ERR_INVALID;
+  if ((rc = check_scales(pool, scales_dev)) != KV_OK) return rc;
+  if (q_heads < 1 || q_heads > (1 << 16) || q_heads % H != 0 || D > 256 || !isfinite(scale) || window < 0 || sinks < 0)
+    return KV_ERR_INVALID;
+  int64_t need = 0;
+  if ((rc = need_of(pool, q_heads, batch->n_seqs, batch->n_rows, &need)) != KV_OK) return rc;
+  if (b->n_rows == 0) return KV_OK;
+  if (q_dev == nullptr || out_dev == nullptr || workspace_dev == nullptr || workspace_bytes < need)
+    return KV_ERR_INVALID;
+  if (b->n_rows > 1 && q_stride < static_cast<int64_t>(q_heads) * D) return KV_ERR_INVALID;
+  if (!aligned(q_dev, 2) || !aligned(out_dev, 2) || !aligned(lse_dev, 4) || !aligned(workspace_dev, 16))
+    return KV_ERR_ALIGN;
+  *a = gtkv::AttendArgs{q_dev, out_dev, lse_dev, scales_dev, q_stride, scale * 1.4426950408889634f, window, sinks,
+                        H,     q_heads, D,       q_heads / H, layer,   type, q_heads / H};
+  return KV_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -136,24 +162,37 @@ int kv_attend_layer(const kv_pool_t* pool, int32_t layer, const kv_batch* batch,
                     kv_stream_t stream) {
   Range nvtx("kv_attend_layer");
   gtkv::Batch b;
-  int rc = enter(pool, layer, batch, &b);
-  if (rc != KV_OK) return rc;
-  const int32_t H = pool->desc.head_num, D = pool->desc.head_dim, it = pool->desc.itemsize;
-  if ((type != KV_TYPE_BF16 && type != KV_TYPE_F16) || (it != 1 && it != 2)) return KV_ERR_INVALID;
-  if ((rc = check_scales(pool, scales_dev)) != KV_OK) return rc;
-  if (q_heads < 1 || q_heads > (1 << 16) || q_heads % H != 0 || D > 256 || !isfinite(scale) || window < 0 || sinks < 0)
-    return KV_ERR_INVALID;
-  int64_t need = 0;
-  if ((rc = kv_attend_workspace_bytes(pool, q_heads, batch->n_seqs, batch->n_rows, &need)) != KV_OK) return rc;
-  if (b.n_rows == 0) return KV_OK;
-  if (q_dev == nullptr || out_dev == nullptr || workspace_dev == nullptr || workspace_bytes < need)
-    return KV_ERR_INVALID;
-  if (b.n_rows > 1 && q_stride < static_cast<int64_t>(q_heads) * D) return KV_ERR_INVALID;
-  if (!aligned(q_dev, 2) || !aligned(out_dev, 2) || !aligned(lse_dev, 4) || !aligned(workspace_dev, 16))
-    return KV_ERR_ALIGN;
-  const gtkv::AttendArgs a{q_dev, out_dev, lse_dev, scales_dev, q_stride, scale * 1.4426950408889634f, window, sinks,
-                           H,     q_heads, D,       q_heads / H, layer,   type};
+  gtkv::AttendArgs a;
+  const int rc = enter_attend(pool, layer, batch, type, q_dev, q_stride, q_heads, out_dev, lse_dev, scale, window, sinks,
+                              scales_dev, workspace_dev, workspace_bytes, kv_attend_workspace_bytes, &b, &a);
+  if (rc != KV_OK || b.n_rows == 0) return rc;
   return launched(gtkv::launch_attend(pool->dev, b, a, kind_of(pool), workspace_dev, pool->sm_count, as_stream(stream)));
+}
+
+int kv_attend_shared_workspace_bytes(const kv_pool_t* pool, int32_t q_heads, int32_t n_seqs, int64_t n_rows,
+                                     int64_t* bytes) {
+  const int rc = kv_attend_workspace_bytes(pool, q_heads, n_seqs, n_rows, bytes);
+  if (rc != KV_OK) return rc;
+  if (n_rows > (int64_t(1) << 40)) return KV_ERR_INVALID;  // (n_rows * q_heads * head_dim stays below 2^63)
+  *bytes = gtkv::attend_shared_workspace_bytes(q_heads, pool->desc.head_dim, n_seqs, n_rows, pool->sm_count);
+  return KV_OK;
+}
+
+int kv_attend_shared_layer(const kv_pool_t* pool, int32_t layer, const kv_batch* batch, const kv_prefix_groups* groups,
+                           int32_t type, const void* q_dev, int64_t q_stride, int32_t q_heads, void* out_dev,
+                           float* lse_dev, float scale, const float* scales_dev, void* workspace_dev,
+                           int64_t workspace_bytes, kv_stream_t stream) {
+  Range nvtx("kv_attend_shared_layer");
+  gtkv::Batch b;
+  gtkv::AttendArgs a;
+  if (groups == nullptr || groups->n_groups < 0 || groups->reserved != 0) return KV_ERR_INVALID;
+  const int rc = enter_attend(pool, layer, batch, type, q_dev, q_stride, q_heads, out_dev, lse_dev, scale, 0, 0, scales_dev,
+                              workspace_dev, workspace_bytes, kv_attend_shared_workspace_bytes, &b, &a);
+  if (rc != KV_OK || b.n_rows == 0) return rc;
+  if (groups->n_groups < 1 || groups->group_dev == nullptr || groups->prefix_len_dev == nullptr) return KV_ERR_INVALID;
+  if (!aligned(groups->group_dev, 4) || !aligned(groups->prefix_len_dev, 4)) return KV_ERR_ALIGN;
+  return launched(gtkv::launch_attend_shared(pool->dev, b, a, kind_of(pool), groups->group_dev, groups->prefix_len_dev,
+                                             groups->n_groups, workspace_dev, pool->sm_count, as_stream(stream)));
 }
 
 int kv_gather_layer_scaled(const kv_pool_t* pool, int32_t layer, const kv_batch* batch, const float* scales_dev,

@@ -36,6 +36,10 @@ struct AttendArgs {
   int32_t H, Q, D, G;   // G = Q / H
   int32_t layer;
   int32_t type;         // KV_TYPE_BF16 or KV_TYPE_F16, of q and out
+  int32_t Gp;           // row f of a sequence is at its position a + f / Gp: G, or past all rows where they share one
+  float* state = nullptr;        // not out and lse but what a row has summed up so far is written, [n_rows, Q] rows
+  const float* prior = nullptr;  // what rows have summed up before; one of the two at most
+  int64_t state_rows = 0;        // n_rows * Q: sums [state_rows][D], references [state_rows], denominators [state_rows]
 };
 
 // Set-up of the kernels on the current device (their shared-memory limits), of those
@@ -44,6 +48,11 @@ struct AttendArgs {
 cudaError_t prepare_append(const kv_pool_desc& d);
 cudaError_t prepare_attend(const kv_pool_desc& d);
 int64_t attend_workspace_bytes(int32_t H, int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int sm_count);
+// Attention of groups of sequences that share their first tokens.
+int64_t attend_shared_workspace_bytes(int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int sm_count);
+cudaError_t launch_attend_shared(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, const int32_t* group,
+                                 const int32_t* prefix_len, int32_t n_groups, void* workspace, int sm_count,
+                                 cudaStream_t s);
 cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, void* workspace,
                           int sm_count, cudaStream_t s);
 

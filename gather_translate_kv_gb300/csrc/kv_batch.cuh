@@ -12,6 +12,8 @@
 
 namespace gtkv {
 
+struct Seq;
+
 struct Batch {
   const int32_t* table;
   const int32_t* start;
@@ -21,17 +23,26 @@ struct Batch {
   int32_t n_seqs;
   int32_t max_pages;
   int32_t kernel_facing;
+  const Seq* seqs = nullptr;      // attention of shared prefixes: the sequences, checked already (kv_attend_shared.cu)
+  int32_t n_spans = 0;            // sequences among them that hold rows, on average's account (0: n_seqs)
+  const int32_t* from = nullptr;  // and the first tokens that they attend to themselves, multiples of 16
 };
+
+inline int64_t spans_of(const Batch& b) { return b.n_spans ? b.n_spans : b.n_seqs; }
 
 // A sequence's part of the step: tokens [a, a + n) are rows row0 + (0 .. n).
 // n = 0 for a sequence without tokens or with inconsistent metadata.
-struct Seq {
+struct alignas(16) Seq {
   int64_t row0;
   int32_t a;
   int32_t n;
 };
 
 __device__ __forceinline__ Seq seq_of(const DevPool& p, const Batch& b, int32_t s, int& bits) {
+  if (b.seqs) {
+    const int4 v = __ldcg(reinterpret_cast<const int4*>(b.seqs) + s);
+    return Seq{static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(v.y)) << 32 | static_cast<uint32_t>(v.x)), v.z, v.w};
+  }
   const int64_t a = b.start ? __ldg(b.start + s) : 0;
   const int64_t e = __ldg(b.len + s);
   const int64_t c0 = __ldg(b.cu + s), c1 = __ldg(b.cu + s + 1);

@@ -156,6 +156,37 @@ int kv_attend_layer(const kv_pool_t* pool, int32_t layer, const kv_batch* batch,
                     int32_t sinks, const float* scales_dev, void* workspace_dev, int64_t workspace_bytes,
                     kv_stream_t stream);
 
+/* Groups of sequences that share their first tokens (a system prompt, a
+ * document, the prompt of several answers): sequences [group[g], group[g + 1])
+ * of a batch hold the same first prefix_len[g] tokens in the same pages, in
+ * whole pages or not, so their rows of the block table begin alike. Every
+ * sequence belongs to one group; a group may be a single sequence and a prefix
+ * may be 0. */
+typedef struct {
+  const int32_t* group_dev;      /* [n_groups + 1], non-decreasing from 0 to n_seqs */
+  const int32_t* prefix_len_dev; /* [n_groups] tokens */
+  int32_t n_groups;
+  int32_t reserved;              /* must be 0 */
+} kv_prefix_groups;
+
+/* kv_attend_layer (without window or first tokens) of a batch whose sequences
+ * share prefixes: the same result, but the tokens of a prefix are read and
+ * attended to once for all rows of its group, through the table row of the group's first sequence
+ * that has new tokens. A prefix that reaches into a member's new tokens counts
+ * up to the first of them, whatever is past a multiple of 16 tokens counts as the
+ * members' own, and head sizes other than 64 and 128 share nothing. Groups that are not what is
+ * said above (KV_DEV_ERR_TABLE) are answered as if nothing were shared; a
+ * prefix that its members' tables do not share gives its rows the first one's tokens.
+ *  workspace_dev  kv_attend_shared_workspace_bytes() bytes, else as in
+ *            kv_attend_layer: 122 MB for a head_dim of 128 on 152 SMs and
+ *            4 * (head_dim + 2) bytes for every row and query head. */
+int kv_attend_shared_workspace_bytes(const kv_pool_t* pool, int32_t q_heads, int32_t n_seqs, int64_t n_rows,
+                                     int64_t* bytes);
+int kv_attend_shared_layer(const kv_pool_t* pool, int32_t layer, const kv_batch* batch, const kv_prefix_groups* groups,
+                           int32_t type, const void* q_dev, int64_t q_stride, int32_t q_heads, void* out_dev,
+                           float* lse_dev, float scale, const float* scales_dev, void* workspace_dev,
+                           int64_t workspace_bytes, kv_stream_t stream);
+
 /* Gather of an 8-bit or a 4-bit pool's values: out[row] = code * scale of the batch's
  * tokens, one layer's K and V as [n_rows, H, D] of `type` (rounded to nearest
  * even; BF16 holds every product with a power-of-two scale exactly, up to its

@@ -54,3 +54,34 @@ def test_plain_codes():
     assert scales.tolist() == [[0x78]] and codes[0, :2].tolist() == [0xD7, 0x02] and not bad.any()
     assert ref4.encode(np.full((1, 16), 1e9, np.float32))[1].tolist() == [[0xE0]]
     assert ref4.encode(np.zeros((1, 16), np.float32))[1].tolist() == [[0]]
+
+
+def test_prefix_groups_match_the_header(tmp_path):
+    import ctypes
+    import subprocess
+
+    from gather_translate_kv_gb300 import build
+
+    fields = [f for f, _ in gt.kv_prefix_groups_t._fields_]
+    src = tmp_path / "t.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "kv_attention.h"\nint main(void) {' +
+                   "".join(f'printf("%zu\\n", offsetof(kv_prefix_groups, {f}));' for f in fields) +
+                   'printf("%zu\\n", sizeof(kv_prefix_groups));return 0;}\n')
+    exe = tmp_path / "t"
+    subprocess.check_call(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-I", build.INCLUDE, str(src), "-o", str(exe)])
+    got = list(map(int, subprocess.check_output([str(exe)], text=True).split()))
+    assert got == [getattr(gt.kv_prefix_groups_t, f).offset for f in fields] + [ctypes.sizeof(gt.kv_prefix_groups_t)]
+
+
+def test_shared_calls_without_a_pool_are_refused():
+    import ctypes
+
+    L, n = gt.lib(), ctypes.c_int64()
+    vp = ctypes.c_void_p
+    g = gt.kv_prefix_groups_t(16, 16, 1, 0)
+    b = gt.kv_batch_t()
+    assert L.kv_attend_shared_workspace_bytes(None, 1, 1, 1, ctypes.byref(n)) == -1
+    assert L.kv_attend_shared_layer(None, 0, ctypes.addressof(b), ctypes.addressof(g), 1, vp(16), 1, 1, vp(16), None, 1.0,
+                                    None, vp(16), 1, None) == -1
+    assert L.kv_attend_shared_layer(None, 0, ctypes.addressof(b), None, 1, vp(16), 1, 1, vp(16), None, 1.0, None, vp(16),
+                                    1, None) == -1

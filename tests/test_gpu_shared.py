@@ -1,0 +1,359 @@
+"""Attention of sequences that share prefixes (kv_attend_shared_layer) on the
+GPU, against the plain 64-bit form of attention_ref.py, which knows of no
+sharing. Bounds as for kv_attend_layer (test_gpu_attention.py, test_gpu_cache4.py): joining
+two sums in 32 bits adds 2^-22 of the mean of |v|, which the 2^-12 of the scores cover.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import attention_ref as ref
+import cache4_ref as ref4
+import gather_translate_kv_gb300 as gt
+from test_gpu_attention import T, U, Dev, _built  # noqa: F401 (fixture)
+from test_gpu_cache4 import Dev4
+
+pytestmark = pytest.mark.gpu
+
+CACHES = [("bf16", "bf16"), ("fp16", "fp16"), ("e4m3", "bf16"), ("e4m3", "fp16"), ("e2m1", "bf16"), ("e2m1", "fp16")]
+
+# groups: (prefix, [(own tokens, new tokens), ...])
+GROUPS = {
+    "one": [(64, [(1, 1), (1, 1)])],
+    "decode": [(200, [(1, 1), (17, 1), (64, 1), (5, 1)]), (0, [(40, 1)]), (33, [(3, 1), (9, 1), (1, 1)])],
+    "long": [(1500, [(3, 1), (40, 1)])],
+    "drafts": [(130, [(5, 3), (9, 4), (2, 1), (30, 5)]), (16, [(9, 2), (4, 4)])],
+    "many": [(300, [(1 + 7 * i % 50, 1 + i % 2) for i in range(40)]), (150, [(4, 1)] * 9)],
+    "mixed": [(100, [(30, 1), (0, 0), (3, 3)]), (50, [(0, 0), (7, 7)]), (48, [(0, 0), (0, 0)]), (15, [(4, 1), (4, 2)])],
+    "alone": [(100, [(5, 1)]), (70, [(6, 2)]), (0, [(3, 1)])],
+    "chunks": [(260, [(40, 40), (70, 33), (90, 20)])],
+}
+
+
+class Shared:
+    """A World whose groups share their first tokens: whole pages by the table, the
+    rest of the last one by its contents."""
+
+    def __init__(self, seed, groups, cache, *, gap=False, **kw):
+        lens = [p + a for p, members in groups for a, _ in members]
+        news = [n for _, members in groups for _, n in members]
+        w = ref4.world(seed, lens, news, gap=gap, **kw) if cache == "e2m1" else ref.world(seed, lens, news, cache=cache,
+                                                                                        gap=gap, **kw)
+        self.w, self.cache = w, cache
+        self.group, self.prefix = [0], []
+        for p, members in groups:
+            s0 = self.group[-1]
+            full = p // w.ps
+            for s in range(s0 + 1, s0 + len(members)):
+                w.table[s, :full] = w.table[s0, :full]
+                if p % w.ps:
+                    a, b = int(w.table[s0, full]), int(w.table[s, full])
+                    view = w.rows_view() if cache == "e2m1" else w.view()
+                    view[b, :, :, : p % w.ps] = view[a, :, :, : p % w.ps]
+                    if w.scales is not None:
+                        w.scales[b] = w.scales[a]
+            self.group.append(s0 + len(members))
+            self.prefix.append(p)
+
+    def dev(self, kernel_facing=False):
+        return (Dev4 if self.cache == "e2m1" else Dev)(self.w, kernel_facing)
+
+    def groups(self, group=None, prefix=None):
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        return gt.kv_prefix_groups(i32(self.group if group is None else group),
+                                   i32(self.prefix if prefix is None else prefix))
+
+
+def attend(d, groups, layer, q, scale, lse=None, stream=None):
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    ws = torch.full((gt.kv_attend_shared_workspace_bytes(d.pool, q.shape[1], d.w.S, d.w.n_rows),), 0xFF,
+                    dtype=torch.uint8, device="cuda")
+    gt.kv_attend_shared_layer(d.pool, layer, d.batch, groups, q, out, scale, ws, scales=d.scales, lse=lse, stream=stream)
+    return out
+
+
+def queries(w, Q, dtype, seed=0):
+    return torch.randn(w.n_rows, Q, w.D, generator=torch.Generator().manual_seed(seed + 77)).to(T[dtype])
+
+
+def check(sh, Q, dtype, *, layer=1, kernel_facing=False, group=None, prefix=None, error=0):
+    w = sh.w
+    d = sh.dev(kernel_facing)
+    q = queries(w, Q, dtype)
+    lse = torch.full((w.n_rows, Q), 7.0, device="cuda")
+    out = attend(d, sh.groups(group, prefix), layer, q.cuda(), w.D ** -0.5, lse=lse)
+    assert d.error() == error
+    want, wlse, size = ref.attend(w, layer, q, w.D ** -0.5)
+    rows = [r for r, _, _ in w.rows()]
+    rest = sorted(set(range(w.n_rows)) - set(rows))
+    got = out.cpu().double()
+    assert (got[rest] == 7.0).all() and (lse.cpu()[rest] == 7.0).all(), "rows of no token were written"
+    u = U[T[dtype]]
+    tol = u * want.abs() + (u + 2.0 ** -12) * size + (2.0 ** -24 if dtype == "fp16" else 0.0)
+    bad = ~((got - want).abs() <= tol)[rows]
+    assert not bad.any(), (int(bad.sum()), bad.numel(), np.argwhere(bad.numpy())[:3].tolist(),
+                           float(((got - want).abs() / tol)[rows].nan_to_num(1e9).max()))
+    e, wl = lse.cpu().double()[rows], wlse[rows]
+    assert torch.equal(e.isinf(), wl.isinf())
+    fin = ~wl.isinf()
+    assert ((e - wl).abs()[fin] <= 2.0 ** -12 * wl.abs().clamp(min=1)[fin]).all()
+    return out
+
+
+@pytest.mark.parametrize("cache,dtype", CACHES)
+@pytest.mark.parametrize("groups", list(GROUPS))
+@pytest.mark.parametrize("D", [64, 128])
+def test_shared(cache, dtype, groups, D):
+    check(Shared(len(groups) + D, GROUPS[groups], cache, D=D, gap=groups in ("mixed", "many")), 8, dtype)
+
+
+@pytest.mark.parametrize("cache,dtype", CACHES[1::2])
+@pytest.mark.parametrize("ps", [1, 4, 7, 16, 24, 64, 256])
+@pytest.mark.parametrize("groups", ["decode", "drafts", "many"])
+def test_shared_page_sizes(cache, dtype, ps, groups):
+    check(Shared(ps, GROUPS[groups], cache, ps=ps), 6, dtype, kernel_facing=ps % 2 == 0)
+
+
+@pytest.mark.parametrize("cache,dtype", [CACHES[0], CACHES[3], CACHES[4]])
+@pytest.mark.parametrize("H,G", [(1, 1), (1, 71), (2, 1), (3, 5), (4, 2), (8, 8), (5, 16), (2, 17)])
+def test_shared_head_layouts(cache, dtype, H, G):
+    D = 128 if cache == "e2m1" and H % 2 else 64
+    check(Shared(H * 100 + G, [(70, [(4, 1), (9, 2), (3, 3)]), (20, [(5, 1), (1, 1)])], cache, H=H, D=D), H * G, dtype)
+
+
+@pytest.mark.parametrize("cache,dtype", [CACHES[0], CACHES[2], CACHES[5]])
+@pytest.mark.parametrize("D", [16, 48, 80, 256])
+def test_shared_other_head_sizes(cache, dtype, D):
+    check(Shared(D, GROUPS["drafts"], cache, D=D, H=1), 2, dtype)
+
+
+@pytest.mark.parametrize("cache,dtype", CACHES[::2])
+def test_shared_tombstones(cache, dtype):
+    """Cleared pages in a prefix, a prefix that is cleared whole, own pages that are."""
+    sh = Shared(5, [(200, [(9, 1), (40, 3), (3, 1)]), (64, [(5, 1), (4, 4)]), (96, [(9, 1), (20, 2)])], cache)
+    w = sh.w
+    w.table[0:3, 3] = -1
+    w.table[0:3, 7] = 0
+    w.table[3:5, :4] = -1
+    w.table[5, 6] = -1   # nothing of its own
+    check(sh, 4, dtype)
+    w.table[5:7] = -1    # nothing at all
+    check(sh, 4, dtype)
+
+
+def test_shared_prefixes_that_reach_into_new_tokens():
+    """A prefix counts up to the members' first new token, in steps of 16 tokens; a negative one shares nothing."""
+    sh = Shared(6, GROUPS["drafts"], "bf16")
+    check(sh, 4, "bf16", prefix=[1000, 2 ** 31 - 1])
+    check(sh, 4, "bf16", prefix=[-5, 0])
+    check(sh, 4, "bf16", prefix=[17, 15])
+    check(sh, 4, "bf16", group=[0, 0, 4, 4, 6], prefix=[7, 130, 9, 16])  # empty groups
+
+
+@pytest.mark.parametrize("group", [[0, 4, 5], [1, 4, 6], [0, 7, 6], [0, -1, 6], [0, 4, 2 ** 31 - 1]])
+def test_shared_groups_that_are_no_groups(group):
+    """An error bit, and the answer of a batch that shares nothing."""
+    sh = Shared(7, GROUPS["drafts"], "bf16")
+    check(sh, 4, "bf16", group=group, error=gt.KV_DEV_ERR_TABLE)
+
+
+@pytest.mark.parametrize("cache,dtype", [CACHES[0], CACHES[2], CACHES[4]])
+@pytest.mark.parametrize("members", [3, 40])
+def test_shared_value_that_is_not_finite(cache, dtype, members):
+    """One element (or block) of one value of a prefix: NaN for every row of its group, there and nowhere else."""
+    sh = Shared(13, [(150, [(5, 1)] * members), (64, [(4, 2), (6, 1)])], cache)
+    w = sh.w
+    q = queries(w, w.H, dtype)
+    clean = attend(sh.dev(), sh.groups(), 1, q.cuda(), 0.125)
+    for at in (0, 77, 143, 149):  # the last: the tokens past a multiple of 16
+        keep = w.raw.clone()
+        for s in {0} if at < 144 else range(members):
+            pg, off = int(w.table[s, at // w.ps]), at % w.ps
+            if cache == "e4m3":
+                w.view().view(torch.uint8)[pg, 1, 1, off, 0, 9] = 0x7F
+            elif cache == "e2m1":
+                w.scale_bytes()[pg, 1, 1, off, 0, 0] = 0xFF
+            else:
+                w.view()[pg, 1, 1, off, 0, 9] = float("nan")
+        out = attend(sh.dev(), sh.groups(), 1, q.cuda(), 0.125)
+        want = torch.zeros(out.shape, dtype=torch.bool)
+        want[:members, 0, slice(0, 16) if cache == "e2m1" else 9] = True
+        assert torch.equal(out.isnan().cpu(), want)
+        rest = ~want.any(-1).cuda()
+        assert torch.equal(out[rest], clean[rest])
+        w.raw = keep
+
+
+@pytest.mark.parametrize("cache,dtype", [CACHES[0], CACHES[3], CACHES[4]])
+@pytest.mark.parametrize("which", [0, 1])
+def test_shared_infinite_keys_and_values(cache, dtype, which):
+    """Whatever is not finite in a prefix gives what kv_attend_layer gives."""
+    sh = Shared(14, [(160, [(5, 1)] * 5)], cache)
+    w = sh.w
+    pg = int(w.table[0, 3])
+    if cache == "e4m3":
+        w.view().view(torch.uint8)[pg, 1, which, 5] = 0x7F
+    elif cache == "e2m1":
+        w.scale_bytes()[pg, 1, which, 5] = 0xE1
+    else:
+        w.view()[pg, 1, which, 5] = float("inf")
+    q = queries(w, 4, dtype).cuda()
+    d = sh.dev()
+    got, want = attend(d, sh.groups(), 1, q, 0.125), d.attend(1, q, 0.125)
+    assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
+    assert got.isfinite().logical_not().any()
+
+
+def test_shared_inconsistent_members():
+    """A member whose metadata is inconsistent takes no part; the others keep their prefix."""
+    for which, at, value in ((1, 1, 10 ** 6), (3, 1, -4), (3, 0, -1), (1, 3, -1)):
+        sh = Shared(8, [(80, [(4, 2)] * 4), (32, [(5, 1), (7, 2)])], "bf16")
+        w = sh.w
+        d = sh.dev()
+        q = queries(w, 4, "bf16")
+        d.batch.tensors[which][at] = value
+        out = attend(d, sh.groups(), 1, q.cuda(), 0.125).cpu().double()
+        assert d.error() == (gt.KV_DEV_ERR_TABLE if value != -1 or which == 3 else 0)
+        want, _, size = ref.attend(w, 1, q, 0.125)
+        gone = list(range(2 * at, 2 * at + 2))
+        rows = [r for r, _, _ in w.rows() if r not in gone]
+        assert (out[gone] == 7.0).all()
+        assert ((out - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -12) * size)[rows].all()
+
+
+def test_shared_bad_entries():
+    sh = Shared(9, [(80, [(4, 2)] * 4), (32, [(5, 1), (7, 2)])], "bf16")
+    w = sh.w
+    w.table[0:4, 2] = w.P + 9  # a page of the prefix past the pool: its tokens drop out
+    d = sh.dev()
+    q = queries(w, 4, "bf16")
+    out = attend(d, sh.groups(), 1, q.cuda(), 0.125).cpu().double()
+    assert d.error() == gt.KV_DEV_ERR_ROW
+    w.table[0:4, 2] = 0
+    want, _, size = ref.attend(w, 1, q, 0.125)
+    assert ((out - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -12) * size).all()
+    d = sh.dev(kernel_facing=True)
+    d.batch.tensors[0][0:4, 1] += 1
+    attend(d, sh.groups(), 1, q.cuda(), 0.125)
+    assert d.error() == gt.KV_DEV_ERR_FORM
+
+
+@pytest.mark.parametrize("cache,dtype", [CACHES[0], CACHES[2], CACHES[4]])
+def test_shared_repeats_bit_for_bit(cache, dtype):
+    """Long prefixes that are cut over the whole GPU, in both kernels; twice on one
+    workspace, in a graph, and two calls at once on two streams: the same bits."""
+    sh = Shared(10, [(3007, [(9 + i, 1) for i in range(50)]), (2005, [(40, 1), (3, 1), (700, 2)])], cache, D=128, H=2,
+                L=2)
+    w = sh.w
+    want = check(sh, 8, dtype)
+    d, groups = sh.dev(), sh.groups()
+    q = queries(w, 8, dtype).cuda()
+    size = gt.kv_attend_shared_workspace_bytes(d.pool, 8, w.S, w.n_rows)
+    ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    outs = [torch.full_like(q, 7.0) for _ in range(2)]
+    call = lambda i, st=None: gt.kv_attend_shared_layer(d.pool, 1, d.batch, groups, q, outs[i], 128 ** -0.5,  # noqa: E731
+                                                        ws[i], scales=d.scales, stream=st)
+    for _ in range(3):
+        call(0)
+    assert torch.equal(outs[0], want)
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        call(1)
+        call(1)
+    for _ in range(3):
+        outs[1].fill_(7.0)
+        gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[1], want)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for o in outs:
+        o.fill_(7.0)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in (0, 1):
+            call(i, streams[i])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+    assert d.error() == 0
+
+
+def test_shared_strided_queries():
+    sh = Shared(11, GROUPS["many"], "bf16", D=128)
+    d, w = sh.dev(), sh.w
+    wide = torch.randn(w.n_rows, 4 * 128 + 41, device="cuda").to(torch.bfloat16)
+    for x in (wide[:, 8:520], wide[:, 3:515]):
+        q = x.unflatten(1, (4, 128))
+        assert torch.equal(attend(d, sh.groups(), 1, q, 0.1), attend(d, sh.groups(), 1, q.contiguous(), 0.1))
+
+
+def test_shared_step():
+    """Decode steps behind a shared prompt as a serving loop runs them, in a 4-bit pool: append, shared attention."""
+    sh = Shared(12, [(96, [(1 + i, 1) for i in range(6)])], "e2m1", D=128, H=2)
+    w = sh.w
+    rot = ref.rotation(1, 128, 128, w.n_rows)
+    g = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn(w.n_rows, h, 128, generator=g).to(torch.bfloat16) for h in (8, 2, 2))
+    d = sh.dev(kernel_facing=True)
+    dq = torch.empty_like(q, device="cuda")
+    gt.kv_append_layer(d.pool, 1, d.batch, k.cuda(), v.cuda(), rotary=gt.kv_rotary(rot.table.cuda()), q=q.cuda(), q_out=dq)
+    out = attend(d, sh.groups(), 1, dq, 0.09).cpu().double()
+    assert d.error() == 0
+    w.raw, _ = ref4.append(w, 1, k, v, rot)
+    assert torch.equal(d.raw.cpu(), w.raw)
+    want, _, size = ref.attend(w, 1, dq.cpu(), 0.09)
+    assert ((out - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -12) * size).all()
+
+
+def test_refusals():
+    sh = Shared(1, [(32, [(4, 1), (5, 1)])], "bf16")
+    d, groups = sh.dev(), sh.groups()
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device="cuda")
+    size = gt.kv_attend_shared_workspace_bytes(d.pool, 4, 2, 2)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(q)
+    at = lambda **kw: gt.kv_attend_shared_layer(d.pool, kw.pop("layer", 1), d.batch, kw.pop("groups", groups),  # noqa: E731
+                                                kw.pop("q", q), kw.pop("out", out), kw.pop("scale", 1.0),
+                                                kw.pop("ws", ws), **kw)
+
+    def refused(code, **kw):
+        with pytest.raises(gt.KVError) as e:
+            at(**kw)
+        assert e.value.code == code, e.value
+
+    refused(-1, layer=2)
+    refused(-1, scale=float("nan"))
+    refused(-1, ws=ws[: size - 16])
+    refused(-5, ws=torch.empty(size + 16, dtype=torch.uint8, device="cuda")[1:])
+    refused(-1, q=q.float(), out=out.float())
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    refused(-1, groups=gt.kv_prefix_groups(i32([0]), i32([])))
+    for bad in ((i32([0, 2]), i32([1, 2])), (i32([[0, 2]]), i32([1])), (torch.tensor([0, 2], device="cuda"), i32([1])),
+                (i32([0, 2]).cpu(), i32([1]))):
+        with pytest.raises(ValueError):
+            gt.kv_prefix_groups(*bad)
+    with pytest.raises(ValueError):
+        at(scales=torch.zeros(4, device="cuda"))
+    with pytest.raises(ValueError):
+        at(q=q[:1])
+    g = gt.kv_prefix_groups(i32([0, 2]), i32([32]))
+    g.struct.reserved = 1
+    refused(-1, groups=g)
+    g.struct.reserved, g.struct.n_groups = 0, -1
+    refused(-1, groups=g)
+    g.struct.n_groups, was = 1, g.struct.group_dev
+    g.struct.group_dev = None
+    refused(-1, groups=g)
+    g.struct.group_dev = was + 2
+    refused(-5, groups=g)
+    with pytest.raises(gt.KVError):
+        gt.kv_attend_shared_workspace_bytes(d.pool, 3, 2, 2)
+    with pytest.raises(gt.KVError):
+        gt.kv_attend_shared_workspace_bytes(d.pool, 4, 2, 1 << 50)
+    empty = gt.kv_batch(torch.zeros(0, 4, dtype=torch.int32, device="cuda"), i32([]),
+                        torch.zeros(1, dtype=torch.int64, device="cuda"), 0)
+    none = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    gt.kv_attend_shared_layer(d.pool, 0, empty, gt.kv_prefix_groups(i32([0]), i32([])), none, none.clone(), 1.0, ws)
+    assert d.error() == 0
