@@ -1,5 +1,5 @@
-// Attention of few rows a sequence: the launch, and the kernel (kv_attend_few.cuh) for caches of 16 and 8 bits.
-#include "kv_attend_few.cuh"
+// Attention of few rows a sequence: the launch. The kernel is kv_attend_few.cuh's, its instances are kv_attend_few_*.cu's.
+#include "kv_attend_launch.h"
 
 namespace gtkv {
 
@@ -13,10 +13,14 @@ int heads_of_worker(int32_t H) { return H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1; }
 }  // namespace
 
 cudaError_t prepare_attend_few(int32_t D, Kind kind, bool p16) {
-  if (kind == Kind::kE2M1) return prepare_few4(D, p16);
-  if (kind == Kind::kE4M3) return prepare_c<CodeE4M3>(D, p16);
-  const cudaError_t e = prepare_c<__half>(D, p16);
-  return e == cudaSuccess ? prepare_c<__nv_bfloat16>(D, p16) : e;
+  auto both = [&]<class C>() {
+    const cudaError_t e = prepare_few<C, false>(D, p16);
+    return e == cudaSuccess ? prepare_few<C, true>(D, p16) : e;
+  };
+  if (kind == Kind::kE2M1) return both.template operator()<CodeE2M1>();
+  if (kind == Kind::kE4M3) return both.template operator()<CodeE4M3>();
+  const cudaError_t e = both.template operator()<__half>();
+  return e == cudaSuccess ? both.template operator()<__nv_bfloat16>() : e;
 }
 
 int64_t attend_few_workspace(int32_t D, int sm_count) {
@@ -44,7 +48,7 @@ cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs
   // units that are short anyway are never cut, and then there is nothing to join: 512 sequences of 300 tokens (8-bit,
   // D = 64) 52 us against 63 cut, 4 of 128 tokens 15.0 against 15.2
   w.whole = most <= (tiles * (a.H / w.hw) >= cap ? kWhole : kWhole / 3);
-  const int64_t all = (w.whole ? 1 : most + kUnitCost) * tiles * (a.H / w.hw);
+  const int64_t all = (w.whole ? 1 : most + kFewUnitCost) * tiles * (a.H / w.hw);
   cap = cap < kMaxWorkers ? cap : kMaxWorkers;
   w.min_share = w.whole ? 1 : kMinShare;
   int64_t workers = (all + w.min_share - 1) / w.min_share;
@@ -65,10 +69,12 @@ cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs
   w.first = how == Launch::kFirst;
   *out = w;
   const bool after = how != Launch::kPlain;
-  if (kind == Kind::kE2M1) return launch_few4(p, b, a, w, nt, after, s);
-  if (kind == Kind::kE4M3) return launch_c<CodeE4M3>(p, b, a, w, nt, after, s);
-  if (a.type == KV_TYPE_BF16) return launch_c<__nv_bfloat16>(p, b, a, w, nt, after, s);
-  return launch_c<__half>(p, b, a, w, nt, after, s);
+  auto go = [&]<class C>() {
+    return b.seqs ? launch_few<C, true>(p, b, a, w, nt, after, s) : launch_few<C, false>(p, b, a, w, nt, after, s);
+  };
+  if (kind == Kind::kE2M1) return go.template operator()<CodeE2M1>();
+  if (kind == Kind::kE4M3) return go.template operator()<CodeE4M3>();
+  return a.type == KV_TYPE_BF16 ? go.template operator()<__nv_bfloat16>() : go.template operator()<__half>();
 }
 
 }  // namespace gtkv

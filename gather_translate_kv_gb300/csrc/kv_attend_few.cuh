@@ -46,10 +46,7 @@ namespace gtkv {
 
 namespace {
 
-constexpr int kFewWarps = 4;
-constexpr int kFewBlock = 32 * kFewWarps;
-constexpr int kFewBlocksPerSM = 4;  // at most
-constexpr int kUnitCost = 2;  // steps' worth of a unit's queries and output
+constexpr int kUnitCost = kFewUnitCost;
 template <class C>
 struct FewType {
   static constexpr int kSize = 2;       // bytes per cached element
@@ -156,11 +153,11 @@ struct FewShape {
 // lane looks up the pages of 32 steps ahead at once; otherwise every key's entry is
 // read on its own, one step ahead. 256 x 4096 tokens in pages of 16, bf16, on one GPU: 686 us against
 // 698 by keys; 8-bit, pages of 32: the same within 1 %.
-// Resident blocks: shared memory for 256-byte rows, registers for 16 columns allow three.
-constexpr int few_blocks(int row, int nt) { return row >= 256 || nt > 1 ? 3 : kFewBlocksPerSM; }
 
-// TWO: weights in two parts.
-template <class C, int D, int NT, bool P16, bool TWO>
+// TWO: weights in two parts. SHARED: a pass over prefixes, whose sums it leaves in a.state, or the one
+// over sequences' own tokens, which takes them up from a.prior (kv_attend_shared.cu); instances of their own, since
+// their code costs the plain ones 1 % (decode) to 6 % (k_attend_tile, prompts).
+template <class C, int D, int NT, bool P16, bool TWO, bool SHARED>
 __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT))
     k_attend_few(DevPool p, Batch b, AttendArgs a, Split w) {
   using Sh = FewShape<C, D>;
@@ -171,7 +168,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ ShareStart loc[kFewWarps];
   __shared__ int64_t tmp[kFewWarps];
-  if (w.first) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (SHARED && w.first) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
@@ -179,20 +176,21 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
   const int wk = warp / w.hw;                  // this warp's worker in the block
   const int hw = warp - wk * w.hw;             // its head of the worker's group
   const int32_t n_groups = a.H / w.hw;
+  const int32_t Gp = SHARED ? a.Gp : a.G;      // rows of a sequence's position
   int bits = 0;
 
   auto tiles_of = [&](const Seq& q) { return q.n == 0 || q.n > w.max_new ? 0 : (q.n * a.G + NQ - 1) / NQ; };
   auto span_of = [&](const Seq& q, int32_t s, int32_t t) {
     const int32_t f0 = t * NQ, f1 = min(f0 + NQ, q.n * a.G);
-    KeySpan k = key_span<16>(a, q.a + f0 / a.Gp, q.a + (f1 - 1) / a.Gp);
-    if (b.from) k.b0 = __ldcg(b.from + s) >> 4;
+    KeySpan k = key_span<16>(a, q.a + f0 / Gp, q.a + (f1 - 1) / Gp);
+    if (SHARED && b.from) k.b0 = __ldcg(b.from + s) >> 4;
     return k;
   };
   const int32_t worker0 = static_cast<int32_t>(blockIdx.x) * kw;
   const int64_t share = find_shares<kFewBlock, kFewWarps>(
       b.n_seqs, worker0, w.n_workers, w.min_share, loc, tmp, [&](int32_t s) -> int64_t {
         int err = 0;
-        const Seq q = seq_of(p, b, s, err);
+        const Seq q = seq_of<SHARED>(p, b, s, err);
         if (blockIdx.x == 0) bits |= err;
         int64_t n = 0;
         if (w.whole) return static_cast<int64_t>(tiles_of(q)) * n_groups;
@@ -229,7 +227,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
   KeySpan span{0, 0, 0};
   if (left > 0) {  // the unit and step where the share begins
     int err = 0;
-    q = seq_of(p, b, s, err);
+    q = seq_of<SHARED>(p, b, s, err);
     int64_t off = at.off;
     for (;;) {
       span = span_of(q, s, tile);
@@ -255,7 +253,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
     const int32_t h = group * w.hw + hw;
     const int32_t f0 = tile * NQ;
     const int32_t nf = min(NQ, q.n * a.G - f0);  // rows of the tile
-    const int32_t i0 = q.a + f0 / a.Gp, i1 = q.a + (f0 + nf - 1) / a.Gp;
+    const int32_t i0 = q.a + f0 / Gp, i1 = q.a + (f0 + nf - 1) / Gp;
 
     // ---- issue of a step's loads
     // the lane's piece of row 0 of a page, in the layer's block of keys; rows are below 2^31
@@ -424,7 +422,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
 #pragma unroll
       for (int e = 0; e < 2; ++e) {  // columns 2c and 2c + 1 of the scores
         cq[nt][e] = __shfl_sync(kFull, row_c, (2 * c + e) * 4);
-        pos[nt][e] = q.a + min(f0 + nt * 8 + 2 * c + e, f0 + nf - 1) / a.Gp;
+        pos[nt][e] = q.a + min(f0 + nt * 8 + 2 * c + e, f0 + nf - 1) / Gp;
       }
     }
 
@@ -736,7 +734,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
         sum[nt][e] += __shfl_xor_sync(kFull, sum[nt][e], 16);
       }
     const bool whole = step0 == 0 && end == n_steps;
-    if (whole && a.state) {
+    if (SHARED && whole && a.state) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -754,7 +752,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
           }
         }
     } else if (whole) {
-      if (a.prior && __ldcg(b.from + s) != 0) {  // what the rows have summed up before, under one reference
+      if (SHARED && a.prior && __ldcg(b.from + s) != 0) {  // what the rows have summed up before, under one reference
         asm volatile("griddepcontrol.wait;" ::: "memory");
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -845,7 +843,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
         tile = 0;
         if (++s >= b.n_seqs) break;
         int err = 0;
-        q = seq_of(p, b, s, err);
+        q = seq_of<SHARED>(p, b, s, err);
       }
       if (s >= b.n_seqs) break;
       span = span_of(q, s, tile);
@@ -853,44 +851,52 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
   }
   if (worker < w.n_workers && hw == 0 && lane == 0) w.rec[worker] = rec;
   store_bits(p, bits);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // whoever waits for this kernel waits for those before it
+  if constexpr (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");  // whoever waits for this kernel waits for those before it
 }
 
-template <class C, int D, int NT>
+template <class C, int D, int NT, bool SHARED>
 cudaError_t launch(const DevPool& p, const Batch& b, const AttendArgs& a, Split w, bool after, cudaStream_t s) {
   using Sh = FewShape<C, D>;
   constexpr bool kOne = std::is_same_v<C, CodeE4M3> || std::is_same_v<C, CodeE2M1>;  // one part will do for a bf16 output
   const bool one = kOne && a.type == KV_TYPE_BF16;
-  auto kernel = p.ps % 16 == 0 ? (one ? k_attend_few<C, D, NT, true, !kOne> : k_attend_few<C, D, NT, true, true>)
-                               : (one ? k_attend_few<C, D, NT, false, !kOne> : k_attend_few<C, D, NT, false, true>);
+  auto kernel = p.ps % 16 == 0
+                    ? (one ? k_attend_few<C, D, NT, true, !kOne, SHARED> : k_attend_few<C, D, NT, true, true, SHARED>)
+                    : (one ? k_attend_few<C, D, NT, false, !kOne, SHARED> : k_attend_few<C, D, NT, false, true, SHARED>);
   const int smem = kFewWarps * (w.deep ? Sh::kDeep : Sh::kStages) * Sh::kStage;
   if (after) return launch_overlapped(kernel, dim3(w.blocks), kFewBlock, smem, s, p, b, a, w);
   kernel<<<w.blocks, kFewBlock, smem, s>>>(p, b, a, w);
   return cudaGetLastError();
 }
 
-template <class C>
-cudaError_t launch_c(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, int nt, bool after, cudaStream_t s) {
-  if (a.D == 64) return nt == 1 ? launch<C, 64, 1>(p, b, a, w, after, s) : launch<C, 64, 2>(p, b, a, w, after, s);
-  return nt == 1 ? launch<C, 128, 1>(p, b, a, w, after, s) : launch<C, 128, 2>(p, b, a, w, after, s);
-}
-
-template <class C, int D, int NT>
+template <class C, int D, int NT, bool SHARED>
 cudaError_t prepare_one(bool p16) {
   constexpr int kBytes = kFewWarps * FewShape<C, D>::kDeep * FewShape<C, D>::kStage;
   auto set = [](auto kernel) { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes); };
-  cudaError_t e = set(p16 ? k_attend_few<C, D, NT, true, true> : k_attend_few<C, D, NT, false, true>);
+  cudaError_t e = set(p16 ? k_attend_few<C, D, NT, true, true, SHARED> : k_attend_few<C, D, NT, false, true, SHARED>);
   if constexpr (std::is_same_v<C, CodeE4M3> || std::is_same_v<C, CodeE2M1>)
-    if (e == cudaSuccess) e = set(p16 ? k_attend_few<C, D, NT, true, false> : k_attend_few<C, D, NT, false, false>);
+    if (e == cudaSuccess) e = set(p16 ? k_attend_few<C, D, NT, true, false, SHARED> : k_attend_few<C, D, NT, false, false, SHARED>);
   return e;
 }
 
-template <class C>
-cudaError_t prepare_c(int32_t D, bool p16) {
-  const cudaError_t e = D == 64 ? prepare_one<C, 64, 1>(p16) : prepare_one<C, 128, 1>(p16);
-  return e != cudaSuccess ? e : D == 64 ? prepare_one<C, 64, 2>(p16) : prepare_one<C, 128, 2>(p16);
+}  // namespace
+
+template <class C, bool SHARED>
+cudaError_t launch_few(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, int nt, bool after,
+                       cudaStream_t s) {
+  if (a.D == 64) return nt == 1 ? launch<C, 64, 1, SHARED>(p, b, a, w, after, s) : launch<C, 64, 2, SHARED>(p, b, a, w, after, s);
+  return nt == 1 ? launch<C, 128, 1, SHARED>(p, b, a, w, after, s) : launch<C, 128, 2, SHARED>(p, b, a, w, after, s);
 }
 
-}  // namespace
+template <class C, bool SHARED>
+cudaError_t prepare_few(int32_t D, bool p16) {
+  const cudaError_t e = D == 64 ? prepare_one<C, 64, 1, SHARED>(p16) : prepare_one<C, 128, 1, SHARED>(p16);
+  return e != cudaSuccess ? e : D == 64 ? prepare_one<C, 64, 2, SHARED>(p16) : prepare_one<C, 128, 2, SHARED>(p16);
+}
+
+// One pair of instances a file (kv_attend_few_*.cu), so that they compile side by side.
+#define GTKV_FEW_INSTANCES(C, SHARED)                                                                                     \
+  template cudaError_t launch_few<C, SHARED>(const DevPool&, const Batch&, const AttendArgs&, const Split&, int, bool,  \
+                                             cudaStream_t);                                                            \
+  template cudaError_t prepare_few<C, SHARED>(int32_t, bool);
 
 }  // namespace gtkv

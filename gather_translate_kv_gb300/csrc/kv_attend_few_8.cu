@@ -1,0 +1,8 @@
+// k_attend_few for 8-bit caches.
+#include "kv_attend_few.cuh"
+
+namespace gtkv {
+
+GTKV_FEW_INSTANCES(CodeE4M3, false)
+
+}  // namespace gtkv

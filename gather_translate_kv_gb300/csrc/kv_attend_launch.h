@@ -9,6 +9,22 @@ namespace gtkv {
 
 constexpr int kMaxWorkers = 2048;
 
+struct CodeE4M3;
+struct CodeE2M1;
+
+// Few rows a sequence.
+constexpr int kFewWarps = 4;
+constexpr int kFewBlock = 32 * kFewWarps;
+constexpr int kFewBlocksPerSM = 4;  // at most
+constexpr int kFewUnitCost = 2;     // steps' worth of a unit's queries and output
+// Resident blocks: shared memory for 256-byte rows, registers for 16 columns allow three.
+constexpr int few_blocks(int row, int nt) { return row >= 256 || nt > 1 ? 3 : kFewBlocksPerSM; }
+
+// Tiles of rows.
+constexpr int kTileRows = 256;    // rows of a unit
+constexpr int kTileKeys = 128;    // keys of a step
+constexpr int kTileUnitCost = 3;  // steps' worth of a unit's queries and output
+
 // What a worker leaves behind for the join: the unit that its last segment
 // left unfinished, s < 0 for none, and the last worker that continues it.
 struct SplitRecord {
@@ -45,11 +61,7 @@ inline int64_t split_record_bytes(int64_t workers) {
 // Shared-memory limits, on the current device, of the kernels for one kind of pool (p16: its page size is a multiple
 // of 16).
 cudaError_t prepare_attend_few(int32_t D, Kind kind, bool p16);
-cudaError_t prepare_few4(int32_t D, bool p16);  // kv_attend_few4.cu
-cudaError_t launch_few4(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, int nt, bool after, cudaStream_t s);
 cudaError_t prepare_attend_tile(int32_t D, Kind kind, bool p16);
-cudaError_t prepare_tile4(int32_t D);  // kv_attend_tile4.cu
-cudaError_t launch_tile4(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, bool after, cudaStream_t s);
 int64_t attend_few_workspace(int32_t D, int sm_count);
 int64_t attend_tile_workspace(int32_t D, int sm_count);
 // How a kernel follows the one before it: at its end, over its tail, or over its tail but reading its result first.
@@ -60,6 +72,16 @@ cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs
                               void* workspace, int sm_count, Launch how, Split* w, cudaStream_t s);
 cudaError_t launch_attend_tile(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, int32_t min_new,
                                void* workspace, int sm_count, Launch how, Split* w, cudaStream_t s);
+// The instances for a cache's element type (kv_attend_few_*.cu, kv_attend_tile_*.cu).
+template <class C, bool SHARED>
+cudaError_t launch_few(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, int nt, bool after,
+                       cudaStream_t s);
+template <class C, bool SHARED>
+cudaError_t prepare_few(int32_t D, bool p16);
+template <class C, bool SHARED>
+cudaError_t launch_tile(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, bool after, cudaStream_t s);
+template <class C, bool SHARED>
+cudaError_t prepare_tile(int32_t D, bool p16);
 // Both, each for the sequences on its side of few_rows_of, and the join (kv_attend.cu).
 cudaError_t launch_tiles(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, void* workspace, int sm_count,
                          Launch how, cudaStream_t s);

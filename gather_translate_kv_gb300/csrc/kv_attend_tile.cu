@@ -1,5 +1,5 @@
-// Attention of many rows a sequence: the launch, and the kernel (kv_attend_tile.cuh) for caches of 16 and 8 bits.
-#include "kv_attend_tile.cuh"
+// Attention of many rows a sequence: the launch. The kernel is kv_attend_tile.cuh's, its instances are kv_attend_tile_*.cu's.
+#include "kv_attend_launch.h"
 
 namespace gtkv {
 
@@ -10,30 +10,29 @@ constexpr int kMinShare = 2;  // steps of 128 keys below which a block's share i
 }  // namespace
 
 cudaError_t prepare_attend_tile(int32_t D, Kind kind, bool p16) {
-  cudaError_t e;
-  if (kind == Kind::kE2M1) return prepare_tile4(D);
-  if (kind == Kind::kElements) {
-    e = prepare_one<__half, false, true>(D);
-    return e == cudaSuccess ? prepare_one<__nv_bfloat16, false, true>(D) : e;
-  }
-  e = p16 ? prepare_one<CodeE4M3, true, false>(D) : prepare_one<CodeE4M3, false, false>(D);
-  if (e != cudaSuccess) return e;
-  return p16 ? prepare_one<CodeE4M3, true, true>(D) : prepare_one<CodeE4M3, false, true>(D);
+  auto both = [&]<class C>() {
+    const cudaError_t e = prepare_tile<C, false>(D, p16);
+    return e == cudaSuccess ? prepare_tile<C, true>(D, p16) : e;
+  };
+  if (kind == Kind::kE2M1) return both.template operator()<CodeE2M1>();
+  if (kind == Kind::kE4M3) return both.template operator()<CodeE4M3>();
+  const cudaError_t e = both.template operator()<__half>();
+  return e == cudaSuccess ? both.template operator()<__nv_bfloat16>() : e;
 }
 
 int64_t attend_tile_workspace(int32_t D, int sm_count) {
-  return split_record_bytes(sm_count) + static_cast<int64_t>(sm_count) * 2 * kRows * (D + 2) * 4;
+  return split_record_bytes(sm_count) + static_cast<int64_t>(sm_count) * 2 * kTileRows * (D + 2) * 4;
 }
 
 cudaError_t launch_attend_tile(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, int32_t min_new,
                                void* workspace, int sm_count, Launch how, Split* out, cudaStream_t s) {
   Split w{};
   w.hw = 1;
-  w.nq = kRows;
+  w.nq = kTileRows;
   w.min_new = min_new;
   w.min_share = kMinShare;
-  const int64_t steps = static_cast<int64_t>(b.max_pages) * p.ps / kKeys + 1 + kUnitCost;
-  const int64_t tiles = b.n_rows * a.G / kRows + (b.n_rows < b.n_seqs ? b.n_rows : b.n_seqs);
+  const int64_t steps = static_cast<int64_t>(b.max_pages) * p.ps / kTileKeys + 1 + kTileUnitCost;
+  const int64_t tiles = b.n_rows * a.G / kTileRows + (b.n_rows < b.n_seqs ? b.n_rows : b.n_seqs);
   const int64_t blocks = (steps * tiles * a.H + kMinShare - 1) / kMinShare;
   w.blocks = static_cast<int>(blocks < sm_count ? blocks : sm_count);
   w.n_workers = w.blocks;
@@ -45,14 +44,12 @@ cudaError_t launch_attend_tile(const DevPool& p, const Batch& b, const AttendArg
   w.first = how == Launch::kFirst;
   *out = w;
   const bool after = how != Launch::kPlain;
-  auto go = [&]<class C, bool P16, bool TWO>() { return launch_one<C, P16, TWO>(p, b, a, w, after, s); };
-  const bool bf16 = a.type == KV_TYPE_BF16;
-  if (kind == Kind::kE2M1) return launch_tile4(p, b, a, w, after, s);
-  if (kind == Kind::kElements)
-    return bf16 ? go.template operator()<__nv_bfloat16, false, true>() : go.template operator()<__half, false, true>();
-  if (p.ps % 16 == 0)
-    return bf16 ? go.template operator()<CodeE4M3, true, false>() : go.template operator()<CodeE4M3, true, true>();
-  return bf16 ? go.template operator()<CodeE4M3, false, false>() : go.template operator()<CodeE4M3, false, true>();
+  auto go = [&]<class C>() {
+    return b.seqs ? launch_tile<C, true>(p, b, a, w, after, s) : launch_tile<C, false>(p, b, a, w, after, s);
+  };
+  if (kind == Kind::kE2M1) return go.template operator()<CodeE2M1>();
+  if (kind == Kind::kE4M3) return go.template operator()<CodeE4M3>();
+  return a.type == KV_TYPE_BF16 ? go.template operator()<__nv_bfloat16>() : go.template operator()<__half>();
 }
 
 }  // namespace gtkv

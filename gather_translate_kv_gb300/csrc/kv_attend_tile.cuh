@@ -53,10 +53,9 @@ namespace gtkv {
 namespace {
 
 constexpr int kTileThreads = 416;  // 13 warps
-constexpr int kRows = 256;         // rows of a unit
-constexpr int kKeys = 128;         // keys of a step
+constexpr int kRows = kTileRows, kKeys = kTileKeys;
 constexpr int kSlots = 8;          // steps whose scales and masks are kept
-constexpr int kUnitCost = 3;       // steps' worth of a unit's queries and output
+constexpr int kUnitCost = kTileUnitCost;
 
 // What the softmax warps need to know of a step's keys.
 struct Masks {
@@ -104,6 +103,7 @@ struct Segment {
   int32_t i0, i1;  // positions of the first and the last
 };
 
+template <bool SHARED>
 struct TileWalk {
   const DevPool& p;
   const Batch& b;
@@ -118,8 +118,8 @@ struct TileWalk {
   __device__ __forceinline__ void shape() {
     g.f0 = g.tile * kRows;
     g.nf = min(kRows, g.q.n * a.G - g.f0);
-    g.i0 = g.q.a + g.f0 / a.Gp;
-    g.i1 = g.q.a + (g.f0 + g.nf - 1) / a.Gp;
+    g.i0 = g.q.a + g.f0 / (SHARED ? a.Gp : a.G);
+    g.i1 = g.q.a + (g.f0 + g.nf - 1) / (SHARED ? a.Gp : a.G);
     g.span = key_span<kKeys>(a, g.i0, g.i1);
   }
   __device__ __forceinline__ bool cut() {
@@ -135,7 +135,7 @@ struct TileWalk {
     int err = 0;
     g.s = at.s;
     g.tile = 0;
-    g.q = seq_of(p, b, g.s, err);
+    g.q = seq_of<SHARED>(p, b, g.s, err);
     int64_t off = at.off;
     for (;;) {
       shape();
@@ -162,7 +162,7 @@ struct TileWalk {
         g.tile = 0;
         if (++g.s >= b.n_seqs) return false;
         int err = 0;
-        g.q = seq_of(p, b, g.s, err);
+        g.q = seq_of<SHARED>(p, b, g.s, err);
       }
       shape();
     }
@@ -215,8 +215,8 @@ __device__ __forceinline__ float2 fadd2(float2 x, float2 y) {
 }
 
 // P16: the page size is a multiple of 16, so 16 keys share the scales of an 8-bit cache.
-// TWO: weights in two parts.
-template <class C, int D, bool P16, bool TWO>
+// TWO: weights in two parts. SHARED: a pass over prefixes (kv_attend_few.cuh).
+template <class C, int D, bool P16, bool TWO, bool SHARED>
 __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batch b, AttendArgs a, Split w) {
   using Sm = TileSmem<C, D>;
   constexpr bool kE4M3 = Sm::kE4M3, kE2M1 = Sm::kE2M1, kCodes = Sm::kCodes;
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
   extern __shared__ uint8_t dyn[];
   __shared__ ShareStart loc[1];
   __shared__ int64_t tmp[kTileThreads / 32];
-  if (w.first) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (SHARED && w.first) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t base = (shared_u32(dyn) + 1023u) & ~1023u;
   uint8_t* gen = dyn + (base - shared_u32(dyn));
@@ -250,11 +250,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  TileWalk walk{p, b, a, w, 0, {}};
+  TileWalk<SHARED> walk{p, b, a, w, 0, {}};
   const int64_t share = find_shares<kTileThreads, 1>(b.n_seqs, blockIdx.x, w.n_workers, w.min_share, loc, tmp,
                                                      [&](int32_t s) -> int64_t {
                                                        int err = 0;
-                                                       walk.g.q = seq_of(p, b, s, err);
+                                                       walk.g.q = seq_of<SHARED>(p, b, s, err);
                                                        if (blockIdx.x == 0) bits |= err;
                                                        int64_t n = 0;
                                                        for (walk.g.tile = 0; walk.g.tile < walk.tiles(); ++walk.g.tile) {
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
       const int32_t f = g.f0 + wt * 128 + r;
       const int32_t fc = min(f, g.f0 + g.nf - 1);
       const bool row_ok = f < g.f0 + g.nf;
-      const int32_t pos = g.q.a + fc / a.Gp;
+      const int32_t pos = g.q.a + fc / (SHARED ? a.Gp : a.G);
       float c = c0;
       float ref = kNoRef;
       float2 sum = make_float2(0.0f, 0.0f);
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
       const bool whole = g.step0 == 0 && g.end == g.span.steps();
       const int64_t orow = g.q.row0 + fc / a.G;
       const int32_t qh = g.h * a.G + fc % a.G;
-      if (whole && a.state) {
+      if (SHARED && whole && a.state) {
         float* to = a.state + (orow * a.Q + qh) * D;
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
@@ -1034,23 +1034,53 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
   store_bits(p, bits);
 }
 
-template <class C, bool P16, bool TWO>
+template <class C, bool P16, bool TWO, bool SHARED>
 cudaError_t prepare_one(int32_t D) {
-  return D == 64 ? cudaFuncSetAttribute(k_attend_tile<C, 64, P16, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        TileSmem<C, 64>::kBytes)
-                 : cudaFuncSetAttribute(k_attend_tile<C, 128, P16, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        TileSmem<C, 128>::kBytes);
+  auto set = [](auto kernel, int bytes) { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); };
+  return D == 64 ? set(k_attend_tile<C, 64, P16, TWO, SHARED>, TileSmem<C, 64>::kBytes)
+                 : set(k_attend_tile<C, 128, P16, TWO, SHARED>, TileSmem<C, 128>::kBytes);
 }
 
-template <class C, bool P16, bool TWO>
+template <class C, bool P16, bool TWO, bool SHARED>
 cudaError_t launch_one(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, bool after, cudaStream_t s) {
-  auto kernel = a.D == 64 ? k_attend_tile<C, 64, P16, TWO> : k_attend_tile<C, 128, P16, TWO>;
+  auto kernel = a.D == 64 ? k_attend_tile<C, 64, P16, TWO, SHARED> : k_attend_tile<C, 128, P16, TWO, SHARED>;
   const int smem = a.D == 64 ? TileSmem<C, 64>::kBytes : TileSmem<C, 128>::kBytes;
   if (after) return launch_overlapped(kernel, dim3(w.blocks), kTileThreads, smem, s, p, b, a, w);
   kernel<<<w.blocks, kTileThreads, smem, s>>>(p, b, a, w);
   return cudaGetLastError();
 }
 
+// Caches of codes: one part of the weights will do for a bf16 output; in 8 bits the page size matters.
+template <class C>
+constexpr bool kIsCode = std::is_same_v<C, CodeE4M3> || std::is_same_v<C, CodeE2M1>;
+template <class C>
+constexpr bool kPaged = std::is_same_v<C, CodeE4M3>;
+
 }  // namespace
+
+template <class C, bool SHARED>
+cudaError_t launch_tile(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, bool after, cudaStream_t s) {
+  constexpr bool kOne = kIsCode<C>;
+  const bool one = kOne && a.type == KV_TYPE_BF16;
+  if (kPaged<C> && p.ps % 16 == 0)
+    return one ? launch_one<C, kPaged<C>, !kOne, SHARED>(p, b, a, w, after, s)
+               : launch_one<C, kPaged<C>, true, SHARED>(p, b, a, w, after, s);
+  return one ? launch_one<C, false, !kOne, SHARED>(p, b, a, w, after, s) : launch_one<C, false, true, SHARED>(p, b, a, w, after, s);
+}
+
+template <class C, bool SHARED>
+cudaError_t prepare_tile(int32_t D, bool p16) {
+  constexpr bool kOne = kIsCode<C>;
+  const bool paged = kPaged<C> && p16;
+  const cudaError_t e = paged ? prepare_one<C, kPaged<C>, true, SHARED>(D) : prepare_one<C, false, true, SHARED>(D);
+  if (e != cudaSuccess || !kOne) return e;
+  return paged ? prepare_one<C, kPaged<C>, !kOne, SHARED>(D) : prepare_one<C, false, !kOne, SHARED>(D);
+}
+
+// One pair of instances a file (kv_attend_tile_*.cu), so that they compile side by side.
+#define GTKV_TILE_INSTANCES(C, SHARED)                                                                                    \
+  template cudaError_t launch_tile<C, SHARED>(const DevPool&, const Batch&, const AttendArgs&, const Split&, bool,       \
+                                              cudaStream_t);                                                            \
+  template cudaError_t prepare_tile<C, SHARED>(int32_t, bool);
 
 }  // namespace gtkv

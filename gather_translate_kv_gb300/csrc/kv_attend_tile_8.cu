@@ -1,0 +1,8 @@
+// k_attend_tile for 8-bit caches.
+#include "kv_attend_tile.cuh"
+
+namespace gtkv {
+
+GTKV_TILE_INSTANCES(CodeE4M3, false)
+
+}  // namespace gtkv

@@ -38,8 +38,10 @@ struct alignas(16) Seq {
   int32_t n;
 };
 
+// SHARED: checked already, from b.seqs.
+template <bool SHARED = false>
 __device__ __forceinline__ Seq seq_of(const DevPool& p, const Batch& b, int32_t s, int& bits) {
-  if (b.seqs) {
+  if constexpr (SHARED) {
     const int4 v = __ldcg(reinterpret_cast<const int4*>(b.seqs) + s);
     return Seq{static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(v.y)) << 32 | static_cast<uint32_t>(v.x)), v.z, v.w};
   }
