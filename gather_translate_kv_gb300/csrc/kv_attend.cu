@@ -89,17 +89,17 @@ int64_t attend_workspace_bytes(int32_t, int32_t, int32_t D, int32_t, int64_t, in
 // turn into fp16, 83 / 174 at 16, 138 / 183 at 32, 194 / 183 at 48 (fp16 output: 93 / 214 at 16, 151 / 218 at 24,
 // 272 / 226 at 64).
 cudaError_t launch_tiles(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, void* workspace, int sm_count,
-                         Launch how, cudaStream_t s) {
+                         cudaStream_t s) {
   const int32_t few_rows = few_rows_of(kind);
-  const bool only_few = b.n_rows * a.G <= few_rows * spans_of(b);
+  const bool only_few = b.n_rows * a.G <= few_rows * static_cast<int64_t>(b.n_seqs);
   const int32_t limit = only_few ? 0x7fffffff : few_rows / a.G;
   Split few{}, tile{};
   cudaError_t e = cudaSuccess;
-  if (limit > 0) e = launch_attend_few(p, b, a, kind, limit, workspace, sm_count, how, &few, s);
+  if (limit > 0) e = launch_attend_few(p, b, a, kind, limit, workspace, sm_count, Launch::kPlain, nullptr, &few, s);
   if (e == cudaSuccess && !only_few)
     e = launch_attend_tile(p, b, a, kind, limit + 1,
                            static_cast<uint8_t*>(workspace) + align256(attend_few_workspace(a.D, sm_count)), sm_count,
-                           limit > 0 ? Launch::kAfter : how, &tile, s);
+                           limit > 0 ? Launch::kAfter : Launch::kPlain, nullptr, &tile, s);
   if (e != cudaSuccess) return e;
   if (few.whole) few.n_workers = 0;
   if (few.n_workers == 0 && tile.n_workers == 0) return e;
@@ -109,7 +109,7 @@ cudaError_t launch_tiles(const DevPool& p, const Batch& b, const AttendArgs& a, 
 cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, void* workspace,
                           int sm_count, cudaStream_t s) {
   if (!has_tiles(a.D)) return launch_rows(p, b, a, kind, s);
-  return launch_tiles(p, b, a, kind, workspace, sm_count, Launch::kPlain, s);
+  return launch_tiles(p, b, a, kind, workspace, sm_count, s);
 }
 
 }  // namespace gtkv

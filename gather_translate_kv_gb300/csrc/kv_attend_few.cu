@@ -29,7 +29,7 @@ int64_t attend_few_workspace(int32_t D, int sm_count) {
 }
 
 cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, int32_t max_new,
-                              void* workspace, int sm_count, Launch how, Split* out, cudaStream_t s) {
+                              void* workspace, int sm_count, Launch how, int32_t* nodes, Split* out, cudaStream_t s) {
   Split w{};
   w.hw = heads_of_worker(a.H);
   w.max_new = max_new;
@@ -67,6 +67,7 @@ cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs
   w.q_wide = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.q_stride % 8 == 0;
   w.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0;
   w.first = how == Launch::kFirst;
+  w.nodes = nodes;
   *out = w;
   const bool after = how != Launch::kPlain;
   auto go = [&]<class C>() {

@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
   int64_t left = at.s < 0 ? 0 : share;
   int32_t s = at.s, tile = 0, group = 0;
   int32_t step0 = 0;
+  int64_t in_unit = 0;  // SHARED: of the share's first unit, what of its line lies before the share
   Seq q{0, 0, 0};
   KeySpan span{0, 0, 0};
   if (left > 0) {  // the unit and step where the share begins
@@ -243,6 +244,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
       group = static_cast<int32_t>(off / unit);
       const int32_t in = static_cast<int32_t>(off - static_cast<int64_t>(group) * unit);
       step0 = in < kUnitCost ? 0 : in - kUnitCost;
+      in_unit = in;
       left -= in < kUnitCost ? kUnitCost - in : 0;
     }
   }
@@ -733,47 +735,90 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
         sum[nt][e] += __shfl_xor_sync(kFull, sum[nt][e], 8);
         sum[nt][e] += __shfl_xor_sync(kFull, sum[nt][e], 16);
       }
-    const bool whole = step0 == 0 && end == n_steps;
-    if (SHARED && whole && a.state) {
+    bool whole = step0 == 0 && end == n_steps;
+    if constexpr (SHARED) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int col = nt * 8 + 2 * c + e;
-          if (col >= nf) continue;
-          const int64_t at = (q.row0 + (f0 + col) / a.G) * a.Q + h * a.G + (f0 + col) % a.G;
-#pragma unroll
-          for (int mt = 0; mt < Sh::kMT; mt += 2)
-            *reinterpret_cast<float4*>(a.state + at * D + element(mt)) =
-                make_float4(o[mt][nt][e], o[mt][nt][e + 2], o[mt + 1][nt][e], o[mt + 1][nt][e + 2]);
-          if (g == 0) {
-            a.state[a.state_rows * D + at] = high[nt][e] == -INFINITY ? kNoRef : low[nt][e];
-            a.state[a.state_rows * (D + 1) + at] = sum[nt][e];
-          }
-        }
-    } else if (whole) {
-      if (SHARED && a.prior && __ldcg(b.from + s) != 0) {  // what the rows have summed up before, under one reference
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        for (int e = 0; e < 2; ++e)
+          if (high[nt][e] == -INFINITY) low[nt][e] = kNoRef;
+      // adds sums of the same rows, in the layout of a.state and of partial results: at(col) their place
+      auto add = [&](const float* base, int64_t refs, int64_t sums, auto at, bool first) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int32_t f = f0 + min(nt * 8 + 2 * c + e, nf - 1);
-            const int64_t at = (q.row0 + f / a.G) * a.Q + h * a.G + f % a.G;
-            const float ref = __ldcg(a.prior + a.state_rows * D + at), own = high[nt][e] == -INFINITY ? kNoRef : low[nt][e];
-            const float top = fmaxf(ref, own), k1 = ex2(own - top), k2 = ex2(ref - top);
-            sum[nt][e] = sum[nt][e] * k1 + __ldcg(a.prior + a.state_rows * (D + 1) + at) * k2;
+            const int64_t r = at(nt * 8 + 2 * c + e);
+            const float ref = __ldcg(base + refs + r), other = __ldcg(base + sums + r);
+            const float top = fmaxf(ref, low[nt][e]), k1 = ex2(low[nt][e] - top), k2 = ex2(ref - top);
             low[nt][e] = top;
+            auto sum_of = [&](float own, float oth) {  // left + right, whoever holds them
+              return first ? __fmaf_rn(own, k1, __fmul_rn(oth, k2)) : __fmaf_rn(oth, k2, __fmul_rn(own, k1));
+            };
+            sum[nt][e] = sum_of(sum[nt][e], other);
 #pragma unroll
             for (int mt = 0; mt < Sh::kMT; mt += 2) {
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(a.prior + at * D + element(mt)));
-              o[mt][nt][e] = o[mt][nt][e] * k1 + x.x * k2;
-              o[mt][nt][e + 2] = o[mt][nt][e + 2] * k1 + x.y * k2;
-              o[mt + 1][nt][e] = o[mt + 1][nt][e] * k1 + x.z * k2;
-              o[mt + 1][nt][e + 2] = o[mt + 1][nt][e + 2] * k1 + x.w * k2;
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(base + r * D + element(mt)));
+              o[mt][nt][e] = sum_of(o[mt][nt][e], x.x);
+              o[mt][nt][e + 2] = sum_of(o[mt][nt][e + 2], x.y);
+              o[mt + 1][nt][e] = sum_of(o[mt + 1][nt][e], x.z);
+              o[mt + 1][nt][e + 2] = sum_of(o[mt + 1][nt][e + 2], x.w);
             }
           }
+      };
+      auto leave = [&](float* base, int64_t refs, int64_t sums, auto at, int32_t cols) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int col = nt * 8 + 2 * c + e;
+            if (col >= cols) continue;
+            const int64_t r = at(col);
+#pragma unroll
+            for (int mt = 0; mt < Sh::kMT; mt += 2)
+              *reinterpret_cast<float4*>(base + r * D + element(mt)) =
+                  make_float4(o[mt][nt][e], o[mt][nt][e + 2], o[mt + 1][nt][e], o[mt + 1][nt][e + 2]);
+            if (g == 0) {
+              base[refs + r] = low[nt][e];
+              base[sums + r] = sum[nt][e];
+            }
+          }
+      };
+      if (!whole) {
+        TreePlace tree;
+        if (step0 == 0)
+          tree.begin(worker, 1 + static_cast<int32_t>((n_steps - end + share - 1) / share));
+        else
+          tree.go_on(worker, share, in_unit, n_steps, kUnitCost);
+        auto part_of = [&](int32_t wk) {
+          return w.part + ((static_cast<int64_t>(wk) * w.hw + hw) * 2 + (wk == tree.worker0 ? 1 : 0)) * static_cast<int64_t>(NQ * (D + 2));
+        };
+        auto same = [](int col) -> int64_t { return col; };
+        whole = true;
+        while (tree.up()) {
+          int32_t other;
+          if (!meet(w.nodes + static_cast<int64_t>(tree.node) * w.hw + hw, worker, &other,
+                    [&]() { leave(part_of(worker), NQ * D, NQ * (D + 1), same, NQ); })) {
+            whole = false;
+            break;
+          }
+          add(part_of(other), NQ * D, NQ * (D + 1), same, tree.left);
+          tree.joined();
+        }
       }
+      auto row_at = [&](int col) -> int64_t {
+        const int32_t f = f0 + min(col, nf - 1);
+        return (q.row0 + f / a.G) * a.Q + h * a.G + f % a.G;
+      };
+      if (whole && a.state) {
+        leave(a.state, a.state_rows * D, a.state_rows * (D + 1), row_at, nf);
+        whole = false;
+      } else if (whole && a.prior && __ldcg(b.from + s) != 0) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        add(a.prior, a.state_rows * D, a.state_rows * (D + 1), row_at, false);
+      }
+    }
+    if (whole) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -812,7 +857,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
               }
           }
         }
-    } else {
+    } else if constexpr (!SHARED) {
       const int slot = step0 == 0 ? 1 : 0;
       float* part = w.part + ((static_cast<int64_t>(worker) * w.hw + hw) * 2 + slot) * static_cast<int64_t>(NQ * (D + 2));
 #pragma unroll
@@ -849,7 +894,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
       span = span_of(q, s, tile);
     }
   }
-  if (worker < w.n_workers && hw == 0 && lane == 0) w.rec[worker] = rec;
+  if (!SHARED && worker < w.n_workers && hw == 0 && lane == 0) w.rec[worker] = rec;
   store_bits(p, bits);
   if constexpr (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");  // whoever waits for this kernel waits for those before it
 }

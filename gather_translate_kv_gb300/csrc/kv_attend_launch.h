@@ -51,6 +51,7 @@ struct Split {
   int32_t deep;       // the longer ring
   int32_t whole;      // units are not cut: nothing to join
   int32_t first;      // the sequences come from the kernel before this one
+  int32_t* nodes;     // shared prefixes: where the segments of a unit meet (TreePlace), [worker][warps], zeros
   float lift;         // log2 of the weights' lift
 };
 
@@ -62,6 +63,9 @@ inline int64_t split_record_bytes(int64_t workers) {
 // of 16).
 cudaError_t prepare_attend_few(int32_t D, Kind kind, bool p16);
 cudaError_t prepare_attend_tile(int32_t D, Kind kind, bool p16);
+// Joining nodes of a kernel, for shared prefixes.
+inline int64_t few_nodes(int sm_count) { return static_cast<int64_t>(sm_count) * kFewBlocksPerSM * kFewWarps; }
+inline int64_t tile_nodes(int sm_count) { return static_cast<int64_t>(sm_count) * 8; }
 int64_t attend_few_workspace(int32_t D, int sm_count);
 int64_t attend_tile_workspace(int32_t D, int sm_count);
 // How a kernel follows the one before it: at its end, over its tail, or over its tail but reading its result first.
@@ -69,9 +73,9 @@ enum class Launch { kPlain, kAfter, kFirst };
 // Sequences of at most max_new, and of at least min_new, new tokens; *w says
 // what is left to join.
 cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, int32_t max_new,
-                              void* workspace, int sm_count, Launch how, Split* w, cudaStream_t s);
+                              void* workspace, int sm_count, Launch how, int32_t* nodes, Split* w, cudaStream_t s);
 cudaError_t launch_attend_tile(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, int32_t min_new,
-                               void* workspace, int sm_count, Launch how, Split* w, cudaStream_t s);
+                               void* workspace, int sm_count, Launch how, int32_t* nodes, Split* w, cudaStream_t s);
 // The instances for a cache's element type (kv_attend_few_*.cu, kv_attend_tile_*.cu).
 template <class C, bool SHARED>
 cudaError_t launch_few(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& w, int nt, bool after,
@@ -84,7 +88,7 @@ template <class C, bool SHARED>
 cudaError_t prepare_tile(int32_t D, bool p16);
 // Both, each for the sequences on its side of few_rows_of, and the join (kv_attend.cu).
 cudaError_t launch_tiles(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, void* workspace, int sm_count,
-                         Launch how, cudaStream_t s);
+                         cudaStream_t s);
 // Rows a KV head up to which a sequence is the few-rows kernel's.
 inline int32_t few_rows_of(Kind kind) { return kind == Kind::kElements ? 16 : 32; }
 inline bool has_tiles(int32_t D) { return D == 64 || D == 128; }

@@ -23,12 +23,14 @@ constexpr int kGroupBlock = 128;
 // member's new tokens; it is shared by two sequences at least.
 __global__ void __launch_bounds__(kGroupBlock) k_share_groups(DevPool p, Batch b, const int32_t* __restrict__ group,
                                                               const int32_t* __restrict__ prefix_len, int32_t n_groups,
-                                                              int32_t G, Seq* own, Seq* shared, int32_t* from) {
+                                                              int32_t G, Seq* own, Seq* shared, int32_t* from,
+                                                              int32_t* nodes, int32_t n_nodes) {
   __shared__ int64_t row0[kGroupBlock / 32], row1[kGroupBlock / 32];
   __shared__ int32_t start[kGroupBlock / 32], first[kGroupBlock / 32], count[kGroupBlock / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int bits = 0;
+  for (int32_t i = blockIdx.x * kGroupBlock + tid; i < n_nodes; i += gridDim.x * kGroupBlock) nodes[i] = 0;
   int bad = 0;
   for (int32_t i = tid; i <= n_groups; i += kGroupBlock) {
     const int32_t s = __ldg(group + i);
@@ -93,7 +95,7 @@ __global__ void __launch_bounds__(kGroupBlock) k_share_groups(DevPool p, Batch b
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
 struct Workspace {
-  int64_t own, shared, from, tiles, few, state, bytes;
+  int64_t own, shared, from, nodes, tiles, few, state, bytes;
 };
 
 Workspace workspace_of(int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int sm_count) {
@@ -108,6 +110,7 @@ Workspace workspace_of(int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int
   w.own = take(n_seqs * static_cast<int64_t>(sizeof(Seq)));
   w.shared = take(n_seqs * static_cast<int64_t>(sizeof(Seq)));
   w.from = take(n_seqs * static_cast<int64_t>(sizeof(int32_t)));
+  w.nodes = take((2 * few_nodes(sm_count) + tile_nodes(sm_count)) * 4);
   w.few = take(attend_few_workspace(D, sm_count));
   w.state = take(n_rows * Q * (D + 2) * 4);
   return w;
@@ -132,32 +135,33 @@ cudaError_t launch_attend_shared(const DevPool& p, const Batch& b, const AttendA
   Seq* own = reinterpret_cast<Seq*>(ws + w.own);
   Seq* shared = reinterpret_cast<Seq*>(ws + w.shared);
   int32_t* from = reinterpret_cast<int32_t*>(ws + w.from);
-  k_share_groups<<<n_groups < 2 * sm_count ? n_groups : 2 * sm_count, kGroupBlock, 0, s>>>(p, b, group, prefix_len, n_groups,
-                                                                                        a.G, own, shared, from);
+  int32_t* nodes = reinterpret_cast<int32_t*>(ws + w.nodes);
+  const int32_t n_nodes = static_cast<int32_t>(2 * few_nodes(sm_count) + tile_nodes(sm_count));
+  k_share_groups<<<n_groups < 2 * sm_count ? n_groups : 2 * sm_count, kGroupBlock, 0, s>>>(
+      p, b, group, prefix_len, n_groups, a.G, own, shared, from, nodes, n_nodes);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  Split split{};
   Batch bb = b;
   AttendArgs aa = a;
   aa.state_rows = b.n_rows * a.Q;
   bb.seqs = shared;
   bb.n_spans = n_groups;
   aa.state = reinterpret_cast<float*>(ws + w.state);
-  aa.lse = nullptr;
   aa.Gp = INT32_MAX;
-  e = launch_tiles(p, bb, aa, kind, ws + w.tiles, sm_count, Launch::kFirst, s);
+  if (b.n_rows * a.G <= few_rows_of(kind) * static_cast<int64_t>(n_groups))
+    e = launch_attend_few(p, bb, aa, kind, INT32_MAX, ws + w.tiles, sm_count, Launch::kFirst, nodes, &split, s);
+  else
+    e = launch_attend_tile(p, bb, aa, kind, 1, ws + w.tiles, sm_count, Launch::kFirst, nodes + 2 * few_nodes(sm_count), &split, s);
   if (e != cudaSuccess) return e;
   bb = b;
   bb.seqs = own;
   bb.from = from;
   aa.prior = aa.state;
   aa.state = nullptr;
-  aa.lse = a.lse;
   aa.Gp = a.G;
-  Split few{};
-  const Split none{};
-  e = launch_attend_few(p, bb, aa, kind, INT32_MAX, ws + w.few, sm_count, Launch::kAfter, &few, s);
-  if (e != cudaSuccess || few.whole) return e;
-  return launch_attend_join(p, bb, aa, kind, few, none, sm_count, s);
+  return launch_attend_few(p, bb, aa, kind, INT32_MAX, ws + w.few, sm_count, Launch::kAfter, nodes + few_nodes(sm_count),
+                           &split, s);
 }
 
 }  // namespace gtkv

@@ -179,6 +179,76 @@ __device__ __forceinline__ float2 unpack16(uint32_t w) {
   return BF16 ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)) : halves(w);
 }
 
+// Where the segments of a cut unit meet when no join follows (shared prefixes): a binary tree over them in the
+// workers' order. Of the two halves of a node the one that is done first leaves its sums and goes on to its other work; the
+// second adds them to its own and goes up. The sums do not depend on who was first.
+struct TreePlace {
+  int32_t worker0;   // of the unit's first segment
+  int32_t n;         // segments
+  int32_t a;         // first segment of what the warp holds
+  int32_t s;         // it holds [a, a + s) of them
+  int32_t node;      // worker whose node it meets the other half at
+  bool left;         // it holds the left half
+
+  // The first of n segments.
+  __device__ __forceinline__ void begin(int32_t worker, int32_t segments) {
+    worker0 = worker;
+    n = segments;
+    a = 0;
+    s = 1;
+  }
+  // A later one, at the start of the worker's share: `in` of the unit's part of the line lies before it.
+  __device__ __forceinline__ void go_on(int64_t worker, int64_t share, int64_t in, int32_t steps, int32_t unit_cost) {
+    const int64_t first = worker * share - in + unit_cost;  // the first step in the line of all
+    worker0 = static_cast<int32_t>(first / share);
+    n = static_cast<int32_t>((first + steps - 1) / share) - worker0 + 1;
+    a = static_cast<int32_t>(worker) - worker0;
+    s = 1;
+  }
+  // The next node; false when the warp holds all segments.
+  __device__ __forceinline__ bool up() {
+    while (s < n) {
+      if (a / s & 1) {
+        left = false;
+        node = worker0 + a;
+        return true;
+      }
+      if (a + s < n) {
+        left = true;
+        node = worker0 + a + s;
+        return true;
+      }
+      s *= 2;  // nobody to meet
+    }
+    return false;
+  }
+  __device__ __forceinline__ void joined() {
+    if (!left) a -= s;
+    s *= 2;
+  }
+};
+
+// A warp's step at a node: true when the other half is there, left by worker *other. `leave` writes
+// the warp's sums where the other half will look for them.
+template <class F>
+__device__ __forceinline__ bool meet(int32_t* node, int32_t worker, int32_t* other, F&& leave) {
+  const int lane = threadIdx.x & 31;
+  int32_t x = 0;
+  if (lane == 0) asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(x) : "l"(node) : "memory");
+  x = __shfl_sync(kFull, x, 0);
+  if (x == 0) {
+    leave();
+    __threadfence();
+    __syncwarp();
+    if (lane == 0) x = atomicExch(node, worker + 1);
+    x = __shfl_sync(kFull, x, 0);
+    if (x == 0) return false;
+  }
+  __threadfence();
+  *other = x - 1;
+  return true;
+}
+
 // Joins the partial sums of units that were cut, adding a unit's segments in
 // the workers' order under a running reference. An item is a row of a cut unit; a warp takes one, or,
 // when there are few items (a long context of few rows, cut many times), the
@@ -265,23 +335,6 @@ __device__ __forceinline__ void join_split(const DevPool& p, const Batch& b, con
       }
     }
     if (!shared || warp == 0) {
-      const int64_t at = (rec.row0 + (rec.f0 + col) / a.G) * a.Q + (rec.head * w.hw + hw) * a.G + (rec.f0 + col) % a.G;
-      if (a.state) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) a.state[at * D + lane * E + e] = acc[e];
-        if (lane == 0) {
-          a.state[a.state_rows * D + at] = m - w.lift;
-          a.state[a.state_rows * (D + 1) + at] = sum;
-        }
-        if (shared) __syncthreads();
-        continue;
-      }
-      if (a.prior && __ldcg(b.from + rec.s) != 0) {
-        float x[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = __ldcg(a.prior + at * D + lane * E + e);
-        add(m, sum, acc, __ldcg(a.prior + a.state_rows * D + at) + w.lift, __ldcg(a.prior + a.state_rows * (D + 1) + at), x);
-      }
       const float inv = sum == 0.0f ? 0.0f : rcp(sum);
       bool bad = !(sum <= 3.402823466e38f);
       const int32_t f = rec.f0 + col;

@@ -25,7 +25,7 @@ int64_t attend_tile_workspace(int32_t D, int sm_count) {
 }
 
 cudaError_t launch_attend_tile(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, int32_t min_new,
-                               void* workspace, int sm_count, Launch how, Split* out, cudaStream_t s) {
+                               void* workspace, int sm_count, Launch how, int32_t* nodes, Split* out, cudaStream_t s) {
   Split w{};
   w.hw = 1;
   w.nq = kTileRows;
@@ -42,6 +42,7 @@ cudaError_t launch_attend_tile(const DevPool& p, const Batch& b, const AttendArg
   w.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
   w.lift = kind == Kind::kElements && a.type == KV_TYPE_BF16 ? 0.0f : 6.0f;
   w.first = how == Launch::kFirst;
+  w.nodes = nodes;
   *out = w;
   const bool after = how != Launch::kPlain;
   auto go = [&]<class C>() {

@@ -101,6 +101,7 @@ struct Segment {
   int32_t step0, end;
   int32_t f0, nf;  // rows
   int32_t i0, i1;  // positions of the first and the last
+  int32_t in;      // of the share's first unit, what of its line lies before the share
 };
 
 template <bool SHARED>
@@ -148,6 +149,7 @@ struct TileWalk {
     g.h = static_cast<int32_t>(off / unit);
     const int32_t in = static_cast<int32_t>(off - static_cast<int64_t>(g.h) * unit);
     g.step0 = in < kUnitCost ? 0 : in - kUnitCost;
+    g.in = in;
     left -= in < kUnitCost ? kUnitCost - in : 0;
     return cut();
   }
@@ -464,22 +466,98 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
       const bool whole = g.step0 == 0 && g.end == g.span.steps();
       const int64_t orow = g.q.row0 + fc / a.G;
       const int32_t qh = g.h * a.G + fc % a.G;
-      if (SHARED && whole && a.state) {
-        float* to = a.state + (orow * a.Q + qh) * D;
+      if constexpr (SHARED) {
+        // The rows' sums go to the state, a cut unit's through the other segments', warp by warp; at a node
+        // they are in tensor memory or, once added to, in the warp's part of the partial results.
+        constexpr int64_t kPart = static_cast<int64_t>(kRows) * (D + 2);
+        const int row = wt * 128 + r;
+        const int32_t me = blockIdx.x;
+        float ref2 = ref, total2 = total;  // (the reference of weights is lifted: the state's is not)
+        bool moved = false, all = true;
+        TreePlace tree;
+        if (!whole) {
+          if (g.step0 == 0)
+            tree.begin(me, 1 + static_cast<int32_t>((g.span.steps() - g.end + share - 1) / share));
+          else
+            tree.go_on(me, share, g.in, g.span.steps(), kUnitCost);
+        }
+        auto part_of = [&](int32_t wk) { return w.part + (static_cast<int64_t>(wk) * 2 + (wk == tree.worker0 ? 1 : 0)) * kPart; };
+        auto own = [&](int k, uint32_t (&x)[32]) {
+          if (moved) {
+            const float* from = part_of(me) + row * D + 32 * k;
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          uint32_t raw[32];
-          tmem_load32(tO + 32 * k, raw);
-          tmem_wait_ld(raw);
-          if (row_ok) {
+            for (int e = 0; e < 8; ++e) {
+              const uint4 v = reinterpret_cast<const uint4*>(from)[e];
+              x[4 * e] = v.x, x[4 * e + 1] = v.y, x[4 * e + 2] = v.z, x[4 * e + 3] = v.w;
+            }
+          } else {
+            tmem_load32(tO + 32 * k, x);
+            tmem_wait_ld(x);
+          }
+        };
+        auto put = [&](float* to, int k, const uint32_t (&x)[32]) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              reinterpret_cast<uint4*>(to + 32 * k)[e] = make_uint4(raw[4 * e], raw[4 * e + 1], raw[4 * e + 2], raw[4 * e + 3]);
+          for (int e = 0; e < 8; ++e)
+            reinterpret_cast<uint4*>(to + 32 * k)[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        };
+        float* state = a.state + (orow * a.Q + qh) * D;
+        bool done = false;  // the sums are in the state
+        while (!whole && tree.up()) {
+          int32_t other;
+          if (!meet(w.nodes + static_cast<int64_t>(tree.node) * 8 + warp, me, &other, [&]() {
+                float* to = part_of(me);
+#pragma unroll 1
+                for (int k = 0; k < D / 32 && !moved; ++k) {
+                  uint32_t x[32];
+                  own(k, x);
+                  put(to + row * D, k, x);
+                }
+                to[kRows * D + row] = ref2;
+                to[kRows * (D + 1) + row] = total2;
+              })) {
+            all = false;
+            break;
+          }
+          const float* from = part_of(other);
+          const float oref = __ldcg(from + kRows * D + row), ototal = __ldcg(from + kRows * (D + 1) + row);
+          const float top = fmaxf(ref2, oref), k1 = ex2(ref2 - top), k2 = ex2(oref - top);
+          auto sum_of = [&](float x, float y) {  // left + right, whoever holds them
+            return tree.left ? __fmaf_rn(x, k1, __fmul_rn(y, k2)) : __fmaf_rn(y, k2, __fmul_rn(x, k1));
+          };
+          ref2 = top;
+          total2 = sum_of(total2, ototal);
+          done = 2 * tree.s >= tree.n;  // the root
+#pragma unroll 1
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t x[32];
+            own(k, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 y = __ldcg(reinterpret_cast<const float4*>(from + row * D + 32 * k) + e);
+              x[4 * e] = __float_as_uint(sum_of(__uint_as_float(x[4 * e]), y.x));
+              x[4 * e + 1] = __float_as_uint(sum_of(__uint_as_float(x[4 * e + 1]), y.y));
+              x[4 * e + 2] = __float_as_uint(sum_of(__uint_as_float(x[4 * e + 2]), y.z));
+              x[4 * e + 3] = __float_as_uint(sum_of(__uint_as_float(x[4 * e + 3]), y.w));
+            }
+            if (!done)
+              put(part_of(me) + row * D, k, x);
+            else if (row_ok)
+              put(state, k, x);
+          }
+          moved = true;
+          tree.joined();
+        }
+        if (all && !done) {
+#pragma unroll 1
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t x[32];
+            own(k, x);  // by the whole warp: loads from tensor memory are the warp's, not a lane's
+            if (row_ok) put(state, k, x);
           }
         }
-        if (row_ok) {
-          a.state[a.state_rows * D + orow * a.Q + qh] = ref - kLift;
-          a.state[a.state_rows * (D + 1) + orow * a.Q + qh] = total;
+        if (all && row_ok) {
+          a.state[a.state_rows * D + orow * a.Q + qh] = ref2 - kLift;
+          a.state[a.state_rows * (D + 1) + orow * a.Q + qh] = total2;
         }
       } else if (whole) {
         bool bad = !(total <= 3.402823466e38f);
@@ -539,7 +617,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
         part[kRows * (D + 1) + row] = total;
       }
     }
-    if (tid == 0) w.rec[blockIdx.x] = ok ? rec : SplitRecord{-1, 0, 0, 0, 0, 0, 0};
+    if (!SHARED && tid == 0) w.rec[blockIdx.x] = ok ? rec : SplitRecord{-1, 0, 0, 0, 0, 0, 0};
     // rows that came out with anything not finite are done again, key by key
     asm volatile("bar.sync 1, 256;" ::: "memory");
     if (stop[1] && !*stop && walk.start(loc[0], share)) do {
