@@ -467,13 +467,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
       const int64_t orow = g.q.row0 + fc / a.G;
       const int32_t qh = g.h * a.G + fc % a.G;
       if constexpr (SHARED) {
-        // The rows' sums go to the state, a cut unit's through the other segments', warp by warp; at a node
-        // they are in tensor memory or, once added to, in the warp's part of the partial results.
-        constexpr int64_t kPart = static_cast<int64_t>(kRows) * (D + 2);
+        // The rows' sums go to the state, a cut unit's through the other segments', warp by warp; they stay in
+        // tensor memory meanwhile. What a warp leaves for another lies by elements, four of all its rows
+        // together, so that a lane's row is not a stride for the others.
         const int row = wt * 128 + r;
         const int32_t me = blockIdx.x;
-        float ref2 = ref, total2 = total;  // (the reference of weights is lifted: the state's is not)
-        bool moved = false, all = true;
+        float ref2 = ref, total2 = total;
+        bool all = true, done = false;  // the warp holds all segments; the sums are in the state
         TreePlace tree;
         if (!whole) {
           if (g.step0 == 0)
@@ -481,36 +481,31 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           else
             tree.go_on(me, share, g.in, g.span.steps(), kUnitCost);
         }
-        auto part_of = [&](int32_t wk) { return w.part + (static_cast<int64_t>(wk) * 2 + (wk == tree.worker0 ? 1 : 0)) * kPart; };
-        auto own = [&](int k, uint32_t (&x)[32]) {
-          if (moved) {
-            const float* from = part_of(me) + row * D + 32 * k;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint4 v = reinterpret_cast<const uint4*>(from)[e];
-              x[4 * e] = v.x, x[4 * e + 1] = v.y, x[4 * e + 2] = v.z, x[4 * e + 3] = v.w;
-            }
-          } else {
-            tmem_load32(tO + 32 * k, x);
-            tmem_wait_ld(x);
-          }
-        };
-        auto put = [&](float* to, int k, const uint32_t (&x)[32]) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            reinterpret_cast<uint4*>(to + 32 * k)[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        auto part_of = [&](int32_t wk) {
+          return w.part + (static_cast<int64_t>(wk) * 2 + (wk == tree.worker0 ? 1 : 0)) * (static_cast<int64_t>(kRows) * (D + 2));
         };
         float* state = a.state + (orow * a.Q + qh) * D;
-        bool done = false;  // the sums are in the state
+        auto put = [&](int k, const uint32_t (&x)[32]) {  // whole 32-byte sectors
+          if (!row_ok) return;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(state + 32 * k + e), "r"(x[e]), "r"(x[e + 1]),
+                         "r"(x[e + 2]), "r"(x[e + 3]), "r"(x[e + 4]), "r"(x[e + 5]), "r"(x[e + 6]), "r"(x[e + 7])
+                         : "memory");
+        };
+        // (Loads from and stores to tensor memory are the whole warp's.)
         while (!whole && tree.up()) {
           int32_t other;
           if (!meet(w.nodes + static_cast<int64_t>(tree.node) * 8 + warp, me, &other, [&]() {
                 float* to = part_of(me);
 #pragma unroll 1
-                for (int k = 0; k < D / 32 && !moved; ++k) {
+                for (int k = 0; k < D / 32; ++k) {
                   uint32_t x[32];
-                  own(k, x);
-                  put(to + row * D, k, x);
+                  tmem_load32(tO + 32 * k, x);
+                  tmem_wait_ld(x);
+#pragma unroll
+                  for (int e = 0; e < 8; ++e)
+                    reinterpret_cast<uint4*>(to)[(8 * k + e) * kRows + row] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
                 }
                 to[kRows * D + row] = ref2;
                 to[kRows * (D + 1) + row] = total2;
@@ -530,32 +525,36 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
 #pragma unroll 1
           for (int k = 0; k < D / 32; ++k) {
             uint32_t x[32];
-            own(k, x);
+            float4 y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = __ldcg(reinterpret_cast<const float4*>(from) + (8 * k + e) * kRows + row);
+            tmem_load32(tO + 32 * k, x);
+            tmem_wait_ld(x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float4 y = __ldcg(reinterpret_cast<const float4*>(from + row * D + 32 * k) + e);
-              x[4 * e] = __float_as_uint(sum_of(__uint_as_float(x[4 * e]), y.x));
-              x[4 * e + 1] = __float_as_uint(sum_of(__uint_as_float(x[4 * e + 1]), y.y));
-              x[4 * e + 2] = __float_as_uint(sum_of(__uint_as_float(x[4 * e + 2]), y.z));
-              x[4 * e + 3] = __float_as_uint(sum_of(__uint_as_float(x[4 * e + 3]), y.w));
+              x[4 * e] = __float_as_uint(sum_of(__uint_as_float(x[4 * e]), y[e].x));
+              x[4 * e + 1] = __float_as_uint(sum_of(__uint_as_float(x[4 * e + 1]), y[e].y));
+              x[4 * e + 2] = __float_as_uint(sum_of(__uint_as_float(x[4 * e + 2]), y[e].z));
+              x[4 * e + 3] = __float_as_uint(sum_of(__uint_as_float(x[4 * e + 3]), y[e].w));
             }
-            if (!done)
-              put(part_of(me) + row * D, k, x);
-            else if (row_ok)
-              put(state, k, x);
+            if (done)
+              put(k, x);
+            else
+              tmem_store32(tO + 32 * k, x);
           }
-          moved = true;
+          tmem_wait_st();
           tree.joined();
         }
         if (all && !done) {
 #pragma unroll 1
           for (int k = 0; k < D / 32; ++k) {
             uint32_t x[32];
-            own(k, x);  // by the whole warp: loads from tensor memory are the warp's, not a lane's
-            if (row_ok) put(state, k, x);
+            tmem_load32(tO + 32 * k, x);
+            tmem_wait_ld(x);
+            put(k, x);
           }
         }
-        if (all && row_ok) {
+        if (all && row_ok) {  // (the reference of weights is lifted, the state's is not)
           a.state[a.state_rows * D + orow * a.Q + qh] = ref2 - kLift;
           a.state[a.state_rows * (D + 1) + orow * a.Q + qh] = total2;
         }
