@@ -44,7 +44,7 @@ cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs
     most = seen < most ? seen : most;
   }
   const int64_t tiles = (b.n_rows * a.G) / (8 * nt) + b.n_seqs;  // row tiles of all sequences
-  int64_t cap = static_cast<int64_t>(sm_count) * few_blocks(kind == Kind::kE2M1 ? a.D / 2 : kind == Kind::kE4M3 ? a.D : 2 * a.D, nt) * kw;
+  int64_t cap = static_cast<int64_t>(sm_count) * few_blocks(kind == Kind::kE2M1 ? a.D / 2 : kind == Kind::kE4M3 ? a.D : 2 * a.D, nt, kind == Kind::kE2M1) * kw;
   // units that are short anyway are never cut, and then there is nothing to join: 512 sequences of 300 tokens (8-bit,
   // D = 64) 52 us against 63 cut, 4 of 128 tokens 15.0 against 15.2
   w.whole = most <= (tiles * (a.H / w.hw) >= cap ? kWhole : kWhole / 3);

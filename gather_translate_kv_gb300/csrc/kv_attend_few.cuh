@@ -143,8 +143,11 @@ struct FewShape {
   static constexpr int kStage = 2 * kK + kMeta;
   // Stages of a warp's ring: as many as shared memory holds with all the
   // blocks that fit an SM, or, for calls of one block an SM, whose time is latency, six.
-  static constexpr int kStages = kRow >= 256 ? 2 : kRow >= 128 ? 3 : kE2M1 && D == 128 ? 5 : 6;
+  static constexpr int kStages = kRow >= 256 ? 2 : kRow >= 128 ? 3 : kE2M1 && D == 128 ? 4 : 6;
   static constexpr int kDeep = 6;
+  // blocks of 16 keys a round of the loop: two of a 4-bit cache, whose loads and softmax are little beside what a
+  // round costs anyway, and whose conversions are chains that then overlap
+  static __host__ __device__ constexpr int blocks(int nt) { return kE2M1 && nt == 1 ? 2 : 1; }
   static constexpr int kKS = D / 16;          // k16 steps of the score product
   static constexpr int kMT = D / 16;          // 16-element tiles of the output
 };
@@ -158,7 +161,7 @@ struct FewShape {
 // over sequences' own tokens, which takes them up from a.prior (kv_attend_shared.cu); instances of their own, since
 // their code costs the plain ones 1 % (decode) to 6 % (k_attend_tile, prompts).
 template <class C, int D, int NT, bool P16, bool TWO, bool SHARED>
-__global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT))
+__global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT, FewShape<C, D>::kE2M1))
     k_attend_few(DevPool p, Batch b, AttendArgs a, Split w) {
   using Sh = FewShape<C, D>;
   constexpr bool kE4M3 = std::is_same_v<C, CodeE4M3>, kE2M1 = Sh::kE2M1;
@@ -263,8 +266,9 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
     const int32_t page_rows = static_cast<int32_t>(p.stride), ps = static_cast<int32_t>(p.ps);
     const float* scale_at = kE4M3 ? a.scales + 2 * static_cast<int64_t>(a.layer) * a.H + h : nullptr;  // of page 0
     const int32_t page_scales = p.blocks * a.H;
-    // the head's scale bytes of row 0 of a page, in the layer's block of keys
-    const uint8_t* scales4 = pool + 2 * static_cast<int64_t>(a.layer) * p.ps * row_bytes + code_bytes(a.H, D) + h * Sh::kScaleRow;
+    // from the lane's piece of row 0 to the scale bytes of its key or value of a step
+    const int64_t scales4 = code_bytes(a.H, D) + h * Sh::kScaleRow - (h * Sh::kRow + cp * 16) + ((lane & 15) - cr) * static_cast<int64_t>(row_bytes) +
+                            (lane >> 4) * p.ps * row_bytes;
     const int64_t round_bytes = Sh::kRPR * static_cast<int64_t>(row_bytes), v_bytes = p.ps * row_bytes;
     uint32_t whole_stages = 0;  // bit s: all 16 keys of stage s are tokens
     int32_t ent = 0;  // P16: page of step seg_base + lane (0: tombstone); else: raw entry of key lane % 16 of the next step
@@ -334,10 +338,13 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
           if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + Sh::kLive), "r"(live) : "memory");
         }
         if constexpr (kE2M1) {  // lanes 0-15: a key's scales, 16-31: a value's
-          const bool ok = all || (live >> (lane & 15) & 1);
-          const int64_t r = P16 ? rk + (lane & 15) : rk;
-          copy_async<Sh::kScaleRow>(st + 2 * Sh::kK + lane * Sh::kScaleRow,
-                                    ok ? scales4 + r * row_bytes + (lane < 16 ? 0 : v_bytes) : pool, ok);
+          if (all) {
+            copy_async<Sh::kScaleRow>(st + 2 * Sh::kK + lane * Sh::kScaleRow, from + static_cast<int64_t>(rk) * row_bytes + scales4);
+          } else {
+            const bool ok = live >> (lane & 15) & 1;
+            const int64_t r = P16 ? rk : rk - (lane & 15);
+            copy_async<Sh::kScaleRow>(st + 2 * Sh::kK + lane * Sh::kScaleRow, ok ? from + r * row_bytes + scales4 : pool, ok);
+          }
         } else if constexpr (kE4M3 && P16) {  // one scale of K (lane 0) and one of V (lane 1)
           if (lane < 2)
             copy_async<4>(st + 2 * Sh::kK + lane * 4,
@@ -350,7 +357,8 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
       }
       copy_commit();
     };
-    for (int i = 0; i < stages - 1; ++i) issue(step0 + i, i);
+    constexpr int KB = Sh::blocks(NT);
+    for (int i = 0; i < stages - KB; ++i) issue(step0 + i, i);
 
     // ---- the queries, while the first loads are in flight
     uint32_t qf[NT][Sh::kKS][2];
@@ -444,131 +452,156 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
     }
 
     int stage = 0;
-    for (int32_t i = step0; i < end; ++i) {
-      {
-        int ahead = stage + stages - 1;
+    for (int32_t i = step0; i < end; i += KB) {
+#pragma unroll
+      for (int hb = 0; hb < KB; ++hb) {
+        int ahead = stage + stages - KB + hb;
         if (ahead >= stages) ahead -= stages;
-        issue(i + stages - 1, ahead);
+        issue(i + stages - KB + hb, ahead);
       }
       if (w.deep)
-        copy_wait<Sh::kDeep - 1>();
+        copy_wait<Sh::kDeep - KB>();
       else
-        copy_wait<Sh::kStages - 1>();
+        copy_wait<Sh::kStages - KB>();
       __syncwarp();
-      const uint32_t st = ring0 + stage * Sh::kStage;
-      const uint32_t live = whole_stages >> stage & 1 ? 0xffffu : lds32(st + Sh::kLive);
-      const int32_t j0 = span.block(i) * 16;
+      uint32_t st[KB], live[KB];
+      int32_t j0[KB];
+      bool mask = false;  // some row may not see some key
+#pragma unroll
+      for (int hb = 0; hb < KB; ++hb) {
+        st[hb] = ring0 + (stage + hb) * Sh::kStage;
+        live[hb] = whole_stages >> (stage + hb) & 1 ? 0xffffu : lds32(st[hb] + Sh::kLive);
+        j0[hb] = span.block(i + hb) * 16;
+        if (hb > 0 && i + hb >= end) live[hb] = 0;  // past the last: nothing was copied
+        mask = mask || live[hb] != 0xffffu || j0[hb] + 15 > i0 || (a.window && j0[hb] <= i1 - a.window);
+      }
 
       // ---- scores
       // two sums for one tile of columns, so that products wait half as long for one another
       constexpr bool kTwo = NT == 1;
-      float x[NT][4], x2[NT][4];
-      uint32_t bytes_v = 0;  // 4-bit caches: the scale bytes of the lane's part of its four values
-      if constexpr (kE2M1) {
-        // the lane's scales of keys g and g + 8 (their first blocks in bytes 0 and 1, second ones in 2 and 3)
-        const uint32_t at = st + 2 * Sh::kK;
-        const uint32_t ka = at + g * Sh::kScaleRow + c * (D / 64), kb = ka + 8 * Sh::kScaleRow;
-        uint32_t bytes_k = D == 128 ? __byte_perm(lds16(ka), lds16(kb), 0x5140) : lds8(ka) | lds8(kb) << 8;
-        bytes_k |= bad_scales(bytes_k);
-        const uint32_t va = at + (16 + 2 * c) * Sh::kScaleRow + (D == 128 ? g : g >> 1);
-        bytes_v = lds8(va) | lds8(va + Sh::kScaleRow) << 8 | lds8(va + 8 * Sh::kScaleRow) << 16 | lds8(va + 9 * Sh::kScaleRow) << 24;
-        constexpr int W = D / 32;  // words of codes
-        uint32_t uu[W], vv[W];
-        if constexpr (W == 4) {
-          const uint4 u = lds128(st + get_k), v = lds128(st + get_k + 8 * Sh::kRow);
-          uu[0] = u.x, uu[1] = u.y, uu[2] = u.z, uu[3] = u.w;
-          vv[0] = v.x, vv[1] = v.y, vv[2] = v.z, vv[3] = v.w;
-        } else {
-          const uint2 u = lds64(st + get_k), v = lds64(st + get_k + 8 * Sh::kRow);
-          uu[0] = u.x, uu[1] = u.y;
-          vv[0] = v.x, vv[1] = v.y;
-        }
+      float x[KB][NT][4];
+      uint32_t s01[KB], s23[KB];  // 4-bit caches: the scales of the lane's part of its four values, as pairs of fp16
 #pragma unroll
-        for (int wd = 0; wd < W; ++wd) {
-          const uint32_t sa = __byte_perm(bytes_k, 0, wd < 2 ? 0x4040 : 0x4242) << 7;  // block wd / 2, twice
-          const uint32_t sb = __byte_perm(bytes_k, 0, wd < 2 ? 0x4141 : 0x4343) << 7;
-          uint32_t y[4], z[4];
-          codes8(uu[wd], y);
-          codes8(vv[wd], z);
+      for (int hb = 0; hb < KB; ++hb) {
+        float x2[NT][4];
+        float(&xb)[NT][4] = x[hb];
+        if constexpr (kE2M1) {
+          const uint32_t at = st[hb] + 2 * Sh::kK;
+          // the lane's scale bytes of keys g and g + 8, a key's in a half
+          const uint32_t ka = at + g * Sh::kScaleRow + c * (D / 64);
+          uint32_t kb;
+          if constexpr (D == 128)
+            kb = lds16(ka) | lds16(ka + 8 * Sh::kScaleRow) << 16;
+          else
+            kb = lds8(ka) | lds8(ka + 8 * Sh::kScaleRow) << 16;
+          const uint32_t va = at + (16 + 2 * c) * Sh::kScaleRow + (D == 128 ? g : g >> 1);
+          s01[hb] = lds8(va) * 0x80u + lds8(va + Sh::kScaleRow) * 0x800000u;
+          s23[hb] = lds8(va + 8 * Sh::kScaleRow) * 0x80u + lds8(va + 9 * Sh::kScaleRow) * 0x800000u;
+          if (const uint32_t bad = above_max(kb)) kb |= (bad >> 7) * 0xffu;
+          constexpr int W = D / 32;  // words of codes
+          uint32_t uu[W], vv[W];
+          if constexpr (W == 4) {
+            const uint4 u = lds128(st[hb] + get_k), v = lds128(st[hb] + get_k + 8 * Sh::kRow);
+            uu[0] = u.x, uu[1] = u.y, uu[2] = u.z, uu[3] = u.w;
+            vv[0] = v.x, vv[1] = v.y, vv[2] = v.z, vv[3] = v.w;
+          } else {
+            const uint2 u = lds64(st[hb] + get_k), v = lds64(st[hb] + get_k + 8 * Sh::kRow);
+            uu[0] = u.x, uu[1] = u.y;
+            vv[0] = v.x, vv[1] = v.y;
+          }
+          uint32_t sa[W / 2], sb[W / 2];  // a block's scale, twice
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            y[k] = mul_h2(y[k], sa);
-            z[k] = mul_h2(z[k], sb);
+          for (int blk = 0; blk < W / 2; ++blk) {
+            sa[blk] = __byte_perm(kb, 0, blk ? 0x4141 : 0x4040) * 0x80u;
+            sb[blk] = __byte_perm(kb, 0, blk ? 0x4343 : 0x4242) * 0x80u;
           }
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
+          for (int wd = 0; wd < W; ++wd) {
+            uint32_t y[4], z[4];
+            codes8(uu[wd], y);
+            codes8(vv[wd], z);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma<C>(kTwo && half ? x2[nt] : x[nt], y[2 * half], z[2 * half], y[2 * half + 1], z[2 * half + 1],
-                     qf[nt][2 * wd + half][0], qf[nt][2 * wd + half][1], 2 * wd + half < 1 + kTwo);
-        }
-      }
+            for (int k = 0; k < 4; ++k) {
+              y[k] = mul_h2(y[k], sa[wd / 2]);
+              z[k] = mul_h2(z[k], sb[wd / 2]);
+            }
 #pragma unroll
-      for (int ch = 0; ch < (kE2M1 ? 0 : Sh::kKC); ++ch) {
-        const uint4 u = lds128(st + (get_k ^ ch * 64)), v = lds128(st + (get_k ^ ch * 64) + 8 * Sh::kRow);
-        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
-        if constexpr (kE4M3) {
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
-          for (int wd = 0; wd < 4; ++wd) {
-            const uint32_t a0 = codes_lo(uu[wd]), a1 = codes_lo(vv[wd]), a2 = codes_hi(uu[wd]), a3 = codes_hi(vv[wd]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma<C>(kTwo && wd & 1 ? x2[nt] : x[nt], a0, a1, a2, a3, qf[nt][ch * 4 + wd][0], qf[nt][ch * 4 + wd][1],
-                     ch * 4 + wd < 1 + kTwo);
+              for (int nt = 0; nt < NT; ++nt)
+                mma<C>(kTwo && half ? x2[nt] : xb[nt], y[2 * half], z[2 * half], y[2 * half + 1], z[2 * half + 1],
+                       qf[nt][2 * wd + half][0], qf[nt][2 * wd + half][1], 2 * wd + half < 1 + kTwo);
           }
-        } else {
-#pragma unroll
-          for (int wd = 0; wd < 2; ++wd)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma<C>(kTwo && wd & 1 ? x2[nt] : x[nt], uu[2 * wd], vv[2 * wd], uu[2 * wd + 1], vv[2 * wd + 1],
-                     qf[nt][ch * 2 + wd][0], qf[nt][ch * 2 + wd][1], ch * 2 + wd < 1 + kTwo);
         }
+#pragma unroll
+        for (int ch = 0; ch < (kE2M1 ? 0 : Sh::kKC); ++ch) {
+          const uint4 u = lds128(st[hb] + (get_k ^ ch * 64)), v = lds128(st[hb] + (get_k ^ ch * 64) + 8 * Sh::kRow);
+          const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+          if constexpr (kE4M3) {
+#pragma unroll
+            for (int wd = 0; wd < 4; ++wd) {
+              const uint32_t a0 = codes_lo(uu[wd]), a1 = codes_lo(vv[wd]), a2 = codes_hi(uu[wd]), a3 = codes_hi(vv[wd]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma<C>(kTwo && wd & 1 ? x2[nt] : xb[nt], a0, a1, a2, a3, qf[nt][ch * 4 + wd][0], qf[nt][ch * 4 + wd][1],
+                       ch * 4 + wd < 1 + kTwo);
+            }
+          } else {
+#pragma unroll
+            for (int wd = 0; wd < 2; ++wd)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma<C>(kTwo && wd & 1 ? x2[nt] : xb[nt], uu[2 * wd], vv[2 * wd], uu[2 * wd + 1], vv[2 * wd + 1],
+                       qf[nt][ch * 2 + wd][0], qf[nt][ch * 2 + wd][1], ch * 2 + wd < 1 + kTwo);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (kTwo) xb[nt][e] += x2[nt][e];
       }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (kTwo) x[nt][e] += x2[nt][e];
 
       // ---- weights; x[.][0], [1]: key g, columns 2c, 2c + 1; [2], [3]: key g + 8
       float lv[2] = {0.0f, 0.0f}, iv[2] = {1.0f, 1.0f}, sk[2] = {1.0f, 1.0f};
       if constexpr (kE4M3) {
         if constexpr (P16) {
-          const uint2 kv = lds64(st + 2 * Sh::kK);
+          const uint2 kv = lds64(st[0] + 2 * Sh::kK);
           sk[0] = sk[1] = __uint_as_float(kv.x);
           lv[0] = lv[1] = lg2(__uint_as_float(kv.y));
           iv[0] = iv[1] = rcp(__uint_as_float(kv.y));
         }
 #pragma unroll
         for (int e = 0; e < (P16 ? 0 : 2); ++e) {
-          sk[e] = __uint_as_float(lds32(st + 2 * Sh::kK + (g + 8 * e) * 4));
-          const float sv = __uint_as_float(lds32(st + 2 * Sh::kK + 64 + (g + 8 * e) * 4));
+          sk[e] = __uint_as_float(lds32(st[0] + 2 * Sh::kK + (g + 8 * e) * 4));
+          const float sv = __uint_as_float(lds32(st[0] + 2 * Sh::kK + 64 + (g + 8 * e) * 4));
           lv[e] = lg2(sv);
           iv[e] = rcp(sv);
         }
       }
-      const bool mask = live != 0xffffu || j0 + 15 > i0 || (a.window && j0 <= i1 - a.window);
       bool over = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int hb = 0; hb < KB; ++hb)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float t = kE4M3 ? fmaf(x[nt][e], cq[nt][e & 1] * sk[e >> 1], lv[e >> 1] - low[nt][e & 1])
-                          : fmaf(x[nt][e], cq[nt][e & 1], -low[nt][e & 1]);
-          if (mask) {
-            const int key = g + 8 * (e >> 1);
-            if (!(live >> key & 1) || !in_sight(a, pos[nt][e & 1], j0 + key)) t = -INFINITY;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float t = kE4M3 ? fmaf(x[hb][nt][e], cq[nt][e & 1] * sk[e >> 1], lv[e >> 1] - low[nt][e & 1])
+                            : fmaf(x[hb][nt][e], cq[nt][e & 1], -low[nt][e & 1]);
+            if (mask) {
+              const int key = g + 8 * (e >> 1);
+              if (!(live[hb] >> key & 1) || !in_sight(a, pos[nt][e & 1], j0[hb] + key)) t = -INFINITY;
+            }
+            x[hb][nt][e] = t;
+            over = over || t > high[nt][e & 1];
           }
-          x[nt][e] = t;
-          over = over || t > high[nt][e & 1];
-        }
       if (__any_sync(kFull, over)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float m = fmaxf(x[nt][e], x[nt][e + 2]);
+            float m = fmaxf(x[0][nt][e], x[0][nt][e + 2]);
+            if constexpr (KB > 1) m = fmaxf(m, fmaxf(x[KB - 1][nt][e], x[KB - 1][nt][e + 2]));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
@@ -577,8 +610,11 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
               const float keep = high[nt][e] == -INFINITY ? 0.0f : ex2(-up);
               low[nt][e] += up;
               high[nt][e] = kLift + 8.0f;
-              x[nt][e] -= up;
-              x[nt][e + 2] -= up;
+#pragma unroll
+              for (int hb = 0; hb < KB; ++hb) {
+                x[hb][nt][e] -= up;
+                x[hb][nt][e + 2] -= up;
+              }
               sum[nt][e] *= keep;
 #pragma unroll
               for (int mt = 0; mt < Sh::kMT; ++mt) {
@@ -588,85 +624,93 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
             }
           }
       }
-      uint32_t pb[NT][2], pl[NT][2];
+      uint32_t pb[KB][NT][2], pl[KB][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[e] = ex2(x[nt][e]);
-          // a dead key adds nothing, whatever its zero-filled scale's inverse is
-          if constexpr (kE4M3 && !P16)
-            sum[nt][e & 1] += live >> (g + 8 * (e >> 1)) & 1 ? y[e] * iv[e >> 1] : 0.0f;
-          else if constexpr (!kE4M3)
-            sum[nt][e & 1] += y[e];
-        }
-        if constexpr (kE4M3 && P16) {
-          if (live) {
-            sum[nt][0] = fmaf(y[0] + y[2], iv[0], sum[nt][0]);
-            sum[nt][1] = fmaf(y[1] + y[3], iv[0], sum[nt][1]);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          constexpr bool kBf16 = std::is_same_v<C, __nv_bfloat16>;
-          const uint32_t hi = pack16<kBf16>(y[2 * e], y[2 * e + 1]);
-          pb[nt][e] = transpose8(hi);
-          if constexpr (TWO) {
-            const float2 h = unpack16<kBf16>(hi);
-            pl[nt][e] = transpose8(pack16<kBf16>(y[2 * e] - h.x, y[2 * e + 1] - h.y));
-          }
-        }
-      }
-
-      // ---- values: registers of keys 2c, 2c + 1 (a0, a1) and 2c + 8, 2c + 9 (a2, a3)
-      auto tile_mma = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+      for (int hb = 0; hb < KB; ++hb)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma<C>(o[mt][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-          if constexpr (TWO) mma<C>(o[mt][nt], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[e] = ex2(x[hb][nt][e]);
+            // a dead key adds nothing, whatever its zero-filled scale's inverse is
+            if constexpr (kE4M3 && !P16)
+              sum[nt][e & 1] += live[hb] >> (g + 8 * (e >> 1)) & 1 ? y[e] * iv[e >> 1] : 0.0f;
+            else if constexpr (!kE4M3)
+              sum[nt][e & 1] += y[e];
+          }
+          if constexpr (kE4M3 && P16) {
+            if (live[hb]) {
+              sum[nt][0] = fmaf(y[0] + y[2], iv[0], sum[nt][0]);
+              sum[nt][1] = fmaf(y[1] + y[3], iv[0], sum[nt][1]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            constexpr bool kBf16 = std::is_same_v<C, __nv_bfloat16>;
+            const uint32_t hi = pack16<kBf16>(y[2 * e], y[2 * e + 1]);
+            pb[hb][nt][e] = transpose8(hi);
+            if constexpr (TWO) {
+              const float2 h = unpack16<kBf16>(hi);
+              pl[hb][nt][e] = transpose8(pack16<kBf16>(y[2 * e] - h.x, y[2 * e + 1] - h.y));
+            }
+          }
+        }
+
+      // ---- values: registers of keys 2c, 2c + 1 (a0, a1) and 2c + 8, 2c + 9 (a2, a3)
+      auto tile_mma = [&](int hb, int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma<C>(o[mt][nt], a0, a1, a2, a3, pb[hb][nt][0], pb[hb][nt][1]);
+          if constexpr (TWO) mma<C>(o[mt][nt], a0, a1, a2, a3, pl[hb][nt][0], pl[hb][nt][1]);
         }
       };
-      if constexpr (kE2M1) {
-        uint32_t v[4][D / 64];
+      // rows that see a key whose value was zeroed are done again
+      auto redo = [&](int hb, uint32_t keys) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (keys >> (g + 8 * (e >> 1)) & 1 && x[hb][nt][e] != -INFINITY) sum[nt][e & 1] = NAN;
+      };
+#pragma unroll
+      for (int hb = 0; hb < (kE2M1 ? KB : 0); ++hb) {
+        uint32_t v[4][D == 128 ? 2 : 1];
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           if constexpr (D == 128) {
-            const uint2 u = lds64(st + Sh::kK + value_at(kk));
+            const uint2 u = lds64(st[hb] + Sh::kK + value_at(kk));
             v[kk][0] = u.x, v[kk][1] = u.y;
           } else {
-            v[kk][0] = lds32(st + Sh::kK + value_at(kk));
+            v[kk][0] = lds32(st[hb] + Sh::kK + value_at(kk));
           }
         }
-        const uint32_t bad = bad_scales(bytes_v);
-        if (mask) {  // as below: zeroed here, and their rows done again at the end
-          bytes_v &= ~bad;
-          uint32_t keys = 0;
-          if (bad) keys = ((bad & 1) | (bad >> 7 & 2) | (bad >> 8 & 0x100) | (bad >> 15 & 0x200)) << 2 * c;
-          keys = __reduce_or_sync(kFull, keys);
-          if (keys) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (keys >> (g + 8 * (e >> 1)) & 1 && x[nt][e] != -INFINITY) sum[nt][e & 1] = NAN;
+        // scales above the largest: NaN, or, where some row may not see some key, zeroed as below
+        const uint32_t bad = above_max_pair(s01[hb]) | above_max_pair(s23[hb]) >> 1;  // bits 15, 31 and 14, 30
+        if (mask) {
+          const uint32_t keys = __reduce_or_sync(kFull, ((bad >> 15 & 1) | (bad >> 30 & 2) | (bad >> 6 & 0x100) | (bad >> 21 & 0x200)) << 2 * c);
+          if (bad) {
+            s01[hb] &= ~((bad >> 15 & 0x10001u) * 0xffffu);
+            s23[hb] &= ~((bad >> 14 & 0x10001u) * 0xffffu);
           }
-        } else {
-          bytes_v |= bad;
+          if (keys) redo(hb, keys);
+        } else if (bad) {
+          s01[hb] |= (bad >> 15 & 0x10001u) * 0x7fffu;
+          s23[hb] |= (bad >> 14 & 0x10001u) * 0x7fffu;
         }
         // Codes of a pair of values share a byte before they become a pair of fp16, so that no halves are exchanged.
-        const uint32_t s01 = __byte_perm(bytes_v, 0, 0x4140) << 7, s23 = __byte_perm(bytes_v, 0, 0x4342) << 7;
 #pragma unroll
         for (int wd = 0; wd < D / 64; ++wd) {
           uint32_t a0[4], a1[4], a2[4], a3[4];
           constexpr uint32_t kLow = 0x0f0f0f0fu;
-          codes8((v[0][wd] & kLow) | (v[1][wd] & kLow) << 4, a0);
+          codes8((v[0][wd] & kLow) | (v[1][wd] << 4 & ~kLow), a0);
           codes8((v[0][wd] >> 4 & kLow) | (v[1][wd] & ~kLow), a1);
-          codes8((v[2][wd] & kLow) | (v[3][wd] & kLow) << 4, a2);
+          codes8((v[2][wd] & kLow) | (v[3][wd] << 4 & ~kLow), a2);
           codes8((v[2][wd] >> 4 & kLow) | (v[3][wd] & ~kLow), a3);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tile_mma(4 * wd + k, mul_h2(a0[k], s01), mul_h2(a1[k], s01), mul_h2(a2[k], s23), mul_h2(a3[k], s23));
+            tile_mma(hb, 4 * wd + k, mul_h2(a0[k], s01[hb]), mul_h2(a1[k], s01[hb]), mul_h2(a2[k], s23[hb]),
+                     mul_h2(a3[k], s23[hb]));
         }
       }
       constexpr int VC = kE2M1 ? 0 : Sh::kVC;
@@ -677,10 +721,10 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           if constexpr (VW == 4) {
-            const uint4 u = lds128(st + Sh::kK + value_at(kk) + ch * 128);
+            const uint4 u = lds128(st[0] + Sh::kK + value_at(kk) + ch * 128);
             v[kk][0] = u.x, v[kk][1] = u.y, v[kk][2] = u.z, v[kk][3] = u.w;
           } else {
-            const uint2 u = lds64(st + Sh::kK + value_at(kk));
+            const uint2 u = lds64(st[0] + Sh::kK + value_at(kk));
             v[kk][0] = u.x, v[kk][1] = u.y;
           }
         }
@@ -699,28 +743,23 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
               if (bad) keys |= 1u << (2 * c + (kk & 1) + 8 * (kk >> 1));
             }
           keys = __reduce_or_sync(kFull, keys);
-          if (keys) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (keys >> (g + 8 * (e >> 1)) & 1 && x[nt][e] != -INFINITY) sum[nt][e & 1] = NAN;
-          }
+          if (keys) redo(0, keys);
         }
 #pragma unroll
         for (int wd = 0; wd < VW; ++wd) {
           if constexpr (kE4M3) {
             const uint32_t x0 = __byte_perm(v[0][wd], v[1][wd], 0x5140), y0 = __byte_perm(v[0][wd], v[1][wd], 0x7362);
             const uint32_t x1 = __byte_perm(v[2][wd], v[3][wd], 0x5140), y1 = __byte_perm(v[2][wd], v[3][wd], 0x7362);
-            tile_mma(ch * 8 + 2 * wd, codes_lo(x0), codes_hi(x0), codes_lo(x1), codes_hi(x1));
-            tile_mma(ch * 8 + 2 * wd + 1, codes_lo(y0), codes_hi(y0), codes_lo(y1), codes_hi(y1));
+            tile_mma(0, ch * 8 + 2 * wd, codes_lo(x0), codes_hi(x0), codes_lo(x1), codes_hi(x1));
+            tile_mma(0, ch * 8 + 2 * wd + 1, codes_lo(y0), codes_hi(y0), codes_lo(y1), codes_hi(y1));
           } else {
-            tile_mma(ch * 4 + wd, __byte_perm(v[0][wd], v[1][wd], 0x5410), __byte_perm(v[0][wd], v[1][wd], 0x7632),
+            tile_mma(0, ch * 4 + wd, __byte_perm(v[0][wd], v[1][wd], 0x5410), __byte_perm(v[0][wd], v[1][wd], 0x7632),
                      __byte_perm(v[2][wd], v[3][wd], 0x5410), __byte_perm(v[2][wd], v[3][wd], 0x7632));
           }
         }
       }
-      if (++stage == stages) stage = 0;
+      stage += KB;
+      if (stage == stages) stage = 0;
       __syncwarp();  // the stage's scales and mask are free for the next issue
     }
     copy_wait<0>();

@@ -18,7 +18,7 @@ constexpr int kFewBlock = 32 * kFewWarps;
 constexpr int kFewBlocksPerSM = 4;  // at most
 constexpr int kFewUnitCost = 2;     // steps' worth of a unit's queries and output
 // Resident blocks: shared memory for 256-byte rows, registers for 16 columns allow three.
-constexpr int few_blocks(int row, int nt) { return row >= 256 || nt > 1 ? 3 : kFewBlocksPerSM; }
+constexpr int few_blocks(int row, int nt, bool e2m1) { return e2m1 && nt > 1 ? 2 : row >= 256 || nt > 1 ? 3 : kFewBlocksPerSM; }
 
 // Tiles of rows.
 constexpr int kTileRows = 256;    // rows of a unit

@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
       struct Step {
         Keys k;
         float ks, vs;     // 8-bit caches: the scales of the lane's key
-        uint32_t k4[2], v4[2];  // 4-bit caches: two scale bytes for each piece that the lane turns, two pieces a word
+        uint32_t k4[kE2M1 ? IT : 1], v4[kE2M1 ? IT : 1];  // 4-bit caches: two scale bytes for each piece that the lane turns
         bool first, queries;  // first of its unit; the unit has rows in the warp's tile
       };
       const uint32_t raw0 = base + Sm::kRaw + lw * 32 * RB + lane * 16;
@@ -808,18 +808,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
         ent = entry(i + 1);
         s.ks = s.vs = 0.0f;
         if constexpr (kE2M1) {
-          s.k4[0] = s.k4[1] = s.v4[0] = s.v4[1] = 0;
           const uint8_t* from = pool + code_bytes(a.H, D) + g.h * (D / 16) + lc * 2;
           int32_t ro[IT];
 #pragma unroll
           for (int it = 0; it < IT; ++it) ro[it] = __shfl_sync(kFull, s.k.row, it * RPI + lr);
 #pragma unroll
           for (int it = 0; it < IT; ++it) {
+            s.k4[it] = s.v4[it] = 0;
             if (ro[it] < 0) continue;
             const uint8_t* row = from + static_cast<int64_t>(ro[it]) * row_bytes;
-            s.k4[it >> 1] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(row))) << (it & 1) * 16;
-            s.v4[it >> 1] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(row + p.ps * row_bytes)))
-                             << (it & 1) * 16;
+            s.k4[it] = __ldg(reinterpret_cast<const uint16_t*>(row));
+            s.v4[it] = __ldg(reinterpret_cast<const uint16_t*>(row + p.ps * row_bytes));
           }
         } else if (s.k.page != 0) {
           const int64_t at = (static_cast<int64_t>(s.k.page) * p.blocks + 2 * a.layer) * a.H + g.h;
@@ -837,14 +836,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           }
         }
       };
-      auto turn_tile = [&](uint32_t t, bool check, const uint32_t (&s4)[2]) -> uint32_t {
+      auto turn_tile = [&](uint32_t t, bool check, const uint32_t (&s4)[kE2M1 ? IT : 1]) -> uint32_t {
         uint32_t bad_rows = 0;
         const uint32_t to = operand(t);
+        uint4 codes[IT];  // all loads first: what follows is a chain each
+#pragma unroll
+        for (int it = 0; it < IT; ++it) codes[it] = lds128(raw(t, it));
         if constexpr (kE2M1) {
 #pragma unroll
           for (int it = 0; it < IT; ++it) {
-            const uint4 v = lds128(raw(t, it));
-            uint32_t bytes = s4[it >> 1] >> (it & 1) * 16 & 0xffffu;
+            const uint4 v = codes[it];
+            uint32_t bytes = s4[it];
             const uint32_t bad = bad_scales(bytes);
             if (!check) {
               bytes |= bad;
@@ -868,7 +870,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
         }
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
-          uint4 v = lds128(raw(t, it));
+          uint4 v = codes[it];
           if (check) {
             const uint4 z = make_uint4(not_finite<C>(v.x), not_finite<C>(v.y), not_finite<C>(v.z), not_finite<C>(v.w));
             if (z.x | z.y | z.z | z.w) {

@@ -34,6 +34,15 @@ __device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
 // All ones in the bytes of a word of scales that stand for NaN.
 __device__ __forceinline__ uint32_t bad_scales(uint32_t w) { return __vcmpgtu4(w, kMaxScaleByte * 0x01010101u); }
 
+// The same in fewer operations: bit 7 of each byte that is above the largest scale, and bit 15 of each half
+// that holds such a scale as fp16 bits.
+__device__ __forceinline__ uint32_t above_max(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + (0x7f - (kMaxScaleByte & 0x7f)) * 0x01010101u) & w & 0x80808080u;
+}
+__device__ __forceinline__ uint32_t above_max_pair(uint32_t s) {
+  return (s + (0x7fff - (kMaxScaleByte << 7)) * 0x00010001u) & 0x80008000u;
+}
+
 // A scale byte (below 256) as a pair of equal fp16.
 __device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
   const uint32_t s = byte > kMaxScaleByte ? 0x7fffu : byte << 7;
