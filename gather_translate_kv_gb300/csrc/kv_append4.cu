@@ -1,6 +1,8 @@
 // 4-bit pools (KV_FORMAT_E2M1): append for any head size, rotary_dim, alignment
 // or stride, and the gather of the values. The append of ordinary shapes is
 // k_append's (kv_append.cu).
+#include <type_traits>
+
 #include "kv_append.cuh"
 #include "kv_e2m1.cuh"
 
@@ -95,46 +97,107 @@ __global__ void __launch_bounds__(kAppendBlock) k_append4_any(DevPool p, Batch b
   store_bits(p, bits);
 }
 
-// Gather: a block per page run, K and then V, a block of 16 elements a thread
-// and step, whose values are 32 (or 64) consecutive bytes of the output: 8 bytes of codes and a
-// scale in, whole sectors out.
-template <class T>
-__global__ void __launch_bounds__(kAppendBlock) k_gather4(DevPool p, Batch b, int32_t layer, int32_t H, int32_t D,
-                                                          T* out_k, T* out_v, bool by_row) {
+__device__ __forceinline__ void store32(void* to, const uint32_t* y, bool wide) {
+  if (!wide) {  // the output starts on 16 bytes alone
+    __stcs(static_cast<uint4*>(to), make_uint4(y[0], y[1], y[2], y[3]));
+    __stcs(static_cast<uint4*>(to) + 1, make_uint4(y[4], y[5], y[6], y[7]));
+    return;
+  }
+  asm volatile("st.global.cs.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]),
+               "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+               : "memory");
+}
+
+// Gather: a block per page run, K and V as one list, N blocks of 16 elements a
+// thread and item: 8 N bytes of codes and N scales in, whole sectors of 32 bytes out,
+// kGatherItems items of a thread in flight. N is 2 where rows hold an even number of blocks.
+// Measured: 232 us for 1.54 GB of whole sequences (98 % of the copy rate; items of 8 bytes of codes and 16-byte stores 276), 33 us
+// for 172 MB of 128-token windows, whose blocks wait for their lookups. Items and resident blocks: 2 / 5 as
+// good, 4 / 5 247 us, 8 / 3 236.
+constexpr int kGatherItems = 4;
+constexpr int kGatherBlocks = 4;
+template <class T, int N>
+__global__ void __launch_bounds__(kAppendBlock, kGatherBlocks) k_gather4(DevPool p, Batch b, int32_t layer, int32_t H, int32_t D,
+                                                             T* out_k, T* out_v, bool by_row, bool wide) {
   int bits = 0;
   check_seqs(p, b, static_cast<int64_t>(blockIdx.x) * kAppendBlock + threadIdx.x,
              static_cast<int64_t>(gridDim.x) * kAppendBlock, bits);
   const PageRun run = page_run(p, b, blockIdx.x, by_row, bits);
   store_bits(p, bits);
   if (run.m == 0) return;
-  const int32_t nb = H * (D / 16);  // blocks of a row
+  const int32_t ni = H * (D / 16) / N;  // items of a row
   const int64_t row_bytes = p.vpr * 16;
-  const int64_t n = static_cast<int64_t>(run.m) * nb;
-  for (int kv = 0; kv < 2; ++kv) {
-    const uint8_t* src = pool_row<uint8_t>(p, layer, kv, run.page, run.off);
-    T* dst = (kv ? out_v : out_k) + run.row * H * D;
-    for (int64_t i = threadIdx.x; i < n; i += kAppendBlock) {
-      uint2 w = make_uint2(0, 0);
-      uint32_t s = 0;
-      if (run.page != 0) {
-        const int64_t row = i / nb, blk = i - row * nb;
-        const uint8_t* at = src + row * row_bytes;
-        w = __ldg(reinterpret_cast<const uint2*>(at + blk * 8));
-        s = scale_pair(__ldg(at + nb * 8 + blk));
-      }
-      uint32_t y[8];
-      codes8(w.x, reinterpret_cast<uint32_t(&)[4]>(y[0]));
-      codes8(w.y, reinterpret_cast<uint32_t(&)[4]>(y[4]));
-      T o[16];
+  const uint8_t* src = pool_row<uint8_t>(p, layer, 0, run.page, run.off);
+  const int64_t v_bytes = p.ps * row_bytes;
+  const int64_t out0 = run.row * H * D;
+  // the thread's items: item `col` of row `row`, rows of K and then of V
+  const int32_t rows = 2 * run.m, step_row = kAppendBlock / ni, step_col = kAppendBlock - step_row * ni;
+  int32_t row = threadIdx.x / ni, col = threadIdx.x - row * ni;
+  while (row < rows) {
+    uint32_t w[kGatherItems][2 * N], s[kGatherItems];
+    int32_t rows_of[kGatherItems], cols[kGatherItems];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float2 v = halves(mul_h2(y[k], s));
-        o[2 * k] = Elem<T>::put(v.x);
-        o[2 * k + 1] = Elem<T>::put(v.y);
-      }
+    for (int u = 0; u < kGatherItems; ++u) {
+      rows_of[u] = row;
+      cols[u] = col;
 #pragma unroll
-      for (int k = 0; k < static_cast<int>(sizeof(T)); ++k)
-        reinterpret_cast<uint4*>(dst + i * 16)[k] = reinterpret_cast<const uint4*>(o)[k];
+      for (int k = 0; k < 2 * N; ++k) w[u][k] = 0;
+      s[u] = 0;
+      if (row < rows && run.page != 0) {
+        const uint8_t* from = src + (row < run.m ? row * row_bytes : v_bytes + (row - run.m) * row_bytes);
+        if constexpr (N == 2) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(from) + col);
+          w[u][0] = v.x, w[u][1] = v.y, w[u][2] = v.z, w[u][3] = v.w;
+          s[u] = __ldg(reinterpret_cast<const uint16_t*>(from + ni * 16) + col);
+        } else {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(from) + col);
+          w[u][0] = v.x, w[u][1] = v.y;
+          s[u] = __ldg(from + ni * 8 + col);
+        }
+      }
+      row += step_row;
+      col += step_col;
+      if (col >= ni) {
+        col -= ni;
+        ++row;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kGatherItems; ++u) {
+      if (rows_of[u] >= rows) break;
+      const bool v = rows_of[u] >= run.m;
+      T* dst = (v ? out_v : out_k) + out0 + (static_cast<int64_t>(v ? rows_of[u] - run.m : rows_of[u]) * ni + cols[u]) * (16 * N);
+#pragma unroll
+      for (int blk = 0; blk < N; ++blk) {
+        const uint32_t sc = scale_pair(s[u] >> 8 * blk & 255);
+        uint32_t y[8];
+        codes8(w[u][2 * blk], reinterpret_cast<uint32_t(&)[4]>(y[0]));
+        codes8(w[u][2 * blk + 1], reinterpret_cast<uint32_t(&)[4]>(y[4]));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = mul_h2(y[k], sc);
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t z[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 a = halves(y[4 * half + k]);
+              z[2 * k] = __float_as_uint(a.x), z[2 * k + 1] = __float_as_uint(a.y);
+            }
+            store32(dst + 16 * blk + 8 * half, z, wide);
+          }
+        } else {
+          if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float2 a = halves(y[k]);
+              const __nv_bfloat162 z = __floats2bfloat162_rn(a.x, a.y);
+              y[k] = *reinterpret_cast<const uint32_t*>(&z);
+            }
+          }
+          store32(dst + 16 * blk, y, wide);
+        }
+      }
     }
   }
 }
@@ -162,8 +225,10 @@ cudaError_t launch_gather4(const DevPool& p, const Batch& b, int32_t layer, int3
   const bool by_row = runs_by_row(b, p.ps);
   const int64_t n_runs = run_numbers(b, p.ps, by_row);
   if (n_runs > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const bool wide = ((reinterpret_cast<uintptr_t>(out_k) | reinterpret_cast<uintptr_t>(out_v)) & 31u) == 0;
   auto go = [&]<class T>(T* k, T* v) {
-    k_gather4<T><<<static_cast<unsigned>(n_runs), kAppendBlock, 0, s>>>(p, b, layer, H, D, k, v, by_row);
+    auto kernel = H * D % 32 == 0 ? k_gather4<T, 2> : k_gather4<T, 1>;
+    kernel<<<static_cast<unsigned>(n_runs), kAppendBlock, 0, s>>>(p, b, layer, H, D, k, v, by_row, wide);
   };
   if (type == KV_TYPE_BF16)
     go(static_cast<__nv_bfloat16*>(out_k), static_cast<__nv_bfloat16*>(out_v));

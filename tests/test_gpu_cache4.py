@@ -193,6 +193,11 @@ def test_gather(dtype, D, H, ps):
         outs = [torch.full((w.n_rows, H, D), 7.0, dtype=T[dtype], device="cuda") for _ in range(2)]
         gt.kv_gather_layer_scaled(d.pool, 1, d.batch, None, *outs)
         assert d.error() == 0
+        n = outs[0].numel()
+        off = 16 // outs[0].element_size()  # outputs that start on 16 bytes, not on 32
+        shifted = [torch.full((n + off,), 7.0, dtype=T[dtype], device="cuda")[off:].view(outs[0].shape) for _ in range(2)]
+        gt.kv_gather_layer_scaled(d.pool, 1, d.batch, None, *shifted)
+        assert all(torch.equal(x.nan_to_num(3.0), y.nan_to_num(3.0)) for x, y in zip(outs, shifted))
         val = w.values()
         for which in (0, 1):
             want = torch.full((w.n_rows, H, D), 7.0, dtype=torch.float64)
