@@ -28,6 +28,12 @@ constexpr int kStageBytes = kStagePieces * 16 * kAppendBlock;
 constexpr int kAppendStages = 3;
 constexpr int kAppendSmem = kAppendStages * kStageBytes;
 
+__device__ __forceinline__ float max_nan(float x, float y) {  // NaN where one of them is
+  float z;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
+}
+
 __device__ __forceinline__ uint4 lds_vec(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
@@ -134,40 +140,45 @@ __device__ __forceinline__ void append_rows(const DevPool& p, const Batch& b, co
     for (int u = 0; u < U; ++u) {
       const int h = h_lo + (item % batches * U + u) * groups;
       if constexpr (FOUR) {
-        // the lanes of a warp stay together, those without a head among them: neighbours exchange below
-        const bool in = h < heads;
-        float x[16];
+        // Where some lane has a head to code, the warp's lanes stay together, those without one among them:
+        // neighbours exchange below.
+        const bool in = h < heads, code = in && h >= g.Q && page != 0;
+        if (__any_sync(kFull, code)) {
+          float x[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = 0.0f;
-        if (in) {
-          Raw<T> raw;
+          for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+          if (in) {
+            Raw<T> raw;
 #pragma unroll
-          for (int v = 0; v < V; ++v) raw.v[v] = lds_vec(slot(item, u, v));
-          unpack(raw, x);
-          if (task.f0 >= 0 && h < g.Q + g.H) turn16(t, x, c, s);
-        }
-        uint32_t top[2] = {0, 0};
-#pragma unroll
-        for (int e = 0; e < 16; ++e) top[e >> 3] = max(top[e >> 3], abs_bits(x[e]));
-#pragma unroll
-        for (int z = 0; z < 2; ++z) top[z] = max(top[z], __shfl_xor_sync(kFull, top[z], 1));
-        if (in && h < g.Q) {
-          store16(static_cast<T*>(g.q_out) + (r * g.Q + h) * g.D, task, x);
-        } else if (in && page != 0) {
-          const int kv = h >= g.Q + g.H;
-          const int hh = h - g.Q - kv * g.H;
-          uint8_t* row = pool_row<uint8_t>(p, g.layer, kv, page, tokens[i].off);
-          uint8_t* codes = row + hh * (g.D / 2);
-          uint8_t* bytes = row + code_bytes(g.H, g.D) + hh * (g.D / 16);
+            for (int v = 0; v < V; ++v) raw.v[v] = lds_vec(slot(item, u, v));
+            unpack(raw, x);
+            if (task.f0 >= 0 && h < g.Q + g.H) turn16_wide(t, x, c, s);
+          }
+          float top[2];
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            const int at = z ? task.b : task.a;
-            const uint32_t byte = scale_byte(top[z]);
-            *reinterpret_cast<uint32_t*>(codes + at / 2) = encode8(x + 8 * z, scale_inverse(byte));
-            if (at % 16 == 0) bytes[at / 16] = static_cast<uint8_t>(byte);
+            top[z] = fabsf(x[8 * z]);
+#pragma unroll
+            for (int e = 1; e < 8; ++e) top[z] = max_nan(top[z], fabsf(x[8 * z + e]));
+            top[z] = max_nan(top[z], __shfl_xor_sync(kFull, top[z], 1));
           }
+          // the even lane works out the scale of the first chunks' block, the odd one of the second chunks'
+          const int odd = lane & 1;
+          const uint32_t byte = scale_byte(abs_bits(odd ? top[1] : top[0]));
+          const float inv = scale_inverse(byte), inv_other = __shfl_xor_sync(kFull, inv, 1);
+          if (code) {
+            const int kv = h >= g.Q + g.H;
+            const int hh = h - g.Q - kv * g.H;
+            uint8_t* row = pool_row<uint8_t>(p, g.layer, kv, page, tokens[i].off);
+            uint8_t* codes = row + hh * (g.D / 2);
+            *reinterpret_cast<uint32_t*>(codes + task.a / 2) = encode8(x, odd ? inv_other : inv);
+            *reinterpret_cast<uint32_t*>(codes + task.b / 2) = encode8(x + 8, odd ? inv : inv_other);
+            row[code_bytes(g.H, g.D) + hh * (g.D / 16) + (odd ? task.b : task.a) / 16] = static_cast<uint8_t>(byte);
+          } else if (in && h < g.Q) {
+            store16(static_cast<T*>(g.q_out) + (r * g.Q + h) * g.D, task, x);
+          }
+          continue;
         }
-        continue;
       }
       if (h >= heads) break;
       T* y;
@@ -184,7 +195,10 @@ __device__ __forceinline__ void append_rows(const DevPool& p, const Batch& b, co
       if (task.f0 >= 0 && h < g.Q + g.H) {
         float x[16];
         unpack(raw, x);
-        turn16(t, x, c, s);
+        if constexpr (FOUR)
+          turn16_wide(t, x, c, s);
+        else
+          turn16(t, x, c, s);
         store16(y, task, x);
       } else {
         store_raw(y, task, raw);

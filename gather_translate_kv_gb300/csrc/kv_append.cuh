@@ -133,6 +133,33 @@ __device__ __forceinline__ void load_cs(const Rot& t, const Task& k, F&& pos, fl
   }
 }
 
+// Two products an instruction, each rounded as on its own. (Sums stay apart: a packed product and a packed sum are
+// fused into one rounding, whatever their rounding says.)
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+
+// turn16 two pairs at a time (half pairing), for the kernel that has more to do than to move rows.
+__device__ __forceinline__ void turn16_wide(const Rot& t, float (&x)[16], const float (&c)[8], const float (&s)[8]) {
+  if (t.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn(x[2 * i], x[2 * i + 1], c[i], s[i]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 x1 = make_float2(x[i], x[i + 1]), x2 = make_float2(x[8 + i], x[9 + i]);
+    const float2 cc = make_float2(c[i], c[i + 1]), ss = make_float2(s[i], s[i + 1]);
+    const float2 c1 = mul2(x1, cc), s2 = mul2(x2, ss), c2 = mul2(x2, cc), s1 = mul2(x1, ss);
+    x[i] = __fsub_rn(c1.x, s2.x), x[i + 1] = __fsub_rn(c1.y, s2.y);
+    x[8 + i] = __fadd_rn(c2.x, s1.x), x[9 + i] = __fadd_rn(c2.y, s1.y);
+  }
+}
+
 __device__ __forceinline__ void turn16(const Rot& t, float (&x)[16], const float (&c)[8], const float (&s)[8]) {
   if (t.interleaved) {
 #pragma unroll
