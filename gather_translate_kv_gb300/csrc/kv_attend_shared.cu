@@ -15,7 +15,12 @@ namespace gtkv {
 
 namespace {
 
-constexpr int kGroupBlock = 128;
+constexpr int kGroupBlock = 256;
+constexpr int kZeroBlocks = 24;  // at least, so that the nodes are zeros at once
+// Rows a KV head and sequence, on average, past which a sequence fills tiles by itself (kv_attend_layer / shared, us, 32 sequences in
+// 4 groups behind 8192 tokens, bf16: 283 / 154 at 64 rows, 287 / 267 at 128, 311 / 489 at 256; 8-bit 316 / 178, 324 / 306,
+// 352 / 571; 4-bit 310 / 190, 318 / 321, 384 / 600).
+constexpr int kOwnTiles = 128;
 
 // Looks at all metadata once. own: the sequences, checked; shared: at the index of a group's first sequence with
 // rows the group as one sequence, whose rows all stand at its prefix' last token, else no rows; from: where the
@@ -116,8 +121,21 @@ Workspace workspace_of(int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int
   return w;
 }
 
-// Rows a KV head and sequence, on average, past which a sequence fills tiles by itself.
-constexpr int kOwnTiles = 128;
+// Whether to share at all, by what the host knows: the tables' width as a bound on the lengths. The shared form is four
+// launches in a row, and until the batch's cache outgrows L2 and what it delivers kv_attend_layer is as fast: elements that it would read
+// more than once, in millions, and us (kv_attend_layer / shared), 8 KV and 32 query heads of 128, one token a sequence: 64
+// sequences of one prefix, bf16, 134 43 / 44, 265 64 / 49, 528 108 / 60; 64 of 16 prefixes 207 66 / 78, 405 110 / 105, 808
+// 346 / 161; 16 of one prefix 128 44 / 51, 253 66 / 60; 8 bits, 64 of 16, 207 60 / 72, 405 99 / 92; 4 bits 64 / 66 and 103 / 86.
+bool worth_sharing(const DevPool& p, const Batch& b, const AttendArgs& a, int32_t n_groups) {
+  if (n_groups >= b.n_seqs || b.n_rows * a.G > kOwnTiles * static_cast<int64_t>(b.n_seqs)) return false;
+  const double again = static_cast<double>(b.n_seqs - n_groups) * b.max_pages * p.ps * a.H * a.D * 2;
+  return again >= (b.n_seqs / 32 >= n_groups ? 0x1p27 : 0x1p28);
+}
+
+// Which kernel attends to the prefixes, by a group's rows of a KV head on average: k_attend_few up to 8 (8-bit and 4-bit caches 32), else
+// k_attend_tile. 16-bit, 16 rows: 64 sequences in 16 groups behind 2048 tokens 84 / 78 us, 8192 tokens 197 / 160, 8 rows (32 groups, 4096)
+// 130 / 152; 8-bit, 16 rows, 8192 tokens 130 / 175, 32 rows, 4096 tokens 116 / 124, 62 rows 489 / 355; 4-bit 125 / 230, 111 / 140.
+int64_t prefix_few_rows(Kind kind) { return kind == Kind::kElements ? 8 : 32; }
 
 }  // namespace
 
@@ -128,7 +146,7 @@ int64_t attend_shared_workspace_bytes(int32_t Q, int32_t D, int32_t n_seqs, int6
 cudaError_t launch_attend_shared(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, const int32_t* group,
                                  const int32_t* prefix_len, int32_t n_groups, void* workspace, int sm_count,
                                  cudaStream_t s) {
-  if (!has_tiles(a.D) || n_groups >= b.n_seqs || b.n_rows * a.G > kOwnTiles * static_cast<int64_t>(b.n_seqs))
+  if (!has_tiles(a.D) || !worth_sharing(p, b, a, n_groups))
     return launch_attend(p, b, a, kind, workspace, sm_count, s);
   const Workspace w = workspace_of(a.Q, a.D, b.n_seqs, b.n_rows, sm_count);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -137,7 +155,7 @@ cudaError_t launch_attend_shared(const DevPool& p, const Batch& b, const AttendA
   int32_t* from = reinterpret_cast<int32_t*>(ws + w.from);
   int32_t* nodes = reinterpret_cast<int32_t*>(ws + w.nodes);
   const int32_t n_nodes = static_cast<int32_t>(2 * few_nodes(sm_count) + tile_nodes(sm_count));
-  k_share_groups<<<n_groups < 2 * sm_count ? n_groups : 2 * sm_count, kGroupBlock, 0, s>>>(
+  k_share_groups<<<n_groups < kZeroBlocks ? kZeroBlocks : n_groups < 2 * sm_count ? n_groups : 2 * sm_count, kGroupBlock, 0, s>>>(
       p, b, group, prefix_len, n_groups, a.G, own, shared, from, nodes, n_nodes);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -149,7 +167,7 @@ cudaError_t launch_attend_shared(const DevPool& p, const Batch& b, const AttendA
   bb.n_spans = n_groups;
   aa.state = reinterpret_cast<float*>(ws + w.state);
   aa.Gp = INT32_MAX;
-  if (b.n_rows * a.G <= few_rows_of(kind) * static_cast<int64_t>(n_groups))
+  if (b.n_rows * a.G <= prefix_few_rows(kind) * static_cast<int64_t>(n_groups))
     e = launch_attend_few(p, bb, aa, kind, INT32_MAX, ws + w.tiles, sm_count, Launch::kFirst, nodes, &split, s);
   else
     e = launch_attend_tile(p, bb, aa, kind, 1, ws + w.tiles, sm_count, Launch::kFirst, nodes + 2 * few_nodes(sm_count), &split, s);

@@ -36,7 +36,7 @@ class Shared:
     """A World whose groups share their first tokens: whole pages by the table, the
     rest of the last one by its contents."""
 
-    def __init__(self, seed, groups, cache, *, gap=False, **kw):
+    def __init__(self, seed, groups, cache, *, gap=False, wide=True, **kw):
         lens = [p + a for p, members in groups for a, _ in members]
         news = [n for _, members in groups for _, n in members]
         w = ref4.world(seed, lens, news, gap=gap, **kw) if cache == "e2m1" else ref.world(seed, lens, news, cache=cache,
@@ -56,6 +56,12 @@ class Shared:
                         w.scales[b] = w.scales[a]
             self.group.append(s0 + len(members))
             self.prefix.append(p)
+        if wide and w.S > len(groups):
+            # tables so wide that the batch may be far larger than the caches: sharing pays, as far as the host can tell
+            pages = -(-2 ** 28 // ((w.S - len(groups)) * w.H * w.D * 2 * w.ps))
+            if pages > w.table.shape[1]:
+                fill = np.full((w.S, pages - w.table.shape[1]), 0x7ffffff0, dtype=np.int32)  # never read
+                w.table = np.concatenate([w.table, fill], 1)
 
     def dev(self, kernel_facing=False):
         return (Dev4 if self.cache == "e2m1" else Dev)(self.w, kernel_facing)
@@ -109,6 +115,13 @@ def test_shared(cache, dtype, groups, D):
     check(Shared(len(groups) + D, GROUPS[groups], cache, D=D, gap=groups in ("mixed", "many")), 8, dtype)
 
 
+@pytest.mark.parametrize("cache,dtype", CACHES[:5:2])
+@pytest.mark.parametrize("groups", list(GROUPS))
+def test_shared_in_narrow_tables(cache, dtype, groups):
+    """Batches that are too small for sharing to pay."""
+    check(Shared(3, GROUPS[groups], cache, wide=False), 8, dtype)
+
+
 @pytest.mark.parametrize("cache,dtype", CACHES[1::2])
 @pytest.mark.parametrize("ps", [1, 4, 7, 16, 24, 64, 256])
 @pytest.mark.parametrize("groups", ["decode", "drafts", "many"])
@@ -139,7 +152,7 @@ def test_shared_tombstones(cache, dtype):
     w.table[3:5, :4] = -1
     w.table[5, 6] = -1   # nothing of its own
     check(sh, 4, dtype)
-    w.table[5:7] = -1    # nothing at all
+    w.table[5:7, :8] = -1  # nothing at all
     check(sh, 4, dtype)
 
 
