@@ -81,7 +81,10 @@ struct TileSmem {
   static constexpr int kQ = 0;  // two tiles
   static constexpr int kTiles = 2 * kOperand;
   static constexpr int kRaw = kTiles + kRing * kOperand;
-  static constexpr int kMasks = kRaw + kRawRing * kRawTile;
+  // 4-bit caches: scale bytes as they were copied, of this step and the next: per key K's and V's
+  static constexpr int kRawScale = kE2M1 ? D / 16 : 0;
+  static constexpr int kRawScales = kRaw + kRawRing * kRawTile;
+  static constexpr int kMasks = kRawScales + 2 * 128 * 2 * kRawScale;
   static constexpr int kScales = kMasks + kSlots * static_cast<int>(sizeof(Masks));
   static constexpr int kQScale = kScales + (kE4M3 ? kSlots * static_cast<int>(sizeof(Scales)) : 0);
   static constexpr int kBar = kQScale + (kCodes ? 2 * kRows * 4 : 0);  // of this unit's and the next one's rows
@@ -184,6 +187,12 @@ __device__ __forceinline__ void sts128(uint32_t at, uint4 v) {
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t lds16(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
   return v;
 }
 
@@ -645,14 +654,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
     uint32_t u = 0;   // units with rows in the warp's tile of queries
     const int qt = lw >> 1;
     bool ok = true;
+    // (positions and rows are below 2^31)
+    auto page_index = [&](uint32_t j) { return p.ps_shift >= 0 ? j >> p.ps_shift : j / static_cast<uint32_t>(p.ps); };
     // the loader's 32 keys of a step: key lw * 32 + lane is this lane's
     auto entry = [&](int32_t i) -> int32_t {
       if (i >= g.end) return 0;
-      const int64_t j = static_cast<int64_t>(g.span.block(i)) * kKeys + lw * 32 + lane;
+      const uint32_t j = static_cast<uint32_t>(g.span.block(i)) * kKeys + lw * 32 + lane;
       // (keys that share the scales of 16 share their page too, so all of them are looked up or none)
       constexpr int64_t kShared = kE4M3 && P16 ? 15 : 0;
-      if (j > g.i1 || !some_row_sees(a, g.i0, j & ~kShared, j | kShared)) return 0;
-      return __ldg(b.table + static_cast<int64_t>(g.s) * b.max_pages + div_ps(p, j));
+      if (j > static_cast<uint32_t>(g.i1) || !some_row_sees(a, g.i0, j & ~kShared, j | kShared)) return 0;
+      return __ldg(b.table + static_cast<int64_t>(g.s) * b.max_pages + page_index(j));
     };
     struct Keys {
       int32_t row, page;  // this lane's key; row -1: no token
@@ -662,11 +673,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
     auto keys_of = [&](int32_t i, int32_t ent) -> Keys {
       Keys k;
       const int32_t j0 = g.span.block(i) * kKeys;
-      const int64_t j = static_cast<int64_t>(j0) + lw * 32 + lane;
+      const uint32_t j = static_cast<uint32_t>(j0) + lw * 32 + lane, ps = static_cast<uint32_t>(p.ps);
       k.page = static_cast<int32_t>(page_of_entry(p, b, ent, bits));
       k.row = k.page == 0 ? -1
-                          : static_cast<int32_t>(k.page * p.stride + 2 * static_cast<int64_t>(a.layer) * p.ps +
-                                                 (j - div_ps(p, j) * p.ps));
+                          : static_cast<int32_t>(static_cast<uint32_t>(k.page) * static_cast<uint32_t>(p.stride) + 2 * a.layer * ps +
+                                                 (p.ps_shift >= 0 ? j & (ps - 1) : j % ps));
       k.live = __ballot_sync(kFull, k.page != 0);
       k.partial = j0 + kKeys - 1 > g.i0 || (a.window && j0 <= g.i1 - a.window) || k.live != kFull;
       return k;
@@ -768,12 +779,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
     // waits until tile t - kRing has been used
     auto claim = [&](uint32_t t) { return wait(bar(Sm::kFree + t % Sm::kRing), (t / Sm::kRing & 1) ^ 1); };
     const int32_t row_bytes = static_cast<int32_t>(p.vpr * 16);
-    // Copies 32 rows (of lane k the k-th) of K, or of V when `v`; at(round, piece): where a lane's piece goes.
-    auto copy = [&](auto at, int32_t row_of_lane, bool v) {
-      const uint8_t* from = pool + static_cast<int64_t>(g.h) * RB + lc * 16 + (v ? p.ps * row_bytes : 0);
-      int32_t ro[IT];  // all shuffles first: their latencies overlap
+    // Copies 32 rows (of round `it` the lane's ro[it]) of K, or of V when `v`; at(round, piece): where a lane's piece goes.
+    auto rows_of = [&](int32_t row_of_lane, int32_t* ro) {  // all shuffles together: their latencies overlap
 #pragma unroll
       for (int it = 0; it < IT; ++it) ro[it] = __shfl_sync(kFull, row_of_lane, it * RPI + lr);
+    };
+    auto copy = [&](auto at, const int32_t* ro, bool v) {
+      const uint8_t* from = pool + static_cast<int64_t>(g.h) * RB + lc * 16 + (v ? p.ps * row_bytes : 0);
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
         const bool ok = ro[it] >= 0;
@@ -790,11 +802,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
       // tile that a copy overwrites is the one turned just before it.
       struct Step {
         Keys k;
-        float ks, vs;     // 8-bit caches: the scales of the lane's key
-        uint32_t k4[kE2M1 ? IT : 1], v4[kE2M1 ? IT : 1];  // 4-bit caches: two scale bytes for each piece that the lane turns
+        float ks, vs;         // 8-bit caches: the scales of the lane's key
         bool first, queries;  // first of its unit; the unit has rows in the warp's tile
       };
       const uint32_t raw0 = base + Sm::kRaw + lw * 32 * RB + lane * 16;
+      // 4-bit caches: scales of step n, of the warp's keys, K's and V's. (Through registers, as the two of an 8-bit cache,
+      // they cost chunks 547 us instead of 502; those in shared memory 531 instead of 520.)
+      constexpr int SB = Sm::kRawScale;
+      const uint32_t scales0 = base + Sm::kRawScales + lw * 32 * 2 * SB;
+      auto raw_scales = [&](uint32_t n) { return scales0 + (n & 1) * (128 * 2 * SB); };
       auto raw = [&](uint32_t t, int it) { return raw0 + t % 3 * Sm::kRawTile + it * 512; };
       int64_t qa = -1, qb = -1;
       // the step after the one in `walk`, as far as its lookups go
@@ -807,25 +823,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
         s.queries = qt * 128 < g.nf;
         ent = entry(i + 1);
         s.ks = s.vs = 0.0f;
-        if constexpr (kE2M1) {
-          const uint8_t* from = pool + code_bytes(a.H, D) + g.h * (D / 16) + lc * 2;
-          int32_t ro[IT];
-#pragma unroll
-          for (int it = 0; it < IT; ++it) ro[it] = __shfl_sync(kFull, s.k.row, it * RPI + lr);
-#pragma unroll
-          for (int it = 0; it < IT; ++it) {
-            s.k4[it] = s.v4[it] = 0;
-            if (ro[it] < 0) continue;
-            const uint8_t* row = from + static_cast<int64_t>(ro[it]) * row_bytes;
-            s.k4[it] = __ldg(reinterpret_cast<const uint16_t*>(row));
-            s.v4[it] = __ldg(reinterpret_cast<const uint16_t*>(row + p.ps * row_bytes));
-          }
-        } else if (s.k.page != 0) {
+        if (kE4M3 && s.k.page != 0) {
           const int64_t at = (static_cast<int64_t>(s.k.page) * p.blocks + 2 * a.layer) * a.H + g.h;
           s.ks = __ldg(a.scales + at);
           s.vs = __ldg(a.scales + at + a.H);
         }
         return s;
+      };
+      // copies a step's scales, in the group of its keys
+      auto copy_scales = [&](uint32_t n, const Keys& k) {
+        if constexpr (kE2M1) {
+          const bool live = k.page != 0;
+          const uint32_t to = raw_scales(n) + lane * 2 * SB;
+          const uint8_t* from = pool + code_bytes(a.H, D) + g.h * SB + static_cast<int64_t>(live ? k.row : 0) * row_bytes;
+          copy_async<SB>(to, from, live);
+          copy_async<SB>(to + SB, from + (live ? p.ps * row_bytes : 0), live);
+        }
       };
       auto advance = [&]() {
         if (++i == g.end) {
@@ -836,102 +849,140 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           }
         }
       };
-      auto turn_tile = [&](uint32_t t, bool check, const uint32_t (&s4)[kE2M1 ? IT : 1]) -> uint32_t {
+      // In batches whose loads come first, and in a loop: the warps of a scheduler run through more code a step than its
+      // instruction cache holds, and what is written out is fetched every time (chunks, batches of all rounds / these, written out: 8-bit 531 /
+      // 484 us, 4-bit 491 / 460).
+      auto turn_tile = [&](uint32_t t, bool check) -> uint32_t {
         uint32_t bad_rows = 0;
         const uint32_t to = operand(t);
-        uint4 codes[IT];  // all loads first: what follows is a chain each
-#pragma unroll
-        for (int it = 0; it < IT; ++it) codes[it] = lds128(raw(t, it));
         if constexpr (kE2M1) {
+          constexpr int B = 2;
+#pragma unroll 1
+          for (int it0 = 0; it0 < IT; it0 += B) {
+            uint32_t s4[B];
+            uint4 codes[B];
 #pragma unroll
-          for (int it = 0; it < IT; ++it) {
-            const uint4 v = codes[it];
-            uint32_t bytes = s4[it];
-            const uint32_t bad = bad_scales(bytes);
-            if (!check) {
-              bytes |= bad;
-            } else if (bad) {
-              bad_rows |= 1u << (it * RPI + lr);
-              bytes &= ~bad;
+            for (int ib = 0; ib < B; ++ib) {
+              codes[ib] = lds128(raw(t, it0 + ib));
+              s4[ib] = lds16(raw_scales(t >> 1) + (((it0 + ib) * RPI + lr) * 2 + (t & 1)) * SB + lc * 2);
             }
-            const uint32_t sc[2] = {__byte_perm(bytes, 0, 0x4040) << 7, __byte_perm(bytes, 0, 0x4141) << 7};
-            const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-            const int rr = lw * 32 + it * RPI + lr;
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              uint32_t y[4];
-              codes8(w4[z], y);
-              sts128(to + piece_at(rr, 4 * lc + z), make_uint4(mul_h2(y[0], sc[z >> 1]), mul_h2(y[1], sc[z >> 1]),
-                                                               mul_h2(y[2], sc[z >> 1]), mul_h2(y[3], sc[z >> 1])));
+            for (int ib = 0; ib < B; ++ib) {
+              const int it = it0 + ib;
+              const uint4 v = codes[ib];
+              uint32_t bytes = s4[ib];
+              const uint32_t bad = bad_scales(bytes);
+              if (!check) {
+                bytes |= bad;
+              } else if (bad) {
+                bad_rows |= 1u << (it * RPI + lr);
+                bytes &= ~bad;
+              }
+              const uint32_t sc[2] = {__byte_perm(bytes, 0, 0x4040) << 7, __byte_perm(bytes, 0, 0x4141) << 7};
+              const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+              const int rr = lw * 32 + it * RPI + lr;
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                uint32_t y[4];
+                codes8(w4[z], y);
+                sts128(to + piece_at(rr, 4 * lc + z), make_uint4(mul_h2(y[0], sc[z >> 1]), mul_h2(y[1], sc[z >> 1]),
+                                                                 mul_h2(y[2], sc[z >> 1]), mul_h2(y[3], sc[z >> 1])));
+              }
             }
           }
           fence_async_shared();
           return bad_rows;
         }
+        constexpr int B = 4;
+#pragma unroll 1
+        for (int it0 = 0; it0 < (kE2M1 ? 0 : IT); it0 += B) {
+          uint4 codes[B];
 #pragma unroll
-        for (int it = 0; it < IT; ++it) {
-          uint4 v = codes[it];
-          if (check) {
-            const uint4 z = make_uint4(not_finite<C>(v.x), not_finite<C>(v.y), not_finite<C>(v.z), not_finite<C>(v.w));
-            if (z.x | z.y | z.z | z.w) {
-              bad_rows |= 1u << (it * RPI + lr);
-              v = make_uint4(v.x & ~z.x, v.y & ~z.y, v.z & ~z.z, v.w & ~z.w);
+          for (int ib = 0; ib < B; ++ib) codes[ib] = lds128(raw(t, it0 + ib));
+#pragma unroll
+          for (int ib = 0; ib < B; ++ib) {
+            const int it = it0 + ib;
+            uint4 v = codes[ib];
+            if (check) {
+              const uint4 z = make_uint4(not_finite<C>(v.x), not_finite<C>(v.y), not_finite<C>(v.z), not_finite<C>(v.w));
+              if (z.x | z.y | z.z | z.w) {
+                bad_rows |= 1u << (it * RPI + lr);
+                v = make_uint4(v.x & ~z.x, v.y & ~z.y, v.z & ~z.z, v.w & ~z.w);
+              }
             }
+            uint4 lo, hi;
+            decode16(v, lo, hi);
+            const int rr = lw * 32 + it * RPI + lr;
+            sts128(to + piece_at(rr, 2 * lc), lo);
+            sts128(to + piece_at(rr, 2 * lc + 1), hi);
           }
-          uint4 lo, hi;
-          decode16(v, lo, hi);
-          const int rr = lw * 32 + it * RPI + lr;
-          sts128(to + piece_at(rr, 2 * lc), lo);
-          sts128(to + piece_at(rr, 2 * lc + 1), hi);
         }
         fence_async_shared();
         return bad_rows;
       };
       if (have) {
         Step cur = look();
-        copy([&](int it, int) { return raw(0, it); }, cur.k.row, false);
-        copy([&](int it, int) { return raw(1, it); }, cur.k.row, true);
+        copy_scales(0, cur.k);
+        int32_t ro[IT];
+        rows_of(cur.k.row, ro);
+        copy([&](int it, int) { return raw(0, it); }, ro, false);
+        copy([&](int it, int) { return raw(1, it); }, ro, true);
         query_rows(qa, qb);
         for (bool go = true; go;) {
-          const uint32_t t = 2 * n;
           int64_t na = -1, nb = -1;
           advance();
           go = have;
           Step next{};
           if (have) {
             next = look();
-            copy([&](int it, int) { return raw(t + 2, it); }, next.k.row, false);
-            if (next.first) query_rows(na, nb);
-          } else {
-            copy_commit();
+            copy_scales(n + 1, next.k);
+            rows_of(next.k.row, ro);
+            if (next.first) {
+              query_rows(na, nb);
+              for (int k = 0; k < 2 * D; k += 128) {  // on their way when the unit begins
+                if (na >= 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.q) + 2 * na + k));
+                if (nb >= 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.q) + 2 * nb + k));
+              }
+            }
           }
-          copy_wait<2>();
-          if (!claim(t)) break;
-          if constexpr (kE4M3) {
-            Scales& sl = scales[n % kSlots];
-            sl.ks[lw * 32 + lane] = cur.k.page != 0 ? cur.ks : 1.0f;  // no token: 2^-inf through lv, whatever the score
-            sl.lv[lw * 32 + lane] = lg2(cur.vs);
-            sl.iv[lw * 32 + lane] = cur.k.page != 0 ? rcp(cur.vs) : 0.0f;
+          bool gone = false;
+#pragma unroll
+          for (uint32_t v = 0; v < 2; ++v) {
+            if (gone) break;
+            const uint32_t t = 2 * n + v;
+            if (have)
+              copy([&](int it, int) { return raw(t + 2, it); }, ro, v != 0);
+            else
+              copy_commit();
+            copy_wait<2>();
+            if constexpr (kE2M1) __syncwarp();  // scales that other lanes copied
+            gone = !claim(t);
+            if (gone) break;
+            if (v == 0) {
+              if constexpr (kE4M3) {
+                Scales& sl = scales[n % kSlots];
+                sl.ks[lw * 32 + lane] = cur.k.page != 0 ? cur.ks : 1.0f;  // no token: 2^-inf through lv, whatever the score
+                sl.lv[lw * 32 + lane] = lg2(cur.vs);
+                sl.iv[lw * 32 + lane] = cur.k.page != 0 ? rcp(cur.vs) : 0.0f;
+              }
+              if (lane == 0) masks[n % kSlots].live[lw] = cur.k.live;
+            }
+            const uint32_t bad_rows = turn_tile(t, v != 0 && cur.k.partial);
+            if (v != 0) {
+              const uint32_t nan = __reduce_or_sync(kFull, bad_rows);
+              if (lane == 0) masks[n % kSlots].nan[lw] = nan;
+            }
+            warp_arrive(full(t));
+            if (v == 0 && cur.first && cur.queries) {
+              gone = !wait(bar(Sm::kQFree + qt), (u & 1) ^ 1);
+              if (gone) break;
+              load_queries(qa, qb);
+              fence_async_shared();
+              warp_arrive(bar(Sm::kQFull + qt));
+              ++u;
+            }
           }
-          if (lane == 0) masks[n % kSlots].live[lw] = cur.k.live;
-          turn_tile(t, false, cur.k4);
-          warp_arrive(full(t));
-          if (cur.first && cur.queries) {
-            if (!wait(bar(Sm::kQFree + qt), (u & 1) ^ 1)) break;
-            load_queries(qa, qb);
-            fence_async_shared();
-            warp_arrive(bar(Sm::kQFull + qt));
-            ++u;
-          }
-          if (have)
-            copy([&](int it, int) { return raw(t + 3, it); }, next.k.row, true);
-          else
-            copy_commit();
-          copy_wait<2>();
-          if (!claim(t + 1)) break;
-          const uint32_t bad_rows = __reduce_or_sync(kFull, turn_tile(t + 1, cur.k.partial, cur.v4));
-          if (lane == 0) masks[n % kSlots].nan[lw] = bad_rows;
-          warp_arrive(full(t + 1));
+          if (gone) break;
           if (next.first) {
             qa = na;
             qb = nb;
@@ -947,7 +998,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
       bool pending = false, pending_partial = false;
       auto put = [&](uint32_t t, const Keys& k) {
         const uint32_t to = operand(t);
-        copy([&](int it, int z) { return to + piece_at(lw * 32 + it * RPI + lr, lc + z * LPR); }, k.row, t & 1);
+        int32_t ro[IT];
+        rows_of(k.row, ro);
+        copy([&](int it, int z) { return to + piece_at(lw * 32 + it * RPI + lr, lc + z * LPR); }, ro, t & 1);
       };
       auto announce_v = [&](uint32_t m) {  // V of step m has arrived
         uint32_t bad_rows = 0;
