@@ -421,7 +421,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           auto buf = [&](int k) -> uint32_t(&)[32] { return k & 1 ? rb : ra; };
           tmem_load32(tS, ra);
           tmem_wait_ld(ra);
-#pragma unroll
+          // Half of it written out: what both tiles' warps run through stays nearer to the instruction caches (8 prompts of 2048 tokens,
+          // written out / half: 16-bit 457 / 410 us, 8-bit 560 / 509, 4-bit 523 / 484; fp16 output 459 / 411, 695 / 598, 638 /
+          // 544). Prefixes of one tile of rows have the whole chain to wait for instead (62 rows: 288 / 295, 8-bit fp16 324 /
+          // 334, 4-bit fp16 284 / 323, but 4-bit bf16 315 / 265).
+          constexpr int kWritten = SHARED && (!kE2M1 || TWO) ? 4 : 2;
+#pragma unroll kWritten
           for (int k = 0; k < 4; ++k) {
             uint32_t(&x)[32] = buf(k);
             if (k < 3) tmem_load32(tS + 32 * (k + 1), buf(k + 1));
