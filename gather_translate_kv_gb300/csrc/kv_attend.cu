@@ -80,14 +80,13 @@ int64_t attend_workspace_bytes(int32_t, int32_t, int32_t D, int32_t, int64_t, in
 }
 
 // Which kernels: the few-rows kernel alone when the sequences' rows of a KV
-// head number at most 16 (8-bit caches: 32) on average (decode steps and
+// head number at most 16 (8-bit and 4-bit caches: 32) on average (decode steps and
 // drafts; a longer sequence among them takes several row tiles there), else both, each taking the
 // sequences on its side of that. Lengths are known on the device alone, so the
 // rule goes by averages. 32 sequences of 4000 tokens, 4 query heads a KV head,
-// D = 128, few-rows against tile kernel: 16-bit 108 / 150 us at 8 rows, 138 /
-// 152 at 16, 205 / 154 at 24; 8-bit, whose codes the tile kernel is slow to
-// turn into fp16, 83 / 174 at 16, 138 / 183 at 32, 194 / 183 at 48 (fp16 output: 93 / 214 at 16, 151 / 218 at 24,
-// 272 / 226 at 64).
+// D = 128, few-rows against tile kernel, us: 16-bit 110 / 148 at 8 rows, 141 / 150 at 16, 206 / 152 at 24; 8-bit 87 / 154
+// at 16, 139 / 160 at 32, 201 / 162 at 48 (fp16 output 95 / 190, 155 / 196, 222 / 197); 4-bit 79 / 157, 131 / 160,
+// 184 / 163 (fp16 output 85 / 186, 143 / 188, 202 / 191).
 cudaError_t launch_tiles(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, void* workspace, int sm_count,
                          cudaStream_t s) {
   const int32_t few_rows = few_rows_of(kind);

@@ -1,5 +1,5 @@
 // Attention of few rows a sequence (decode steps, drafted tokens): at most 16
-// rows (8-bit caches: 32) on average, a row being a (token, query head) pair of one KV head, in
+// rows (8-bit and 4-bit caches: 32) on average, a row being a (token, query head) pair of one KV head, in
 // tiles of 8 or 16; a sequence with more takes several tiles. Every key and
 // value is read once and meets a handful of rows, so the bound is memory; the
 // work is laid out so that nothing stands between the loads.
@@ -33,6 +33,14 @@
 // us from one GPU to another, 91 to 93 % of the copy rate; 40 sequences of 9 to 40 961 tokens with drafts
 // (8-bit, 1.68 GB) 364 us, 68 %, bound by latency inside a warp (codes into fp16, products,
 // weights, one after the other) with three warps a scheduler; one sequence of 203 tokens 14 us, latency.
+//
+// 4-bit caches. A lane's piece of a key is a quarter of the head (two blocks of 16 and their scale bytes), its part of a
+// value an eighth (one block, or half of one). Two elements become fp16 by one conversion and one product with
+// the block's scale, exactly; codes of two values share a byte before that, so that no halves are exchanged. That is 64 conversions (at half
+// rate) and 64 products a lane and step, which is what bounds the kernel, with the chains between them: 256 x 4096 tokens
+// (1.2 GB) 336 us, 53 % of the copy rate, issue slots 60 % busy, `wait` the top stall; two blocks of keys a round 336 us, one 365;
+// four stages of the ring, not six, which leave room for L1 (365 / 392); 16 columns need all registers of two blocks an SM (drafts of 9 to
+// 40 961 tokens, fp16, 388 us; three blocks, which spill, 416).
 //
 // Workers (as many warps as share a step's heads) take equal shares of all
 // steps of the batch (kv_attend_split.cuh); units cut at a border are joined by
@@ -146,7 +154,7 @@ struct FewShape {
   static constexpr int kStages = kRow >= 256 ? 2 : kRow >= 128 ? 3 : kE2M1 && D == 128 ? 4 : 6;
   static constexpr int kDeep = 6;
   // blocks of 16 keys a round of the loop: two of a 4-bit cache, whose loads and softmax are little beside what a
-  // round costs anyway, and whose conversions are chains that then overlap
+  // round costs anyway, and whose conversions are chains that then overlap (16 columns have no registers for it: drafts 389 / 400 us)
   static __host__ __device__ constexpr int blocks(int nt) { return kE2M1 && nt == 1 ? 2 : 1; }
   static constexpr int kKS = D / 16;          // k16 steps of the score product
   static constexpr int kMT = D / 16;          // 16-element tiles of the output

@@ -17,7 +17,8 @@ constexpr int kFewWarps = 4;
 constexpr int kFewBlock = 32 * kFewWarps;
 constexpr int kFewBlocksPerSM = 4;  // at most
 constexpr int kFewUnitCost = 2;     // steps' worth of a unit's queries and output
-// Resident blocks: shared memory for 256-byte rows, registers for 16 columns allow three.
+// Resident blocks: shared memory for 256-byte rows, registers for 16 columns allow three, or two without spills
+// where codes of 4 bits are turned.
 constexpr int few_blocks(int row, int nt, bool e2m1) { return e2m1 && nt > 1 ? 2 : row >= 256 || nt > 1 ? 3 : kFewBlocksPerSM; }
 
 // Tiles of rows.

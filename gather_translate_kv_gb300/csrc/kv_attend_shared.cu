@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kGroupBlock) k_share_groups(DevPool p, Batch b
     }
     __syncthreads();
     int32_t prefix = min(__ldg(prefix_len + g), a) & ~15;
-    if (n < 2 || prefix < 16 || (r1 - r0) * G > INT32_MAX) prefix = 0;
+    if (n < 2 || prefix < 16 || (r1 - r0) * G > INT32_MAX - 1024) prefix = 0;
     for (int32_t s = s0 + tid; s < s1; s += kGroupBlock) {
       from[s] = prefix;
       shared[s] = prefix != 0 && s == s_first ? Seq{r0, prefix - 1, static_cast<int32_t>(r1 - r0)} : Seq{0, 0, 0};
@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(kGroupBlock) k_share_groups(DevPool p, Batch b
   store_bits(p, bits);
 }
 
-int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+constexpr int64_t kAlign = 256;
+int64_t aligned(int64_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
 struct Workspace {
   int64_t own, shared, from, nodes, tiles, few, state, bytes;
@@ -107,7 +108,7 @@ Workspace workspace_of(int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int
   Workspace w{};
   auto take = [&](int64_t n) {
     const int64_t at = w.bytes;
-    w.bytes += align256(n);
+    w.bytes += aligned(n);
     return at;
   };
   w.tiles = take(attend_workspace_bytes(0, Q, D, n_seqs, n_rows, sm_count));
@@ -118,6 +119,7 @@ Workspace workspace_of(int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int
   w.nodes = take((2 * few_nodes(sm_count) + tile_nodes(sm_count)) * 4);
   w.few = take(attend_few_workspace(D, sm_count));
   w.state = take(n_rows * Q * (D + 2) * 4);
+  w.bytes += kAlign;  // the caller's buffer starts on 16 bytes, sums are written 32 at a time
   return w;
 }
 
@@ -149,7 +151,7 @@ cudaError_t launch_attend_shared(const DevPool& p, const Batch& b, const AttendA
   if (!has_tiles(a.D) || !worth_sharing(p, b, a, n_groups))
     return launch_attend(p, b, a, kind, workspace, sm_count, s);
   const Workspace w = workspace_of(a.Q, a.D, b.n_seqs, b.n_rows, sm_count);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(aligned(static_cast<int64_t>(reinterpret_cast<uintptr_t>(workspace))));
   Seq* own = reinterpret_cast<Seq*>(ws + w.own);
   Seq* shared = reinterpret_cast<Seq*>(ws + w.shared);
   int32_t* from = reinterpret_cast<int32_t*>(ws + w.from);

@@ -244,6 +244,7 @@ __device__ __forceinline__ bool meet(int32_t* node, int32_t worker, int32_t* oth
     x = __shfl_sync(kFull, x, 0);
     if (x == 0) return false;
   }
+  __syncwarp();  // what lane 0 has seen comes before the other lanes' loads
   __threadfence();
   *other = x - 1;
   return true;

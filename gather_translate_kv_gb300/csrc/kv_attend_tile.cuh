@@ -15,7 +15,7 @@
 // Warps 0-3 and 4-7: softmax of tile 0 and 1, one row a thread (no shuffles).
 // Warps 8-11: loaders; they look up the pages, copy keys and values into the
 // 128-byte-swizzled operand layout with cp.async (16-bit caches) or through
-// registers, turning codes into fp16 (8-bit caches), and zero what is no live
+// registers, turning codes into fp16 (8-bit and 4-bit caches), and zero what is no live
 // token. Pages of any size end anywhere in a tile, so keys are placed row by
 // row rather than by a tensor map. Warp 12 issues the products.
 //
@@ -25,8 +25,8 @@
 // the cache's 16-bit type (bf16, or fp16 lifted by 2^6 for fp16 and 8-bit caches), rounded
 // and what the rounding left, so that the result's error is the output's own rounding: 1.479e-4
 // (root mean square, prompts of 2048 tokens in bf16), as the formula in 32 bits has it, where one part
-// gave 1.903e-4 for 698 us instead of 831. Of 8-bit caches read into bf16, whose 8 bits
-// hide fp16's 11, one part is enough (7.45e-5 and 7.39e-5; 1180 and 1420 us for the same prompts in 8 bits). Denominators
+// gave 1.903e-4 for 698 us instead of 831 (in an earlier form of the kernel). Of 8-bit and 4-bit caches read into bf16, whose 8 bits
+// hide fp16's 11, one part is enough (7.45e-5 and 7.39e-5; the same prompts in 8 bits 952 us, in fp16 with two parts 1108). Denominators
 // add the 32-bit weights. The scale of
 // an 8-bit value is part of its weight, t = score * log2(e) + log2(scale), and
 // the denominator adds weight / scale. Queries for 8-bit caches become fp16
@@ -35,14 +35,12 @@
 // Work is cut as in kv_attend_split.cuh, 128 keys a step.
 //
 // Measured: 16 prompts of 2048 tokens (bf16, 8 KV and 32 query heads of 128,
-// 550 GFLOP) 831 us, 35 % of the measured cuBLAS burst; 4 of 8192 tokens 2220 us. From the two, a step of
-// both tiles takes 2.1 us (4390 cycles at 2070 MHz; 48 products of 64 cycles each are
-// 70 % of them), the rest the chain from scores through
-// weights to the second product, and a unit ~13 us more for its queries,
-// masked last step and output. The kernel is at the limit of 128 registers a thread. 4
-// chunks of ~1000 tokens on 6001 to 8190 (8-bit) 530 us; three more loader warps there, sharing rounds of rows or
-// taking the values alone, made an earlier form slower (630 against 945 us, 4 x 1000 tokens on 8000), idle ones
-// did not (647).
+// 550 GFLOP) 752 to 766 us, 38 % of the measured cuBLAS burst; 4 of 8192 tokens 2240 us; the 16 prompts in 8 bits 952, in 4 bits
+// 890 us. Chunks of ~1000 tokens on 6001 to 8190: 16-bit 457 us, 8-bit 451, 4-bit 440, so that what bounds them is no
+// longer the loaders but the chain from scores through weights to the second product. The kernel is at the limit of 128
+// registers a thread, and the code that its warps run through in a step is larger than the instruction caches near them: where
+// loops of the loaders and of the softmax are written out only in part it is 10 to 15 % faster (figures beside them).
+// A unit costs ~13 us beside its steps, for its queries, masked last step and output.
 #pragma once
 
 #include "kv_attend_split.cuh"

@@ -173,7 +173,7 @@ int kv_attend_shared_workspace_bytes(const kv_pool_t* pool, int32_t q_heads, int
                                      int64_t* bytes) {
   const int rc = kv_attend_workspace_bytes(pool, q_heads, n_seqs, n_rows, bytes);
   if (rc != KV_OK) return rc;
-  if (n_rows > (int64_t(1) << 40)) return KV_ERR_INVALID;  // (n_rows * q_heads * head_dim stays below 2^63)
+  if (n_rows > (int64_t(1) << 36)) return KV_ERR_INVALID;  // 4 * n_rows * q_heads * (head_dim + 2) stays below 2^63
   *bytes = gtkv::attend_shared_workspace_bytes(q_heads, pool->desc.head_dim, n_seqs, n_rows, pool->sm_count);
   return KV_OK;
 }

@@ -179,7 +179,10 @@ typedef struct {
  * prefix that its members' tables do not share gives its rows the first one's tokens.
  *  workspace_dev  kv_attend_shared_workspace_bytes() bytes, else as in
  *            kv_attend_layer: 122 MB for a head_dim of 128 on 152 SMs and
- *            4 * (head_dim + 2) bytes for every row and query head. */
+ *            4 * (head_dim + 2) bytes for every row and query head.
+ * Batches that are too small for sharing to pay (by the tables' width, rows
+ * and groups) are kv_attend_layer's calls. Should a wait run out (KV_DEV_ERR_TIMEOUT), all rows of
+ * groups that share are unspecified. */
 int kv_attend_shared_workspace_bytes(const kv_pool_t* pool, int32_t q_heads, int32_t n_seqs, int64_t n_rows,
                                      int64_t* bytes);
 int kv_attend_shared_layer(const kv_pool_t* pool, int32_t layer, const kv_batch* batch, const kv_prefix_groups* groups,

@@ -293,6 +293,45 @@ def test_shared_repeats_bit_for_bit(cache, dtype):
     assert d.error() == 0
 
 
+def test_shared_workspace_on_sixteen_bytes():
+    sh = Shared(11, GROUPS["many"], "bf16", D=128)
+    d, w = sh.dev(), sh.w
+    q = queries(w, 8, "bf16").cuda()
+    want = attend(d, sh.groups(), 1, q, 0.1)
+    size = gt.kv_attend_shared_workspace_bytes(d.pool, 8, w.S, w.n_rows)
+    for off in (16, 48, 240):
+        ws = torch.empty(size + 256, dtype=torch.uint8, device="cuda")[off:off + size]
+        assert ws.data_ptr() % 32 == off % 32
+        out = torch.empty_like(q)
+        gt.kv_attend_shared_layer(d.pool, 1, d.batch, sh.groups(), q, out, 0.1, ws)
+        rows = [r for r, _, _ in w.rows()]
+        assert torch.equal(out[rows], want[rows])
+    assert d.error() == 0
+
+
+@pytest.mark.parametrize("cache,dtype", [CACHES[0], CACHES[4]])
+def test_shared_by_thousands(cache, dtype):
+    """A group of thousands of sequences and groups of two, in tables so narrow that units are not cut: against
+    kv_attend_layer, twice that one's bound."""
+    g = [(128, [(1 + 7 * i % 90, 1) for i in range(3000)])] + [(16 + 16 * (i % 5), [(3, 1), (40, 2)]) for i in range(700)]
+    sh = Shared(17, g, cache, wide=False, H=2, D=128, L=2)
+    w = sh.w
+    assert (w.S - len(g)) * w.table.shape[1] * w.ps * w.H * w.D * 2 >= 2 ** 28
+    d = sh.dev()
+    q = queries(w, 4, dtype).cuda()
+    got, want = attend(d, sh.groups(), 1, q, 128 ** -0.5), d.attend(1, q, 128 ** -0.5)
+    assert d.error() == 0
+    top = {"bf16": 6.0, "fp16": 6.0, "e4m3": 448 * 2.0 ** -5, "e2m1": 6.0}[cache]  # of |v|: the bound's mean is below it
+    u = U[T[dtype]]
+    assert ((got.double() - want.double()).abs() <= 2 * (u * want.double().abs() + (u + 2.0 ** -12) * top)).all()
+    # and a few rows against the formula
+    for s in (0, 1501, 2999, 3000, 4399):
+        one = type(w)(**{**w.__dict__, "lens": [w.lens[s]], "news": [w.news[s]], "gap": [0], "table": w.table[s:s + 1]})
+        a, b = int(w.cu[s]), int(w.cu[s]) + w.news[s]
+        ref_out, _, size = ref.attend(one, 1, q[a:b].cpu(), 128 ** -0.5)
+        assert ((got[a:b].cpu().double() - ref_out).abs() <= u * ref_out.abs() + (u + 2.0 ** -12) * size + 2.0 ** -24).all()
+
+
 def test_shared_strided_queries():
     sh = Shared(11, GROUPS["many"], "bf16", D=128)
     d, w = sh.dev(), sh.w
