@@ -157,6 +157,8 @@ struct FewShape {
   // round costs anyway, and whose conversions are chains that then overlap (16 columns have no registers for it: drafts 389 / 400 us)
   static __host__ __device__ constexpr int blocks(int nt) { return kE2M1 && nt == 1 ? 2 : 1; }
   static constexpr int kKS = D / 16;          // k16 steps of the score product
+  // bytes of a warp's queries in shared memory: of 4-bit caches and 8 columns, whose registers they would not leave
+  static __host__ __device__ constexpr int queries(int nt) { return kE2M1 && nt == 1 ? D * 16 : 0; }
   static constexpr int kMT = D / 16;          // 16-element tiles of the output
 };
 
@@ -228,6 +230,8 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
   };
   const int stages = w.deep ? Sh::kDeep : Sh::kStages;
   const uint32_t ring0 = shared_u32(ring) + warp * stages * Sh::kStage;
+  constexpr bool kQShared = Sh::queries(NT) > 0;
+  const uint32_t qs = shared_u32(ring) + kFewWarps * stages * Sh::kStage + warp * Sh::queries(NT) + lane * 16;  // + 512 for two steps
   const uint8_t* pool = reinterpret_cast<const uint8_t*>(p.base);
   const int32_t row_bytes = static_cast<int32_t>(p.vpr * 16);
 
@@ -369,7 +373,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
     for (int i = 0; i < stages - KB; ++i) issue(step0 + i, i);
 
     // ---- the queries, while the first loads are in flight
-    uint32_t qf[NT][Sh::kKS][2];
+    uint32_t qf[NT][kQShared ? 2 : Sh::kKS][2];
     float cq[NT][2];
     int32_t pos[NT][2];
 #pragma unroll
@@ -433,8 +437,14 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
         row_c *= __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
 #pragma unroll
         for (int ks = 0; ks < Sh::kKS; ++ks) {
-          qf[nt][ks][0] = pack_h(x[4 * ks] * up, x[4 * ks + 1] * up);
-          qf[nt][ks][1] = pack_h(x[4 * ks + 2] * up, x[4 * ks + 3] * up);
+          const int at = kQShared ? ks & 1 : ks;
+          qf[nt][at][0] = pack_h(x[4 * ks] * up, x[4 * ks + 1] * up);
+          qf[nt][at][1] = pack_h(x[4 * ks + 2] * up, x[4 * ks + 3] * up);
+          if constexpr (kQShared)  // (a lane reads what it wrote)
+            if (ks & 1)
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qs + ks / 2 * 512), "r"(qf[nt][0][0]), "r"(qf[nt][0][1]),
+                           "r"(qf[nt][1][0]), "r"(qf[nt][1][1])
+                           : "memory");
         }
       }
 #pragma unroll
@@ -533,12 +543,15 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
               y[k] = mul_h2(y[k], sa[wd / 2]);
               z[k] = mul_h2(z[k], sb[wd / 2]);
             }
+            uint4 qq = make_uint4(0, 0, 0, 0);
+            if constexpr (kQShared) qq = lds128(qs + wd * 512);
 #pragma unroll
             for (int half = 0; half < 2; ++half)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 mma<C>(kTwo && half ? x2[nt] : xb[nt], y[2 * half], z[2 * half], y[2 * half + 1], z[2 * half + 1],
-                       qf[nt][2 * wd + half][0], qf[nt][2 * wd + half][1], 2 * wd + half < 1 + kTwo);
+                       kQShared ? (half ? qq.z : qq.x) : qf[nt][kQShared ? 0 : 2 * wd + half][0],
+                       kQShared ? (half ? qq.w : qq.y) : qf[nt][kQShared ? 0 : 2 * wd + half][1], 2 * wd + half < 1 + kTwo);
           }
         }
 #pragma unroll
@@ -954,7 +967,7 @@ cudaError_t launch(const DevPool& p, const Batch& b, const AttendArgs& a, Split 
   auto kernel = p.ps % 16 == 0
                     ? (one ? k_attend_few<C, D, NT, true, !kOne, SHARED> : k_attend_few<C, D, NT, true, true, SHARED>)
                     : (one ? k_attend_few<C, D, NT, false, !kOne, SHARED> : k_attend_few<C, D, NT, false, true, SHARED>);
-  const int smem = kFewWarps * (w.deep ? Sh::kDeep : Sh::kStages) * Sh::kStage;
+  const int smem = kFewWarps * ((w.deep ? Sh::kDeep : Sh::kStages) * Sh::kStage + Sh::queries(NT));
   if (after) return launch_overlapped(kernel, dim3(w.blocks), kFewBlock, smem, s, p, b, a, w);
   kernel<<<w.blocks, kFewBlock, smem, s>>>(p, b, a, w);
   return cudaGetLastError();
@@ -962,7 +975,8 @@ cudaError_t launch(const DevPool& p, const Batch& b, const AttendArgs& a, Split 
 
 template <class C, int D, int NT, bool SHARED>
 cudaError_t prepare_one(bool p16) {
-  constexpr int kBytes = kFewWarps * FewShape<C, D>::kDeep * FewShape<C, D>::kStage;
+  using Sh = FewShape<C, D>;
+  constexpr int kBytes = kFewWarps * (Sh::kDeep * Sh::kStage + Sh::queries(NT));
   auto set = [](auto kernel) { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes); };
   cudaError_t e = set(p16 ? k_attend_few<C, D, NT, true, true, SHARED> : k_attend_few<C, D, NT, false, true, SHARED>);
   if constexpr (std::is_same_v<C, CodeE4M3> || std::is_same_v<C, CodeE2M1>)
