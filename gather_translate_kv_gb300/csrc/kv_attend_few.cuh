@@ -600,22 +600,32 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
           iv[e] = rcp(sv);
         }
       }
+#pragma unroll
+      for (int hb = 0; hb < KB; ++hb)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[hb][nt][e] = kE4M3 ? fmaf(x[hb][nt][e], cq[nt][e & 1] * sk[e >> 1], lv[e >> 1] - low[nt][e & 1])
+                                 : fmaf(x[hb][nt][e], cq[nt][e & 1], -low[nt][e & 1]);
+      if (mask) {
+#pragma unroll
+        for (int hb = 0; hb < KB; ++hb)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = g + 8 * (e >> 1);
+              if (!(live[hb] >> key & 1) || !in_sight(a, pos[nt][e & 1], j0[hb] + key)) x[hb][nt][e] = -INFINITY;
+            }
+      }
       bool over = false;
 #pragma unroll
       for (int hb = 0; hb < KB; ++hb)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float t = kE4M3 ? fmaf(x[hb][nt][e], cq[nt][e & 1] * sk[e >> 1], lv[e >> 1] - low[nt][e & 1])
-                            : fmaf(x[hb][nt][e], cq[nt][e & 1], -low[nt][e & 1]);
-            if (mask) {
-              const int key = g + 8 * (e >> 1);
-              if (!(live[hb] >> key & 1) || !in_sight(a, pos[nt][e & 1], j0[hb] + key)) t = -INFINITY;
-            }
-            x[hb][nt][e] = t;
-            over = over || t > high[nt][e & 1];
-          }
+          for (int e = 0; e < 4; ++e) over = over || x[hb][nt][e] > high[nt][e & 1];
       if (__any_sync(kFull, over)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
