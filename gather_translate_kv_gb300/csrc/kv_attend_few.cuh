@@ -26,21 +26,22 @@
 // alone adds 40 % to it (fp16 output, 4096 keys, root mean square: 5.39e-6 and 7.54e-6). Under
 // 16-bit caches the second product is free, memory being the bound. Of 8-bit caches read
 // into bf16, whose 8 bits hide the 11 of one fp16 part (8.73e-5 and 8.79e-5), the weights are
-// one part: drafts take 364 us so and 405 with two. Queries for 8-bit caches are fp16 after a power-of-two scaling per row, exact for all
+// one part: drafts took 364 us so and 405 with two. Queries for 8-bit caches are fp16 after a power-of-two scaling per row, exact for all
 // bits that matter (2^-29 of the row's largest).
 //
 // Measured: 256 sequences of 4096 tokens (bf16, 8 KV heads of 128, 4.3 GB) 680 to 698
 // us from one GPU to another, 91 to 93 % of the copy rate; 40 sequences of 9 to 40 961 tokens with drafts
-// (8-bit, 1.68 GB) 364 us, 68 %, bound by latency inside a warp (codes into fp16, products,
+// (8-bit, 1.68 GB) 332 us, 74 %, bound by latency inside a warp (codes into fp16, products,
 // weights, one after the other) with three warps a scheduler; one sequence of 203 tokens 14 us, latency.
 //
 // 4-bit caches. A lane's piece of a key is a quarter of the head (two blocks of 16 and their scale bytes), its part of a
 // value an eighth (one block, or half of one). Two elements become fp16 by one conversion and one product with
 // the block's scale, exactly; codes of two values share a byte before that, so that no halves are exchanged. That is 64 conversions (at half
-// rate) and 64 products a lane and step, which is what bounds the kernel, with the chains between them: 256 x 4096 tokens
-// (1.2 GB) 336 us, 53 % of the copy rate, issue slots 60 % busy, `wait` the top stall; two blocks of keys a round 336 us, one 365;
-// four stages of the ring, not six, which leave room for L1 (365 / 392); 16 columns need all registers of two blocks an SM (drafts of 9 to
-// 40 961 tokens, fp16, 388 us; three blocks, which spill, 416).
+// rate) and 64 products a lane and step, beside some 300 other instructions; issue and latency bound the kernel: 256 x 4096 tokens
+// (1.2 GB) 320 us, 56 % of the copy rate. What it is sensitive to, in us: one block of keys a round instead of two 323 (365 / 336 in an
+// earlier form); shared memory that leaves little of L1, where the heads of a block find each other's scale sectors, rings of
+// five or six stages 392 to 398; three blocks an SM 423, five 399. 16 columns need all registers of two blocks an SM (drafts of 9 to
+// 40 961 tokens, fp16, 376 us; with three blocks, which spill, 416 against 389).
 //
 // Workers (as many warps as share a step's heads) take equal shares of all
 // steps of the batch (kv_attend_split.cuh); units cut at a border are joined by
@@ -154,7 +155,7 @@ struct FewShape {
   static constexpr int kStages = kRow >= 256 ? 2 : kRow >= 128 ? 3 : kE2M1 && D == 128 ? 4 : 6;
   static constexpr int kDeep = 6;
   // blocks of 16 keys a round of the loop: two of a 4-bit cache, whose loads and softmax are little beside what a
-  // round costs anyway, and whose conversions are chains that then overlap (16 columns have no registers for it: drafts 389 / 400 us)
+  // round costs anyway, and whose conversions are chains that then overlap (16 columns have no registers for it: drafts 389 us with one, 400 with two)
   static __host__ __device__ constexpr int blocks(int nt) { return kE2M1 && nt == 1 ? 2 : 1; }
   static constexpr int kKS = D / 16;          // k16 steps of the score product
   // bytes of a warp's queries in shared memory: of 4-bit caches and 8 columns, whose registers they would not leave
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
           for (int e = 0; e < 4; ++e)
             x[hb][nt][e] = kE4M3 ? fmaf(x[hb][nt][e], cq[nt][e & 1] * sk[e >> 1], lv[e >> 1] - low[nt][e & 1])
                                  : fmaf(x[hb][nt][e], cq[nt][e & 1], -low[nt][e & 1]);
-      if (mask) {
+      if (mask) {  // apart from the common step, where as predicates they were a third of its instructions (8-bit drafts 363 us, 332 so)
 #pragma unroll
         for (int hb = 0; hb < KB; ++hb)
 #pragma unroll
