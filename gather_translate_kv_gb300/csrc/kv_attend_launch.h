@@ -1,5 +1,5 @@
 // The attention kernels behind launch_attend: few rows a sequence
-// (kv_attend_few.cu), tiles of rows (kv_attend_tile.cu) and the join of units
+// (kv_attend_few.cuh), tiles of rows (kv_attend_tile.cuh) and the join of units
 // that they cut (kv_attend.cu), head sizes 64 and 128.
 #pragma once
 

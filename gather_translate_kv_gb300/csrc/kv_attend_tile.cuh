@@ -893,31 +893,30 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
               }
             }
           }
-          fence_async_shared();
-          return bad_rows;
-        }
-        constexpr int B = 4;
+        } else {
+          constexpr int B = 4;
 #pragma unroll 1
-        for (int it0 = 0; it0 < (kE2M1 ? 0 : IT); it0 += B) {
-          uint4 codes[B];
+          for (int it0 = 0; it0 < IT; it0 += B) {
+            uint4 codes[B];
 #pragma unroll
-          for (int ib = 0; ib < B; ++ib) codes[ib] = lds128(raw(t, it0 + ib));
+            for (int ib = 0; ib < B; ++ib) codes[ib] = lds128(raw(t, it0 + ib));
 #pragma unroll
-          for (int ib = 0; ib < B; ++ib) {
-            const int it = it0 + ib;
-            uint4 v = codes[ib];
-            if (check) {
-              const uint4 z = make_uint4(not_finite<C>(v.x), not_finite<C>(v.y), not_finite<C>(v.z), not_finite<C>(v.w));
-              if (z.x | z.y | z.z | z.w) {
-                bad_rows |= 1u << (it * RPI + lr);
-                v = make_uint4(v.x & ~z.x, v.y & ~z.y, v.z & ~z.z, v.w & ~z.w);
+            for (int ib = 0; ib < B; ++ib) {
+              const int it = it0 + ib;
+              uint4 v = codes[ib];
+              if (check) {
+                const uint4 z = make_uint4(not_finite<C>(v.x), not_finite<C>(v.y), not_finite<C>(v.z), not_finite<C>(v.w));
+                if (z.x | z.y | z.z | z.w) {
+                  bad_rows |= 1u << (it * RPI + lr);
+                  v = make_uint4(v.x & ~z.x, v.y & ~z.y, v.z & ~z.z, v.w & ~z.w);
+                }
               }
+              uint4 lo, hi;
+              decode16(v, lo, hi);
+              const int rr = lw * 32 + it * RPI + lr;
+              sts128(to + piece_at(rr, 2 * lc), lo);
+              sts128(to + piece_at(rr, 2 * lc + 1), hi);
             }
-            uint4 lo, hi;
-            decode16(v, lo, hi);
-            const int rr = lw * 32 + it * RPI + lr;
-            sts128(to + piece_at(rr, 2 * lc), lo);
-            sts128(to + piece_at(rr, 2 * lc + 1), hi);
           }
         }
         fence_async_shared();

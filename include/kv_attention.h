@@ -19,7 +19,7 @@
  * past the pool sets KV_DEV_ERR_ROW, one off the kernel-facing grid
  * KV_DEV_ERR_FORM; both then count as tombstones.
  *
- * 8-bit pools. In a pool of itemsize 1 these calls hold e4m3 codes with one
+ * 8-bit pools. In a pool of itemsize 1 (KV_FORMAT_ELEMENTS) these calls hold e4m3 codes with one
  * float scale for each page, layer, K or V, and head, in the caller's buffer
  * scales[num_pages][L][2][H] (kv_scale_bytes): value = code * scale. Calls
  * that move bytes (kv_move, kv_store_layer) do not know of scales: move

@@ -12,7 +12,7 @@
  * page envelopes; each envelope is 2L equal row-blocks of page_size rows,
  * [L0_K | L0_V | L1_K | L1_V | ...], so layer l's K is block 2l and its V is
  * block 2l+1. A row is R = head_num * head_dim * itemsize bytes (one token's
- * K, or V, for one layer). A token slot t (physical page t/ps, offset t%ps)
+ * K, or V, for one layer; of 4-bit pools see KV_FORMAT_E2M1). A token slot t (physical page t/ps, offset t%ps)
  * has the kernel-facing id
  *
  *      kernel_id(t) = (t / ps) * (ps * 2L) + t % ps
