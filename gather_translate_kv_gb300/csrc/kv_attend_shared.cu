@@ -123,7 +123,7 @@ Workspace workspace_of(int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int
   return w;
 }
 
-// Whether to share at all, by what the host knows: the tables' width as a bound on the lengths. The shared form is four
+// Whether to share at all, by what the host knows: the tables' width as a bound on the lengths. The shared form is three
 // launches in a row, and until the batch's cache outgrows L2 and what it delivers kv_attend_layer is as fast: elements that it would read
 // more than once, in millions, and us (kv_attend_layer / shared), 8 KV and 32 query heads of 128, one token a sequence: 64
 // sequences of one prefix, bf16, 134 43 / 44, 265 64 / 49, 528 108 / 60; 64 of 16 prefixes 207 66 / 78, 405 110 / 105, 808
