@@ -142,8 +142,8 @@ __device__ __forceinline__ void append_rows(const DevPool& p, const Batch& b, co
     for (int u = 0; u < U; ++u) {
       const int h = h_lo + (item % batches * U + u) * groups;
       if constexpr (FOUR) {
-        // Where some lane has a head to code, the warp's lanes stay together, those without one among them:
-        // neighbours exchange below.
+        // All lanes of the warp vote in every round, those that have no head among them (row and round are the
+        // warp's); where one has a head to code they stay together, since neighbours exchange below.
         const bool in = h < heads, code = in && h >= g.Q && page != 0;
         if (__any_sync(kFull, code)) {
           float x[16];
@@ -182,12 +182,17 @@ __device__ __forceinline__ void append_rows(const DevPool& p, const Batch& b, co
           continue;
         }
       }
-      if (h >= heads) break;
+      // no head, or a tombstone's key or value, which is not stored (they come after all queries)
+      if (h >= heads || (h >= g.Q && page == 0)) {
+        if constexpr (FOUR)
+          continue;  // the next head's vote and exchanges are the whole warp's
+        else
+          break;
+      }
       T* y;
       if (h < g.Q) {
         y = static_cast<T*>(g.q_out) + (r * g.Q + h) * g.D;
       } else {
-        if (page == 0) break;  // tombstone: not stored (keys and values come after all queries)
         const int kv = h >= g.Q + g.H;
         y = pool_row<T>(p, g.layer, kv, page, tokens[i].off) + (h - g.Q - kv * g.H) * g.D;
       }

@@ -108,6 +108,25 @@ def test_append(D, rd, H, Q, ps, dtype, interleaved):
         run_append(w, Q, dtype, rot, kernel_facing=i == 1, strided=0 if i else 16)
 
 
+# Head sizes that leave lanes without a head, and heads of which a warp holds queries and keys.
+LANES = [(96, 96, 32, 32), (96, 64, 3, 21), (160, 160, 2, 13), (192, 64, 2, 16), (224, 224, 1, 5), (128, 128, 2, 10),
+         (64, 32, 3, 11)]
+
+
+@pytest.mark.parametrize("D,rd,H,Q", LANES)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("cleared", ["none", "some", "all"])
+def test_append_rounds_without_a_head_to_code(D, rd, H, Q, dtype, cleared):
+    """Rounds in which lanes of a warp have queries, lanes have no head and no lane has one to code, before rounds
+    in which some do; new rows of live and of cleared pages: bytes and queries as the formula has them."""
+    for lens, news in (([9, 30, 1, 65], [1, 1, 1, 1]), ([70, 33, 0, 40], [41, 33, 0, 2])):
+        w = ref4.world(D + Q, lens, news, D=D, H=H, ps=8)
+        for s, j in ((s, j) for _, s, j in w.rows()):
+            if cleared == "all" or (cleared == "some" and (s + j // 8) % 2):
+                w.table[s, j // 8] = -1
+        run_append(w, Q, dtype, ref.rotation(1, rd, 80, w.n_rows))
+
+
 @pytest.mark.parametrize("axes", [2, 3, 4])
 @pytest.mark.parametrize("strided", [0, 3])
 def test_append_several_axes(axes, strided):
