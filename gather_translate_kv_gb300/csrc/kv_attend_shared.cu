@@ -25,7 +25,8 @@ constexpr int kOwnTiles = 128;
 // Looks at all metadata once. own: the sequences, checked; shared: at the index of a group's first sequence with
 // rows the group as one sequence, whose rows all stand at its prefix' last token, else no rows; from: where the
 // sequences' own tokens begin. A prefix is cut to whole steps of 16 keys and ends before any
-// member's new tokens; it is shared by two sequences at least.
+// member's new tokens; it is shared by two sequences at least. The runs of rows that stand for groups are disjoint,
+// whatever cu holds: each lies in its group's part of the rows, and those parts follow one another.
 __global__ void __launch_bounds__(kGroupBlock) k_share_groups(DevPool p, Batch b, const int32_t* __restrict__ group,
                                                               const int32_t* __restrict__ prefix_len, int32_t n_groups,
                                                               int32_t G, Seq* own, Seq* shared, int32_t* from,
@@ -36,11 +37,13 @@ __global__ void __launch_bounds__(kGroupBlock) k_share_groups(DevPool p, Batch b
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int bits = 0;
   for (int32_t i = blockIdx.x * kGroupBlock + tid; i < n_nodes; i += gridDim.x * kGroupBlock) nodes[i] = 0;
-  int bad = 0;
+  bool bad = false;
   for (int32_t i = tid; i <= n_groups; i += kGroupBlock) {
-    const int32_t s = __ldg(group + i);
-    bad |= i == 0 ? s != 0 : s < __ldg(group + i - 1);
-    bad |= i == n_groups && s != b.n_seqs;
+    const int32_t s = __ldg(group + i), before = i == 0 ? 0 : __ldg(group + i - 1);
+    if (before < 0 || s < before || s > b.n_seqs || (i == 0 && s != 0) || (i == n_groups && s != b.n_seqs))
+      bad = true;
+    else  // rows in the groups' order, else the sums of two groups could share a place
+      bad = bad || __ldg(b.cu + s) < __ldg(b.cu + before);
   }
   if (__syncthreads_or(bad)) {  // nothing is shared
     for (int64_t s = blockIdx.x * static_cast<int64_t>(kGroupBlock) + tid; s < b.n_seqs;
@@ -89,6 +92,8 @@ __global__ void __launch_bounds__(kGroupBlock) k_share_groups(DevPool p, Batch b
     __syncthreads();
     int32_t prefix = min(__ldg(prefix_len + g), a) & ~15;
     if (n < 2 || prefix < 16 || (r1 - r0) * G > INT32_MAX - 1024) prefix = 0;
+    // the group's rows as one run, which has to lie in the group's part of the rows (it does where cu does not decrease)
+    if (r0 < __ldg(b.cu + s0) || r1 > __ldg(b.cu + s1)) prefix = 0;
     for (int32_t s = s0 + tid; s < s1; s += kGroupBlock) {
       from[s] = prefix;
       shared[s] = prefix != 0 && s == s_first ? Seq{r0, prefix - 1, static_cast<int32_t>(r1 - r0)} : Seq{0, 0, 0};

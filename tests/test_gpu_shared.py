@@ -236,6 +236,38 @@ def test_shared_inconsistent_members():
         assert ((out - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -12) * size)[rows].all()
 
 
+@pytest.mark.parametrize("cache,dtype", [CACHES[0], CACHES[2], CACHES[4]])
+@pytest.mark.parametrize("entry,value", [(4, 10), (5, 50), (6, 20), (7, 30)])
+def test_shared_rows_that_step_back(cache, dtype, entry, value):
+    """One entry of the rows' offsets that decreases, so that the next sequence's rows lie between those of another
+    group: the sequence before it takes no part, every other one keeps its own answer."""
+    sh = Shared(18, [(96, [(9, 4), (20, 4), (5, 4)]), (48, [(7, 4), (4, 4), (30, 4)]), (64, [(4, 4), (33, 4), (5, 4)])],
+                cache)
+    w = sh.w
+    w.gap = [0, 92, 0] + [0] * 6
+    cu = w.cu
+    cu[entry] = value
+    d = sh.dev()
+    d.batch.tensors[2].copy_(torch.from_numpy(cu))
+    q = queries(w, 4, dtype)
+    u = U[T[dtype]]
+    for _ in range(3):
+        out = attend(d, sh.groups(), 1, q.cuda(), 0.125).cpu().double()
+        assert d.error() == gt.KV_DEV_ERR_TABLE
+        tokens = set()
+        for s in range(w.S):
+            a, b = int(cu[s]), int(cu[s]) + w.news[s]
+            if cu[s + 1] < b:
+                assert s == entry - 1
+                continue
+            tokens |= set(range(a, b))
+            one = type(w)(**{**w.__dict__, "lens": [w.lens[s]], "news": [w.news[s]], "gap": [0],
+                             "table": w.table[s:s + 1]})
+            want, _, size = ref.attend(one, 1, q[a:b], 0.125)
+            assert ((out[a:b] - want).abs() <= u * want.abs() + (u + 2.0 ** -12) * size).all(), s
+        assert (out[sorted(set(range(w.n_rows)) - tokens)] == 7.0).all()
+
+
 def test_shared_bad_entries():
     sh = Shared(9, [(80, [(4, 2)] * 4), (32, [(5, 1), (7, 2)])], "bf16")
     w = sh.w
