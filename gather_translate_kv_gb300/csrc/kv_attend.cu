@@ -56,22 +56,32 @@ int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
 template <class C>
 cudaError_t launch_join(const DevPool& p, const Batch& b, const AttendArgs& a, const Split& few, const Split& tile,
-                        int sm_count, cudaStream_t s) {
+                        const Groups& g, int sm_count, cudaStream_t s) {
   const int workers = few.n_workers > tile.n_workers ? few.n_workers : tile.n_workers;
   const int rows = workers * (few.n_workers ? few.hw * few.nq : tile.nq);
   const dim3 grid(rows / (kJoinBlock / 32) < 4 * sm_count ? (rows + kJoinBlock / 32 - 1) / (kJoinBlock / 32) : 4 * sm_count);
   return launch_overlapped(a.D == 64 ? k_attend_join<C, 64> : k_attend_join<C, 128>, grid, kJoinBlock, 0, s, p, b, a,
-                           few, tile);
+                           few, tile, g);
+}
+
+// Groups of a call that has nothing to join. It outlasts the kernel before it, over whose tail it runs.
+__global__ void __launch_bounds__(kJoinBlock) k_check_groups(DevPool p, Batch b, Groups g) {
+  store_bits(p, groups_bad(b, g, threadIdx.x, kJoinBlock) ? KV_DEV_ERR_TABLE : 0);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+cudaError_t launch_check(const DevPool& p, const Batch& b, const Groups& g, cudaStream_t s) {
+  return g.first ? launch_overlapped(k_check_groups, dim3(1), kJoinBlock, 0, s, p, b, g) : cudaSuccess;
 }
 
 }  // namespace
 
 cudaError_t launch_attend_join(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, const Split& few,
-                               const Split& tile, int sm_count, cudaStream_t s) {
-  if (kind == Kind::kE2M1) return launch_join<CodeE2M1>(p, b, a, few, tile, sm_count, s);
-  if (kind == Kind::kE4M3) return launch_join<CodeE4M3>(p, b, a, few, tile, sm_count, s);
-  return a.type == KV_TYPE_BF16 ? launch_join<__nv_bfloat16>(p, b, a, few, tile, sm_count, s)
-                                : launch_join<__half>(p, b, a, few, tile, sm_count, s);
+                               const Split& tile, const Groups& g, int sm_count, cudaStream_t s) {
+  if (kind == Kind::kE2M1) return launch_join<CodeE2M1>(p, b, a, few, tile, g, sm_count, s);
+  if (kind == Kind::kE4M3) return launch_join<CodeE4M3>(p, b, a, few, tile, g, sm_count, s);
+  return a.type == KV_TYPE_BF16 ? launch_join<__nv_bfloat16>(p, b, a, few, tile, g, sm_count, s)
+                                : launch_join<__half>(p, b, a, few, tile, g, sm_count, s);
 }
 
 int64_t attend_workspace_bytes(int32_t, int32_t, int32_t D, int32_t, int64_t, int sm_count) {
@@ -87,8 +97,8 @@ int64_t attend_workspace_bytes(int32_t, int32_t, int32_t D, int32_t, int64_t, in
 // D = 128, few-rows against tile kernel, us: 16-bit 110 / 148 at 8 rows, 141 / 150 at 16, 206 / 152 at 24; 8-bit 87 / 154
 // at 16, 139 / 160 at 32, 201 / 162 at 48 (fp16 output 95 / 190, 155 / 196, 222 / 197); 4-bit 79 / 157, 131 / 160,
 // 184 / 163 (fp16 output 85 / 186, 143 / 188, 202 / 191).
-cudaError_t launch_tiles(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, void* workspace, int sm_count,
-                         cudaStream_t s) {
+cudaError_t launch_tiles(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, const Groups& g,
+                         void* workspace, int sm_count, cudaStream_t s) {
   const int32_t few_rows = few_rows_of(kind);
   const bool only_few = b.n_rows * a.G <= few_rows * static_cast<int64_t>(b.n_seqs);
   const int32_t limit = only_few ? 0x7fffffff : few_rows / a.G;
@@ -101,14 +111,15 @@ cudaError_t launch_tiles(const DevPool& p, const Batch& b, const AttendArgs& a, 
                            limit > 0 ? Launch::kAfter : Launch::kPlain, nullptr, &tile, s);
   if (e != cudaSuccess) return e;
   if (few.whole) few.n_workers = 0;
-  if (few.n_workers == 0 && tile.n_workers == 0) return e;
-  return launch_attend_join(p, b, a, kind, few, tile, sm_count, s);
+  if (few.n_workers == 0 && tile.n_workers == 0) return launch_check(p, b, g, s);
+  return launch_attend_join(p, b, a, kind, few, tile, g, sm_count, s);
 }
 
-cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, void* workspace,
-                          int sm_count, cudaStream_t s) {
-  if (!has_tiles(a.D)) return launch_rows(p, b, a, kind, s);
-  return launch_tiles(p, b, a, kind, workspace, sm_count, s);
+cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, const Groups& g,
+                          void* workspace, int sm_count, cudaStream_t s) {
+  if (has_tiles(a.D)) return launch_tiles(p, b, a, kind, g, workspace, sm_count, s);
+  const cudaError_t e = launch_rows(p, b, a, kind, s);
+  return e == cudaSuccess ? launch_check(p, b, g, s) : e;
 }
 
 }  // namespace gtkv

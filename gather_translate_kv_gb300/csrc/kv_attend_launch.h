@@ -88,12 +88,12 @@ cudaError_t launch_tile(const DevPool& p, const Batch& b, const AttendArgs& a, c
 template <class C, bool SHARED>
 cudaError_t prepare_tile(int32_t D, bool p16);
 // Both, each for the sequences on its side of few_rows_of, and the join (kv_attend.cu).
-cudaError_t launch_tiles(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, void* workspace, int sm_count,
-                         cudaStream_t s);
+cudaError_t launch_tiles(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, const Groups& g,
+                         void* workspace, int sm_count, cudaStream_t s);
 // Rows a KV head up to which a sequence is the few-rows kernel's.
 inline int32_t few_rows_of(Kind kind) { return kind == Kind::kElements ? 16 : 32; }
 inline bool has_tiles(int32_t D) { return D == 64 || D == 128; }
 cudaError_t launch_attend_join(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, const Split& few,
-                               const Split& tile, int sm_count, cudaStream_t s);
+                               const Split& tile, const Groups& g, int sm_count, cudaStream_t s);
 
 }  // namespace gtkv

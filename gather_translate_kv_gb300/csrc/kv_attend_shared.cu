@@ -27,25 +27,16 @@ constexpr int kOwnTiles = 128;
 // sequences' own tokens begin. A prefix is cut to whole steps of 16 keys and ends before any
 // member's new tokens; it is shared by two sequences at least. The runs of rows that stand for groups are disjoint,
 // whatever cu holds: each lies in its group's part of the rows, and those parts follow one another.
-__global__ void __launch_bounds__(kGroupBlock) k_share_groups(DevPool p, Batch b, const int32_t* __restrict__ group,
-                                                              const int32_t* __restrict__ prefix_len, int32_t n_groups,
-                                                              int32_t G, Seq* own, Seq* shared, int32_t* from,
-                                                              int32_t* nodes, int32_t n_nodes) {
+__global__ void __launch_bounds__(kGroupBlock) k_share_groups(DevPool p, Batch b, Groups gr,
+                                                              const int32_t* __restrict__ prefix_len, int32_t G, Seq* own,
+                                                              Seq* shared, int32_t* from, int32_t* nodes, int32_t n_nodes) {
   __shared__ int64_t row0[kGroupBlock / 32], row1[kGroupBlock / 32];
   __shared__ int32_t start[kGroupBlock / 32], first[kGroupBlock / 32], count[kGroupBlock / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int bits = 0;
   for (int32_t i = blockIdx.x * kGroupBlock + tid; i < n_nodes; i += gridDim.x * kGroupBlock) nodes[i] = 0;
-  bool bad = false;
-  for (int32_t i = tid; i <= n_groups; i += kGroupBlock) {
-    const int32_t s = __ldg(group + i), before = i == 0 ? 0 : __ldg(group + i - 1);
-    if (before < 0 || s < before || s > b.n_seqs || (i == 0 && s != 0) || (i == n_groups && s != b.n_seqs))
-      bad = true;
-    else  // rows in the groups' order, else the sums of two groups could share a place
-      bad = bad || __ldg(b.cu + s) < __ldg(b.cu + before);
-  }
-  if (__syncthreads_or(bad)) {  // nothing is shared
+  if (__syncthreads_or(groups_bad(b, gr, tid, kGroupBlock))) {  // nothing is shared
     for (int64_t s = blockIdx.x * static_cast<int64_t>(kGroupBlock) + tid; s < b.n_seqs;
          s += static_cast<int64_t>(gridDim.x) * kGroupBlock) {
       own[s] = seq_of(p, b, static_cast<int32_t>(s), bits);
@@ -55,8 +46,13 @@ __global__ void __launch_bounds__(kGroupBlock) k_share_groups(DevPool p, Batch b
     store_bits(p, bits | KV_DEV_ERR_TABLE);
     return;
   }
-  for (int32_t g = blockIdx.x; g < n_groups; g += gridDim.x) {
-    const int32_t s0 = __ldg(group + g), s1 = __ldg(group + g + 1);
+  // Do some group's rows begin before those of the group before it? (A sequence is inconsistent then.)
+  bool back = false;
+  for (int32_t i = tid; i < gr.n; i += kGroupBlock)
+    back = back || __ldg(b.cu + __ldg(gr.first + i + 1)) < __ldg(b.cu + __ldg(gr.first + i));
+  for (int32_t g = blockIdx.x; g < gr.n; g += gridDim.x) {
+    const int32_t s0 = __ldg(gr.first + g), s1 = __ldg(gr.first + g + 1);
+    const int64_t c0 = __ldg(b.cu + s0), c1 = __ldg(b.cu + s1);
     int64_t r0 = INT64_MAX, r1 = 0;
     int32_t a = INT32_MAX, s_first = INT32_MAX, n = 0;
     for (int32_t s = s0 + tid; s < s1; s += kGroupBlock) {
@@ -79,7 +75,7 @@ __global__ void __launch_bounds__(kGroupBlock) k_share_groups(DevPool p, Batch b
     s_first = __reduce_min_sync(kFull, s_first);
     n = __reduce_add_sync(kFull, n);
     if (lane == 0) row0[warp] = r0, row1[warp] = r1, start[warp] = a, first[warp] = s_first, count[warp] = n;
-    __syncthreads();
+    const bool apart = !__syncthreads_or(back);
     r0 = INT64_MAX, r1 = 0, a = INT32_MAX, s_first = INT32_MAX, n = 0;
 #pragma unroll
     for (int w = 0; w < kGroupBlock / 32; ++w) {
@@ -92,8 +88,8 @@ __global__ void __launch_bounds__(kGroupBlock) k_share_groups(DevPool p, Batch b
     __syncthreads();
     int32_t prefix = min(__ldg(prefix_len + g), a) & ~15;
     if (n < 2 || prefix < 16 || (r1 - r0) * G > INT32_MAX - 1024) prefix = 0;
-    // the group's rows as one run, which has to lie in the group's part of the rows (it does where cu does not decrease)
-    if (r0 < __ldg(b.cu + s0) || r1 > __ldg(b.cu + s1)) prefix = 0;
+    // the run of the group's rows has to lie in its part of the rows (it does where cu does not decrease)
+    if (!apart || r0 < c0 || r1 > c1) prefix = 0;
     for (int32_t s = s0 + tid; s < s1; s += kGroupBlock) {
       from[s] = prefix;
       shared[s] = prefix != 0 && s == s_first ? Seq{r0, prefix - 1, static_cast<int32_t>(r1 - r0)} : Seq{0, 0, 0};
@@ -150,11 +146,10 @@ int64_t attend_shared_workspace_bytes(int32_t Q, int32_t D, int32_t n_seqs, int6
   return workspace_of(Q, D, n_seqs, n_rows, sm_count).bytes;
 }
 
-cudaError_t launch_attend_shared(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, const int32_t* group,
-                                 const int32_t* prefix_len, int32_t n_groups, void* workspace, int sm_count,
-                                 cudaStream_t s) {
-  if (!has_tiles(a.D) || !worth_sharing(p, b, a, n_groups))
-    return launch_attend(p, b, a, kind, workspace, sm_count, s);
+cudaError_t launch_attend_shared(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, const Groups& gr,
+                                 const int32_t* prefix_len, void* workspace, int sm_count, cudaStream_t s) {
+  const int32_t n_groups = gr.n;
+  if (!has_tiles(a.D) || !worth_sharing(p, b, a, gr.n)) return launch_attend(p, b, a, kind, gr, workspace, sm_count, s);
   const Workspace w = workspace_of(a.Q, a.D, b.n_seqs, b.n_rows, sm_count);
   uint8_t* ws = reinterpret_cast<uint8_t*>(aligned(static_cast<int64_t>(reinterpret_cast<uintptr_t>(workspace))));
   Seq* own = reinterpret_cast<Seq*>(ws + w.own);
@@ -163,7 +158,7 @@ cudaError_t launch_attend_shared(const DevPool& p, const Batch& b, const AttendA
   int32_t* nodes = reinterpret_cast<int32_t*>(ws + w.nodes);
   const int32_t n_nodes = static_cast<int32_t>(2 * few_nodes(sm_count) + tile_nodes(sm_count));
   k_share_groups<<<n_groups < kZeroBlocks ? kZeroBlocks : n_groups < 2 * sm_count ? n_groups : 2 * sm_count, kGroupBlock, 0, s>>>(
-      p, b, group, prefix_len, n_groups, a.G, own, shared, from, nodes, n_nodes);
+      p, b, gr, prefix_len, a.G, own, shared, from, nodes, n_nodes);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   Split split{};

@@ -357,12 +357,16 @@ __device__ __forceinline__ void join_split(const DevPool& p, const Batch& b, con
   }
 }
 
+// Looks at groups on the way, where there are any.
 template <class C, int D>
-__global__ void __launch_bounds__(kJoinBlock) k_attend_join(DevPool p, Batch b, AttendArgs a, Split few, Split tile) {
+__global__ void __launch_bounds__(kJoinBlock) k_attend_join(DevPool p, Batch b, AttendArgs a, Split few, Split tile,
+                                                               Groups g) {
   __shared__ int32_t owners[kMaxWorkers];
   __shared__ float tmp[kJoinBlock / 32 * (D + 2)];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   int bits = 0;
+  // while the kernels before it run
+  if (g.first && blockIdx.x == 0 && groups_bad(b, g, threadIdx.x, kJoinBlock)) bits |= KV_DEV_ERR_TABLE;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (few.n_workers) join_split<C, D>(p, b, a, few, owners, tmp, bits);
   __syncthreads();
   if (tile.n_workers) join_split<C, D>(p, b, a, tile, owners, tmp, bits);

@@ -166,7 +166,7 @@ int kv_attend_layer(const kv_pool_t* pool, int32_t layer, const kv_batch* batch,
   const int rc = enter_attend(pool, layer, batch, type, q_dev, q_stride, q_heads, out_dev, lse_dev, scale, window, sinks,
                               scales_dev, workspace_dev, workspace_bytes, kv_attend_workspace_bytes, &b, &a);
   if (rc != KV_OK || b.n_rows == 0) return rc;
-  return launched(gtkv::launch_attend(pool->dev, b, a, kind_of(pool), workspace_dev, pool->sm_count, as_stream(stream)));
+  return launched(gtkv::launch_attend(pool->dev, b, a, kind_of(pool), {}, workspace_dev, pool->sm_count, as_stream(stream)));
 }
 
 int kv_attend_shared_workspace_bytes(const kv_pool_t* pool, int32_t q_heads, int32_t n_seqs, int64_t n_rows,
@@ -191,8 +191,8 @@ int kv_attend_shared_layer(const kv_pool_t* pool, int32_t layer, const kv_batch*
   if (rc != KV_OK || b.n_rows == 0) return rc;
   if (groups->n_groups < 1 || groups->group_dev == nullptr || groups->prefix_len_dev == nullptr) return KV_ERR_INVALID;
   if (!aligned(groups->group_dev, 4) || !aligned(groups->prefix_len_dev, 4)) return KV_ERR_ALIGN;
-  return launched(gtkv::launch_attend_shared(pool->dev, b, a, kind_of(pool), groups->group_dev, groups->prefix_len_dev,
-                                             groups->n_groups, workspace_dev, pool->sm_count, as_stream(stream)));
+  return launched(gtkv::launch_attend_shared(pool->dev, b, a, kind_of(pool), gtkv::Groups{groups->group_dev, groups->n_groups},
+                                             groups->prefix_len_dev, workspace_dev, pool->sm_count, as_stream(stream)));
 }
 
 int kv_gather_layer_scaled(const kv_pool_t* pool, int32_t layer, const kv_batch* batch, const float* scales_dev,

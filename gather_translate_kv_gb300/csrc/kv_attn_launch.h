@@ -50,11 +50,11 @@ cudaError_t prepare_attend(const kv_pool_desc& d);
 int64_t attend_workspace_bytes(int32_t H, int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int sm_count);
 // Attention of groups of sequences that share their first tokens.
 int64_t attend_shared_workspace_bytes(int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int sm_count);
-cudaError_t launch_attend_shared(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, const int32_t* group,
-                                 const int32_t* prefix_len, int32_t n_groups, void* workspace, int sm_count,
-                                 cudaStream_t s);
-cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, void* workspace,
-                          int sm_count, cudaStream_t s);
+cudaError_t launch_attend_shared(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, const Groups& g,
+                                 const int32_t* prefix_len, void* workspace, int sm_count, cudaStream_t s);
+// Attention that shares nothing; groups, if there are any, are looked at.
+cudaError_t launch_attend(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, const Groups& g,
+                          void* workspace, int sm_count, cudaStream_t s);
 
 // A launch that starts while the kernel before it drains (programmatic dependent launch).
 template <class... A, class... B>

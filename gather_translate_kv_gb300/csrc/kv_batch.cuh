@@ -67,6 +67,22 @@ __device__ __forceinline__ void check_seqs(const DevPool& p, const Batch& b, int
   for (int64_t s = first; s < b.n_seqs; s += step) seq_of(p, b, static_cast<int32_t>(s), bits);
 }
 
+// Groups of sequences [first[g], first[g + 1]) that share tokens; of none where first is null.
+struct Groups {
+  const int32_t* first = nullptr;
+  int32_t n = 0;
+};
+
+// Whether they are no groups: first[0 .. n] does not rise from 0 to n_seqs. A thread looks at entries `from` of `step`.
+__device__ __forceinline__ bool groups_bad(const Batch& b, const Groups& g, int64_t from, int64_t step) {
+  bool bad = false;
+  for (int64_t i = from; i <= g.n; i += step) {
+    const int32_t s = __ldg(g.first + i);
+    bad = bad || s < (i == 0 ? 0 : __ldg(g.first + i - 1)) || (i == 0 && s != 0) || (i == g.n && s != b.n_seqs);
+  }
+  return bad;
+}
+
 // Table entry -> physical page, 0 (the sink) for tombstones and bad entries.
 __device__ __forceinline__ int64_t page_of_entry(const DevPool& p, const Batch& b, int32_t e, int& bits) {
   if (e <= 0) return 0;

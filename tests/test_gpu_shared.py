@@ -173,6 +173,21 @@ def test_shared_groups_that_are_no_groups(group):
 
 
 @pytest.mark.parametrize("cache,dtype", [CACHES[0], CACHES[2], CACHES[4]])
+@pytest.mark.parametrize("group", [[0, 4, 5], [1, 4, 6], [0, 7, 6], [0, -1, 6], [0, 4, 2 ** 31 - 1], [0, 1, 2, 3, 4, 5, 5]])
+@pytest.mark.parametrize("D,H,Q", [(64, 2, 4), (128, 1, 17), (128, 1, 33), (80, 2, 4)])
+@pytest.mark.parametrize("most", [32, 130])
+def test_shared_groups_that_are_no_groups_where_nothing_is_shared(cache, dtype, group, D, H, Q, most):
+    """Batches that are too small for sharing to pay, and head sizes that never share: the error bit all the same, whichever
+    kernels take the rows (few rows of 2 heads, in one piece or cut; too many rows of one head's 17 or 33 query heads; row
+    by row)."""
+    news = 1 if D == 64 else 9
+    sh = Shared(7, [(most, [(9, news), (10, news), (11, news), (30, news)]), (16, [(9, news), (14, news)])], cache, D=D, H=H,
+                wide=False)
+    check(sh, Q, dtype, group=group, prefix=[16] * (len(group) - 1), error=gt.KV_DEV_ERR_TABLE)
+    check(sh, Q, dtype, group=[0, 0, 1, 6], prefix=[16, 16, 0])
+
+
+@pytest.mark.parametrize("cache,dtype", [CACHES[0], CACHES[2], CACHES[4]])
 @pytest.mark.parametrize("members", [3, 40])
 def test_shared_value_that_is_not_finite(cache, dtype, members):
     """One element (or block) of one value of a prefix: NaN for every row of its group, there and nowhere else."""
