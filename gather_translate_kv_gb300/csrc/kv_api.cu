@@ -113,7 +113,7 @@ int kv_pool_create(const kv_pool_desc* desc, void* raw_dev, int64_t raw_bytes, k
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     return failed_call();
   if (gtkv::prepare_gather() != cudaSuccess || gtkv::prepare_append(*desc) != cudaSuccess ||
-      gtkv::prepare_attend(*desc) != cudaSuccess)
+      gtkv::prepare_attend(*desc, false) != cudaSuccess)
     return failed_call();
   if (raw_dev != nullptr) {
     // a borrowed buffer must be device (or managed) memory of this device:

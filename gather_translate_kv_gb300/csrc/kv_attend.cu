@@ -42,12 +42,12 @@ cudaError_t launch_rows(const DevPool& p, const Batch& b, const AttendArgs& a, K
 
 }  // namespace
 
-cudaError_t prepare_attend(const kv_pool_desc& d) {
+cudaError_t prepare_attend(const kv_pool_desc& d, bool shared) {
   if (d.latent_only || d.itemsize > 2 || !has_tiles(d.head_dim)) return cudaSuccess;
   const Kind kind = kind_of(d);
   const bool p16 = d.page_size % 16 == 0;
-  const cudaError_t e = prepare_attend_few(d.head_dim, kind, p16);
-  return e == cudaSuccess ? prepare_attend_tile(d.head_dim, kind, p16) : e;
+  const cudaError_t e = prepare_attend_few(d.head_dim, kind, p16, shared);
+  return e == cudaSuccess ? prepare_attend_tile(d.head_dim, kind, p16, shared) : e;
 }
 
 namespace {

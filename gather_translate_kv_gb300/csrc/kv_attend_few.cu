@@ -12,15 +12,12 @@ int heads_of_worker(int32_t H) { return H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1; }
 
 }  // namespace
 
-cudaError_t prepare_attend_few(int32_t D, Kind kind, bool p16) {
-  auto both = [&]<class C>() {
-    const cudaError_t e = prepare_few<C, false>(D, p16);
-    return e == cudaSuccess ? prepare_few<C, true>(D, p16) : e;
-  };
-  if (kind == Kind::kE2M1) return both.template operator()<CodeE2M1>();
-  if (kind == Kind::kE4M3) return both.template operator()<CodeE4M3>();
-  const cudaError_t e = both.template operator()<__half>();
-  return e == cudaSuccess ? both.template operator()<__nv_bfloat16>() : e;
+cudaError_t prepare_attend_few(int32_t D, Kind kind, bool p16, bool shared) {
+  auto set = [&]<class C>() { return shared ? prepare_few<C, true>(D, p16) : prepare_few<C, false>(D, p16); };
+  if (kind == Kind::kE2M1) return set.template operator()<CodeE2M1>();
+  if (kind == Kind::kE4M3) return set.template operator()<CodeE4M3>();
+  const cudaError_t e = set.template operator()<__half>();
+  return e == cudaSuccess ? set.template operator()<__nv_bfloat16>() : e;
 }
 
 int64_t attend_few_workspace(int32_t D, int sm_count) {

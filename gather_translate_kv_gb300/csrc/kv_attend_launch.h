@@ -61,9 +61,9 @@ inline int64_t split_record_bytes(int64_t workers) {
 }
 
 // Shared-memory limits, on the current device, of the kernels for one kind of pool (p16: its page size is a multiple
-// of 16).
-cudaError_t prepare_attend_few(int32_t D, Kind kind, bool p16);
-cudaError_t prepare_attend_tile(int32_t D, Kind kind, bool p16);
+// of 16), the plain ones or those for shared prefixes.
+cudaError_t prepare_attend_few(int32_t D, Kind kind, bool p16, bool shared);
+cudaError_t prepare_attend_tile(int32_t D, Kind kind, bool p16, bool shared);
 // Joining nodes of a kernel, for shared prefixes.
 inline int64_t few_nodes(int sm_count) { return static_cast<int64_t>(sm_count) * kFewBlocksPerSM * kFewWarps; }
 inline int64_t tile_nodes(int sm_count) { return static_cast<int64_t>(sm_count) * 8; }

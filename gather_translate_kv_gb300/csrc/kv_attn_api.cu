@@ -109,6 +109,21 @@ int enter_attend(const kv_pool_t* pool, int32_t layer, const kv_batch* batch, in
   return KV_OK;
 }
 
+// Sets up the kernels for shared prefixes, with the pool's device current, once a pool: kv_pool_create leaves them out,
+// since loading them takes a process 1 to 1.5 ms for each kind of pool. It may be called while a stream is captured.
+int ready_shared(const kv_pool_t* pool) {
+  if (pool->shared_ready.load(std::memory_order_acquire)) return KV_OK;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e == cudaSuccess) {
+    e = gtkv::prepare_attend(pool->desc, true);
+    const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e == cudaSuccess) e = back;
+  }
+  if (e == cudaSuccess) pool->shared_ready.store(true, std::memory_order_release);
+  return launched(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -174,6 +189,9 @@ int kv_attend_shared_workspace_bytes(const kv_pool_t* pool, int32_t q_heads, int
   const int rc = kv_attend_workspace_bytes(pool, q_heads, n_seqs, n_rows, bytes);
   if (rc != KV_OK) return rc;
   if (n_rows > (int64_t(1) << 36)) return KV_ERR_INVALID;  // 4 * n_rows * q_heads * (head_dim + 2) stays below 2^63
+  int dev = -1;  // a program asks before its first call, which then finds its kernels; on another device that call sets them up
+  if (!pool->shared_ready.load(std::memory_order_acquire) && cudaGetDevice(&dev) == cudaSuccess && dev == pool->device)
+    ready_shared(pool);
   *bytes = gtkv::attend_shared_workspace_bytes(q_heads, pool->desc.head_dim, n_seqs, n_rows, pool->sm_count);
   return KV_OK;
 }
@@ -186,11 +204,12 @@ int kv_attend_shared_layer(const kv_pool_t* pool, int32_t layer, const kv_batch*
   gtkv::Batch b;
   gtkv::AttendArgs a;
   if (groups == nullptr || groups->n_groups < 0 || groups->reserved != 0) return KV_ERR_INVALID;
-  const int rc = enter_attend(pool, layer, batch, type, q_dev, q_stride, q_heads, out_dev, lse_dev, scale, 0, 0, scales_dev,
-                              workspace_dev, workspace_bytes, kv_attend_shared_workspace_bytes, &b, &a);
+  int rc = enter_attend(pool, layer, batch, type, q_dev, q_stride, q_heads, out_dev, lse_dev, scale, 0, 0, scales_dev,
+                        workspace_dev, workspace_bytes, kv_attend_shared_workspace_bytes, &b, &a);
   if (rc != KV_OK || b.n_rows == 0) return rc;
   if (groups->n_groups < 1 || groups->group_dev == nullptr || groups->prefix_len_dev == nullptr) return KV_ERR_INVALID;
   if (!aligned(groups->group_dev, 4) || !aligned(groups->prefix_len_dev, 4)) return KV_ERR_ALIGN;
+  if ((rc = ready_shared(pool)) != KV_OK) return rc;
   return launched(gtkv::launch_attend_shared(pool->dev, b, a, kind_of(pool), gtkv::Groups{groups->group_dev, groups->n_groups},
                                              groups->prefix_len_dev, workspace_dev, pool->sm_count, as_stream(stream)));
 }

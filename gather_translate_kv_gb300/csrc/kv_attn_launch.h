@@ -44,9 +44,10 @@ struct AttendArgs {
 
 // Set-up of the kernels on the current device (their shared-memory limits), of those
 // that calls on a pool of this geometry can take (a pool more takes 84 us so, and 106 when
-// all kernels are set up each time). Called by kv_pool_create.
+// all kernels are set up each time). Called by kv_pool_create, but for the attention of shared prefixes, which a pool
+// sets up at its first use.
 cudaError_t prepare_append(const kv_pool_desc& d);
-cudaError_t prepare_attend(const kv_pool_desc& d);
+cudaError_t prepare_attend(const kv_pool_desc& d, bool shared);
 int64_t attend_workspace_bytes(int32_t H, int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int sm_count);
 // Attention of groups of sequences that share their first tokens.
 int64_t attend_shared_workspace_bytes(int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int sm_count);

@@ -4,6 +4,8 @@
 
 #include <stdint.h>
 
+#include <atomic>
+
 #include "kv_common.cuh"
 #include "kv_layout.h"
 #include "kv_pool.h"
@@ -18,4 +20,5 @@ struct kv_pool {
   int device;
   int sm_count;
   gtkv::DevPool dev;
+  mutable std::atomic<bool> shared_ready{false};  // the kernels for shared prefixes are set up
 };

@@ -184,7 +184,7 @@ typedef struct {
  * and groups) are kv_attend_layer's calls. Should a wait run out (KV_DEV_ERR_TIMEOUT), all rows of
  * groups that share are unspecified. */
 int kv_attend_shared_workspace_bytes(const kv_pool_t* pool, int32_t q_heads, int32_t n_seqs, int64_t n_rows,
-                                     int64_t* bytes);
+                                     int64_t* bytes); /* with the pool's device current it also loads the kernels */
 int kv_attend_shared_layer(const kv_pool_t* pool, int32_t layer, const kv_batch* batch, const kv_prefix_groups* groups,
                            int32_t type, const void* q_dev, int64_t q_stride, int32_t q_heads, void* out_dev,
                            float* lse_dev, float scale, const float* scales_dev, void* workspace_dev,

@@ -5,6 +5,10 @@ two sums in 32 bits adds 2^-22 of the mean of |v|, which the 2^-12 of the scores
 """
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -377,6 +381,54 @@ def test_shared_by_thousands(cache, dtype):
         a, b = int(w.cu[s]), int(w.cu[s]) + w.news[s]
         ref_out, _, size = ref.attend(one, 1, q[a:b].cpu(), 128 ** -0.5)
         assert ((got[a:b].cpu().double() - ref_out).abs() <= u * ref_out.abs() + (u + 2.0 ** -12) * size + 2.0 ** -24).all()
+
+
+FIRST = """
+import sys
+sys.path[:0] = {path!r}
+import threading
+import torch
+import gather_translate_kv_gb300 as gt
+from test_gpu_shared import GROUPS, Shared, attend, check, queries
+sh = Shared(19, GROUPS["many"], {cache!r}, D=128)
+w, q = sh.w, queries(sh.w, 8, "bf16").cuda()
+first = sh.dev()
+size = gt.kv_attend_workspace_bytes(first.pool, 8, w.S, w.n_rows) + (64 << 20) + w.n_rows * 8 * 130 * 4
+ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(3)]
+outs = [torch.full_like(q, 7.0) for _ in range(3)]
+groups, devs = sh.groups(), [sh.dev() for _ in range(3)]
+call = lambda i, st=None: gt.kv_attend_shared_layer(devs[i].pool, 1, devs[i].batch, groups, q, outs[i], 128 ** -0.5, ws[i],
+                                                    scales=devs[i].scales, stream=st)
+torch.cuda.synchronize()
+if {how!r} == "captured":
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(0)
+        call(1)
+        call(2)
+    assert all((o == 7.0).all() for o in outs)
+    graph.replay()
+else:
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    at = [threading.Thread(target=call, args=(i, streams[i])) for i in range(3)]
+    [x.start() for x in at]
+    [x.join() for x in at]
+torch.cuda.synchronize()
+want = check(sh, 8, "bf16")
+assert all(torch.equal(o, want) for o in outs) and all(d.error() == 0 for d in devs)
+print("done")
+"""
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3", "e2m1"])
+@pytest.mark.parametrize("how", ["captured", "threads"])
+def test_shared_first_calls_of_a_process(cache, how):
+    """A pool sets up its kernels at its first shared call, or when it is asked for the workspace: without having been
+    asked, the first calls of a process while a stream is captured, and from three threads at once."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(path=[os.path.dirname(here), here], cache=cache, how=how)],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("done"), r.stdout[-2000:] + r.stderr[-2000:]
 
 
 def test_shared_strided_queries():
