@@ -708,7 +708,7 @@ def kv_attend_shared_layer(pool: KVPool, layer: int, batch: KVBatch, groups: KVP
                            out: torch.Tensor, scale: float, workspace: torch.Tensor,
                            scales: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None) -> None:
     """kv_attend_layer of a batch whose groups of sequences share their first
-    tokens, which are attended to once for all rows of a group.
+    tokens, which are attended to by the rows of a group together; for decode steps and drafts.
     workspace: uint8, kv_attend_shared_workspace_bytes() long, one per call in flight."""
     dev = _here()
     rc = (_lib or lib()).kv_attend_shared_layer(

@@ -94,9 +94,9 @@ int64_t attend_workspace_bytes(int32_t, int32_t, int32_t D, int32_t, int64_t, in
 // drafts; a longer sequence among them takes several row tiles there), else both, each taking the
 // sequences on its side of that. Lengths are known on the device alone, so the
 // rule goes by averages. 32 sequences of 4000 tokens, 4 query heads a KV head,
-// D = 128, few-rows against tile kernel, us: 16-bit 110 / 148 at 8 rows, 141 / 150 at 16, 206 / 152 at 24; 8-bit 87 / 154
-// at 16, 139 / 160 at 32, 201 / 162 at 48 (fp16 output 95 / 190, 155 / 196, 222 / 197); 4-bit 79 / 157, 131 / 160,
-// 184 / 163 (fp16 output 85 / 186, 143 / 188, 202 / 191).
+// D = 128, few-rows against tile kernel, us: 16-bit 110 / 147 at 8 rows, 137 / 150 at 16, 195 / 151 at 20; 8-bit 83 / 154
+// at 16, 126 / 159 at 32, 182 / 160 at 40 (fp16 output 91 / 189, 143 / 195, 205 / 195); 4-bit 75 / 158, 121 / 162,
+// 169 / 162 (fp16 output 82 / 187, 138 / 189, 195 / 189).
 cudaError_t launch_tiles(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, const Groups& g,
                          void* workspace, int sm_count, cudaStream_t s) {
   const int32_t few_rows = few_rows_of(kind);

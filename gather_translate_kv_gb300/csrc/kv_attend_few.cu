@@ -48,7 +48,7 @@ cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs
   const int64_t all = (w.whole ? 1 : most + kFewUnitCost) * tiles * (a.H / w.hw);
   cap = cap < kMaxWorkers ? cap : kMaxWorkers;
   // a prefix of few rows is cut into many segments, which then meet level by level: 4 sequences in 2 groups behind 8192
-  // tokens 54 us with 4 steps a segment, 50 with 8 (8-bit 56 / 49, 4-bit 55 / 47), with more groups the same
+  // tokens (in wide tables) 43 us with 4 steps a segment and with 8, 8-bit 51 / 45, 4-bit 49 / 45; with more groups the same
   w.min_share = w.whole ? 1 : a.state ? 2 * kMinShare : kMinShare;
   int64_t workers = (all + w.min_share - 1) / w.min_share;
   workers = workers > cap ? cap : workers;

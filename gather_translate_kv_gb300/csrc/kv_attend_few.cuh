@@ -1,8 +1,9 @@
 // Attention of few rows a sequence (decode steps, drafted tokens): at most 16
 // rows (8-bit and 4-bit caches: 32) on average, a row being a (token, query head) pair of one KV head, in
-// tiles of 8 or 16; a sequence with more takes several tiles. Every key and
-// value is read once and meets a handful of rows, so the bound is memory; the
-// work is laid out so that nothing stands between the loads.
+// tiles of 8 or 16; a sequence with more takes several tiles, each of which reads its keys and values again. A tile reads
+// them once for a handful of rows, so the bound is memory; the work is laid out so that nothing stands between
+// the loads. Behind shared prefixes the kernel takes the own tokens of all sequences, however many rows they have, and
+// prefixes of groups of few rows (kv_attend_shared.cu has the limits).
 //
 // One warp owns one KV head over its own run of keys, 16 keys a step, and never
 // talks to another warp. Both products run as mma m16n8k16 with the CACHE as
@@ -26,7 +27,8 @@
 // alone adds 40 % to it (fp16 output, 4096 keys, root mean square: 5.39e-6 and 7.54e-6). Under
 // 16-bit caches the second product is free, memory being the bound. Of 8-bit caches read
 // into bf16, whose 8 bits hide the 11 of one fp16 part (8.73e-5 and 8.79e-5), the weights are
-// one part: drafts took 364 us so and 405 with two. Queries for 8-bit caches are fp16 after a power-of-two scaling per row, exact for all
+// one part, and so they are of 4-bit caches (the result's whole error grows by 0.8 %): drafts in 8 bits take 334 us so
+// and 377 with two, 256 x 4096 tokens in 4 bits 320 and 337. Queries for 8-bit caches are fp16 after a power-of-two scaling per row, exact for all
 // bits that matter (2^-29 of the row's largest).
 //
 // Measured: 256 sequences of 4096 tokens (bf16, 8 KV heads of 128, 4.3 GB) 680 to 698
@@ -38,10 +40,10 @@
 // value an eighth (one block, or half of one). Two elements become fp16 by one conversion and one product with
 // the block's scale, exactly; codes of two values share a byte before that, so that no halves are exchanged. That is 64 conversions (at half
 // rate) and 64 products a lane and step, beside some 300 other instructions; issue and latency bound the kernel: 256 x 4096 tokens
-// (1.2 GB) 320 us, 56 % of the copy rate. What it is sensitive to, in us: one block of keys a round instead of two 323 (365 / 336 in an
-// earlier form); shared memory that leaves little of L1, where the heads of a block find each other's scale sectors, rings of
-// five or six stages 392 to 398; three blocks an SM 423, five 399. 16 columns need all registers of two blocks an SM (drafts of 9 to
-// 40 961 tokens, fp16, 376 us; with three blocks, which spill, 416 against 389).
+// (1.2 GB) 320 us, 56 % of the copy rate. What it is sensitive to, in us: one block of keys a round instead of two 324;
+// shared memory that leaves little of L1, where the heads of a block find each other's scale sectors, rings of
+// six stages 393; three blocks an SM 319, five, which spill, 494. 16 columns need all registers of two blocks an SM (drafts of 9 to
+// 40 961 tokens, fp16, 377 us; with three blocks, which spill, 398).
 //
 // Workers (as many warps as share a step's heads) take equal shares of all
 // steps of the batch (kv_attend_split.cuh); units cut at a border are joined by
@@ -155,7 +157,7 @@ struct FewShape {
   static constexpr int kStages = kRow >= 256 ? 2 : kRow >= 128 ? 3 : kE2M1 && D == 128 ? 4 : 6;
   static constexpr int kDeep = 6;
   // blocks of 16 keys a round of the loop: two of a 4-bit cache, whose loads and softmax are little beside what a
-  // round costs anyway, and whose conversions are chains that then overlap (16 columns have no registers for it: drafts 389 us with one, 400 with two)
+  // round costs anyway, and whose conversions are chains that then overlap (256 x 4096 tokens 320 us, with one 324)
   static __host__ __device__ constexpr int blocks(int nt) { return kE2M1 && nt == 1 ? 2 : 1; }
   static constexpr int kKS = D / 16;          // k16 steps of the score product
   // bytes of a warp's queries in shared memory: of 4-bit caches and 8 columns, whose registers they would not leave

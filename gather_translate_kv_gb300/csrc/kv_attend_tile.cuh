@@ -25,8 +25,9 @@
 // the cache's 16-bit type (bf16, or fp16 lifted by 2^6 for fp16 and 8-bit caches), rounded
 // and what the rounding left, so that the result's error is the output's own rounding: 1.479e-4
 // (root mean square, prompts of 2048 tokens in bf16), as the formula in 32 bits has it, where one part
-// gave 1.903e-4 for 698 us instead of 831 (in an earlier form of the kernel). Of 8-bit and 4-bit caches read into bf16, whose 8 bits
-// hide fp16's 11, one part is enough (7.45e-5 and 7.39e-5; the same prompts in 8 bits 952 us, in fp16 with two parts 1108). Denominators
+// gave 1.903e-4 for 582 us instead of 757. Of 8-bit and 4-bit caches read into bf16, whose 8 bits
+// hide fp16's 11, one part is enough (7.45e-5 and 7.39e-5; chunks of ~1000 tokens in 8 bits 452 us, with two parts 561, in
+// 4 bits 440 and 524). Denominators
 // add the 32-bit weights. The scale of
 // an 8-bit value is part of its weight, t = score * log2(e) + log2(scale), and
 // the denominator adds weight / scale. Queries for 8-bit caches become fp16
@@ -39,7 +40,7 @@
 // 890 us. Chunks of ~1000 tokens on 6001 to 8190: 16-bit 457 us, 8-bit 451, 4-bit 440, so that what bounds them is no
 // longer the loaders but the chain from scores through weights to the second product. The kernel is at the limit of 128
 // registers a thread, and the code that its warps run through in a step is larger than the instruction caches near them: where
-// loops of the loaders and of the softmax are written out only in part it is 10 to 15 % faster (figures beside them).
+// loops of the loaders (3 to 5 %) and of the softmax (7 to 15 %) are written out only in part it is faster (figures beside them).
 // A unit costs ~13 us beside its steps, for its queries, masked last step and output.
 #pragma once
 
@@ -420,9 +421,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           tmem_load32(tS, ra);
           tmem_wait_ld(ra);
           // Half of it written out: what both tiles' warps run through stays nearer to the instruction caches (8 prompts of 2048 tokens,
-          // written out / half: 16-bit 457 / 410 us, 8-bit 560 / 509, 4-bit 523 / 484; fp16 output 459 / 411, 695 / 598, 638 /
-          // 544). Prefixes of one tile of rows have the whole chain to wait for instead (62 rows: 288 / 295, 8-bit fp16 324 /
-          // 334, 4-bit fp16 284 / 323, but 4-bit bf16 315 / 265).
+          // written out / half: 16-bit 458 / 409 us, 8-bit 564 / 508, 4-bit 520 / 484; fp16 output 458 / 408, 697 / 598, 644 /
+          // 546). Prefixes of one tile of rows have the whole chain to wait for instead (24 groups of 64 rows behind 8192 tokens:
+          // 210 / 212, 8-bit 221 / 223, fp16 267 / 279, 4-bit fp16 248 / 292, but 4-bit bf16 283 / 232).
           constexpr int kWritten = SHARED && (!kE2M1 || TWO) ? 4 : 2;
 #pragma unroll kWritten
           for (int k = 0; k < 4; ++k) {
@@ -485,7 +486,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
         const int row = wt * 128 + r;
         const int32_t me = blockIdx.x;
         float ref2 = ref, total2 = total;
-        bool all = true, done = false;  // the warp holds all segments; the sums are in the state
+        bool all = true, put_out = false;  // the warp holds all segments; the sums are in the state
         TreePlace tree;
         if (!whole) {
           if (g.step0 == 0)
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           };
           ref2 = top;
           total2 = sum_of(total2, ototal);
-          done = 2 * tree.s >= tree.n;  // the root
+          put_out = 2 * tree.s >= tree.n;  // the root
 #pragma unroll 1
           for (int k = 0; k < D / 32; ++k) {
             uint32_t x[32];
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
               x[4 * e + 2] = __float_as_uint(sum_of(__uint_as_float(x[4 * e + 2]), y[e].z));
               x[4 * e + 3] = __float_as_uint(sum_of(__uint_as_float(x[4 * e + 3]), y[e].w));
             }
-            if (done)
+            if (put_out)
               put(k, x);
             else
               tmem_store32(tO + 32 * k, x);
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           tmem_wait_st();
           tree.joined();
         }
-        if (all && !done) {
+        if (all && !put_out) {
 #pragma unroll 1
           for (int k = 0; k < D / 32; ++k) {
             uint32_t x[32];
@@ -809,8 +810,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
         bool first, queries;  // first of its unit; the unit has rows in the warp's tile
       };
       const uint32_t raw0 = base + Sm::kRaw + lw * 32 * RB + lane * 16;
-      // 4-bit caches: scales of step n, of the warp's keys, K's and V's. (Through registers, as the two of an 8-bit cache,
-      // they cost chunks 547 us instead of 502; those in shared memory 531 instead of 520.)
+      // 4-bit caches: scales of step n, of the warp's keys, K's and V's; in shared memory, since a key has 8 to 16 bytes of them and
+      // the kernel no register to spare. (The two scales of an 8-bit cache's key are held by its lane.)
       constexpr int SB = Sm::kRawScale;
       const uint32_t scales0 = base + Sm::kRawScales + lw * 32 * 2 * SB;
       auto raw_scales = [&](uint32_t n) { return scales0 + (n & 1) * (128 * 2 * SB); };
@@ -853,8 +854,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
         }
       };
       // In batches whose loads come first, and in a loop: the warps of a scheduler run through more code a step than its
-      // instruction cache holds, and what is written out is fetched every time (chunks, batches of all rounds / these, written out: 8-bit 531 /
-      // 484 us, 4-bit 491 / 460).
+      // instruction cache holds, and what is written out is fetched every time (chunks, written out / in a loop: 8-bit
+      // 474 / 450 us, 4-bit 454 / 440).
       auto turn_tile = [&](uint32_t t, bool check) -> uint32_t {
         uint32_t bad_rows = 0;
         const uint32_t to = operand(t);

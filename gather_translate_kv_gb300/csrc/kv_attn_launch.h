@@ -43,8 +43,7 @@ struct AttendArgs {
 };
 
 // Set-up of the kernels on the current device (their shared-memory limits), of those
-// that calls on a pool of this geometry can take (a pool more takes 84 us so, and 106 when
-// all kernels are set up each time). Called by kv_pool_create, but for the attention of shared prefixes, which a pool
+// that calls on a pool of this geometry can take. Called by kv_pool_create, but for the attention of shared prefixes, which a pool
 // sets up at its first use.
 cudaError_t prepare_append(const kv_pool_desc& d);
 cudaError_t prepare_attend(const kv_pool_desc& d, bool shared);

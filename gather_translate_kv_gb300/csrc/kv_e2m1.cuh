@@ -14,7 +14,7 @@ namespace gtkv {
 
 constexpr uint32_t kMaxScaleByte = 0xE0;
 
-// Bytes of a row: H heads' codes, their scales, rounded up to whole vectors (kv_layout.cpp).
+// Bytes of the codes of a row's H heads, behind which their scales lie (the whole row: kv_layout.cpp).
 __host__ __device__ constexpr int32_t code_bytes(int32_t H, int32_t D) { return H * D / 2; }
 
 // The codes of a word as four pairs of fp16, in order.

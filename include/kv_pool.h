@@ -99,7 +99,7 @@ typedef struct CUstream_st* kv_stream_t;
  * multiple of 16, itemsize is 1, and R = H * D / 2 + H * D / 16 rounded up to a
  * multiple of 16: the codes of the heads in order (element 2i of a head in
  * the low half of its byte i), then the scale bytes of their blocks of 16
- * elements, then bytes that no call reads or writes. Written and read by the
+ * elements, then bytes that hold nothing (the calls that move whole rows move them along). Written and read by the
  * calls of kv_attention.h, which has the meaning of codes and scales; moves and
  * stores carry a token's scales along with its codes. MHA / SWA pools only. */
 enum { KV_FORMAT_ELEMENTS = 0, KV_FORMAT_E2M1 = 1 };
