@@ -40,17 +40,14 @@ __device__ __forceinline__ uint4 lds_vec(uint32_t at) {
   return v;
 }
 
-// Heads [0, heads) of the list (queries, keys, values) of rows [r0, r0 + rows),
-// 64 threads a row, four rows at a time. A thread copies the pieces that it
-// will turn into shared memory of its own (cp.async), two batches of heads or groups of
-// rows ahead, so that loads never stop; no barrier is needed for them. Where the rows belong is a
-// chain of four or five dependent loads; one warp follows it, a row a lane,
-// under the first copies.
-// FOUR: the pool holds 4-bit values. A block's 16 elements are the same chunk
-// of two neighbouring lanes, which exchange their largest magnitudes and share the arithmetic of their two scales (so
-// rotary_dim and D are multiples of 32). Measured: 16 sequences of 2048 tokens (fp16, three axes, 709 MB) 140 us; what a
-// row costs in instructions bounds it (issue slots 52 % busy with two blocks an SM): with the queries' lanes coding along, both scales worked
-// out in every lane and single products it took 166.
+// Heads [0, heads) of the list (queries, keys, values) of rows [r0, r0 + rows), 64 threads a row, four rows at a time.
+// A thread copies the pieces that it will turn into shared memory of its own (cp.async), two batches of heads or groups
+// of rows ahead, so that loads never stop; no barrier is needed for them. Where the rows belong is a chain of four or
+// five dependent loads; one warp follows it, a row a lane, under the first copies. FOUR: the pool holds 4-bit values. A
+// block's 16 elements are the same chunk of two neighbouring lanes, which exchange their largest magnitudes and share
+// the arithmetic of their two scales (so rotary_dim and D are multiples of 32). Measured: 16 sequences of 2048 tokens
+// (fp16, three axes, 709 MB) 140 us; what a row costs in instructions bounds it (issue slots 52 % busy with two blocks
+// an SM): with the queries' lanes coding along, both scales worked out in every lane and single products it took 166.
 template <class T, bool FOUR>
 __device__ __forceinline__ void append_rows(const DevPool& p, const Batch& b, const AppendArgs& g, const Rot& t,
                                             int64_t r0, int rows, int heads, Token* tokens, uint8_t* stage, int& bits) {

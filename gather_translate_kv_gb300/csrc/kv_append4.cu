@@ -108,12 +108,11 @@ __device__ __forceinline__ void store32(void* to, const uint32_t* y, bool wide) 
                : "memory");
 }
 
-// Gather: a block per page run, K and V as one list, N blocks of 16 elements a
-// thread and item: 8 N bytes of codes and N scales in, whole sectors of 32 bytes out,
-// kGatherItems items of a thread in flight. N is 2 where rows hold an even number of blocks.
-// Measured: 232 us for 1.54 GB of whole sequences (98 % of the copy rate; items of 8 bytes of codes and 16-byte stores 276), 33 us
-// for 172 MB of 128-token windows, whose blocks wait for their lookups. Items and resident blocks: 2 / 5 as
-// good, 4 / 5 247 us, 8 / 3 236.
+// Gather: a block per page run, K and V as one list, N blocks of 16 elements a thread and item: 8 N bytes of codes and
+// N scales in, whole sectors of 32 bytes out, kGatherItems items of a thread in flight. N is 2 where rows hold an even
+// number of blocks. Measured: 232 us for 1.54 GB of whole sequences (98 % of the copy rate; items of 8 bytes of codes
+// and 16-byte stores 276), 33 us for 172 MB of 128-token windows, whose blocks wait for their lookups. Items and
+// resident blocks: 2 / 5 as good, 4 / 5 247 us, 8 / 3 236.
 constexpr int kGatherItems = 4;
 constexpr int kGatherBlocks = 4;
 template <class T, int N>

@@ -89,14 +89,13 @@ int64_t attend_workspace_bytes(int32_t, int32_t, int32_t D, int32_t, int64_t, in
   return align256(attend_few_workspace(D, sm_count)) + attend_tile_workspace(D, sm_count);
 }
 
-// Which kernels: the few-rows kernel alone when the sequences' rows of a KV
-// head number at most 16 (8-bit and 4-bit caches: 32) on average (decode steps and
-// drafts; a longer sequence among them takes several row tiles there), else both, each taking the
-// sequences on its side of that. Lengths are known on the device alone, so the
-// rule goes by averages. 32 sequences of 4000 tokens, 4 query heads a KV head,
-// D = 128, few-rows against tile kernel, us: 16-bit 110 / 147 at 8 rows, 137 / 150 at 16, 195 / 151 at 20; 8-bit 83 / 154
-// at 16, 126 / 159 at 32, 182 / 160 at 40 (fp16 output 91 / 189, 143 / 195, 205 / 195); 4-bit 75 / 158, 121 / 162,
-// 169 / 162 (fp16 output 82 / 187, 138 / 189, 195 / 189).
+// Which kernels: the few-rows kernel alone when the sequences' rows of a KV head number at most 16 (8-bit and 4-bit
+// caches: 32) on average (decode steps and drafts; a longer sequence among them takes several row tiles there), else
+// both, each taking the sequences on its side of that. Lengths are known on the device alone, so the rule goes by
+// averages. 32 sequences of 4000 tokens, 4 query heads a KV head, D = 128, few-rows against tile kernel, us: 16-bit 110
+// / 147 at 8 rows, 137 / 150 at 16, 195 / 151 at 20; 8-bit 83 / 154 at 16, 126 / 159 at 32, 182 / 160 at 40 (fp16
+// output 91 / 189, 143 / 195, 205 / 195); 4-bit 75 / 158, 121 / 162, 169 / 162 (fp16 output 82 / 187, 138 / 189, 195 /
+// 189).
 cudaError_t launch_tiles(const DevPool& p, const Batch& b, const AttendArgs& a, Kind kind, const Groups& g,
                          void* workspace, int sm_count, cudaStream_t s) {
   const int32_t few_rows = few_rows_of(kind);

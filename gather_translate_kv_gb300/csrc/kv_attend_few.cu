@@ -1,4 +1,5 @@
-// Attention of few rows a sequence: the launch. The kernel is kv_attend_few.cuh's, its instances are kv_attend_few_*.cu's.
+// Attention of few rows a sequence: the launch. The kernel is kv_attend_few.cuh's, its instances are
+// kv_attend_few_*.cu's.
 #include "kv_attend_launch.h"
 
 namespace gtkv {
@@ -31,8 +32,8 @@ cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs
   w.hw = heads_of_worker(a.H);
   w.max_new = max_new;
   const int kw = kFewWarps / w.hw;
-  // one tile of 8 columns when the sequences' rows of a KV head fit on average, else 16 (4 rows, 256 x 4096 tokens, on one
-  // GPU: 686 us with 8 columns, 803 with 16)
+  // one tile of 8 columns when the sequences' rows of a KV head fit on average, else 16 (4 rows, 256 x 4096 tokens, on
+  // one GPU: 686 us with 8 columns, 803 with 16)
   const int nt = b.n_rows * a.G <= 8 * spans_of(b) ? 1 : 2;
   // steps of one unit at most, and of all units
   int64_t most = static_cast<int64_t>(b.max_pages) * p.ps / 16 + 1;
@@ -41,14 +42,16 @@ cudaError_t launch_attend_few(const DevPool& p, const Batch& b, const AttendArgs
     most = seen < most ? seen : most;
   }
   const int64_t tiles = (b.n_rows * a.G) / (8 * nt) + b.n_seqs;  // row tiles of all sequences
-  int64_t cap = static_cast<int64_t>(sm_count) * few_blocks(kind == Kind::kE2M1 ? a.D / 2 : kind == Kind::kE4M3 ? a.D : 2 * a.D, nt, kind == Kind::kE2M1) * kw;
+  const int row_bytes = kind == Kind::kE2M1 ? a.D / 2 : kind == Kind::kE4M3 ? a.D : 2 * a.D;
+  int64_t cap = static_cast<int64_t>(sm_count) * few_blocks(row_bytes, nt, kind == Kind::kE2M1) * kw;
   // units that are short anyway are never cut, and then there is nothing to join: 512 sequences of 300 tokens (8-bit,
   // D = 64) 52 us against 63 cut, 4 of 128 tokens 15.0 against 15.2
   w.whole = most <= (tiles * (a.H / w.hw) >= cap ? kWhole : kWhole / 3);
   const int64_t all = (w.whole ? 1 : most + kFewUnitCost) * tiles * (a.H / w.hw);
   cap = cap < kMaxWorkers ? cap : kMaxWorkers;
   // a prefix of few rows is cut into many segments, which then meet level by level: 4 sequences in 2 groups behind 8192
-  // tokens (in wide tables) 43 us with 4 steps a segment and with 8, 8-bit 51 / 45, 4-bit 49 / 45; with more groups the same
+  // tokens (in wide tables) 43 us with 4 steps a segment and with 8, 8-bit 51 / 45, 4-bit 49 / 45; with more groups the
+  // same
   w.min_share = w.whole ? 1 : a.state ? 2 * kMinShare : kMinShare;
   int64_t workers = (all + w.min_share - 1) / w.min_share;
   workers = workers > cap ? cap : workers;

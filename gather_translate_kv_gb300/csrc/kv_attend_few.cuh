@@ -1,53 +1,47 @@
-// Attention of few rows a sequence (decode steps, drafted tokens): at most 16
-// rows (8-bit and 4-bit caches: 32) on average, a row being a (token, query head) pair of one KV head, in
-// tiles of 8 or 16; a sequence with more takes several tiles, each of which reads its keys and values again. A tile reads
-// them once for a handful of rows, so the bound is memory; the work is laid out so that nothing stands between
-// the loads. Behind shared prefixes the kernel takes the own tokens of all sequences, however many rows they have, and
-// prefixes of groups of few rows (kv_attend_shared.cu has the limits).
+// Attention of few rows a sequence (decode steps, drafted tokens): at most 16 rows (8-bit and 4-bit caches: 32) on
+// average, a row being a (token, query head) pair of one KV head, in tiles of 8 or 16; a sequence with more takes
+// several tiles, each of which reads its keys and values again. A tile reads them once for a handful of rows, so the
+// bound is memory; the work is laid out so that nothing stands between the loads. Behind shared prefixes the kernel
+// takes the own tokens of all sequences, however many rows they have, and prefixes of groups of few rows
+// (kv_attend_shared.cu has the limits).
 //
-// One warp owns one KV head over its own run of keys, 16 keys a step, and never
-// talks to another warp. Both products run as mma m16n8k16 with the CACHE as
-// the 16-row operand, S^T = K Q^T and O^T = V^T P^T, rows as the 8 (or 16)
-// columns, so 4 query heads fill half of an instruction instead of a quarter.
-// The order of the summed index is free, so operand registers are filled from
-// whole 16-byte pieces of the rows as they lie in the cache: lane (g, c) =
-// (lane / 4, lane % 4) takes pieces of keys g and g + 8 for K, and its eighth
-// of the elements of keys 2c, 2c + 1, 2c + 8, 2c + 9 for V, where byte
-// permutes pair up two keys. Rows come by cp.async into a ring of the warp's
-// own, whole rows an instruction. No transpose, no bank conflict, no barrier. Codes become fp16 (exact) on the
-// way into the registers; P^T comes out of the score registers by movmatrix.
+// One warp owns one KV head over its own run of keys, 16 keys a step, and never talks to another warp. Both products
+// run as mma m16n8k16 with the CACHE as the 16-row operand, S^T = K Q^T and O^T = V^T P^T, rows as the 8 (or 16)
+// columns, so 4 query heads fill half of an instruction instead of a quarter. The order of the summed index is free, so
+// operand registers are filled from whole 16-byte pieces of the rows as they lie in the cache: lane (g, c) = (lane / 4,
+// lane % 4) takes pieces of keys g and g + 8 for K, and its eighth of the elements of keys 2c, 2c + 1, 2c + 8, 2c + 9
+// for V, where byte permutes pair up two keys. Rows come by cp.async into a ring of the warp's own, whole rows an
+// instruction. No transpose, no bank conflict, no barrier. Codes become fp16 (exact) on the way into the registers; P^T
+// comes out of the score registers by movmatrix.
 //
-// Softmax: the running reference m moves only when a score exceeds it by
-// 2^8 (a vote per step), so the common step has no shuffle. Weights are
-// 2^(t - m), t = score * log2(e) + log2(value scale): the scale of an 8-bit
-// value is part of its weight, so that weights stay in one range, and the
-// denominator adds weight / scale. Weights meet the values as the sum of two 16-bit
-// parts and keep 16 bits (bf16) or 22 (fp16, lifted by 2^6 so that 2^-30 of the largest
-// still counts): the result's error is then the output's own rounding and no more, where one part
-// alone adds 40 % to it (fp16 output, 4096 keys, root mean square: 5.39e-6 and 7.54e-6). Under
-// 16-bit caches the second product is free, memory being the bound. Of 8-bit caches read
-// into bf16, whose 8 bits hide the 11 of one fp16 part (8.73e-5 and 8.79e-5), the weights are
-// one part, and so they are of 4-bit caches (the result's whole error grows by 0.8 %): drafts in 8 bits take 334 us so
-// and 377 with two, 256 x 4096 tokens in 4 bits 320 and 337. Queries for 8-bit caches are fp16 after a power-of-two scaling per row, exact for all
-// bits that matter (2^-29 of the row's largest).
+// Softmax: the running reference m moves only when a score exceeds it by 2^8 (a vote per step), so the common step has
+// no shuffle. Weights are 2^(t - m), t = score * log2(e) + log2(value scale): the scale of an 8-bit value is part of
+// its weight, so that weights stay in one range, and the denominator adds weight / scale. Weights meet the values as
+// the sum of two 16-bit parts and keep 16 bits (bf16) or 22 (fp16, lifted by 2^6 so that 2^-30 of the largest still
+// counts): the result's error is then the output's own rounding and no more, where one part alone adds 40 % to it (fp16
+// output, 4096 keys, root mean square: 5.39e-6 and 7.54e-6). Under 16-bit caches the second product is free, memory
+// being the bound. Of 8-bit caches read into bf16, whose 8 bits hide the 11 of one fp16 part (8.73e-5 and 8.79e-5), the
+// weights are one part, and so they are of 4-bit caches (the result's whole error grows by 0.8 %): drafts in 8 bits
+// take 334 us so and 377 with two, 256 x 4096 tokens in 4 bits 320 and 337. Queries for 8-bit caches are fp16 after a
+// power-of-two scaling per row, exact for all bits that matter (2^-29 of the row's largest).
 //
-// Measured: 256 sequences of 4096 tokens (bf16, 8 KV heads of 128, 4.3 GB) 680 to 698
-// us from one GPU to another, 91 to 93 % of the copy rate; 40 sequences of 9 to 40 961 tokens with drafts
-// (8-bit, 1.68 GB) 332 us, 74 %, bound by latency inside a warp (codes into fp16, products,
-// weights, one after the other) with three warps a scheduler; one sequence of 203 tokens 14 us, latency.
+// Measured: 256 sequences of 4096 tokens (bf16, 8 KV heads of 128, 4.3 GB) 680 to 698 us from one GPU to another, 91 to
+// 93 % of the copy rate; 40 sequences of 9 to 40 961 tokens with drafts (8-bit, 1.68 GB) 332 us, 74 %, bound by latency
+// inside a warp (codes into fp16, products, weights, one after the other) with three warps a scheduler; one sequence of
+// 203 tokens 14 us, latency.
 //
-// 4-bit caches. A lane's piece of a key is a quarter of the head (two blocks of 16 and their scale bytes), its part of a
-// value an eighth (one block, or half of one). Two elements become fp16 by one conversion and one product with
-// the block's scale, exactly; codes of two values share a byte before that, so that no halves are exchanged. That is 64 conversions (at half
-// rate) and 64 products a lane and step, beside some 300 other instructions; issue and latency bound the kernel: 256 x 4096 tokens
-// (1.2 GB) 320 us, 56 % of the copy rate. What it is sensitive to, in us: one block of keys a round instead of two 324;
-// shared memory that leaves little of L1, where the heads of a block find each other's scale sectors, rings of
-// six stages 393; three blocks an SM 319, five, which spill, 494. 16 columns need all registers of two blocks an SM (drafts of 9 to
-// 40 961 tokens, fp16, 377 us; with three blocks, which spill, 398).
+// 4-bit caches. A lane's piece of a key is a quarter of the head (two blocks of 16 and their scale bytes), its part of
+// a value an eighth (one block, or half of one). Two elements become fp16 by one conversion and one product with the
+// block's scale, exactly; codes of two values share a byte before that, so that no halves are exchanged. That is 64
+// conversions (at half rate) and 64 products a lane and step, beside some 300 other instructions; latency bounds the
+// kernel (issue slots 60 % busy): 256 x 4096 tokens (1.2 GB) 320 us, 56 % of the copy rate. What it is sensitive to, in
+// us: one block of keys a round instead of two 324; shared memory that leaves little of L1, where the heads of a block
+// find each other's scale sectors, rings of six stages 393; three blocks an SM 319, five, which spill, 494. 16 columns
+// need all registers of two blocks an SM (drafts of 9 to 40 961 tokens, fp16, 377 us; with three blocks, which spill,
+// 398).
 //
-// Workers (as many warps as share a step's heads) take equal shares of all
-// steps of the batch (kv_attend_split.cuh); units cut at a border are joined by
-// k_attend_join from 32-bit partial sums in the workspace.
+// Workers (as many warps as share a step's heads) take equal shares of all steps of the batch (kv_attend_split.cuh);
+// units cut at a border are joined by k_attend_join from 32-bit partial sums in the workspace.
 #pragma once
 
 #include "kv_attend_launch.h"
@@ -224,9 +218,14 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
   // V's stay whole, row r at r ^ (r / 4 % 2)).
   const int cr = lane / Sh::kLPR, cp = lane % Sh::kLPR;  // row of a round and piece that the lane copies
   const uint32_t put_k = cr * Sh::kRow + (Sh::kRow > 64 ? cp ^ (cr & 1) * 4 : cp) * 16;
-  const uint32_t put_v = Sh::kRow == 32 ? (cr ^ (cr >> 2 & 1)) * 32 + cp * 16 : cr * Sh::kRow + (Sh::kRow >= 256 ? cp : Sh::kRow > 64 ? cp ^ (cr >> 1) * 2 : cp ^ (cr >> 1 & 3)) * 16;
+  const uint32_t put_v =
+      Sh::kRow == 32 ? (cr ^ (cr >> 2 & 1)) * 32 + cp * 16
+                     : cr * Sh::kRow +
+                           (Sh::kRow >= 256 ? cp : Sh::kRow > 64 ? cp ^ (cr >> 1) * 2 : cp ^ (cr >> 1 & 3)) * 16;
   const uint32_t get_k = g * Sh::kRow + (Sh::kRow > 64 ? c ^ (g & 1) * 4 : c) * (Sh::kRow == 32 ? 8 : 16);  // ^ 64 ch, + 8 rows
-  const uint32_t get_v = Sh::kRow == 32 ? (2 * c + (c >> 1)) * 32 + g * 4 : 2 * c * Sh::kRow + (Sh::kRow > 64 ? (g ^ 2 * c) * 16 : ((g >> 1) ^ c) * 16 + (g & 1) * 8);
+  const uint32_t get_v =
+      Sh::kRow == 32 ? (2 * c + (c >> 1)) * 32 + g * 4
+                     : 2 * c * Sh::kRow + (Sh::kRow > 64 ? (g ^ 2 * c) * 16 : ((g >> 1) ^ c) * 16 + (g & 1) * 8);
   // where the lane's part of values 2c, 2c + 1, 2c + 8, 2c + 9 lies
   auto value_at = [&](int kk) {
     return Sh::kRow == 32 ? (get_v ^ (kk & 1) * 32) + 8 * (kk >> 1) * 32 : get_v + ((kk & 1) + 8 * (kk >> 1)) * Sh::kRow;
@@ -404,7 +403,8 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
           qf[nt][2 * ch + 1][0] = v.z, qf[nt][2 * ch + 1][1] = v.w;
         }
       } else {
-        // the lane's elements of a key, in the order of its codes: sixteen of every 64, or (4-bit caches) a quarter of the head
+        // the lane's elements of a key, in the order of its codes: sixteen of every 64, or (4-bit caches) a quarter of
+        // the head
         constexpr int NV = D / 32;  // in vectors of eight
         float x[8 * NV];
         float amax = 0.0f;
@@ -611,7 +611,9 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
           for (int e = 0; e < 4; ++e)
             x[hb][nt][e] = kE4M3 ? fmaf(x[hb][nt][e], cq[nt][e & 1] * sk[e >> 1], lv[e >> 1] - low[nt][e & 1])
                                  : fmaf(x[hb][nt][e], cq[nt][e & 1], -low[nt][e & 1]);
-      if (mask) {  // apart from the common step, where as predicates they were a third of its instructions (8-bit drafts 363 us, 332 so)
+      // apart from the common step, where as predicates they were a third of its instructions (8-bit drafts 363 us, 332
+      // so)
+      if (mask) {
 #pragma unroll
         for (int hb = 0; hb < KB; ++hb)
 #pragma unroll
@@ -722,7 +724,8 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
         // scales above the largest: NaN, or, where some row may not see some key, zeroed as below
         const uint32_t bad = above_max_pair(s01[hb]) | above_max_pair(s23[hb]) >> 1;  // bits 15, 31 and 14, 30
         if (mask) {
-          const uint32_t keys = __reduce_or_sync(kFull, ((bad >> 15 & 1) | (bad >> 30 & 2) | (bad >> 6 & 0x100) | (bad >> 21 & 0x200)) << 2 * c);
+          const uint32_t own = (bad >> 15 & 1) | (bad >> 30 & 2) | (bad >> 6 & 0x100) | (bad >> 21 & 0x200);
+          const uint32_t keys = __reduce_or_sync(kFull, own << 2 * c);
           if (bad) {
             s01[hb] &= ~((bad >> 15 & 0x10001u) * 0xffffu);
             s23[hb] &= ~((bad >> 14 & 0x10001u) * 0xffffu);
@@ -969,7 +972,8 @@ __global__ void __launch_bounds__(kFewBlock, few_blocks(FewShape<C, D>::kRow, NT
   }
   if (!SHARED && worker < w.n_workers && hw == 0 && lane == 0) w.rec[worker] = rec;
   store_bits(p, bits);
-  if constexpr (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");  // whoever waits for this kernel waits for those before it
+  // whoever waits for this kernel waits for those before it
+  if constexpr (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <class C, int D, int NT, bool SHARED>

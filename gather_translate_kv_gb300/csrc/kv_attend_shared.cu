@@ -17,11 +17,12 @@ namespace {
 
 constexpr int kGroupBlock = 256;
 constexpr int kZeroBlocks = 24;  // at least, so that the nodes are zeros at once
-// Rows a KV head and sequence, on average, past which a sequence fills tiles by itself (kv_attend_layer / shared, us, 32 sequences in
-// 4 groups behind 8192 tokens, with 100 own tokens before the new ones, bf16: 276 / 132 at 64 rows, 284 / 205 at 128, 325 / 291
-// at 192, 336 / 373 at 256; 8-bit 282 / 139, 289 / 209, 312 / 292, 318 / 377; 4-bit 257 / 126, 267 / 201, 302 / 282, 313 / 363).
-// Own tokens are read again for every 16 rows, so with more of them the crossing comes sooner: 1024 of them, bf16, 299 / 202
-// at 64 rows, 303 / 338 at 128; 4096 behind 4096 shared ones 270 / 452 and 275 / 809. Lengths are known on the device alone.
+// Rows a KV head and sequence, on average, past which a sequence fills tiles by itself (kv_attend_layer / shared, us,
+// 32 sequences in 4 groups behind 8192 tokens, with 100 own tokens before the new ones, bf16: 276 / 132 at 64 rows, 284
+// / 205 at 128, 325 / 291 at 192, 336 / 373 at 256; 8-bit 282 / 139, 289 / 209, 312 / 292, 318 / 377; 4-bit 257 / 126,
+// 267 / 201, 302 / 282, 313 / 363). Own tokens are read again for every 16 rows, so with more of them the crossing
+// comes sooner: 1024 of them, bf16, 299 / 202 at 64 rows, 303 / 338 at 128; 4096 behind 4096 shared ones 270 / 452 and
+// 275 / 809. Lengths are known on the device alone.
 constexpr int kOwnTiles = 128;
 
 // Looks at all metadata once. own: the sequences, checked; shared: at the index of a group's first sequence with
@@ -126,24 +127,26 @@ Workspace workspace_of(int32_t Q, int32_t D, int32_t n_seqs, int64_t n_rows, int
   return w;
 }
 
-// Whether to share at all, by what the host knows: the tables' width as a bound on the lengths. The shared form is three
-// launches in a row, and until the batch's cache outgrows L2 and what it delivers kv_attend_layer is as fast: elements that it would read
-// more than once, in millions, and us (kv_attend_layer / shared), 8 KV and 32 query heads of 128, one token a sequence: 64
-// sequences of one prefix, bf16, 134 41 / 43, 266 62 / 48, 531 105 / 53; 64 of 16 prefixes 203 64 / 67, 404 133 / 95, 807
-// 335 / 154; 16 of one prefix 126 43 / 47, 252 64 / 51; 8 bits, 64 of one 134 39 / 49, 266 57 / 54, 64 of 16 203 59 / 60,
-// 404 102 / 77; 4 bits 46 / 51, 63 / 56, 63 / 52, 99 / 67. In tables that are wider than the batch is long it shares too
-// early: four answers behind 608 tokens 17 us, in a table for 131072 tokens 29 (8 bits 17 and 35, 4 bits 19 and 33).
+// Whether to share at all, by what the host knows: the tables' width as a bound on the lengths. The shared form is
+// three launches in a row, and until the batch's cache outgrows L2 and what it delivers kv_attend_layer is as fast:
+// elements that it would read more than once, in millions, and us (kv_attend_layer / shared), 8 KV and 32 query heads
+// of 128, one token a sequence: 64 sequences of one prefix, bf16, 134 41 / 43, 266 62 / 48, 531 105 / 53; 64 of 16
+// prefixes 203 64 / 67, 404 133 / 95, 807 335 / 154; 16 of one prefix 126 43 / 47, 252 64 / 51; 8 bits, 64 of one 134
+// 39 / 49, 266 57 / 54, 64 of 16 203 59 / 60, 404 102 / 77; 4 bits 46 / 51, 63 / 56, 63 / 52, 99 / 67. In tables that
+// are wider than the batch is long it shares too early: four answers behind 608 tokens 17 us, in a table for 131072
+// tokens 29 (8 bits 17 and 35, 4 bits 19 and 33).
 bool worth_sharing(const DevPool& p, const Batch& b, const AttendArgs& a, int32_t n_groups) {
   if (n_groups >= b.n_seqs || b.n_rows * a.G > kOwnTiles * static_cast<int64_t>(b.n_seqs)) return false;
   const double again = static_cast<double>(b.n_seqs - n_groups) * b.max_pages * p.ps * a.H * a.D * 2;
   return again >= (b.n_seqs / 32 >= n_groups ? 0x1p27 : 0x1p28);
 }
 
-// Which kernel attends to the prefixes, by a group's rows of a KV head on average: k_attend_few up to 8 (8-bit and 4-bit caches 32), else
-// k_attend_tile. us, few / tile: 16-bit, 8 rows (64 sequences in 32 groups behind 4096 tokens) 117 / 153, 16 rows (16 groups, 2048 tokens)
-// 69 / 67, 32 rows (8 groups, 4096) 83 / 68; 8-bit 16 rows (8192) 102 / 158, 32 rows (4096) 71 / 74, 48 rows 80 / 79, 64 rows 92 / 84;
-// 4-bit 91 / 157, 63 / 68, 74 / 72, 87 / 79. One kernel takes all prefixes: a group far larger than the average is gone over
-// once for every 8 or 16 of its rows in the first, one far smaller leaves tiles empty in the second.
+// Which kernel attends to the prefixes, by a group's rows of a KV head on average: k_attend_few up to 8 (8-bit and
+// 4-bit caches 32), else k_attend_tile. us, few / tile: 16-bit, 8 rows (64 sequences in 32 groups behind 4096 tokens)
+// 117 / 153, 16 rows (16 groups, 2048 tokens) 69 / 67, 32 rows (8 groups, 4096) 83 / 68; 8-bit 16 rows (8192) 102 /
+// 158, 32 rows (4096) 71 / 74, 48 rows 80 / 79, 64 rows 92 / 84; 4-bit 91 / 157, 63 / 68, 74 / 72, 87 / 79. One kernel
+// takes all prefixes: a group far larger than the average is gone over once for every 8 or 16 of its rows in the first,
+// one far smaller leaves tiles empty in the second.
 int64_t prefix_few_rows(Kind kind) { return kind == Kind::kElements ? 8 : 32; }
 
 }  // namespace

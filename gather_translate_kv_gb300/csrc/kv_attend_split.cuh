@@ -179,8 +179,8 @@ __device__ __forceinline__ float2 unpack16(uint32_t w) {
   return BF16 ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)) : halves(w);
 }
 
-// Where the segments of a cut unit meet when no join follows (shared prefixes): a binary tree over them in the
-// workers' order. Of the two halves of a node the one that is done first leaves its sums and goes on to its other work; the
+// Where the segments of a cut unit meet when no join follows (shared prefixes): a binary tree over them in the workers'
+// order. Of the two halves of a node the one that is done first leaves its sums and goes on to its other work; the
 // second adds them to its own and goes up. The sums do not depend on who was first.
 struct TreePlace {
   int32_t worker0;   // of the unit's first segment

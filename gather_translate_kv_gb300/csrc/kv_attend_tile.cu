@@ -1,4 +1,5 @@
-// Attention of many rows a sequence: the launch. The kernel is kv_attend_tile.cuh's, its instances are kv_attend_tile_*.cu's.
+// Attention of many rows a sequence: the launch. The kernel is kv_attend_tile.cuh's, its instances are
+// kv_attend_tile_*.cu's.
 #include "kv_attend_launch.h"
 
 namespace gtkv {

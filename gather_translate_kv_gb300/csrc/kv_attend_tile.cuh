@@ -1,47 +1,38 @@
-// Attention of many rows a sequence (prompts, chunks, long drafts) on the
-// 5th-generation tensor cores.
+// Attention of many rows a sequence (prompts, chunks, long drafts) on the 5th-generation tensor cores.
 //
-// A block owns a unit: up to 256 rows of one KV head of a sequence, a row being
-// a (token, query head of the group) pair, as two tiles of 128 rows. For each 128 keys
+// A block owns a unit: up to 256 rows of one KV head of a sequence, a row being a (token, query head of the group)
+// pair, as two tiles of 128 rows. For each 128 keys
 //   S_w = Q_w K^T   (tile w of rows; both operands in shared memory)
 //   P_w = 2^(t - m) (softmax warps; written over S_w in tensor memory)
 //   O_w += P_w V    (P_w from tensor memory, V as the M/N-major operand)
-// with S_0, S_1, O_0, O_1 filling the 512 columns of tensor memory. The two
-// tiles alternate: while four warps turn S_0 into P_0 the tensor cores work on tile 1
-// and the other way round, which is what bounds the kernel: per 128 keys and
-// tile 4 * 128 * 128 * D operations (6 with weights in two parts) on the tensor cores against
-// 128 * 128 exponentials.
+// with S_0, S_1, O_0, O_1 filling the 512 columns of tensor memory. The two tiles alternate: while four warps turn S_0
+// into P_0 the tensor cores work on tile 1 and the other way round, which is what bounds the kernel: per 128 keys and
+// tile 4 * 128 * 128 * D operations (6 with weights in two parts) on the tensor cores against 128 * 128 exponentials.
 //
-// Warps 0-3 and 4-7: softmax of tile 0 and 1, one row a thread (no shuffles).
-// Warps 8-11: loaders; they look up the pages, copy keys and values into the
-// 128-byte-swizzled operand layout with cp.async (16-bit caches) or through
-// registers, turning codes into fp16 (8-bit and 4-bit caches), and zero what is no live
-// token. Pages of any size end anywhere in a tile, so keys are placed row by
-// row rather than by a tensor map. Warp 12 issues the products.
+// Warps 0-3 and 4-7: softmax of tile 0 and 1, one row a thread (no shuffles). Warps 8-11: loaders; they look up the
+// pages, copy keys and values into the 128-byte-swizzled operand layout with cp.async (16-bit caches) or through
+// registers, turning codes into fp16 (8-bit and 4-bit caches), and zero what is no live token. Pages of any size end
+// anywhere in a tile, so keys are placed row by row rather than by a tensor map. Warp 12 issues the products.
 //
-// The running reference m of a row moves only when a tile's maximum exceeds it
-// by 2^8; only then is O read back and scaled. A first pass over the scores finds that
-// maximum, a second turns them into weights in place. Weights meet the values as two parts of
-// the cache's 16-bit type (bf16, or fp16 lifted by 2^6 for fp16 and 8-bit caches), rounded
-// and what the rounding left, so that the result's error is the output's own rounding: 1.479e-4
-// (root mean square, prompts of 2048 tokens in bf16), as the formula in 32 bits has it, where one part
-// gave 1.903e-4 for 582 us instead of 757. Of 8-bit and 4-bit caches read into bf16, whose 8 bits
-// hide fp16's 11, one part is enough (7.45e-5 and 7.39e-5; chunks of ~1000 tokens in 8 bits 452 us, with two parts 561, in
-// 4 bits 440 and 524). Denominators
-// add the 32-bit weights. The scale of
-// an 8-bit value is part of its weight, t = score * log2(e) + log2(scale), and
-// the denominator adds weight / scale. Queries for 8-bit caches become fp16
-// after a power-of-two scaling per row.
+// The running reference m of a row moves only when a tile's maximum exceeds it by 2^8; only then is O read back and
+// scaled. A first pass over the scores finds that maximum, a second turns them into weights in place. Weights meet the
+// values as two parts of the cache's 16-bit type (bf16, or fp16 lifted by 2^6 for fp16 and 8-bit caches), rounded and
+// what the rounding left, so that the result's error is the output's own rounding: 1.479e-4 (root mean square, prompts
+// of 2048 tokens in bf16), as the formula in 32 bits has it, where one part gave 1.903e-4 for 582 us instead of 757. Of
+// 8-bit and 4-bit caches read into bf16, whose 8 bits hide fp16's 11, one part is enough (7.45e-5 and 7.39e-5; chunks
+// of ~1000 tokens in 8 bits 452 us, with two parts 561, in 4 bits 440 and 524). Denominators add the 32-bit weights.
+// The scale of an 8-bit value is part of its weight, t = score * log2(e) + log2(scale), and the denominator adds weight
+// / scale. Queries for 8-bit caches become fp16 after a power-of-two scaling per row.
 //
 // Work is cut as in kv_attend_split.cuh, 128 keys a step.
 //
-// Measured: 16 prompts of 2048 tokens (bf16, 8 KV and 32 query heads of 128,
-// 550 GFLOP) 752 to 766 us, 38 % of the measured cuBLAS burst; 4 of 8192 tokens 2240 us; the 16 prompts in 8 bits 952, in 4 bits
-// 890 us. Chunks of ~1000 tokens on 6001 to 8190: 16-bit 457 us, 8-bit 451, 4-bit 440, so that what bounds them is no
-// longer the loaders but the chain from scores through weights to the second product. The kernel is at the limit of 128
-// registers a thread, and the code that its warps run through in a step is larger than the instruction caches near them: where
-// loops of the loaders (3 to 5 %) and of the softmax (7 to 15 %) are written out only in part it is faster (figures beside them).
-// A unit costs ~13 us beside its steps, for its queries, masked last step and output.
+// Measured: 16 prompts of 2048 tokens (bf16, 8 KV and 32 query heads of 128, 550 GFLOP) 752 to 766 us, 38 % of the
+// measured cuBLAS burst; 4 of 8192 tokens 2240 us; the 16 prompts in 8 bits 952, in 4 bits 890 us. Chunks of ~1000
+// tokens on 6001 to 8190: 16-bit 457 us, 8-bit 451, 4-bit 440, so that what bounds them is no longer the loaders but
+// the chain from scores through weights to the second product. The kernel is at the limit of 128 registers a thread,
+// and the code that its warps run through in a step is larger than the instruction caches near them: where loops of the
+// loaders (3 to 5 %) and of the softmax (7 to 15 %) are written out only in part it is faster (figures beside them). A
+// unit costs ~13 us beside its steps, for its queries, masked last step and output.
 #pragma once
 
 #include "kv_attend_split.cuh"
@@ -420,10 +411,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           auto buf = [&](int k) -> uint32_t(&)[32] { return k & 1 ? rb : ra; };
           tmem_load32(tS, ra);
           tmem_wait_ld(ra);
-          // Half of it written out: what both tiles' warps run through stays nearer to the instruction caches (8 prompts of 2048 tokens,
-          // written out / half: 16-bit 458 / 409 us, 8-bit 564 / 508, 4-bit 520 / 484; fp16 output 458 / 408, 697 / 598, 644 /
-          // 546). Prefixes of one tile of rows have the whole chain to wait for instead (24 groups of 64 rows behind 8192 tokens:
-          // 210 / 212, 8-bit 221 / 223, fp16 267 / 279, 4-bit fp16 248 / 292, but 4-bit bf16 283 / 232).
+          // Half of it written out: what both tiles' warps run through stays nearer to the instruction caches (8
+          // prompts of 2048 tokens, written out / half: 16-bit 458 / 409 us, 8-bit 564 / 508, 4-bit 520 / 484; fp16
+          // output 458 / 408, 697 / 598, 644 / 546). Prefixes of one tile of rows have the whole chain to wait for
+          // instead (24 groups of 64 rows behind 8192 tokens: 210 / 212, 8-bit 221 / 223, fp16 267 / 279, 4-bit fp16
+          // 248 / 292, but 4-bit bf16 283 / 232).
           constexpr int kWritten = SHARED && (!kE2M1 || TWO) ? 4 : 2;
 #pragma unroll kWritten
           for (int k = 0; k < 4; ++k) {
@@ -640,7 +632,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
         const int32_t qh = g.h * a.G + f % a.G;
         const uint16_t* out = static_cast<const uint16_t*>(a.out) + (orow * a.Q + qh) * D;
         bool bad = false;
-        for (int e = lane; e < D; e += 32) bad = bad || (out[e] & (a.type == KV_TYPE_BF16 ? 0x7f80 : 0x7c00)) == (a.type == KV_TYPE_BF16 ? 0x7f80 : 0x7c00);
+        const int exponent = a.type == KV_TYPE_BF16 ? 0x7f80 : 0x7c00;
+        for (int e = lane; e < D; e += 32) bad = bad || (out[e] & exponent) == exponent;
         if (__any_sync(kFull, bad)) attend_row<C>(p, b, a, g.s, g.q.a + f / a.G, orow, qh, &bits);
       }
     } while (walk.next());
@@ -783,7 +776,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
     // waits until tile t - kRing has been used
     auto claim = [&](uint32_t t) { return wait(bar(Sm::kFree + t % Sm::kRing), (t / Sm::kRing & 1) ^ 1); };
     const int32_t row_bytes = static_cast<int32_t>(p.vpr * 16);
-    // Copies 32 rows (of round `it` the lane's ro[it]) of K, or of V when `v`; at(round, piece): where a lane's piece goes.
+    // Copies 32 rows (of round `it` the lane's ro[it]) of K, or of V when `v`; at(round, piece): where a lane's piece
+    // goes.
     auto rows_of = [&](int32_t row_of_lane, int32_t* ro) {  // all shuffles together: their latencies overlap
 #pragma unroll
       for (int it = 0; it < IT; ++it) ro[it] = __shfl_sync(kFull, row_of_lane, it * RPI + lr);
@@ -810,8 +804,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
         bool first, queries;  // first of its unit; the unit has rows in the warp's tile
       };
       const uint32_t raw0 = base + Sm::kRaw + lw * 32 * RB + lane * 16;
-      // 4-bit caches: scales of step n, of the warp's keys, K's and V's; in shared memory, since a key has 8 to 16 bytes of them and
-      // the kernel no register to spare. (The two scales of an 8-bit cache's key are held by its lane.)
+      // 4-bit caches: scales of step n, of the warp's keys, K's and V's; in shared memory, since a key has 8 to 16
+      // bytes of them and the kernel no register to spare. (The two scales of an 8-bit cache's key are held by its
+      // lane.)
       constexpr int SB = Sm::kRawScale;
       const uint32_t scales0 = base + Sm::kRawScales + lw * 32 * 2 * SB;
       auto raw_scales = [&](uint32_t n) { return scales0 + (n & 1) * (128 * 2 * SB); };
@@ -853,9 +848,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(DevPool p, Batc
           }
         }
       };
-      // In batches whose loads come first, and in a loop: the warps of a scheduler run through more code a step than its
-      // instruction cache holds, and what is written out is fetched every time (chunks, written out / in a loop: 8-bit
-      // 474 / 450 us, 4-bit 454 / 440).
+      // In batches whose loads come first, and in a loop: the warps of a scheduler run through more code a step than
+      // its instruction cache holds, and what is written out is fetched every time (chunks, written out / in a loop:
+      // 8-bit 474 / 450 us, 4-bit 454 / 440).
       auto turn_tile = [&](uint32_t t, bool check) -> uint32_t {
         uint32_t bad_rows = 0;
         const uint32_t to = operand(t);

@@ -189,7 +189,8 @@ int kv_attend_shared_workspace_bytes(const kv_pool_t* pool, int32_t q_heads, int
   const int rc = kv_attend_workspace_bytes(pool, q_heads, n_seqs, n_rows, bytes);
   if (rc != KV_OK) return rc;
   if (n_rows > (int64_t(1) << 36)) return KV_ERR_INVALID;  // 4 * n_rows * q_heads * (head_dim + 2) stays below 2^63
-  int dev = -1;  // a program asks before its first call, which then finds its kernels; on another device that call sets them up
+  // a program asks before its first call, which then finds its kernels (asked on another device, it sets them up)
+  int dev = -1;
   if (!pool->shared_ready.load(std::memory_order_acquire) && cudaGetDevice(&dev) == cudaSuccess && dev == pool->device)
     ready_shared(pool);
   *bytes = gtkv::attend_shared_workspace_bytes(q_heads, pool->desc.head_dim, n_seqs, n_rows, pool->sm_count);
