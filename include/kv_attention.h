@@ -179,18 +179,18 @@ typedef struct {
  * members' own, and head sizes other than 64 and 128 share nothing. Groups that are not what is
  * said above (KV_DEV_ERR_TABLE), or whose rows do not follow one another, are answered as if nothing were shared; of a
  * prefix that its members' tables do not share, a member's rows see the group's first one's tokens or its own.
- *  It is made for decode steps and drafts behind long prefixes. A sequence's own tokens are read
- * again for every 16 of its rows, so where sequences bring many new tokens and long contexts of their own,
- * kv_attend_layer is faster (32 sequences of 32 new tokens with 4096 own tokens behind 4096 shared ones: 0.27 ms and 0.8 ms; 63
- * decode steps beside a chunk of 1500 tokens, 2048 shared: 0.20 and 0.37), and one kernel takes all prefixes by their groups'
- * average rows, groups that share nothing included.
+ *  It is made for decode steps and drafts behind long prefixes. A sequence's own tokens are read again
+ * for every 16 of its rows, so where sequences bring many new tokens and long contexts of their own,
+ * kv_attend_layer is faster (32 sequences of 32 new tokens with 4096 own tokens behind 4096 shared
+ * ones: 0.27 ms and 0.8 ms; 63 decode steps beside a chunk of 1500 tokens, 2048 shared: 0.20 and 0.37).
+ * One kernel takes all prefixes, by their groups' average rows, groups that share nothing included.
  *  workspace_dev  kv_attend_shared_workspace_bytes() bytes, else as in
  *            kv_attend_layer: 122 MB for a head_dim of 128 on 152 SMs and
  *            4 * (head_dim + 2) bytes for every row and query head.
  * Batches that are too small for sharing to pay are kv_attend_layer's calls. That goes by the width
  * of the tables (max_pages, not the sequences' lengths), rows and groups: tables much wider than
- * the batch is long have small batches share, too (four answers behind 608 tokens 29 us instead of 17). Should a wait run out (KV_DEV_ERR_TIMEOUT), all rows of
- * groups that share are unspecified. */
+ * the batch is long have small batches share, too (four answers behind 608 tokens 29 us instead of
+ * 17). Should a wait run out (KV_DEV_ERR_TIMEOUT), all rows of groups that share are unspecified. */
 int kv_attend_shared_workspace_bytes(const kv_pool_t* pool, int32_t q_heads, int32_t n_seqs, int64_t n_rows,
                                      int64_t* bytes); /* with the pool's device current it also loads the kernels */
 int kv_attend_shared_layer(const kv_pool_t* pool, int32_t layer, const kv_batch* batch, const kv_prefix_groups* groups,
